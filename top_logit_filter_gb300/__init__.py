@@ -10,6 +10,14 @@ the calls raise.
     token, out = sample(filtered, min_p=None, q=None, eps=1e-10, out=None, want_out=True)
     sorted_value, sorted_indices = sort(logits)
 
+and, for decoding with beams or drafted tokens (``decode``):
+
+    score, parent, token = beam_select(logits, scores, n)
+    states = beam_reorder(states, parent, lengths=None, out=None)
+    cache_write(k, v, slots, k_cache, v_cache)
+    k, v = cache_read(slots, k_cache, v_cache)
+    out = tree_attention(q, k_cache, v_cache, context, pages=None, tree=None)
+
 Semantics: section 2 of the web page "CANN ops-nn 算子实战：
 ApplyTopKTopPWithSorted 的 top-k/top-p 采样过滤原理与 aclnn 调用指南" --
 per row, values strictly below the k-th largest become -inf, then sorted
@@ -306,3 +314,6 @@ def device_status(device=None) -> None:
 def last_launch_count() -> int:
     """Kernel launches enqueued by the most recent successful call."""
     return _lib.load().topkp_last_launch_count()
+
+
+from .decode import beam_reorder, beam_select, cache_read, cache_write, tree_attention  # noqa: E402,F401

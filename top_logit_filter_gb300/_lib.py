@@ -26,6 +26,40 @@ EXPORTS = ("topkp_apply", "topkp_apply_sample", "topkp_apply_sorted", "topkp_sam
            "topkp_sort", "topkp_sort_workspace_size", "topkp_sort_static", "topkp_last_error_string",
            "topkp_device_status", "topkp_last_launch_count")
 
+# every entry point declared in include/topkp_decode.h
+DECODE_EXPORTS = ("topkp_beam_select", "topkp_beam_select_workspace_size", "topkp_beam_reorder", "topkp_cache_write",
+                  "topkp_cache_read", "topkp_tree_attention", "topkp_tree_attention_workspace_size")
+TOPKP_E4M3 = 3
+TOPKP_MAX_BEAMS = 64
+TOPKP_MAX_CANDIDATES = 128
+TOPKP_MAX_HEAD_DIM = 256
+TOPKP_MAX_TREE = 64
+
+
+class State(ctypes.Structure):
+    """topkp_state"""
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p)] + [(n, ctypes.c_int64) for n in (
+        "src_row_stride", "dst_row_stride", "src_block_stride", "dst_block_stride", "blocks", "entries", "entry_bytes")]
+
+
+class Cache(ctypes.Structure):
+    """topkp_cache"""
+    _fields_ = [("data", ctypes.c_void_p), ("exponents", ctypes.c_void_p), ("dtype", ctypes.c_int32)] + [
+        (n, ctypes.c_int64) for n in ("page_stride", "token_stride", "head_stride", "exp_page_stride",
+                                      "exp_token_stride", "exp_head_stride")]
+
+
+class TreeAttentionArgs(ctypes.Structure):
+    """topkp_tree_attention_args"""
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("k", Cache), ("v", Cache),
+                ("table", ctypes.c_void_p), ("context", ctypes.c_void_p), ("nodes", ctypes.c_void_p),
+                ("tree", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)] + [
+        (n, ctypes.c_int64) for n in ("B", "T", "Hq", "Hkv", "D", "pages", "page_size", "max_pages", "ld_table",
+                                      "max_context", "q_batch_stride", "q_token_stride", "q_head_stride",
+                                      "out_batch_stride", "out_token_stride", "out_head_stride")] + [
+        ("dtype", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
 _lib = None
 
 
@@ -58,6 +92,23 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.topkp_sort.restype = c_int
     lib.topkp_sort_static.argtypes = [vp, i64, i64, i64, c_int, vp, vp, vp]
     lib.topkp_sort_static.restype = c_int
+    lib.topkp_beam_select_workspace_size.argtypes = [i64, i64, i64, c_int, ctypes.c_int32]
+    lib.topkp_beam_select_workspace_size.restype = ctypes.c_size_t
+    lib.topkp_beam_select.argtypes = [vp, i64, i64, i64, i64, c_int, vp, vp, ctypes.c_int32, ctypes.c_int32, vp, vp, vp,
+                                      vp, ctypes.c_size_t, vp]
+    lib.topkp_beam_select.restype = c_int
+    lib.topkp_beam_reorder.argtypes = [ctypes.POINTER(State), i64, i64, i64, vp, vp, vp]
+    lib.topkp_beam_reorder.restype = c_int
+    lib.topkp_cache_write.argtypes = [vp, vp, i64, i64, i64, i64, i64, i64, i64, c_int, vp, ctypes.POINTER(Cache),
+                                      ctypes.POINTER(Cache), i64, i64, vp]
+    lib.topkp_cache_write.restype = c_int
+    lib.topkp_cache_read.argtypes = [vp, i64, i64, i64, ctypes.POINTER(Cache), ctypes.POINTER(Cache), i64, i64, c_int,
+                                     vp, vp, vp]
+    lib.topkp_cache_read.restype = c_int
+    lib.topkp_tree_attention_workspace_size.argtypes = [ctypes.POINTER(TreeAttentionArgs)]
+    lib.topkp_tree_attention_workspace_size.restype = ctypes.c_size_t
+    lib.topkp_tree_attention.argtypes = [ctypes.POINTER(TreeAttentionArgs), vp]
+    lib.topkp_tree_attention.restype = c_int
     lib.topkp_last_error_string.argtypes = []
     lib.topkp_last_error_string.restype = ctypes.c_char_p
     lib.topkp_device_status.argtypes = [vp]

@@ -1,0 +1,437 @@
+// topkp_beam_select: the best continuations of each request's beams.
+//
+// Within one row the candidates' order is the order of the logits, since
+// score and normaliser shift a row as a whole.  So one pass over the logits
+// gives everything: each CTA holds a slice of a row in registers, sums its
+// exponentials, and lists the slice's n largest logits; a second kernel, one
+// CTA per request, turns those into scores and takes the n best.
+//
+// The sum.  exp(x) = 2^(x log2 e).  A slice sums 2^(x log2 e - c) with c the
+// integer ceil(max x log2 e): slices (and rows) then combine by exact powers
+// of two, and the largest term is in (1/2, 1].
+//
+// The n largest of a slice.  Disjoint units of elements (the elements of one
+// or of a few threads) each have a maximum; the n-th largest of those maxima
+// is reached by at least n elements, and hardly any more when there are many
+// units.  Every element not below it is listed, and each listed element's
+// rank is the number of listed ones before it in the order (value
+// descending, index ascending).  Rows of many equal values overflow the list
+// and take n rounds of a block-wide maximum instead.
+#include "common.cuh"
+#include "decode.h"
+
+namespace topkp {
+namespace {
+
+constexpr int kList = 1024;  // listed candidates of a slice, and of a request
+constexpr float kLog2eHi = 1.44268798828125f;  // log2 e to 16 bits
+constexpr float kLog2eLo = 7.0526077e-06f;     // the rest
+// Logits beyond this magnitude count as this magnitude in the normaliser and
+// the score (a mask may have put the type's lowest value there); their order
+// within the row stays their own.
+constexpr float kFar = 60000.0f;
+
+template <int DT>
+__device__ __forceinline__ float elem(const uint4& q, int j) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  if (DT == TOPKP_F32) return __uint_as_float(w[j]);
+  return DType<DT>::to_float((typename DType<DT>::raw)(w[j >> 1] >> (16 * (j & 1))));
+}
+template <int DT>
+__device__ __forceinline__ typename DType<DT>::raw elem_raw(const uint4& q, int j) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  if (DT == TOPKP_F32) return (typename DType<DT>::raw)w[j];
+  return (typename DType<DT>::raw)(w[j >> 1] >> (16 * (j & 1)));
+}
+
+// A double as an unsigned key of the same order; 0 stands for no candidate.
+__device__ __forceinline__ unsigned long long double_key(double d) {
+  const unsigned long long u = (unsigned long long)__double_as_longlong(d + 0.0);
+  return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double key_double(unsigned long long k) {
+  const unsigned long long u = (k >> 63) ? (k & 0x7fffffffffffffffull) : ~k;
+  return __longlong_as_double((long long)u);
+}
+
+constexpr int kBW = kBeamThreads / 32;
+
+template <int DT, int NV>
+__global__ void __launch_bounds__(kBeamThreads) beam_scan(const BeamArgs a) {
+  using raw = typename DType<DT>::raw;
+  constexpr int VEC = 16 / (int)sizeof(raw);
+  __shared__ unsigned long long list[kList];
+  __shared__ float unit[kBeamThreads];
+  __shared__ float wmax[kBW];
+  __shared__ double wsum[kBW];
+  __shared__ unsigned long long wkey[kBW];
+  __shared__ float tau_s;
+  __shared__ int count;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t part = blockIdx.x;
+  const int64_t row = part / a.slices;
+  const int slice = (int)(part - row * a.slices);
+  unsigned long long* out = a.cand + part * a.n;
+
+  const float score = a.scores[row];
+  if ((a.finished && a.finished[row]) || score == -INFINITY) {
+    if (tid == 0) a.stat[part] = make_double2(0.0, 0.0);
+    for (int i = tid; i < a.n; i += kBeamThreads) out[i] = 0ull;
+    return;
+  }
+
+  // 16-byte vectors of the row's aligned window; a vector that sticks out of
+  // the row is read element by element
+  const raw* xr = reinterpret_cast<const raw*>(a.x) + row * a.ldx;
+  const int head = (int)((reinterpret_cast<uintptr_t>(xr) & 15) / sizeof(raw));
+  const int e0 = slice * (kBeamThreads * NV * VEC) - head;  // row index of this slice's first element
+  uint4 q[NV];
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    const int e = e0 + (u * kBeamThreads + tid) * VEC;
+    if (e >= 0 && e + VEC <= a.V) {
+      q[u] = __ldcs(reinterpret_cast<const uint4*>(xr + e));
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = DT == TOPKP_F32 ? 0xff800000u : DType<DT>::kNegInf * 0x10001u;
+      if (e < a.V && e + VEC > 0) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          if (e + j >= 0 && e + j < a.V) {
+            const uint32_t r = xr[e + j];
+            if (DT == TOPKP_F32) w[j] = r;
+            else w[j >> 1] = (j & 1) ? ((w[j >> 1] & 0xffffu) | (r << 16)) : ((w[j >> 1] & 0xffff0000u) | r);
+          }
+        }
+      }
+      q[u] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+
+  float m = -INFINITY;
+#pragma unroll
+  for (int u = 0; u < NV; ++u)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) m = fmaxf(m, elem<DT>(q[u], j));
+  // units of 1, 2 or 4 threads, at least 2 n of them
+  const int per = a.n <= 32 ? 4 : a.n <= 64 ? 2 : 1;
+  float um = m;
+  if (per >= 2) um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, 1));
+  if (per >= 4) um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, 2));
+  if (tid % per == 0) unit[tid / per] = um;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) wmax[warp] = m;
+  if (tid == 0) {
+    count = 0;
+    tau_s = -INFINITY;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kBW; ++i) m = fmaxf(m, wmax[i]);
+  const int units = kBeamThreads / per;
+  if (tid < units) {
+    const float mine = unit[tid];
+    int rank = 0;
+    for (int i = 0; i < units; ++i) rank += (unit[i] > mine || (unit[i] == mine && i < tid)) ? 1 : 0;
+    if (rank == a.n - 1) tau_s = mine;
+  }
+  const float c = m == -INFINITY ? 0.0f : ceilf(fminf(fmaxf(m, -kFar), kFar) * (kLog2eHi + kLog2eLo));
+  auto term = [&](float x) {
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(x, kLog2eLo, fmaf(x, kLog2eHi, -c))));
+    return e;
+  };
+  float sum = 0.0f;
+  if (fabsf(m) <= kFar) {
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) sum += term(elem<DT>(q[u], j));
+  } else if (m > -INFINITY) {
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const float x = elem<DT>(q[u], j);
+        if (x > -INFINITY) sum += term(fminf(fmaxf(x, -kFar), kFar));
+      }
+  }
+  double total = (double)sum;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (lane == 0) wsum[warp] = total;
+  __syncthreads();
+  if (tid == 0) {
+    total = 0.0;
+    for (int i = 0; i < kBW; ++i) total += wsum[i];
+    a.stat[part] = make_double2((double)c, total);
+  }
+
+  const float tau = tau_s;
+#pragma unroll
+  for (int u = 0; u < NV; ++u)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const float x = elem<DT>(q[u], j);
+      if (x >= tau && x > -INFINITY) {
+        const int at = atomicAdd(&count, 1);
+        const uint32_t idx = (uint32_t)(e0 + (u * kBeamThreads + tid) * VEC + j);
+        if (at < kList) list[at] = ((unsigned long long)order_key<DT>(elem_raw<DT>(q[u], j)) << 32) | (uint32_t)~idx;
+      }
+    }
+  __syncthreads();
+  const int found = count;
+  if (found <= kList) {
+    for (int i = tid; i < found; i += kBeamThreads) {
+      const unsigned long long mine = list[i];
+      int rank = 0;
+      for (int j = 0; j < found; ++j) rank += list[j] > mine ? 1 : 0;
+      if (rank < a.n) out[rank] = mine;
+    }
+    for (int i = found + tid; i < a.n; i += kBeamThreads) out[i] = 0ull;
+    return;
+  }
+  // many equal values: the next one in order, n times
+  unsigned long long last = ~0ull;
+  for (int r = 0; r < a.n; ++r) {
+    unsigned long long best = 0ull;
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const float x = elem<DT>(q[u], j);
+        const uint32_t idx = (uint32_t)(e0 + (u * kBeamThreads + tid) * VEC + j);
+        const unsigned long long key =
+            ((unsigned long long)order_key<DT>(elem_raw<DT>(q[u], j)) << 32) | (uint32_t)~idx;
+        if (x >= tau && x > -INFINITY && key < last && key > best) best = key;
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const unsigned long long w = __shfl_xor_sync(0xffffffffu, best, o);
+      best = w > best ? w : best;
+    }
+    if (lane == 0) wkey[warp] = best;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kBW; ++i) best = wkey[i] > best ? wkey[i] : best;
+    __syncthreads();
+    if (tid == 0) out[r] = best;
+    last = best;
+  }
+}
+
+// One CTA per request.  Entry i of list l (a slice of a beam) is candidate
+// (score of the beam + logit - normaliser); the lists are descending, so the
+// d-th entry of a list bounds d candidates from below, and the q-th largest
+// of those (q d >= n) bounds n.
+template <int DT>
+__global__ void __launch_bounds__(kBeamThreads) beam_merge(const BeamArgs a) {
+  __shared__ unsigned long long key[kList];
+  __shared__ uint32_t flat[kList];  // ~(k * V + v): larger is earlier
+  __shared__ unsigned long long unit[kBeamThreads];
+  __shared__ double shift[TOPKP_MAX_BEAMS];  // score - normaliser; the score itself where finished
+  __shared__ uint8_t state[TOPKP_MAX_BEAMS];  // 0: no candidate, 1: live, 2: finished
+  __shared__ unsigned long long tau_s, wk[kBW];
+  __shared__ uint32_t wf[kBW];
+  __shared__ int count;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t b = blockIdx.x;
+  const int n = a.n, S = a.slices;
+
+  for (int k = warp; k < a.K; k += kBW) {
+    const int64_t row = b * a.K + k;
+    const float score = a.scores[row];
+    const bool done = a.finished && a.finished[row];
+    float c = -INFINITY;
+    for (int s = lane; s < S; s += 32) {
+      const double2 st = a.stat[row * S + s];
+      if (st.y > 0.0) c = fmaxf(c, (float)st.x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, o));
+    double l = 0.0;
+    for (int s = lane; s < S; s += 32) {
+      const double2 st = a.stat[row * S + s];
+      // 2^(st.x - c), an exact power of two
+      if (st.y > 0.0) l += st.y * (double)__int_as_float((127 + max((int)((float)st.x - c), -126)) << 23);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) {
+      const bool live = !done && score != -INFINITY && l > 0.0;
+      state[k] = done ? (score != -INFINITY ? 2 : 0) : live ? 1 : 0;
+      shift[k] = done ? (double)score : live ? (double)score - (log(l) + (double)c * 0.693147180559945309417) : 0.0;
+    }
+  }
+  if (tid == 0) {
+    count = 0;
+    tau_s = 0ull;
+  }
+  __syncthreads();
+
+  const int lists = a.K * S;
+  const unsigned long long* cand = a.cand + b * lists * (int64_t)n;
+  // entry i of list l: its key and place (key 0: none)
+  auto entry = [&](int l, int i, uint32_t* f) -> unsigned long long {
+    const int k = l / S;
+    const int st = state[k];
+    if (st == 0) return 0ull;
+    if (st == 2) {
+      *f = ~(uint32_t)(k * a.V + a.pad);
+      return (l == k * S && i == 0) ? double_key(shift[k]) : 0ull;
+    }
+    const unsigned long long e = cand[(int64_t)l * n + i];
+    if (e == 0ull) return 0ull;
+    *f = ~(uint32_t)(k * a.V + (int)~(uint32_t)e);
+    const float x = value_of_key<DT>((uint32_t)(e >> 32));
+    return double_key(shift[k] + (double)fminf(fmaxf(x, -kFar), kFar));
+  };
+
+  const int depth = lists >= n ? 1 : (n + lists - 1) / lists;
+  const int want = (n + depth - 1) / depth;
+  if (lists * (int64_t)n > kList / 2) {
+    unsigned long long mine = 0ull;
+    uint32_t f;
+    for (int l = tid; l < lists; l += kBeamThreads) {
+      const unsigned long long e = entry(l, depth - 1, &f);
+      mine = e > mine ? e : mine;
+    }
+    unit[tid] = mine;
+    __syncthreads();
+    int rank = 0;
+    for (int i = 0; i < kBeamThreads; ++i) rank += (unit[i] > mine || (unit[i] == mine && i < tid)) ? 1 : 0;
+    if (rank == want - 1) tau_s = mine;
+    __syncthreads();
+  }
+  const unsigned long long tau = tau_s > 0ull ? tau_s : 1ull;
+  for (int l = warp; l < lists; l += kBW)
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      uint32_t f = 0;
+      const unsigned long long e = i0 + lane < n ? entry(l, i0 + lane, &f) : 0ull;
+      if (e >= tau) {
+        const int at = atomicAdd(&count, 1);
+        if (at < kList) {
+          key[at] = e;
+          flat[at] = f;
+        }
+      }
+      if (__shfl_sync(0xffffffffu, e, 31) < tau) break;
+    }
+  __syncthreads();
+  const int found = count;
+  float* os = a.out_score + b * n;
+  int32_t* op = a.out_parent + b * n;
+  int32_t* ot = a.out_token + b * n;
+  auto put = [&](int r, unsigned long long e, uint32_t f) {
+    const uint32_t p = ~f;
+    os[r] = (float)key_double(e);
+    op[r] = (int32_t)(p / (uint32_t)a.V);
+    ot[r] = (int32_t)(p % (uint32_t)a.V);
+  };
+  auto none = [&](int r) {
+    os[r] = -INFINITY;
+    op[r] = r % a.K;
+    ot[r] = -1;
+  };
+  if (found <= kList) {
+    for (int i = tid; i < found; i += kBeamThreads) {
+      const unsigned long long e = key[i];
+      const uint32_t f = flat[i];
+      int rank = 0;
+      for (int j = 0; j < found; ++j) rank += (key[j] > e || (key[j] == e && flat[j] > f)) ? 1 : 0;
+      if (rank < n) put(rank, e, f);
+    }
+    for (int r = found + tid; r < n; r += kBeamThreads) none(r);
+    return;
+  }
+  // many equal candidates: the next one in order, n times
+  unsigned long long le = ~0ull;
+  uint32_t lf = ~0u;
+  for (int r = 0; r < n; ++r) {
+    unsigned long long be = 0ull;
+    uint32_t bf = 0;
+    for (int l = tid; l < lists; l += kBeamThreads)
+      for (int i = 0; i < n; ++i) {
+        uint32_t f = 0;
+        const unsigned long long e = entry(l, i, &f);
+        if (e < tau) break;
+        if (e < be || (e == be && f < bf)) break;
+        if (e < le || (e == le && f < lf)) {
+          be = e;
+          bf = f;
+          break;
+        }
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const unsigned long long e = __shfl_xor_sync(0xffffffffu, be, o);
+      const uint32_t f = __shfl_xor_sync(0xffffffffu, bf, o);
+      if (e > be || (e == be && f > bf)) {
+        be = e;
+        bf = f;
+      }
+    }
+    if (lane == 0) {
+      wk[warp] = be;
+      wf[warp] = bf;
+    }
+    __syncthreads();
+    be = wk[0];
+    bf = wf[0];
+    for (int i = 1; i < kBW; ++i)
+      if (wk[i] > be || (wk[i] == be && wf[i] > bf)) {
+        be = wk[i];
+        bf = wf[i];
+      }
+    __syncthreads();
+    if (tid == 0) {
+      if (be) put(r, be, bf);
+      else none(r);
+    }
+    le = be;
+    lf = bf;
+  }
+}
+
+template <int DT>
+cudaError_t launch_dt(const BeamArgs& a, cudaStream_t s) {
+  const unsigned int grid = (unsigned int)(a.B * a.K * a.slices);
+  switch (a.nv) {
+    case 1: beam_scan<DT, 1><<<grid, kBeamThreads, 0, s>>>(a); break;
+    case 2: beam_scan<DT, 2><<<grid, kBeamThreads, 0, s>>>(a); break;
+    case 4: beam_scan<DT, 4><<<grid, kBeamThreads, 0, s>>>(a); break;
+    default: beam_scan<DT, 8><<<grid, kBeamThreads, 0, s>>>(a); break;
+  }
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  beam_merge<DT><<<(unsigned int)a.B, kBeamThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// The longest slices that still give every SM two CTAs.
+BeamPlan plan_beam(int64_t rows, int64_t V, int esize, int32_t n, int num_sms) {
+  BeamPlan p;
+  const int vec = 16 / esize;
+  p.nv = kBeamMaxVec;
+  // the aligned window may start up to vec - 1 elements before the row
+  auto slices = [&](int nv) { return (V + vec - 1 + (int64_t)kBeamThreads * nv * vec - 1) / ((int64_t)kBeamThreads * nv * vec); };
+  while (p.nv > 1 && rows * slices(p.nv) < 2LL * num_sms) p.nv /= 2;
+  p.slices = (int)slices(p.nv);
+  p.stat_bytes = ((size_t)rows * p.slices * sizeof(double2) + 255) / 256 * 256;
+  p.cand_bytes = (size_t)rows * p.slices * n * sizeof(unsigned long long);
+  return p;
+}
+
+cudaError_t launch_beam(topkp_dtype dt, const BeamArgs& a, cudaStream_t s) {
+  switch (dt) {
+    case TOPKP_F32: return launch_dt<TOPKP_F32>(a, s);
+    case TOPKP_F16: return launch_dt<TOPKP_F16>(a, s);
+    default: return launch_dt<TOPKP_BF16>(a, s);
+  }
+}
+
+}  // namespace topkp

@@ -1,0 +1,330 @@
+"""Decoding with several hypotheses at once: beams and drafted tokens.
+
+Python face of include/topkp_decode.h, next to the logit filter and with its
+manner: CUDA tensors in, the calling thread's current stream, no CPU path.
+
+    score, parent, token = beam_select(logits, scores, n, finished=None, pad_token=0)
+    states = beam_reorder(states, parent, lengths=None, out=None)
+    cache_write(k, v, slots, k_cache, v_cache, k_exp=None, v_exp=None)
+    k, v = cache_read(slots, k_cache, v_cache, k_exp=None, v_exp=None, dtype=None)
+    out = tree_attention(q, k_cache, v_cache, context, pages=None, tree=None, ...)
+
+A cache is [pages, page_size, heads, dim] with a block table, or
+[requests, capacity, heads, dim] without one; its elements are of the rows'
+type, or ``torch.float8_e4m3fn`` with a uint8 exponent for each (page, token,
+head).  Every call runs forward only: none records a gradient.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import _lib
+
+
+def _base():
+    import top_logit_filter_gb300 as base  # the shared helpers; the package imports this module at its end
+    return base
+
+
+def _cuda(t, name, dim=None, dtype=None, device=None):
+    torch = _base()._torch()
+    if not torch.is_tensor(t) or not t.is_cuda or (dim is not None and t.dim() != dim):
+        raise ValueError(f"{name} must be a {'' if dim is None else str(dim) + '-D '}CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    return t
+
+
+def _workspace(workspace, need, device):
+    torch = _base()._torch()
+    if workspace is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    if workspace.dtype != torch.uint8 or workspace.device != device or workspace.numel() < need:
+        raise ValueError(f"workspace must be a uint8 tensor of at least {need} bytes on {device}")
+    return workspace
+
+
+def beam_select(logits, scores, n: int, finished=None, pad_token: int = 0, workspace=None):
+    """One step of beam search (topkp_beam_select).
+
+    logits: [B * K, V] CUDA tensor (float32, float16 or bfloat16); scores:
+    [B, K] float32, the beams' summed log-probabilities (-inf: no beam);
+    finished: [B, K] bool or uint8, beams that go on with ``pad_token`` only,
+    at their score.  Returns (score [B, n] float32 descending, parent [B, n]
+    int32, token [B, n] int32); a slot without a candidate holds -inf, its
+    index mod K and -1.  ``workspace``: a uint8 tensor of at least
+    ``beam_select_workspace_size`` bytes (allocated when None)."""
+    base = _base()
+    torch, lib = base._torch(), _lib.load()
+    _cuda(logits, "logits", 2)
+    dt, dev = base._dtype_code(logits), logits.device
+    _cuda(scores, "scores", 2, torch.float32, dev)
+    B, K = scores.shape
+    R, V = logits.shape
+    if R != B * K:
+        raise ValueError(f"logits has {R} rows; scores has {B} x {K}")
+    if logits.stride(1) != 1 and V > 1:
+        logits = logits.contiguous()
+    scores = scores.contiguous()
+    if finished is not None:
+        _cuda(finished, "finished", 2, None, dev)
+        if finished.shape != (B, K) or finished.dtype not in (torch.bool, torch.uint8):
+            raise ValueError("finished must be a bool or uint8 tensor shaped like scores")
+        finished = finished.contiguous()
+    n = int(n)
+    need = int(lib.topkp_beam_select_workspace_size(B, K, V, dt, n))
+    workspace = _workspace(workspace, need, dev)
+    score = torch.empty((B, max(n, 0)), dtype=torch.float32, device=dev)
+    parent = torch.empty((B, max(n, 0)), dtype=torch.int32, device=dev)
+    token = torch.empty((B, max(n, 0)), dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        base._check(lib.topkp_beam_select(base._ptr(logits), B, K, V, logits.stride(0) if R > 1 else V, dt,
+                                          base._ptr(scores), base._ptr(finished), int(pad_token), n, base._ptr(score),
+                                          base._ptr(parent), base._ptr(token), base._ptr(workspace),
+                                          workspace.numel(), base._stream(dev)))
+    return score, parent, token
+
+
+def beam_select_workspace_size(B: int, K: int, V: int, dtype, n: int) -> int:
+    """Bytes of workspace ``beam_select`` needs."""
+    torch = _base()._torch()
+    codes = {torch.float32: _lib.TOPKP_F32, torch.float16: _lib.TOPKP_F16, torch.bfloat16: _lib.TOPKP_BF16}
+    return int(_lib.load().topkp_beam_select_workspace_size(B, K, V, codes[dtype], n))
+
+
+def _layout(t, time_dim, name):
+    """(row stride, block stride, blocks, entries, entry bytes) of a state in bytes."""
+    es = t.element_size()
+    shape, stride = list(t.shape), list(t.stride())
+    if not 1 <= time_dim < max(t.dim(), 2):
+        raise ValueError(f"time_dim {time_dim} of a {t.dim()}-D {name}")
+
+    def run(dims):  # (elements, stride of the innermost step) of dimensions that lie densely in each other
+        count, step = 1, None
+        for d in reversed(dims):
+            if shape[d] == 1:
+                continue
+            if step is None:
+                step = stride[d]
+            elif stride[d] != step * count:
+                raise ValueError(f"{name} must be dense within a row (shape {tuple(shape)}, strides {tuple(stride)})")
+            count *= shape[d]
+        return count, step
+
+    inner = list(range(time_dim, t.dim()))
+    total, step = run(inner)
+    if total > 1 and step != 1:
+        raise ValueError(f"{name} must be dense within a row (shape {tuple(shape)}, strides {tuple(stride)})")
+    entries = shape[time_dim] if t.dim() > 1 else 1
+    blocks, block_step = run(list(range(1, time_dim)))
+    if 0 in shape:
+        return 0, 0, 0, 0, 0
+    row = stride[0] if shape[0] > 1 else max(total, (blocks - 1) * (block_step or 0) + total)
+    return row * es, (block_step if blocks > 1 else total) * es, blocks, entries, total // entries * es
+
+
+def beam_reorder(states, parent, lengths=None, time_dim: int = 1, out=None):
+    """The beams' states follow their parents (topkp_beam_reorder).
+
+    states: one tensor or a sequence of them, each [B * K, ...] and dense
+    within a row, of any dtype; parent: [B, K] int32.  Row b * K + j becomes
+    row b * K + parent[b, j], in place, or in ``out`` (tensors like
+    ``states``).  lengths: [B, K] int32, how many entries along ``time_dim``
+    of each row are live: only they move, and the rest of a destination row
+    keeps what it held.  Returns the reordered tensors."""
+    base = _base()
+    torch, lib = base._torch(), _lib.load()
+    single = torch.is_tensor(states)
+    src = [states] if single else list(states)
+    dst = src if out is None else [out] if torch.is_tensor(out) else list(out)
+    if len(dst) != len(src):
+        raise ValueError(f"{len(src)} states and {len(dst)} outputs")
+    if not torch.is_tensor(parent) or not parent.is_cuda or parent.dim() != 2 or parent.dtype != torch.int32:
+        raise ValueError("parent must be a 2-D int32 CUDA tensor")
+    dev = parent.device
+    B, K = parent.shape
+    parent = parent.contiguous()
+    if lengths is not None:
+        _cuda(lengths, "lengths", 2, torch.int32, dev)
+        if lengths.shape != (B, K):
+            raise ValueError("lengths must be shaped like parent")
+        lengths = lengths.contiguous()
+    table = (_lib.State * max(len(src), 1))()
+    for i, (s, d) in enumerate(zip(src, dst)):
+        for t in (s, d):
+            _cuda(t, f"states[{i}]", None, None, dev)
+            if t.dim() < 1 or t.shape[0] != B * K or t.shape != s.shape or t.dtype != s.dtype:
+                raise ValueError(f"states[{i}] must have {B} x {K} rows, and its output its shape and dtype")
+        row, blk, blocks, entries, size = _layout(s, time_dim if s.dim() > 1 else 1, f"states[{i}]")
+        drow, dblk = _layout(d, time_dim if d.dim() > 1 else 1, f"out[{i}]")[:2]
+        table[i] = _lib.State(base._ptr(s), base._ptr(d), row, drow, blk, dblk, blocks, entries, size)
+    with torch.cuda.device(dev):
+        base._check(lib.topkp_beam_reorder(table, len(src), B, K, base._ptr(parent), base._ptr(lengths),
+                                           base._stream(dev)))
+    return dst[0] if single else dst
+
+
+def _cache(t, exp, name, device, row_dtype):
+    base = _base()
+    torch = base._torch()
+    _cuda(t, name, 4, None, device)
+    quant = t.dtype == torch.float8_e4m3fn
+    if not quant and t.dtype != row_dtype:
+        raise TypeError(f"{name} must be {row_dtype} or torch.float8_e4m3fn, not {t.dtype}")
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"{name}: a head's elements must be contiguous")
+    if quant != (exp is not None):
+        raise ValueError(f"{name}: exponents go with torch.float8_e4m3fn, and only with it")
+    c = _lib.Cache(base._ptr(t), None, _lib.TOPKP_E4M3 if quant else base._dtype_code(t), t.stride(0), t.stride(1),
+                   t.stride(2), 0, 0, 0)
+    if quant:
+        _cuda(exp, f"{name}'s exponents", 3, torch.uint8, device)
+        if exp.shape != t.shape[:3]:
+            raise ValueError(f"{name}'s exponents must be {tuple(t.shape[:3])}, not {tuple(exp.shape)}")
+        c.exponents = base._ptr(exp)
+        c.exp_page_stride, c.exp_token_stride, c.exp_head_stride = exp.stride()
+    return c
+
+
+def _pair(k_cache, v_cache):
+    if k_cache.shape != v_cache.shape:
+        raise ValueError(f"k_cache is {tuple(k_cache.shape)} and v_cache {tuple(v_cache.shape)}")
+
+
+def cache_write(k, v, slots, k_cache, v_cache, k_exp=None, v_exp=None):
+    """Rows of keys and values into a cache (topkp_cache_write).
+
+    k, v: [N, H, D] CUDA tensors (float32, float16 or bfloat16; heads and
+    tokens may be strided); slots: [N] int64, page * page_size + place, -1 to
+    skip a row; k_cache, v_cache: [pages, page_size, H, D], of the rows'
+    dtype, or float8_e4m3fn with k_exp, v_exp [pages, page_size, H] uint8,
+    quantised as they are written.  v and v_cache may both be None."""
+    base = _base()
+    torch, lib = base._torch(), _lib.load()
+    _cuda(k, "k", 3)
+    dt, dev = base._dtype_code(k), k.device
+    N, H, D = k.shape
+    rows = [k] if v is None else [k, v]
+    if (v is None) != (v_cache is None):
+        raise ValueError("v and v_cache go together")
+    for i, t in enumerate(rows):
+        _cuda(t, "kv"[i], 3, k.dtype, dev)
+        if t.shape != k.shape:
+            raise ValueError(f"v is {tuple(t.shape)} and k {tuple(k.shape)}")
+        if t.stride(2) != 1 and D > 1:
+            rows[i] = t.contiguous()
+    _cuda(slots, "slots", 1, torch.int64, dev)
+    if slots.shape[0] != N:
+        raise ValueError(f"{N} rows and {slots.shape[0]} slots")
+    slots = slots.contiguous()
+    kc = _cache(k_cache, k_exp, "k_cache", dev, k.dtype)
+    vc = None
+    if v is not None:
+        vc = _cache(v_cache, v_exp, "v_cache", dev, k.dtype)
+        _pair(k_cache, v_cache)
+    if tuple(k_cache.shape[2:]) != (H, D):
+        raise ValueError(f"rows are {H} x {D} and the cache's {tuple(k_cache.shape[2:])}")
+    last = rows[-1]
+    with torch.cuda.device(dev):
+        base._check(lib.topkp_cache_write(
+            base._ptr(rows[0]), base._ptr(last) if v is not None else None, N, H, D, rows[0].stride(0),
+            rows[0].stride(1), last.stride(0), last.stride(1), dt, base._ptr(slots), ctypes.byref(kc),
+            ctypes.byref(vc) if vc is not None else None, k_cache.shape[0], k_cache.shape[1], base._stream(dev)))
+
+
+def cache_read(slots, k_cache, v_cache, k_exp=None, v_exp=None, dtype=None):
+    """The cache's entries as dense rows (topkp_cache_read): (k, v), each
+    [N, H, D] of ``dtype`` (the cache's own, or any of the three for an e4m3
+    cache, bfloat16 when None).  A slot outside the cache gives zeros.
+    v_cache may be None; v is then None."""
+    base = _base()
+    torch, lib = base._torch(), _lib.load()
+    _cuda(slots, "slots", 1, torch.int64)
+    dev = slots.device
+    slots = slots.contiguous()
+    _cuda(k_cache, "k_cache", 4, None, dev)
+    if dtype is None:
+        dtype = torch.bfloat16 if k_cache.dtype == torch.float8_e4m3fn else k_cache.dtype
+    kc = _cache(k_cache, k_exp, "k_cache", dev, dtype)
+    vc = None
+    if v_cache is not None:
+        vc = _cache(v_cache, v_exp, "v_cache", dev, dtype)
+        _pair(k_cache, v_cache)
+    N, (H, D) = slots.shape[0], k_cache.shape[2:]
+    k = torch.empty((N, H, D), dtype=dtype, device=dev)
+    v = torch.empty((N, H, D), dtype=dtype, device=dev) if vc is not None else None
+    with torch.cuda.device(dev):
+        base._check(lib.topkp_cache_read(base._ptr(slots), N, H, D, ctypes.byref(kc),
+                                         ctypes.byref(vc) if vc is not None else None, k_cache.shape[0],
+                                         k_cache.shape[1], base._dtype_code(k), base._ptr(k), base._ptr(v),
+                                         base._stream(dev)))
+    return k, v
+
+
+def tree_attention(q, k_cache, v_cache, context, pages=None, tree=None, nodes=None, k_exp=None, v_exp=None,
+                   scale=None, max_context=None, out=None, want_lse: bool = False, workspace=None):
+    """Attention of drafted nodes over a cache and each other (topkp_tree_attention).
+
+    q: [B, T, Hq, D] (float16 or bfloat16); k_cache, v_cache:
+    [pages, page_size, Hkv, D] with ``pages`` [B, max_pages] int32 (the block
+    table), or [B, capacity, Hkv, D] without; context: [B] int32, tokens in
+    the cache before the drafted ones, which stand at context[b] + i.  tree:
+    [B, T] int64, bit j of tree[b, i] set where node i sees node j (T <= 64);
+    None is a chain, and T = 1 ordinary decoding.  nodes: [B] int32, how many
+    of the T nodes a request has.  scale: D ** -0.5 when None.  max_context:
+    a bound of ``context`` known on the host, which plans the work (the
+    capacity when None).  Returns out ([B, T, Hq, D]), or (out, lse) with
+    lse [B, T, Hq] float32."""
+    base = _base()
+    torch, lib = base._torch(), _lib.load()
+    _cuda(q, "q", 4)
+    if q.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"q must be float16 or bfloat16, not {q.dtype}")
+    dev = q.device
+    B, T, Hq, D = q.shape
+    if D > 1 and q.stride(3) != 1:
+        q = q.contiguous()
+    kc = _cache(k_cache, k_exp, "k_cache", dev, q.dtype)
+    vc = _cache(v_cache, v_exp, "v_cache", dev, q.dtype)
+    _pair(k_cache, v_cache)
+    pool, page_size, Hkv, Dc = k_cache.shape
+    if Dc != D:
+        raise ValueError(f"head dimension {D} of q and {Dc} of the cache")
+    context = base._vec(context, B, torch.int32, "context", dev)
+    nodes = base._vec(nodes, B, torch.int32, "nodes", dev)
+    if pages is not None:
+        _cuda(pages, "pages", 2, torch.int32, dev)
+        if pages.shape[0] != B:
+            raise ValueError(f"pages has {pages.shape[0]} rows and q {B} requests")
+        if pages.shape[1] > 1 and pages.stride(1) != 1:
+            pages = pages.contiguous()
+    elif pool != B:
+        raise ValueError(f"without a block table the cache holds one entry a request ({B}), not {pool}")
+    if tree is not None:
+        _cuda(tree, "tree", 2, torch.int64, dev)
+        if tree.shape != (B, T):
+            raise ValueError(f"tree must be {(B, T)}, not {tuple(tree.shape)}")
+        tree = tree.contiguous()
+    if out is None:
+        out = torch.empty((B, T, Hq, D), dtype=q.dtype, device=dev)
+    if out.shape != q.shape or out.dtype != q.dtype or out.device != dev or (D > 1 and out.stride(3) != 1):
+        raise ValueError("out must match q in shape, dtype and device, with its last dimension contiguous")
+    lse = torch.empty((B, T, Hq), dtype=torch.float32, device=dev) if want_lse else None
+    max_pages = 1 if pages is None else pages.shape[1]
+    a = _lib.TreeAttentionArgs(
+        q=base._ptr(q), out=base._ptr(out), lse=base._ptr(lse), k=kc, v=vc, table=base._ptr(pages),
+        context=base._ptr(context), nodes=base._ptr(nodes), tree=base._ptr(tree), B=B, T=T, Hq=Hq, Hkv=Hkv, D=D,
+        pages=pool, page_size=page_size, max_pages=max_pages, ld_table=0 if pages is None else (pages.stride(0) if B > 1 else max_pages),
+        max_context=max_pages * page_size if max_context is None else int(max_context),
+        q_batch_stride=q.stride(0), q_token_stride=q.stride(1), q_head_stride=q.stride(2),
+        out_batch_stride=out.stride(0), out_token_stride=out.stride(1), out_head_stride=out.stride(2),
+        dtype=base._dtype_code(q), scale=float(D) ** -0.5 if scale is None else float(scale))
+    need = int(lib.topkp_tree_attention_workspace_size(ctypes.byref(a)))
+    if need:
+        workspace = _workspace(workspace, need, dev)
+        a.workspace, a.workspace_bytes = base._ptr(workspace), workspace.numel()
+    with torch.cuda.device(dev):
+        base._check(lib.topkp_tree_attention(ctypes.byref(a), base._stream(dev)))
+    return (out, lse) if want_lse else out

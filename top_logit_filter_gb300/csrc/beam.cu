@@ -23,7 +23,8 @@
 namespace topkp {
 namespace {
 
-constexpr int kList = 1024;  // listed candidates of a slice, and of a request
+constexpr int kList = 1024;   // listed candidates of a slice, and of a request
+constexpr int kHeads = 1024;  // lists whose first entries a request holds on chip
 constexpr float kLog2eHi = 1.44268798828125f;  // log2 e to 16 bits
 constexpr float kLog2eLo = 7.0526077e-06f;     // the rest
 // Logits beyond this magnitude count as this magnitude in the normaliser and
@@ -56,22 +57,67 @@ __device__ __forceinline__ double key_double(unsigned long long k) {
 
 constexpr int kBW = kBeamThreads / 32;
 
+// Two fp32 lanes in a 64-bit register, one instruction for both.
+__device__ __forceinline__ unsigned long long f32x2(float lo, float hi) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ unsigned long long fma_x2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ unsigned long long add_x2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float ex2(float t) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  return e;
+}
+// 2^(x log2 e - c) of two logits.
+__device__ __forceinline__ unsigned long long terms(float x0, float x1, unsigned long long c2) {
+  const unsigned long long x = f32x2(x0, x1);
+  const unsigned long long t =
+      fma_x2(x, f32x2(kLog2eLo, kLog2eLo), fma_x2(x, f32x2(kLog2eHi, kLog2eHi), c2));
+  float t0, t1;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(t0), "=f"(t1) : "l"(t));
+  return f32x2(ex2(t0), ex2(t1));
+}
+// The largest element of a vector (packed 16-bit maxima; NaN is passed over).
+template <int DT>
+__device__ __forceinline__ float vec_max(const uint4& q) {
+  if (DT == TOPKP_F32)
+    return fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)), fmaxf(__uint_as_float(q.z), __uint_as_float(q.w)));
+  uint32_t m;
+  if (DT == TOPKP_F16)
+    asm("{.reg .b32 a, b;\n\tmax.f16x2 a, %1, %2;\n\tmax.f16x2 b, %3, %4;\n\tmax.f16x2 %0, a, b;}"
+        : "=r"(m) : "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w));
+  else
+    asm("{.reg .b32 a, b;\n\tmax.bf16x2 a, %1, %2;\n\tmax.bf16x2 b, %3, %4;\n\tmax.bf16x2 %0, a, b;}"
+        : "=r"(m) : "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w));
+  return fmaxf(elem<DT>(make_uint4(m, 0, 0, 0), 0), elem<DT>(make_uint4(m, 0, 0, 0), DT == TOPKP_F32 ? 0 : 1));
+}
+
 template <int DT, int NV>
-__global__ void __launch_bounds__(kBeamThreads) beam_scan(const BeamArgs a) {
+__global__ void __launch_bounds__(kBeamThreads, NV == 4 ? 4 : 6) beam_scan(const BeamArgs a) {
   using raw = typename DType<DT>::raw;
   constexpr int VEC = 16 / (int)sizeof(raw);
   __shared__ unsigned long long list[kList];
-  __shared__ float unit[kBeamThreads];
+  __shared__ __align__(16) float unit[kBeamThreads];
   __shared__ float wmax[kBW];
-  __shared__ double wsum[kBW];
   __shared__ unsigned long long wkey[kBW];
   __shared__ float tau_s;
   __shared__ int count;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t part = blockIdx.x;
-  const int64_t row = part / a.slices;
-  const int slice = (int)(part - row * a.slices);
-  unsigned long long* out = a.cand + part * a.n;
+  const uint32_t part = blockIdx.x;
+  const uint32_t row = part / (uint32_t)a.slices;
+  const int slice = (int)(part - row * (uint32_t)a.slices);
+  unsigned long long* out = a.cand + (int64_t)part * a.n;
 
   const float score = a.scores[row];
   if ((a.finished && a.finished[row]) || score == -INFINITY) {
@@ -86,34 +132,41 @@ __global__ void __launch_bounds__(kBeamThreads) beam_scan(const BeamArgs a) {
   const int head = (int)((reinterpret_cast<uintptr_t>(xr) & 15) / sizeof(raw));
   const int e0 = slice * (kBeamThreads * NV * VEC) - head;  // row index of this slice's first element
   uint4 q[NV];
+  if (e0 >= 0 && e0 + kBeamThreads * NV * VEC <= a.V) {
+    const uint4* p = reinterpret_cast<const uint4*>(xr + e0) + tid;
 #pragma unroll
-  for (int u = 0; u < NV; ++u) {
-    const int e = e0 + (u * kBeamThreads + tid) * VEC;
-    if (e >= 0 && e + VEC <= a.V) {
-      q[u] = __ldcs(reinterpret_cast<const uint4*>(xr + e));
-    } else {
-      uint32_t w[4];
+    for (int u = 0; u < NV; ++u) q[u] = __ldcs(p + u * kBeamThreads);
+  } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = DT == TOPKP_F32 ? 0xff800000u : DType<DT>::kNegInf * 0x10001u;
-      if (e < a.V && e + VEC > 0) {
+    for (int u = 0; u < NV; ++u) {
+      const int e = e0 + (u * kBeamThreads + tid) * VEC;
+      if (e >= 0 && e + VEC <= a.V) {
+        q[u] = __ldcs(reinterpret_cast<const uint4*>(xr + e));
+      } else {
+        uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          if (e + j >= 0 && e + j < a.V) {
-            const uint32_t r = xr[e + j];
-            if (DT == TOPKP_F32) w[j] = r;
-            else w[j >> 1] = (j & 1) ? ((w[j >> 1] & 0xffffu) | (r << 16)) : ((w[j >> 1] & 0xffff0000u) | r);
+        for (int i = 0; i < 4; ++i) w[i] = DT == TOPKP_F32 ? 0xff800000u : DType<DT>::kNegInf * 0x10001u;
+        if (e < a.V && e + VEC > 0) {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) {
+            if (e + j >= 0 && e + j < a.V) {
+              const uint32_t r = xr[e + j];
+              if (DT == TOPKP_F32) w[j] = r;
+              else w[j >> 1] = (j & 1) ? ((w[j >> 1] & 0xffffu) | (r << 16)) : ((w[j >> 1] & 0xffff0000u) | r);
+            }
           }
         }
+        q[u] = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      q[u] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 
-  float m = -INFINITY;
+  float vm[NV], m = -INFINITY;
 #pragma unroll
-  for (int u = 0; u < NV; ++u)
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) m = fmaxf(m, elem<DT>(q[u], j));
+  for (int u = 0; u < NV; ++u) {
+    vm[u] = vec_max<DT>(q[u]);
+    m = fmaxf(m, vm[u]);
+  }
   // units of 1, 2 or 4 threads, at least 2 n of them
   const int per = a.n <= 32 ? 4 : a.n <= 64 ? 2 : 1;
   float um = m;
@@ -134,51 +187,59 @@ __global__ void __launch_bounds__(kBeamThreads) beam_scan(const BeamArgs a) {
   if (tid < units) {
     const float mine = unit[tid];
     int rank = 0;
-    for (int i = 0; i < units; ++i) rank += (unit[i] > mine || (unit[i] == mine && i < tid)) ? 1 : 0;
+    for (int i = 0; i < units; i += 4) {
+      const float4 o = *reinterpret_cast<const float4*>(&unit[i]);
+      rank += (o.x > mine || (o.x == mine && i < tid)) + (o.y > mine || (o.y == mine && i + 1 < tid)) +
+              (o.z > mine || (o.z == mine && i + 2 < tid)) + (o.w > mine || (o.w == mine && i + 3 < tid));
+    }
     if (rank == a.n - 1) tau_s = mine;
   }
   const float c = m == -INFINITY ? 0.0f : ceilf(fminf(fmaxf(m, -kFar), kFar) * (kLog2eHi + kLog2eLo));
-  auto term = [&](float x) {
-    float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(x, kLog2eLo, fmaf(x, kLog2eHi, -c))));
-    return e;
-  };
-  float sum = 0.0f;
+  const unsigned long long c2 = f32x2(-c, -c);
+  unsigned long long sum2 = 0ull;
   if (fabsf(m) <= kFar) {
 #pragma unroll
     for (int u = 0; u < NV; ++u)
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) sum += term(elem<DT>(q[u], j));
+      for (int j = 0; j < VEC; j += 2) sum2 = add_x2(sum2, terms(elem<DT>(q[u], j), elem<DT>(q[u], j + 1), c2));
   } else if (m > -INFINITY) {
 #pragma unroll
     for (int u = 0; u < NV; ++u)
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float x = elem<DT>(q[u], j);
-        if (x > -INFINITY) sum += term(fminf(fmaxf(x, -kFar), kFar));
+      for (int j = 0; j < VEC; j += 2) {
+        // -inf stays -inf
+        const float x0 = elem<DT>(q[u], j), x1 = elem<DT>(q[u], j + 1);
+        sum2 = add_x2(sum2, terms(x0 > -INFINITY ? fminf(fmaxf(x0, -kFar), kFar) : x0,
+                                  x1 > -INFINITY ? fminf(fmaxf(x1, -kFar), kFar) : x1, c2));
       }
   }
-  double total = (double)sum;
+  float s0, s1;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(s0), "=f"(s1) : "l"(sum2));
+  // up to 64 fp32 terms a thread, the rest in 2^-40 fixed point: exact, and
+  // away from the narrow FP64 pipe
+  unsigned long long total = f2ull_rn(s0 * kMassScaleF) + f2ull_rn(s1 * kMassScaleF);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  if (lane == 0) wsum[warp] = total;
+  if (lane == 0) wkey[warp] = total;
   __syncthreads();
   if (tid == 0) {
-    total = 0.0;
-    for (int i = 0; i < kBW; ++i) total += wsum[i];
-    a.stat[part] = make_double2((double)c, total);
+    total = 0;
+    for (int i = 0; i < kBW; ++i) total += wkey[i];
+    a.stat[part] = make_double2((double)c, (double)total * (1.0 / 1099511627776.0));
   }
 
   const float tau = tau_s;
 #pragma unroll
   for (int u = 0; u < NV; ++u)
+    if (vm[u] >= tau && vm[u] > -INFINITY) {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const float x = elem<DT>(q[u], j);
-      if (x >= tau && x > -INFINITY) {
-        const int at = atomicAdd(&count, 1);
-        const uint32_t idx = (uint32_t)(e0 + (u * kBeamThreads + tid) * VEC + j);
-        if (at < kList) list[at] = ((unsigned long long)order_key<DT>(elem_raw<DT>(q[u], j)) << 32) | (uint32_t)~idx;
+      for (int j = 0; j < VEC; ++j) {
+        const float x = elem<DT>(q[u], j);
+        if (x >= tau && x > -INFINITY) {
+          const int at = atomicAdd(&count, 1);
+          const uint32_t idx = (uint32_t)(e0 + (u * kBeamThreads + tid) * VEC + j);
+          if (at < kList) list[at] = ((unsigned long long)order_key<DT>(elem_raw<DT>(q[u], j)) << 32) | (uint32_t)~idx;
+        }
       }
     }
   __syncthreads();
@@ -195,6 +256,7 @@ __global__ void __launch_bounds__(kBeamThreads) beam_scan(const BeamArgs a) {
   }
   // many equal values: the next one in order, n times
   unsigned long long last = ~0ull;
+#pragma unroll 1
   for (int r = 0; r < a.n; ++r) {
     unsigned long long best = 0ull;
 #pragma unroll
@@ -212,11 +274,11 @@ __global__ void __launch_bounds__(kBeamThreads) beam_scan(const BeamArgs a) {
       const unsigned long long w = __shfl_xor_sync(0xffffffffu, best, o);
       best = w > best ? w : best;
     }
+    __syncthreads();  // wkey may still be read
     if (lane == 0) wkey[warp] = best;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kBW; ++i) best = wkey[i] > best ? wkey[i] : best;
-    __syncthreads();
     if (tid == 0) out[r] = best;
     last = best;
   }
@@ -230,8 +292,10 @@ template <int DT>
 __global__ void __launch_bounds__(kBeamThreads) beam_merge(const BeamArgs a) {
   __shared__ unsigned long long key[kList];
   __shared__ uint32_t flat[kList];  // ~(k * V + v): larger is earlier
-  __shared__ unsigned long long unit[kBeamThreads];
+  __shared__ __align__(16) unsigned long long unit[kBeamThreads];
+  __shared__ unsigned long long head[kHeads];
   __shared__ double shift[TOPKP_MAX_BEAMS];  // score - normaliser; the score itself where finished
+  __shared__ float top[TOPKP_MAX_BEAMS];
   __shared__ uint8_t state[TOPKP_MAX_BEAMS];  // 0: no candidate, 1: live, 2: finished
   __shared__ unsigned long long tau_s, wk[kBW];
   __shared__ uint32_t wf[kBW];
@@ -240,10 +304,9 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge(const BeamArgs a) {
   const int64_t b = blockIdx.x;
   const int n = a.n, S = a.slices;
 
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int k = warp; k < a.K; k += kBW) {
     const int64_t row = b * a.K + k;
-    const float score = a.scores[row];
-    const bool done = a.finished && a.finished[row];
     float c = -INFINITY;
     for (int s = lane; s < S; s += 32) {
       const double2 st = a.stat[row * S + s];
@@ -260,14 +323,23 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge(const BeamArgs a) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane == 0) {
-      const bool live = !done && score != -INFINITY && l > 0.0;
-      state[k] = done ? (score != -INFINITY ? 2 : 0) : live ? 1 : 0;
-      shift[k] = done ? (double)score : live ? (double)score - (log(l) + (double)c * 0.693147180559945309417) : 0.0;
+      shift[k] = l;
+      top[k] = c;
     }
   }
   if (tid == 0) {
     count = 0;
     tau_s = 0ull;
+  }
+  __syncthreads();
+  if (tid < a.K) {
+    const int64_t row = b * a.K + tid;
+    const float score = a.scores[row];
+    const bool done = a.finished && a.finished[row];
+    const double l = shift[tid];
+    const bool live = !done && score != -INFINITY && l > 0.0;
+    state[tid] = done ? (score != -INFINITY ? 2 : 0) : live ? 1 : 0;
+    shift[tid] = done ? (double)score : live ? (double)score - (log(l) + (double)top[tid] * 0.693147180559945309417) : 0.0;
   }
   __syncthreads();
 
@@ -291,34 +363,45 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge(const BeamArgs a) {
 
   const int depth = lists >= n ? 1 : (n + lists - 1) / lists;
   const int want = (n + depth - 1) / depth;
-  if (lists * (int64_t)n > kList / 2) {
+  // the lists' first entries; those past kHeads lists are read again below
+  for (int l = tid; l < lists && l < kHeads; l += kBeamThreads) {
+    uint32_t f;
+    head[l] = entry(l, 0, &f);
+  }
+  if (lists * (int64_t)n > 128) {
     unsigned long long mine = 0ull;
     uint32_t f;
     for (int l = tid; l < lists; l += kBeamThreads) {
-      const unsigned long long e = entry(l, depth - 1, &f);
+      const unsigned long long e = depth == 1 && l < kHeads ? head[l] : entry(l, depth - 1, &f);
       mine = e > mine ? e : mine;
     }
+    const int units = min(kBeamThreads, (lists + 1) & ~1);
     unit[tid] = mine;
     __syncthreads();
-    int rank = 0;
-    for (int i = 0; i < kBeamThreads; ++i) rank += (unit[i] > mine || (unit[i] == mine && i < tid)) ? 1 : 0;
-    if (rank == want - 1) tau_s = mine;
-    __syncthreads();
-  }
-  const unsigned long long tau = tau_s > 0ull ? tau_s : 1ull;
-  for (int l = warp; l < lists; l += kBW)
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      uint32_t f = 0;
-      const unsigned long long e = i0 + lane < n ? entry(l, i0 + lane, &f) : 0ull;
-      if (e >= tau) {
-        const int at = atomicAdd(&count, 1);
-        if (at < kList) {
-          key[at] = e;
-          flat[at] = f;
-        }
+    if (tid < units) {
+      int rank = 0;
+      for (int i = 0; i < units; i += 2) {
+        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&unit[i]);
+        rank += (o.x > mine || (o.x == mine && i < tid)) + (o.y > mine || (o.y == mine && i + 1 < tid));
       }
-      if (__shfl_sync(0xffffffffu, e, 31) < tau) break;
+      if (rank == want - 1) tau_s = mine;
     }
+  }
+  __syncthreads();
+  const unsigned long long tau = tau_s > 0ull ? tau_s : 1ull;
+  for (int i = tid; i < lists * n; i += kBeamThreads) {
+    const int l = (int)((uint32_t)i / (uint32_t)n);
+    if (l < kHeads && head[l] < tau) continue;
+    uint32_t f = 0;
+    const unsigned long long e = entry(l, i - l * n, &f);
+    if (e >= tau) {
+      const int at = atomicAdd(&count, 1);
+      if (at < kList) {
+        key[at] = e;
+        flat[at] = f;
+      }
+    }
+  }
   __syncthreads();
   const int found = count;
   float* os = a.out_score + b * n;
@@ -401,13 +484,21 @@ cudaError_t launch_dt(const BeamArgs& a, cudaStream_t s) {
   switch (a.nv) {
     case 1: beam_scan<DT, 1><<<grid, kBeamThreads, 0, s>>>(a); break;
     case 2: beam_scan<DT, 2><<<grid, kBeamThreads, 0, s>>>(a); break;
-    case 4: beam_scan<DT, 4><<<grid, kBeamThreads, 0, s>>>(a); break;
-    default: beam_scan<DT, 8><<<grid, kBeamThreads, 0, s>>>(a); break;
+    default: beam_scan<DT, 4><<<grid, kBeamThreads, 0, s>>>(a); break;
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  beam_merge<DT><<<(unsigned int)a.B, kBeamThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  // the merge's launch overlaps the scan; it waits for the scan's results itself
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned int)a.B);
+  cfg.blockDim = dim3(kBeamThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, beam_merge<DT>, a);
 }
 
 }  // namespace

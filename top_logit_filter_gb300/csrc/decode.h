@@ -13,7 +13,7 @@ namespace topkp {
 // ------------------------------------------------------------ beam select
 // One CTA scans a slice of a row: 256 threads hold NV 16-byte vectors each.
 constexpr int kBeamThreads = 256;
-constexpr int kBeamMaxVec = 8;
+constexpr int kBeamMaxVec = 4;
 
 struct BeamArgs {
   const void* x;  // logits [B * K, ldx]
@@ -22,7 +22,7 @@ struct BeamArgs {
   const uint8_t* finished;  // or nullptr
   int64_t B;
   int32_t K, V, n, pad;
-  int32_t nv;      // vectors per thread: 1, 2, 4 or 8
+  int32_t nv;      // vectors per thread: 1, 2 or 4
   int32_t slices;  // CTAs per row
   // workspace, per (row, slice): shift and sum of the slice, its candidates
   double2* stat;               // (c, sum of 2^(x log2 e - c)); c is an integer, sum 0 if nothing is finite

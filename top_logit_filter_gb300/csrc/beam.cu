@@ -10,13 +10,19 @@
 // integer ceil(max x log2 e): slices (and rows) then combine by exact powers
 // of two, and the largest term is in (1/2, 1].
 //
-// The n largest of a slice.  Disjoint units of elements (the elements of one
-// or of a few threads) each have a maximum; the n-th largest of those maxima
-// is reached by at least n elements, and hardly any more when there are many
-// units.  Every element not below it is listed, and each listed element's
-// rank is the number of listed ones before it in the order (value
-// descending, index ascending).  Rows of many equal values overflow the list
-// and take n rounds of a block-wide maximum instead.
+// The n largest of a slice.  The slice goes through the CTA in chunks, each
+// thread four 16-byte vectors at a time, the next chunk on its way.  In the
+// first chunk, disjoint units of elements (those of one or of a few threads)
+// each have a maximum; the n-th largest of the maxima is reached by at least
+// n elements, and hardly any more when there are many units.  Every element
+// not below it is listed.  Later elements are listed if they are above the
+// bound; when the list has grown, and at the end, each listed element's rank
+// (the number of listed ones before it, by value descending and index
+// ascending) leaves the first n in order, and the last of them is the new
+// bound.  A chunk that overflows the list (rows of many equal values) takes n
+// rounds of a block-wide maximum instead.
+#include <limits.h>
+
 #include "common.cuh"
 #include "decode.h"
 
@@ -31,6 +37,10 @@ constexpr float kLog2eLo = 7.0526077e-06f;     // the rest
 // the score (a mask may have put the type's lowest value there); their order
 // within the row stays their own.
 constexpr float kFar = 60000.0f;
+// Sums are kept in 64-bit fixed point: a chunk's few fp32 terms, each at most
+// 1, are added up in 2^-38 units (2^23 elements of a row stay below 2^61), so
+// a long row loses nothing behind a large term and the order does not matter.
+constexpr float kSumScale = 274877906944.0f;  // 2^38
 
 template <int DT>
 __device__ __forceinline__ float elem(const uint4& q, int j) {
@@ -45,14 +55,19 @@ __device__ __forceinline__ typename DType<DT>::raw elem_raw(const uint4& q, int 
   return (typename DType<DT>::raw)(w[j >> 1] >> (16 * (j & 1)));
 }
 
-// A double as an unsigned key of the same order; 0 stands for no candidate.
-__device__ __forceinline__ unsigned long long double_key(double d) {
-  const unsigned long long u = (unsigned long long)__double_as_longlong(d + 0.0);
-  return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+// Scores are compared in 64-bit fixed point, 2^-40 a unit (FP64 runs on a
+// narrow pipe here).  A score as an unsigned key of the same order; 0 stands
+// for no candidate.
+__device__ __forceinline__ long long fixed_of(float x) {
+  x = fminf(fmaxf(x, -kFar), kFar);
+  const long long f = (long long)f2ull_rn(fabsf(x) * kMassScaleF);
+  return x < 0.0f ? -f : f;
 }
-__device__ __forceinline__ double key_double(unsigned long long k) {
-  const unsigned long long u = (k >> 63) ? (k & 0x7fffffffffffffffull) : ~k;
-  return __longlong_as_double((long long)u);
+__device__ __forceinline__ unsigned long long fixed_key(long long f) {
+  return (unsigned long long)f ^ 0x8000000000000000ull;
+}
+__device__ __forceinline__ float key_score(unsigned long long k) {
+  return (float)(long long)(k ^ 0x8000000000000000ull) * (1.0f / kMassScaleF);
 }
 
 constexpr int kBW = kBeamThreads / 32;
@@ -102,16 +117,60 @@ __device__ __forceinline__ float vec_max(const uint4& q) {
   return fmaxf(elem<DT>(make_uint4(m, 0, 0, 0), 0), elem<DT>(make_uint4(m, 0, 0, 0), DT == TOPKP_F32 ? 0 : 1));
 }
 
+// The NV vectors of chunk elements [e, e + 256 * NV * VEC) that this thread
+// holds; a vector that sticks out of the row is read element by element, and
+// what lies outside reads as -inf.
 template <int DT, int NV>
-__global__ void __launch_bounds__(kBeamThreads, NV == 4 ? 4 : 6) beam_scan(const BeamArgs a) {
+__device__ __forceinline__ void load_chunk(uint4 (&q)[NV], const typename DType<DT>::raw* xr, int e0, int V) {
   using raw = typename DType<DT>::raw;
   constexpr int VEC = 16 / (int)sizeof(raw);
-  __shared__ unsigned long long list[kList];
-  __shared__ __align__(16) float unit[kBeamThreads];
-  __shared__ float wmax[kBW];
-  __shared__ unsigned long long wkey[kBW];
-  __shared__ float tau_s;
-  __shared__ int count;
+  if (e0 >= 0 && e0 + kBeamThreads * NV * VEC <= V) {
+    const uint4* p = reinterpret_cast<const uint4*>(xr + e0) + threadIdx.x;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) q[u] = __ldcs(p + u * kBeamThreads);
+    return;
+  }
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    const int e = e0 + (u * kBeamThreads + (int)threadIdx.x) * VEC;
+    if (e >= 0 && e + VEC <= V) {
+      q[u] = __ldcs(reinterpret_cast<const uint4*>(xr + e));
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = DT == TOPKP_F32 ? 0xff800000u : DType<DT>::kNegInf * 0x10001u;
+      if (e < V && e + VEC > 0) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          if (e + j >= 0 && e + j < V) {
+            const uint32_t r = xr[e + j];
+            if (DT == TOPKP_F32) w[j] = r;
+            else w[j >> 1] = (j & 1) ? ((w[j >> 1] & 0xffffu) | (r << 16)) : ((w[j >> 1] & 0xffff0000u) | r);
+          }
+        }
+      }
+      q[u] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+struct ScanShared {
+  unsigned long long list[2][kList];  // the current list, and where its first n go
+  __align__(16) float unit[kBeamThreads];
+  float wmax[kBW];
+  unsigned long long wkey[kBW];
+  unsigned long long wsum[kBW];
+  int wtop[kBW];
+  float tau;
+  int count;
+};
+
+template <int DT, int NV>
+__global__ void __launch_bounds__(kBeamThreads, 3) beam_scan(const BeamArgs a) {
+  using raw = typename DType<DT>::raw;
+  constexpr int VEC = 16 / (int)sizeof(raw);
+  constexpr int CHUNK = kBeamThreads * NV * VEC;
+  __shared__ ScanShared s;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t part = blockIdx.x;
@@ -121,167 +180,188 @@ __global__ void __launch_bounds__(kBeamThreads, NV == 4 ? 4 : 6) beam_scan(const
 
   const float score = a.scores[row];
   if ((a.finished && a.finished[row]) || score == -INFINITY) {
-    if (tid == 0) a.stat[part] = make_double2(0.0, 0.0);
+    if (tid == 0) a.stat[part] = make_longlong2(0, 0);
     for (int i = tid; i < a.n; i += kBeamThreads) out[i] = 0ull;
     return;
   }
 
-  // 16-byte vectors of the row's aligned window; a vector that sticks out of
-  // the row is read element by element
+  // 16-byte vectors of the row's aligned window
   const raw* xr = reinterpret_cast<const raw*>(a.x) + row * a.ldx;
-  const int head = (int)((reinterpret_cast<uintptr_t>(xr) & 15) / sizeof(raw));
-  const int e0 = slice * (kBeamThreads * NV * VEC) - head;  // row index of this slice's first element
-  uint4 q[NV];
-  if (e0 >= 0 && e0 + kBeamThreads * NV * VEC <= a.V) {
-    const uint4* p = reinterpret_cast<const uint4*>(xr + e0) + tid;
-#pragma unroll
-    for (int u = 0; u < NV; ++u) q[u] = __ldcs(p + u * kBeamThreads);
-  } else {
+  const int lead = (int)((reinterpret_cast<uintptr_t>(xr) & 15) / sizeof(raw));
+  const int e_first = slice * a.chunks * CHUNK - lead;  // row index of this slice's first element
+  const int e_end = min(e_first + a.chunks * CHUNK, a.V);
+
+  uint4 q[NV], nx[NV];
+  load_chunk<DT, NV>(q, xr, e_first, a.V);
+  int cur = 0;             // which list is current
+  float tau = -INFINITY;   // an element is listed if it is above (in the first chunk: not below)
+  float c = -INFINITY;     // this thread's shift: an integer, or -inf before its first finite element
+  unsigned long long acc = 0ull;  // this thread's sum in units of 2^(c - 38)
+  if (tid == 0) s.count = 0;
+
+#pragma unroll 1
+  for (int e0 = e_first; e0 < e_end; e0 += CHUNK) {
+    const bool first = e0 == e_first, last = e0 + CHUNK >= e_end;
+    if (!last) load_chunk<DT, NV>(nx, xr, e0 + CHUNK, a.V);
+    float vm[NV], m = -INFINITY;
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
-      const int e = e0 + (u * kBeamThreads + tid) * VEC;
-      if (e >= 0 && e + VEC <= a.V) {
-        q[u] = __ldcs(reinterpret_cast<const uint4*>(xr + e));
+      vm[u] = vec_max<DT>(q[u]);
+      m = fmaxf(m, vm[u]);
+    }
+    if (first) {
+      // units of 1, 2 or 4 threads, at least 2 n of them
+      const int per = a.n <= 32 ? 4 : a.n <= 64 ? 2 : 1;
+      float um = m;
+      if (per >= 2) um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, 1));
+      if (per >= 4) um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, 2));
+      if (tid % per == 0) s.unit[tid / per] = um;
+      if (tid == 0) s.tau = -INFINITY;
+      __syncthreads();
+      const int units = kBeamThreads / per;
+      if (tid < units) {
+        const float mine = s.unit[tid];
+        int rank = 0;
+        for (int i = 0; i < units; i += 4) {
+          const float4 o = *reinterpret_cast<const float4*>(&s.unit[i]);
+          rank += (o.x > mine || (o.x == mine && i < tid)) + (o.y > mine || (o.y == mine && i + 1 < tid)) +
+                  (o.z > mine || (o.z == mine && i + 2 < tid)) + (o.w > mine || (o.w == mine && i + 3 < tid));
+        }
+        if (rank == a.n - 1) s.tau = mine;
+      }
+    }
+    // the sum, in 2^c units of this thread's own
+    const float mc = fminf(fmaxf(m, -kFar), kFar);
+    if (m > -INFINITY && mc * (kLog2eHi + kLog2eLo) > c) {
+      const float nc = ceilf(mc * (kLog2eHi + kLog2eLo));
+      acc = c == -INFINITY ? 0ull : acc >> min((int)(nc - c), 63);
+      c = nc;
+    }
+    const unsigned long long c2 = f32x2(-c, -c);
+    if (m > -INFINITY) {
+      unsigned long long sum2 = 0ull;
+      if (fabsf(m) <= kFar) {
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+#pragma unroll
+          for (int j = 0; j < VEC; j += 2) sum2 = add_x2(sum2, terms(elem<DT>(q[u], j), elem<DT>(q[u], j + 1), c2));
       } else {
-        uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = DT == TOPKP_F32 ? 0xff800000u : DType<DT>::kNegInf * 0x10001u;
-        if (e < a.V && e + VEC > 0) {
+        for (int u = 0; u < NV; ++u)
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            if (e + j >= 0 && e + j < a.V) {
-              const uint32_t r = xr[e + j];
-              if (DT == TOPKP_F32) w[j] = r;
-              else w[j >> 1] = (j & 1) ? ((w[j >> 1] & 0xffffu) | (r << 16)) : ((w[j >> 1] & 0xffff0000u) | r);
-            }
+          for (int j = 0; j < VEC; j += 2) {
+            // -inf stays -inf
+            const float x0 = elem<DT>(q[u], j), x1 = elem<DT>(q[u], j + 1);
+            sum2 = add_x2(sum2, terms(x0 > -INFINITY ? fminf(fmaxf(x0, -kFar), kFar) : x0,
+                                      x1 > -INFINITY ? fminf(fmaxf(x1, -kFar), kFar) : x1, c2));
+          }
+      }
+      float s0, s1;
+      asm("mov.b64 {%0, %1}, %2;" : "=f"(s0), "=f"(s1) : "l"(sum2));
+      acc += f2ull_rn(s0 * kSumScale) + f2ull_rn(s1 * kSumScale);
+    }
+    if (first) {
+      __syncthreads();
+      tau = s.tau;
+    }
+    const int before = s.count;  // entries kept from earlier chunks (stable: a barrier follows every change)
+    auto wanted = [&](float x) { return first ? x >= tau && x > -INFINITY : x > tau; };
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+      if (wanted(vm[u])) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const float x = elem<DT>(q[u], j);
+          if (wanted(x)) {
+            const int at = atomicAdd(&s.count, 1);
+            const uint32_t idx = (uint32_t)(e0 + (u * kBeamThreads + tid) * VEC + j);
+            if (at < kList)
+              s.list[cur][at] = ((unsigned long long)order_key<DT>(elem_raw<DT>(q[u], j)) << 32) | (uint32_t)~idx;
           }
         }
-        q[u] = make_uint4(w[0], w[1], w[2], w[3]);
       }
+    __syncthreads();
+    const int found = s.count;
+    if (found > kList) {
+      // many equal or rising values: the next one in order, n times, of this
+      // chunk and of what was kept (entries listed by this chunk are in q)
+      const int kept = before < kList ? before : 0;
+      unsigned long long prev = ~0ull;
+#pragma unroll 1
+      for (int r = 0; r < a.n; ++r) {
+        unsigned long long best = 0ull;
+#pragma unroll
+        for (int u = 0; u < NV; ++u)  // the keys are made anew each round, not held
+          asm volatile("" : "+r"(q[u].x), "+r"(q[u].y), "+r"(q[u].z), "+r"(q[u].w));
+        for (int i = tid; i < kept; i += kBeamThreads) {
+          const unsigned long long k = s.list[cur][i];
+          if (k < prev && k > best) best = k;
+        }
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) {
+            const float x = elem<DT>(q[u], j);
+            const uint32_t idx = (uint32_t)(e0 + (u * kBeamThreads + tid) * VEC + j);
+            const unsigned long long k =
+                ((unsigned long long)order_key<DT>(elem_raw<DT>(q[u], j)) << 32) | (uint32_t)~idx;
+            if (wanted(x) && k < prev && k > best) best = k;
+          }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          const unsigned long long w = __shfl_xor_sync(0xffffffffu, best, o);
+          best = w > best ? w : best;
+        }
+        if (lane == 0) s.wkey[warp] = best;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kBW; ++i) best = s.wkey[i] > best ? s.wkey[i] : best;
+        __syncthreads();
+        if (tid == 0) s.list[cur ^ 1][r] = best;
+        prev = best;
+      }
+      if (tid == 0) s.count = a.n;
+      __syncthreads();
+      cur ^= 1;
+      tau = value_of_key<DT>((uint32_t)(s.list[cur][a.n - 1] >> 32));
+    } else if (last || found >= max(3 * a.n, 96)) {
+      for (int i = tid; i < found; i += kBeamThreads) {
+        const unsigned long long mine = s.list[cur][i];
+        int rank = 0;
+#pragma unroll 4
+        for (int j = 0; j < found; ++j) rank += s.list[cur][j] > mine ? 1 : 0;
+        if (rank < a.n) s.list[cur ^ 1][rank] = mine;
+      }
+      __syncthreads();
+      if (tid == 0) s.count = min(found, a.n);
+      cur ^= 1;
+      if (!last && found >= a.n) tau = value_of_key<DT>((uint32_t)(s.list[cur][a.n - 1] >> 32));
+      __syncthreads();
     }
+#pragma unroll
+    for (int u = 0; u < NV; ++u) q[u] = nx[u];
   }
 
-  float vm[NV], m = -INFINITY;
+  // the slice's sum: the threads' at the largest of their shifts, exact and in no order
+  float top = c;
 #pragma unroll
-  for (int u = 0; u < NV; ++u) {
-    vm[u] = vec_max<DT>(q[u]);
-    m = fmaxf(m, vm[u]);
-  }
-  // units of 1, 2 or 4 threads, at least 2 n of them
-  const int per = a.n <= 32 ? 4 : a.n <= 64 ? 2 : 1;
-  float um = m;
-  if (per >= 2) um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, 1));
-  if (per >= 4) um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, 2));
-  if (tid % per == 0) unit[tid / per] = um;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) wmax[warp] = m;
-  if (tid == 0) {
-    count = 0;
-    tau_s = -INFINITY;
-  }
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) s.wmax[warp] = top;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kBW; ++i) m = fmaxf(m, wmax[i]);
-  const int units = kBeamThreads / per;
-  if (tid < units) {
-    const float mine = unit[tid];
-    int rank = 0;
-    for (int i = 0; i < units; i += 4) {
-      const float4 o = *reinterpret_cast<const float4*>(&unit[i]);
-      rank += (o.x > mine || (o.x == mine && i < tid)) + (o.y > mine || (o.y == mine && i + 1 < tid)) +
-              (o.z > mine || (o.z == mine && i + 2 < tid)) + (o.w > mine || (o.w == mine && i + 3 < tid));
-    }
-    if (rank == a.n - 1) tau_s = mine;
-  }
-  const float c = m == -INFINITY ? 0.0f : ceilf(fminf(fmaxf(m, -kFar), kFar) * (kLog2eHi + kLog2eLo));
-  const unsigned long long c2 = f32x2(-c, -c);
-  unsigned long long sum2 = 0ull;
-  if (fabsf(m) <= kFar) {
-#pragma unroll
-    for (int u = 0; u < NV; ++u)
-#pragma unroll
-      for (int j = 0; j < VEC; j += 2) sum2 = add_x2(sum2, terms(elem<DT>(q[u], j), elem<DT>(q[u], j + 1), c2));
-  } else if (m > -INFINITY) {
-#pragma unroll
-    for (int u = 0; u < NV; ++u)
-#pragma unroll
-      for (int j = 0; j < VEC; j += 2) {
-        // -inf stays -inf
-        const float x0 = elem<DT>(q[u], j), x1 = elem<DT>(q[u], j + 1);
-        sum2 = add_x2(sum2, terms(x0 > -INFINITY ? fminf(fmaxf(x0, -kFar), kFar) : x0,
-                                  x1 > -INFINITY ? fminf(fmaxf(x1, -kFar), kFar) : x1, c2));
-      }
-  }
-  float s0, s1;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(s0), "=f"(s1) : "l"(sum2));
-  // up to 64 fp32 terms a thread, the rest in 2^-40 fixed point: exact, and
-  // away from the narrow FP64 pipe
-  unsigned long long total = f2ull_rn(s0 * kMassScaleF) + f2ull_rn(s1 * kMassScaleF);
+  for (int i = 0; i < kBW; ++i) top = fmaxf(top, s.wmax[i]);
+  unsigned long long total = c == -INFINITY ? 0ull : acc >> min((int)(top - c), 63);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  if (lane == 0) wkey[warp] = total;
+  if (lane == 0) s.wsum[warp] = total;
   __syncthreads();
   if (tid == 0) {
     total = 0;
-    for (int i = 0; i < kBW; ++i) total += wkey[i];
-    a.stat[part] = make_double2((double)c, (double)total * (1.0 / 1099511627776.0));
+    for (int i = 0; i < kBW; ++i) total += s.wsum[i];
+    a.stat[part] = make_longlong2(top == -INFINITY ? 0 : (long long)(int)top, (long long)total);
   }
-
-  const float tau = tau_s;
-#pragma unroll
-  for (int u = 0; u < NV; ++u)
-    if (vm[u] >= tau && vm[u] > -INFINITY) {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float x = elem<DT>(q[u], j);
-        if (x >= tau && x > -INFINITY) {
-          const int at = atomicAdd(&count, 1);
-          const uint32_t idx = (uint32_t)(e0 + (u * kBeamThreads + tid) * VEC + j);
-          if (at < kList) list[at] = ((unsigned long long)order_key<DT>(elem_raw<DT>(q[u], j)) << 32) | (uint32_t)~idx;
-        }
-      }
-    }
-  __syncthreads();
-  const int found = count;
-  if (found <= kList) {
-    for (int i = tid; i < found; i += kBeamThreads) {
-      const unsigned long long mine = list[i];
-      int rank = 0;
-      for (int j = 0; j < found; ++j) rank += list[j] > mine ? 1 : 0;
-      if (rank < a.n) out[rank] = mine;
-    }
-    for (int i = found + tid; i < a.n; i += kBeamThreads) out[i] = 0ull;
-    return;
-  }
-  // many equal values: the next one in order, n times
-  unsigned long long last = ~0ull;
-#pragma unroll 1
-  for (int r = 0; r < a.n; ++r) {
-    unsigned long long best = 0ull;
-#pragma unroll
-    for (int u = 0; u < NV; ++u)
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float x = elem<DT>(q[u], j);
-        const uint32_t idx = (uint32_t)(e0 + (u * kBeamThreads + tid) * VEC + j);
-        const unsigned long long key =
-            ((unsigned long long)order_key<DT>(elem_raw<DT>(q[u], j)) << 32) | (uint32_t)~idx;
-        if (x >= tau && x > -INFINITY && key < last && key > best) best = key;
-      }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const unsigned long long w = __shfl_xor_sync(0xffffffffu, best, o);
-      best = w > best ? w : best;
-    }
-    __syncthreads();  // wkey may still be read
-    if (lane == 0) wkey[warp] = best;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kBW; ++i) best = wkey[i] > best ? wkey[i] : best;
-    if (tid == 0) out[r] = best;
-    last = best;
-  }
+  const int found = s.count;
+  for (int i = tid; i < a.n; i += kBeamThreads) out[i] = i < found ? s.list[cur][i] : 0ull;
 }
 
 // One CTA per request.  Entry i of list l (a slice of a beam) is candidate
@@ -294,8 +374,8 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge(const BeamArgs a) {
   __shared__ uint32_t flat[kList];  // ~(k * V + v): larger is earlier
   __shared__ __align__(16) unsigned long long unit[kBeamThreads];
   __shared__ unsigned long long head[kHeads];
-  __shared__ double shift[TOPKP_MAX_BEAMS];  // score - normaliser; the score itself where finished
-  __shared__ float top[TOPKP_MAX_BEAMS];
+  __shared__ long long shift[TOPKP_MAX_BEAMS];  // score - normaliser; the score itself where finished
+  __shared__ int top[TOPKP_MAX_BEAMS];
   __shared__ uint8_t state[TOPKP_MAX_BEAMS];  // 0: no candidate, 1: live, 2: finished
   __shared__ unsigned long long tau_s, wk[kBW];
   __shared__ uint32_t wf[kBW];
@@ -307,18 +387,17 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge(const BeamArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int k = warp; k < a.K; k += kBW) {
     const int64_t row = b * a.K + k;
-    float c = -INFINITY;
+    int c = INT_MIN;
     for (int s = lane; s < S; s += 32) {
-      const double2 st = a.stat[row * S + s];
-      if (st.y > 0.0) c = fmaxf(c, (float)st.x);
+      const longlong2 st = a.stat[row * S + s];
+      if (st.y > 0) c = max(c, (int)st.x);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, o));
-    double l = 0.0;
+    for (int o = 16; o > 0; o >>= 1) c = max(c, __shfl_xor_sync(0xffffffffu, c, o));
+    long long l = 0;
     for (int s = lane; s < S; s += 32) {
-      const double2 st = a.stat[row * S + s];
-      // 2^(st.x - c), an exact power of two
-      if (st.y > 0.0) l += st.y * (double)__int_as_float((127 + max((int)((float)st.x - c), -126)) << 23);
+      const longlong2 st = a.stat[row * S + s];
+      if (st.y > 0) l += st.y >> min(c - (int)st.x, 63);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -336,10 +415,12 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge(const BeamArgs a) {
     const int64_t row = b * a.K + tid;
     const float score = a.scores[row];
     const bool done = a.finished && a.finished[row];
-    const double l = shift[tid];
-    const bool live = !done && score != -INFINITY && l > 0.0;
+    const long long l = shift[tid];
+    const bool live = !done && score != -INFINITY && l > 0;
     state[tid] = done ? (score != -INFINITY ? 2 : 0) : live ? 1 : 0;
-    shift[tid] = done ? (double)score : live ? (double)score - (log(l) + (double)top[tid] * 0.693147180559945309417) : 0.0;
+    // the 38 fractional bits of l go with its shift
+    const double lse = live ? log((double)l) + (double)(top[tid] - 38) * 0.693147180559945309417 : 0.0;
+    shift[tid] = state[tid] ? llrint(((double)score - lse) * 1099511627776.0) : 0;
   }
   __syncthreads();
 
@@ -352,13 +433,12 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge(const BeamArgs a) {
     if (st == 0) return 0ull;
     if (st == 2) {
       *f = ~(uint32_t)(k * a.V + a.pad);
-      return (l == k * S && i == 0) ? double_key(shift[k]) : 0ull;
+      return (l == k * S && i == 0) ? fixed_key(shift[k]) : 0ull;
     }
     const unsigned long long e = cand[(int64_t)l * n + i];
     if (e == 0ull) return 0ull;
     *f = ~(uint32_t)(k * a.V + (int)~(uint32_t)e);
-    const float x = value_of_key<DT>((uint32_t)(e >> 32));
-    return double_key(shift[k] + (double)fminf(fmaxf(x, -kFar), kFar));
+    return fixed_key(shift[k] + fixed_of(value_of_key<DT>((uint32_t)(e >> 32))));
   };
 
   const int depth = lists >= n ? 1 : (n + lists - 1) / lists;
@@ -409,7 +489,7 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge(const BeamArgs a) {
   int32_t* ot = a.out_token + b * n;
   auto put = [&](int r, unsigned long long e, uint32_t f) {
     const uint32_t p = ~f;
-    os[r] = (float)key_double(e);
+    os[r] = key_score(e);
     op[r] = (int32_t)(p / (uint32_t)a.V);
     ot[r] = (int32_t)(p % (uint32_t)a.V);
   };
@@ -440,11 +520,10 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge(const BeamArgs a) {
         uint32_t f = 0;
         const unsigned long long e = entry(l, i, &f);
         if (e < tau) break;
-        if (e < be || (e == be && f < bf)) break;
-        if (e < le || (e == le && f < lf)) {
+        if (e < be) break;
+        if ((e < le || (e == le && f < lf)) && (e > be || f > bf)) {
           be = e;
           bf = f;
-          break;
         }
       }
 #pragma unroll
@@ -481,11 +560,8 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge(const BeamArgs a) {
 template <int DT>
 cudaError_t launch_dt(const BeamArgs& a, cudaStream_t s) {
   const unsigned int grid = (unsigned int)(a.B * a.K * a.slices);
-  switch (a.nv) {
-    case 1: beam_scan<DT, 1><<<grid, kBeamThreads, 0, s>>>(a); break;
-    case 2: beam_scan<DT, 2><<<grid, kBeamThreads, 0, s>>>(a); break;
-    default: beam_scan<DT, 4><<<grid, kBeamThreads, 0, s>>>(a); break;
-  }
+  if (a.nv == 1) beam_scan<DT, 1><<<grid, kBeamThreads, 0, s>>>(a);
+  else beam_scan<DT, 4><<<grid, kBeamThreads, 0, s>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // the merge's launch overlaps the scan; it waits for the scan's results itself
@@ -503,16 +579,22 @@ cudaError_t launch_dt(const BeamArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// The longest slices that still give every SM two CTAs.
+// A row is cut into slices of whole chunks so that the device has about
+// three waves of three CTAs an SM, and into single short chunks when there
+// are too few rows for that.
 BeamPlan plan_beam(int64_t rows, int64_t V, int esize, int32_t n, int num_sms) {
   BeamPlan p;
   const int vec = 16 / esize;
-  p.nv = kBeamMaxVec;
   // the aligned window may start up to vec - 1 elements before the row
-  auto slices = [&](int nv) { return (V + vec - 1 + (int64_t)kBeamThreads * nv * vec - 1) / ((int64_t)kBeamThreads * nv * vec); };
-  while (p.nv > 1 && rows * slices(p.nv) < 2LL * num_sms) p.nv /= 2;
-  p.slices = (int)slices(p.nv);
-  p.stat_bytes = ((size_t)rows * p.slices * sizeof(double2) + 255) / 256 * 256;
+  auto chunks = [&](int nv) { return (V + vec - 1 + (int64_t)kBeamThreads * nv * vec - 1) / ((int64_t)kBeamThreads * nv * vec); };
+  const int64_t wave = 3LL * num_sms;
+  p.nv = rows * chunks(4) >= wave ? 4 : 1;
+  const int64_t all = chunks(p.nv);
+  int64_t slices = (3 * wave + rows - 1) / rows;
+  if (slices > all) slices = all;
+  p.chunks = (int)((all + slices - 1) / slices);
+  p.slices = (int)((all + p.chunks - 1) / p.chunks);
+  p.stat_bytes = ((size_t)rows * p.slices * sizeof(longlong2) + 255) / 256 * 256;
   p.cand_bytes = (size_t)rows * p.slices * n * sizeof(unsigned long long);
   return p;
 }

@@ -11,9 +11,8 @@
 namespace topkp {
 
 // ------------------------------------------------------------ beam select
-// One CTA scans a slice of a row: 256 threads hold NV 16-byte vectors each.
+// One CTA scans a slice of a row, 256 threads of NV 16-byte vectors at a time.
 constexpr int kBeamThreads = 256;
-constexpr int kBeamMaxVec = 4;
 
 struct BeamArgs {
   const void* x;  // logits [B * K, ldx]
@@ -22,10 +21,11 @@ struct BeamArgs {
   const uint8_t* finished;  // or nullptr
   int64_t B;
   int32_t K, V, n, pad;
-  int32_t nv;      // vectors per thread: 1, 2 or 4
+  int32_t nv;      // vectors of a chunk per thread: 1 or 4
+  int32_t chunks;  // chunks of a slice
   int32_t slices;  // CTAs per row
   // workspace, per (row, slice): shift and sum of the slice, its candidates
-  double2* stat;               // (c, sum of 2^(x log2 e - c)); c is an integer, sum 0 if nothing is finite
+  longlong2* stat;             // (c, sum of 2^(x log2 e - c) in 2^-38 units); sum 0 if nothing is finite
   unsigned long long* cand;    // [rows * slices][n]: order key << 32 | ~index, descending; 0 past the last
   float* out_score;
   int32_t* out_parent;
@@ -33,7 +33,7 @@ struct BeamArgs {
 };
 
 struct BeamPlan {
-  int nv, slices;
+  int nv, chunks, slices;
   size_t stat_bytes, cand_bytes;
 };
 BeamPlan plan_beam(int64_t rows, int64_t V, int esize, int32_t n, int num_sms);

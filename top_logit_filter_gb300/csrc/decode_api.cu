@@ -110,8 +110,9 @@ topkp_status topkp_beam_select(const void* logits, int64_t B, int64_t K, int64_t
   a.n = n;
   a.pad = pad_token;
   a.nv = p.nv;
+  a.chunks = p.chunks;
   a.slices = p.slices;
-  a.stat = reinterpret_cast<double2*>(workspace);
+  a.stat = reinterpret_cast<longlong2*>(workspace);
   a.cand = reinterpret_cast<unsigned long long*>((char*)workspace + p.stat_bytes);
   a.out_score = out_score;
   a.out_parent = out_parent;

@@ -110,6 +110,13 @@ def test_beam_select_ties_and_masks(tk, dtype):
     x[3] = -INF
     x[3, 77] = lowest
     check_beam(tk, x, torch.tensor([[0.0, -1.0], [-3.0, -2.0]]), 30)
+    # rising and falling rows: every later chunk outbids the bound, or none does
+    ramp = torch.arange(150000.0) / 1000.0
+    check_beam(tk, torch.stack([ramp, ramp.flip(0)]).to(T_[dtype]).repeat(200, 1), torch.zeros(200, 2), 20)
+    # one token far above a flat row: the sum of many small terms behind a large one
+    x = torch.zeros(512, 140001, dtype=T_[dtype])
+    x[:, 70001] = 11.0
+    check_beam(tk, x, torch.zeros(256, 2), 2)
     # signed zeros are equal
     x = torch.zeros(2, 600, dtype=T_[dtype])
     x[:, ::2] = -0.0

@@ -15,12 +15,12 @@
 // first chunk, disjoint units of elements (those of one or of a few threads)
 // each have a maximum; the n-th largest of the maxima is reached by at least
 // n elements, and hardly any more when there are many units.  Every element
-// not below it is listed.  Later elements are listed if they are above the
-// bound; when the list has grown, and at the end, each listed element's rank
-// (the number of listed ones before it, by value descending and index
-// ascending) leaves the first n in order, and the last of them is the new
-// bound.  A chunk that overflows the list (rows of many equal values) takes n
-// rounds of a block-wide maximum instead.
+// not below it is listed; later elements are listed if they are above the
+// bound.  When the list has outgrown 3 n, a bisection over the listed keys
+// (value, then index: no two are equal) finds one with n keys not below it:
+// those stay, and the bound moves up to it.  What is left at the end goes to
+// the second kernel in any order.  A chunk that overflows the list (rows of
+// many equal values) takes n rounds of a block-wide maximum instead.
 #include <limits.h>
 
 #include "common.cuh"
@@ -29,8 +29,9 @@
 namespace topkp {
 namespace {
 
-constexpr int kList = 1024;   // listed candidates of a slice, and of a request
-constexpr int kHeads = 1024;  // lists whose first entries a request holds on chip
+constexpr int kList = 1024;   // listed candidates of a slice
+constexpr int kPool = 2560;   // of a request
+constexpr int kFew = 288;     // of a request, once cut
 constexpr float kLog2eHi = 1.44268798828125f;  // log2 e to 16 bits
 constexpr float kLog2eLo = 7.0526077e-06f;     // the rest
 // Logits beyond this magnitude count as this magnitude in the normaliser and
@@ -71,6 +72,34 @@ __device__ __forceinline__ float key_score(unsigned long long k) {
 }
 
 constexpr int kBW = kBeamThreads / 32;
+
+// The sum of one value of each thread, with one barrier: `slots` has two
+// alternating rows, so that the next sum does not wait for this one's readers.
+__device__ __forceinline__ int block_count(int v, int (*slots)[kBW], int& phase) {
+  v = __reduce_add_sync(0xffffffffu, v);
+  if ((threadIdx.x & 31) == 0) slots[phase][threadIdx.x >> 5] = v;
+  __syncthreads();
+  int t = 0;
+#pragma unroll
+  for (int i = 0; i < kBW; ++i) t += slots[phase][i];
+  phase ^= 1;
+  return t;
+}
+// A key with exactly `want` of list[0 .. found) not below it; want < found,
+// all keys different, all at least lo and below hi.  Every thread gets it.
+__device__ __forceinline__ unsigned long long bisect_keys(const unsigned long long* list, int found, int want,
+                                                          unsigned long long lo, unsigned long long hi,
+                                                          int (*slots)[kBW], int& phase) {
+  for (;;) {  // more than `want` keys are >= lo, fewer are >= hi: at most 64 halvings
+    const unsigned long long mid = lo + (hi - lo) / 2;
+    int c = 0;
+    for (int i = threadIdx.x; i < found; i += kBeamThreads) c += list[i] >= mid ? 1 : 0;
+    c = block_count(c, slots, phase);
+    if (c == want) return mid;
+    if (c > want) lo = mid;
+    else hi = mid;
+  }
+}
 
 // Two fp32 lanes in a 64-bit register, one instruction for both.
 __device__ __forceinline__ unsigned long long f32x2(float lo, float hi) {
@@ -117,6 +146,9 @@ __device__ __forceinline__ float vec_max(const uint4& q) {
   return fmaxf(elem<DT>(make_uint4(m, 0, 0, 0), 0), elem<DT>(make_uint4(m, 0, 0, 0), DT == TOPKP_F32 ? 0 : 1));
 }
 
+// Candidates that a slice may hand on.
+__host__ __device__ inline int beam_keep(int n) { return n < 16 ? 48 : 3 * n; }
+
 // The NV vectors of chunk elements [e, e + 256 * NV * VEC) that this thread
 // holds; a vector that sticks out of the row is read element by element, and
 // what lies outside reads as -inf.
@@ -160,7 +192,7 @@ struct ScanShared {
   float wmax[kBW];
   unsigned long long wkey[kBW];
   unsigned long long wsum[kBW];
-  int wtop[kBW];
+  int slots[2][kBW];
   float tau;
   int count;
 };
@@ -176,12 +208,12 @@ __global__ void __launch_bounds__(kBeamThreads, 3) beam_scan(const BeamArgs a) {
   const uint32_t part = blockIdx.x;
   const uint32_t row = part / (uint32_t)a.slices;
   const int slice = (int)(part - row * (uint32_t)a.slices);
-  unsigned long long* out = a.cand + (int64_t)part * a.n;
+  const int keep = beam_keep(a.n);
+  unsigned long long* out = a.cand + (int64_t)part * keep;
 
   const float score = a.scores[row];
   if ((a.finished && a.finished[row]) || score == -INFINITY) {
     if (tid == 0) a.stat[part] = make_longlong2(0, 0);
-    for (int i = tid; i < a.n; i += kBeamThreads) out[i] = 0ull;
     return;
   }
 
@@ -194,6 +226,8 @@ __global__ void __launch_bounds__(kBeamThreads, 3) beam_scan(const BeamArgs a) {
   uint4 q[NV], nx[NV];
   load_chunk<DT, NV>(q, xr, e_first, a.V);
   int cur = 0;             // which list is current
+  int phase = 0;
+  int held = 0;            // entries of it
   float tau = -INFINITY;   // an element is listed if it is above (in the first chunk: not below)
   float c = -INFINITY;     // this thread's shift: an integer, or -inf before its first finite element
   unsigned long long acc = 0ull;  // this thread's sum in units of 2^(c - 38)
@@ -264,7 +298,7 @@ __global__ void __launch_bounds__(kBeamThreads, 3) beam_scan(const BeamArgs a) {
       __syncthreads();
       tau = s.tau;
     }
-    const int before = s.count;  // entries kept from earlier chunks (stable: a barrier follows every change)
+    int mine = 0;
     auto wanted = [&](float x) { return first ? x >= tau && x > -INFINITY : x > tau; };
 #pragma unroll
     for (int u = 0; u < NV; ++u)
@@ -273,6 +307,7 @@ __global__ void __launch_bounds__(kBeamThreads, 3) beam_scan(const BeamArgs a) {
         for (int j = 0; j < VEC; ++j) {
           const float x = elem<DT>(q[u], j);
           if (wanted(x)) {
+            ++mine;
             const int at = atomicAdd(&s.count, 1);
             const uint32_t idx = (uint32_t)(e0 + (u * kBeamThreads + tid) * VEC + j);
             if (at < kList)
@@ -280,12 +315,12 @@ __global__ void __launch_bounds__(kBeamThreads, 3) beam_scan(const BeamArgs a) {
           }
         }
       }
-    __syncthreads();
-    const int found = s.count;
+    // the count is summed, not read from s.count: a fast thread may be adding
+    // the next chunk's already
+    const int found = held + block_count(mine, s.slots, phase);
     if (found > kList) {
       // many equal or rising values: the next one in order, n times, of this
       // chunk and of what was kept (entries listed by this chunk are in q)
-      const int kept = before < kList ? before : 0;
       unsigned long long prev = ~0ull;
 #pragma unroll 1
       for (int r = 0; r < a.n; ++r) {
@@ -293,7 +328,7 @@ __global__ void __launch_bounds__(kBeamThreads, 3) beam_scan(const BeamArgs a) {
 #pragma unroll
         for (int u = 0; u < NV; ++u)  // the keys are made anew each round, not held
           asm volatile("" : "+r"(q[u].x), "+r"(q[u].y), "+r"(q[u].z), "+r"(q[u].w));
-        for (int i = tid; i < kept; i += kBeamThreads) {
+        for (int i = tid; i < held; i += kBeamThreads) {
           const unsigned long long k = s.list[cur][i];
           if (k < prev && k > best) best = k;
         }
@@ -323,20 +358,24 @@ __global__ void __launch_bounds__(kBeamThreads, 3) beam_scan(const BeamArgs a) {
       if (tid == 0) s.count = a.n;
       __syncthreads();
       cur ^= 1;
+      held = a.n;
       tau = value_of_key<DT>((uint32_t)(s.list[cur][a.n - 1] >> 32));
-    } else if (last || found >= max(3 * a.n, 96)) {
+    } else if (found > keep) {
+      const unsigned long long bound =
+          bisect_keys(s.list[cur], found, a.n, 0ull, DT == TOPKP_F32 ? ~0ull : 1ull << 48, s.slots, phase);
+      if (tid == 0) s.count = 0;
+      __syncthreads();
       for (int i = tid; i < found; i += kBeamThreads) {
-        const unsigned long long mine = s.list[cur][i];
-        int rank = 0;
-#pragma unroll 4
-        for (int j = 0; j < found; ++j) rank += s.list[cur][j] > mine ? 1 : 0;
-        if (rank < a.n) s.list[cur ^ 1][rank] = mine;
+        const unsigned long long k = s.list[cur][i];
+        if (k >= bound) s.list[cur ^ 1][atomicAdd(&s.count, 1)] = k;
       }
-      __syncthreads();
-      if (tid == 0) s.count = min(found, a.n);
       cur ^= 1;
-      if (!last && found >= a.n) tau = value_of_key<DT>((uint32_t)(s.list[cur][a.n - 1] >> 32));
-      __syncthreads();
+      // the bound lies above the largest key dropped, so a later element
+      // (of a larger index) with that key's value is not wanted either
+      tau = value_of_key<DT>((uint32_t)(bound >> 32));
+      held = a.n;
+    } else {
+      held = found;
     }
 #pragma unroll
     for (int u = 0; u < NV; ++u) q[u] = nx[u];
@@ -358,32 +397,40 @@ __global__ void __launch_bounds__(kBeamThreads, 3) beam_scan(const BeamArgs a) {
   if (tid == 0) {
     total = 0;
     for (int i = 0; i < kBW; ++i) total += s.wsum[i];
-    a.stat[part] = make_longlong2(top == -INFINITY ? 0 : (long long)(int)top, (long long)total);
+    // shift in the low half, number of candidates in the high one
+    a.stat[part] = make_longlong2((long long)(((unsigned long long)held << 32) | (uint32_t)(top == -INFINITY ? 0 : (int)top)),
+                                  (long long)total);
   }
-  const int found = s.count;
-  for (int i = tid; i < a.n; i += kBeamThreads) out[i] = i < found ? s.list[cur][i] : 0ull;
+  for (int i = tid; i < held; i += kBeamThreads) out[i] = s.list[cur][i];
 }
 
-// One CTA per request.  Entry i of list l (a slice of a beam) is candidate
-// (score of the beam + logit - normaliser); the lists are descending, so the
-// d-th entry of a list bounds d candidates from below, and the q-th largest
-// of those (q d >= n) bounds n.
+// One CTA per request: the candidates of its beams' slices become scores in
+// shared memory, a bisection leaves n of them, and each one's rank among
+// those is its place.  More candidates than the pool holds are cut first by
+// the n-th largest of the threads' own maxima.
 template <int DT>
 __global__ void __launch_bounds__(kBeamThreads) beam_merge(const BeamArgs a) {
-  __shared__ unsigned long long key[kList];
-  __shared__ uint32_t flat[kList];  // ~(k * V + v): larger is earlier
+  __shared__ unsigned long long key[kPool];
+  __shared__ uint32_t flat[kPool];  // ~(k * V + v): larger is earlier
+  __shared__ unsigned long long key2[kFew];
+  __shared__ uint32_t flat2[kFew];
   __shared__ __align__(16) unsigned long long unit[kBeamThreads];
-  __shared__ unsigned long long head[kHeads];
   __shared__ long long shift[TOPKP_MAX_BEAMS];  // score - normaliser; the score itself where finished
   __shared__ int top[TOPKP_MAX_BEAMS];
   __shared__ uint8_t state[TOPKP_MAX_BEAMS];  // 0: no candidate, 1: live, 2: finished
+  __shared__ int slots[2][kBW];
   __shared__ unsigned long long tau_s, wk[kBW];
   __shared__ uint32_t wf[kBW];
-  __shared__ int count;
+  __shared__ int count, few;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t b = blockIdx.x;
-  const int n = a.n, S = a.slices;
+  const int n = a.n, S = a.slices, keep = beam_keep(a.n);
+  int phase = 0;
 
+  if (tid == 0) {
+    count = few = 0;
+    tau_s = 1ull;
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int k = warp; k < a.K; k += kBW) {
     const int64_t row = b * a.K + k;
@@ -392,8 +439,7 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge(const BeamArgs a) {
       const longlong2 st = a.stat[row * S + s];
       if (st.y > 0) c = max(c, (int)st.x);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) c = max(c, __shfl_xor_sync(0xffffffffu, c, o));
+    c = __reduce_max_sync(0xffffffffu, c);
     long long l = 0;
     for (int s = lane; s < S; s += 32) {
       const longlong2 st = a.stat[row * S + s];
@@ -405,10 +451,6 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge(const BeamArgs a) {
       shift[k] = l;
       top[k] = c;
     }
-  }
-  if (tid == 0) {
-    count = 0;
-    tau_s = 0ull;
   }
   __syncthreads();
   if (tid < a.K) {
@@ -425,65 +467,53 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge(const BeamArgs a) {
   __syncthreads();
 
   const int lists = a.K * S;
-  const unsigned long long* cand = a.cand + b * lists * (int64_t)n;
-  // entry i of list l: its key and place (key 0: none)
-  auto entry = [&](int l, int i, uint32_t* f) -> unsigned long long {
-    const int k = l / S;
-    const int st = state[k];
-    if (st == 0) return 0ull;
-    if (st == 2) {
-      *f = ~(uint32_t)(k * a.V + a.pad);
-      return (l == k * S && i == 0) ? fixed_key(shift[k]) : 0ull;
+  const unsigned long long* cand = a.cand + b * lists * (int64_t)keep;
+  // every candidate of the request: a warp takes a list, its lanes the entries
+  auto each = [&](auto&& f) {
+    for (int l = warp; l < lists; l += kBW) {
+      const int k = l / S;
+      const int st = state[k];
+      if (st == 2) {
+        if (l == k * S && lane == 0) f(fixed_key(shift[k]), ~(uint32_t)(k * a.V + a.pad));
+      } else if (st == 1) {
+        const int m = (int)(a.stat[b * lists + l].x >> 32);
+        for (int i = lane; i < m; i += 32) {
+          const unsigned long long e = cand[(int64_t)l * keep + i];
+          f(fixed_key(shift[k] + fixed_of(value_of_key<DT>((uint32_t)(e >> 32)))), ~(uint32_t)(k * a.V + (int)~(uint32_t)e));
+        }
+      }
     }
-    const unsigned long long e = cand[(int64_t)l * n + i];
-    if (e == 0ull) return 0ull;
-    *f = ~(uint32_t)(k * a.V + (int)~(uint32_t)e);
-    return fixed_key(shift[k] + fixed_of(value_of_key<DT>((uint32_t)(e >> 32))));
   };
-
-  const int depth = lists >= n ? 1 : (n + lists - 1) / lists;
-  const int want = (n + depth - 1) / depth;
-  // the lists' first entries; those past kHeads lists are read again below
-  for (int l = tid; l < lists && l < kHeads; l += kBeamThreads) {
-    uint32_t f;
-    head[l] = entry(l, 0, &f);
-  }
-  if (lists * (int64_t)n > 128) {
-    unsigned long long mine = 0ull;
-    uint32_t f;
-    for (int l = tid; l < lists; l += kBeamThreads) {
-      const unsigned long long e = depth == 1 && l < kHeads ? head[l] : entry(l, depth - 1, &f);
-      mine = e > mine ? e : mine;
+  auto pool = [&](unsigned long long e, uint32_t f) {
+    const int at = atomicAdd(&count, 1);
+    if (at < kPool) {
+      key[at] = e;
+      flat[at] = f;
     }
-    const int units = min(kBeamThreads, (lists + 1) & ~1);
+  };
+  unsigned long long mine = 0ull;
+  each([&](unsigned long long e, uint32_t f) {
+    mine = e > mine ? e : mine;
+    pool(e, f);
+  });
+  __syncthreads();
+  int found = count;
+  unsigned long long tau = 1ull;
+  if (found > kPool) {
     unit[tid] = mine;
     __syncthreads();
-    if (tid < units) {
-      int rank = 0;
-      for (int i = 0; i < units; i += 2) {
-        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&unit[i]);
-        rank += (o.x > mine || (o.x == mine && i < tid)) + (o.y > mine || (o.y == mine && i + 1 < tid));
-      }
-      if (rank == want - 1) tau_s = mine;
-    }
+    int rank = 0;
+    for (int i = 0; i < kBeamThreads; ++i) rank += (unit[i] > mine || (unit[i] == mine && i < tid)) ? 1 : 0;
+    if (rank == n - 1 && mine) tau_s = mine;
+    if (tid == 0) count = 0;  // read by all before the barrier above
+    __syncthreads();
+    tau = tau_s;
+    each([&](unsigned long long e, uint32_t f) {
+      if (e >= tau) pool(e, f);
+    });
+    __syncthreads();
+    found = count;
   }
-  __syncthreads();
-  const unsigned long long tau = tau_s > 0ull ? tau_s : 1ull;
-  for (int i = tid; i < lists * n; i += kBeamThreads) {
-    const int l = (int)((uint32_t)i / (uint32_t)n);
-    if (l < kHeads && head[l] < tau) continue;
-    uint32_t f = 0;
-    const unsigned long long e = entry(l, i - l * n, &f);
-    if (e >= tau) {
-      const int at = atomicAdd(&count, 1);
-      if (at < kList) {
-        key[at] = e;
-        flat[at] = f;
-      }
-    }
-  }
-  __syncthreads();
-  const int found = count;
   float* os = a.out_score + b * n;
   int32_t* op = a.out_parent + b * n;
   int32_t* ot = a.out_token + b * n;
@@ -498,12 +528,53 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge(const BeamArgs a) {
     op[r] = r % a.K;
     ot[r] = -1;
   };
-  if (found <= kList) {
+  if (found <= kPool) {
+    // lo: a bound with at least n candidates not below it, hardly more
+    const unsigned long long* ks = key;
+    const uint32_t* fs = flat;
+    if (found > 2 * n + 32) {
+      unit[tid] = mine;
+      __syncthreads();
+      unsigned long long hi = 0ull;
+      for (int i = lane; i < kBeamThreads; i += 32) hi = unit[i] > hi ? unit[i] : hi;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const unsigned long long w = __shfl_xor_sync(0xffffffffu, hi, o);
+        hi = w > hi ? w : hi;
+      }
+      unsigned long long lo = 1ull;
+      unsigned long long mid = hi > (1ull << 44) ? hi - (1ull << 43) : 1ull;  // 8 below the best: often the first half
+      ++hi;
+      while (hi - lo > 1) {
+        int c = 0;
+        for (int i = tid; i < found; i += kBeamThreads) c += key[i] >= mid ? 1 : 0;
+        c = block_count(c, slots, phase);
+        if (c >= n) lo = mid;
+        else hi = mid;
+        if (c >= n && c <= n + 32) break;
+        mid = lo + (hi - lo) / 2;
+      }
+      for (int i = tid; i < found; i += kBeamThreads)
+        if (key[i] >= lo) {
+          const int at = atomicAdd(&few, 1);
+          if (at < kFew) {
+            key2[at] = key[i];
+            flat2[at] = flat[i];
+          }
+        }
+      __syncthreads();
+      if (few <= kFew) {  // else many equal candidates: ranked among all
+        found = few;
+        ks = key2;
+        fs = flat2;
+      }
+    }
     for (int i = tid; i < found; i += kBeamThreads) {
-      const unsigned long long e = key[i];
-      const uint32_t f = flat[i];
+      const unsigned long long e = ks[i];
+      const uint32_t f = fs[i];
       int rank = 0;
-      for (int j = 0; j < found; ++j) rank += (key[j] > e || (key[j] == e && flat[j] > f)) ? 1 : 0;
+#pragma unroll 4
+      for (int j = 0; j < found; ++j) rank += (ks[j] > e || (ks[j] == e && fs[j] > f)) ? 1 : 0;
       if (rank < n) put(rank, e, f);
     }
     for (int r = found + tid; r < n; r += kBeamThreads) none(r);
@@ -515,17 +586,12 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge(const BeamArgs a) {
   for (int r = 0; r < n; ++r) {
     unsigned long long be = 0ull;
     uint32_t bf = 0;
-    for (int l = tid; l < lists; l += kBeamThreads)
-      for (int i = 0; i < n; ++i) {
-        uint32_t f = 0;
-        const unsigned long long e = entry(l, i, &f);
-        if (e < tau) break;
-        if (e < be) break;
-        if ((e < le || (e == le && f < lf)) && (e > be || f > bf)) {
-          be = e;
-          bf = f;
-        }
+    each([&](unsigned long long e, uint32_t f) {
+      if (e >= tau && (e < le || (e == le && f < lf)) && (e > be || (e == be && f > bf))) {
+        be = e;
+        bf = f;
       }
+    });
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const unsigned long long e = __shfl_xor_sync(0xffffffffu, be, o);
@@ -595,7 +661,7 @@ BeamPlan plan_beam(int64_t rows, int64_t V, int esize, int32_t n, int num_sms) {
   p.chunks = (int)((all + slices - 1) / slices);
   p.slices = (int)((all + p.chunks - 1) / p.chunks);
   p.stat_bytes = ((size_t)rows * p.slices * sizeof(longlong2) + 255) / 256 * 256;
-  p.cand_bytes = (size_t)rows * p.slices * n * sizeof(unsigned long long);
+  p.cand_bytes = (size_t)rows * p.slices * beam_keep(n) * sizeof(unsigned long long);
   return p;
 }
 

@@ -25,8 +25,8 @@ struct BeamArgs {
   int32_t chunks;  // chunks of a slice
   int32_t slices;  // CTAs per row
   // workspace, per (row, slice): shift and sum of the slice, its candidates
-  longlong2* stat;             // (c, sum of 2^(x log2 e - c) in 2^-38 units); sum 0 if nothing is finite
-  unsigned long long* cand;    // [rows * slices][n]: order key << 32 | ~index, descending; 0 past the last
+  longlong2* stat;             // (candidates << 32 | c, sum of 2^(x log2 e - c) in 2^-38 units); sum 0 if nothing is finite
+  unsigned long long* cand;    // [rows * slices][3 n]: order key << 32 | ~index, in no order
   float* out_score;
   int32_t* out_parent;
   int32_t* out_token;

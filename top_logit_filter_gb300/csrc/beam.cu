@@ -1,26 +1,18 @@
 // topkp_beam_select: the best continuations of each request's beams.
 //
 // Within one row the candidates' order is the order of the logits, since
-// score and normaliser shift a row as a whole.  So one pass over the logits
-// gives everything: each CTA holds a slice of a row in registers, sums its
-// exponentials, and lists the slice's n largest logits; a second kernel, one
-// CTA per request, turns those into scores and takes the n best.
+// score and normaliser shift a row as a whole.  One pass over the logits
+// leaves what the choice needs: each row's sum of exponentials, and the
+// largest logit of every unit of 512 bytes.  An element of the best n lies in
+// one of the n units with the best maxima (a unit before it in that order has
+// a maximum that beats it), so a second kernel, one CTA per request, takes
+// the n best units by (score of the maximum, position), reads those again,
+// 512 n bytes, and ranks their elements.  Nothing is selected in the pass
+// over the logits, and rows of equal values cost no more than others there.
 //
-// The sum.  exp(x) = 2^(x log2 e).  A slice sums 2^(x log2 e - c) with c the
-// integer ceil(max x log2 e): slices (and rows) then combine by exact powers
-// of two, and the largest term is in (1/2, 1].
-//
-// The n largest of a slice.  The slice goes through the CTA in chunks, each
-// thread four 16-byte vectors at a time, the next chunk on its way.  In the
-// first chunk, disjoint units of elements (those of one or of a few threads)
-// each have a maximum; the n-th largest of the maxima is reached by at least
-// n elements, and hardly any more when there are many units.  Every element
-// not below it is listed; later elements are listed if they are above the
-// bound.  When the list has outgrown 3 n, a bisection over the listed keys
-// (value, then index: no two are equal) finds one with n keys not below it:
-// those stay, and the bound moves up to it.  What is left at the end goes to
-// the second kernel in any order.  A chunk that overflows the list (rows of
-// many equal values) takes n rounds of a block-wide maximum instead.
+// The sum.  exp(x) = 2^(x log2 e).  A warp sums 2^(x log2 e - c) with c the
+// integer ceil(max x log2 e) of what it has seen: sums then combine by exact
+// powers of two, and the largest term is in (1/2, 1].
 #include <limits.h>
 
 #include "common.cuh"
@@ -29,9 +21,9 @@
 namespace topkp {
 namespace {
 
-constexpr int kList = 1024;   // listed candidates of a slice
-constexpr int kPool = 2560;   // of a request
-constexpr int kFew = 288;     // of a request, once cut
+constexpr int kMergeThreads = 512;
+constexpr int kMW = kMergeThreads / 32;
+constexpr int kPool = 1024;  // units, then elements, of a request that may be chosen
 constexpr float kLog2eHi = 1.44268798828125f;  // log2 e to 16 bits
 constexpr float kLog2eLo = 7.0526077e-06f;     // the rest
 // Logits beyond this magnitude count as this magnitude in the normaliser and
@@ -73,33 +65,11 @@ __device__ __forceinline__ float key_score(unsigned long long k) {
 
 constexpr int kBW = kBeamThreads / 32;
 
-// The sum of one value of each thread, with one barrier: `slots` has two
-// alternating rows, so that the next sum does not wait for this one's readers.
-__device__ __forceinline__ int block_count(int v, int (*slots)[kBW], int& phase) {
-  v = __reduce_add_sync(0xffffffffu, v);
-  if ((threadIdx.x & 31) == 0) slots[phase][threadIdx.x >> 5] = v;
-  __syncthreads();
-  int t = 0;
-#pragma unroll
-  for (int i = 0; i < kBW; ++i) t += slots[phase][i];
-  phase ^= 1;
-  return t;
+// The float of a float_order_key, and the key of -inf (0: no element).
+__device__ __forceinline__ float order_key_float(uint32_t k) {
+  return k ? __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k) : -INFINITY;
 }
-// A key with exactly `want` of list[0 .. found) not below it; want < found,
-// all keys different, all at least lo and below hi.  Every thread gets it.
-__device__ __forceinline__ unsigned long long bisect_keys(const unsigned long long* list, int found, int want,
-                                                          unsigned long long lo, unsigned long long hi,
-                                                          int (*slots)[kBW], int& phase) {
-  for (;;) {  // more than `want` keys are >= lo, fewer are >= hi: at most 64 halvings
-    const unsigned long long mid = lo + (hi - lo) / 2;
-    int c = 0;
-    for (int i = threadIdx.x; i < found; i += kBeamThreads) c += list[i] >= mid ? 1 : 0;
-    c = block_count(c, slots, phase);
-    if (c == want) return mid;
-    if (c > want) lo = mid;
-    else hi = mid;
-  }
-}
+constexpr uint32_t kNegInfKey = 0x007fffffu;
 
 // Two fp32 lanes in a 64-bit register, one instruction for both.
 __device__ __forceinline__ unsigned long long f32x2(float lo, float hi) {
@@ -146,133 +116,99 @@ __device__ __forceinline__ float vec_max(const uint4& q) {
   return fmaxf(elem<DT>(make_uint4(m, 0, 0, 0), 0), elem<DT>(make_uint4(m, 0, 0, 0), DT == TOPKP_F32 ? 0 : 1));
 }
 
-// Candidates that a slice may hand on.
-__host__ __device__ inline int beam_keep(int n) { return n < 16 ? 48 : 3 * n; }
-
-// The NV vectors of chunk elements [e, e + 256 * NV * VEC) that this thread
-// holds; a vector that sticks out of the row is read element by element, and
+// Vector `i` of a row's aligned window, which starts `lead` elements before
+// the row; one that sticks out of the row is read element by element, and
 // what lies outside reads as -inf.
-template <int DT, int NV>
-__device__ __forceinline__ void load_chunk(uint4 (&q)[NV], const typename DType<DT>::raw* xr, int e0, int V) {
+template <int DT>
+__device__ __forceinline__ uint4 edge_vector(const typename DType<DT>::raw* xr, int e, int V) {
   using raw = typename DType<DT>::raw;
   constexpr int VEC = 16 / (int)sizeof(raw);
-  if (e0 >= 0 && e0 + kBeamThreads * NV * VEC <= V) {
-    const uint4* p = reinterpret_cast<const uint4*>(xr + e0) + threadIdx.x;
+  uint32_t w[4];
 #pragma unroll
-    for (int u = 0; u < NV; ++u) q[u] = __ldcs(p + u * kBeamThreads);
+  for (int i = 0; i < 4; ++i) w[i] = DT == TOPKP_F32 ? 0xff800000u : DType<DT>::kNegInf * 0x10001u;
+  if (e < V && e + VEC > 0) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      if (e + j >= 0 && e + j < V) {
+        const uint32_t r = xr[e + j];
+        if (DT == TOPKP_F32) w[j] = r;
+        else w[j >> 1] = (j & 1) ? ((w[j >> 1] & 0xffffu) | (r << 16)) : ((w[j >> 1] & 0xffff0000u) | r);
+      }
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// A warp's NV * 32 vectors from row element e0 on.
+template <int DT, int NV>
+__device__ __forceinline__ void load_vectors(uint4 (&q)[NV], const typename DType<DT>::raw* xr, int e0, int V) {
+  constexpr int VEC = 16 / (int)sizeof(typename DType<DT>::raw);
+  const int lane = threadIdx.x & 31;
+  if (e0 >= 0 && e0 + NV * 32 * VEC <= V) {
+    const uint4* p = reinterpret_cast<const uint4*>(xr + e0) + lane;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) q[u] = __ldcs(p + u * 32);
     return;
   }
 #pragma unroll
   for (int u = 0; u < NV; ++u) {
-    const int e = e0 + (u * kBeamThreads + (int)threadIdx.x) * VEC;
-    if (e >= 0 && e + VEC <= V) {
-      q[u] = __ldcs(reinterpret_cast<const uint4*>(xr + e));
-    } else {
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = DT == TOPKP_F32 ? 0xff800000u : DType<DT>::kNegInf * 0x10001u;
-      if (e < V && e + VEC > 0) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          if (e + j >= 0 && e + j < V) {
-            const uint32_t r = xr[e + j];
-            if (DT == TOPKP_F32) w[j] = r;
-            else w[j >> 1] = (j & 1) ? ((w[j >> 1] & 0xffffu) | (r << 16)) : ((w[j >> 1] & 0xffff0000u) | r);
-          }
-        }
-      }
-      q[u] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+    const int e = e0 + (u * 32 + lane) * VEC;
+    q[u] = e >= 0 && e + VEC <= V ? __ldcs(reinterpret_cast<const uint4*>(xr + e)) : edge_vector<DT>(xr, e, V);
   }
 }
 
-struct ScanShared {
-  unsigned long long list[2][kList];  // the current list, and where its first n go
-  __align__(16) float unit[kBeamThreads];
-  float wmax[kBW];
-  unsigned long long wkey[kBW];
-  unsigned long long wsum[kBW];
-  int slots[2][kBW];
-  float tau;
-  int count;
-};
-
 template <int DT, int NV>
-__global__ void __launch_bounds__(kBeamThreads, 3) beam_scan(const BeamArgs a) {
+__global__ void __launch_bounds__(kBeamThreads, 4) beam_scan(const BeamArgs a) {
   using raw = typename DType<DT>::raw;
   constexpr int VEC = 16 / (int)sizeof(raw);
-  constexpr int CHUNK = kBeamThreads * NV * VEC;
-  __shared__ ScanShared s;
+  constexpr int PIECE = NV * 32 * VEC;     // elements a warp takes at a time
+  constexpr int CHUNK = kBW * PIECE;
+  __shared__ float wtop[kBW];
+  __shared__ unsigned long long wsum[kBW];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t part = blockIdx.x;
   const uint32_t row = part / (uint32_t)a.slices;
   const int slice = (int)(part - row * (uint32_t)a.slices);
-  const int keep = beam_keep(a.n);
-  unsigned long long* out = a.cand + (int64_t)part * keep;
-
   const float score = a.scores[row];
   if ((a.finished && a.finished[row]) || score == -INFINITY) {
-    if (tid == 0) a.stat[part] = make_longlong2(0, 0);
+    if (threadIdx.x == 0) a.stat[part] = make_longlong2(0, 0);
     return;
   }
 
-  // 16-byte vectors of the row's aligned window
   const raw* xr = reinterpret_cast<const raw*>(a.x) + row * a.ldx;
   const int lead = (int)((reinterpret_cast<uintptr_t>(xr) & 15) / sizeof(raw));
-  const int e_first = slice * a.chunks * CHUNK - lead;  // row index of this slice's first element
-  const int e_end = min(e_first + a.chunks * CHUNK, a.V);
+  // row element of this warp's first piece, and the end of the slice
+  const int c_first = slice * a.chunks;
+  int e0 = c_first * CHUNK + warp * PIECE - lead;
+  const int e_end = min((c_first + a.chunks) * CHUNK - lead, a.V);
+  uint32_t* units = a.units + (int64_t)row * a.unit_count + (c_first * kBW + warp) * NV;
 
   uint4 q[NV], nx[NV];
-  load_chunk<DT, NV>(q, xr, e_first, a.V);
-  int cur = 0;             // which list is current
-  int phase = 0;
-  int held = 0;            // entries of it
-  float tau = -INFINITY;   // an element is listed if it is above (in the first chunk: not below)
-  float c = -INFINITY;     // this thread's shift: an integer, or -inf before its first finite element
+  load_vectors<DT, NV>(q, xr, e0, a.V);
+  float c = -INFINITY;            // the warp's shift: an integer, or -inf before its first finite element
   unsigned long long acc = 0ull;  // this thread's sum in units of 2^(c - 38)
-  if (tid == 0) s.count = 0;
-
 #pragma unroll 1
-  for (int e0 = e_first; e0 < e_end; e0 += CHUNK) {
-    const bool first = e0 == e_first, last = e0 + CHUNK >= e_end;
-    if (!last) load_chunk<DT, NV>(nx, xr, e0 + CHUNK, a.V);
-    float vm[NV], m = -INFINITY;
+  for (; e0 < e_end; e0 += CHUNK, units += kBW * NV) {
+    if (e0 + CHUNK < e_end) load_vectors<DT, NV>(nx, xr, e0 + CHUNK, a.V);
+    uint32_t key = 0;  // of unit `lane`, for lane < NV
+    uint32_t kmax = 0;
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
-      vm[u] = vec_max<DT>(q[u]);
-      m = fmaxf(m, vm[u]);
+      const float v = vec_max<DT>(q[u]);
+      const uint32_t k = __reduce_max_sync(0xffffffffu, float_order_key(v));
+      key = lane == u ? k : key;
+      kmax = max(kmax, k);
     }
-    if (first) {
-      // units of 1, 2 or 4 threads, at least 2 n of them
-      const int per = a.n <= 32 ? 4 : a.n <= 64 ? 2 : 1;
-      float um = m;
-      if (per >= 2) um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, 1));
-      if (per >= 4) um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, 2));
-      if (tid % per == 0) s.unit[tid / per] = um;
-      if (tid == 0) s.tau = -INFINITY;
-      __syncthreads();
-      const int units = kBeamThreads / per;
-      if (tid < units) {
-        const float mine = s.unit[tid];
-        int rank = 0;
-        for (int i = 0; i < units; i += 4) {
-          const float4 o = *reinterpret_cast<const float4*>(&s.unit[i]);
-          rank += (o.x > mine || (o.x == mine && i < tid)) + (o.y > mine || (o.y == mine && i + 1 < tid)) +
-                  (o.z > mine || (o.z == mine && i + 2 < tid)) + (o.w > mine || (o.w == mine && i + 3 < tid));
-        }
-        if (rank == a.n - 1) s.tau = mine;
-      }
-    }
-    // the sum, in 2^c units of this thread's own
-    const float mc = fminf(fmaxf(m, -kFar), kFar);
-    if (m > -INFINITY && mc * (kLog2eHi + kLog2eLo) > c) {
-      const float nc = ceilf(mc * (kLog2eHi + kLog2eLo));
-      acc = c == -INFINITY ? 0ull : acc >> min((int)(nc - c), 63);
-      c = nc;
-    }
-    const unsigned long long c2 = f32x2(-c, -c);
+    if (lane < NV) units[lane] = key;
+    const float m = order_key_float(kmax);
     if (m > -INFINITY) {
+      const float mc = fminf(fmaxf(m, -kFar), kFar) * (kLog2eHi + kLog2eLo);
+      if (mc > c) {
+        const float nc = ceilf(mc);
+        acc = c == -INFINITY ? 0ull : acc >> min((int)(nc - c), 63);
+        c = nc;
+      }
+      const unsigned long long c2 = f32x2(-c, -c);
       unsigned long long sum2 = 0ull;
       if (fabsf(m) <= kFar) {
 #pragma unroll
@@ -292,147 +228,103 @@ __global__ void __launch_bounds__(kBeamThreads, 3) beam_scan(const BeamArgs a) {
       }
       float s0, s1;
       asm("mov.b64 {%0, %1}, %2;" : "=f"(s0), "=f"(s1) : "l"(sum2));
-      acc += f2ull_rn(s0 * kSumScale) + f2ull_rn(s1 * kSumScale);
-    }
-    if (first) {
-      __syncthreads();
-      tau = s.tau;
-    }
-    int mine = 0;
-    auto wanted = [&](float x) { return first ? x >= tau && x > -INFINITY : x > tau; };
-#pragma unroll
-    for (int u = 0; u < NV; ++u)
-      if (wanted(vm[u])) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float x = elem<DT>(q[u], j);
-          if (wanted(x)) {
-            ++mine;
-            const int at = atomicAdd(&s.count, 1);
-            const uint32_t idx = (uint32_t)(e0 + (u * kBeamThreads + tid) * VEC + j);
-            if (at < kList)
-              s.list[cur][at] = ((unsigned long long)order_key<DT>(elem_raw<DT>(q[u], j)) << 32) | (uint32_t)~idx;
-          }
-        }
-      }
-    // the count is summed, not read from s.count: a fast thread may be adding
-    // the next chunk's already
-    const int found = held + block_count(mine, s.slots, phase);
-    if (found > kList) {
-      // many equal or rising values: the next one in order, n times, of this
-      // chunk and of what was kept (entries listed by this chunk are in q)
-      unsigned long long prev = ~0ull;
-#pragma unroll 1
-      for (int r = 0; r < a.n; ++r) {
-        unsigned long long best = 0ull;
-#pragma unroll
-        for (int u = 0; u < NV; ++u)  // the keys are made anew each round, not held
-          asm volatile("" : "+r"(q[u].x), "+r"(q[u].y), "+r"(q[u].z), "+r"(q[u].w));
-        for (int i = tid; i < held; i += kBeamThreads) {
-          const unsigned long long k = s.list[cur][i];
-          if (k < prev && k > best) best = k;
-        }
-#pragma unroll
-        for (int u = 0; u < NV; ++u)
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            const float x = elem<DT>(q[u], j);
-            const uint32_t idx = (uint32_t)(e0 + (u * kBeamThreads + tid) * VEC + j);
-            const unsigned long long k =
-                ((unsigned long long)order_key<DT>(elem_raw<DT>(q[u], j)) << 32) | (uint32_t)~idx;
-            if (wanted(x) && k < prev && k > best) best = k;
-          }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          const unsigned long long w = __shfl_xor_sync(0xffffffffu, best, o);
-          best = w > best ? w : best;
-        }
-        if (lane == 0) s.wkey[warp] = best;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kBW; ++i) best = s.wkey[i] > best ? s.wkey[i] : best;
-        __syncthreads();
-        if (tid == 0) s.list[cur ^ 1][r] = best;
-        prev = best;
-      }
-      if (tid == 0) s.count = a.n;
-      __syncthreads();
-      cur ^= 1;
-      held = a.n;
-      tau = value_of_key<DT>((uint32_t)(s.list[cur][a.n - 1] >> 32));
-    } else if (found > keep) {
-      const unsigned long long bound =
-          bisect_keys(s.list[cur], found, a.n, 0ull, DT == TOPKP_F32 ? ~0ull : 1ull << 48, s.slots, phase);
-      if (tid == 0) s.count = 0;
-      __syncthreads();
-      for (int i = tid; i < found; i += kBeamThreads) {
-        const unsigned long long k = s.list[cur][i];
-        if (k >= bound) s.list[cur ^ 1][atomicAdd(&s.count, 1)] = k;
-      }
-      cur ^= 1;
-      // the bound lies above the largest key dropped, so a later element
-      // (of a larger index) with that key's value is not wanted either
-      tau = value_of_key<DT>((uint32_t)(bound >> 32));
-      held = a.n;
-    } else {
-      held = found;
+      acc += f2ull_rn((s0 + s1) * kSumScale);
     }
 #pragma unroll
     for (int u = 0; u < NV; ++u) q[u] = nx[u];
   }
 
-  // the slice's sum: the threads' at the largest of their shifts, exact and in no order
-  float top = c;
+  // the slice's sum: the warps' at the largest of their shifts, exact and in no order
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane == 0) s.wmax[warp] = top;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kBW; ++i) top = fmaxf(top, s.wmax[i]);
-  unsigned long long total = c == -INFINITY ? 0ull : acc >> min((int)(top - c), 63);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  if (lane == 0) s.wsum[warp] = total;
-  __syncthreads();
-  if (tid == 0) {
-    total = 0;
-    for (int i = 0; i < kBW; ++i) total += s.wsum[i];
-    // shift in the low half, number of candidates in the high one
-    a.stat[part] = make_longlong2((long long)(((unsigned long long)held << 32) | (uint32_t)(top == -INFINITY ? 0 : (int)top)),
-                                  (long long)total);
+  for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+  if (lane == 0) {
+    wtop[warp] = c;
+    wsum[warp] = acc;
   }
-  for (int i = tid; i < held; i += kBeamThreads) out[i] = s.list[cur][i];
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float top = -INFINITY;
+    for (int i = 0; i < kBW; ++i) top = fmaxf(top, wtop[i]);
+    unsigned long long total = 0ull;
+    for (int i = 0; i < kBW; ++i)
+      if (wtop[i] > -INFINITY) total += wsum[i] >> min((int)(top - wtop[i]), 63);
+    a.stat[part] = make_longlong2(top == -INFINITY ? 0 : (long long)(int)top, (long long)total);
+  }
 }
 
-// One CTA per request: the candidates of its beams' slices become scores in
-// shared memory, a bisection leaves n of them, and each one's rank among
-// those is its place.  More candidates than the pool holds are cut first by
-// the n-th largest of the threads' own maxima.
+// (key, place) pairs in shared memory: larger key first, then larger place.
+struct Pool {
+  unsigned long long key[kPool];
+  uint32_t place[kPool];
+  int count;
+};
+__device__ __forceinline__ void pool_add(Pool& p, unsigned long long key, uint32_t place) {
+  const int at = atomicAdd(&p.count, 1);
+  if (at < kPool) {
+    p.key[at] = key;
+    p.place[at] = place;
+  }
+}
+// The best pair below (lk, lp) that `each` hands out, over the CTA.
+template <class F>
+__device__ __forceinline__ void next_best(F&& each, unsigned long long& lk, uint32_t& lp, unsigned long long* wk,
+                                          uint32_t* wp) {
+  unsigned long long bk = 0ull;
+  uint32_t bp = 0;
+  each([&](unsigned long long k, uint32_t p) {
+    if ((k < lk || (k == lk && p < lp)) && (k > bk || (k == bk && p > bp))) {
+      bk = k;
+      bp = p;
+    }
+  });
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const unsigned long long k = __shfl_xor_sync(0xffffffffu, bk, o);
+    const uint32_t p = __shfl_xor_sync(0xffffffffu, bp, o);
+    if (k > bk || (k == bk && p > bp)) {
+      bk = k;
+      bp = p;
+    }
+  }
+  __syncthreads();  // the slots may still be read from the last round
+  if ((threadIdx.x & 31) == 0) {
+    wk[threadIdx.x >> 5] = bk;
+    wp[threadIdx.x >> 5] = bp;
+  }
+  __syncthreads();
+  for (int i = 0; i < kMW; ++i)
+    if (wk[i] > bk || (wk[i] == bk && wp[i] > bp)) {
+      bk = wk[i];
+      bp = wp[i];
+    }
+  lk = bk;
+  lp = bp;
+}
+
+// One CTA per request.
 template <int DT>
-__global__ void __launch_bounds__(kBeamThreads) beam_merge(const BeamArgs a) {
-  __shared__ unsigned long long key[kPool];
-  __shared__ uint32_t flat[kPool];  // ~(k * V + v): larger is earlier
-  __shared__ unsigned long long key2[kFew];
-  __shared__ uint32_t flat2[kFew];
-  __shared__ __align__(16) unsigned long long unit[kBeamThreads];
+__global__ void __launch_bounds__(kMergeThreads) beam_merge(const BeamArgs a) {
+  using raw = typename DType<DT>::raw;
+  constexpr int VEC = 16 / (int)sizeof(raw);
+  __shared__ Pool pool;
+  __shared__ __align__(16) unsigned long long best[kMergeThreads];
+  __shared__ unsigned long long ukey[TOPKP_MAX_CANDIDATES];  // the chosen units, in order
+  __shared__ uint32_t uplace[TOPKP_MAX_CANDIDATES];
   __shared__ long long shift[TOPKP_MAX_BEAMS];  // score - normaliser; the score itself where finished
   __shared__ int top[TOPKP_MAX_BEAMS];
   __shared__ uint8_t state[TOPKP_MAX_BEAMS];  // 0: no candidate, 1: live, 2: finished
-  __shared__ int slots[2][kBW];
-  __shared__ unsigned long long tau_s, wk[kBW];
-  __shared__ uint32_t wf[kBW];
-  __shared__ int count, few;
+  __shared__ unsigned long long tau_s, wk[kMW];
+  __shared__ uint32_t wp[kMW];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t b = blockIdx.x;
-  const int n = a.n, S = a.slices, keep = beam_keep(a.n);
-  int phase = 0;
+  const int n = a.n, S = a.slices, U = a.unit_count;
 
   if (tid == 0) {
-    count = few = 0;
+    pool.count = 0;
     tau_s = 1ull;
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int k = warp; k < a.K; k += kBW) {
+  for (int k = warp; k < a.K; k += kMW) {
     const int64_t row = b * a.K + k;
     int c = INT_MIN;
     for (int s = lane; s < S; s += 32) {
@@ -466,160 +358,156 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge(const BeamArgs a) {
   }
   __syncthreads();
 
-  const int lists = a.K * S;
-  const unsigned long long* cand = a.cand + b * lists * (int64_t)keep;
-  // every candidate of the request: a warp takes a list, its lanes the entries
-  auto each = [&](auto&& f) {
-    for (int l = warp; l < lists; l += kBW) {
-      const int k = l / S;
-      const int st = state[k];
-      if (st == 2) {
-        if (l == k * S && lane == 0) f(fixed_key(shift[k]), ~(uint32_t)(k * a.V + a.pad));
-      } else if (st == 1) {
-        const int m = (int)(a.stat[b * lists + l].x >> 32);
-        for (int i = lane; i < m; i += 32) {
-          const unsigned long long e = cand[(int64_t)l * keep + i];
-          f(fixed_key(shift[k] + fixed_of(value_of_key<DT>((uint32_t)(e >> 32)))), ~(uint32_t)(k * a.V + (int)~(uint32_t)e));
+  // ---- the n best units.  Place of unit u of beam k: ~(k U + u) ----
+  const uint32_t* units = a.units + b * a.K * (int64_t)U;
+  const int share = max(1, kMW / a.K);  // warps to a beam
+  auto row_units = [&](int k) {         // units of the beam's row that hold an element
+    const raw* xr = reinterpret_cast<const raw*>(a.x) + (b * a.K + k) * a.ldx;
+    const int lead = (int)((reinterpret_cast<uintptr_t>(xr) & 15) / sizeof(raw));
+    return (a.V + lead + 32 * VEC - 1) / (32 * VEC);
+  };
+  auto unit_key = [&](int k, uint32_t fk) { return fixed_key(shift[k] + fixed_of(order_key_float(fk))); };
+  // every unit whose key may reach `least` (0: all); finished beams are a unit of their own
+  auto each_unit = [&](unsigned long long least, auto&& f) {
+    for (int i = warp; i < a.K * share; i += kMW) {
+      const int k = i / share, from = (i - k * share) * 32 + lane;
+      if (state[k] == 2) {
+        const unsigned long long e = fixed_key(shift[k]);
+        if (from == 0 && e >= least) f(e, ~(uint32_t)(k * U));
+      } else if (state[k] == 1) {
+        // the bound as a logit of this beam, one part in 10^6 lower
+        uint32_t low = kNegInfKey + 1;
+        if (least > 1ull) {
+          const float x = (float)((long long)(least ^ 0x8000000000000000ull) - shift[k]) * (1.0f / kMassScaleF);
+          if (x > -0.999f * kFar) low = float_order_key(x - fabsf(x) * 1e-6f - 1e-6f);
+        }
+        const uint32_t* ur = units + (int64_t)k * U;
+        const int end = row_units(k);
+        for (int u = from; u < end; u += 32 * share) {
+          const uint32_t fk = ur[u];
+          if (fk >= low) {
+            const unsigned long long e = unit_key(k, fk);
+            if (e >= least) f(e, ~(uint32_t)(k * U + u));
+          }
         }
       }
     }
   };
-  auto pool = [&](unsigned long long e, uint32_t f) {
-    const int at = atomicAdd(&count, 1);
-    if (at < kPool) {
-      key[at] = e;
-      flat[at] = f;
+  {
+    // the n-th largest of the threads' own maxima bounds the n-th unit
+    unsigned long long mine = 0ull;
+    for (int i = warp; i < a.K * share; i += kMW) {
+      const int k = i / share, from = (i - k * share) * 32 + lane;
+      if (state[k] == 2 && from == 0) mine = max(mine, fixed_key(shift[k]));
+      if (state[k] != 1) continue;
+      uint32_t fk = 0;
+      const uint32_t* ur = units + (int64_t)k * U;
+      const int end = row_units(k);
+#pragma unroll 4
+      for (int u = from; u < end; u += 32 * share) fk = max(fk, ur[u]);
+      if (fk > kNegInfKey) mine = max(mine, unit_key(k, fk));
+    }
+    const int used = min(a.K * share, kMW) * 32;
+    best[tid] = mine;
+    __syncthreads();
+    if (tid < used && mine) {
+      int rank = 0;
+#pragma unroll 4
+      for (int i = 0; i < used; i += 2) {
+        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&best[i]);
+        rank += (o.x > mine || (o.x == mine && i < tid)) + (o.y > mine || (o.y == mine && i + 1 < tid));
+      }
+      if (rank == n - 1) tau_s = mine;
+    }
+    __syncthreads();
+  }
+  unsigned long long least = tau_s;
+  each_unit(least, [&](unsigned long long k, uint32_t p) { pool_add(pool, k, p); });
+  __syncthreads();
+  const int listed = pool.count;
+  int chosen = min(listed, n);
+  if (listed <= kPool) {
+    for (int i = tid; i < listed; i += kMergeThreads) {
+      const unsigned long long k = pool.key[i];
+      const uint32_t p = pool.place[i];
+      int rank = 0;
+#pragma unroll 4
+      for (int j = 0; j < listed; ++j) rank += (pool.key[j] > k || (pool.key[j] == k && pool.place[j] > p)) ? 1 : 0;
+      if (rank < n) {
+        ukey[rank] = k;
+        uplace[rank] = p;
+      }
+    }
+  } else {  // many equal maxima: the next unit in order, n times
+    unsigned long long lk = ~0ull;
+    uint32_t lp = ~0u;
+    for (int r = 0; r < n; ++r) {
+      next_best([&](auto&& f) { each_unit(least, f); }, lk, lp, wk, wp);
+      if (tid == 0) {
+        ukey[r] = lk;
+        uplace[r] = lp;
+      }
+    }
+  }
+  __syncthreads();
+  if (tid == 0) pool.count = 0;  // its readers are past the barrier above
+  __syncthreads();
+
+  // ---- their elements.  Place of token v of beam k: ~(k V + v) ----
+  least = chosen == n ? ukey[n - 1] : 1ull;  // n maxima reach it
+  auto each_element = [&](auto&& f) {
+    for (int i = warp; i < chosen; i += kMW) {
+      const uint32_t p = ~uplace[i];
+      const int k = (int)(p / (uint32_t)U), u = (int)(p - (uint32_t)k * U);
+      if (state[k] == 2) {
+        if (lane == 0) f(fixed_key(shift[k]), ~(uint32_t)(k * a.V + a.pad));
+        continue;
+      }
+      const raw* xr = reinterpret_cast<const raw*>(a.x) + (b * a.K + k) * a.ldx;
+      const int lead = (int)((reinterpret_cast<uintptr_t>(xr) & 15) / sizeof(raw));
+      uint4 q[1];
+      const int e = u * 32 * VEC - lead;
+      load_vectors<DT, 1>(q, xr, e, a.V);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const float x = elem<DT>(q[0], j);
+        if (x > -INFINITY) {
+          const unsigned long long key = fixed_key(shift[k] + fixed_of(x));
+          if (key >= least) f(key, ~(uint32_t)(k * a.V + e + lane * VEC + j));
+        }
+      }
     }
   };
-  unsigned long long mine = 0ull;
-  each([&](unsigned long long e, uint32_t f) {
-    mine = e > mine ? e : mine;
-    pool(e, f);
-  });
+  each_element([&](unsigned long long k, uint32_t p) { pool_add(pool, k, p); });
   __syncthreads();
-  int found = count;
-  unsigned long long tau = 1ull;
-  if (found > kPool) {
-    unit[tid] = mine;
-    __syncthreads();
-    int rank = 0;
-    for (int i = 0; i < kBeamThreads; ++i) rank += (unit[i] > mine || (unit[i] == mine && i < tid)) ? 1 : 0;
-    if (rank == n - 1 && mine) tau_s = mine;
-    if (tid == 0) count = 0;  // read by all before the barrier above
-    __syncthreads();
-    tau = tau_s;
-    each([&](unsigned long long e, uint32_t f) {
-      if (e >= tau) pool(e, f);
-    });
-    __syncthreads();
-    found = count;
-  }
+  const int found = pool.count;
   float* os = a.out_score + b * n;
   int32_t* op = a.out_parent + b * n;
   int32_t* ot = a.out_token + b * n;
-  auto put = [&](int r, unsigned long long e, uint32_t f) {
-    const uint32_t p = ~f;
-    os[r] = key_score(e);
-    op[r] = (int32_t)(p / (uint32_t)a.V);
-    ot[r] = (int32_t)(p % (uint32_t)a.V);
-  };
-  auto none = [&](int r) {
-    os[r] = -INFINITY;
-    op[r] = r % a.K;
-    ot[r] = -1;
+  auto put = [&](int r, unsigned long long k, uint32_t place) {
+    const uint32_t p = ~place;
+    os[r] = k ? key_score(k) : -INFINITY;
+    op[r] = k ? (int32_t)(p / (uint32_t)a.V) : r % a.K;
+    ot[r] = k ? (int32_t)(p % (uint32_t)a.V) : -1;
   };
   if (found <= kPool) {
-    // lo: a bound with at least n candidates not below it, hardly more
-    const unsigned long long* ks = key;
-    const uint32_t* fs = flat;
-    if (found > 2 * n + 32) {
-      unit[tid] = mine;
-      __syncthreads();
-      unsigned long long hi = 0ull;
-      for (int i = lane; i < kBeamThreads; i += 32) hi = unit[i] > hi ? unit[i] : hi;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const unsigned long long w = __shfl_xor_sync(0xffffffffu, hi, o);
-        hi = w > hi ? w : hi;
-      }
-      unsigned long long lo = 1ull;
-      unsigned long long mid = hi > (1ull << 44) ? hi - (1ull << 43) : 1ull;  // 8 below the best: often the first half
-      ++hi;
-      while (hi - lo > 1) {
-        int c = 0;
-        for (int i = tid; i < found; i += kBeamThreads) c += key[i] >= mid ? 1 : 0;
-        c = block_count(c, slots, phase);
-        if (c >= n) lo = mid;
-        else hi = mid;
-        if (c >= n && c <= n + 32) break;
-        mid = lo + (hi - lo) / 2;
-      }
-      for (int i = tid; i < found; i += kBeamThreads)
-        if (key[i] >= lo) {
-          const int at = atomicAdd(&few, 1);
-          if (at < kFew) {
-            key2[at] = key[i];
-            flat2[at] = flat[i];
-          }
-        }
-      __syncthreads();
-      if (few <= kFew) {  // else many equal candidates: ranked among all
-        found = few;
-        ks = key2;
-        fs = flat2;
-      }
-    }
-    for (int i = tid; i < found; i += kBeamThreads) {
-      const unsigned long long e = ks[i];
-      const uint32_t f = fs[i];
+    for (int i = tid; i < found; i += kMergeThreads) {
+      const unsigned long long k = pool.key[i];
+      const uint32_t p = pool.place[i];
       int rank = 0;
 #pragma unroll 4
-      for (int j = 0; j < found; ++j) rank += (ks[j] > e || (ks[j] == e && fs[j] > f)) ? 1 : 0;
-      if (rank < n) put(rank, e, f);
+      for (int j = 0; j < found; ++j) rank += (pool.key[j] > k || (pool.key[j] == k && pool.place[j] > p)) ? 1 : 0;
+      if (rank < n) put(rank, k, p);
     }
-    for (int r = found + tid; r < n; r += kBeamThreads) none(r);
+    for (int r = found + tid; r < n; r += kMergeThreads) put(r, 0ull, 0u);
     return;
   }
-  // many equal candidates: the next one in order, n times
-  unsigned long long le = ~0ull;
-  uint32_t lf = ~0u;
+  // many equal elements: the next one in order, n times
+  unsigned long long lk = ~0ull;
+  uint32_t lp = ~0u;
   for (int r = 0; r < n; ++r) {
-    unsigned long long be = 0ull;
-    uint32_t bf = 0;
-    each([&](unsigned long long e, uint32_t f) {
-      if (e >= tau && (e < le || (e == le && f < lf)) && (e > be || (e == be && f > bf))) {
-        be = e;
-        bf = f;
-      }
-    });
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const unsigned long long e = __shfl_xor_sync(0xffffffffu, be, o);
-      const uint32_t f = __shfl_xor_sync(0xffffffffu, bf, o);
-      if (e > be || (e == be && f > bf)) {
-        be = e;
-        bf = f;
-      }
-    }
-    if (lane == 0) {
-      wk[warp] = be;
-      wf[warp] = bf;
-    }
-    __syncthreads();
-    be = wk[0];
-    bf = wf[0];
-    for (int i = 1; i < kBW; ++i)
-      if (wk[i] > be || (wk[i] == be && wf[i] > bf)) {
-        be = wk[i];
-        bf = wf[i];
-      }
-    __syncthreads();
-    if (tid == 0) {
-      if (be) put(r, be, bf);
-      else none(r);
-    }
-    le = be;
-    lf = bf;
+    next_best(each_element, lk, lp, wk, wp);
+    if (tid == 0) put(r, lk, lp);
   }
 }
 
@@ -633,7 +521,7 @@ cudaError_t launch_dt(const BeamArgs& a, cudaStream_t s) {
   // the merge's launch overlaps the scan; it waits for the scan's results itself
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned int)a.B);
-  cfg.blockDim = dim3(kBeamThreads);
+  cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -646,14 +534,14 @@ cudaError_t launch_dt(const BeamArgs& a, cudaStream_t s) {
 }  // namespace
 
 // A row is cut into slices of whole chunks so that the device has about
-// three waves of three CTAs an SM, and into single short chunks when there
+// three waves of four CTAs an SM, and into single short chunks when there
 // are too few rows for that.
-BeamPlan plan_beam(int64_t rows, int64_t V, int esize, int32_t n, int num_sms) {
+BeamPlan plan_beam(int64_t rows, int64_t V, int esize, int num_sms) {
   BeamPlan p;
   const int vec = 16 / esize;
   // the aligned window may start up to vec - 1 elements before the row
   auto chunks = [&](int nv) { return (V + vec - 1 + (int64_t)kBeamThreads * nv * vec - 1) / ((int64_t)kBeamThreads * nv * vec); };
-  const int64_t wave = 3LL * num_sms;
+  const int64_t wave = 4LL * num_sms;
   p.nv = rows * chunks(4) >= wave ? 4 : 1;
   const int64_t all = chunks(p.nv);
   int64_t slices = (3 * wave + rows - 1) / rows;
@@ -661,7 +549,8 @@ BeamPlan plan_beam(int64_t rows, int64_t V, int esize, int32_t n, int num_sms) {
   p.chunks = (int)((all + slices - 1) / slices);
   p.slices = (int)((all + p.chunks - 1) / p.chunks);
   p.stat_bytes = ((size_t)rows * p.slices * sizeof(longlong2) + 255) / 256 * 256;
-  p.cand_bytes = (size_t)rows * p.slices * beam_keep(n) * sizeof(unsigned long long);
+  p.unit_count = p.slices * p.chunks * kBW * p.nv;
+  p.unit_bytes = (size_t)rows * p.unit_count * sizeof(uint32_t);
   return p;
 }
 

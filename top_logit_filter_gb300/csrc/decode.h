@@ -24,9 +24,10 @@ struct BeamArgs {
   int32_t nv;      // vectors of a chunk per thread: 1 or 4
   int32_t chunks;  // chunks of a slice
   int32_t slices;  // CTAs per row
-  // workspace, per (row, slice): shift and sum of the slice, its candidates
-  longlong2* stat;             // (candidates << 32 | c, sum of 2^(x log2 e - c) in 2^-38 units); sum 0 if nothing is finite
-  unsigned long long* cand;    // [rows * slices][3 n]: order key << 32 | ~index, in no order
+  // workspace
+  longlong2* stat;             // [rows][slices]: (c, sum of 2^(x log2 e - c) in 2^-38 units); sum 0 if nothing is finite
+  uint32_t* units;             // [rows][unit_count]: order key of the largest logit of each 512 bytes
+  int32_t unit_count;
   float* out_score;
   int32_t* out_parent;
   int32_t* out_token;
@@ -34,9 +35,10 @@ struct BeamArgs {
 
 struct BeamPlan {
   int nv, chunks, slices;
-  size_t stat_bytes, cand_bytes;
+  int unit_count;
+  size_t stat_bytes, unit_bytes;
 };
-BeamPlan plan_beam(int64_t rows, int64_t V, int esize, int32_t n, int num_sms);
+BeamPlan plan_beam(int64_t rows, int64_t V, int esize, int num_sms);
 cudaError_t launch_beam(topkp_dtype dt, const BeamArgs& a, cudaStream_t s);
 
 // ---------------------------------------------------------------- reorder

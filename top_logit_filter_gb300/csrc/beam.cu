@@ -23,6 +23,7 @@ namespace {
 
 constexpr int kMergeThreads = 512;
 constexpr int kMW = kMergeThreads / 32;
+constexpr int kAhead = 4;  // 16-byte reads of unit maxima on their way at once
 constexpr int kPool = 1024;  // units, then elements, of a request that may be chosen
 constexpr float kLog2eHi = 1.44268798828125f;  // log2 e to 16 bits
 constexpr float kLog2eLo = 7.0526077e-06f;     // the rest
@@ -258,6 +259,10 @@ struct Pool {
   uint32_t place[kPool];
   int count;
 };
+// 1 if pair a comes before pair b, without a branch.
+__device__ __forceinline__ int before(unsigned long long ak, uint32_t ap, unsigned long long bk, uint32_t bp) {
+  return (int)(ak > bk) | ((int)(ak == bk) & (int)(ap > bp));
+}
 __device__ __forceinline__ void pool_add(Pool& p, unsigned long long key, uint32_t place) {
   const int at = atomicAdd(&p.count, 1);
   if (at < kPool) {
@@ -366,6 +371,12 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const BeamArgs a) {
     const int lead = (int)((reinterpret_cast<uintptr_t>(xr) & 15) / sizeof(raw));
     return (a.V + lead + 32 * VEC - 1) / (32 * VEC);
   };
+  // a thread reads four units at once, or one where that leaves no thread idle
+  const int wide = U >= 256 * share ? 4 : 1, step = wide * 32 * share;
+  auto some_units = [&](const uint32_t* ur, int u, int end) {
+    if (u >= end) return make_uint4(0, 0, 0, 0);
+    return wide == 4 ? *reinterpret_cast<const uint4*>(ur + u) : make_uint4(ur[u], 0, 0, 0);
+  };
   auto unit_key = [&](int k, uint32_t fk) { return fixed_key(shift[k] + fixed_of(order_key_float(fk))); };
   // every unit whose key may reach `least` (0: all); finished beams are a unit of their own
   auto each_unit = [&](unsigned long long least, auto&& f) {
@@ -383,11 +394,25 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const BeamArgs a) {
         }
         const uint32_t* ur = units + (int64_t)k * U;
         const int end = row_units(k);
-        for (int u = from; u < end; u += 32 * share) {
-          const uint32_t fk = ur[u];
-          if (fk >= low) {
+        auto take = [&](uint32_t fk, int u) {
+          if (fk >= low && u < end) {
             const unsigned long long e = unit_key(k, fk);
             if (e >= least) f(e, ~(uint32_t)(k * U + u));
+          }
+        };
+        for (int u0 = wide * from; u0 < end; u0 += kAhead * step) {
+          uint4 v[kAhead];
+#pragma unroll
+          for (int i2 = 0; i2 < kAhead; ++i2) v[i2] = some_units(ur, u0 + i2 * step, end);
+#pragma unroll
+          for (int i2 = 0; i2 < kAhead; ++i2) {
+            const int u = u0 + i2 * step;
+            if (max(max(v[i2].x, v[i2].y), max(v[i2].z, v[i2].w)) >= low) {
+              take(v[i2].x, u);
+              take(v[i2].y, u + 1);
+              take(v[i2].z, u + 2);
+              take(v[i2].w, u + 3);
+            }
           }
         }
       }
@@ -404,18 +429,31 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const BeamArgs a) {
       const uint32_t* ur = units + (int64_t)k * U;
       const int end = row_units(k);
 #pragma unroll 4
-      for (int u = from; u < end; u += 32 * share) fk = max(fk, ur[u]);
+      for (int u = wide * from; u < end; u += step) {
+        const uint4 v = some_units(ur, u, end);
+        fk = max(fk, max(max(v.x, u + 1 < end ? v.y : 0u), max(u + 2 < end ? v.z : 0u, u + 3 < end ? v.w : 0u)));
+      }
       if (fk > kNegInfKey) mine = max(mine, unit_key(k, fk));
     }
+    // groups of lanes, at least 2 n of them; few beams leave warps without a
+    // row, whose maxima are 0
     const int used = min(a.K * share, kMW) * 32;
-    best[tid] = mine;
+    int group = 1;
+    while (group < 32 && used / (2 * group) >= max(2 * n, 32)) {
+      const unsigned long long o = __shfl_xor_sync(0xffffffffu, mine, group);
+      mine = o > mine ? o : mine;
+      group *= 2;
+    }
+    const int groups = used / group;
+    if (tid % group == 0) best[tid / group] = mine;
     __syncthreads();
-    if (tid < used && mine) {
+    if (tid < groups && best[tid]) {
+      mine = best[tid];
       int rank = 0;
 #pragma unroll 4
-      for (int i = 0; i < used; i += 2) {
+      for (int i = 0; i < groups; i += 2) {
         const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&best[i]);
-        rank += (o.x > mine || (o.x == mine && i < tid)) + (o.y > mine || (o.y == mine && i + 1 < tid));
+        rank += before(o.x, tid, mine, i) + before(o.y, tid, mine, i + 1);
       }
       if (rank == n - 1) tau_s = mine;
     }
@@ -432,7 +470,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const BeamArgs a) {
       const uint32_t p = pool.place[i];
       int rank = 0;
 #pragma unroll 4
-      for (int j = 0; j < listed; ++j) rank += (pool.key[j] > k || (pool.key[j] == k && pool.place[j] > p)) ? 1 : 0;
+      for (int j = 0; j < listed; ++j) rank += before(pool.key[j], pool.place[j], k, p);
       if (rank < n) {
         ukey[rank] = k;
         uplace[rank] = p;
@@ -496,7 +534,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const BeamArgs a) {
       const uint32_t p = pool.place[i];
       int rank = 0;
 #pragma unroll 4
-      for (int j = 0; j < found; ++j) rank += (pool.key[j] > k || (pool.key[j] == k && pool.place[j] > p)) ? 1 : 0;
+      for (int j = 0; j < found; ++j) rank += before(pool.key[j], pool.place[j], k, p);
       if (rank < n) put(rank, k, p);
     }
     for (int r = found + tid; r < n; r += kMergeThreads) put(r, 0ull, 0u);

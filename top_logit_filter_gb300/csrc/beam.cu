@@ -23,7 +23,6 @@ namespace {
 
 constexpr int kMergeThreads = 512;
 constexpr int kMW = kMergeThreads / 32;
-constexpr int kAhead = 4;  // 16-byte reads of unit maxima on their way at once
 constexpr int kPool = 1024;  // units, then elements, of a request that may be chosen
 constexpr float kLog2eHi = 1.44268798828125f;  // log2 e to 16 bits
 constexpr float kLog2eLo = 7.0526077e-06f;     // the rest
@@ -183,13 +182,14 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_scan(const BeamArgs a) {
   int e0 = c_first * CHUNK + warp * PIECE - lead;
   const int e_end = min((c_first + a.chunks) * CHUNK - lead, a.V);
   uint32_t* units = a.units + (int64_t)row * a.unit_count + (c_first * kBW + warp) * NV;
+  uint32_t* pieces = a.pieces + (int64_t)row * (a.unit_count / NV) + c_first * kBW + warp;
 
   uint4 q[NV], nx[NV];
   load_vectors<DT, NV>(q, xr, e0, a.V);
   float c = -INFINITY;            // the warp's shift: an integer, or -inf before its first finite element
   unsigned long long acc = 0ull;  // this thread's sum in units of 2^(c - 38)
 #pragma unroll 1
-  for (; e0 < e_end; e0 += CHUNK, units += kBW * NV) {
+  for (; e0 < e_end; e0 += CHUNK, units += kBW * NV, pieces += kBW) {
     if (e0 + CHUNK < e_end) load_vectors<DT, NV>(nx, xr, e0 + CHUNK, a.V);
     uint32_t key = 0;  // of unit `lane`, for lane < NV
     uint32_t kmax = 0;
@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_scan(const BeamArgs a) {
       kmax = max(kmax, k);
     }
     if (lane < NV) units[lane] = key;
+    if (NV > 1 && lane == 0) *pieces = kmax;
     const float m = order_key_float(kmax);
     if (m > -INFINITY) {
       const float mc = fminf(fmaxf(m, -kFar), kFar) * (kLog2eHi + kLog2eLo);
@@ -270,6 +271,26 @@ __device__ __forceinline__ void pool_add(Pool& p, unsigned long long key, uint32
     p.place[at] = place;
   }
 }
+// f(item, rank) for m <= kMergeThreads items by one thread of each; the pairs
+// before an item are counted by several threads where there are enough.
+// Warps whose threads hold no item skip it.
+template <class F>
+__device__ __forceinline__ void rank_items(const unsigned long long* key, const uint32_t* place, int m, F&& f) {
+  int parts = 32;
+  while (parts > 1 && kMergeThreads / parts < m) parts /= 2;
+  for (int i0 = 0; i0 < m; i0 += kMergeThreads / parts) {
+    const int i = i0 + (int)threadIdx.x / parts, part = threadIdx.x % parts;
+    const unsigned long long k = i < m ? key[i] : 0ull;
+    const uint32_t p = i < m ? place[i] : 0u;
+    int rank = 0;
+    if (i < m) {
+#pragma unroll 4
+      for (int j = part; j < m; j += parts) rank += before(key[j], place[j], k, p);
+    }
+    for (int o = parts / 2; o > 0; o /= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    if (i < m && part == 0) f(i, rank);
+  }
+}
 // The best pair below (lk, lp) that `each` hands out, over the CTA.
 template <class F>
 __device__ __forceinline__ void next_best(F&& each, unsigned long long& lk, uint32_t& lp, unsigned long long* wk,
@@ -312,7 +333,8 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const BeamArgs a) {
   using raw = typename DType<DT>::raw;
   constexpr int VEC = 16 / (int)sizeof(raw);
   __shared__ Pool pool;
-  __shared__ __align__(16) unsigned long long best[kMergeThreads];
+  __shared__ unsigned long long best[kMergeThreads];
+  __shared__ uint32_t bplace[kMergeThreads];
   __shared__ unsigned long long ukey[TOPKP_MAX_CANDIDATES];  // the chosen units, in order
   __shared__ uint32_t uplace[TOPKP_MAX_CANDIDATES];
   __shared__ long long shift[TOPKP_MAX_BEAMS];  // score - normaliser; the score itself where finished
@@ -366,16 +388,19 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const BeamArgs a) {
   // ---- the n best units.  Place of unit u of beam k: ~(k U + u) ----
   const uint32_t* units = a.units + b * a.K * (int64_t)U;
   const int share = max(1, kMW / a.K);  // warps to a beam
-  auto row_units = [&](int k) {         // units of the beam's row that hold an element
+  // pieces of nv units, and how many of them hold an element of the beam's row
+  const int P = U / a.nv;
+  const uint32_t* pieces = a.pieces + b * a.K * (int64_t)P;
+  auto row_pieces = [&](int k) {
     const raw* xr = reinterpret_cast<const raw*>(a.x) + (b * a.K + k) * a.ldx;
     const int lead = (int)((reinterpret_cast<uintptr_t>(xr) & 15) / sizeof(raw));
-    return (a.V + lead + 32 * VEC - 1) / (32 * VEC);
+    return (a.V + lead + a.nv * 32 * VEC - 1) / (a.nv * 32 * VEC);
   };
-  // a thread reads four units at once, or one where that leaves no thread idle
-  const int wide = U >= 256 * share ? 4 : 1, step = wide * 32 * share;
-  auto some_units = [&](const uint32_t* ur, int u, int end) {
-    if (u >= end) return make_uint4(0, 0, 0, 0);
-    return wide == 4 ? *reinterpret_cast<const uint4*>(ur + u) : make_uint4(ur[u], 0, 0, 0);
+  // a thread reads four pieces at once, or one where that leaves no thread idle
+  const int wide = P >= 256 * share ? 4 : 1, step = wide * 32 * share;
+  auto some_pieces = [&](const uint32_t* pr, int i, int end) {
+    if (i >= end) return make_uint4(0, 0, 0, 0);
+    return wide == 4 ? *reinterpret_cast<const uint4*>(pr + i) : make_uint4(pr[i], 0, 0, 0);
   };
   auto unit_key = [&](int k, uint32_t fk) { return fixed_key(shift[k] + fixed_of(order_key_float(fk))); };
   // every unit whose key may reach `least` (0: all); finished beams are a unit of their own
@@ -393,27 +418,30 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const BeamArgs a) {
           if (x > -0.999f * kFar) low = float_order_key(x - fabsf(x) * 1e-6f - 1e-6f);
         }
         const uint32_t* ur = units + (int64_t)k * U;
-        const int end = row_units(k);
+        const uint32_t* pr = pieces + (int64_t)k * P;
+        const int end = row_pieces(k);
         auto take = [&](uint32_t fk, int u) {
-          if (fk >= low && u < end) {
+          if (fk >= low) {
             const unsigned long long e = unit_key(k, fk);
             if (e >= least) f(e, ~(uint32_t)(k * U + u));
           }
         };
-        for (int u0 = wide * from; u0 < end; u0 += kAhead * step) {
-          uint4 v[kAhead];
-#pragma unroll
-          for (int i2 = 0; i2 < kAhead; ++i2) v[i2] = some_units(ur, u0 + i2 * step, end);
-#pragma unroll
-          for (int i2 = 0; i2 < kAhead; ++i2) {
-            const int u = u0 + i2 * step;
-            if (max(max(v[i2].x, v[i2].y), max(v[i2].z, v[i2].w)) >= low) {
-              take(v[i2].x, u);
-              take(v[i2].y, u + 1);
-              take(v[i2].z, u + 2);
-              take(v[i2].w, u + 3);
-            }
-          }
+        auto open = [&](uint32_t fk, int i) {
+          if (fk < low || i >= end) return;
+          if (a.nv == 1) return take(fk, i);
+          const uint4 v = *reinterpret_cast<const uint4*>(ur + 4 * i);
+          take(v.x, 4 * i);
+          take(v.y, 4 * i + 1);
+          take(v.z, 4 * i + 2);
+          take(v.w, 4 * i + 3);
+        };
+        for (int i0 = wide * from; i0 < end; i0 += step) {
+          const uint4 v = some_pieces(pr, i0, end);
+          if (max(max(v.x, v.y), max(v.z, v.w)) < low) continue;
+          open(v.x, i0);
+          open(v.y, i0 + 1);
+          open(v.z, i0 + 2);
+          open(v.w, i0 + 3);
         }
       }
     }
@@ -426,12 +454,12 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const BeamArgs a) {
       if (state[k] == 2 && from == 0) mine = max(mine, fixed_key(shift[k]));
       if (state[k] != 1) continue;
       uint32_t fk = 0;
-      const uint32_t* ur = units + (int64_t)k * U;
-      const int end = row_units(k);
+      const uint32_t* pr = pieces + (int64_t)k * P;
+      const int end = row_pieces(k);
 #pragma unroll 4
-      for (int u = wide * from; u < end; u += step) {
-        const uint4 v = some_units(ur, u, end);
-        fk = max(fk, max(max(v.x, u + 1 < end ? v.y : 0u), max(u + 2 < end ? v.z : 0u, u + 3 < end ? v.w : 0u)));
+      for (int i2 = wide * from; i2 < end; i2 += step) {
+        const uint4 v = some_pieces(pr, i2, end);
+        fk = max(fk, max(max(v.x, i2 + 1 < end ? v.y : 0u), max(i2 + 2 < end ? v.z : 0u, i2 + 3 < end ? v.w : 0u)));
       }
       if (fk > kNegInfKey) mine = max(mine, unit_key(k, fk));
     }
@@ -445,18 +473,14 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const BeamArgs a) {
       group *= 2;
     }
     const int groups = used / group;
-    if (tid % group == 0) best[tid / group] = mine;
-    __syncthreads();
-    if (tid < groups && best[tid]) {
-      mine = best[tid];
-      int rank = 0;
-#pragma unroll 4
-      for (int i = 0; i < groups; i += 2) {
-        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&best[i]);
-        rank += before(o.x, tid, mine, i) + before(o.y, tid, mine, i + 1);
-      }
-      if (rank == n - 1) tau_s = mine;
+    if (tid % group == 0 && tid < used) {
+      best[tid / group] = mine;
+      bplace[tid / group] = (uint32_t)tid;
     }
+    __syncthreads();
+    rank_items(best, bplace, groups, [&](int i, int rank) {
+      if (rank == n - 1 && best[i]) tau_s = best[i];
+    });
     __syncthreads();
   }
   unsigned long long least = tau_s;
@@ -465,17 +489,12 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const BeamArgs a) {
   const int listed = pool.count;
   int chosen = min(listed, n);
   if (listed <= kPool) {
-    for (int i = tid; i < listed; i += kMergeThreads) {
-      const unsigned long long k = pool.key[i];
-      const uint32_t p = pool.place[i];
-      int rank = 0;
-#pragma unroll 4
-      for (int j = 0; j < listed; ++j) rank += before(pool.key[j], pool.place[j], k, p);
+    rank_items(pool.key, pool.place, listed, [&](int i, int rank) {
       if (rank < n) {
-        ukey[rank] = k;
-        uplace[rank] = p;
+        ukey[rank] = pool.key[i];
+        uplace[rank] = pool.place[i];
       }
-    }
+    });
   } else {  // many equal maxima: the next unit in order, n times
     unsigned long long lk = ~0ull;
     uint32_t lp = ~0u;
@@ -529,14 +548,9 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const BeamArgs a) {
     ot[r] = k ? (int32_t)(p % (uint32_t)a.V) : -1;
   };
   if (found <= kPool) {
-    for (int i = tid; i < found; i += kMergeThreads) {
-      const unsigned long long k = pool.key[i];
-      const uint32_t p = pool.place[i];
-      int rank = 0;
-#pragma unroll 4
-      for (int j = 0; j < found; ++j) rank += before(pool.key[j], pool.place[j], k, p);
-      if (rank < n) put(rank, k, p);
-    }
+    rank_items(pool.key, pool.place, found, [&](int i, int rank) {
+      if (rank < n) put(rank, pool.key[i], pool.place[i]);
+    });
     for (int r = found + tid; r < n; r += kMergeThreads) put(r, 0ull, 0u);
     return;
   }
@@ -588,7 +602,8 @@ BeamPlan plan_beam(int64_t rows, int64_t V, int esize, int num_sms) {
   p.slices = (int)((all + p.chunks - 1) / p.chunks);
   p.stat_bytes = ((size_t)rows * p.slices * sizeof(longlong2) + 255) / 256 * 256;
   p.unit_count = p.slices * p.chunks * kBW * p.nv;
-  p.unit_bytes = (size_t)rows * p.unit_count * sizeof(uint32_t);
+  p.unit_bytes = ((size_t)rows * p.unit_count * sizeof(uint32_t) + 255) / 256 * 256;
+  p.piece_bytes = p.nv > 1 ? p.unit_bytes / p.nv + 256 : 0;
   return p;
 }
 

@@ -27,6 +27,7 @@ struct BeamArgs {
   // workspace
   longlong2* stat;             // [rows][slices]: (c, sum of 2^(x log2 e - c) in 2^-38 units); sum 0 if nothing is finite
   uint32_t* units;             // [rows][unit_count]: order key of the largest logit of each 512 bytes
+  uint32_t* pieces;            // [rows][unit_count / nv]: of each nv units; the units themselves if nv is 1
   int32_t unit_count;
   float* out_score;
   int32_t* out_parent;
@@ -36,7 +37,7 @@ struct BeamArgs {
 struct BeamPlan {
   int nv, chunks, slices;
   int unit_count;
-  size_t stat_bytes, unit_bytes;
+  size_t stat_bytes, unit_bytes, piece_bytes;
 };
 BeamPlan plan_beam(int64_t rows, int64_t V, int esize, int num_sms);
 cudaError_t launch_beam(topkp_dtype dt, const BeamArgs& a, cudaStream_t s);

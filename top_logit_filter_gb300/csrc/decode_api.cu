@@ -57,7 +57,7 @@ size_t topkp_beam_select_workspace_size(int64_t B, int64_t K, int64_t V, topkp_d
       !row_type(dtype))
     return 0;
   const BeamPlan p = plan_beam(B * K, V, esize(dtype), kPlanSms);
-  return p.stat_bytes + p.unit_bytes;
+  return p.stat_bytes + p.unit_bytes + p.piece_bytes;
 }
 
 topkp_status topkp_beam_select(const void* logits, int64_t B, int64_t K, int64_t V, int64_t ld_logits,
@@ -86,7 +86,7 @@ topkp_status topkp_beam_select(const void* logits, int64_t B, int64_t K, int64_t
   if (B > INT_MAX / TOPKP_MAX_BEAMS) return fail(TOPKP_ERR_PARAM_INVALID, "%s: B=%lld is too large", fn, (long long)B);
   const BeamPlan p = plan_beam(B * K, V, es, kPlanSms);
   if (B * K * p.slices > INT_MAX) return fail(TOPKP_ERR_PARAM_INVALID, "%s: B * K * V is too large", fn);
-  const size_t need = p.stat_bytes + p.unit_bytes;
+  const size_t need = p.stat_bytes + p.unit_bytes + p.piece_bytes;
   if ((uintptr_t)workspace % 256 || workspace_bytes < need)
     return fail(TOPKP_ERR_PARAM_INVALID, "%s: the workspace needs %zu bytes, 256-byte aligned", fn, need);
   const Range ins[3] = {{logits, (size_t)((B * K - 1) * ld_logits + V) * es}, {scores, (size_t)(B * K) * 4}, {finished, (size_t)(B * K)}};
@@ -114,6 +114,7 @@ topkp_status topkp_beam_select(const void* logits, int64_t B, int64_t K, int64_t
   a.slices = p.slices;
   a.stat = reinterpret_cast<longlong2*>(workspace);
   a.units = reinterpret_cast<uint32_t*>((char*)workspace + p.stat_bytes);
+  a.pieces = p.nv > 1 ? a.units + p.unit_bytes / sizeof(uint32_t) : a.units;
   a.unit_count = p.unit_count;
   a.out_score = out_score;
   a.out_parent = out_parent;

@@ -76,133 +76,213 @@ __device__ __forceinline__ typename DType<DT>::raw from_float(float f) {
   return (typename DType<DT>::raw)__bfloat16_as_ushort(__float2bfloat16_rn(f));
 }
 
-// One group of lanes moves one row; a lane moves elements lane * VEC + i *
-// lanes * VEC of it.
-template <int DT, int VEC, bool QUANT>
+// A thread's place is fixed for its life: a side (keys or values), a head and
+// a lane of the row, and a token of each group of `tokens` tokens that the
+// CTA takes; it moves kTokens tokens at once, so that as many reads are on
+// their way.  Only the slot is divided, by a multiplication.
+struct Place {
+  int side, head, lane, token;
+  bool on;
+};
+__device__ __forceinline__ Place place_of(const CacheRowsArgs& a, int lanes) {
+  Place p;
+  const int per_token = a.sides * a.H * lanes;           // threads of a token
+  const int base = (int)blockIdx.y * kCacheThreads;      // first of them in this CTA, where a token has several CTAs
+  const int t = base + (int)threadIdx.x;
+  p.token = per_token < kCacheThreads ? t / per_token : 0;
+  const int c = t - p.token * per_token;
+  p.on = c < per_token && p.token < a.tokens;
+  p.lane = c & (lanes - 1);
+  const int row = c / lanes;
+  p.side = row / a.H;
+  p.head = row - p.side * a.H;
+  if (!p.on) p.side = p.head = 0;
+  return p;
+}
+struct Spot {
+  int64_t page;
+  int at;
+  bool in;
+};
+__device__ __forceinline__ Spot spot_of(const CacheRowsArgs& a, int64_t slot) {
+  Spot s;
+  s.in = slot >= 0 && slot < a.slots_end;
+  if (!s.in) slot = 0;
+  // slots below 2^31 go through a 32-bit reciprocal (exact there)
+  s.page = a.page_mul ? (int64_t)(__umulhi((uint32_t)slot, a.page_mul) >> a.page_shift) : slot / a.page_size;
+  s.at = (int)(slot - s.page * a.page_size);
+  return s;
+}
+
+template <int DT, int VEC, bool QUANT, int TOK>
 __global__ void __launch_bounds__(kCacheThreads) write_kernel(const __grid_constant__ CacheRowsArgs a) {
   using D_ = DType<DT>;
   using raw = typename D_::raw;
-  const int lanes = row_lanes(a.D, VEC);
-  const int64_t rows = a.N * a.H * a.sides;
-  const int64_t r = ((int64_t)blockIdx.x * kCacheThreads + threadIdx.x) / lanes;
-  const int lane = threadIdx.x & (lanes - 1);
-  const unsigned mask = lanes == 32 ? 0xffffffffu : ((1u << lanes) - 1u) << (threadIdx.x & 31 & ~(lanes - 1));
-  if (r >= rows) return;
-  const int64_t th = r / a.sides;
-  const int side = (int)(r - th * a.sides);
-  const int64_t tok = th / a.H;
-  const int h = (int)(th - tok * a.H);
-  const int64_t slot = a.slots[tok];
-  if (slot < 0 || slot >= a.slots_end) return;
-  const int64_t page = slot / a.page_size;
-  const int64_t at = slot - page * a.page_size;
-  const raw* x = reinterpret_cast<const raw*>(a.in[side]) + tok * a.token_stride[side] + h * a.head_stride[side];
-  const topkp_cache& c = a.cache[side];
-  const int64_t off = page * c.page_stride + at * c.token_stride + h * c.head_stride;
-  if (!QUANT) {
-    raw* o = reinterpret_cast<raw*>(c.data) + off;
-    for (int d = lane * VEC; d < a.D; d += lanes * VEC) store_rows<DT, VEC>(o + d, load_rows<DT, VEC>(x + d));
-    return;
-  }
-  uint32_t amax = 0;
   constexpr int kKeep = VEC == 8 ? 1 : TOPKP_MAX_HEAD_DIM / 32;
-  Rows<DT, VEC> keep[kKeep];
-#pragma unroll
-  for (int i = 0; i < kKeep; ++i) {
-    const int d = (i * lanes + lane) * VEC;
-    if (d < a.D) {
-      keep[i] = load_rows<DT, VEC>(x + d);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const uint32_t m = __float_as_uint(D_::to_float(keep[i].v[j])) & 0x7fffffffu;
-        if (m < 0x7f800000u) amax = max(amax, m);
-      }
-    }
-  }
-  for (int o = lanes / 2; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(mask, amax, o));
-  // below the normal range (and for zeros) e stays at its lowest
-  const int e = max((int)(amax >> 23) - 127 - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0), -126);
-  const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-  uint8_t* o = reinterpret_cast<uint8_t*>(c.data) + off;
-#pragma unroll
-  for (int i = 0; i < kKeep; ++i) {
-    const int d = (i * lanes + lane) * VEC;
-    if (d < a.D) {
-      if (VEC == 1) {
-        o[d] = (uint8_t)to_e4m3x2(D_::to_float(keep[i].v[0]) * inv, 0.0f);
-      } else {
-        uint32_t w[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          w[j] = to_e4m3x2(D_::to_float(keep[i].v[4 * j]) * inv, D_::to_float(keep[i].v[4 * j + 1]) * inv) |
-                 (to_e4m3x2(D_::to_float(keep[i].v[4 * j + 2]) * inv, D_::to_float(keep[i].v[4 * j + 3]) * inv) << 16);
-        *reinterpret_cast<uint2*>(o + d) = make_uint2(w[0], w[1]);
-      }
-    }
-  }
-  if (lane == 0) c.exponents[page * c.exp_page_stride + at * c.exp_token_stride + h * c.exp_head_stride] = (uint8_t)(e + 127);
-}
-
-template <int DT, int VEC, bool QUANT>
-__global__ void __launch_bounds__(kCacheThreads) read_kernel(const __grid_constant__ CacheRowsArgs a) {
-  using raw = typename DType<DT>::raw;
   const int lanes = row_lanes(a.D, VEC);
-  const int64_t rows = a.N * a.H * a.sides;
-  const int64_t r = ((int64_t)blockIdx.x * kCacheThreads + threadIdx.x) / lanes;
-  const int lane = threadIdx.x & (lanes - 1);
-  if (r >= rows) return;
-  const int64_t th = r / a.sides;
-  const int side = (int)(r - th * a.sides);
-  const int64_t tok = th / a.H;
-  const int h = (int)(th - tok * a.H);
-  raw* o = reinterpret_cast<raw*>(a.out[side]) + tok * a.token_stride[side] + h * a.head_stride[side];
-  const int64_t slot = a.slots[tok];
-  const bool in = slot >= 0 && slot < a.slots_end;
-  const int64_t page = in ? slot / a.page_size : 0;
-  const int64_t at = in ? slot - page * a.page_size : 0;
-  const topkp_cache& c = a.cache[side];
-  const int64_t off = page * c.page_stride + at * c.token_stride + h * c.head_stride;
-  float scale = 0.0f;
-  if (QUANT && in) {
-    const uint32_t e = c.exponents[page * c.exp_page_stride + at * c.exp_token_stride + h * c.exp_head_stride];
-    scale = __uint_as_float(e ? e << 23 : 0x400000u);
+  const Place p = place_of(a, lanes);
+  const unsigned mask = lanes == 32 ? 0xffffffffu : ((1u << lanes) - 1u) << (threadIdx.x & 31 & ~(lanes - 1));
+  const topkp_cache& c = a.cache[p.side];
+  const raw* x = reinterpret_cast<const raw*>(a.in[p.side]) + p.head * a.head_stride[p.side];
+  const int64_t tok0 = (int64_t)blockIdx.x * (a.tokens * TOK) + p.token;
+
+  Spot spot[TOK];
+  Rows<DT, VEC> keep[TOK][kKeep];
+#pragma unroll
+  for (int u = 0; u < TOK; ++u) {
+    const int64_t tok = tok0 + u * a.tokens;
+    spot[u] = spot_of(a, p.on && tok < a.N ? a.slots[tok] : -1);
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) {
+      const int d = (i * lanes + p.lane) * VEC;
+      if (spot[u].in && d < a.D) keep[u][i] = load_rows<DT, VEC>(x + tok * a.token_stride[p.side] + d);
+    }
   }
-  for (int d = lane * VEC; d < a.D; d += lanes * VEC) {
-    Rows<DT, VEC> v;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) v.v[j] = 0;
-    if (in) {
-      if (!QUANT) {
-        v = load_rows<DT, VEC>(reinterpret_cast<const raw*>(c.data) + off + d);
-      } else if (VEC == 1) {
-        v.v[0] = from_float<DT>(from_e4m3x2(reinterpret_cast<const uint8_t*>(c.data)[off + d]).x * scale);
-      } else {
-        const uint2 w = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(c.data) + off + d);
-        const uint32_t two[4] = {w.x & 0xffffu, w.x >> 16, w.y & 0xffffu, w.y >> 16};
+  for (int u = 0; u < TOK; ++u) {
+    if (!spot[u].in) continue;  // all lanes of the row alike
+    const int64_t off = spot[u].page * c.page_stride + spot[u].at * c.token_stride + p.head * c.head_stride;
+    if (!QUANT) {
+      raw* o = reinterpret_cast<raw*>(c.data) + off;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f = from_e4m3x2(two[j]);
-          v.v[2 * j % VEC] = from_float<DT>(f.x * scale);
-          v.v[(2 * j + 1) % VEC] = from_float<DT>(f.y * scale);
+      for (int i = 0; i < kKeep; ++i) {
+        const int d = (i * lanes + p.lane) * VEC;
+        if (d < a.D) store_rows<DT, VEC>(o + d, keep[u][i]);
+      }
+      continue;
+    }
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i)
+      if ((i * lanes + p.lane) * VEC < a.D) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const uint32_t m = __float_as_uint(D_::to_float(keep[u][i].v[j])) & 0x7fffffffu;
+          if (m < 0x7f800000u) amax = max(amax, m);
+        }
+      }
+    for (int o = lanes / 2; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(mask, amax, o));
+    // below the normal range (and for zeros) e stays at its lowest
+    const int e = max((int)(amax >> 23) - 127 - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0), -126);
+    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+    uint8_t* o = reinterpret_cast<uint8_t*>(c.data) + off;
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) {
+      const int d = (i * lanes + p.lane) * VEC;
+      if (d < a.D) {
+        const Rows<DT, VEC>& r = keep[u][i];
+        if (VEC == 1) {
+          o[d] = (uint8_t)to_e4m3x2(D_::to_float(r.v[0]) * inv, 0.0f);
+        } else {
+          uint32_t w[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            w[j] = to_e4m3x2(D_::to_float(r.v[4 * j % VEC]) * inv, D_::to_float(r.v[(4 * j + 1) % VEC]) * inv) |
+                   (to_e4m3x2(D_::to_float(r.v[(4 * j + 2) % VEC]) * inv, D_::to_float(r.v[(4 * j + 3) % VEC]) * inv) << 16);
+          *reinterpret_cast<uint2*>(o + d) = make_uint2(w[0], w[1]);
         }
       }
     }
-    store_rows<DT, VEC>(o + d, v);
+    if (p.lane == 0)
+      c.exponents[spot[u].page * c.exp_page_stride + spot[u].at * c.exp_token_stride + p.head * c.exp_head_stride] =
+          (uint8_t)(e + 127);
+  }
+}
+
+template <int DT, int VEC, bool QUANT, int TOK>
+__global__ void __launch_bounds__(kCacheThreads) read_kernel(const __grid_constant__ CacheRowsArgs a) {
+  using raw = typename DType<DT>::raw;
+  constexpr int kKeep = VEC == 8 ? 1 : TOPKP_MAX_HEAD_DIM / 32;
+  const int lanes = row_lanes(a.D, VEC);
+  const Place p = place_of(a, lanes);
+  if (!p.on) return;
+  const topkp_cache& c = a.cache[p.side];
+  raw* out = reinterpret_cast<raw*>(a.out[p.side]) + p.head * a.head_stride[p.side];
+  const int64_t tok0 = (int64_t)blockIdx.x * (a.tokens * TOK) + p.token;
+
+  Spot spot[TOK];
+  Rows<DT, VEC> v[TOK][kKeep];
+  uint2 w[TOK][kKeep];
+  uint32_t e[TOK];
+#pragma unroll
+  for (int u = 0; u < TOK; ++u) {
+    const int64_t tok = tok0 + u * a.tokens;
+    spot[u] = spot_of(a, tok < a.N ? a.slots[tok] : -1);
+    const int64_t off = spot[u].page * c.page_stride + spot[u].at * c.token_stride + p.head * c.head_stride;
+    e[u] = QUANT && spot[u].in
+               ? c.exponents[spot[u].page * c.exp_page_stride + spot[u].at * c.exp_token_stride + p.head * c.exp_head_stride]
+               : 0;
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) {
+      const int d = (i * lanes + p.lane) * VEC;
+      w[u][i] = make_uint2(0, 0);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[u][i].v[j] = 0;
+      if (!spot[u].in || d >= a.D) continue;
+      if (!QUANT) v[u][i] = load_rows<DT, VEC>(reinterpret_cast<const raw*>(c.data) + off + d);
+      else if (VEC == 1) w[u][i].x = reinterpret_cast<const uint8_t*>(c.data)[off + d];
+      else w[u][i] = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(c.data) + off + d);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < TOK; ++u) {
+    const int64_t tok = tok0 + u * a.tokens;
+    if (tok >= a.N) continue;
+    const float scale = spot[u].in ? __uint_as_float(e[u] ? e[u] << 23 : 0x400000u) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) {
+      const int d = (i * lanes + p.lane) * VEC;
+      if (d >= a.D) continue;
+      if (QUANT && VEC == 1) {
+        v[u][i].v[0] = from_float<DT>(from_e4m3x2(w[u][i].x).x * scale);
+      } else if (QUANT) {
+        const uint32_t two[4] = {w[u][i].x & 0xffffu, w[u][i].x >> 16, w[u][i].y & 0xffffu, w[u][i].y >> 16};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = from_e4m3x2(two[j]);
+          v[u][i].v[2 * j % VEC] = from_float<DT>(f.x * scale);
+          v[u][i].v[(2 * j + 1) % VEC] = from_float<DT>(f.y * scale);
+        }
+      }
+      store_rows<DT, VEC>(out + tok * a.token_stride[p.side] + d, v[u][i]);
+    }
   }
 }
 
 template <int DT>
-cudaError_t launch_dt(const CacheRowsArgs& a, bool write, cudaStream_t s) {
-  const int64_t threads = a.N * a.H * a.sides * row_lanes(a.D, a.vec);
-  const unsigned int grid = (unsigned int)((threads + kCacheThreads - 1) / kCacheThreads);
+cudaError_t launch_dt(const CacheRowsArgs& args, bool write, cudaStream_t s) {
+  CacheRowsArgs a = args;
+  const int lanes = row_lanes(a.D, a.vec);
+  const int64_t per_token = (int64_t)a.sides * a.H * lanes;
+  a.tokens = per_token < kCacheThreads ? (int)(kCacheThreads / per_token) : 1;
+  // page = slot / page_size = (slot * mul) >> (32 + shift), exact below 2^31
+  a.page_mul = 0;
+  a.page_shift = 0;
+  if (a.slots_end <= (1LL << 31) && a.page_size > 1) {
+    int l = 1;
+    while ((1LL << l) < a.page_size) ++l;
+    a.page_mul = (uint32_t)(((1ull << (31 + l)) + a.page_size - 1) / a.page_size);
+    a.page_shift = l - 1;
+  }
   const bool q = a.cache[0].dtype == TOPKP_E4M3;
+  // four tokens a thread once that fills the device (16384 threads an SM's
+  // worth of reads on their way), one where there are few
+  const unsigned gy = (unsigned)((per_token + kCacheThreads - 1) / kCacheThreads);
+  const bool many = a.vec == 8 && a.N * per_token >= 4LL * 152 * 2048;
+  const int64_t per_cta = (int64_t)a.tokens * (many ? 4 : 1);
+  const dim3 grid((unsigned)((a.N + per_cta - 1) / per_cta), gy);
 #define TOPKP_CACHE_GO(KERNEL)                                             \
   if (a.vec == 8) {                                                        \
-    if (q) KERNEL<DT, 8, true><<<grid, kCacheThreads, 0, s>>>(a);          \
-    else KERNEL<DT, 8, false><<<grid, kCacheThreads, 0, s>>>(a);           \
+    if (many) {                                                            \
+      if (q) KERNEL<DT, 8, true, 4><<<grid, kCacheThreads, 0, s>>>(a);     \
+      else KERNEL<DT, 8, false, 4><<<grid, kCacheThreads, 0, s>>>(a);      \
+    } else {                                                               \
+      if (q) KERNEL<DT, 8, true, 1><<<grid, kCacheThreads, 0, s>>>(a);     \
+      else KERNEL<DT, 8, false, 1><<<grid, kCacheThreads, 0, s>>>(a);      \
+    }                                                                      \
   } else {                                                                 \
-    if (q) KERNEL<DT, 1, true><<<grid, kCacheThreads, 0, s>>>(a);          \
-    else KERNEL<DT, 1, false><<<grid, kCacheThreads, 0, s>>>(a);           \
+    if (q) KERNEL<DT, 1, true, 1><<<grid, kCacheThreads, 0, s>>>(a);       \
+    else KERNEL<DT, 1, false, 1><<<grid, kCacheThreads, 0, s>>>(a);        \
   }
   if (write) {
     TOPKP_CACHE_GO(write_kernel)

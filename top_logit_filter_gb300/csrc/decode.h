@@ -55,6 +55,7 @@ struct ReorderArgs {
   int32_t unit;   // bytes moved by a thread: 16, 4 or 1
   int32_t chunks; // grid.x
 };
+int32_t reorder_chunks(int64_t units, int64_t groups);
 cudaError_t launch_reorder(const ReorderArgs& a, cudaStream_t s);
 
 // ------------------------------------------------------------------ cache
@@ -68,6 +69,10 @@ struct CacheRowsArgs {
   int32_t H, D, page_size;
   int32_t sides;  // 1 (keys alone) or 2
   int32_t vec;    // elements moved by a thread: 8 or 1
+  // set by the launcher
+  int32_t tokens;       // tokens of a CTA at a time
+  uint32_t page_mul;    // reciprocal of page_size, 0: divide
+  int32_t page_shift;
 };
 cudaError_t launch_cache_write(topkp_dtype dt, const CacheRowsArgs& a, cudaStream_t s);
 cudaError_t launch_cache_read(topkp_dtype dt, const CacheRowsArgs& a, cudaStream_t s);

@@ -196,8 +196,7 @@ topkp_status topkp_beam_reorder(const topkp_state* states, int64_t count, int64_
         widest = bytes > widest ? bytes : widest;
       }
       if (a.count == kReorderStates || (i == count && a.count)) {
-        const int64_t chunks = (widest / unit + 255) / 256;
-        a.chunks = (int32_t)(chunks < 1 ? 1 : chunks > 4096 ? 4096 : chunks);
+        a.chunks = reorder_chunks(widest / unit, B * a.count);
         const cudaError_t e = launch_reorder(a, (cudaStream_t)stream);
         if (e != cudaSuccess) return launched(fn, e, 0);
         ++launches;
@@ -253,7 +252,7 @@ topkp_status cache_shapes(const char* fn, int64_t N, int64_t H, int64_t D, int64
     return fail(TOPKP_ERR_PARAM_INVALID, "%s: head dimension %lld (1 to %d)", fn, (long long)D, TOPKP_MAX_HEAD_DIM);
   if (pages < 1 || page_size < 1 || page_size > INT_MAX || pages > INT_MAX)
     return fail(TOPKP_ERR_PARAM_INVALID, "%s: pages=%lld page_size=%lld", fn, (long long)pages, (long long)page_size);
-  if (N > 0 && H > 0 && N > (1LL << 36) / H) return fail(TOPKP_ERR_PARAM_INVALID, "%s: N * H is too large", fn);
+  if (H > 65535LL * 4 || N > INT_MAX) return fail(TOPKP_ERR_PARAM_INVALID, "%s: N * H is too large", fn);
   return TOPKP_SUCCESS;
 }
 

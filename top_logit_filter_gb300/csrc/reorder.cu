@@ -13,15 +13,6 @@ namespace {
 
 constexpr int kReorderThreads = 256;
 
-template <typename U>
-struct Zero {
-  __device__ static U get() { return U(0); }
-};
-template <>
-struct Zero<uint4> {
-  __device__ static uint4 get() { return make_uint4(0, 0, 0, 0); }
-};
-
 template <typename U, int KMAX>
 __global__ void __launch_bounds__(kReorderThreads) reorder_kernel(const __grid_constant__ ReorderArgs a) {
   __shared__ unsigned long long kids[TOPKP_MAX_BEAMS];  // rows that become row p
@@ -52,26 +43,38 @@ __global__ void __launch_bounds__(kReorderThreads) reorder_kernel(const __grid_c
   const long long total = width * st.blocks;
   const char* src = reinterpret_cast<const char*>(st.src) + b * K * st.src_row_stride;
   char* dst = reinterpret_cast<char*>(st.dst) + b * K * st.dst_row_stride;
-  for (long long i = (long long)blockIdx.x * kReorderThreads + tid; i < total;
-       i += (long long)gridDim.x * kReorderThreads) {
-    const long long blk = st.blocks == 1 ? 0 : i / width;
-    const long long col = i - blk * width;
-    const char* s = src + blk * st.src_block_stride + col * (long long)sizeof(U);
-    char* d = dst + blk * st.dst_block_stride + col * (long long)sizeof(U);
-    U r[KMAX];
+  constexpr int COLS = KMAX <= 4 ? 4 : KMAX <= 8 ? 2 : 1;
+  const long long step = (long long)gridDim.x * kReorderThreads;
+  for (long long i0 = (long long)blockIdx.x * kReorderThreads + tid; i0 < total; i0 += step * COLS) {
+    U r[COLS][KMAX];
+    long long col[COLS], at[COLS];
 #pragma unroll
-    for (int p = 0; p < KMAX; ++p)
-      r[p] = p < K && col < live[p] ? *reinterpret_cast<const U*>(s + p * st.src_row_stride) : Zero<U>::get();
+    for (int c = 0; c < COLS; ++c) {
+      const long long i = i0 + c * step;
+      long long blk = 0;
+      if (st.blocks > 1) blk = total <= 0x7fffffffll ? (long long)((uint32_t)i / (uint32_t)width) : i / width;
+      col[c] = i < total ? i - blk * width : width;  // a column past every live one moves nothing
+      at[c] = blk;
 #pragma unroll
-    for (int p = 0; p < KMAX; ++p)
-      if (p < K && col < live[p]) {
-        unsigned long long m = kids[p];
-        while (m) {
-          const int j = __ffsll((long long)m) - 1;
-          m &= m - 1;
-          *reinterpret_cast<U*>(d + j * st.dst_row_stride) = r[p];
+      for (int p = 0; p < KMAX; ++p)
+        if (p < K && col[c] < live[p])
+          r[c][p] = *reinterpret_cast<const U*>(src + p * st.src_row_stride + blk * st.src_block_stride +
+                                                col[c] * (long long)sizeof(U));
+    }
+#pragma unroll
+    for (int c = 0; c < COLS; ++c) {
+      char* d = dst + at[c] * st.dst_block_stride + col[c] * (long long)sizeof(U);
+#pragma unroll
+      for (int p = 0; p < KMAX; ++p)
+        if (p < K && col[c] < live[p]) {
+          unsigned long long m = kids[p];
+          while (m) {
+            const int j = __ffsll((long long)m) - 1;
+            m &= m - 1;
+            *reinterpret_cast<U*>(d + j * st.dst_row_stride) = r[c][p];
+          }
         }
-      }
+    }
   }
 }
 
@@ -86,6 +89,15 @@ cudaError_t launch_unit(const ReorderArgs& a, cudaStream_t s) {
 }
 
 }  // namespace
+
+// CTAs of one request and state: enough for eight an SM over all of them, so
+// that each has several rounds to spread the setup of its tables over.
+int32_t reorder_chunks(int64_t units, int64_t groups) {
+  const int64_t all = (units + kReorderThreads - 1) / kReorderThreads;
+  const int64_t want = (8LL * 152 + groups - 1) / groups;
+  const int64_t c = all < want ? all : want;
+  return (int32_t)(c < 1 ? 1 : c);
+}
 
 cudaError_t launch_reorder(const ReorderArgs& a, cudaStream_t s) {
   if (a.K > 32) {  // registers for 64 rows: columns of 4 bytes at most

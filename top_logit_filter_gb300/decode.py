@@ -18,17 +18,12 @@ from __future__ import annotations
 
 import ctypes
 
-from . import _lib
-
-
-def _base():
-    import top_logit_filter_gb300 as base  # the shared helpers; the package imports this module at its end
-    return base
+from . import _check, _dtype_code, _lib, _ptr, _torch, _vec  # defined before the package imports this module
 
 
 def _cuda(t, name, dim=None, dtype=None, device=None):
-    torch = _base()._torch()
-    if not torch.is_tensor(t) or not t.is_cuda or (dim is not None and t.dim() != dim):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or (dim is not None and t.dim() != dim):
         raise ValueError(f"{name} must be a {'' if dim is None else str(dim) + '-D '}CUDA tensor")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}")
@@ -37,8 +32,19 @@ def _cuda(t, name, dim=None, dtype=None, device=None):
     return t
 
 
+def _launch(device, call, *args):
+    """call(*args, the current stream of device) with that device current."""
+    torch = _torch()
+    index = device.index
+    if index == torch.cuda.current_device():  # the usual case, without the guard's cost
+        _check(call(*args, torch._C._cuda_getCurrentRawStream(index)))
+    else:
+        with torch.cuda.device(device):
+            _check(call(*args, torch._C._cuda_getCurrentRawStream(index)))
+
+
 def _workspace(workspace, need, device):
-    torch = _base()._torch()
+    torch = _torch()
     if workspace is None:
         return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
     if workspace.dtype != torch.uint8 or workspace.device != device or workspace.numel() < need:
@@ -56,10 +62,9 @@ def beam_select(logits, scores, n: int, finished=None, pad_token: int = 0, works
     int32, token [B, n] int32); a slot without a candidate holds -inf, its
     index mod K and -1.  ``workspace``: a uint8 tensor of at least
     ``beam_select_workspace_size`` bytes (allocated when None)."""
-    base = _base()
-    torch, lib = base._torch(), _lib.load()
+    torch, lib = _torch(), _lib.load()
     _cuda(logits, "logits", 2)
-    dt, dev = base._dtype_code(logits), logits.device
+    dt, dev = _dtype_code(logits), logits.device
     _cuda(scores, "scores", 2, torch.float32, dev)
     B, K = scores.shape
     R, V = logits.shape
@@ -79,17 +84,15 @@ def beam_select(logits, scores, n: int, finished=None, pad_token: int = 0, works
     score = torch.empty((B, max(n, 0)), dtype=torch.float32, device=dev)
     parent = torch.empty((B, max(n, 0)), dtype=torch.int32, device=dev)
     token = torch.empty((B, max(n, 0)), dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
-        base._check(lib.topkp_beam_select(base._ptr(logits), B, K, V, logits.stride(0) if R > 1 else V, dt,
-                                          base._ptr(scores), base._ptr(finished), int(pad_token), n, base._ptr(score),
-                                          base._ptr(parent), base._ptr(token), base._ptr(workspace),
-                                          workspace.numel(), base._stream(dev)))
+    _launch(dev, lib.topkp_beam_select, _ptr(logits), B, K, V, logits.stride(0) if R > 1 else V, dt, _ptr(scores),
+            _ptr(finished), int(pad_token), n, _ptr(score), _ptr(parent), _ptr(token), _ptr(workspace),
+            workspace.numel())
     return score, parent, token
 
 
 def beam_select_workspace_size(B: int, K: int, V: int, dtype, n: int) -> int:
     """Bytes of workspace ``beam_select`` needs."""
-    torch = _base()._torch()
+    torch = _torch()
     codes = {torch.float32: _lib.TOPKP_F32, torch.float16: _lib.TOPKP_F16, torch.bfloat16: _lib.TOPKP_BF16}
     return int(_lib.load().topkp_beam_select_workspace_size(B, K, V, codes[dtype], n))
 
@@ -97,6 +100,9 @@ def beam_select_workspace_size(B: int, K: int, V: int, dtype, n: int) -> int:
 def _layout(t, time_dim, name):
     """(row stride, block stride, blocks, entries, entry bytes) of a state in bytes."""
     es = t.element_size()
+    if time_dim == 1 and t.dim() > 1 and t.numel() and t.is_contiguous():  # the usual case
+        row = t.numel() // t.shape[0] * es
+        return row, row, 1, t.shape[1], row // t.shape[1]
     shape, stride = list(t.shape), list(t.stride())
     if not 1 <= time_dim < max(t.dim(), 2):
         raise ValueError(f"time_dim {time_dim} of a {t.dim()}-D {name}")
@@ -134,8 +140,7 @@ def beam_reorder(states, parent, lengths=None, time_dim: int = 1, out=None):
     ``states``).  lengths: [B, K] int32, how many entries along ``time_dim``
     of each row are live: only they move, and the rest of a destination row
     keeps what it held.  Returns the reordered tensors."""
-    base = _base()
-    torch, lib = base._torch(), _lib.load()
+    torch, lib = _torch(), _lib.load()
     single = torch.is_tensor(states)
     src = [states] if single else list(states)
     dst = src if out is None else [out] if torch.is_tensor(out) else list(out)
@@ -153,22 +158,19 @@ def beam_reorder(states, parent, lengths=None, time_dim: int = 1, out=None):
         lengths = lengths.contiguous()
     table = (_lib.State * max(len(src), 1))()
     for i, (s, d) in enumerate(zip(src, dst)):
-        for t in (s, d):
+        for t in (s,) if d is s else (s, d):
             _cuda(t, f"states[{i}]", None, None, dev)
             if t.dim() < 1 or t.shape[0] != B * K or t.shape != s.shape or t.dtype != s.dtype:
                 raise ValueError(f"states[{i}] must have {B} x {K} rows, and its output its shape and dtype")
         row, blk, blocks, entries, size = _layout(s, time_dim if s.dim() > 1 else 1, f"states[{i}]")
-        drow, dblk = _layout(d, time_dim if d.dim() > 1 else 1, f"out[{i}]")[:2]
-        table[i] = _lib.State(base._ptr(s), base._ptr(d), row, drow, blk, dblk, blocks, entries, size)
-    with torch.cuda.device(dev):
-        base._check(lib.topkp_beam_reorder(table, len(src), B, K, base._ptr(parent), base._ptr(lengths),
-                                           base._stream(dev)))
+        drow, dblk = (row, blk) if d is s else _layout(d, time_dim if d.dim() > 1 else 1, f"out[{i}]")[:2]
+        table[i] = _lib.State(_ptr(s), _ptr(d), row, drow, blk, dblk, blocks, entries, size)
+    _launch(dev, lib.topkp_beam_reorder, table, len(src), B, K, _ptr(parent), _ptr(lengths))
     return dst[0] if single else dst
 
 
 def _cache(t, exp, name, device, row_dtype):
-    base = _base()
-    torch = base._torch()
+    torch = _torch()
     _cuda(t, name, 4, None, device)
     quant = t.dtype == torch.float8_e4m3fn
     if not quant and t.dtype != row_dtype:
@@ -177,15 +179,13 @@ def _cache(t, exp, name, device, row_dtype):
         raise ValueError(f"{name}: a head's elements must be contiguous")
     if quant != (exp is not None):
         raise ValueError(f"{name}: exponents go with torch.float8_e4m3fn, and only with it")
-    c = _lib.Cache(base._ptr(t), None, _lib.TOPKP_E4M3 if quant else base._dtype_code(t), t.stride(0), t.stride(1),
-                   t.stride(2), 0, 0, 0)
-    if quant:
-        _cuda(exp, f"{name}'s exponents", 3, torch.uint8, device)
-        if exp.shape != t.shape[:3]:
-            raise ValueError(f"{name}'s exponents must be {tuple(t.shape[:3])}, not {tuple(exp.shape)}")
-        c.exponents = base._ptr(exp)
-        c.exp_page_stride, c.exp_token_stride, c.exp_head_stride = exp.stride()
-    return c
+    p0, p1, p2, _ = t.stride()
+    if not quant:
+        return _lib.Cache(_ptr(t), None, _dtype_code(t), p0, p1, p2, 0, 0, 0)
+    _cuda(exp, f"{name}'s exponents", 3, torch.uint8, device)
+    if exp.shape != t.shape[:3]:
+        raise ValueError(f"{name}'s exponents must be {tuple(t.shape[:3])}, not {tuple(exp.shape)}")
+    return _lib.Cache(_ptr(t), _ptr(exp), _lib.TOPKP_E4M3, p0, p1, p2, *exp.stride())
 
 
 def _pair(k_cache, v_cache):
@@ -201,10 +201,9 @@ def cache_write(k, v, slots, k_cache, v_cache, k_exp=None, v_exp=None):
     skip a row; k_cache, v_cache: [pages, page_size, H, D], of the rows'
     dtype, or float8_e4m3fn with k_exp, v_exp [pages, page_size, H] uint8,
     quantised as they are written.  v and v_cache may both be None."""
-    base = _base()
-    torch, lib = base._torch(), _lib.load()
+    torch, lib = _torch(), _lib.load()
     _cuda(k, "k", 3)
-    dt, dev = base._dtype_code(k), k.device
+    dt, dev = _dtype_code(k), k.device
     N, H, D = k.shape
     rows = [k] if v is None else [k, v]
     if (v is None) != (v_cache is None):
@@ -227,11 +226,9 @@ def cache_write(k, v, slots, k_cache, v_cache, k_exp=None, v_exp=None):
     if tuple(k_cache.shape[2:]) != (H, D):
         raise ValueError(f"rows are {H} x {D} and the cache's {tuple(k_cache.shape[2:])}")
     last = rows[-1]
-    with torch.cuda.device(dev):
-        base._check(lib.topkp_cache_write(
-            base._ptr(rows[0]), base._ptr(last) if v is not None else None, N, H, D, rows[0].stride(0),
-            rows[0].stride(1), last.stride(0), last.stride(1), dt, base._ptr(slots), ctypes.byref(kc),
-            ctypes.byref(vc) if vc is not None else None, k_cache.shape[0], k_cache.shape[1], base._stream(dev)))
+    _launch(dev, lib.topkp_cache_write, _ptr(rows[0]), _ptr(last) if v is not None else None, N, H, D,
+            *rows[0].stride()[:2], *last.stride()[:2], dt, _ptr(slots), ctypes.byref(kc),
+            ctypes.byref(vc) if vc is not None else None, *k_cache.shape[:2])
 
 
 def cache_read(slots, k_cache, v_cache, k_exp=None, v_exp=None, dtype=None):
@@ -239,8 +236,7 @@ def cache_read(slots, k_cache, v_cache, k_exp=None, v_exp=None, dtype=None):
     [N, H, D] of ``dtype`` (the cache's own, or any of the three for an e4m3
     cache, bfloat16 when None).  A slot outside the cache gives zeros.
     v_cache may be None; v is then None."""
-    base = _base()
-    torch, lib = base._torch(), _lib.load()
+    torch, lib = _torch(), _lib.load()
     _cuda(slots, "slots", 1, torch.int64)
     dev = slots.device
     slots = slots.contiguous()
@@ -255,11 +251,8 @@ def cache_read(slots, k_cache, v_cache, k_exp=None, v_exp=None, dtype=None):
     N, (H, D) = slots.shape[0], k_cache.shape[2:]
     k = torch.empty((N, H, D), dtype=dtype, device=dev)
     v = torch.empty((N, H, D), dtype=dtype, device=dev) if vc is not None else None
-    with torch.cuda.device(dev):
-        base._check(lib.topkp_cache_read(base._ptr(slots), N, H, D, ctypes.byref(kc),
-                                         ctypes.byref(vc) if vc is not None else None, k_cache.shape[0],
-                                         k_cache.shape[1], base._dtype_code(k), base._ptr(k), base._ptr(v),
-                                         base._stream(dev)))
+    _launch(dev, lib.topkp_cache_read, _ptr(slots), N, H, D, ctypes.byref(kc),
+            ctypes.byref(vc) if vc is not None else None, *k_cache.shape[:2], _dtype_code(k), _ptr(k), _ptr(v))
     return k, v
 
 
@@ -277,8 +270,7 @@ def tree_attention(q, k_cache, v_cache, context, pages=None, tree=None, nodes=No
     a bound of ``context`` known on the host, which plans the work (the
     capacity when None).  Returns out ([B, T, Hq, D]), or (out, lse) with
     lse [B, T, Hq] float32."""
-    base = _base()
-    torch, lib = base._torch(), _lib.load()
+    torch, lib = _torch(), _lib.load()
     _cuda(q, "q", 4)
     if q.dtype not in (torch.float16, torch.bfloat16):
         raise TypeError(f"q must be float16 or bfloat16, not {q.dtype}")
@@ -292,8 +284,8 @@ def tree_attention(q, k_cache, v_cache, context, pages=None, tree=None, nodes=No
     pool, page_size, Hkv, Dc = k_cache.shape
     if Dc != D:
         raise ValueError(f"head dimension {D} of q and {Dc} of the cache")
-    context = base._vec(context, B, torch.int32, "context", dev)
-    nodes = base._vec(nodes, B, torch.int32, "nodes", dev)
+    context = _vec(context, B, torch.int32, "context", dev)
+    nodes = _vec(nodes, B, torch.int32, "nodes", dev)
     if pages is not None:
         _cuda(pages, "pages", 2, torch.int32, dev)
         if pages.shape[0] != B:
@@ -313,18 +305,19 @@ def tree_attention(q, k_cache, v_cache, context, pages=None, tree=None, nodes=No
         raise ValueError("out must match q in shape, dtype and device, with its last dimension contiguous")
     lse = torch.empty((B, T, Hq), dtype=torch.float32, device=dev) if want_lse else None
     max_pages = 1 if pages is None else pages.shape[1]
+    qs, os = q.stride(), out.stride()
     a = _lib.TreeAttentionArgs(
-        q=base._ptr(q), out=base._ptr(out), lse=base._ptr(lse), k=kc, v=vc, table=base._ptr(pages),
-        context=base._ptr(context), nodes=base._ptr(nodes), tree=base._ptr(tree), B=B, T=T, Hq=Hq, Hkv=Hkv, D=D,
-        pages=pool, page_size=page_size, max_pages=max_pages, ld_table=0 if pages is None else (pages.stride(0) if B > 1 else max_pages),
+        q=_ptr(q), out=_ptr(out), lse=_ptr(lse), k=kc, v=vc, table=_ptr(pages),
+        context=_ptr(context), nodes=_ptr(nodes), tree=_ptr(tree), B=B, T=T, Hq=Hq, Hkv=Hkv, D=D,
+        pages=pool, page_size=page_size, max_pages=max_pages,
+        ld_table=0 if pages is None else pages.stride(0) if B > 1 else max_pages,
         max_context=max_pages * page_size if max_context is None else int(max_context),
-        q_batch_stride=q.stride(0), q_token_stride=q.stride(1), q_head_stride=q.stride(2),
-        out_batch_stride=out.stride(0), out_token_stride=out.stride(1), out_head_stride=out.stride(2),
-        dtype=base._dtype_code(q), scale=float(D) ** -0.5 if scale is None else float(scale))
+        q_batch_stride=qs[0], q_token_stride=qs[1], q_head_stride=qs[2],
+        out_batch_stride=os[0], out_token_stride=os[1], out_head_stride=os[2],
+        dtype=_dtype_code(q), scale=float(D) ** -0.5 if scale is None else float(scale))
     need = int(lib.topkp_tree_attention_workspace_size(ctypes.byref(a)))
     if need:
         workspace = _workspace(workspace, need, dev)
-        a.workspace, a.workspace_bytes = base._ptr(workspace), workspace.numel()
-    with torch.cuda.device(dev):
-        base._check(lib.topkp_tree_attention(ctypes.byref(a), base._stream(dev)))
+        a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel()
+    _launch(dev, lib.topkp_tree_attention, ctypes.byref(a))
     return (out, lse) if want_lse else out

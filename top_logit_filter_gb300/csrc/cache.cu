@@ -89,18 +89,17 @@ __device__ __forceinline__ Place place_of(const CacheRowsArgs& a, int lanes) {
   const int per_token = a.sides * a.H * lanes;           // threads of a token
   const int base = (int)blockIdx.y * kCacheThreads;      // first of them in this CTA, where a token has several CTAs
   const int t = base + (int)threadIdx.x;
-  p.token = per_token < kCacheThreads ? t / per_token : 0;
+  p.token = per_token < kCacheThreads ? (int)((uint32_t)t / (uint32_t)per_token) : 0;
   const int c = t - p.token * per_token;
   p.on = c < per_token && p.token < a.tokens;
   p.lane = c & (lanes - 1);
-  const int row = c / lanes;
-  p.side = row / a.H;
+  const int row = p.on ? c >> (31 - __clz(lanes)) : 0;
+  p.side = row >= a.H ? 1 : 0;
   p.head = row - p.side * a.H;
-  if (!p.on) p.side = p.head = 0;
   return p;
 }
 struct Spot {
-  int64_t page;
+  uint32_t page;
   int at;
   bool in;
 };
@@ -109,8 +108,8 @@ __device__ __forceinline__ Spot spot_of(const CacheRowsArgs& a, int64_t slot) {
   s.in = slot >= 0 && slot < a.slots_end;
   if (!s.in) slot = 0;
   // slots below 2^31 go through a 32-bit reciprocal (exact there)
-  s.page = a.page_mul ? (int64_t)(__umulhi((uint32_t)slot, a.page_mul) >> a.page_shift) : slot / a.page_size;
-  s.at = (int)(slot - s.page * a.page_size);
+  s.page = a.page_mul ? __umulhi((uint32_t)slot, a.page_mul) >> a.page_shift : (uint32_t)(slot / a.page_size);
+  s.at = (int)(slot - (int64_t)s.page * a.page_size);
   return s;
 }
 
@@ -151,17 +150,43 @@ __global__ void __launch_bounds__(kCacheThreads) write_kernel(const __grid_const
       }
       continue;
     }
-    uint32_t amax = 0;
+    uint32_t amax = 0;  // magnitude bits as fp32's
+    if (VEC == 8 && sizeof(raw) == 2) {
+      // two 16-bit magnitudes at once; a row with an infinity or NaN is gone
+      // through again for its finite ones
+      uint32_t two = 0;
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&keep[u][0].v[0]);
+      if (p.lane * VEC < a.D) {
 #pragma unroll
-    for (int i = 0; i < kKeep; ++i)
-      if ((i * lanes + p.lane) * VEC < a.D) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const uint32_t m = __float_as_uint(D_::to_float(keep[u][i].v[j])) & 0x7fffffffu;
-          if (m < 0x7f800000u) amax = max(amax, m);
-        }
+        for (int j = 0; j < 4; ++j) two = __vmaxu2(two, w[j % (VEC / 2 > 0 ? VEC / 2 : 1)] & 0x7fff7fffu);
       }
-    for (int o = lanes / 2; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(mask, amax, o));
+      uint32_t top = max(two & 0xffffu, two >> 16);
+      for (int o = lanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(mask, top, o));
+      constexpr uint32_t kInf = DT == TOPKP_F16 ? 0x7c00u : 0x7f80u;
+      if (top >= kInf) {
+        top = 0;
+        if (p.lane * VEC < a.D) {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) {
+            const uint32_t m = (uint32_t)keep[u][0].v[j] & 0x7fffu;
+            if (m < kInf) top = max(top, m);
+          }
+        }
+        for (int o = lanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(mask, top, o));
+      }
+      amax = __float_as_uint(D_::to_float((raw)top));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i)
+        if ((i * lanes + p.lane) * VEC < a.D) {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) {
+            const uint32_t m = __float_as_uint(D_::to_float(keep[u][i].v[j])) & 0x7fffffffu;
+            if (m < 0x7f800000u) amax = max(amax, m);
+          }
+        }
+      for (int o = lanes / 2; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(mask, amax, o));
+    }
     // below the normal range (and for zeros) e stays at its lowest
     const int e = max((int)(amax >> 23) - 127 - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0), -126);
     const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
@@ -265,8 +290,8 @@ cudaError_t launch_dt(const CacheRowsArgs& args, bool write, cudaStream_t s) {
     a.page_shift = l - 1;
   }
   const bool q = a.cache[0].dtype == TOPKP_E4M3;
-  // four tokens a thread once that fills the device (16384 threads an SM's
-  // worth of reads on their way), one where there are few
+  // four tokens a thread where that still leaves every SM its 2048 threads,
+  // one where there are fewer
   const unsigned gy = (unsigned)((per_token + kCacheThreads - 1) / kCacheThreads);
   const bool many = a.vec == 8 && a.N * per_token >= 4LL * 152 * 2048;
   const int64_t per_cta = (int64_t)a.tokens * (many ? 4 : 1);

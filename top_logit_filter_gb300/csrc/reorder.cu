@@ -43,38 +43,27 @@ __global__ void __launch_bounds__(kReorderThreads) reorder_kernel(const __grid_c
   const long long total = width * st.blocks;
   const char* src = reinterpret_cast<const char*>(st.src) + b * K * st.src_row_stride;
   char* dst = reinterpret_cast<char*>(st.dst) + b * K * st.dst_row_stride;
-  constexpr int COLS = KMAX <= 4 ? 4 : KMAX <= 8 ? 2 : 1;
   const long long step = (long long)gridDim.x * kReorderThreads;
-  for (long long i0 = (long long)blockIdx.x * kReorderThreads + tid; i0 < total; i0 += step * COLS) {
-    U r[COLS][KMAX];
-    long long col[COLS], at[COLS];
+  for (long long i = (long long)blockIdx.x * kReorderThreads + tid; i < total; i += step) {
+    long long blk = 0;
+    if (st.blocks > 1) blk = total <= 0x7fffffffll ? (long long)((uint32_t)i / (uint32_t)width) : i / width;
+    const long long col = i - blk * width;
+    const char* s = src + blk * st.src_block_stride + col * (long long)sizeof(U);
+    char* d = dst + blk * st.dst_block_stride + col * (long long)sizeof(U);
+    U r[KMAX];
 #pragma unroll
-    for (int c = 0; c < COLS; ++c) {
-      const long long i = i0 + c * step;
-      long long blk = 0;
-      if (st.blocks > 1) blk = total <= 0x7fffffffll ? (long long)((uint32_t)i / (uint32_t)width) : i / width;
-      col[c] = i < total ? i - blk * width : width;  // a column past every live one moves nothing
-      at[c] = blk;
+    for (int p = 0; p < KMAX; ++p)
+      if (p < K && col < live[p]) r[p] = *reinterpret_cast<const U*>(s + p * st.src_row_stride);
 #pragma unroll
-      for (int p = 0; p < KMAX; ++p)
-        if (p < K && col[c] < live[p])
-          r[c][p] = *reinterpret_cast<const U*>(src + p * st.src_row_stride + blk * st.src_block_stride +
-                                                col[c] * (long long)sizeof(U));
-    }
-#pragma unroll
-    for (int c = 0; c < COLS; ++c) {
-      char* d = dst + at[c] * st.dst_block_stride + col[c] * (long long)sizeof(U);
-#pragma unroll
-      for (int p = 0; p < KMAX; ++p)
-        if (p < K && col[c] < live[p]) {
-          unsigned long long m = kids[p];
-          while (m) {
-            const int j = __ffsll((long long)m) - 1;
-            m &= m - 1;
-            *reinterpret_cast<U*>(d + j * st.dst_row_stride) = r[c][p];
-          }
+    for (int p = 0; p < KMAX; ++p)
+      if (p < K && col < live[p]) {
+        unsigned long long m = kids[p];
+        while (m) {
+          const int j = __ffsll((long long)m) - 1;
+          m &= m - 1;
+          *reinterpret_cast<U*>(d + j * st.dst_row_stride) = r[p];
         }
-    }
+      }
   }
 }
 
@@ -90,13 +79,15 @@ cudaError_t launch_unit(const ReorderArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// CTAs of one request and state: enough for eight an SM over all of them, so
-// that each has several rounds to spread the setup of its tables over.
+// CTAs of one request and state, from the columns of a row and the number of
+// (request, state) pairs.  A CTA sets up its tables (two dependent reads and
+// four barriers) before it moves anything: eight columns a thread spread that
+// where there is work for it.
 int32_t reorder_chunks(int64_t units, int64_t groups) {
-  const int64_t all = (units + kReorderThreads - 1) / kReorderThreads;
-  const int64_t want = (8LL * 152 + groups - 1) / groups;
-  const int64_t c = all < want ? all : want;
-  return (int32_t)(c < 1 ? 1 : c);
+  int64_t rounds = 8;
+  while (rounds > 1 && groups * units < rounds * kReorderThreads * 8 * 152) rounds /= 2;
+  const int64_t c = (units + kReorderThreads * rounds - 1) / (kReorderThreads * rounds);
+  return (int32_t)(c < 1 ? 1 : c > 65535 ? 65535 : c);
 }
 
 cudaError_t launch_reorder(const ReorderArgs& a, cudaStream_t s) {

@@ -593,8 +593,10 @@ topkp_status topkp_device_status(void* stream) {
     cudaGetLastError();
     return fail(TOPKP_ERR_LAUNCH, "topkp_device_status: stream error: %s", cudaGetErrorString(e));
   }
-  unsigned int w = 0;
+  unsigned int w = 0, wa = 0;
   e = sorted_take_device_error(&w);
+  if (e == cudaSuccess) e = attention_take_device_error(&wa);
+  w |= wa;
   if (e != cudaSuccess) {
     cudaGetLastError();
     return fail(TOPKP_ERR_LAUNCH, "topkp_device_status: cannot read the device error word: %s", cudaGetErrorString(e));

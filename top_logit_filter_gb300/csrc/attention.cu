@@ -8,6 +8,7 @@
 // few rows, and the parts joined by their log-sums.
 #include "common.cuh"
 #include "decode.h"
+#include "internal.h"
 
 namespace topkp {
 namespace {
@@ -20,6 +21,9 @@ struct AttnDev {
   int splits;
   float* part_o;  // [splits][B * T * Hq][D]
   float* part_l;  // [splits][B * T * Hq]
+  uint32_t page_mul;  // reciprocal of page_size below 2^31, 0: divide
+  int page_shift;
+  int wide;           // an e4m3 row may be read 16 bytes at a time
 };
 
 // Tokens of request b that its nodes may see: the context, and the end of
@@ -333,6 +337,14 @@ __global__ void __launch_bounds__(kMmaThreads) attn_mma(const __grid_constant__ 
   }
 }
 
+}  // namespace
+}  // namespace topkp
+
+#include "attention_tc.cuh"
+
+namespace topkp {
+namespace {
+
 // Joins the parts of a row: weights exp(lse_i - lse).  One warp per row.
 template <bool BF>
 __global__ void __launch_bounds__(128) attn_join(const __grid_constant__ AttnDev p) {
@@ -380,14 +392,41 @@ cudaError_t launch_mma(const AttnDev& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+template <int DP, bool BF, bool Q8>
+cudaError_t launch_tc(const AttnDev& p, cudaStream_t s) {
+  const topkp_tree_attention_args& a = p.a;
+  constexpr size_t smem = TcShape<DP>::kSmem;
+  cudaError_t e = cudaFuncSetAttribute(attn_tc<DP, BF, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = a.T * (a.Hq / a.Hkv);
+  const dim3 grid((unsigned)((rows + kTcRows - 1) / kTcRows), (unsigned)p.splits, (unsigned)(a.B * a.Hkv));
+  attn_tc<DP, BF, Q8><<<grid, kTcThreads, smem, s>>>(p);
+  return cudaGetLastError();
+}
+
+// Tensor memory's 128 rows pay from here on.
+bool on_tensor_cores(const topkp_tree_attention_args& a) { return a.T * (a.Hq / a.Hkv) > 16; }
+
 template <bool BF, bool Q8>
 cudaError_t launch_dim(const AttnDev& p, cudaStream_t s) {
+  if (on_tensor_cores(p.a)) {
+    if (p.a.D <= 64) return launch_tc<64, BF, Q8>(p, s);
+    if (p.a.D <= 128) return launch_tc<128, BF, Q8>(p, s);
+    return launch_tc<256, BF, Q8>(p, s);
+  }
   if (p.a.D <= 64) return launch_mma<64, BF, Q8>(p, s);
   if (p.a.D <= 128) return launch_mma<128, BF, Q8>(p, s);
   return launch_mma<256, BF, Q8>(p, s);
 }
 
 }  // namespace
+
+cudaError_t attention_take_device_error(unsigned int* out) {
+  const unsigned int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_attention_error, sizeof(*out));
+  if (e == cudaSuccess && *out) e = cudaMemcpyToSymbol(g_attention_error, &zero, sizeof(zero));
+  return e;
+}
 
 AttnPlan plan_attention(const topkp_tree_attention_args& a, int num_sms) {
   AttnPlan p;
@@ -396,6 +435,25 @@ AttnPlan plan_attention(const topkp_tree_attention_args& a, int num_sms) {
   const int64_t cap = a.max_pages * a.page_size;
   const int64_t len = (a.max_context < cap ? (a.max_context > 0 ? a.max_context : 0) : cap) + a.T;
   const int64_t tiles = (len + kTile - 1) / kTile;
+  if (on_tensor_cores(a)) {
+    // the number of parts with the least rounds of CTAs times tiles of each
+    // (and four tiles' time for a CTA's start and end)
+    const int64_t slots = (a.D > 128 ? 1LL : 2LL) * num_sms;
+    const int64_t base = a.B * a.Hkv * ((rows + kTcRows - 1) / kTcRows);
+    int64_t best = -1;
+    p.splits = 1;
+    for (int64_t n = 1; n <= 64 && n <= tiles; ++n) {
+      const int64_t per = (tiles + n - 1) / n;
+      if ((tiles + per - 1) / per != n) continue;
+      const int64_t cost = (base * n + slots - 1) / slots * (per + 4) + (n > 1 ? 2 : 0);
+      if (best < 0 || cost < best) {
+        best = cost;
+        p.splits = (int)n;
+      }
+    }
+    p.part_bytes = p.splits > 1 ? (size_t)p.splits * (size_t)(a.B * a.T * a.Hq) * (a.D + 1) * sizeof(float) : 0;
+    return p;
+  }
   int64_t splits = (3LL * num_sms + ctas - 1) / ctas;
   if (splits > (tiles + 1) / 2) splits = (tiles + 1) / 2;
   if (splits < 1) splits = 1;
@@ -413,6 +471,18 @@ cudaError_t launch_attention(const topkp_tree_attention_args& a, const AttnPlan&
   const size_t all = (size_t)(a.B * a.T * a.Hq);
   p.part_o = reinterpret_cast<float*>(a.workspace);
   p.part_l = p.part_o + (plan.splits > 1 ? (size_t)plan.splits * all * a.D : 0);
+  p.page_mul = 0;
+  p.page_shift = 0;
+  if (a.page_size > 1) {  // t / page_size = (t * mul) >> (32 + shift), exact below 2^31
+    int l = 1;
+    while ((1LL << l) < a.page_size) ++l;
+    p.page_mul = (uint32_t)(((1ull << (31 + l)) + a.page_size - 1) / a.page_size);
+    p.page_shift = l - 1;
+  }
+  auto by16 = [](const topkp_cache& c) {
+    return ((uintptr_t)c.data | (uintptr_t)c.page_stride | (uintptr_t)c.token_stride | (uintptr_t)c.head_stride) % 16 == 0;
+  };
+  p.wide = a.D % 16 == 0 && by16(a.k) && by16(a.v);
   const bool bf = a.dtype == TOPKP_BF16, q8 = a.k.dtype == TOPKP_E4M3;
   cudaError_t e = bf ? (q8 ? launch_dim<true, true>(p, s) : launch_dim<true, false>(p, s))
                      : (q8 ? launch_dim<false, true>(p, s) : launch_dim<false, false>(p, s));

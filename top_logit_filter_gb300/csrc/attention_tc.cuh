@@ -1,0 +1,528 @@
+// The tensor-memory kernel of topkp_tree_attention (included by attention.cu).
+//
+// One CTA: 128 rows against tiles of 64 tokens.  Warps 0-3 do the softmax, a
+// thread a row (TMEM lane i is row i); warps 4-6 bring keys and values into
+// shared memory; one thread of warp 7 issues the matrix instructions (eight
+// warps in all, so that two CTAs leave 128 registers a thread):
+//   S = Q K^T   both operands in shared memory, K-major, 128-byte swizzle
+//   O += P V    P in TMEM over its S, V in shared memory as it lies (tokens
+//               by dims), read with the dims as the major direction
+// S is double-buffered, so the product of tile j + 1 runs under the softmax
+// of tile j, and two CTAs share an SM, so one's products run under the
+// other's softmax.  O stays in TMEM; a row's reference maximum moves only
+// when a tile's maximum exceeds it by 2^8, which spares the rescaling of O
+// but for the first few tiles (probabilities up to 2^8 lose nothing in
+// floating point).
+#pragma once
+
+namespace topkp {
+namespace {
+
+constexpr int kTcRows = 128;
+constexpr int kTcThreads = 256;
+constexpr int kTcFeeders = 96;  // threads that bring keys and values
+constexpr float kSlack = 8.0f;
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+// bit 0: a wait of this translation unit gave up
+__device__ unsigned int g_attention_error;
+
+__device__ __forceinline__ float exp2_approx(float t) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  return e;
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((int)acc)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((int)acc)
+      : "memory");
+}
+// 32 columns of this thread's lane.
+__device__ __forceinline__ void tc_ld32(uint32_t (&r)[32], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+      "%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+      "%30,%31};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
+      "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_ld16(uint32_t (&r)[16], uint32_t addr) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(addr));
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Shared-memory operand of a matrix instruction, 128-byte swizzle.  K-major:
+// groups of eight rows are `stride` bytes apart.  Major in the other
+// direction: groups of eight k are `stride` apart, blocks of 64 elements of
+// the major direction `lead`.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead, uint32_t stride) {
+  return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)((lead >> 4) & 0x3fff) << 16) |
+         ((uint64_t)((stride >> 4) & 0x3fff) << 32) | (1ull << 46) | (2ull << 61);
+}
+// Where 16-byte piece c of row r lies in a swizzled operand of ROWS rows.
+template <int ROWS>
+__device__ __forceinline__ uint32_t swizzled(int r, int c) {
+  return (uint32_t)((c >> 3) * (ROWS * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull; }
+
+template <int DP>
+struct TcShape {
+  static constexpr int kStages = DP == 64 ? 4 : 2;
+  static constexpr int kQBytes = kTcRows * DP * 2;
+  static constexpr int kTileBytes = kTile * DP * 2;
+  static constexpr int kColumns = DP == 256 ? 512 : 256;  // TMEM: two S of 64, O of DP
+  static constexpr size_t kSmem = 1024 + kQBytes + (size_t)kStages * 2 * kTileBytes;
+};
+
+// A bounded wait; once one has given up, none of the CTA waits any more.
+__device__ __forceinline__ void tc_wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
+  if (mbar_try_wait(bar, parity)) return;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*dead) return;
+    if (globaltimer_ns() - t0 > kWaitNs) {
+      *dead = 1;
+      atomicOr(&g_attention_error, 1u);
+      return;
+    }
+  }
+}
+
+// Two e4m3 in the high bytes of the halves of t as bf16: sign, then exponent
+// and mantissa four bits down, which reads as the value times 2^-120,
+// subnormals too.  Scaled back exactly by powers of two.
+__device__ __forceinline__ uint32_t e4m3_to_bf16x2(uint32_t t, uint32_t scale) {
+  uint32_t r = (t & 0x80008000u) | ((t >> 4) & 0x07f007f0u);
+  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(0x7b807b80u));  // 2^120
+  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(scale));
+  return r;
+}
+// Sixteen e4m3 times 2^(e - 127) in the rows' type.
+template <bool BF>
+__device__ __forceinline__ void widen16(const uint4& w, uint32_t e, uint4& lo, uint4& hi) {
+  uint32_t r[8];
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+  // the code 0x7f of either sign is NaN, which the shift would read as 480
+  uint32_t nan = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) nan |= (in[i] & 0x7f7f7f7fu) + 0x01010101u;
+  if (BF && !(nan & 0x80808080u)) {
+    // e = 0 does not occur in a written cache; it reads as 2^-126
+    const uint32_t sc = (e ? e : 1u) << 7, s2 = sc | (sc << 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r[2 * i] = e4m3_to_bf16x2(__byte_perm(in[i], 0u, 0x1404), s2);
+      r[2 * i + 1] = e4m3_to_bf16x2(__byte_perm(in[i], 0u, 0x3424), s2);
+    }
+  } else {
+    const float s = exponent_scale(e);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t h;
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(in[i >> 1] >> (16 * (i & 1)))));
+      r[i] = pack2<BF>(__half2float(__ushort_as_half((uint16_t)h)) * s, __half2float(__ushort_as_half((uint16_t)(h >> 16))) * s);
+    }
+  }
+  lo = make_uint4(r[0], r[1], r[2], r[3]);
+  hi = make_uint4(r[4], r[5], r[6], r[7]);
+}
+// Sixteen e4m3 of a row, in two pieces where the row's alignment or end asks for it.
+__device__ __forceinline__ uint4 fetch16(const uint8_t* p, int wide, bool both) {
+  if (wide) return __ldg(reinterpret_cast<const uint4*>(p));
+  const uint2 lo = __ldg(reinterpret_cast<const uint2*>(p));
+  const uint2 hi = both ? __ldg(reinterpret_cast<const uint2*>(p) + 1) : make_uint2(0, 0);
+  return make_uint4(lo.x, lo.y, hi.x, hi.y);
+}
+
+template <int DP, bool BF, bool Q8>
+__global__ void __launch_bounds__(kTcThreads, DP == 256 ? 1 : 2) attn_tc(const __grid_constant__ AttnDev p) {
+  using Shape = TcShape<DP>;
+  constexpr int ST = Shape::kStages;
+  extern __shared__ unsigned char tc_smem[];
+  unsigned char* smem = tc_smem + ((1024 - (smem_u32(tc_smem) & 1023)) & 1023);
+  unsigned char* sq = smem;
+  unsigned char* sk = smem + Shape::kQBytes;  // ST keys, then ST values
+  unsigned char* sv = sk + ST * Shape::kTileBytes;
+  __shared__ uint64_t full[ST], empty[ST], s_full[2], p_full[2], pv_done, q_full;
+  __shared__ uint32_t tmem_base;
+  __shared__ volatile int dead;
+  const topkp_tree_attention_args& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int G = (int)(a.Hq / a.Hkv);
+  const int rows = (int)a.T * G;
+  const int64_t bh = blockIdx.z;
+  const int64_t b = bh / a.Hkv;
+  const int h = (int)(bh - b * a.Hkv);
+  const int row0 = blockIdx.x * kTcRows;
+  const int split = blockIdx.y;
+  int ctx, len, nodes;
+  request_span(a, b, &ctx, &len, &nodes);
+  const int tiles = (len + kTile - 1) / kTile;
+  const int per = (tiles + p.splits - 1) / p.splits;
+  const int t_begin = min(split * per, tiles), n = min(t_begin + per, tiles) - t_begin;
+
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&full[i], kTcFeeders);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 128);
+    }
+    mbar_init(&pv_done, 1);
+    mbar_init(&q_full, 128);
+    fence_mbar_init();
+    dead = 0;
+  }
+  if (warp == 7) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)),
+                 "n"(Shape::kColumns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = tmem_base;
+  constexpr uint32_t kO = 128;  // first column of O
+
+  if (warp < 4) {
+    // ---- softmax: thread = row ----
+    const int r = row0 + tid;
+    const int node = r / G;
+    const int hq = h * G + (r - node * G);
+    const bool in = r < rows;
+    {
+      // the row of Q into its place
+      const uint16_t* qr = reinterpret_cast<const uint16_t*>(a.q) + b * a.q_batch_stride +
+                           (in ? node * a.q_token_stride + hq * a.q_head_stride : 0);
+#pragma unroll 4
+      for (int c = 0; c < DP / 8; ++c) {
+        const uint4 v = in && c * 8 < a.D ? *reinterpret_cast<const uint4*>(qr + c * 8) : make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(sq + swizzled<kTcRows>(tid, c)) = v;
+      }
+      fence_proxy_async_shared();
+      mbar_arrive(&q_full);
+    }
+    // rows past the last (their Q is zero) and of missing nodes go along as
+    // if they saw the context; what they get is not written
+    const bool seen = in && node < nodes;
+    const uint64_t bits = seen && a.tree ? a.tree[b * a.T + node] : 0;
+    const bool idle = row0 + warp * 32 >= rows;  // the whole warp
+    const float sc0 = a.scale * kLog2e;
+    const float sc = sc0 > 0.0f ? sc0 : 1.0f;  // a scale of zero or less is applied to the products first
+    const uint32_t lanes = tm + ((uint32_t)(warp * 32) << 16);
+    float m = -INFINITY, l = 0.0f;
+    for (int j = 0; j < n; ++j) {
+      const uint32_t sb = lanes + (j & 1) * 64;
+      tc_wait(&s_full[j & 1], (j >> 1) & 1, &dead);
+      if (idle) {
+        mbar_arrive(&p_full[j & 1]);
+        continue;
+      }
+      tc_fence_after();
+      uint32_t s0[32], s1[32];
+      tc_ld32(s0, sb);
+      tc_ld32(s1, sb + 32);
+      tc_wait_ld();
+      const int t0 = (t_begin + j) * kTile;
+      if (!(sc0 > 0.0f)) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          s0[i] = __float_as_uint(__uint_as_float(s0[i]) * sc0);
+          s1[i] = __float_as_uint(__uint_as_float(s1[i]) * sc0);
+        }
+      }
+      if (t0 + kTile > ctx) {  // a tile with drafted nodes in it, or past the end
+        // bit i: whether the row sees token t0 + i
+        const int d = t0 - ctx;
+        uint64_t vis;
+        if (a.tree) vis = d >= 64 ? 0 : d >= 0 ? bits >> d : (bits << -d) | low_bits(-d);
+        else vis = low_bits(node + 1 - d);
+        vis &= low_bits(len - t0);
+        const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> 32);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          s0[i] = v0 & (1u << i) ? s0[i] : 0xff800000u;
+          s1[i] = v1 & (1u << i) ? s1[i] : 0xff800000u;
+        }
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fmaxf(__uint_as_float(s0[i]), __uint_as_float(s1[i])));
+      const float top = mx == -INFINITY ? -INFINITY : mx * sc;
+      if (j == 0) {
+        m = top;
+      } else {
+        const bool up = top > m + kSlack || (m == -INFINITY && top > -INFINITY);
+        if (__any_sync(0xffffffffu, up)) {
+          const float f = up ? exp2f(m - top) : 1.0f;
+          if (up) {
+            m = top;
+            l *= f;
+          }
+          tc_wait(&pv_done, (j - 1) & 1, &dead);
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < DP; c += 16) {
+            uint32_t o[16];
+            tc_ld16(o, lanes + kO + c);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tc_st16(lanes + kO + c, o);
+          }
+        }
+      }
+      const float base = m == -INFINITY ? 0.0f : m;
+      float sum0 = 0.0f, sum1 = 0.0f;
+      uint32_t pk[32];
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const float x0 = exp2_approx(fmaf(__uint_as_float(s0[i]), sc, -base));
+        const float x1 = exp2_approx(fmaf(__uint_as_float(s0[i + 1]), sc, -base));
+        const float y0 = exp2_approx(fmaf(__uint_as_float(s1[i]), sc, -base));
+        const float y1 = exp2_approx(fmaf(__uint_as_float(s1[i + 1]), sc, -base));
+        sum0 += x0 + y0;
+        sum1 += x1 + y1;
+        pk[i / 2] = pack2<BF>(x0, x1);
+        pk[16 + i / 2] = pack2<BF>(y0, y1);
+      }
+      l += sum0 + sum1;
+      tc_st32(sb, pk);
+      tc_wait_st();
+      tc_fence_before();
+      mbar_arrive(&p_full[j & 1]);
+    }
+    if (n > 0) {
+      tc_wait(&pv_done, (n - 1) & 1, &dead);
+      tc_fence_after();
+    }
+    const int64_t all_rows = a.B * a.T * a.Hq;
+    const int64_t row = (b * a.T + node) * a.Hq + hq;
+    if (!seen) l = 0.0f;
+    const float inv = l > 0.0f ? 1.0f / l : l;
+    const float lse = l > 0.0f ? (m + log2f(l)) * kLn2 : l == 0.0f ? -INFINITY : l;
+    const bool write = in && !dead;
+#pragma unroll 1
+    for (int c = 0; c < DP; c += 32) {
+      uint32_t o[32];
+      if (n > 0) {
+        tc_ld32(o, lanes + kO + c);
+        tc_wait_ld();
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = n > 0 && l != 0.0f ? __float_as_uint(__uint_as_float(o[i]) * inv) : 0u;
+      if (write) {
+        if (p.splits > 1) {
+          uint4* po = reinterpret_cast<uint4*>(p.part_o + ((int64_t)split * all_rows + row) * a.D + c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c + i * 4 < a.D) po[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        } else {
+          uint4* po = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + b * a.out_batch_stride +
+                                               node * a.out_token_stride + hq * a.out_head_stride + c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (c + i * 8 < a.D) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = pack2<BF>(__uint_as_float(o[8 * i + 2 * k]), __uint_as_float(o[8 * i + 2 * k + 1]));
+              po[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+      }
+      __syncwarp();
+    }
+    if (write) {
+      if (p.splits > 1) p.part_l[(int64_t)split * all_rows + row] = lse;
+      else if (a.lse) a.lse[row] = lse;
+    }
+    tc_fence_before();
+  } else if (warp < 7) {
+    // ---- keys and values ----
+    const int pt = tid - 128;
+    const int32_t* table = a.table ? a.table + b * a.ld_table : nullptr;
+    constexpr int CH = Q8 ? DP / 16 : DP / 8;  // 16-byte pieces of a cached row
+    constexpr int STEP = kTcFeeders / CH;      // rows between a thread's rows
+    constexpr int NR = (kTile + STEP - 1) / STEP;
+    const int c = pt % CH, r0 = pt / CH;
+    const bool c_in = c * (Q8 ? 16 : 8) < a.D;
+    auto mine = [&](int i) { return NR * STEP == kTile || r0 + i * STEP < kTile; };
+    // the page and place of token t, page -1 if there is none to read
+    auto find = [&](int t, int& page, int& at) {
+      page = -1;
+      at = t;
+      if (t < len && c_in) {
+        page = (int)b;
+        if (table) {
+          const int pg = p.page_mul ? (int)(__umulhi((uint32_t)t, p.page_mul) >> p.page_shift) : t / (int)a.page_size;
+          at = t - pg * (int)a.page_size;
+          page = table[pg];
+          if (page < 0 || page >= a.pages) page = -1;
+        }
+      }
+    };
+    if constexpr (!Q8) {
+      const uint16_t* kb = reinterpret_cast<const uint16_t*>(a.k.data) + h * a.k.head_stride + c * 8;
+      const uint16_t* vb = reinterpret_cast<const uint16_t*>(a.v.data) + h * a.v.head_stride + c * 8;
+      const uint32_t ks = smem_u32(sk), vs = smem_u32(sv);
+      int told = 0;  // tiles handed over
+      auto tell = [&](int upto) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_shared();
+        for (; told < upto; ++told) mbar_arrive(&full[told % ST]);
+      };
+      for (int j = 0; j < n; ++j) {
+        const int st = j % ST;
+        int page[NR], at[NR];
+#pragma unroll
+        for (int i = 0; i < NR; ++i) find((t_begin + j) * kTile + r0 + i * STEP, page[i], at[i]);
+        if (j >= ST) {
+          tell(j);  // before waiting for room: what is there may be what makes it
+          tc_wait(&empty[st], (j / ST - 1) & 1, &dead);
+        }
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          if (!mine(i)) continue;
+          const bool in = page[i] >= 0;
+          const int64_t pg = in ? page[i] : 0, to = in ? at[i] : 0;
+          const uint32_t off = st * Shape::kTileBytes + swizzled<kTile>(r0 + i * STEP, c);
+          cp16(ks + off, in ? kb + pg * a.k.page_stride + to * a.k.token_stride : reinterpret_cast<const uint16_t*>(a.k.data), in);
+          cp16(vs + off, in ? vb + pg * a.v.page_stride + to * a.v.token_stride : reinterpret_cast<const uint16_t*>(a.v.data), in);
+        }
+      }
+      tell(n);
+    } else {
+      const uint8_t* kb = reinterpret_cast<const uint8_t*>(a.k.data) + h * a.k.head_stride + c * 16;
+      const uint8_t* vb = reinterpret_cast<const uint8_t*>(a.v.data) + h * a.v.head_stride + c * 16;
+      const uint8_t* ke = a.k.exponents + h * a.k.exp_head_stride;
+      const uint8_t* ve = a.v.exponents + h * a.v.exp_head_stride;
+      uint4 kr[NR], vr[NR];
+      uint32_t ex[NR];
+      auto fetch = [&](int j) {
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          int page, at;
+          find((t_begin + j) * kTile + r0 + i * STEP, page, at);
+          kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
+          ex[i] = 0x7f7f;
+          if (page >= 0 && mine(i)) {
+            const int64_t pg = page, to = at;
+            kr[i] = fetch16(kb + pg * a.k.page_stride + to * a.k.token_stride, p.wide, c * 16 + 8 < a.D);
+            vr[i] = fetch16(vb + pg * a.v.page_stride + to * a.v.token_stride, p.wide, c * 16 + 8 < a.D);
+            ex[i] = (uint32_t)ke[pg * a.k.exp_page_stride + to * a.k.exp_token_stride] |
+                    ((uint32_t)ve[pg * a.v.exp_page_stride + to * a.v.exp_token_stride] << 8);
+          }
+        }
+      };
+      if (n > 0) fetch(0);
+      for (int j = 0; j < n; ++j) {
+        const int st = j % ST;
+        if (j >= ST) tc_wait(&empty[st], (j / ST - 1) & 1, &dead);
+        unsigned char* kd = sk + st * Shape::kTileBytes;
+        unsigned char* vd = sv + st * Shape::kTileBytes;
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          const int r = r0 + i * STEP;
+          if (!mine(i)) continue;
+          uint4 lo, hi;
+          widen16<BF>(kr[i], ex[i] & 0xff, lo, hi);
+          *reinterpret_cast<uint4*>(kd + swizzled<kTile>(r, 2 * c)) = lo;
+          *reinterpret_cast<uint4*>(kd + swizzled<kTile>(r, 2 * c + 1)) = hi;
+          widen16<BF>(vr[i], ex[i] >> 8, lo, hi);
+          *reinterpret_cast<uint4*>(vd + swizzled<kTile>(r, 2 * c)) = lo;
+          *reinterpret_cast<uint4*>(vd + swizzled<kTile>(r, 2 * c + 1)) = hi;
+        }
+        if (j + 1 < n) fetch(j + 1);
+        fence_proxy_async_shared();
+        mbar_arrive(&full[st]);
+      }
+    }
+  } else if (lane == 0) {
+    // ---- matrix instructions ----
+    constexpr uint32_t kind = BF ? 1u : 0u;
+    constexpr uint32_t common = (1u << 4) | (kind << 7) | (kind << 10) | ((uint32_t)(kTcRows / 16) << 24);
+    constexpr uint32_t i_qk = common | ((uint32_t)(kTile / 8) << 17);
+    constexpr uint32_t i_pv = common | (1u << 16) | ((uint32_t)(DP / 8) << 17);
+    const uint32_t q0 = smem_u32(sq), k0 = smem_u32(sk), v0 = smem_u32(sv);
+    auto product_s = [&](int j) {
+      tc_wait(&full[j % ST], (j / ST) & 1, &dead);
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < DP / 16; ++kk)
+        tc_mma_ss(tm + (j & 1) * 64, operand(q0 + (kk / 4) * (kTcRows * 128) + (kk % 4) * 32, 16, 1024),
+                  operand(k0 + (j % ST) * Shape::kTileBytes + (kk / 4) * (kTile * 128) + (kk % 4) * 32, 16, 1024), i_qk, kk > 0);
+      tc_commit(&s_full[j & 1]);
+    };
+    if (n > 0) {
+      tc_wait(&q_full, 0, &dead);
+      product_s(0);
+    }
+    for (int j = 0; j < n; ++j) {
+      if (j + 1 < n) {
+        // the other S still holds P of tile j - 1 until its product is done
+        if (j > 0) tc_wait(&pv_done, (j - 1) & 1, &dead);
+        product_s(j + 1);
+      }
+      tc_wait(&p_full[j & 1], (j >> 1) & 1, &dead);
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < kTile / 16; ++kk)
+        tc_mma_ts(tm + kO, tm + (j & 1) * 64 + kk * 8,
+                  operand(v0 + (j % ST) * Shape::kTileBytes + kk * 2048, kTile * 128, 1024), i_pv, j > 0 || kk > 0);
+      tc_commit(&empty[j % ST]);
+      tc_commit(&pv_done);
+    }
+    tc_fence_before();
+  }
+  __syncwarp();
+  __syncthreads();
+  if (dead) {  // products may still be in flight: time for them to end
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 10000000ull) __nanosleep(1000);
+  }
+  if (warp == 7) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(Shape::kColumns) : "memory");
+  }
+}
+
+}  // namespace
+}  // namespace topkp

@@ -195,5 +195,7 @@ int device_sms(int* dev);
 // The sorted-path translation unit keeps a device error word (bit 0: a
 // bounded wait gave up); this reads and clears it (synchronous).
 cudaError_t sorted_take_device_error(unsigned int* out);
+// The same of the attention's translation unit.
+cudaError_t attention_take_device_error(unsigned int* out);
 
 }  // namespace topkp

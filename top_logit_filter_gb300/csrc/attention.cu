@@ -6,6 +6,8 @@
 // and value is read once for a tile of rows, with the running maximum and
 // sum of the softmax; a request's tokens are split over CTAs when there are
 // few rows, and the parts joined by their log-sums.
+#include <cuda.h>
+
 #include "common.cuh"
 #include "decode.h"
 #include "internal.h"
@@ -24,6 +26,7 @@ struct AttnDev {
   uint32_t page_mul;  // reciprocal of page_size below 2^31, 0: divide
   int page_shift;
   int wide;           // an e4m3 row may be read 16 bytes at a time
+  int box;            // tokens of a TMA box, 0: plain copies
 };
 
 // Tokens of request b that its nodes may see: the context, and the end of
@@ -392,27 +395,73 @@ cudaError_t launch_mma(const AttnDev& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <int DP, bool BF, bool Q8>
-cudaError_t launch_tc(const AttnDev& p, cudaStream_t s) {
+// The driver's encoder of tensor maps, looked up once (null where it is missing).
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encoder() {
+  static const EncodeTiled fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      f = nullptr;
+    }
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  return fn;
+}
+// A cache as (element, head, token, page); false where TMA cannot take it.
+bool make_map(CUtensorMap* map, const topkp_cache& c, const topkp_tree_attention_args& a, int box, int width) {
+  const bool q8 = c.dtype == TOPKP_E4M3;
+  const uint64_t es = q8 ? 1 : 2;
+  // a dimension of one entry may have any stride: give it one that is valid
+  auto stride = [&](int64_t s, int64_t count) { return count > 1 ? (uint64_t)s * es : ((uint64_t)a.D * es + 15) / 16 * 16; };
+  const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.Hkv, (cuuint64_t)a.page_size, (cuuint64_t)a.pages};
+  const cuuint64_t strides[3] = {stride(c.head_stride, a.Hkv), stride(c.token_stride, a.page_size), stride(c.page_stride, a.pages)};
+  for (const cuuint64_t s : strides)
+    if (s % 16 || s >= (1ull << 40)) return false;
+  if ((uintptr_t)c.data % 16) return false;
+  const cuuint32_t boxes[4] = {(cuuint32_t)width, 1, (cuuint32_t)box, 1}, steps[4] = {1, 1, 1, 1};
+  const EncodeTiled encode = encoder();
+  return encode && encode(map, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, c.data, dims, strides,
+                          boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          q8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DP, int NT, bool BF, bool Q8>
+cudaError_t launch_tc(AttnDev p, cudaStream_t s) {
+  using Shape = TcShape<DP, NT, Q8>;
   const topkp_tree_attention_args& a = p.a;
-  constexpr size_t smem = TcShape<DP>::kSmem;
-  cudaError_t e = cudaFuncSetAttribute(attn_tc<DP, BF, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(attn_tc<DP, NT, BF, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kSmem);
   if (e != cudaSuccess) return e;
+  // tokens of a box: they lie in one page, and eight rows make a swizzle's group
+  CUtensorMap km = {}, vm = {};
+  p.box = kTile;
+  if (a.table)
+    while (p.box > 4 && a.page_size % p.box) p.box /= 2;
+  const int width = Q8 ? DP : 64;
+  if (p.box < 8 || !make_map(&km, a.k, a, p.box, width) || !make_map(&vm, a.v, a, p.box, width)) p.box = 0;
   const int64_t rows = a.T * (a.Hq / a.Hkv);
-  const dim3 grid((unsigned)((rows + kTcRows - 1) / kTcRows), (unsigned)p.splits, (unsigned)(a.B * a.Hkv));
-  attn_tc<DP, BF, Q8><<<grid, kTcThreads, smem, s>>>(p);
+  const dim3 grid((unsigned)((rows + NT * kTcRows - 1) / (NT * kTcRows)), (unsigned)p.splits, (unsigned)(a.B * a.Hkv));
+  attn_tc<DP, NT, BF, Q8><<<grid, Shape::kThreads, Shape::kSmem, s>>>(p, km, vm);
   return cudaGetLastError();
 }
 
 // Tensor memory's 128 rows pay from here on.
 bool on_tensor_cores(const topkp_tree_attention_args& a) { return a.T * (a.Hq / a.Hkv) > 16; }
+// Tiles of 128 rows of a CTA (256 dims leave tensor memory for one).
+int row_tiles(const topkp_tree_attention_args& a) { return a.T * (a.Hq / a.Hkv) > kTcRows && a.D <= 128 ? 2 : 1; }
 
 template <bool BF, bool Q8>
 cudaError_t launch_dim(const AttnDev& p, cudaStream_t s) {
   if (on_tensor_cores(p.a)) {
-    if (p.a.D <= 64) return launch_tc<64, BF, Q8>(p, s);
-    if (p.a.D <= 128) return launch_tc<128, BF, Q8>(p, s);
-    return launch_tc<256, BF, Q8>(p, s);
+    const bool two = row_tiles(p.a) == 2;
+    if (p.a.D <= 64) return two ? launch_tc<64, 2, BF, Q8>(p, s) : launch_tc<64, 1, BF, Q8>(p, s);
+    if (p.a.D <= 128) return two ? launch_tc<128, 2, BF, Q8>(p, s) : launch_tc<128, 1, BF, Q8>(p, s);
+    return launch_tc<256, 1, BF, Q8>(p, s);
   }
   if (p.a.D <= 64) return launch_mma<64, BF, Q8>(p, s);
   if (p.a.D <= 128) return launch_mma<128, BF, Q8>(p, s);
@@ -438,8 +487,9 @@ AttnPlan plan_attention(const topkp_tree_attention_args& a, int num_sms) {
   if (on_tensor_cores(a)) {
     // the number of parts with the least rounds of CTAs times tiles of each
     // (and four tiles' time for a CTA's start and end)
-    const int64_t slots = (a.D > 128 ? 1LL : 2LL) * num_sms;
-    const int64_t base = a.B * a.Hkv * ((rows + kTcRows - 1) / kTcRows);
+    const int64_t nt = row_tiles(a);
+    const int64_t slots = (a.D > 128 || nt == 2 || a.k.dtype == TOPKP_E4M3 ? 1LL : 2LL) * num_sms;
+    const int64_t base = a.B * a.Hkv * ((rows + nt * kTcRows - 1) / (nt * kTcRows));
     int64_t best = -1;
     p.splits = 1;
     for (int64_t n = 1; n <= 64 && n <= tiles; ++n) {

@@ -1,26 +1,33 @@
 // The tensor-memory kernel of topkp_tree_attention (included by attention.cu).
 //
-// One CTA: 128 rows against tiles of 64 tokens.  Warps 0-3 do the softmax, a
-// thread a row (TMEM lane i is row i); warps 4-6 bring keys and values into
-// shared memory; one thread of warp 7 issues the matrix instructions (eight
-// warps in all, so that two CTAs leave 128 registers a thread):
+// One CTA: NT tiles of 128 rows against tiles of 64 tokens.  Warps 0 .. 4 NT - 1
+// do the softmax, a thread a row (TMEM lane i is row i of its tile); the next
+// warps bring keys and values into shared memory; one thread of the last warp
+// issues the matrix instructions:
 //   S = Q K^T   both operands in shared memory, K-major, 128-byte swizzle
 //   O += P V    P in TMEM over its S, V in shared memory as it lies (tokens
 //               by dims), read with the dims as the major direction
 // S is double-buffered, so the product of tile j + 1 runs under the softmax
-// of tile j, and two CTAs share an SM, so one's products run under the
-// other's softmax.  O stays in TMEM; a row's reference maximum moves only
-// when a tile's maximum exceeds it by 2^8, which spares the rescaling of O
-// but for the first few tiles (probabilities up to 2^8 lose nothing in
-// floating point).
+// of tile j.  Up to 128 rows, two CTAs share an SM (eight warps each leave
+// 128 registers a thread), and one's products run under the other's softmax;
+// beyond, one CTA takes 256 rows, so that keys and values are brought (and
+// widened from e4m3) once for both tiles.  O stays in TMEM; a row's reference
+// maximum moves only when a tile's maximum exceeds it by 2^8, which spares
+// the rescaling of O but for the first few tiles (probabilities up to 2^8
+// lose nothing in floating point).
+//
+// Keys and values come by TMA, a box of tokens that lie in one page at a
+// time; in 16 bits straight into the swizzled operands (the last, ragged tile
+// by plain copies that zero what no token fills), as e4m3 into a raw ring
+// that the feeder warps widen from: sixteen values a thread, by shifts and
+// two exact products with powers of two.  Layouts TMA cannot take (pages of a
+// size that is no multiple of 8, e4m3 rows off 16 bytes) are copied plainly.
 #pragma once
 
 namespace topkp {
 namespace {
 
 constexpr int kTcRows = 128;
-constexpr int kTcThreads = 256;
-constexpr int kTcFeeders = 96;  // threads that bring keys and values
 constexpr float kSlack = 8.0f;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
@@ -99,14 +106,32 @@ __device__ __forceinline__ uint32_t swizzled(int r, int c) {
 
 __device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull; }
 
-template <int DP>
+template <int DP, int NT, bool Q8>
 struct TcShape {
-  static constexpr int kStages = DP == 64 ? 4 : 2;
-  static constexpr int kQBytes = kTcRows * DP * 2;
+  static constexpr int kSoftWarps = 4 * NT;
+  static constexpr int kFeedWarps = Q8 ? 7 : 3;
+  static constexpr int kThreads = 32 * (kSoftWarps + kFeedWarps + 1);
+  static constexpr int kPerSm = !Q8 && NT == 1 && DP <= 128 ? 2 : 1;
   static constexpr int kTileBytes = kTile * DP * 2;
-  static constexpr int kColumns = DP == 256 ? 512 : 256;  // TMEM: two S of 64, O of DP
-  static constexpr size_t kSmem = 1024 + kQBytes + (size_t)kStages * 2 * kTileBytes;
+  static constexpr int kQBytes = NT * kTcRows * DP * 2;
+  // operand stages (keys and values each) and raw stages
+  static constexpr int kStages = Q8 ? (NT == 1 && DP <= 128 ? 3 : 2) : DP == 64 ? 4 : DP == 128 && NT == 2 ? 4 : 2;
+  static constexpr int kRaw = !Q8 ? 0 : DP == 256 ? 1 : 4;
+  static constexpr int kRawBytes = 2 * kTile * DP;  // keys, then values
+  static constexpr uint32_t kO = NT * 128;          // TMEM: two S of 64 columns a row tile, then the O of DP
+  static constexpr int kColumns = kO + NT * DP <= 256 ? 256 : 512;
+  static constexpr size_t kSmem = 1024 + kQBytes + (size_t)kStages * 2 * kTileBytes + (size_t)kRaw * kRawBytes;
+  static_assert(kO + NT * DP <= 512, "O does not fit tensor memory");
 };
+
+// A box of tokens of one page: element x, head, token and page.
+__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int head, int token, int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(head), "r"(token), "r"(page)
+      : "memory");
+}
 
 // A bounded wait; once one has given up, none of the CTA waits any more.
 __device__ __forceinline__ void tc_wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
@@ -168,16 +193,20 @@ __device__ __forceinline__ uint4 fetch16(const uint8_t* p, int wide, bool both) 
   return make_uint4(lo.x, lo.y, hi.x, hi.y);
 }
 
-template <int DP, bool BF, bool Q8>
-__global__ void __launch_bounds__(kTcThreads, DP == 256 ? 1 : 2) attn_tc(const __grid_constant__ AttnDev p) {
-  using Shape = TcShape<DP>;
+template <int DP, int NT, bool BF, bool Q8>
+__global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT, Q8>::kPerSm)
+    attn_tc(const __grid_constant__ AttnDev p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  using Shape = TcShape<DP, NT, Q8>;
   constexpr int ST = Shape::kStages;
+  constexpr int RS = Shape::kRaw > 0 ? Shape::kRaw : 1;
+  constexpr int kFeed = Shape::kFeedWarps;
   extern __shared__ unsigned char tc_smem[];
   unsigned char* smem = tc_smem + ((1024 - (smem_u32(tc_smem) & 1023)) & 1023);
   unsigned char* sq = smem;
   unsigned char* sk = smem + Shape::kQBytes;  // ST keys, then ST values
   unsigned char* sv = sk + ST * Shape::kTileBytes;
-  __shared__ uint64_t full[ST], empty[ST], s_full[2], p_full[2], pv_done, q_full;
+  unsigned char* raw = sv + ST * Shape::kTileBytes;
+  __shared__ uint64_t full[ST], empty[ST], raw_full[RS], raw_empty[RS], s_full[NT][2], p_full[NT][2], pv_done[NT], q_full;
   __shared__ uint32_t tmem_base;
   __shared__ volatile int dead;
   const topkp_tree_attention_args& a = p.a;
@@ -187,7 +216,7 @@ __global__ void __launch_bounds__(kTcThreads, DP == 256 ? 1 : 2) attn_tc(const _
   const int64_t bh = blockIdx.z;
   const int64_t b = bh / a.Hkv;
   const int h = (int)(bh - b * a.Hkv);
-  const int row0 = blockIdx.x * kTcRows;
+  const int row0 = blockIdx.x * (NT * kTcRows);
   const int split = blockIdx.y;
   int ctx, len, nodes;
   request_span(a, b, &ctx, &len, &nodes);
@@ -197,19 +226,25 @@ __global__ void __launch_bounds__(kTcThreads, DP == 256 ? 1 : 2) attn_tc(const _
 
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
-      mbar_init(&full[i], kTcFeeders);
+      mbar_init(&full[i], kFeed);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
+    for (int i = 0; i < RS; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], kFeed);
     }
-    mbar_init(&pv_done, 1);
-    mbar_init(&q_full, 128);
+    for (int t = 0; t < NT; ++t) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&s_full[t][i], 1);
+        mbar_init(&p_full[t][i], 128);
+      }
+      mbar_init(&pv_done[t], 1);
+    }
+    mbar_init(&q_full, NT * 128);
     fence_mbar_init();
     dead = 0;
   }
-  if (warp == 7) {
+  if (warp == Shape::kSoftWarps + kFeed) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)),
                  "n"(Shape::kColumns)
                  : "memory");
@@ -219,10 +254,10 @@ __global__ void __launch_bounds__(kTcThreads, DP == 256 ? 1 : 2) attn_tc(const _
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = tmem_base;
-  constexpr uint32_t kO = 128;  // first column of O
 
-  if (warp < 4) {
+  if (warp < Shape::kSoftWarps) {
     // ---- softmax: thread = row ----
+    const int tile = NT == 1 ? 0 : warp >> 2;
     const int r = row0 + tid;
     const int node = r / G;
     const int hq = h * G + (r - node * G);
@@ -234,7 +269,7 @@ __global__ void __launch_bounds__(kTcThreads, DP == 256 ? 1 : 2) attn_tc(const _
 #pragma unroll 4
       for (int c = 0; c < DP / 8; ++c) {
         const uint4 v = in && c * 8 < a.D ? *reinterpret_cast<const uint4*>(qr + c * 8) : make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(sq + swizzled<kTcRows>(tid, c)) = v;
+        *reinterpret_cast<uint4*>(sq + tile * (kTcRows * DP * 2) + swizzled<kTcRows>(tid & 127, c)) = v;
       }
       fence_proxy_async_shared();
       mbar_arrive(&q_full);
@@ -246,15 +281,17 @@ __global__ void __launch_bounds__(kTcThreads, DP == 256 ? 1 : 2) attn_tc(const _
     const bool idle = row0 + warp * 32 >= rows;  // the whole warp
     const float sc0 = a.scale * kLog2e;
     const float sc = sc0 > 0.0f ? sc0 : 1.0f;  // a scale of zero or less is applied to the products first
-    const uint32_t lanes = tm + ((uint32_t)(warp * 32) << 16);
+    const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t ocol = lanes + Shape::kO + tile * DP;
     float m = -INFINITY, l = 0.0f;
     for (int j = 0; j < n; ++j) {
-      const uint32_t sb = lanes + (j & 1) * 64;
-      tc_wait(&s_full[j & 1], (j >> 1) & 1, &dead);
+      const uint32_t sb = lanes + tile * 128 + (j & 1) * 64;
+      tc_wait(&s_full[tile][j & 1], (j >> 1) & 1, &dead);
       if (idle) {
-        mbar_arrive(&p_full[j & 1]);
+        mbar_arrive(&p_full[tile][j & 1]);
         continue;
       }
+      __syncwarp();
       tc_fence_after();
       uint32_t s0[32], s1[32];
       tc_ld32(s0, sb);
@@ -296,16 +333,17 @@ __global__ void __launch_bounds__(kTcThreads, DP == 256 ? 1 : 2) attn_tc(const _
             m = top;
             l *= f;
           }
-          tc_wait(&pv_done, (j - 1) & 1, &dead);
+          tc_wait(&pv_done[tile], (j - 1) & 1, &dead);
+          __syncwarp();
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < DP; c += 16) {
             uint32_t o[16];
-            tc_ld16(o, lanes + kO + c);
+            tc_ld16(o, ocol + c);
             tc_wait_ld();
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tc_st16(lanes + kO + c, o);
+            tc_st16(ocol + c, o);
           }
         }
       }
@@ -327,10 +365,13 @@ __global__ void __launch_bounds__(kTcThreads, DP == 256 ? 1 : 2) attn_tc(const _
       tc_st32(sb, pk);
       tc_wait_st();
       tc_fence_before();
-      mbar_arrive(&p_full[j & 1]);
+      mbar_arrive(&p_full[tile][j & 1]);
     }
     if (n > 0) {
-      tc_wait(&pv_done, (n - 1) & 1, &dead);
+      // the last S says that product n - 3 is done: one phase at a time from there
+      if (n > 1) tc_wait(&pv_done[tile], (n - 2) & 1, &dead);
+      tc_wait(&pv_done[tile], (n - 1) & 1, &dead);
+      __syncwarp();
       tc_fence_after();
     }
     const int64_t all_rows = a.B * a.T * a.Hq;
@@ -343,7 +384,7 @@ __global__ void __launch_bounds__(kTcThreads, DP == 256 ? 1 : 2) attn_tc(const _
     for (int c = 0; c < DP; c += 32) {
       uint32_t o[32];
       if (n > 0) {
-        tc_ld32(o, lanes + kO + c);
+        tc_ld32(o, ocol + c);
         tc_wait_ld();
       }
 #pragma unroll
@@ -375,49 +416,80 @@ __global__ void __launch_bounds__(kTcThreads, DP == 256 ? 1 : 2) attn_tc(const _
       else if (a.lse) a.lse[row] = lse;
     }
     tc_fence_before();
-  } else if (warp < 7) {
+  } else if (warp < Shape::kSoftWarps + kFeed) {
     // ---- keys and values ----
-    const int pt = tid - 128;
+    const int pt = tid - 32 * Shape::kSoftWarps, feeder = warp - Shape::kSoftWarps;
     const int32_t* table = a.table ? a.table + b * a.ld_table : nullptr;
     constexpr int CH = Q8 ? DP / 16 : DP / 8;  // 16-byte pieces of a cached row
-    constexpr int STEP = kTcFeeders / CH;      // rows between a thread's rows
+    constexpr int STEP = 32 * kFeed / CH;      // rows between a thread's rows
     constexpr int NR = (kTile + STEP - 1) / STEP;
     const int c = pt % CH, r0 = pt / CH;
     const bool c_in = c * (Q8 ? 16 : 8) < a.D;
-    auto mine = [&](int i) { return NR * STEP == kTile || r0 + i * STEP < kTile; };
-    // the page and place of token t, page -1 if there is none to read
+    auto mine = [&](int i) { return r0 < STEP && r0 + i * STEP < kTile; };
+    // the page and place of token t; the page is outside the pool if there is none
+    auto place = [&](int t, int& page, int& at) {
+      page = (int)b;
+      at = t;
+      if (table) {
+        const int pg = p.page_mul ? (int)(__umulhi((uint32_t)t, p.page_mul) >> p.page_shift) : t / (int)a.page_size;
+        at = t - pg * (int)a.page_size;
+        page = table[pg];
+      }
+    };
+    // the same of a token that this thread reads itself; page -1: nothing to read
     auto find = [&](int t, int& page, int& at) {
       page = -1;
-      at = t;
-      if (t < len && c_in) {
-        page = (int)b;
-        if (table) {
-          const int pg = p.page_mul ? (int)(__umulhi((uint32_t)t, p.page_mul) >> p.page_shift) : t / (int)a.page_size;
-          at = t - pg * (int)a.page_size;
-          page = table[pg];
-          if (page < 0 || page >= a.pages) page = -1;
-        }
+      at = 0;
+      if (t < len) {
+        place(t, page, at);
+        if (page < 0 || page >= a.pages) page = -1;
       }
+    };
+    // boxes of one tile by the lanes of a warp; every token of them is below max_pages * page_size
+    const int per_tile = p.box ? kTile / p.box : 0;
+    auto boxes = [&](unsigned char* kd, unsigned char* vd, uint64_t* bar, int tile) {
+      constexpr int BLOCKS = Q8 ? 1 : DP / 64;
+      constexpr int ROW = Q8 ? DP : 128;  // bytes of a box's row in shared memory
+      if (lane == 0) mbar_arrive_expect_tx(bar, 2 * kTile * DP * (Q8 ? 1 : 2));
+      __syncwarp();
+      for (int i = lane; i < per_tile * BLOCKS; i += 32) {
+        const int blk = i / per_tile, piece = i - blk * per_tile;
+        const int t = tile * kTile + piece * p.box;
+        int page = -1, at = 0;
+        if (t < len) place(t, page, at);
+        const int o = blk * (kTile * 128) + piece * p.box * ROW;
+        tma_box(kd + o, &kmap, bar, blk * 64, h, at, page);
+        tma_box(vd + o, &vmap, bar, blk * 64, h, at, page);
+      }
+    };
+    auto hand_over = [&](int st) {  // this warp's part of a stage, written by plain stores
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[st]);
     };
     if constexpr (!Q8) {
       const uint16_t* kb = reinterpret_cast<const uint16_t*>(a.k.data) + h * a.k.head_stride + c * 8;
       const uint16_t* vb = reinterpret_cast<const uint16_t*>(a.v.data) + h * a.v.head_stride + c * 8;
       const uint32_t ks = smem_u32(sk), vs = smem_u32(sv);
-      int told = 0;  // tiles handed over
-      auto tell = [&](int upto) {
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_proxy_async_shared();
-        for (; told < upto; ++told) mbar_arrive(&full[told % ST]);
-      };
       for (int j = 0; j < n; ++j) {
         const int st = j % ST;
+        const bool ragged = (t_begin + j + 1) * kTile > len;
+        if (p.box && !ragged) {
+          // every feeder follows the phases, or a parity would be read too early
+          if (j >= ST) tc_wait(&empty[st], (j / ST - 1) & 1, &dead);
+          if (feeder > 0) continue;
+          if (lane == 0)
+            for (int i = 1; i < kFeed; ++i) mbar_arrive(&full[st]);  // for the other warps
+          boxes(sk + st * Shape::kTileBytes, sv + st * Shape::kTileBytes, &full[st], t_begin + j);
+          continue;
+        }
         int page[NR], at[NR];
 #pragma unroll
-        for (int i = 0; i < NR; ++i) find((t_begin + j) * kTile + r0 + i * STEP, page[i], at[i]);
-        if (j >= ST) {
-          tell(j);  // before waiting for room: what is there may be what makes it
-          tc_wait(&empty[st], (j / ST - 1) & 1, &dead);
+        for (int i = 0; i < NR; ++i) {
+          page[i] = -1;
+          if (mine(i) && c_in) find((t_begin + j) * kTile + r0 + i * STEP, page[i], at[i]);
         }
+        if (j >= ST) tc_wait(&empty[st], (j / ST - 1) & 1, &dead);
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
           if (!mine(i)) continue;
@@ -427,34 +499,68 @@ __global__ void __launch_bounds__(kTcThreads, DP == 256 ? 1 : 2) attn_tc(const _
           cp16(ks + off, in ? kb + pg * a.k.page_stride + to * a.k.token_stride : reinterpret_cast<const uint16_t*>(a.k.data), in);
           cp16(vs + off, in ? vb + pg * a.v.page_stride + to * a.v.token_stride : reinterpret_cast<const uint16_t*>(a.v.data), in);
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        hand_over(st);
       }
-      tell(n);
     } else {
       const uint8_t* kb = reinterpret_cast<const uint8_t*>(a.k.data) + h * a.k.head_stride + c * 16;
       const uint8_t* vb = reinterpret_cast<const uint8_t*>(a.v.data) + h * a.v.head_stride + c * 16;
       const uint8_t* ke = a.k.exponents + h * a.k.exp_head_stride;
       const uint8_t* ve = a.v.exponents + h * a.v.exp_head_stride;
-      uint4 kr[NR], vr[NR];
+      // exponents of this thread's rows (0: no token), one tile ahead; without TMA the rows' pages too
       uint32_t ex[NR];
-      auto fetch = [&](int j) {
+      int page[NR], at[NR];
+      auto look = [&](int j) {
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
-          int page, at;
-          find((t_begin + j) * kTile + r0 + i * STEP, page, at);
-          kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
-          ex[i] = 0x7f7f;
-          if (page >= 0 && mine(i)) {
-            const int64_t pg = page, to = at;
-            kr[i] = fetch16(kb + pg * a.k.page_stride + to * a.k.token_stride, p.wide, c * 16 + 8 < a.D);
-            vr[i] = fetch16(vb + pg * a.v.page_stride + to * a.v.token_stride, p.wide, c * 16 + 8 < a.D);
-            ex[i] = (uint32_t)ke[pg * a.k.exp_page_stride + to * a.k.exp_token_stride] |
-                    ((uint32_t)ve[pg * a.v.exp_page_stride + to * a.v.exp_token_stride] << 8);
+          ex[i] = 0;
+          page[i] = -1;
+          if (!mine(i) || !c_in) continue;
+          find((t_begin + j) * kTile + r0 + i * STEP, page[i], at[i]);
+          if (page[i] >= 0) {
+            const int64_t pg = page[i], to = at[i];
+            ex[i] = (uint32_t)__ldg(ke + pg * a.k.exp_page_stride + to * a.k.exp_token_stride) |
+                    ((uint32_t)__ldg(ve + pg * a.v.exp_page_stride + to * a.v.exp_token_stride) << 8);
           }
         }
       };
-      if (n > 0) fetch(0);
+      if (p.box && feeder == 0)
+        for (int j = 0; j < RS && j < n; ++j)
+          boxes(raw + j * Shape::kRawBytes, raw + j * Shape::kRawBytes + kTile * DP, &raw_full[j], t_begin + j);
+      if (n > 0) look(0);
       for (int j = 0; j < n; ++j) {
-        const int st = j % ST;
+        const int st = j % ST, rs = j % RS;
+        uint32_t e[NR];
+        bool in[NR];
+        uint4 kr[NR], vr[NR];
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          e[i] = ex[i];
+          in[i] = page[i] >= 0;
+        }
+        if (p.box) {
+          tc_wait(&raw_full[rs], (j / RS) & 1, &dead);
+          const unsigned char* rk = raw + rs * Shape::kRawBytes;
+#pragma unroll
+          for (int i = 0; i < NR; ++i) {
+            kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
+            if (in[i]) {  // rows past the last token, or of a page outside, are zeros whatever the box held
+              kr[i] = *reinterpret_cast<const uint4*>(rk + (r0 + i * STEP) * DP + c * 16);
+              vr[i] = *reinterpret_cast<const uint4*>(rk + kTile * DP + (r0 + i * STEP) * DP + c * 16);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < NR; ++i) {
+            kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
+            if (in[i]) {
+              const int64_t pg = page[i], to = at[i];
+              kr[i] = fetch16(kb + pg * a.k.page_stride + to * a.k.token_stride, p.wide, c * 16 + 8 < a.D);
+              vr[i] = fetch16(vb + pg * a.v.page_stride + to * a.v.token_stride, p.wide, c * 16 + 8 < a.D);
+            }
+          }
+        }
+        if (j + 1 < n) look(j + 1);
         if (j >= ST) tc_wait(&empty[st], (j / ST - 1) & 1, &dead);
         unsigned char* kd = sk + st * Shape::kTileBytes;
         unsigned char* vd = sv + st * Shape::kTileBytes;
@@ -463,16 +569,21 @@ __global__ void __launch_bounds__(kTcThreads, DP == 256 ? 1 : 2) attn_tc(const _
           const int r = r0 + i * STEP;
           if (!mine(i)) continue;
           uint4 lo, hi;
-          widen16<BF>(kr[i], ex[i] & 0xff, lo, hi);
+          widen16<BF>(kr[i], e[i] & 0xff, lo, hi);
           *reinterpret_cast<uint4*>(kd + swizzled<kTile>(r, 2 * c)) = lo;
           *reinterpret_cast<uint4*>(kd + swizzled<kTile>(r, 2 * c + 1)) = hi;
-          widen16<BF>(vr[i], ex[i] >> 8, lo, hi);
+          widen16<BF>(vr[i], e[i] >> 8, lo, hi);
           *reinterpret_cast<uint4*>(vd + swizzled<kTile>(r, 2 * c)) = lo;
           *reinterpret_cast<uint4*>(vd + swizzled<kTile>(r, 2 * c + 1)) = hi;
         }
-        if (j + 1 < n) fetch(j + 1);
-        fence_proxy_async_shared();
-        mbar_arrive(&full[st]);
+        hand_over(st);
+        if (p.box) {
+          if (lane == 0) mbar_arrive(&raw_empty[rs]);
+          if (feeder == 0 && j + RS < n) {
+            tc_wait(&raw_empty[rs], (j / RS) & 1, &dead);
+            boxes(raw + rs * Shape::kRawBytes, raw + rs * Shape::kRawBytes + kTile * DP, &raw_full[rs], t_begin + j + RS);
+          }
+        }
       }
     }
   } else if (lane == 0) {
@@ -482,43 +593,49 @@ __global__ void __launch_bounds__(kTcThreads, DP == 256 ? 1 : 2) attn_tc(const _
     constexpr uint32_t i_qk = common | ((uint32_t)(kTile / 8) << 17);
     constexpr uint32_t i_pv = common | (1u << 16) | ((uint32_t)(DP / 8) << 17);
     const uint32_t q0 = smem_u32(sq), k0 = smem_u32(sk), v0 = smem_u32(sv);
-    auto product_s = [&](int j) {
-      tc_wait(&full[j % ST], (j / ST) & 1, &dead);
-      tc_fence_after();
+    auto product_s = [&](int t, int j) {
 #pragma unroll
       for (int kk = 0; kk < DP / 16; ++kk)
-        tc_mma_ss(tm + (j & 1) * 64, operand(q0 + (kk / 4) * (kTcRows * 128) + (kk % 4) * 32, 16, 1024),
+        tc_mma_ss(tm + t * 128 + (j & 1) * 64, operand(q0 + t * (kTcRows * DP * 2) + (kk / 4) * (kTcRows * 128) + (kk % 4) * 32, 16, 1024),
                   operand(k0 + (j % ST) * Shape::kTileBytes + (kk / 4) * (kTile * 128) + (kk % 4) * 32, 16, 1024), i_qk, kk > 0);
-      tc_commit(&s_full[j & 1]);
+      tc_commit(&s_full[t][j & 1]);
     };
     if (n > 0) {
       tc_wait(&q_full, 0, &dead);
-      product_s(0);
+      tc_wait(&full[0], 0, &dead);
+      tc_fence_after();
+      for (int t = 0; t < NT; ++t) product_s(t, 0);
     }
     for (int j = 0; j < n; ++j) {
       if (j + 1 < n) {
-        // the other S still holds P of tile j - 1 until its product is done
-        if (j > 0) tc_wait(&pv_done, (j - 1) & 1, &dead);
-        product_s(j + 1);
+        tc_wait(&full[(j + 1) % ST], ((j + 1) / ST) & 1, &dead);
+        for (int t = 0; t < NT; ++t) {
+          // the other S still holds P of tile j - 1 until its product is done
+          if (j > 0) tc_wait(&pv_done[t], (j - 1) & 1, &dead);
+          tc_fence_after();
+          product_s(t, j + 1);
+        }
       }
-      tc_wait(&p_full[j & 1], (j >> 1) & 1, &dead);
-      tc_fence_after();
+      for (int t = 0; t < NT; ++t) {
+        tc_wait(&p_full[t][j & 1], (j >> 1) & 1, &dead);
+        tc_fence_after();
 #pragma unroll
-      for (int kk = 0; kk < kTile / 16; ++kk)
-        tc_mma_ts(tm + kO, tm + (j & 1) * 64 + kk * 8,
-                  operand(v0 + (j % ST) * Shape::kTileBytes + kk * 2048, kTile * 128, 1024), i_pv, j > 0 || kk > 0);
-      tc_commit(&empty[j % ST]);
-      tc_commit(&pv_done);
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          tc_mma_ts(tm + Shape::kO + t * DP, tm + t * 128 + (j & 1) * 64 + kk * 8,
+                    operand(v0 + (j % ST) * Shape::kTileBytes + kk * 2048, kTile * 128, 1024), i_pv, j > 0 || kk > 0);
+        if (t == NT - 1) tc_commit(&empty[j % ST]);
+        tc_commit(&pv_done[t]);
+      }
     }
     tc_fence_before();
   }
   __syncwarp();
   __syncthreads();
-  if (dead) {  // products may still be in flight: time for them to end
+  if (dead) {  // products and copies may still be in flight: time for them to end
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < 10000000ull) __nanosleep(1000);
   }
-  if (warp == 7) {
+  if (warp == Shape::kSoftWarps + kFeed) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(Shape::kColumns) : "memory");
   }

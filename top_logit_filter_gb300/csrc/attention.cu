@@ -21,6 +21,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 struct AttnDev {
   topkp_tree_attention_args a;
   int splits;
+  int per;        // tiles of a part; the last part takes what is left
   float* part_o;  // [splits][B * T * Hq][D]
   float* part_l;  // [splits][B * T * Hq]
   uint32_t page_mul;  // reciprocal of page_size below 2^31, 0: divide
@@ -125,8 +126,8 @@ __global__ void __launch_bounds__(kMmaThreads) attn_mma(const __grid_constant__ 
   int ctx, len, nodes;
   request_span(a, b, &ctx, &len, &nodes);
   const int tiles = (len + kTile - 1) / kTile;
-  const int per = (tiles + p.splits - 1) / p.splits;
-  const int t_begin = min(split * per, tiles), t_end = min(t_begin + per, tiles);
+  const int t_begin = min(split * p.per, tiles);
+  const int t_end = split == p.splits - 1 ? tiles : min(t_begin + p.per, tiles);
 
   // the two rows of this thread (lane / 4 and that plus 8)
   int node[2];
@@ -485,20 +486,28 @@ AttnPlan plan_attention(const topkp_tree_attention_args& a, int num_sms) {
   const int64_t len = (a.max_context < cap ? (a.max_context > 0 ? a.max_context : 0) : cap) + a.T;
   const int64_t tiles = (len + kTile - 1) / kTile;
   if (on_tensor_cores(a)) {
-    // the number of parts with the least rounds of CTAs times tiles of each
-    // (and four tiles' time for a CTA's start and end)
+    // Parts of equal size, whatever a request's length, so that the CTAs of
+    // ragged requests even out.  In units of a tile's time: the work over the
+    // slots, half a part as the last round's loss, and writing and reading
+    // the partial outputs (a tile is 64 keys and values).
     const int64_t nt = row_tiles(a);
-    const int64_t slots = (a.D > 128 || nt == 2 || a.k.dtype == TOPKP_E4M3 ? 1LL : 2LL) * num_sms;
-    const int64_t base = a.B * a.Hkv * ((rows + nt * kTcRows - 1) / (nt * kTcRows));
-    int64_t best = -1;
+    const double slots = (a.D > 128 || nt == 2 || a.k.dtype == TOPKP_E4M3 ? 1.0 : 2.0) * num_sms;
+    const double base = (double)(a.B * a.Hkv * ((rows + nt * kTcRows - 1) / (nt * kTcRows)));
+    const double join = (double)(a.B * a.T * a.Hq) * 8.0 / (slots * kTile * 2 * (a.k.dtype == TOPKP_E4M3 ? 1 : 2));
+    double best = -1.0;
     p.splits = 1;
-    for (int64_t n = 1; n <= 64 && n <= tiles; ++n) {
+    p.per = (int)tiles;
+    for (int64_t n = 1; n <= 128 && n <= tiles; ++n) {
       const int64_t per = (tiles + n - 1) / n;
       if ((tiles + per - 1) / per != n) continue;
-      const int64_t cost = (base * n + slots - 1) / slots * (per + 4) + (n > 1 ? 2 : 0);
+      const double part = (double)per + 4.0;
+      double cost = base * n / slots * part + part / 2;
+      if (cost < part) cost = part;
+      if (n > 1) cost += 3.0 + join * n;
       if (best < 0 || cost < best) {
         best = cost;
         p.splits = (int)n;
+        p.per = (int)per;
       }
     }
     p.part_bytes = p.splits > 1 ? (size_t)p.splits * (size_t)(a.B * a.T * a.Hq) * (a.D + 1) * sizeof(float) : 0;
@@ -508,7 +517,9 @@ AttnPlan plan_attention(const topkp_tree_attention_args& a, int num_sms) {
   if (splits > (tiles + 1) / 2) splits = (tiles + 1) / 2;
   if (splits < 1) splits = 1;
   if (splits > 256) splits = 256;
-  p.splits = (int)splits;
+  p.per = (int)((tiles + splits - 1) / splits);
+  p.splits = (int)((tiles + p.per - 1) / p.per);
+  splits = p.splits;
   const size_t all = (size_t)(a.B * a.T * a.Hq);
   p.part_bytes = splits > 1 ? (size_t)splits * all * (a.D + 1) * sizeof(float) : 0;
   return p;
@@ -518,6 +529,7 @@ cudaError_t launch_attention(const topkp_tree_attention_args& a, const AttnPlan&
   AttnDev p;
   p.a = a;
   p.splits = plan.splits;
+  p.per = plan.per;
   const size_t all = (size_t)(a.B * a.T * a.Hq);
   p.part_o = reinterpret_cast<float*>(a.workspace);
   p.part_l = p.part_o + (plan.splits > 1 ? (size_t)plan.splits * all * a.D : 0);

@@ -109,18 +109,20 @@ __device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0ull : n >
 template <int DP, int NT, bool Q8>
 struct TcShape {
   static constexpr int kSoftWarps = 4 * NT;
-  static constexpr int kFeedWarps = Q8 ? 7 : 3;
+  static constexpr int kFeedWarps = Q8 ? 7 : 2;  // 16 bits: one for keys, one for values
   static constexpr int kThreads = 32 * (kSoftWarps + kFeedWarps + 1);
   static constexpr int kPerSm = !Q8 && NT == 1 && DP <= 128 ? 2 : 1;
   static constexpr int kTileBytes = kTile * DP * 2;
   static constexpr int kQBytes = NT * kTcRows * DP * 2;
-  // operand stages (keys and values each) and raw stages
-  static constexpr int kStages = Q8 ? (NT == 1 && DP <= 128 ? 3 : 2) : DP == 64 ? 4 : DP == 128 && NT == 2 ? 4 : 2;
-  static constexpr int kRaw = !Q8 ? 0 : DP == 256 ? 1 : 4;
+  // stages of keys, of values, and of raw e4m3 (both).  Keys free theirs as
+  // soon as their product is done, well before the softmax
+  static constexpr int kKeys = Q8 ? (NT == 1 && DP <= 128 ? 3 : 2) : DP == 64 || (DP == 128 && NT == 2) ? 4 : 2;
+  static constexpr int kValues = Q8 && DP == 256 ? 1 : kKeys;
+  static constexpr int kRaw = !Q8 ? 0 : DP == 256 ? 2 : 4;
   static constexpr int kRawBytes = 2 * kTile * DP;  // keys, then values
   static constexpr uint32_t kO = NT * 128;          // TMEM: two S of 64 columns a row tile, then the O of DP
   static constexpr int kColumns = kO + NT * DP <= 256 ? 256 : 512;
-  static constexpr size_t kSmem = 1024 + kQBytes + (size_t)kStages * 2 * kTileBytes + (size_t)kRaw * kRawBytes;
+  static constexpr size_t kSmem = 1024 + kQBytes + (size_t)(kKeys + kValues) * kTileBytes + (size_t)kRaw * kRawBytes;
   static_assert(kO + NT * DP <= 512, "O does not fit tensor memory");
 };
 
@@ -149,10 +151,9 @@ __device__ __forceinline__ void tc_wait(uint64_t* bar, uint32_t parity, volatile
 
 // Two e4m3 in the high bytes of the halves of t as bf16: sign, then exponent
 // and mantissa four bits down, which reads as the value times 2^-120,
-// subnormals too.  Scaled back exactly by powers of two.
+// subnormals too.  `scale` brings it back, exactly.
 __device__ __forceinline__ uint32_t e4m3_to_bf16x2(uint32_t t, uint32_t scale) {
   uint32_t r = (t & 0x80008000u) | ((t >> 4) & 0x07f007f0u);
-  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(0x7b807b80u));  // 2^120
   asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(scale));
   return r;
 }
@@ -165,9 +166,9 @@ __device__ __forceinline__ void widen16(const uint4& w, uint32_t e, uint4& lo, u
   uint32_t nan = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) nan |= (in[i] & 0x7f7f7f7fu) + 0x01010101u;
-  if (BF && !(nan & 0x80808080u)) {
-    // e = 0 does not occur in a written cache; it reads as 2^-126
-    const uint32_t sc = (e ? e : 1u) << 7, s2 = sc | (sc << 16);
+  // 2^120 times the scale is a bf16 up to a scale of 2^7 (rows up to 57344)
+  if (BF && !(nan & 0x80808080u) && e <= 134) {
+    const uint32_t sc = (e + 120) << 7, s2 = sc | (sc << 16);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       r[2 * i] = e4m3_to_bf16x2(__byte_perm(in[i], 0u, 0x1404), s2);
@@ -197,17 +198,17 @@ template <int DP, int NT, bool BF, bool Q8>
 __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT, Q8>::kPerSm)
     attn_tc(const __grid_constant__ AttnDev p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using Shape = TcShape<DP, NT, Q8>;
-  constexpr int ST = Shape::kStages;
+  constexpr int KS = Shape::kKeys, VS = Shape::kValues;
   constexpr int RS = Shape::kRaw > 0 ? Shape::kRaw : 1;
   constexpr int kFeed = Shape::kFeedWarps;
   extern __shared__ unsigned char tc_smem[];
   unsigned char* smem = tc_smem + ((1024 - (smem_u32(tc_smem) & 1023)) & 1023);
   unsigned char* sq = smem;
-  unsigned char* sk = smem + Shape::kQBytes;  // ST keys, then ST values
-  unsigned char* sv = sk + ST * Shape::kTileBytes;
-  unsigned char* raw = sv + ST * Shape::kTileBytes;
-  __shared__ uint64_t full[ST], empty[ST], raw_full[RS], raw_empty[RS], s_full[NT][2], p_full[NT][2], pv_done[NT], q_full;
-  __shared__ uint32_t tmem_base;
+  unsigned char* sk = smem + Shape::kQBytes;
+  unsigned char* sv = sk + KS * Shape::kTileBytes;
+  unsigned char* raw = sv + VS * Shape::kTileBytes;
+  __shared__ uint64_t k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], raw_full[RS], raw_empty[RS], s_full[NT][2], p_full[NT][2], pv_done[NT], q_full;
+  __shared__ uint32_t tmem_base, sexp[RS][kTile];
   __shared__ volatile int dead;
   const topkp_tree_attention_args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -221,17 +222,22 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
   int ctx, len, nodes;
   request_span(a, b, &ctx, &len, &nodes);
   const int tiles = (len + kTile - 1) / kTile;
-  const int per = (tiles + p.splits - 1) / p.splits;
-  const int t_begin = min(split * per, tiles), n = min(t_begin + per, tiles) - t_begin;
+  const int t_begin = min(split * p.per, tiles);
+  const int n = (split == p.splits - 1 ? tiles : min(t_begin + p.per, tiles)) - t_begin;
 
   if (tid == 0) {
-    for (int i = 0; i < ST; ++i) {
-      mbar_init(&full[i], kFeed);
-      mbar_init(&empty[i], 1);
+    constexpr int kParts = Q8 ? kFeed - 1 : 1;  // warps that fill a stage
+    for (int i = 0; i < KS; ++i) {
+      mbar_init(&k_full[i], kParts);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < VS; ++i) {
+      mbar_init(&v_full[i], kParts);
+      mbar_init(&v_empty[i], 1);
     }
     for (int i = 0; i < RS; ++i) {
       mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], kFeed);
+      mbar_init(&raw_empty[i], kFeed - 1);
     }
     for (int t = 0; t < NT; ++t) {
       for (int i = 0; i < 2; ++i) {
@@ -418,15 +424,9 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
     tc_fence_before();
   } else if (warp < Shape::kSoftWarps + kFeed) {
     // ---- keys and values ----
-    const int pt = tid - 32 * Shape::kSoftWarps, feeder = warp - Shape::kSoftWarps;
+    const int feeder = warp - Shape::kSoftWarps;
     const int32_t* table = a.table ? a.table + b * a.ld_table : nullptr;
-    constexpr int CH = Q8 ? DP / 16 : DP / 8;  // 16-byte pieces of a cached row
-    constexpr int STEP = 32 * kFeed / CH;      // rows between a thread's rows
-    constexpr int NR = (kTile + STEP - 1) / STEP;
-    const int c = pt % CH, r0 = pt / CH;
-    const bool c_in = c * (Q8 ? 16 : 8) < a.D;
-    auto mine = [&](int i) { return r0 < STEP && r0 + i * STEP < kTile; };
-    // the page and place of token t; the page is outside the pool if there is none
+    // the page and place of token t; the page may lie outside the pool
     auto place = [&](int t, int& page, int& at) {
       page = (int)b;
       at = t;
@@ -445,143 +445,147 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
         if (page < 0 || page >= a.pages) page = -1;
       }
     };
-    // boxes of one tile by the lanes of a warp; every token of them is below max_pages * page_size
-    const int per_tile = p.box ? kTile / p.box : 0;
-    auto boxes = [&](unsigned char* kd, unsigned char* vd, uint64_t* bar, int tile) {
-      constexpr int BLOCKS = Q8 ? 1 : DP / 64;
-      constexpr int ROW = Q8 ? DP : 128;  // bytes of a box's row in shared memory
-      if (lane == 0) mbar_arrive_expect_tx(bar, 2 * kTile * DP * (Q8 ? 1 : 2));
-      __syncwarp();
-      for (int i = lane; i < per_tile * BLOCKS; i += 32) {
-        const int blk = i / per_tile, piece = i - blk * per_tile;
-        const int t = tile * kTile + piece * p.box;
-        int page = -1, at = 0;
-        if (t < len) place(t, page, at);
-        const int o = blk * (kTile * 128) + piece * p.box * ROW;
-        tma_box(kd + o, &kmap, bar, blk * 64, h, at, page);
-        tma_box(vd + o, &vmap, bar, blk * 64, h, at, page);
-      }
-    };
-    auto hand_over = [&](int st) {  // this warp's part of a stage, written by plain stores
+    auto hand_over = [&](uint64_t* bar) {  // this warp's part of a stage, written by plain stores
       fence_proxy_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&full[st]);
+      if (lane == 0) mbar_arrive(bar);
     };
+    const int per_tile = p.box ? kTile / p.box : 0;  // boxes of a tile (and of each 64 dims in 16 bits)
     if constexpr (!Q8) {
-      const uint16_t* kb = reinterpret_cast<const uint16_t*>(a.k.data) + h * a.k.head_stride + c * 8;
-      const uint16_t* vb = reinterpret_cast<const uint16_t*>(a.v.data) + h * a.v.head_stride + c * 8;
-      const uint32_t ks = smem_u32(sk), vs = smem_u32(sv);
+      // one warp for keys, one for values; a lane a box, its page looked up a tile ahead
+      const topkp_cache& ca = feeder == 0 ? a.k : a.v;
+      const CUtensorMap* map = feeder == 0 ? &kmap : &vmap;
+      unsigned char* ring = feeder == 0 ? sk : sv;
+      uint64_t* full = feeder == 0 ? k_full : v_full;
+      uint64_t* empty = feeder == 0 ? k_empty : v_empty;
+      const int S = feeder == 0 ? KS : VS;
+      const uint16_t* base = reinterpret_cast<const uint16_t*>(ca.data) + h * ca.head_stride;
+      const int blk = per_tile ? lane / per_tile : 0, piece = per_tile ? lane - blk * per_tile : 0;
+      const bool boxed = lane < per_tile * (DP / 64);
+      int page = -1, at = 0;
+      if (boxed && n > 0) place(min(t_begin * kTile + piece * p.box, len - 1), page, at);
+      int st = 0, phase = 1;  // the first round finds every stage empty
       for (int j = 0; j < n; ++j) {
-        const int st = j % ST;
-        const bool ragged = (t_begin + j + 1) * kTile > len;
-        if (p.box && !ragged) {
-          // every feeder follows the phases, or a parity would be read too early
-          if (j >= ST) tc_wait(&empty[st], (j / ST - 1) & 1, &dead);
-          if (feeder > 0) continue;
-          if (lane == 0)
-            for (int i = 1; i < kFeed; ++i) mbar_arrive(&full[st]);  // for the other warps
-          boxes(sk + st * Shape::kTileBytes, sv + st * Shape::kTileBytes, &full[st], t_begin + j);
-          continue;
-        }
-        int page[NR], at[NR];
-#pragma unroll
-        for (int i = 0; i < NR; ++i) {
-          page[i] = -1;
-          if (mine(i) && c_in) find((t_begin + j) * kTile + r0 + i * STEP, page[i], at[i]);
-        }
-        if (j >= ST) tc_wait(&empty[st], (j / ST - 1) & 1, &dead);
-#pragma unroll
-        for (int i = 0; i < NR; ++i) {
-          if (!mine(i)) continue;
-          const bool in = page[i] >= 0;
-          const int64_t pg = in ? page[i] : 0, to = in ? at[i] : 0;
-          const uint32_t off = st * Shape::kTileBytes + swizzled<kTile>(r0 + i * STEP, c);
-          cp16(ks + off, in ? kb + pg * a.k.page_stride + to * a.k.token_stride : reinterpret_cast<const uint16_t*>(a.k.data), in);
-          cp16(vs + off, in ? vb + pg * a.v.page_stride + to * a.v.token_stride : reinterpret_cast<const uint16_t*>(a.v.data), in);
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        hand_over(st);
-      }
-    } else {
-      const uint8_t* kb = reinterpret_cast<const uint8_t*>(a.k.data) + h * a.k.head_stride + c * 16;
-      const uint8_t* vb = reinterpret_cast<const uint8_t*>(a.v.data) + h * a.v.head_stride + c * 16;
-      const uint8_t* ke = a.k.exponents + h * a.k.exp_head_stride;
-      const uint8_t* ve = a.v.exponents + h * a.v.exp_head_stride;
-      // exponents of this thread's rows (0: no token), one tile ahead; without TMA the rows' pages too
-      uint32_t ex[NR];
-      int page[NR], at[NR];
-      auto look = [&](int j) {
-#pragma unroll
-        for (int i = 0; i < NR; ++i) {
-          ex[i] = 0;
-          page[i] = -1;
-          if (!mine(i) || !c_in) continue;
-          find((t_begin + j) * kTile + r0 + i * STEP, page[i], at[i]);
-          if (page[i] >= 0) {
-            const int64_t pg = page[i], to = at[i];
-            ex[i] = (uint32_t)__ldg(ke + pg * a.k.exp_page_stride + to * a.k.exp_token_stride) |
-                    ((uint32_t)__ldg(ve + pg * a.v.exp_page_stride + to * a.v.exp_token_stride) << 8);
-          }
-        }
-      };
-      if (p.box && feeder == 0)
-        for (int j = 0; j < RS && j < n; ++j)
-          boxes(raw + j * Shape::kRawBytes, raw + j * Shape::kRawBytes + kTile * DP, &raw_full[j], t_begin + j);
-      if (n > 0) look(0);
-      for (int j = 0; j < n; ++j) {
-        const int st = j % ST, rs = j % RS;
-        uint32_t e[NR];
-        bool in[NR];
-        uint4 kr[NR], vr[NR];
-#pragma unroll
-        for (int i = 0; i < NR; ++i) {
-          e[i] = ex[i];
-          in[i] = page[i] >= 0;
-        }
-        if (p.box) {
-          tc_wait(&raw_full[rs], (j / RS) & 1, &dead);
-          const unsigned char* rk = raw + rs * Shape::kRawBytes;
-#pragma unroll
-          for (int i = 0; i < NR; ++i) {
-            kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
-            if (in[i]) {  // rows past the last token, or of a page outside, are zeros whatever the box held
-              kr[i] = *reinterpret_cast<const uint4*>(rk + (r0 + i * STEP) * DP + c * 16);
-              vr[i] = *reinterpret_cast<const uint4*>(rk + kTile * DP + (r0 + i * STEP) * DP + c * 16);
-            }
+        unsigned char* dst = ring + st * Shape::kTileBytes;
+        tc_wait(&empty[st], phase, &dead);
+        __syncwarp();
+        if (p.box && (t_begin + j + 1) * kTile <= len) {
+          if (lane == 0) mbar_arrive_expect_tx(&full[st], Shape::kTileBytes);
+          __syncwarp();
+          if (boxed) {
+            tma_box(dst + blk * (kTile * 128) + piece * p.box * 128, map, &full[st], blk * 64, h, at, page);
+            if (j + 1 < n) place(min((t_begin + j + 1) * kTile + piece * p.box, len - 1), page, at);
           }
         } else {
+          // the ragged tile, and layouts TMA cannot take: zeros where no token is
+          constexpr int CH = DP / 8;
+          for (int i = lane; i < kTile * CH; i += 32) {
+            const int r = i / CH, c = i - r * CH;
+            int pg = -1, to = 0;
+            if (c * 8 < a.D) find((t_begin + j) * kTile + r, pg, to);
+            const bool in = pg >= 0;
+            cp16(smem_u32(dst) + swizzled<kTile>(r, c),
+                 in ? base + (int64_t)pg * ca.page_stride + (int64_t)to * ca.token_stride + c * 8 : reinterpret_cast<const uint16_t*>(ca.data), in);
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          hand_over(&full[st]);
+        }
+        if (++st == S) {
+          st = 0;
+          phase ^= 1;
+        }
+      }
+    } else {
+      // The first warp fills the raw ring, exponents too (a fence of a warp
+      // that widens would wait for such loads); the others widen, keys one
+      // tile ahead of values, as the products go.
+      constexpr uint32_t kToken = 1u << 16;  // beside a row's two exponents: there is a token
+      if (feeder == 0) {
+        const uint8_t* ke = a.k.exponents + h * a.k.exp_head_stride;
+        const uint8_t* ve = a.v.exponents + h * a.v.exp_head_stride;
+        const int piece = lane & 15;  // boxes: lanes 0-15 keys, 16-31 values
+        for (int j = 0; j < n; ++j) {
+          const int rs = j % RS, t0 = (t_begin + j) * kTile;
+          uint32_t e[2] = {0, 0};
 #pragma unroll
-          for (int i = 0; i < NR; ++i) {
-            kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
-            if (in[i]) {
-              const int64_t pg = page[i], to = at[i];
-              kr[i] = fetch16(kb + pg * a.k.page_stride + to * a.k.token_stride, p.wide, c * 16 + 8 < a.D);
-              vr[i] = fetch16(vb + pg * a.v.page_stride + to * a.v.token_stride, p.wide, c * 16 + 8 < a.D);
+          for (int i = 0; i < 2; ++i) {
+            int page, at;
+            find(t0 + lane + 32 * i, page, at);
+            if (page >= 0) {
+              const int64_t pg = page, to = at;
+              e[i] = (uint32_t)__ldg(ke + pg * a.k.exp_page_stride + to * a.k.exp_token_stride) |
+                     ((uint32_t)__ldg(ve + pg * a.v.exp_page_stride + to * a.v.exp_token_stride) << 8) | kToken;
             }
           }
+          int page = -1, at = 0;  // past the last token: outside, which reads as zeros
+          const int t = t0 + piece * p.box;
+          if (piece < per_tile && t < len) place(t, page, at);
+          if (j >= RS) tc_wait(&raw_empty[rs], (j / RS - 1) & 1, &dead);
+          __syncwarp();
+          sexp[rs][lane] = e[0];
+          sexp[rs][lane + 32] = e[1];
+          __syncwarp();
+          if (lane == 0) {
+            if (p.box) mbar_arrive_expect_tx(&raw_full[rs], Shape::kRawBytes);
+            else mbar_arrive(&raw_full[rs]);
+          }
+          __syncwarp();
+          if (piece < per_tile)
+            tma_box(raw + rs * Shape::kRawBytes + (lane >> 4) * (kTile * DP) + piece * p.box * DP, lane < 16 ? &kmap : &vmap, &raw_full[rs], 0,
+                    h, at, page);
         }
-        if (j + 1 < n) look(j + 1);
-        if (j >= ST) tc_wait(&empty[st], (j / ST - 1) & 1, &dead);
-        unsigned char* kd = sk + st * Shape::kTileBytes;
-        unsigned char* vd = sv + st * Shape::kTileBytes;
+      } else {
+        const int pt = tid - 32 * (Shape::kSoftWarps + 1);
+        constexpr int CH = DP / 16;                  // 16-byte pieces of a cached row
+        constexpr int STEP = 32 * (kFeed - 1) / CH;  // rows between a thread's rows
+        constexpr int NR = (kTile + STEP - 1) / STEP;
+        const int c = pt % CH, r0 = pt / CH;
+        const bool c_in = c * 16 < a.D;
+        // this thread's pieces of one operand of tile j: widened from the ring or the cache
+        auto widen = [&](int j, bool values, unsigned char* dst) {
+          const topkp_cache& ca = values ? a.v : a.k;
+          const unsigned char* from = raw + (j % RS) * Shape::kRawBytes + (values ? kTile * DP : 0);
+          uint4 w[NR];
+          uint32_t e[NR];
 #pragma unroll
-        for (int i = 0; i < NR; ++i) {
-          const int r = r0 + i * STEP;
-          if (!mine(i)) continue;
-          uint4 lo, hi;
-          widen16<BF>(kr[i], e[i] & 0xff, lo, hi);
-          *reinterpret_cast<uint4*>(kd + swizzled<kTile>(r, 2 * c)) = lo;
-          *reinterpret_cast<uint4*>(kd + swizzled<kTile>(r, 2 * c + 1)) = hi;
-          widen16<BF>(vr[i], e[i] >> 8, lo, hi);
-          *reinterpret_cast<uint4*>(vd + swizzled<kTile>(r, 2 * c)) = lo;
-          *reinterpret_cast<uint4*>(vd + swizzled<kTile>(r, 2 * c + 1)) = hi;
-        }
-        hand_over(st);
-        if (p.box) {
-          if (lane == 0) mbar_arrive(&raw_empty[rs]);
-          if (feeder == 0 && j + RS < n) {
-            tc_wait(&raw_empty[rs], (j / RS) & 1, &dead);
-            boxes(raw + rs * Shape::kRawBytes, raw + rs * Shape::kRawBytes + kTile * DP, &raw_full[rs], t_begin + j + RS);
+          for (int i = 0; i < NR; ++i) {
+            const int r = r0 + i * STEP;
+            e[i] = r < kTile && c_in ? sexp[j % RS][r] : 0;
+            w[i] = make_uint4(0, 0, 0, 0);
+            if (!(e[i] & kToken)) continue;  // zeros whatever the box held
+            if (p.box) {
+              w[i] = *reinterpret_cast<const uint4*>(from + r * DP + c * 16);
+            } else {
+              int page, at;
+              find((t_begin + j) * kTile + r, page, at);
+              w[i] = fetch16(reinterpret_cast<const uint8_t*>(ca.data) + h * ca.head_stride + (int64_t)page * ca.page_stride +
+                                 (int64_t)at * ca.token_stride + c * 16,
+                             p.wide, c * 16 + 8 < a.D);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < NR; ++i) {
+            const int r = r0 + i * STEP;
+            if (r >= kTile) continue;
+            uint4 lo, hi;
+            widen16<BF>(w[i], (values ? e[i] >> 8 : e[i]) & 0xff, lo, hi);
+            *reinterpret_cast<uint4*>(dst + swizzled<kTile>(r, 2 * c)) = lo;
+            *reinterpret_cast<uint4*>(dst + swizzled<kTile>(r, 2 * c + 1)) = hi;
+          }
+        };
+        for (int j = 0; j <= n && n > 0; ++j) {
+          if (j < n) {
+            tc_wait(&raw_full[j % RS], (j / RS) & 1, &dead);
+            if (j >= KS) tc_wait(&k_empty[j % KS], (j / KS - 1) & 1, &dead);
+            widen(j, false, sk + (j % KS) * Shape::kTileBytes);
+            hand_over(&k_full[j % KS]);
+          }
+          if (j > 0) {
+            const int v = j - 1;
+            if (v >= VS) tc_wait(&v_empty[v % VS], (v / VS - 1) & 1, &dead);
+            widen(v, true, sv + (v % VS) * Shape::kTileBytes);
+            hand_over(&v_full[v % VS]);
+            if (lane == 0) mbar_arrive(&raw_empty[v % RS]);
           }
         }
       }
@@ -597,18 +601,19 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
 #pragma unroll
       for (int kk = 0; kk < DP / 16; ++kk)
         tc_mma_ss(tm + t * 128 + (j & 1) * 64, operand(q0 + t * (kTcRows * DP * 2) + (kk / 4) * (kTcRows * 128) + (kk % 4) * 32, 16, 1024),
-                  operand(k0 + (j % ST) * Shape::kTileBytes + (kk / 4) * (kTile * 128) + (kk % 4) * 32, 16, 1024), i_qk, kk > 0);
+                  operand(k0 + (j % KS) * Shape::kTileBytes + (kk / 4) * (kTile * 128) + (kk % 4) * 32, 16, 1024), i_qk, kk > 0);
+      if (t == NT - 1) tc_commit(&k_empty[j % KS]);
       tc_commit(&s_full[t][j & 1]);
     };
     if (n > 0) {
       tc_wait(&q_full, 0, &dead);
-      tc_wait(&full[0], 0, &dead);
+      tc_wait(&k_full[0], 0, &dead);
       tc_fence_after();
       for (int t = 0; t < NT; ++t) product_s(t, 0);
     }
     for (int j = 0; j < n; ++j) {
       if (j + 1 < n) {
-        tc_wait(&full[(j + 1) % ST], ((j + 1) / ST) & 1, &dead);
+        tc_wait(&k_full[(j + 1) % KS], ((j + 1) / KS) & 1, &dead);
         for (int t = 0; t < NT; ++t) {
           // the other S still holds P of tile j - 1 until its product is done
           if (j > 0) tc_wait(&pv_done[t], (j - 1) & 1, &dead);
@@ -618,12 +623,13 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
       }
       for (int t = 0; t < NT; ++t) {
         tc_wait(&p_full[t][j & 1], (j >> 1) & 1, &dead);
+        if (t == 0) tc_wait(&v_full[j % VS], (j / VS) & 1, &dead);
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)
           tc_mma_ts(tm + Shape::kO + t * DP, tm + t * 128 + (j & 1) * 64 + kk * 8,
-                    operand(v0 + (j % ST) * Shape::kTileBytes + kk * 2048, kTile * 128, 1024), i_pv, j > 0 || kk > 0);
-        if (t == NT - 1) tc_commit(&empty[j % ST]);
+                    operand(v0 + (j % VS) * Shape::kTileBytes + kk * 2048, kTile * 128, 1024), i_pv, j > 0 || kk > 0);
+        if (t == NT - 1) tc_commit(&v_empty[j % VS]);
         tc_commit(&pv_done[t]);
       }
     }

@@ -80,6 +80,7 @@ cudaError_t launch_cache_read(topkp_dtype dt, const CacheRowsArgs& a, cudaStream
 // -------------------------------------------------------------- attention
 struct AttnPlan {
   int splits;         // parts of a request's tokens
+  int per;            // tiles of 64 tokens of a part
   size_t part_bytes;  // workspace: partial outputs and their (lse) rows
 };
 AttnPlan plan_attention(const topkp_tree_attention_args& a, int num_sms);

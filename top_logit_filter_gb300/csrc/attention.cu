@@ -7,6 +7,7 @@
 // sum of the softmax; a request's tokens are split over CTAs when there are
 // few rows, and the parts joined by their log-sums.
 #include <cuda.h>
+#include <math.h>
 
 #include "common.cuh"
 #include "decode.h"
@@ -452,7 +453,7 @@ cudaError_t launch_tc(AttnDev p, cudaStream_t s) {
 }
 
 // Tensor memory's 128 rows pay from here on.
-bool on_tensor_cores(const topkp_tree_attention_args& a) { return a.T * (a.Hq / a.Hkv) > 16; }
+bool on_tensor_cores(const topkp_tree_attention_args& a) { return a.T * (a.Hq / a.Hkv) > 0; }
 // Tiles of 128 rows of a CTA (256 dims leave tensor memory for one).
 int row_tiles(const topkp_tree_attention_args& a) { return a.T * (a.Hq / a.Hkv) > kTcRows && a.D <= 128 ? 2 : 1; }
 
@@ -487,13 +488,16 @@ AttnPlan plan_attention(const topkp_tree_attention_args& a, int num_sms) {
   const int64_t tiles = (len + kTile - 1) / kTile;
   if (on_tensor_cores(a)) {
     // Parts of equal size, whatever a request's length, so that the CTAs of
-    // ragged requests even out.  In units of a tile's time: the work over the
-    // slots, half a part as the last round's loss, and writing and reading
-    // the partial outputs (a tile is 64 keys and values).
+    // ragged requests even out.  In units of a tile's time: the rounds of CTAs
+    // (between whole ones, as for equal requests, and what ragged ones average
+    // to), four tiles for a CTA's start and end, and writing and reading the
+    // partial outputs.
     const int64_t nt = row_tiles(a);
     const double slots = (a.D > 128 || nt == 2 || a.k.dtype == TOPKP_E4M3 ? 1.0 : 2.0) * num_sms;
     const double base = (double)(a.B * a.Hkv * ((rows + nt * kTcRows - 1) / (nt * kTcRows)));
-    const double join = (double)(a.B * a.T * a.Hq) * 8.0 / (slots * kTile * 2 * (a.k.dtype == TOPKP_E4M3 ? 1 : 2));
+    // a tile takes a CTA about 0.9 us (1.3 with two of them on an SM); a part
+    // of every row costs 8 bytes an element at the copy's rate
+    const double join = (double)(a.B * a.T * a.Hq * a.D) * 8.0 / 6.8e6 / (slots > num_sms ? 1.3 : 0.9);
     double best = -1.0;
     p.splits = 1;
     p.per = (int)tiles;
@@ -501,8 +505,8 @@ AttnPlan plan_attention(const topkp_tree_attention_args& a, int num_sms) {
       const int64_t per = (tiles + n - 1) / n;
       if ((tiles + per - 1) / per != n) continue;
       const double part = (double)per + 4.0;
-      double cost = base * n / slots * part + part / 2;
-      if (cost < part) cost = part;
+      const double rounds = base * n / slots;
+      double cost = rounds <= 1.0 ? part : 0.5 * (ceil(rounds) + rounds + 0.5) * part;
       if (n > 1) cost += 3.0 + join * n;
       if (best < 0 || cost < best) {
         best = cost;

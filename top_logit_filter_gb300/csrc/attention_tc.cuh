@@ -504,22 +504,43 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
         const uint8_t* ke = a.k.exponents + h * a.k.exp_head_stride;
         const uint8_t* ve = a.v.exponents + h * a.v.exp_head_stride;
         const int piece = lane & 15;  // boxes: lanes 0-15 keys, 16-31 values
-        for (int j = 0; j < n; ++j) {
-          const int rs = j % RS, t0 = (t_begin + j) * kTile;
-          uint32_t e[2] = {0, 0};
+        // A tile's pages are looked up before the wait for its predecessor's
+        // room, its exponents after.  Entries 0 and 1: this lane's
+        // two rows; 2: its box, outside the pool past the last token, which
+        // reads as zeros.
+        int page[3], at[3], box_page = -1, box_at = 0;
+        uint32_t e[2], e_next[2] = {0, 0};
+        auto pages_of = [&](int j) {
+          const int t0 = (t_begin + j) * kTile;
+          find(t0 + lane, page[0], at[0]);
+          find(t0 + lane + 32, page[1], at[1]);
+          page[2] = -1;
+          at[2] = 0;
+          const int t = t0 + piece * p.box;
+          if (piece < per_tile && t < len) place(t, page[2], at[2]);
+        };
+        auto exponents_of = [&](int j) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            int page, at;
-            find(t0 + lane + 32 * i, page, at);
-            if (page >= 0) {
-              const int64_t pg = page, to = at;
-              e[i] = (uint32_t)__ldg(ke + pg * a.k.exp_page_stride + to * a.k.exp_token_stride) |
-                     ((uint32_t)__ldg(ve + pg * a.v.exp_page_stride + to * a.v.exp_token_stride) << 8) | kToken;
+            e_next[i] = 0;
+            if (j < n && page[i] >= 0) {
+              const int64_t pg = page[i], to = at[i];
+              e_next[i] = (uint32_t)__ldg(ke + pg * a.k.exp_page_stride + to * a.k.exp_token_stride) |
+                          ((uint32_t)__ldg(ve + pg * a.v.exp_page_stride + to * a.v.exp_token_stride) << 8) | kToken;
             }
           }
-          int page = -1, at = 0;  // past the last token: outside, which reads as zeros
-          const int t = t0 + piece * p.box;
-          if (piece < per_tile && t < len) place(t, page, at);
+        };
+        if (n > 0) {
+          pages_of(0);
+          exponents_of(0);
+        }
+        for (int j = 0; j < n; ++j) {
+          const int rs = j % RS;
+          e[0] = e_next[0];
+          e[1] = e_next[1];
+          box_page = page[2];
+          box_at = at[2];
+          if (j + 1 < n) pages_of(j + 1);
           if (j >= RS) tc_wait(&raw_empty[rs], (j / RS - 1) & 1, &dead);
           __syncwarp();
           sexp[rs][lane] = e[0];
@@ -532,7 +553,8 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
           __syncwarp();
           if (piece < per_tile)
             tma_box(raw + rs * Shape::kRawBytes + (lane >> 4) * (kTile * DP) + piece * p.box * DP, lane < 16 ? &kmap : &vmap, &raw_full[rs], 0,
-                    h, at, page);
+                    h, box_at, box_page);
+          exponents_of(j + 1);
         }
       } else {
         const int pt = tid - 32 * (Shape::kSoftWarps + 1);
@@ -541,51 +563,76 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
         constexpr int NR = (kTile + STEP - 1) / STEP;
         const int c = pt % CH, r0 = pt / CH;
         const bool c_in = c * 16 < a.D;
-        // this thread's pieces of one operand of tile j: widened from the ring or the cache
-        auto widen = [&](int j, bool values, unsigned char* dst) {
-          const topkp_cache& ca = values ? a.v : a.k;
-          const unsigned char* from = raw + (j % RS) * Shape::kRawBytes + (values ? kTile * DP : 0);
+        // This thread's pieces of one operand of tile j.  Everything is read
+        // before anything is widened; rows without a token become zeros
+        // whatever the box held.
+        struct Pieces {
           uint4 w[NR];
           uint32_t e[NR];
+        };
+        auto read = [&](int j, bool values, Pieces& x) {
+          const topkp_cache& ca = values ? a.v : a.k;
+          const unsigned char* from = raw + (j % RS) * Shape::kRawBytes + (values ? kTile * DP : 0);
 #pragma unroll
           for (int i = 0; i < NR; ++i) {
-            const int r = r0 + i * STEP;
-            e[i] = r < kTile && c_in ? sexp[j % RS][r] : 0;
-            w[i] = make_uint4(0, 0, 0, 0);
-            if (!(e[i] & kToken)) continue;  // zeros whatever the box held
+            const int r = NR * STEP == kTile ? r0 + i * STEP : min(r0 + i * STEP, kTile - 1);
+            const uint32_t e = sexp[j % RS][r];
             if (p.box) {
-              w[i] = *reinterpret_cast<const uint4*>(from + r * DP + c * 16);
+              x.w[i] = *reinterpret_cast<const uint4*>(from + r * DP + c * 16);
             } else {
-              int page, at;
-              find((t_begin + j) * kTile + r, page, at);
-              w[i] = fetch16(reinterpret_cast<const uint8_t*>(ca.data) + h * ca.head_stride + (int64_t)page * ca.page_stride +
-                                 (int64_t)at * ca.token_stride + c * 16,
-                             p.wide, c * 16 + 8 < a.D);
+              x.w[i] = make_uint4(0, 0, 0, 0);
+              if ((e & kToken) && c_in) {
+                int page, at;
+                find((t_begin + j) * kTile + r, page, at);
+                x.w[i] = fetch16(reinterpret_cast<const uint8_t*>(ca.data) + h * ca.head_stride + (int64_t)page * ca.page_stride +
+                                     (int64_t)at * ca.token_stride + c * 16,
+                                 p.wide, c * 16 + 8 < a.D);
+              }
             }
+            x.e[i] = values ? (e >> 8) & 0xff : e & 0xff;
+            const uint32_t keep = e & kToken ? ~0u : 0u;
+            x.w[i].x &= keep;
+            x.w[i].y &= keep;
+            x.w[i].z &= keep;
+            x.w[i].w &= keep;
           }
+        };
+        auto write = [&](const Pieces& x, unsigned char* dst) {
 #pragma unroll
           for (int i = 0; i < NR; ++i) {
             const int r = r0 + i * STEP;
-            if (r >= kTile) continue;
             uint4 lo, hi;
-            widen16<BF>(w[i], (values ? e[i] >> 8 : e[i]) & 0xff, lo, hi);
+            widen16<BF>(x.w[i], x.e[i], lo, hi);
+            if (NR * STEP != kTile && r >= kTile) continue;
             *reinterpret_cast<uint4*>(dst + swizzled<kTile>(r, 2 * c)) = lo;
             *reinterpret_cast<uint4*>(dst + swizzled<kTile>(r, 2 * c + 1)) = hi;
           }
         };
         for (int j = 0; j <= n && n > 0; ++j) {
+          const int v = j - 1;
+          Pieces kx, vx;
           if (j < n) {
             tc_wait(&raw_full[j % RS], (j / RS) & 1, &dead);
+            read(j, false, kx);
+          }
+          if (j > 0) read(v, true, vx);
+          if (j < n) {
             if (j >= KS) tc_wait(&k_empty[j % KS], (j / KS - 1) & 1, &dead);
-            widen(j, false, sk + (j % KS) * Shape::kTileBytes);
-            hand_over(&k_full[j % KS]);
+            write(kx, sk + (j % KS) * Shape::kTileBytes);
           }
           if (j > 0) {
-            const int v = j - 1;
             if (v >= VS) tc_wait(&v_empty[v % VS], (v / VS - 1) & 1, &dead);
-            widen(v, true, sv + (v % VS) * Shape::kTileBytes);
-            hand_over(&v_full[v % VS]);
-            if (lane == 0) mbar_arrive(&raw_empty[v % RS]);
+            write(vx, sv + (v % VS) * Shape::kTileBytes);
+          }
+          // one fence for both
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            if (j < n) mbar_arrive(&k_full[j % KS]);
+            if (j > 0) {
+              mbar_arrive(&v_full[v % VS]);
+              mbar_arrive(&raw_empty[v % RS]);
+            }
           }
         }
       }

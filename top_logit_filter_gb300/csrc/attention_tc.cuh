@@ -109,7 +109,8 @@ __device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0ull : n >
 template <int DP, int NT, bool Q8>
 struct TcShape {
   static constexpr int kSoftWarps = 4 * NT;
-  static constexpr int kFeedWarps = Q8 ? 7 : 2;  // 16 bits: one for keys, one for values
+  // 16 bits: one warp for keys, one for values; e4m3: one loads, the others widen
+  static constexpr int kFeedWarps = !Q8 ? 2 : NT == 1 ? 11 : 7;
   static constexpr int kThreads = 32 * (kSoftWarps + kFeedWarps + 1);
   static constexpr int kPerSm = !Q8 && NT == 1 && DP <= 128 ? 2 : 1;
   static constexpr int kTileBytes = kTile * DP * 2;
@@ -135,6 +136,19 @@ __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, uint6
       : "memory");
 }
 
+// A stage of a ring and the parity of its round.
+struct Ring {
+  int at;
+  uint32_t phase;
+  template <int N>
+  __device__ __forceinline__ void step() {
+    if (++at == N) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
+};
+
 // A bounded wait; once one has given up, none of the CTA waits any more.
 __device__ __forceinline__ void tc_wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
   if (mbar_try_wait(bar, parity)) return;
@@ -149,42 +163,62 @@ __device__ __forceinline__ void tc_wait(uint64_t* bar, uint32_t parity, volatile
   }
 }
 
-// Two e4m3 in the high bytes of the halves of t as bf16: sign, then exponent
-// and mantissa four bits down, which reads as the value times 2^-120,
-// subnormals too.  `scale` brings it back, exactly.
-__device__ __forceinline__ uint32_t e4m3_to_bf16x2(uint32_t t, uint32_t scale) {
-  uint32_t r = (t & 0x80008000u) | ((t >> 4) & 0x07f007f0u);
-  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(scale));
-  return r;
-}
-// Sixteen e4m3 times 2^(e - 127) in the rows' type.
+// Sixteen e4m3 by the conversion instruction: fp16 rows, and what the shifts
+// below do not take.
 template <bool BF>
-__device__ __forceinline__ void widen16(const uint4& w, uint32_t e, uint4& lo, uint4& hi) {
+__device__ __noinline__ void widen16_slow(const uint4& w, uint32_t e, uint4& lo, uint4& hi) {
   uint32_t r[8];
   const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-  // the code 0x7f of either sign is NaN, which the shift would read as 480
-  uint32_t nan = 0;
+  const float s = exponent_scale(e);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) nan |= (in[i] & 0x7f7f7f7fu) + 0x01010101u;
-  // 2^120 times the scale is a bf16 up to a scale of 2^7 (rows up to 57344)
-  if (BF && !(nan & 0x80808080u) && e <= 134) {
-    const uint32_t sc = (e + 120) << 7, s2 = sc | (sc << 16);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      r[2 * i] = e4m3_to_bf16x2(__byte_perm(in[i], 0u, 0x1404), s2);
-      r[2 * i + 1] = e4m3_to_bf16x2(__byte_perm(in[i], 0u, 0x3424), s2);
-    }
-  } else {
+  for (int i = 0; i < 8; ++i) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(in[i >> 1] >> (16 * (i & 1)))));
+    r[i] = pack2<BF>(__half2float(__ushort_as_half((uint16_t)h)) * s, __half2float(__ushort_as_half((uint16_t)(h >> 16))) * s);
+  }
+  lo = make_uint4(r[0], r[1], r[2], r[3]);
+  hi = make_uint4(r[4], r[5], r[6], r[7]);
+}
+// Sixteen e4m3 times 2^(e - 127) in the rows' type.  bf16: two bytes go to
+// the high bytes of two halves; sign, then exponent and mantissa four bits
+// down, read as the value times 2^-120 (subnormals too), and one exact
+// product with 2^(e - 7) brings it to its size.  That factor is a bf16 up to
+// e = 134 (rows up to 57344), and the code 0x7f of either sign is NaN, which
+// the shift would read as 480: both are left to the conversion.
+template <bool BF>
+__device__ __forceinline__ void widen16(const uint4& w, uint32_t e, uint4& lo, uint4& hi) {
+  if (!BF) {
+    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+    uint32_t r[8];
+    // fp16 holds the values themselves; the scale in two exact steps where one leaves fp16's range
     const float s = exponent_scale(e);
+    const bool one = e >= 112 && e <= 142;
+    const uint32_t s2 = one ? pack2<false>(s, s) : 0u;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       uint32_t h;
       asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(in[i >> 1] >> (16 * (i & 1)))));
-      r[i] = pack2<BF>(__half2float(__ushort_as_half((uint16_t)h)) * s, __half2float(__ushort_as_half((uint16_t)(h >> 16))) * s);
+      asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r[i]) : "r"(h), "r"(s2));
     }
+    lo = make_uint4(r[0], r[1], r[2], r[3]);
+    hi = make_uint4(r[4], r[5], r[6], r[7]);
+    if (!one) widen16_slow<BF>(w, e, lo, hi);
+    return;
+  }
+  const uint32_t sc = (e + 120) << 7, s2 = sc | (sc << 16);
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+  uint32_t r[8], most = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t t = __byte_perm(in[i >> 1], 0u, i & 1 ? 0x3424 : 0x1404);
+    const uint32_t u = (t >> 4) & 0x07f007f0u;
+    most = __vmaxu2(most, u);
+    r[i] = (t & 0x80008000u) | u;
+    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(r[i]) : "r"(s2));
   }
   lo = make_uint4(r[0], r[1], r[2], r[3]);
   hi = make_uint4(r[4], r[5], r[6], r[7]);
+  if (e > 134 || (most & 0xffffu) == 0x07f0u || (most >> 16) == 0x07f0u) widen16_slow<BF>(w, e, lo, hi);
 }
 // Sixteen e4m3 of a row, in two pieces where the row's alignment or end asks for it.
 __device__ __forceinline__ uint4 fetch16(const uint8_t* p, int wide, bool both) {
@@ -504,136 +538,127 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
         const uint8_t* ke = a.k.exponents + h * a.k.exp_head_stride;
         const uint8_t* ve = a.v.exponents + h * a.v.exp_head_stride;
         const int piece = lane & 15;  // boxes: lanes 0-15 keys, 16-31 values
-        // A tile's pages are looked up before the wait for its predecessor's
-        // room, its exponents after.  Entries 0 and 1: this lane's
-        // two rows; 2: its box, outside the pool past the last token, which
-        // reads as zeros.
-        int page[3], at[3], box_page = -1, box_at = 0;
-        uint32_t e[2], e_next[2] = {0, 0};
-        auto pages_of = [&](int j) {
+        // A tile's pages are looked up four tiles ahead, its exponents two, so
+        // that neither latency is waited for: [0] is the tile at hand.
+        // Entries 0 and 1 are this lane's two rows, 2 its box (outside the
+        // pool past the last token, which reads as zeros).
+        int page[5][3], at[5][3];
+        uint32_t e[3][2];
+        auto pages_of = [&](int j, int (&pg)[3], int (&to)[3]) {
+          pg[0] = pg[1] = pg[2] = -1;
+          to[0] = to[1] = to[2] = 0;
+          if (j >= n) return;
           const int t0 = (t_begin + j) * kTile;
-          find(t0 + lane, page[0], at[0]);
-          find(t0 + lane + 32, page[1], at[1]);
-          page[2] = -1;
-          at[2] = 0;
+          find(t0 + lane, pg[0], to[0]);
+          find(t0 + lane + 32, pg[1], to[1]);
           const int t = t0 + piece * p.box;
-          if (piece < per_tile && t < len) place(t, page[2], at[2]);
+          if (piece < per_tile && t < len) place(t, pg[2], to[2]);
         };
-        auto exponents_of = [&](int j) {
+        auto exponents_of = [&](const int (&pg)[3], const int (&to)[3], uint32_t (&x)[2]) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            e_next[i] = 0;
-            if (j < n && page[i] >= 0) {
-              const int64_t pg = page[i], to = at[i];
-              e_next[i] = (uint32_t)__ldg(ke + pg * a.k.exp_page_stride + to * a.k.exp_token_stride) |
-                          ((uint32_t)__ldg(ve + pg * a.v.exp_page_stride + to * a.v.exp_token_stride) << 8) | kToken;
+            x[i] = 0;
+            if (pg[i] >= 0) {
+              const int64_t q = pg[i], t = to[i];
+              x[i] = (uint32_t)__ldg(ke + q * a.k.exp_page_stride + t * a.k.exp_token_stride) |
+                     ((uint32_t)__ldg(ve + q * a.v.exp_page_stride + t * a.v.exp_token_stride) << 8) | kToken;
             }
           }
         };
-        if (n > 0) {
-          pages_of(0);
-          exponents_of(0);
-        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pages_of(i, page[i], at[i]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) exponents_of(page[i], at[i], e[i]);
+        Ring rr = {0, 1};
+#pragma unroll 1
         for (int j = 0; j < n; ++j) {
-          const int rs = j % RS;
-          e[0] = e_next[0];
-          e[1] = e_next[1];
-          box_page = page[2];
-          box_at = at[2];
-          if (j + 1 < n) pages_of(j + 1);
-          if (j >= RS) tc_wait(&raw_empty[rs], (j / RS - 1) & 1, &dead);
+          exponents_of(page[2], at[2], e[2]);
+          pages_of(j + 4, page[4], at[4]);
+          tc_wait(&raw_empty[rr.at], rr.phase, &dead);
           __syncwarp();
-          sexp[rs][lane] = e[0];
-          sexp[rs][lane + 32] = e[1];
+          sexp[rr.at][lane] = e[0][0];
+          sexp[rr.at][lane + 32] = e[0][1];
           __syncwarp();
           if (lane == 0) {
-            if (p.box) mbar_arrive_expect_tx(&raw_full[rs], Shape::kRawBytes);
-            else mbar_arrive(&raw_full[rs]);
+            if (p.box) mbar_arrive_expect_tx(&raw_full[rr.at], Shape::kRawBytes);
+            else mbar_arrive(&raw_full[rr.at]);
           }
           __syncwarp();
           if (piece < per_tile)
-            tma_box(raw + rs * Shape::kRawBytes + (lane >> 4) * (kTile * DP) + piece * p.box * DP, lane < 16 ? &kmap : &vmap, &raw_full[rs], 0,
-                    h, box_at, box_page);
-          exponents_of(j + 1);
+            tma_box(raw + rr.at * Shape::kRawBytes + (lane >> 4) * (kTile * DP) + piece * p.box * DP, lane < 16 ? &kmap : &vmap,
+                    &raw_full[rr.at], 0, h, at[0][2], page[0][2]);
+          rr.template step<RS>();
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+              page[i][k] = page[i + 1][k];
+              at[i][k] = at[i + 1][k];
+            }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            e[i][0] = e[i + 1][0];
+            e[i][1] = e[i + 1][1];
+          }
         }
       } else {
         const int pt = tid - 32 * (Shape::kSoftWarps + 1);
         constexpr int CH = DP / 16;                  // 16-byte pieces of a cached row
         constexpr int STEP = 32 * (kFeed - 1) / CH;  // rows between a thread's rows
-        constexpr int NR = (kTile + STEP - 1) / STEP;
         const int c = pt % CH, r0 = pt / CH;
         const bool c_in = c * 16 < a.D;
-        // This thread's pieces of one operand of tile j.  Everything is read
-        // before anything is widened; rows without a token become zeros
-        // whatever the box held.
-        struct Pieces {
-          uint4 w[NR];
-          uint32_t e[NR];
-        };
-        auto read = [&](int j, bool values, Pieces& x) {
-          const topkp_cache& ca = values ? a.v : a.k;
-          const unsigned char* from = raw + (j % RS) * Shape::kRawBytes + (values ? kTile * DP : 0);
-#pragma unroll
-          for (int i = 0; i < NR; ++i) {
-            const int r = NR * STEP == kTile ? r0 + i * STEP : min(r0 + i * STEP, kTile - 1);
-            const uint32_t e = sexp[j % RS][r];
+        // This thread's pieces of one operand of tile j; rows without a token
+        // become zeros whatever the box held.  A small loop: the roles of
+        // this kernel share the instruction cache.
+        auto widen = [&](int rs, int j, bool values, unsigned char* dst) {
+          const unsigned char* from = raw + rs * Shape::kRawBytes + (values ? kTile * DP : 0) + c * 16;
+#pragma unroll 1
+          for (int r = r0; r < kTile; r += STEP) {
+            const uint32_t e = sexp[rs][r];
+            uint4 w = make_uint4(0, 0, 0, 0);
             if (p.box) {
-              x.w[i] = *reinterpret_cast<const uint4*>(from + r * DP + c * 16);
-            } else {
-              x.w[i] = make_uint4(0, 0, 0, 0);
-              if ((e & kToken) && c_in) {
-                int page, at;
-                find((t_begin + j) * kTile + r, page, at);
-                x.w[i] = fetch16(reinterpret_cast<const uint8_t*>(ca.data) + h * ca.head_stride + (int64_t)page * ca.page_stride +
-                                     (int64_t)at * ca.token_stride + c * 16,
-                                 p.wide, c * 16 + 8 < a.D);
-              }
+              w = *reinterpret_cast<const uint4*>(from + r * DP);
+            } else if ((e & kToken) && c_in) {
+              const topkp_cache& ca = values ? a.v : a.k;
+              int page, at;
+              find((t_begin + j) * kTile + r, page, at);
+              w = fetch16(reinterpret_cast<const uint8_t*>(ca.data) + h * ca.head_stride + (int64_t)page * ca.page_stride +
+                              (int64_t)at * ca.token_stride + c * 16,
+                          p.wide, c * 16 + 8 < a.D);
             }
-            x.e[i] = values ? (e >> 8) & 0xff : e & 0xff;
-            const uint32_t keep = e & kToken ? ~0u : 0u;
-            x.w[i].x &= keep;
-            x.w[i].y &= keep;
-            x.w[i].z &= keep;
-            x.w[i].w &= keep;
-          }
-        };
-        auto write = [&](const Pieces& x, unsigned char* dst) {
-#pragma unroll
-          for (int i = 0; i < NR; ++i) {
-            const int r = r0 + i * STEP;
+            if (!(e & kToken)) w = make_uint4(0, 0, 0, 0);
             uint4 lo, hi;
-            widen16<BF>(x.w[i], x.e[i], lo, hi);
-            if (NR * STEP != kTile && r >= kTile) continue;
+            widen16<BF>(w, (values ? e >> 8 : e) & 0xff, lo, hi);
             *reinterpret_cast<uint4*>(dst + swizzled<kTile>(r, 2 * c)) = lo;
             *reinterpret_cast<uint4*>(dst + swizzled<kTile>(r, 2 * c + 1)) = hi;
           }
         };
+        Ring kr = {0, 1}, vr = {0, 1}, rr = {0, 0};  // an empty stage's wait starts passed
+        int r_last = 0;
         for (int j = 0; j <= n && n > 0; ++j) {
-          const int v = j - 1;
-          Pieces kx, vx;
           if (j < n) {
-            tc_wait(&raw_full[j % RS], (j / RS) & 1, &dead);
-            read(j, false, kx);
-          }
-          if (j > 0) read(v, true, vx);
-          if (j < n) {
-            if (j >= KS) tc_wait(&k_empty[j % KS], (j / KS - 1) & 1, &dead);
-            write(kx, sk + (j % KS) * Shape::kTileBytes);
+            tc_wait(&raw_full[rr.at], rr.phase, &dead);
+            tc_wait(&k_empty[kr.at], kr.phase, &dead);
+            if (r0 < STEP) widen(rr.at, j, false, sk + kr.at * Shape::kTileBytes);
           }
           if (j > 0) {
-            if (v >= VS) tc_wait(&v_empty[v % VS], (v / VS - 1) & 1, &dead);
-            write(vx, sv + (v % VS) * Shape::kTileBytes);
+            tc_wait(&v_empty[vr.at], vr.phase, &dead);
+            if (r0 < STEP) widen(r_last, j - 1, true, sv + vr.at * Shape::kTileBytes);
           }
           // one fence for both
           fence_proxy_async_shared();
           __syncwarp();
           if (lane == 0) {
-            if (j < n) mbar_arrive(&k_full[j % KS]);
+            if (j < n) mbar_arrive(&k_full[kr.at]);
             if (j > 0) {
-              mbar_arrive(&v_full[v % VS]);
-              mbar_arrive(&raw_empty[v % RS]);
+              mbar_arrive(&v_full[vr.at]);
+              mbar_arrive(&raw_empty[r_last]);
             }
           }
+          if (j > 0) vr.template step<VS>();
+          kr.template step<KS>();
+          r_last = rr.at;
+          rr.template step<RS>();
         }
       }
     }
@@ -644,41 +669,49 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
     constexpr uint32_t i_qk = common | ((uint32_t)(kTile / 8) << 17);
     constexpr uint32_t i_pv = common | (1u << 16) | ((uint32_t)(DP / 8) << 17);
     const uint32_t q0 = smem_u32(sq), k0 = smem_u32(sk), v0 = smem_u32(sv);
-    auto product_s = [&](int t, int j) {
+    Ring kr = {0, 0}, vr = {0, 0};
+    // S of row tile t against the keys of stage kr, into buffer `buf`
+    auto product_s = [&](int t, int buf) {
+      const uint64_t qd = operand(q0 + t * (kTcRows * DP * 2), 16, 1024), kd = operand(k0 + kr.at * Shape::kTileBytes, 16, 1024);
 #pragma unroll
-      for (int kk = 0; kk < DP / 16; ++kk)
-        tc_mma_ss(tm + t * 128 + (j & 1) * 64, operand(q0 + t * (kTcRows * DP * 2) + (kk / 4) * (kTcRows * 128) + (kk % 4) * 32, 16, 1024),
-                  operand(k0 + (j % KS) * Shape::kTileBytes + (kk / 4) * (kTile * 128) + (kk % 4) * 32, 16, 1024), i_qk, kk > 0);
-      if (t == NT - 1) tc_commit(&k_empty[j % KS]);
-      tc_commit(&s_full[t][j & 1]);
+      for (int kk = 0; kk < DP / 16; ++kk)  // 16-byte units: a step of 16 dims, a block of 64
+        tc_mma_ss(tm + t * 128 + buf * 64, qd + (kk / 4) * (kTcRows * 8) + (kk % 4) * 2, kd + (kk / 4) * (kTile * 8) + (kk % 4) * 2, i_qk,
+                  kk > 0);
+      if (t == NT - 1) tc_commit(&k_empty[kr.at]);
+      tc_commit(&s_full[t][buf]);
     };
     if (n > 0) {
       tc_wait(&q_full, 0, &dead);
       tc_wait(&k_full[0], 0, &dead);
       tc_fence_after();
       for (int t = 0; t < NT; ++t) product_s(t, 0);
+      kr.template step<KS>();
     }
+#pragma unroll 1
     for (int j = 0; j < n; ++j) {
+      const int buf = j & 1;
       if (j + 1 < n) {
-        tc_wait(&k_full[(j + 1) % KS], ((j + 1) / KS) & 1, &dead);
+        tc_wait(&k_full[kr.at], kr.phase, &dead);
         for (int t = 0; t < NT; ++t) {
           // the other S still holds P of tile j - 1 until its product is done
           if (j > 0) tc_wait(&pv_done[t], (j - 1) & 1, &dead);
           tc_fence_after();
-          product_s(t, j + 1);
+          product_s(t, buf ^ 1);
         }
+        kr.template step<KS>();
       }
       for (int t = 0; t < NT; ++t) {
-        tc_wait(&p_full[t][j & 1], (j >> 1) & 1, &dead);
-        if (t == 0) tc_wait(&v_full[j % VS], (j / VS) & 1, &dead);
+        tc_wait(&p_full[t][buf], (j >> 1) & 1, &dead);
+        if (t == 0) tc_wait(&v_full[vr.at], vr.phase, &dead);
         tc_fence_after();
+        const uint64_t vd = operand(v0 + vr.at * Shape::kTileBytes, kTile * 128, 1024);
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)
-          tc_mma_ts(tm + Shape::kO + t * DP, tm + t * 128 + (j & 1) * 64 + kk * 8,
-                    operand(v0 + (j % VS) * Shape::kTileBytes + kk * 2048, kTile * 128, 1024), i_pv, j > 0 || kk > 0);
-        if (t == NT - 1) tc_commit(&v_empty[j % VS]);
+          tc_mma_ts(tm + Shape::kO + t * DP, tm + t * 128 + buf * 64 + kk * 8, vd + kk * 128, i_pv, j > 0 || kk > 0);
+        if (t == NT - 1) tc_commit(&v_empty[vr.at]);
         tc_commit(&pv_done[t]);
       }
+      vr.template step<VS>();
     }
     tc_fence_before();
   }

@@ -4,11 +4,12 @@
 // do the softmax, a thread a row (TMEM lane i is row i of its tile); the next
 // warps bring keys and values into shared memory; one thread of the last warp
 // issues the matrix instructions:
-//   S = Q K^T   both operands in shared memory, K-major, 128-byte swizzle
+//   S = Q K^T   Q in TMEM (or shared memory), K in shared memory, K-major,
+//               128-byte swizzle
 //   O += P V    P in TMEM over its S, V in shared memory as it lies (tokens
 //               by dims), read with the dims as the major direction
-// S is double-buffered, so the product of tile j + 1 runs under the softmax
-// of tile j.  Up to 128 rows, two CTAs share an SM (eight warps each leave
+// S is double-buffered where TMEM has room, so the product of tile j + 1 runs
+// under the softmax of tile j.  Up to 128 rows, two CTAs share an SM (eight warps each leave
 // 128 registers a thread), and one's products run under the other's softmax;
 // beyond, one CTA takes 256 rows, so that keys and values are brought (and
 // widened from e4m3) once for both tiles.  O stays in TMEM; a row's reference
@@ -114,14 +115,20 @@ struct TcShape {
   static constexpr int kThreads = 32 * (kSoftWarps + kFeedWarps + 1);
   static constexpr int kPerSm = !Q8 && NT == 1 && DP <= 128 ? 2 : 1;
   static constexpr int kTileBytes = kTile * DP * 2;
-  static constexpr int kQBytes = NT * kTcRows * DP * 2;
+  // Q as a shared-memory operand would be read again for every product (4 KB
+  // a step, twice what a step of 64 tokens' keys is), so it sits in TMEM,
+  // except where two CTAs of 128 dims share an SM.  TMEM columns: S, Q, O.
+  static constexpr bool kQInTmem = kPerSm == 1 || DP == 64;
+  static constexpr int kQBytes = kQInTmem ? 0 : NT * kTcRows * DP * 2;
+  static constexpr int kS = NT == 2 && DP == 128 ? 1 : 2;  // buffers of S a row tile
   // stages of keys, of values, and of raw e4m3 (both).  Keys free theirs as
   // soon as their product is done, well before the softmax
-  static constexpr int kKeys = Q8 ? (NT == 1 && DP <= 128 ? 3 : 2) : DP == 64 || (DP == 128 && NT == 2) ? 4 : 2;
+  static constexpr int kKeys = Q8 ? (DP <= 128 ? 3 : 2) : DP == 64 || (DP == 128 && NT == 2) ? 4 : DP == 256 ? 3 : 2;
   static constexpr int kValues = Q8 && DP == 256 ? 1 : kKeys;
   static constexpr int kRaw = !Q8 ? 0 : DP == 256 ? 2 : 4;
   static constexpr int kRawBytes = 2 * kTile * DP;  // keys, then values
-  static constexpr uint32_t kO = NT * 128;          // TMEM: two S of 64 columns a row tile, then the O of DP
+  static constexpr uint32_t kQ = NT * kS * 64;
+  static constexpr uint32_t kO = kQ + (kQInTmem ? NT * DP / 2 : 0);
   static constexpr int kColumns = kO + NT * DP <= 256 ? 256 : 512;
   static constexpr size_t kSmem = 1024 + kQBytes + (size_t)(kKeys + kValues) * kTileBytes + (size_t)kRaw * kRawBytes;
   static_assert(kO + NT * DP <= 512, "O does not fit tensor memory");
@@ -306,12 +313,31 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
       // the row of Q into its place
       const uint16_t* qr = reinterpret_cast<const uint16_t*>(a.q) + b * a.q_batch_stride +
                            (in ? node * a.q_token_stride + hq * a.q_head_stride : 0);
+      auto piece = [&](int c) {
+        return in && c * 8 < a.D ? *reinterpret_cast<const uint4*>(qr + c * 8) : make_uint4(0, 0, 0, 0);
+      };
+      if constexpr (Shape::kQInTmem) {
+#pragma unroll
+        for (int c = 0; c < DP / 64; ++c) {
+          uint32_t w[32];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 v = piece(c * 8 + i);
+            w[4 * i] = v.x;
+            w[4 * i + 1] = v.y;
+            w[4 * i + 2] = v.z;
+            w[4 * i + 3] = v.w;
+          }
+          tc_st32(tm + ((uint32_t)((warp & 3) * 32) << 16) + Shape::kQ + tile * (DP / 2) + c * 32, w);
+        }
+        tc_wait_st();
+        tc_fence_before();
+      } else {
 #pragma unroll 4
-      for (int c = 0; c < DP / 8; ++c) {
-        const uint4 v = in && c * 8 < a.D ? *reinterpret_cast<const uint4*>(qr + c * 8) : make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(sq + tile * (kTcRows * DP * 2) + swizzled<kTcRows>(tid & 127, c)) = v;
+        for (int c = 0; c < DP / 8; ++c)
+          *reinterpret_cast<uint4*>(sq + tile * (kTcRows * DP * 2) + swizzled<kTcRows>(tid & 127, c)) = piece(c);
+        fence_proxy_async_shared();
       }
-      fence_proxy_async_shared();
       mbar_arrive(&q_full);
     }
     // rows past the last (their Q is zero) and of missing nodes go along as
@@ -325,10 +351,12 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
     const uint32_t ocol = lanes + Shape::kO + tile * DP;
     float m = -INFINITY, l = 0.0f;
     for (int j = 0; j < n; ++j) {
-      const uint32_t sb = lanes + tile * 128 + (j & 1) * 64;
-      tc_wait(&s_full[tile][j & 1], (j >> 1) & 1, &dead);
+      const int buf = Shape::kS == 2 ? j & 1 : 0;
+      const uint32_t sb = lanes + (tile * Shape::kS + buf) * 64;
+      tc_wait(&s_full[tile][buf], Shape::kS == 2 ? (j >> 1) & 1 : j & 1, &dead);
       if (idle) {
-        mbar_arrive(&p_full[tile][j & 1]);
+        if (j == n - 1 && j > 0) tc_wait(&pv_done[tile], (j - 1) & 1, &dead);
+        mbar_arrive(&p_full[tile][buf]);
         continue;
       }
       __syncwarp();
@@ -405,11 +433,12 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
       tc_st32(sb, pk);
       tc_wait_st();
       tc_fence_before();
-      mbar_arrive(&p_full[tile][j & 1]);
+      // a parity tells one phase from the next only: product n - 2 is seen done
+      // before product n - 1, which needs this arrival, can be
+      if (j == n - 1 && j > 0) tc_wait(&pv_done[tile], (j - 1) & 1, &dead);
+      mbar_arrive(&p_full[tile][buf]);
     }
     if (n > 0) {
-      // the last S says that product n - 3 is done: one phase at a time from there
-      if (n > 1) tc_wait(&pv_done[tile], (n - 2) & 1, &dead);
       tc_wait(&pv_done[tile], (n - 1) & 1, &dead);
       __syncwarp();
       tc_fence_after();
@@ -672,11 +701,18 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
     Ring kr = {0, 0}, vr = {0, 0};
     // S of row tile t against the keys of stage kr, into buffer `buf`
     auto product_s = [&](int t, int buf) {
-      const uint64_t qd = operand(q0 + t * (kTcRows * DP * 2), 16, 1024), kd = operand(k0 + kr.at * Shape::kTileBytes, 16, 1024);
+      const uint64_t kd = operand(k0 + kr.at * Shape::kTileBytes, 16, 1024);
+      const uint32_t d = tm + (t * Shape::kS + buf) * 64;
+      if constexpr (Shape::kQInTmem) {
+        const uint32_t qa = tm + Shape::kQ + t * (DP / 2);
 #pragma unroll
-      for (int kk = 0; kk < DP / 16; ++kk)  // 16-byte units: a step of 16 dims, a block of 64
-        tc_mma_ss(tm + t * 128 + buf * 64, qd + (kk / 4) * (kTcRows * 8) + (kk % 4) * 2, kd + (kk / 4) * (kTile * 8) + (kk % 4) * 2, i_qk,
-                  kk > 0);
+        for (int kk = 0; kk < DP / 16; ++kk) tc_mma_ts(d, qa + kk * 8, kd + (kk / 4) * (kTile * 8) + (kk % 4) * 2, i_qk, kk > 0);
+      } else {
+        const uint64_t qd = operand(q0 + t * (kTcRows * DP * 2), 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk)  // 16-byte units: a step of 16 dims, a block of 64
+          tc_mma_ss(d, qd + (kk / 4) * (kTcRows * 8) + (kk % 4) * 2, kd + (kk / 4) * (kTile * 8) + (kk % 4) * 2, i_qk, kk > 0);
+      }
       if (t == NT - 1) tc_commit(&k_empty[kr.at]);
       tc_commit(&s_full[t][buf]);
     };
@@ -689,8 +725,8 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
     }
 #pragma unroll 1
     for (int j = 0; j < n; ++j) {
-      const int buf = j & 1;
-      if (j + 1 < n) {
+      const int buf = Shape::kS == 2 ? j & 1 : 0;
+      if (Shape::kS == 2 && j + 1 < n) {
         tc_wait(&k_full[kr.at], kr.phase, &dead);
         for (int t = 0; t < NT; ++t) {
           // the other S still holds P of tile j - 1 until its product is done
@@ -701,16 +737,25 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
         kr.template step<KS>();
       }
       for (int t = 0; t < NT; ++t) {
-        tc_wait(&p_full[t][buf], (j >> 1) & 1, &dead);
+        tc_wait(&p_full[t][buf], Shape::kS == 2 ? (j >> 1) & 1 : j & 1, &dead);
         if (t == 0) tc_wait(&v_full[vr.at], vr.phase, &dead);
         tc_fence_after();
         const uint64_t vd = operand(v0 + vr.at * Shape::kTileBytes, kTile * 128, 1024);
+        const uint32_t pa = tm + (t * Shape::kS + buf) * 64;
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)
-          tc_mma_ts(tm + Shape::kO + t * DP, tm + t * 128 + buf * 64 + kk * 8, vd + kk * 128, i_pv, j > 0 || kk > 0);
+          tc_mma_ts(tm + Shape::kO + t * DP, pa + kk * 8, vd + kk * 128, i_pv, j > 0 || kk > 0);
         if (t == NT - 1) tc_commit(&v_empty[vr.at]);
         tc_commit(&pv_done[t]);
+        if (Shape::kS == 1 && j + 1 < n) {
+          // one S a row tile: the other row tile's softmax fills the gap
+          if (t == 0) tc_wait(&k_full[kr.at], kr.phase, &dead);
+          tc_wait(&pv_done[t], j & 1, &dead);
+          tc_fence_after();
+          product_s(t, 0);
+        }
       }
+      if (Shape::kS == 1) kr.template step<KS>();
       vr.template step<VS>();
     }
     tc_fence_before();

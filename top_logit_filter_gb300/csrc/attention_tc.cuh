@@ -29,6 +29,7 @@ namespace topkp {
 namespace {
 
 constexpr int kTcRows = 128;
+constexpr int kRun = 4;  // tiles that a loading warp looks up at once
 constexpr float kSlack = 8.0f;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
@@ -111,21 +112,25 @@ template <int DP, int NT, bool Q8>
 struct TcShape {
   static constexpr int kSoftWarps = 4 * NT;
   // 16 bits: one warp for keys, one for values; e4m3: one loads, the others widen
-  static constexpr int kFeedWarps = !Q8 ? 2 : NT == 1 ? 11 : 7;
+  static constexpr int kFeedWarps = !Q8 ? 2 : NT == 1 ? 9 : 7;
+  static constexpr int kLoadWarps = 1;
   static constexpr int kThreads = 32 * (kSoftWarps + kFeedWarps + 1);
   static constexpr int kPerSm = !Q8 && NT == 1 && DP <= 128 ? 2 : 1;
   static constexpr int kTileBytes = kTile * DP * 2;
   // Q as a shared-memory operand would be read again for every product (4 KB
   // a step, twice what a step of 64 tokens' keys is), so it sits in TMEM,
-  // except where two CTAs of 128 dims share an SM.  TMEM columns: S, Q, O.
-  static constexpr bool kQInTmem = kPerSm == 1 || DP == 64;
+  // except at 128 dims where two CTAs share an SM or a CTA has two row tiles:
+  // there the second S is worth more (one S a row tile makes its two products
+  // and its softmax take turns: 714 against 640 us for trees of 64 over e4m3).
+  // TMEM columns: S, Q, O.
+  static constexpr bool kQInTmem = DP != 128 || (kPerSm == 1 && NT == 1);
   static constexpr int kQBytes = kQInTmem ? 0 : NT * kTcRows * DP * 2;
-  static constexpr int kS = NT == 2 && DP == 128 ? 1 : 2;  // buffers of S a row tile
+  static constexpr int kS = 2;  // buffers of S a row tile
   // stages of keys, of values, and of raw e4m3 (both).  Keys free theirs as
   // soon as their product is done, well before the softmax
   static constexpr int kKeys = Q8 ? (DP <= 128 ? 3 : 2) : DP == 64 || (DP == 128 && NT == 2) ? 4 : DP == 256 ? 3 : 2;
-  static constexpr int kValues = Q8 && DP == 256 ? 1 : kKeys;
-  static constexpr int kRaw = !Q8 ? 0 : DP == 256 ? 2 : 4;
+  static constexpr int kValues = Q8 && DP == 256 ? 1 : Q8 && NT == 2 ? 2 : kKeys;
+  static constexpr int kRaw = !Q8 ? 0 : DP == 256 ? 2 : NT == 2 ? 3 : 4;
   static constexpr int kRawBytes = 2 * kTile * DP;  // keys, then values
   static constexpr uint32_t kQ = NT * kS * 64;
   static constexpr uint32_t kO = kQ + (kQInTmem ? NT * DP / 2 : 0);
@@ -267,7 +272,7 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
   const int n = (split == p.splits - 1 ? tiles : min(t_begin + p.per, tiles)) - t_begin;
 
   if (tid == 0) {
-    constexpr int kParts = Q8 ? kFeed - 1 : 1;  // warps that fill a stage
+    constexpr int kParts = Q8 ? kFeed - Shape::kLoadWarps : 1;  // warps that fill a stage
     for (int i = 0; i < KS; ++i) {
       mbar_init(&k_full[i], kParts);
       mbar_init(&k_empty[i], 1);
@@ -277,8 +282,8 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
       mbar_init(&v_empty[i], 1);
     }
     for (int i = 0; i < RS; ++i) {
-      mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], kFeed - 1);
+      mbar_init(&raw_full[i], 2);
+      mbar_init(&raw_empty[i], kFeed - Shape::kLoadWarps);
     }
     for (int t = 0; t < NT; ++t) {
       for (int i = 0; i < 2; ++i) {
@@ -559,105 +564,114 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
         }
       }
     } else {
-      // The first warp fills the raw ring, exponents too (a fence of a warp
-      // that widens would wait for such loads); the others widen, keys one
-      // tile ahead of values, as the products go.
+      // The first warps fill the raw ring, exponents too (a fence of a warp
+      // that widens would wait for such loads), each a run of kRun tiles in
+      // turn; the others widen, keys one tile ahead of values, as the
+      // products go.
+      constexpr int kLoad = Shape::kLoadWarps;
       constexpr uint32_t kToken = 1u << 16;  // beside a row's two exponents: there is a token
-      if (feeder == 0) {
+      if (feeder < kLoad) {
         const uint8_t* ke = a.k.exponents + h * a.k.exp_head_stride;
         const uint8_t* ve = a.v.exponents + h * a.v.exp_head_stride;
         const int piece = lane & 15;  // boxes: lanes 0-15 keys, 16-31 values
-        // A tile's pages are looked up four tiles ahead, its exponents two, so
-        // that neither latency is waited for: [0] is the tile at hand.
-        // Entries 0 and 1 are this lane's two rows, 2 its box (outside the
-        // pool past the last token, which reads as zeros).
-        int page[5][3], at[5][3];
-        uint32_t e[3][2];
-        auto pages_of = [&](int j, int (&pg)[3], int (&to)[3]) {
-          pg[0] = pg[1] = pg[2] = -1;
-          to[0] = to[1] = to[2] = 0;
-          if (j >= n) return;
-          const int t0 = (t_begin + j) * kTile;
-          find(t0 + lane, pg[0], to[0]);
-          find(t0 + lane + 32, pg[1], to[1]);
-          const int t = t0 + piece * p.box;
-          if (piece < per_tile && t < len) place(t, pg[2], to[2]);
-        };
-        auto exponents_of = [&](const int (&pg)[3], const int (&to)[3], uint32_t (&x)[2]) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            x[i] = 0;
-            if (pg[i] >= 0) {
-              const int64_t q = pg[i], t = to[i];
-              x[i] = (uint32_t)__ldg(ke + q * a.k.exp_page_stride + t * a.k.exp_token_stride) |
-                     ((uint32_t)__ldg(ve + q * a.v.exp_page_stride + t * a.v.exp_token_stride) << 8) | kToken;
-            }
-          }
-        };
-#pragma unroll
-        for (int i = 0; i < 4; ++i) pages_of(i, page[i], at[i]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) exponents_of(page[i], at[i], e[i]);
-        Ring rr = {0, 1};
+        // All pages of a run are asked for at once, then all its exponents,
+        // so that a run waits for each once: this lane's two rows of each
+        // tile, and its box (outside the pool past the last token, which
+        // reads as zeros).
 #pragma unroll 1
-        for (int j = 0; j < n; ++j) {
-          exponents_of(page[2], at[2], e[2]);
-          pages_of(j + 4, page[4], at[4]);
-          tc_wait(&raw_empty[rr.at], rr.phase, &dead);
-          __syncwarp();
-          sexp[rr.at][lane] = e[0][0];
-          sexp[rr.at][lane + 32] = e[0][1];
-          __syncwarp();
-          if (lane == 0) {
-            if (p.box) mbar_arrive_expect_tx(&raw_full[rr.at], Shape::kRawBytes);
-            else mbar_arrive(&raw_full[rr.at]);
+        for (int j0 = feeder * kRun; j0 < n; j0 += kLoad * kRun) {
+          // The reads are unconditional, at places that exist, and what is not
+          // wanted is dropped after: a branch around each would make them wait
+          // for one another.
+          int page[2 * kRun], at[2 * kRun], bpage[kRun], bat[kRun];
+          uint32_t e[2 * kRun];
+          const int t0 = (t_begin + j0) * kTile, t_end = min(len, (t_begin + n) * kTile);
+#pragma unroll
+          for (int i = 0; i < 2 * kRun; ++i) place(min(t0 + i * 32 + lane, len - 1), page[i], at[i]);
+#pragma unroll
+          for (int i = 0; i < kRun; ++i) place(min(t0 + i * kTile + piece * p.box, len - 1), bpage[i], bat[i]);
+#pragma unroll
+          for (int i = 0; i < kRun; ++i)
+            if (piece >= per_tile || t0 + i * kTile + piece * p.box >= t_end) bpage[i] = -1;
+          uint32_t ek[2 * kRun], ev[2 * kRun];
+#pragma unroll
+          for (int i = 0; i < 2 * kRun; ++i) {
+            const bool in = page[i] >= 0 && page[i] < a.pages && t0 + i * 32 + lane < t_end;
+            const int64_t q = in ? page[i] : 0, t = in ? at[i] : 0;
+            e[i] = in ? kToken : 0;
+            ek[i] = __ldg(ke + q * a.k.exp_page_stride + t * a.k.exp_token_stride);
+            ev[i] = __ldg(ve + q * a.v.exp_page_stride + t * a.v.exp_token_stride);
           }
-          __syncwarp();
-          if (piece < per_tile)
-            tma_box(raw + rr.at * Shape::kRawBytes + (lane >> 4) * (kTile * DP) + piece * p.box * DP, lane < 16 ? &kmap : &vmap,
-                    &raw_full[rr.at], 0, h, at[0][2], page[0][2]);
-          rr.template step<RS>();
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 2 * kRun; ++i) e[i] = e[i] ? kToken | ek[i] | (ev[i] << 8) : 0u;
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
-              page[i][k] = page[i + 1][k];
-              at[i][k] = at[i + 1][k];
+          for (int i = 0; i < kRun; ++i) {
+            const int rs = (j0 + i) % RS;
+            const uint32_t phase = ((j0 + i) / RS + 1) & 1;
+            if (j0 + i < n) {
+              tc_wait(&raw_empty[rs], phase, &dead);
+              __syncwarp();
+              // two arrivals: the boxes on their way, and the exponents
+              if (lane == 0) {
+                if (p.box) mbar_arrive_expect_tx(&raw_full[rs], Shape::kRawBytes);
+                else mbar_arrive(&raw_full[rs]);
+              }
+              __syncwarp();
+              if (piece < per_tile)
+                tma_box(raw + rs * Shape::kRawBytes + (lane >> 4) * (kTile * DP) + piece * p.box * DP, lane < 16 ? &kmap : &vmap,
+                        &raw_full[rs], 0, h, bat[i], bpage[i]);
+              sexp[rs][lane] = e[2 * i];
+              sexp[rs][lane + 32] = e[2 * i + 1];
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&raw_full[rs]);
             }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            e[i][0] = e[i + 1][0];
-            e[i][1] = e[i + 1][1];
           }
         }
       } else {
-        const int pt = tid - 32 * (Shape::kSoftWarps + 1);
+        const int pt = tid - 32 * (Shape::kSoftWarps + kLoad);
         constexpr int CH = DP / 16;                  // 16-byte pieces of a cached row
-        constexpr int STEP = 32 * (kFeed - 1) / CH;  // rows between a thread's rows
+        constexpr int STEP = 32 * (kFeed - kLoad) / CH;  // rows between a thread's rows
         const int c = pt % CH, r0 = pt / CH;
         const bool c_in = c * 16 < a.D;
         // This thread's pieces of one operand of tile j; rows without a token
-        // become zeros whatever the box held.  A small loop: the roles of
-        // this kernel share the instruction cache.
+        // become zeros whatever the box held.  All are read before the first
+        // is widened.
+        constexpr int NR = (kTile + STEP - 1) / STEP;
         auto widen = [&](int rs, int j, bool values, unsigned char* dst) {
           const unsigned char* from = raw + rs * Shape::kRawBytes + (values ? kTile * DP : 0) + c * 16;
+          uint4 w[NR];
+          uint32_t e[NR];
+#pragma unroll
+          for (int i = 0; i < NR; ++i) {
+            const int r = min(r0 + i * STEP, kTile - 1);
+            e[i] = sexp[rs][r];
+            w[i] = *reinterpret_cast<const uint4*>(from + r * DP);
+          }
+          if (!p.box) {
 #pragma unroll 1
-          for (int r = r0; r < kTile; r += STEP) {
-            const uint32_t e = sexp[rs][r];
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (p.box) {
-              w = *reinterpret_cast<const uint4*>(from + r * DP);
-            } else if ((e & kToken) && c_in) {
-              const topkp_cache& ca = values ? a.v : a.k;
-              int page, at;
-              find((t_begin + j) * kTile + r, page, at);
-              w = fetch16(reinterpret_cast<const uint8_t*>(ca.data) + h * ca.head_stride + (int64_t)page * ca.page_stride +
-                              (int64_t)at * ca.token_stride + c * 16,
-                          p.wide, c * 16 + 8 < a.D);
+            for (int i = 0; i < NR; ++i) {
+              uint4 x = make_uint4(0, 0, 0, 0);
+              const int r = min(r0 + i * STEP, kTile - 1);
+              if ((sexp[rs][r] & kToken) && c_in) {
+                const topkp_cache& ca = values ? a.v : a.k;
+                int page, at;
+                find((t_begin + j) * kTile + r, page, at);
+                x = fetch16(reinterpret_cast<const uint8_t*>(ca.data) + h * ca.head_stride + (int64_t)page * ca.page_stride +
+                                (int64_t)at * ca.token_stride + c * 16,
+                            p.wide, c * 16 + 8 < a.D);
+              }
+#pragma unroll
+              for (int k = 0; k < NR; ++k)
+                if (k == i) w[k] = x;
             }
-            if (!(e & kToken)) w = make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int i = 0; i < NR; ++i) {
+            const int r = r0 + i * STEP;
+            if (NR * STEP != kTile && r >= kTile) continue;
+            if (!(e[i] & kToken)) w[i] = make_uint4(0, 0, 0, 0);
             uint4 lo, hi;
-            widen16<BF>(w, (values ? e >> 8 : e) & 0xff, lo, hi);
+            widen16<BF>(w[i], (values ? e[i] >> 8 : e[i]) & 0xff, lo, hi);
             *reinterpret_cast<uint4*>(dst + swizzled<kTile>(r, 2 * c)) = lo;
             *reinterpret_cast<uint4*>(dst + swizzled<kTile>(r, 2 * c + 1)) = hi;
           }

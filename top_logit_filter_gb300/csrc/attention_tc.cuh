@@ -2,12 +2,14 @@
 //
 // One CTA: NT tiles of 128 rows against tiles of 64 tokens.  Warps 0 .. 4 NT - 1
 // do the softmax, a thread a row (TMEM lane i is row i of its tile); the next
-// warps bring keys and values into shared memory; one thread of the last warp
-// issues the matrix instructions:
+// warps bring keys and values into shared memory; the last warp issues
+// the matrix instructions:
 //   S = Q K^T   Q in TMEM (or shared memory), K in shared memory, K-major,
 //               128-byte swizzle
 //   O += P V    P in TMEM over its S, V in shared memory as it lies (tokens
 //               by dims), read with the dims as the major direction
+// (issued from uniform code: behind a branch to one lane every descriptor went
+// through general registers, about 100 cycles an instruction).
 // S is double-buffered where TMEM has room, so the product of tile j + 1 runs
 // under the softmax of tile j.  Up to 128 rows, two CTAs share an SM (eight warps each leave
 // 128 registers a thread), and one's products run under the other's softmax;
@@ -43,19 +45,25 @@ __device__ __forceinline__ float exp2_approx(float t) {
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// The next three are called by a whole warp and executed by one thread of it
+// (the same each time), so that the code around them stays uniform and the
+// operands' descriptors stay in uniform registers.
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
 }
 __device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((int)acc)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((int)acc)
       : "memory");
 }
 __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((int)acc)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((int)acc)
       : "memory");
 }
 // 32 columns of this thread's lane.
@@ -257,7 +265,7 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
   __shared__ uint32_t tmem_base, sexp[RS][kTile];
   __shared__ volatile int dead;
   const topkp_tree_attention_args& a = p.a;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int G = (int)(a.Hq / a.Hkv);
   const int rows = (int)a.T * G;
   const int64_t bh = blockIdx.z;
@@ -705,7 +713,7 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
         }
       }
     }
-  } else if (lane == 0) {
+  } else {
     // ---- matrix instructions ----
     constexpr uint32_t kind = BF ? 1u : 0u;
     constexpr uint32_t common = (1u << 4) | (kind << 7) | (kind << 10) | ((uint32_t)(kTcRows / 16) << 24);

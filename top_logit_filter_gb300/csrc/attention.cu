@@ -43,38 +43,8 @@ __device__ __forceinline__ void request_span(const topkp_tree_attention_args& a,
   *nodes = n;
 }
 
-// ------------------------------------------------------------- mma.sync
-// One CTA: 16 rows, four warps; each warp takes 16 of the 64 tokens of a
-// tile with a softmax of its own, and the four are joined at the end.
-constexpr int kTile = 64;
-constexpr int kRowTile = 16;
-constexpr int kMmaThreads = 128;
+constexpr int kTile = 64;  // tokens
 
-template <bool BF>
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if (BF)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
 template <bool BF>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t r;
@@ -82,264 +52,11 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// Eight e4m3 of a cache, scaled, in the rows' type (exact in bf16).
-template <bool BF>
-__device__ __forceinline__ uint4 widen8(uint2 w, float scale) {
-  const uint32_t two[4] = {w.x & 0xffffu, w.x >> 16, w.y & 0xffffu, w.y >> 16};
-  uint32_t r[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two[i]));
-    r[i] = pack2<BF>(__half2float(__ushort_as_half((uint16_t)h)) * scale,
-                     __half2float(__ushort_as_half((uint16_t)(h >> 16))) * scale);
-  }
-  return make_uint4(r[0], r[1], r[2], r[3]);
-}
 __device__ __forceinline__ float exponent_scale(uint32_t e) { return __uint_as_float(e ? e << 23 : 0x400000u); }
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool in) {
   const int n = in ? 16 : 0;
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-
-template <int DP>
-constexpr size_t mma_smem() {
-  return (size_t)2 * 2 * kTile * (DP + 8) * 2;
-}
-
-template <int DP, bool BF, bool Q8>
-__global__ void __launch_bounds__(kMmaThreads) attn_mma(const __grid_constant__ AttnDev p) {
-  constexpr int LD = DP + 8;  // a padded row: eight consecutive rows fall into different banks
-  constexpr int KS = DP / 16;
-  extern __shared__ __align__(16) unsigned char smem[];
-  uint16_t* sk = reinterpret_cast<uint16_t*>(smem);  // [2][kTile][LD]
-  uint16_t* sv = sk + 2 * kTile * LD;
-  const topkp_tree_attention_args& a = p.a;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int G = (int)(a.Hq / a.Hkv);
-  const int rows = (int)a.T * G;
-  const int64_t bh = blockIdx.y;
-  const int64_t b = bh / a.Hkv;
-  const int h = (int)(bh - b * a.Hkv);
-  const int row0 = blockIdx.z * kRowTile;
-  const int split = blockIdx.x;
-  int ctx, len, nodes;
-  request_span(a, b, &ctx, &len, &nodes);
-  const int tiles = (len + kTile - 1) / kTile;
-  const int t_begin = min(split * p.per, tiles);
-  const int t_end = split == p.splits - 1 ? tiles : min(t_begin + p.per, tiles);
-
-  // the two rows of this thread (lane / 4 and that plus 8)
-  int node[2];
-  uint64_t bits[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = row0 + (lane >> 2) + 8 * i;
-    node[i] = r / G;
-    bits[i] = 0;
-    if (node[i] >= nodes) node[i] = -1;
-    else if (a.tree) bits[i] = a.tree[b * a.T + node[i]];
-  }
-  // Q in registers, as the left operand's 16 x 16 pieces
-  uint32_t qf[KS][4];
-  {
-    const uint16_t* q = reinterpret_cast<const uint16_t*>(a.q) + b * a.q_batch_stride;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = row0 + (lane >> 2) + 8 * i;
-      const bool in = r < rows;
-      const uint16_t* qr = q + (in ? (r / G) * a.q_token_stride + (h * G + r % G) * a.q_head_stride : 0);
-#pragma unroll
-      for (int k = 0; k < KS; ++k)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int d = k * 16 + j * 8 + (lane & 3) * 2;
-          qf[k][i + 2 * j] = in && d < a.D ? *reinterpret_cast<const uint32_t*>(qr + d) : 0u;
-        }
-    }
-  }
-
-  float o[DP / 8][4];
-#pragma unroll
-  for (int i = 0; i < DP / 8; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-  const float sc = a.scale * kLog2e;
-  const int32_t* table = a.table ? a.table + b * a.ld_table : nullptr;
-
-  auto load = [&](int tile, int buf) {
-    constexpr int CH = DP / 8;  // 8-element pieces of a row
-#pragma unroll 4
-    for (int i = tid; i < kTile * CH; i += kMmaThreads) {
-      const int r = i / CH, c = i - r * CH;
-      const int t = tile * kTile + r;
-      bool in = t < len && c * 8 < a.D;
-      int64_t page = b, at = t;
-      if (table && in) {
-        const int pg = t / (int)a.page_size;
-        at = t - pg * (int)a.page_size;
-        page = table[pg];
-        in = page >= 0 && page < a.pages;
-      }
-      if (!in) page = at = 0;
-      const int cc = in ? c * 8 : 0;
-      const int64_t ko = page * a.k.page_stride + at * a.k.token_stride + h * a.k.head_stride + cc;
-      const int64_t vo = page * a.v.page_stride + at * a.v.token_stride + h * a.v.head_stride + cc;
-      uint16_t* dk = sk + (buf * kTile + r) * LD + c * 8;
-      uint16_t* dv = sv + (buf * kTile + r) * LD + c * 8;
-      if (Q8) {
-        uint4 kk = make_uint4(0, 0, 0, 0), vv = kk;
-        if (in) {
-          const float ks = exponent_scale(
-              a.k.exponents[page * a.k.exp_page_stride + at * a.k.exp_token_stride + h * a.k.exp_head_stride]);
-          const float vs = exponent_scale(
-              a.v.exponents[page * a.v.exp_page_stride + at * a.v.exp_token_stride + h * a.v.exp_head_stride]);
-          kk = widen8<BF>(*reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(a.k.data) + ko), ks);
-          vv = widen8<BF>(*reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(a.v.data) + vo), vs);
-        }
-        *reinterpret_cast<uint4*>(dk) = kk;
-        *reinterpret_cast<uint4*>(dv) = vv;
-      } else {
-        cp16(smem_u32(dk), reinterpret_cast<const uint16_t*>(a.k.data) + ko, in);
-        cp16(smem_u32(dv), reinterpret_cast<const uint16_t*>(a.v.data) + vo, in);
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-
-  if (t_begin < t_end) load(t_begin, 0);
-  for (int tile = t_begin; tile < t_end; ++tile) {
-    const int buf = (tile - t_begin) & 1;
-    if (tile + 1 < t_end) {
-      load(tile + 1, buf ^ 1);
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-    } else {
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-    }
-    __syncthreads();
-    const uint16_t* kt = sk + (buf * kTile + warp * 16) * LD;
-    const uint16_t* vt = sv + (buf * kTile + warp * 16) * LD;
-    float s[2][4] = {};
-#pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      uint32_t f[4];
-      // matrices: tokens 0-7 and 8-15, each of 16 elements in two halves
-      ldsm4(f, smem_u32(kt + ((lane & 7) + (lane >> 4) * 8) * LD + k * 16 + ((lane >> 3) & 1) * 8));
-      mma16816<BF>(s[0], qf[k], f[0], f[1]);
-      mma16816<BF>(s[1], qf[k], f[2], f[3]);
-    }
-    const int t0 = tile * kTile + warp * 16;
-    float mx[2] = {m[0], m[1]};
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int t = t0 + n * 8 + (lane & 3) * 2 + (e & 1);
-        const int i = e >> 1;
-        bool see = node[i] >= 0 && t < len;
-        if (t >= ctx) see = see && (a.tree ? (bits[i] >> (t - ctx)) & 1 : t - ctx <= node[i]);
-        s[n][e] = see ? s[n][e] * sc : -INFINITY;
-        mx[i] = fmaxf(mx[i], s[n][e]);
-      }
-    float f[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-      mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-      const float base = mx[i] == -INFINITY ? 0.0f : mx[i];
-      f[i] = exp2f(m[i] - base);
-      m[i] = mx[i];
-      l[i] *= f[i];
-      mx[i] = base;
-    }
-    uint32_t pf[4];
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      float e[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        e[j] = exp2f(s[n][j] - mx[j >> 1]);
-        l[j >> 1] += e[j];
-      }
-      pf[2 * n] = pack2<BF>(e[0], e[1]);
-      pf[2 * n + 1] = pack2<BF>(e[2], e[3]);
-    }
-#pragma unroll
-    for (int d = 0; d < DP / 16; ++d) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        o[2 * d][j] *= f[j >> 1];
-        o[2 * d + 1][j] *= f[j >> 1];
-      }
-      uint32_t v[4];
-      ldsm4t(v, smem_u32(vt + ((lane & 7) + ((lane >> 3) & 1) * 8) * LD + d * 16 + (lane >> 4) * 8));
-      mma16816<BF>(o[2 * d], pf, v[0], v[1]);
-      mma16816<BF>(o[2 * d + 1], pf, v[2], v[3]);
-    }
-    __syncthreads();
-  }
-
-  // join the four warps: row statistics, then the weighted outputs through
-  // shared memory (the tiles are done with)
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-  }
-  float* so = reinterpret_cast<float*>(smem);  // [4 warps][16][DP + 4]
-  __shared__ float sm[4][16], sl[4][16];
-  if ((lane & 3) == 0) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      sm[warp][(lane >> 2) + 8 * i] = m[i];
-      sl[warp][(lane >> 2) + 8 * i] = l[i];
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = (lane >> 2) + 8 * i;
-    const float all = fmaxf(fmaxf(sm[0][r], sm[1][r]), fmaxf(sm[2][r], sm[3][r]));
-    const float f = m[i] == -INFINITY ? 0.0f : exp2f(m[i] - all);
-#pragma unroll
-    for (int d = 0; d < DP / 8; ++d) {
-      float* at = so + (warp * 16 + r) * (DP + 4) + d * 8 + (lane & 3) * 2;
-      at[0] = o[d][2 * i] * f;
-      at[1] = o[d][2 * i + 1] * f;
-    }
-  }
-  __syncthreads();
-  const int64_t all_rows = a.B * a.T * a.Hq;
-  for (int i = tid; i < kRowTile * (DP / 2); i += kMmaThreads) {
-    const int rr = i / (DP / 2), d = (i - rr * (DP / 2)) * 2;
-    const int r = row0 + rr;
-    if (r >= rows || d >= a.D) continue;
-    const float all = fmaxf(fmaxf(sm[0][rr], sm[1][rr]), fmaxf(sm[2][rr], sm[3][rr]));
-    float total = 0.0f, x = 0.0f, y = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      if (sm[w][rr] == -INFINITY) continue;
-      total += sl[w][rr] * exp2f(sm[w][rr] - all);
-      x += so[(w * 16 + rr) * (DP + 4) + d];
-      y += so[(w * 16 + rr) * (DP + 4) + d + 1];
-    }
-    const float inv = total > 0.0f ? 1.0f / total : total;
-    const float lse = total > 0.0f ? (all + log2f(total)) * kLn2 : total == 0.0f ? -INFINITY : total;
-    const int node_r = r / G, hq = h * G + r % G;
-    const int64_t row = (b * a.T + node_r) * a.Hq + hq;
-    if (p.splits > 1) {
-      float* po = p.part_o + (split * all_rows + row) * a.D + d;
-      *reinterpret_cast<float2*>(po) = make_float2(x * inv, y * inv);
-      if (d == 0) p.part_l[split * all_rows + row] = lse;
-    } else {
-      uint16_t* po = reinterpret_cast<uint16_t*>(a.out) + b * a.out_batch_stride + node_r * a.out_token_stride +
-                     hq * a.out_head_stride + d;
-      *reinterpret_cast<uint32_t*>(po) = pack2<BF>(x * inv, y * inv);
-      if (d == 0 && a.lse) a.lse[row] = lse;
-    }
-  }
 }
 
 }  // namespace
@@ -350,51 +67,61 @@ __global__ void __launch_bounds__(kMmaThreads) attn_mma(const __grid_constant__ 
 namespace topkp {
 namespace {
 
-// Joins the parts of a row: weights exp(lse_i - lse).  One warp per row.
+// Joins the parts of a row: weights exp(lse_i - lse).  One warp per row; a
+// lane holds the log-sums of four parts and four elements of the row, and the
+// parts' elements are read four parts at a time.
+constexpr int kMaxParts = 128;
 template <bool BF>
 __global__ void __launch_bounds__(128) attn_join(const __grid_constant__ AttnDev p) {
   const topkp_tree_attention_args& a = p.a;
   const int lane = threadIdx.x & 31;
   const int64_t rows = a.B * a.T * a.Hq;
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (row >= rows) return;
-  float m = -INFINITY;
-  for (int s = lane; s < p.splits; s += 32) m = fmaxf(m, p.part_l[s * rows + row]);
+  float l[kMaxParts / 32], m = -INFINITY, total = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kMaxParts / 32; ++i) {
+    const int s = i * 32 + lane;
+    l[i] = s < p.splits ? p.part_l[s * rows + row] : -INFINITY;
+    m = fmaxf(m, l[i]);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float acc[TOPKP_MAX_HEAD_DIM / 32] = {};
-  float total = 0.0f;
-  for (int s = 0; s < p.splits; ++s) {
-    const float li = p.part_l[s * rows + row];
-    if (li == -INFINITY) continue;
-    const float w = exp2f((li - m) * kLog2e);
-    total += w;
-    const float* po = p.part_o + (s * rows + row) * a.D;
 #pragma unroll
-    for (int i = 0; i < TOPKP_MAX_HEAD_DIM / 32; ++i)
-      if (i * 32 + lane < a.D) acc[i] += w * po[i * 32 + lane];
+  for (int i = 0; i < kMaxParts / 32; ++i) {
+    l[i] = l[i] == -INFINITY ? 0.0f : exp2f((l[i] - m) * kLog2e);  // from here on the part's weight
+    total += l[i];
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   const float inv = total > 0.0f ? 1.0f / total : total;
   const int64_t bt = row / a.Hq;
   const int64_t hq = row - bt * a.Hq, b = bt / a.T, t = bt - b * a.T;
   uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + b * a.out_batch_stride + t * a.out_token_stride + hq * a.out_head_stride;
+  for (int d0 = 0; d0 < a.D; d0 += 128) {
+    const int d = d0 + lane * 4;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-  for (int i = 0; i < TOPKP_MAX_HEAD_DIM / 32; ++i)
-    if (i * 32 + lane < a.D) out[i * 32 + lane] = (uint16_t)pack2<BF>(acc[i] * inv, 0.0f);
+    for (int i = 0; i < kMaxParts / 32; ++i) {
+      const int count = min(32, p.splits - i * 32);
+#pragma unroll 4
+      for (int k = 0; k < count; ++k) {
+        const float w = __shfl_sync(0xffffffffu, l[i], k);
+        // a part that saw nothing was not written
+        if (w != 0.0f && d < a.D) {
+          const float4 x = *reinterpret_cast<const float4*>(p.part_o + ((int64_t)(i * 32 + k) * rows + row) * a.D + d);
+          acc.x += w * x.x;
+          acc.y += w * x.y;
+          acc.z += w * x.z;
+          acc.w += w * x.w;
+        }
+      }
+    }
+    if (d < a.D)
+      *reinterpret_cast<uint2*>(out + d) = make_uint2(pack2<BF>(acc.x * inv, acc.y * inv), pack2<BF>(acc.z * inv, acc.w * inv));
+  }
   if (lane == 0 && a.lse) a.lse[row] = total > 0.0f ? m + log2f(total) * kLn2 : total == 0.0f ? -INFINITY : total;
-}
-
-template <int DP, bool BF, bool Q8>
-cudaError_t launch_mma(const AttnDev& p, cudaStream_t s) {
-  const topkp_tree_attention_args& a = p.a;
-  constexpr size_t tiles = mma_smem<DP>(), join = (size_t)4 * 16 * (DP + 4) * 4;
-  constexpr size_t smem = tiles > join ? tiles : join;
-  cudaError_t e = cudaFuncSetAttribute(attn_mma<DP, BF, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  const int64_t rows = a.T * (a.Hq / a.Hkv);
-  const dim3 grid((unsigned)p.splits, (unsigned)(a.B * a.Hkv), (unsigned)((rows + kRowTile - 1) / kRowTile));
-  attn_mma<DP, BF, Q8><<<grid, kMmaThreads, smem, s>>>(p);
-  return cudaGetLastError();
 }
 
 // The driver's encoder of tensor maps, looked up once (null where it is missing).
@@ -452,22 +179,15 @@ cudaError_t launch_tc(AttnDev p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// Tensor memory's 128 rows pay from here on.
-bool on_tensor_cores(const topkp_tree_attention_args& a) { return a.T * (a.Hq / a.Hkv) > 0; }
 // Tiles of 128 rows of a CTA (256 dims leave tensor memory for one).
 int row_tiles(const topkp_tree_attention_args& a) { return a.T * (a.Hq / a.Hkv) > kTcRows && a.D <= 128 ? 2 : 1; }
 
 template <bool BF, bool Q8>
 cudaError_t launch_dim(const AttnDev& p, cudaStream_t s) {
-  if (on_tensor_cores(p.a)) {
-    const bool two = row_tiles(p.a) == 2;
-    if (p.a.D <= 64) return two ? launch_tc<64, 2, BF, Q8>(p, s) : launch_tc<64, 1, BF, Q8>(p, s);
-    if (p.a.D <= 128) return two ? launch_tc<128, 2, BF, Q8>(p, s) : launch_tc<128, 1, BF, Q8>(p, s);
-    return launch_tc<256, 1, BF, Q8>(p, s);
-  }
-  if (p.a.D <= 64) return launch_mma<64, BF, Q8>(p, s);
-  if (p.a.D <= 128) return launch_mma<128, BF, Q8>(p, s);
-  return launch_mma<256, BF, Q8>(p, s);
+  const bool two = row_tiles(p.a) == 2;
+  if (p.a.D <= 64) return two ? launch_tc<64, 2, BF, Q8>(p, s) : launch_tc<64, 1, BF, Q8>(p, s);
+  if (p.a.D <= 128) return two ? launch_tc<128, 2, BF, Q8>(p, s) : launch_tc<128, 1, BF, Q8>(p, s);
+  return launch_tc<256, 1, BF, Q8>(p, s);
 }
 
 }  // namespace
@@ -482,50 +202,37 @@ cudaError_t attention_take_device_error(unsigned int* out) {
 AttnPlan plan_attention(const topkp_tree_attention_args& a, int num_sms) {
   AttnPlan p;
   const int64_t rows = a.T * (a.Hq / a.Hkv);
-  const int64_t ctas = a.B * a.Hkv * ((rows + kRowTile - 1) / kRowTile);
   const int64_t cap = a.max_pages * a.page_size;
   const int64_t len = (a.max_context < cap ? (a.max_context > 0 ? a.max_context : 0) : cap) + a.T;
   const int64_t tiles = (len + kTile - 1) / kTile;
-  if (on_tensor_cores(a)) {
-    // Parts of equal size, whatever a request's length, so that the CTAs of
-    // ragged requests even out.  In units of a tile's time: the rounds of CTAs
-    // (between whole ones, as for equal requests, and what ragged ones average
-    // to), four tiles for a CTA's start and end, and writing and reading the
-    // partial outputs.
-    const int64_t nt = row_tiles(a);
-    const double slots = (a.D > 128 || nt == 2 || a.k.dtype == TOPKP_E4M3 ? 1.0 : 2.0) * num_sms;
-    const double base = (double)(a.B * a.Hkv * ((rows + nt * kTcRows - 1) / (nt * kTcRows)));
-    // a tile takes a CTA about 0.9 us (1.3 with two of them on an SM); a part
-    // of every row costs 8 bytes an element at the copy's rate
-    const double join = (double)(a.B * a.T * a.Hq * a.D) * 8.0 / 6.8e6 / (slots > num_sms ? 1.3 : 0.9);
-    double best = -1.0;
-    p.splits = 1;
-    p.per = (int)tiles;
-    for (int64_t n = 1; n <= 128 && n <= tiles; ++n) {
-      const int64_t per = (tiles + n - 1) / n;
-      if ((tiles + per - 1) / per != n) continue;
-      const double part = (double)per + 4.0;
-      const double rounds = base * n / slots;
-      double cost = rounds <= 1.0 ? part : 0.5 * (ceil(rounds) + rounds + 0.5) * part;
-      if (n > 1) cost += 3.0 + join * n;
-      if (best < 0 || cost < best) {
-        best = cost;
-        p.splits = (int)n;
-        p.per = (int)per;
-      }
+  // Parts of equal size, whatever a request's length, so that the CTAs of
+  // ragged requests even out.  In units of a tile's time: the rounds of CTAs
+  // (between whole ones, as for equal requests, and what ragged ones average
+  // to), four tiles for a CTA's start and end, and writing and reading the
+  // partial outputs.
+  const int64_t nt = row_tiles(a);
+  const double slots = (a.D > 128 || nt == 2 || a.k.dtype == TOPKP_E4M3 ? 1.0 : 2.0) * num_sms;
+  const double base = (double)(a.B * a.Hkv * ((rows + nt * kTcRows - 1) / (nt * kTcRows)));
+  // a tile takes a CTA about 0.9 us (1.3 with two of them on an SM); a part
+  // of every row costs 8 bytes an element at the copy's rate
+  const double join = (double)(a.B * a.T * a.Hq * a.D) * 8.0 / 6.8e6 / (slots > num_sms ? 1.3 : 0.9);
+  double best = -1.0;
+  p.splits = 1;
+  p.per = (int)tiles;
+  for (int64_t n = 1; n <= kMaxParts && n <= tiles; ++n) {
+    const int64_t per = (tiles + n - 1) / n;
+    if ((tiles + per - 1) / per != n) continue;
+    const double part = (double)per + 4.0;
+    const double rounds = base * n / slots;
+    double cost = rounds <= 1.0 ? part : 0.5 * (ceil(rounds) + rounds + 0.5) * part;
+    if (n > 1) cost += 3.0 + join * n;
+    if (best < 0 || cost < best) {
+      best = cost;
+      p.splits = (int)n;
+      p.per = (int)per;
     }
-    p.part_bytes = p.splits > 1 ? (size_t)p.splits * (size_t)(a.B * a.T * a.Hq) * (a.D + 1) * sizeof(float) : 0;
-    return p;
   }
-  int64_t splits = (3LL * num_sms + ctas - 1) / ctas;
-  if (splits > (tiles + 1) / 2) splits = (tiles + 1) / 2;
-  if (splits < 1) splits = 1;
-  if (splits > 256) splits = 256;
-  p.per = (int)((tiles + splits - 1) / splits);
-  p.splits = (int)((tiles + p.per - 1) / p.per);
-  splits = p.splits;
-  const size_t all = (size_t)(a.B * a.T * a.Hq);
-  p.part_bytes = splits > 1 ? (size_t)splits * all * (a.D + 1) * sizeof(float) : 0;
+  p.part_bytes = p.splits > 1 ? (size_t)p.splits * (size_t)(a.B * a.T * a.Hq) * (a.D + 1) * sizeof(float) : 0;
   return p;
 }
 
@@ -554,11 +261,18 @@ cudaError_t launch_attention(const topkp_tree_attention_args& a, const AttnPlan&
                      : (q8 ? launch_dim<false, true>(p, s) : launch_dim<false, false>(p, s));
   *launches = 1;
   if (e != cudaSuccess || plan.splits <= 1) return e;
-  const unsigned grid = (unsigned)((all + 3) / 4);
-  if (bf) attn_join<true><<<grid, 128, 0, s>>>(p);
-  else attn_join<false><<<grid, 128, 0, s>>>(p);
+  // the join's launch overlaps the parts; it waits for them itself
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((all + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
   *launches = 2;
-  return cudaGetLastError();
+  return bf ? cudaLaunchKernelEx(&cfg, attn_join<true>, p) : cudaLaunchKernelEx(&cfg, attn_join<false>, p);
 }
 
 }  // namespace topkp

@@ -10,8 +10,8 @@
 //               by dims), read with the dims as the major direction
 // (issued from uniform code: behind a branch to one lane every descriptor went
 // through general registers, about 100 cycles an instruction).
-// S is double-buffered where TMEM has room, so the product of tile j + 1 runs
-// under the softmax of tile j.  Up to 128 rows, two CTAs share an SM (eight warps each leave
+// S is double-buffered, so the product of tile j + 1 runs under the softmax
+// of tile j.  Up to 128 rows, two CTAs share an SM (eight warps each leave
 // 128 registers a thread), and one's products run under the other's softmax;
 // beyond, one CTA takes 256 rows, so that keys and values are brought (and
 // widened from e4m3) once for both tiles.  O stays in TMEM; a row's reference
@@ -133,14 +133,13 @@ struct TcShape {
   // TMEM columns: S, Q, O.
   static constexpr bool kQInTmem = DP != 128 || (kPerSm == 1 && NT == 1);
   static constexpr int kQBytes = kQInTmem ? 0 : NT * kTcRows * DP * 2;
-  static constexpr int kS = 2;  // buffers of S a row tile
   // stages of keys, of values, and of raw e4m3 (both).  Keys free theirs as
   // soon as their product is done, well before the softmax
   static constexpr int kKeys = Q8 ? (DP <= 128 ? 3 : 2) : DP == 64 || (DP == 128 && NT == 2) ? 4 : DP == 256 ? 3 : 2;
   static constexpr int kValues = Q8 && DP == 256 ? 1 : Q8 && NT == 2 ? 2 : kKeys;
   static constexpr int kRaw = !Q8 ? 0 : DP == 256 ? 2 : NT == 2 ? 3 : 4;
   static constexpr int kRawBytes = 2 * kTile * DP;  // keys, then values
-  static constexpr uint32_t kQ = NT * kS * 64;
+  static constexpr uint32_t kQ = NT * 128;  // after two S of 64 columns a row tile
   static constexpr uint32_t kO = kQ + (kQInTmem ? NT * DP / 2 : 0);
   static constexpr int kColumns = kO + NT * DP <= 256 ? 256 : 512;
   static constexpr size_t kSmem = 1024 + kQBytes + (size_t)(kKeys + kValues) * kTileBytes + (size_t)kRaw * kRawBytes;
@@ -255,6 +254,7 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
   constexpr int KS = Shape::kKeys, VS = Shape::kValues;
   constexpr int RS = Shape::kRaw > 0 ? Shape::kRaw : 1;
   constexpr int kFeed = Shape::kFeedWarps;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ unsigned char tc_smem[];
   unsigned char* smem = tc_smem + ((1024 - (smem_u32(tc_smem) & 1023)) & 1023);
   unsigned char* sq = smem;
@@ -364,9 +364,9 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
     const uint32_t ocol = lanes + Shape::kO + tile * DP;
     float m = -INFINITY, l = 0.0f;
     for (int j = 0; j < n; ++j) {
-      const int buf = Shape::kS == 2 ? j & 1 : 0;
-      const uint32_t sb = lanes + (tile * Shape::kS + buf) * 64;
-      tc_wait(&s_full[tile][buf], Shape::kS == 2 ? (j >> 1) & 1 : j & 1, &dead);
+      const int buf = j & 1;
+      const uint32_t sb = lanes + (tile * 2 + buf) * 64;
+      tc_wait(&s_full[tile][buf], (j >> 1) & 1, &dead);
       if (idle) {
         if (j == n - 1 && j > 0) tc_wait(&pv_done[tile], (j - 1) & 1, &dead);
         mbar_arrive(&p_full[tile][buf]);
@@ -724,7 +724,7 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
     // S of row tile t against the keys of stage kr, into buffer `buf`
     auto product_s = [&](int t, int buf) {
       const uint64_t kd = operand(k0 + kr.at * Shape::kTileBytes, 16, 1024);
-      const uint32_t d = tm + (t * Shape::kS + buf) * 64;
+      const uint32_t d = tm + (t * 2 + buf) * 64;
       if constexpr (Shape::kQInTmem) {
         const uint32_t qa = tm + Shape::kQ + t * (DP / 2);
 #pragma unroll
@@ -747,8 +747,8 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
     }
 #pragma unroll 1
     for (int j = 0; j < n; ++j) {
-      const int buf = Shape::kS == 2 ? j & 1 : 0;
-      if (Shape::kS == 2 && j + 1 < n) {
+      const int buf = j & 1;
+      if (j + 1 < n) {
         tc_wait(&k_full[kr.at], kr.phase, &dead);
         for (int t = 0; t < NT; ++t) {
           // the other S still holds P of tile j - 1 until its product is done
@@ -759,25 +759,17 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
         kr.template step<KS>();
       }
       for (int t = 0; t < NT; ++t) {
-        tc_wait(&p_full[t][buf], Shape::kS == 2 ? (j >> 1) & 1 : j & 1, &dead);
+        tc_wait(&p_full[t][buf], (j >> 1) & 1, &dead);
         if (t == 0) tc_wait(&v_full[vr.at], vr.phase, &dead);
         tc_fence_after();
         const uint64_t vd = operand(v0 + vr.at * Shape::kTileBytes, kTile * 128, 1024);
-        const uint32_t pa = tm + (t * Shape::kS + buf) * 64;
+        const uint32_t pa = tm + (t * 2 + buf) * 64;
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)
           tc_mma_ts(tm + Shape::kO + t * DP, pa + kk * 8, vd + kk * 128, i_pv, j > 0 || kk > 0);
         if (t == NT - 1) tc_commit(&v_empty[vr.at]);
         tc_commit(&pv_done[t]);
-        if (Shape::kS == 1 && j + 1 < n) {
-          // one S a row tile: the other row tile's softmax fills the gap
-          if (t == 0) tc_wait(&k_full[kr.at], kr.phase, &dead);
-          tc_wait(&pv_done[t], j & 1, &dead);
-          tc_fence_after();
-          product_s(t, 0);
-        }
       }
-      if (Shape::kS == 1) kr.template step<KS>();
       vr.template step<VS>();
     }
     tc_fence_before();

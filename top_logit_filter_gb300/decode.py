@@ -18,11 +18,35 @@ from __future__ import annotations
 
 import ctypes
 
-from . import _check, _dtype_code, _lib, _ptr, _torch, _vec  # defined before the package imports this module
+from . import TopKPError, _lib
+
+torch = None    # imported by the first call, as the package itself does
+_CODES = {}     # torch dtype -> topkp_dtype
+
+
+def _ready():
+    """The loaded library; imports torch once."""
+    global torch
+    if torch is None:
+        import torch as module
+        _CODES.update({module.float32: _lib.TOPKP_F32, module.float16: _lib.TOPKP_F16, module.bfloat16: _lib.TOPKP_BF16})
+        torch = module
+    return _lib._lib or _lib.load()
+
+
+def _dtype_code(t) -> int:
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype} (float32, float16 or bfloat16)")
+    return code
+
+
+def _ptr(t):
+    # a present but empty tensor may have no address: any one will do, since empty problems return before it is used
+    return None if t is None else t.data_ptr() or (16 if t.numel() == 0 else None)
 
 
 def _cuda(t, name, dim=None, dtype=None, device=None):
-    torch = _torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda or (dim is not None and t.dim() != dim):
         raise ValueError(f"{name} must be a {'' if dim is None else str(dim) + '-D '}CUDA tensor")
     if device is not None and t.device != device:
@@ -32,19 +56,29 @@ def _cuda(t, name, dim=None, dtype=None, device=None):
     return t
 
 
+def _vec(t, n, dtype, name, device):
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        t = torch.as_tensor(t, dtype=dtype, device=device)
+    if t.device != device or t.dtype != dtype or t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{name} must be a 1-D {dtype} tensor of length {n} on {device}")
+    return t.contiguous()
+
+
 def _launch(device, call, *args):
     """call(*args, the current stream of device) with that device current."""
-    torch = _torch()
     index = device.index
     if index == torch.cuda.current_device():  # the usual case, without the guard's cost
-        _check(call(*args, torch._C._cuda_getCurrentRawStream(index)))
+        status = call(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            _check(call(*args, torch._C._cuda_getCurrentRawStream(index)))
+            status = call(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != _lib.TOPKP_SUCCESS:
+        raise TopKPError(status, _lib.last_error())
 
 
 def _workspace(workspace, need, device):
-    torch = _torch()
     if workspace is None:
         return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
     if workspace.dtype != torch.uint8 or workspace.device != device or workspace.numel() < need:
@@ -62,7 +96,7 @@ def beam_select(logits, scores, n: int, finished=None, pad_token: int = 0, works
     int32, token [B, n] int32); a slot without a candidate holds -inf, its
     index mod K and -1.  ``workspace``: a uint8 tensor of at least
     ``beam_select_workspace_size`` bytes (allocated when None)."""
-    torch, lib = _torch(), _lib.load()
+    lib = _ready()
     _cuda(logits, "logits", 2)
     dt, dev = _dtype_code(logits), logits.device
     _cuda(scores, "scores", 2, torch.float32, dev)
@@ -92,9 +126,7 @@ def beam_select(logits, scores, n: int, finished=None, pad_token: int = 0, works
 
 def beam_select_workspace_size(B: int, K: int, V: int, dtype, n: int) -> int:
     """Bytes of workspace ``beam_select`` needs."""
-    torch = _torch()
-    codes = {torch.float32: _lib.TOPKP_F32, torch.float16: _lib.TOPKP_F16, torch.bfloat16: _lib.TOPKP_BF16}
-    return int(_lib.load().topkp_beam_select_workspace_size(B, K, V, codes[dtype], n))
+    return int(_ready().topkp_beam_select_workspace_size(B, K, V, _CODES[dtype], n))
 
 
 def _layout(t, time_dim, name):
@@ -140,7 +172,7 @@ def beam_reorder(states, parent, lengths=None, time_dim: int = 1, out=None):
     ``states``).  lengths: [B, K] int32, how many entries along ``time_dim``
     of each row are live: only they move, and the rest of a destination row
     keeps what it held.  Returns the reordered tensors."""
-    torch, lib = _torch(), _lib.load()
+    lib = _ready()
     single = torch.is_tensor(states)
     src = [states] if single else list(states)
     dst = src if out is None else [out] if torch.is_tensor(out) else list(out)
@@ -159,18 +191,18 @@ def beam_reorder(states, parent, lengths=None, time_dim: int = 1, out=None):
     table = (_lib.State * max(len(src), 1))()
     for i, (s, d) in enumerate(zip(src, dst)):
         for t in (s,) if d is s else (s, d):
-            _cuda(t, f"states[{i}]", None, None, dev)
+            if not isinstance(t, torch.Tensor) or t.device != dev:
+                raise ValueError(f"states[{i}] must be a CUDA tensor on {dev}")
             if t.dim() < 1 or t.shape[0] != B * K or t.shape != s.shape or t.dtype != s.dtype:
                 raise ValueError(f"states[{i}] must have {B} x {K} rows, and its output its shape and dtype")
-        row, blk, blocks, entries, size = _layout(s, time_dim if s.dim() > 1 else 1, f"states[{i}]")
-        drow, dblk = (row, blk) if d is s else _layout(d, time_dim if d.dim() > 1 else 1, f"out[{i}]")[:2]
+        row, blk, blocks, entries, size = _layout(s, time_dim if s.dim() > 1 else 1, "a state")
+        drow, dblk = (row, blk) if d is s else _layout(d, time_dim if d.dim() > 1 else 1, "an output")[:2]
         table[i] = _lib.State(_ptr(s), _ptr(d), row, drow, blk, dblk, blocks, entries, size)
     _launch(dev, lib.topkp_beam_reorder, table, len(src), B, K, _ptr(parent), _ptr(lengths))
     return dst[0] if single else dst
 
 
 def _cache(t, exp, name, device, row_dtype):
-    torch = _torch()
     _cuda(t, name, 4, None, device)
     quant = t.dtype == torch.float8_e4m3fn
     if not quant and t.dtype != row_dtype:
@@ -182,7 +214,8 @@ def _cache(t, exp, name, device, row_dtype):
     p0, p1, p2, _ = t.stride()
     if not quant:
         return _lib.Cache(_ptr(t), None, _dtype_code(t), p0, p1, p2, 0, 0, 0)
-    _cuda(exp, f"{name}'s exponents", 3, torch.uint8, device)
+    if not isinstance(exp, torch.Tensor) or exp.dtype != torch.uint8 or exp.device != device:
+        raise ValueError(f"{name}'s exponents must be a uint8 tensor on {device}")
     if exp.shape != t.shape[:3]:
         raise ValueError(f"{name}'s exponents must be {tuple(t.shape[:3])}, not {tuple(exp.shape)}")
     return _lib.Cache(_ptr(t), _ptr(exp), _lib.TOPKP_E4M3, p0, p1, p2, *exp.stride())
@@ -201,7 +234,7 @@ def cache_write(k, v, slots, k_cache, v_cache, k_exp=None, v_exp=None):
     skip a row; k_cache, v_cache: [pages, page_size, H, D], of the rows'
     dtype, or float8_e4m3fn with k_exp, v_exp [pages, page_size, H] uint8,
     quantised as they are written.  v and v_cache may both be None."""
-    torch, lib = _torch(), _lib.load()
+    lib = _ready()
     _cuda(k, "k", 3)
     dt, dev = _dtype_code(k), k.device
     N, H, D = k.shape
@@ -236,7 +269,7 @@ def cache_read(slots, k_cache, v_cache, k_exp=None, v_exp=None, dtype=None):
     [N, H, D] of ``dtype`` (the cache's own, or any of the three for an e4m3
     cache, bfloat16 when None).  A slot outside the cache gives zeros.
     v_cache may be None; v is then None."""
-    torch, lib = _torch(), _lib.load()
+    lib = _ready()
     _cuda(slots, "slots", 1, torch.int64)
     dev = slots.device
     slots = slots.contiguous()
@@ -270,7 +303,7 @@ def tree_attention(q, k_cache, v_cache, context, pages=None, tree=None, nodes=No
     a bound of ``context`` known on the host, which plans the work (the
     capacity when None).  Returns out ([B, T, Hq, D]), or (out, lse) with
     lse [B, T, Hq] float32."""
-    torch, lib = _torch(), _lib.load()
+    lib = _ready()
     _cuda(q, "q", 4)
     if q.dtype not in (torch.float16, torch.bfloat16):
         raise TypeError(f"q must be float16 or bfloat16, not {q.dtype}")

@@ -113,6 +113,21 @@ __device__ __forceinline__ Spot spot_of(const CacheRowsArgs& a, int64_t slot) {
   return s;
 }
 
+// base + i * x + j * y, one instruction a product where the strides (in
+// bytes) have 32 bits: the eight-element kernels, whose 64-bit products
+// would be a third of their instructions.
+template <int VEC>
+__device__ __forceinline__ char* at_bytes(const void* base, uint32_t i, int64_t x, uint32_t j, int64_t y) {
+  uint64_t r = reinterpret_cast<uint64_t>(base);
+  if (VEC == 8) {
+    asm("mad.wide.u32 %0, %1, %2, %0;" : "+l"(r) : "r"(i), "r"((uint32_t)x));
+    asm("mad.wide.u32 %0, %1, %2, %0;" : "+l"(r) : "r"(j), "r"((uint32_t)y));
+  } else {
+    r += (uint64_t)i * (uint64_t)x + (uint64_t)j * (uint64_t)y;
+  }
+  return reinterpret_cast<char*>(r);
+}
+
 template <int DT, int VEC, bool QUANT, int TOK>
 __global__ void __launch_bounds__(kCacheThreads) write_kernel(const __grid_constant__ CacheRowsArgs a) {
   using D_ = DType<DT>;
@@ -122,32 +137,36 @@ __global__ void __launch_bounds__(kCacheThreads) write_kernel(const __grid_const
   const Place p = place_of(a, lanes);
   const unsigned mask = lanes == 32 ? 0xffffffffu : ((1u << lanes) - 1u) << (threadIdx.x & 31 & ~(lanes - 1));
   const topkp_cache& c = a.cache[p.side];
-  const raw* x = reinterpret_cast<const raw*>(a.in[p.side]) + p.head * a.head_stride[p.side];
-  const int64_t tok0 = (int64_t)blockIdx.x * (a.tokens * TOK) + p.token;
+  constexpr int ES = QUANT ? 1 : (int)sizeof(raw);
+  const char* x = reinterpret_cast<const char*>(a.in[p.side]) + (p.head * a.head_stride[p.side] + p.lane * VEC) * (int64_t)sizeof(raw);
+  char* o0 = reinterpret_cast<char*>(c.data) + (p.head * c.head_stride + p.lane * VEC) * ES;
+  uint8_t* e0 = QUANT ? c.exponents + p.head * c.exp_head_stride : nullptr;
+  const uint32_t tok0 = blockIdx.x * (uint32_t)(a.tokens * TOK) + p.token;
+  const bool own = p.lane * VEC < a.D;  // this lane's first piece lies in the row
 
   Spot spot[TOK];
   Rows<DT, VEC> keep[TOK][kKeep];
+  // every read is of a row that exists, wanted or not: a branch around each
+  // would make the reads wait for one another
+  int64_t slot[TOK];
 #pragma unroll
   for (int u = 0; u < TOK; ++u) {
-    const int64_t tok = tok0 + u * a.tokens;
-    spot[u] = spot_of(a, p.on && tok < a.N ? a.slots[tok] : -1);
+    const uint32_t tok = min(tok0 + u * a.tokens, (uint32_t)a.N - 1u);
+    slot[u] = a.slots[tok];
+    const char* xt = at_bytes<VEC>(x, tok, a.token_stride[p.side] * (int64_t)sizeof(raw), 0, 0);
 #pragma unroll
-    for (int i = 0; i < kKeep; ++i) {
-      const int d = (i * lanes + p.lane) * VEC;
-      if (spot[u].in && d < a.D) keep[u][i] = load_rows<DT, VEC>(x + tok * a.token_stride[p.side] + d);
-    }
+    for (int i = 0; i < kKeep; ++i)
+      if (VEC == 8 ? own : (i * lanes + p.lane) * VEC < a.D) keep[u][i] = load_rows<DT, VEC>(xt + i * lanes * VEC * sizeof(raw));
   }
 #pragma unroll
   for (int u = 0; u < TOK; ++u) {
+    spot[u] = spot_of(a, p.on && tok0 + u * a.tokens < a.N ? slot[u] : -1);
     if (!spot[u].in) continue;  // all lanes of the row alike
-    const int64_t off = spot[u].page * c.page_stride + spot[u].at * c.token_stride + p.head * c.head_stride;
+    char* o = at_bytes<VEC>(o0, spot[u].page, c.page_stride * ES, (uint32_t)spot[u].at, c.token_stride * ES);
     if (!QUANT) {
-      raw* o = reinterpret_cast<raw*>(c.data) + off;
 #pragma unroll
-      for (int i = 0; i < kKeep; ++i) {
-        const int d = (i * lanes + p.lane) * VEC;
-        if (d < a.D) store_rows<DT, VEC>(o + d, keep[u][i]);
-      }
+      for (int i = 0; i < kKeep; ++i)
+        if (VEC == 8 ? own : (i * lanes + p.lane) * VEC < a.D) store_rows<DT, VEC>(o + i * lanes * VEC * sizeof(raw), keep[u][i]);
       continue;
     }
     uint32_t amax = 0;  // magnitude bits as fp32's
@@ -156,7 +175,7 @@ __global__ void __launch_bounds__(kCacheThreads) write_kernel(const __grid_const
       // through again for its finite ones
       uint32_t two = 0;
       const uint32_t* w = reinterpret_cast<const uint32_t*>(&keep[u][0].v[0]);
-      if (p.lane * VEC < a.D) {
+      if (own) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) two = __vmaxu2(two, w[j % (VEC / 2 > 0 ? VEC / 2 : 1)] & 0x7fff7fffu);
       }
@@ -165,7 +184,7 @@ __global__ void __launch_bounds__(kCacheThreads) write_kernel(const __grid_const
       constexpr uint32_t kInf = DT == TOPKP_F16 ? 0x7c00u : 0x7f80u;
       if (top >= kInf) {
         top = 0;
-        if (p.lane * VEC < a.D) {
+        if (own) {
 #pragma unroll
           for (int j = 0; j < VEC; ++j) {
             const uint32_t m = (uint32_t)keep[u][0].v[j] & 0x7fffu;
@@ -190,27 +209,23 @@ __global__ void __launch_bounds__(kCacheThreads) write_kernel(const __grid_const
     // below the normal range (and for zeros) e stays at its lowest
     const int e = max((int)(amax >> 23) - 127 - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0), -126);
     const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-    uint8_t* o = reinterpret_cast<uint8_t*>(c.data) + off;
 #pragma unroll
     for (int i = 0; i < kKeep; ++i) {
-      const int d = (i * lanes + p.lane) * VEC;
-      if (d < a.D) {
-        const Rows<DT, VEC>& r = keep[u][i];
-        if (VEC == 1) {
-          o[d] = (uint8_t)to_e4m3x2(D_::to_float(r.v[0]) * inv, 0.0f);
-        } else {
-          uint32_t w[2];
+      if (VEC == 8 ? !own : (i * lanes + p.lane) * VEC >= a.D) continue;
+      const Rows<DT, VEC>& r = keep[u][i];
+      if (VEC == 1) {
+        o[i * lanes] = (char)to_e4m3x2(D_::to_float(r.v[0]) * inv, 0.0f);
+      } else {
+        uint32_t w[2];
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            w[j] = to_e4m3x2(D_::to_float(r.v[4 * j % VEC]) * inv, D_::to_float(r.v[(4 * j + 1) % VEC]) * inv) |
-                   (to_e4m3x2(D_::to_float(r.v[(4 * j + 2) % VEC]) * inv, D_::to_float(r.v[(4 * j + 3) % VEC]) * inv) << 16);
-          *reinterpret_cast<uint2*>(o + d) = make_uint2(w[0], w[1]);
-        }
+        for (int j = 0; j < 2; ++j)
+          w[j] = to_e4m3x2(D_::to_float(r.v[4 * j % VEC]) * inv, D_::to_float(r.v[(4 * j + 1) % VEC]) * inv) |
+                 (to_e4m3x2(D_::to_float(r.v[(4 * j + 2) % VEC]) * inv, D_::to_float(r.v[(4 * j + 3) % VEC]) * inv) << 16);
+        *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
       }
     }
     if (p.lane == 0)
-      c.exponents[spot[u].page * c.exp_page_stride + spot[u].at * c.exp_token_stride + p.head * c.exp_head_stride] =
-          (uint8_t)(e + 127);
+      *at_bytes<VEC>(e0, spot[u].page, c.exp_page_stride, (uint32_t)spot[u].at, c.exp_token_stride) = (char)(e + 127);
   }
 }
 
@@ -222,42 +237,54 @@ __global__ void __launch_bounds__(kCacheThreads) read_kernel(const __grid_consta
   const Place p = place_of(a, lanes);
   if (!p.on) return;
   const topkp_cache& c = a.cache[p.side];
-  raw* out = reinterpret_cast<raw*>(a.out[p.side]) + p.head * a.head_stride[p.side];
-  const int64_t tok0 = (int64_t)blockIdx.x * (a.tokens * TOK) + p.token;
+  constexpr int ES = QUANT ? 1 : (int)sizeof(raw);
+  char* out = reinterpret_cast<char*>(a.out[p.side]) + (p.head * a.head_stride[p.side] + p.lane * VEC) * (int64_t)sizeof(raw);
+  const char* c0 = reinterpret_cast<const char*>(c.data) + (p.head * c.head_stride + p.lane * VEC) * ES;
+  const uint8_t* e0 = QUANT ? c.exponents + p.head * c.exp_head_stride : nullptr;
+  const uint32_t tok0 = blockIdx.x * (uint32_t)(a.tokens * TOK) + p.token;
 
   Spot spot[TOK];
   Rows<DT, VEC> v[TOK][kKeep];
   uint2 w[TOK][kKeep];
   uint32_t e[TOK];
+  int64_t slot[TOK];
+#pragma unroll
+  for (int u = 0; u < TOK; ++u) slot[u] = a.slots[min(tok0 + u * a.tokens, (uint32_t)a.N - 1u)];
+  // a slot outside reads the cache's first row, and drops it
 #pragma unroll
   for (int u = 0; u < TOK; ++u) {
-    const int64_t tok = tok0 + u * a.tokens;
-    spot[u] = spot_of(a, tok < a.N ? a.slots[tok] : -1);
-    const int64_t off = spot[u].page * c.page_stride + spot[u].at * c.token_stride + p.head * c.head_stride;
-    e[u] = QUANT && spot[u].in
-               ? c.exponents[spot[u].page * c.exp_page_stride + spot[u].at * c.exp_token_stride + p.head * c.exp_head_stride]
-               : 0;
+    spot[u] = spot_of(a, slot[u]);
+    const char* from = at_bytes<VEC>(c0, spot[u].page, c.page_stride * ES, (uint32_t)spot[u].at, c.token_stride * ES);
+    e[u] = QUANT ? (uint32_t)*reinterpret_cast<const uint8_t*>(
+                       at_bytes<VEC>(e0, spot[u].page, c.exp_page_stride, (uint32_t)spot[u].at, c.exp_token_stride))
+                 : 0u;
 #pragma unroll
     for (int i = 0; i < kKeep; ++i) {
-      const int d = (i * lanes + p.lane) * VEC;
       w[u][i] = make_uint2(0, 0);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) v[u][i].v[j] = 0;
-      if (!spot[u].in || d >= a.D) continue;
-      if (!QUANT) v[u][i] = load_rows<DT, VEC>(reinterpret_cast<const raw*>(c.data) + off + d);
-      else if (VEC == 1) w[u][i].x = reinterpret_cast<const uint8_t*>(c.data)[off + d];
-      else w[u][i] = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(c.data) + off + d);
+      if ((i * lanes + p.lane) * VEC >= a.D) continue;
+      const char* f = from + i * lanes * VEC * ES;
+      if (!QUANT) v[u][i] = load_rows<DT, VEC>(f);
+      else if (VEC == 1) w[u][i].x = *reinterpret_cast<const uint8_t*>(f);
+      else w[u][i] = *reinterpret_cast<const uint2*>(f);
     }
   }
 #pragma unroll
   for (int u = 0; u < TOK; ++u) {
-    const int64_t tok = tok0 + u * a.tokens;
+    const uint32_t tok = tok0 + u * a.tokens;
     if (tok >= a.N) continue;
+    char* to = at_bytes<VEC>(out, tok, a.token_stride[p.side] * (int64_t)sizeof(raw), 0, 0);
     const float scale = spot[u].in ? __uint_as_float(e[u] ? e[u] << 23 : 0x400000u) : 0.0f;
 #pragma unroll
     for (int i = 0; i < kKeep; ++i) {
       const int d = (i * lanes + p.lane) * VEC;
       if (d >= a.D) continue;
+      if (!QUANT && !spot[u].in) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) v[u][i].v[j] = 0;
+      }
+      if (QUANT && !spot[u].in) w[u][i] = make_uint2(0, 0);
       if (QUANT && VEC == 1) {
         v[u][i].v[0] = from_float<DT>(from_e4m3x2(w[u][i].x).x * scale);
       } else if (QUANT) {
@@ -269,7 +296,7 @@ __global__ void __launch_bounds__(kCacheThreads) read_kernel(const __grid_consta
           v[u][i].v[(2 * j + 1) % VEC] = from_float<DT>(f.y * scale);
         }
       }
-      store_rows<DT, VEC>(out + tok * a.token_stride[p.side] + d, v[u][i]);
+      store_rows<DT, VEC>(to + i * lanes * VEC * sizeof(raw), v[u][i]);
     }
   }
 }

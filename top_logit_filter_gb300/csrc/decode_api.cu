@@ -244,6 +244,11 @@ bool cache_by_8(const topkp_cache& c) {
   return (uintptr_t)c.data % (unit * esize(c.dtype)) == 0 && c.page_stride % unit == 0 && c.token_stride % unit == 0 &&
          c.head_stride % unit == 0;
 }
+// Whether every stride (in bytes) that a row's place is multiplied with has 32 bits.
+bool strides_32(const topkp_cache& c) {
+  const int64_t most = 0xffffffffll / esize(c.dtype);
+  return c.page_stride <= most && c.token_stride <= most && c.exp_page_stride <= most && c.exp_token_stride <= most;
+}
 
 topkp_status cache_shapes(const char* fn, int64_t N, int64_t H, int64_t D, int64_t pages, int64_t page_size, int dtype) {
   if (!row_type(dtype)) return fail(TOPKP_ERR_PARAM_INVALID, "%s: unknown dtype %d", fn, dtype);
@@ -285,7 +290,7 @@ topkp_status topkp_cache_write(const void* k, const void* v, int64_t N, int64_t 
     if (st) return st;
     if ((uintptr_t)in[i] % es || ts[i] < 0 || hs[i] < 0)
       return fail(TOPKP_ERR_PARAM_INVALID, "%s: %s is not aligned to its element size or has a negative stride", fn, i ? "v" : "k");
-    by8 = by8 && cache_by_8(*cs[i]) && ((uintptr_t)in[i] | (uint64_t)ts[i] * es | (uint64_t)hs[i] * es) % 16 == 0;
+    by8 = by8 && cache_by_8(*cs[i]) && strides_32(*cs[i]) && ts[i] <= 0xffffffffll / es && ((uintptr_t)in[i] | (uint64_t)ts[i] * es | (uint64_t)hs[i] * es) % 16 == 0;
     a.in[i] = in[i];
     a.cache[i] = *cs[i];
     a.token_stride[i] = ts[i];
@@ -336,7 +341,7 @@ topkp_status topkp_cache_read(const int64_t* slots, int64_t N, int64_t H, int64_
     st = check_cache(fn, i ? "v_cache" : "k_cache", cs[i], H, D, pages, page_size, dtype);
     if (st) return st;
     if ((uintptr_t)out[i] % es) return fail(TOPKP_ERR_PARAM_INVALID, "%s: an output is not aligned to its element size", fn);
-    by8 = by8 && cache_by_8(*cs[i]) && (uintptr_t)out[i] % 16 == 0;
+    by8 = by8 && cache_by_8(*cs[i]) && strides_32(*cs[i]) && H * D <= 0xffffffffll / es && (uintptr_t)out[i] % 16 == 0;
     a.out[i] = out[i];
     a.cache[i] = *cs[i];
     a.token_stride[i] = H * D;

@@ -142,7 +142,8 @@ EncodeTiled encoder() {
   return fn;
 }
 // A cache as (element, head, token, page); false where TMA cannot take it.
-bool make_map(CUtensorMap* map, const topkp_cache& c, const topkp_tree_attention_args& a, int box, int width) {
+bool make_map(CUtensorMap* map, const topkp_cache& c, const topkp_tree_attention_args& a, int box, int width,
+              CUtensorMapSwizzle swizzle) {
   const bool q8 = c.dtype == TOPKP_E4M3;
   const uint64_t es = q8 ? 1 : 2;
   // a dimension of one entry may have any stride: give it one that is valid
@@ -155,14 +156,13 @@ bool make_map(CUtensorMap* map, const topkp_cache& c, const topkp_tree_attention
   const cuuint32_t boxes[4] = {(cuuint32_t)width, 1, (cuuint32_t)box, 1}, steps[4] = {1, 1, 1, 1};
   const EncodeTiled encode = encoder();
   return encode && encode(map, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, c.data, dims, strides,
-                          boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          q8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                          boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int DP, int NT, bool BF, bool Q8>
 cudaError_t launch_tc(AttnDev p, cudaStream_t s) {
-  using Shape = TcShape<DP, NT, Q8>;
+  using Shape = TcShape<DP, NT, BF, Q8>;
   const topkp_tree_attention_args& a = p.a;
   cudaError_t e = cudaFuncSetAttribute(attn_tc<DP, NT, BF, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kSmem);
   if (e != cudaSuccess) return e;
@@ -171,8 +171,11 @@ cudaError_t launch_tc(AttnDev p, cudaStream_t s) {
   p.box = kTile;
   if (a.table)
     while (p.box > 4 && a.page_size % p.box) p.box /= 2;
-  const int width = Q8 ? DP : 64;
-  if (p.box < 8 || !make_map(&km, a.k, a, p.box, width) || !make_map(&vm, a.v, a, p.box, width)) p.box = 0;
+  // operands are swizzled (rows of 128 bytes, or of 64 e4m3); raw values are not
+  constexpr auto by128 = CU_TENSOR_MAP_SWIZZLE_128B, by64 = CU_TENSOR_MAP_SWIZZLE_64B, plain = CU_TENSOR_MAP_SWIZZLE_NONE;
+  if (p.box < 8 || !make_map(&km, a.k, a, p.box, !Q8 ? 64 : DP < 128 ? DP : 128, Q8 && DP == 64 ? by64 : by128) ||
+      !make_map(&vm, a.v, a, p.box, Q8 ? DP : 64, Q8 ? plain : by128))
+    p.box = 0;
   const int64_t rows = a.T * (a.Hq / a.Hkv);
   const dim3 grid((unsigned)((rows + NT * kTcRows - 1) / (NT * kTcRows)), (unsigned)p.splits, (unsigned)(a.B * a.Hkv));
   attn_tc<DP, NT, BF, Q8><<<grid, Shape::kThreads, Shape::kSmem, s>>>(p, km, vm);

@@ -14,7 +14,7 @@
 // of tile j.  Up to 128 rows, two CTAs share an SM (eight warps each leave
 // 128 registers a thread), and one's products run under the other's softmax;
 // beyond, one CTA takes 256 rows, so that keys and values are brought (and
-// widened from e4m3) once for both tiles.  O stays in TMEM; a row's reference
+// values widened from e4m3) once for both tiles.  O stays in TMEM; a row's reference
 // maximum moves only when a tile's maximum exceeds it by 2^8, which spares
 // the rescaling of O but for the first few tiles (probabilities up to 2^8
 // lose nothing in floating point).
@@ -25,6 +25,12 @@
 // that the feeder warps widen from: sixteen values a thread, by shifts and
 // two exact products with powers of two.  Layouts TMA cannot take (pages of a
 // size that is no multiple of 8, e4m3 rows off 16 bytes) are copied plainly.
+//
+// An e4m3 key is an operand as it lies, against Q as a sum of e4m3 terms (two
+// for bf16, three for fp16, both exact but for what lies 2^18 below a row's
+// largest element); its scale is a factor of its column of S.  Values have to
+// meet probabilities, which two or three e4m3 do not hold (a far tail of
+// small ones matters together), so they are widened.
 #pragma once
 
 namespace topkp {
@@ -54,17 +60,31 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
       "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
 }
+template <bool F8>
 __device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((int)acc)
-      : "memory");
+  if (F8)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((int)acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((int)acc)
+        : "memory");
 }
+template <bool F8>
 __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((int)acc)
-      : "memory");
+  if (F8)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((int)acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((int)acc)
+        : "memory");
 }
 // 32 columns of this thread's lane.
 __device__ __forceinline__ void tc_ld32(uint32_t (&r)[32], uint32_t addr) {
@@ -116,35 +136,38 @@ __device__ __forceinline__ uint32_t swizzled(int r, int c) {
 
 __device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull; }
 
-template <int DP, int NT, bool Q8>
+template <int DP, int NT, bool BF, bool Q8>
 struct TcShape {
   static constexpr int kSoftWarps = 4 * NT;
   // 16 bits: one warp for keys, one for values; e4m3: one loads, the others widen
   static constexpr int kFeedWarps = !Q8 ? 2 : NT == 1 ? 9 : 7;
-  static constexpr int kLoadWarps = 1;
   static constexpr int kThreads = 32 * (kSoftWarps + kFeedWarps + 1);
   static constexpr int kPerSm = !Q8 && NT == 1 && DP <= 128 ? 2 : 1;
-  static constexpr int kTileBytes = kTile * DP * 2;
+  // e4m3 keys are operands as they lie: Q is then a sum of terms in e4m3
+  static constexpr int kTerms = !Q8 ? 1 : BF ? 2 : 3;
+  static constexpr int kKeyBytes = kTile * DP * (Q8 ? 1 : 2), kValueBytes = kTile * DP * 2, kRawBytes = kTile * DP;
   // Q as a shared-memory operand would be read again for every product (4 KB
-  // a step, twice what a step of 64 tokens' keys is), so it sits in TMEM,
-  // except at 128 dims where two CTAs share an SM or a CTA has two row tiles:
-  // there the second S is worth more (one S a row tile makes its two products
-  // and its softmax take turns: 714 against 640 us for trees of 64 over e4m3).
-  // TMEM columns: S, Q, O.
-  static constexpr bool kQInTmem = DP != 128 || (kPerSm == 1 && NT == 1);
-  static constexpr int kQBytes = kQInTmem ? 0 : NT * kTcRows * DP * 2;
-  // stages of keys, of values, and of raw e4m3 (both).  Keys free theirs as
+  // a step, twice what a step of 64 tokens' keys is), so it sits in TMEM
+  // where there is room; the second S is worth more (with one S a row tile,
+  // its two products and its softmax take turns).  TMEM columns: S, Q, O.
+  static constexpr int kQColumns = DP / 2 * (Q8 ? kTerms : 2) / 2;
+  static constexpr bool kQInTmem = NT * (128 + kQColumns + DP) <= 512 / kPerSm;
+  static constexpr int kQBytes = kQInTmem ? 0 : NT * kTcRows * DP * (Q8 ? kTerms : 2);
+  // stages of keys, of values, and of raw e4m3 values.  Keys free theirs as
   // soon as their product is done, well before the softmax
-  static constexpr int kKeys = Q8 ? (DP <= 128 ? 3 : 2) : DP == 64 || (DP == 128 && NT == 2) ? 4 : DP == 256 ? 3 : 2;
-  static constexpr int kValues = Q8 && DP == 256 ? 1 : Q8 && NT == 2 ? 2 : kKeys;
-  static constexpr int kRaw = !Q8 ? 0 : DP == 256 ? 2 : NT == 2 ? 3 : 4;
-  static constexpr int kRawBytes = 2 * kTile * DP;  // keys, then values
+  static constexpr int kKeys = Q8 ? (DP <= 128 ? 4 : 2) : DP == 64 || (DP == 128 && NT == 2) ? 4 : DP == 256 ? 3 : 2;
+  static constexpr int kValues = !Q8 ? kKeys : DP == 256 ? (BF ? 3 : 1) : DP == 128 && NT == 2 ? 2 : 3;
+  static constexpr int kRaw = !Q8 ? 0 : DP == 256 ? 2 : 4;
   static constexpr uint32_t kQ = NT * 128;  // after two S of 64 columns a row tile
-  static constexpr uint32_t kO = kQ + (kQInTmem ? NT * DP / 2 : 0);
+  static constexpr uint32_t kO = kQ + (kQInTmem ? NT * kQColumns : 0);
   static constexpr int kColumns = kO + NT * DP <= 256 ? 256 : 512;
-  static constexpr size_t kSmem = 1024 + kQBytes + (size_t)(kKeys + kValues) * kTileBytes + (size_t)kRaw * kRawBytes;
+  static constexpr size_t kSmem = 1024 + kQBytes + (size_t)kKeys * kKeyBytes + (size_t)kValues * kValueBytes + (size_t)kRaw * kRawBytes;
   static_assert(kO + NT * DP <= 512, "O does not fit tensor memory");
+  static_assert(kSmem * kPerSm <= 225 * 1024, "the rings do not fit shared memory");
 };
+// Tiles of keys' scales kept: a softmax reads those of a tile whose keys'
+// stage may have been filled again since, by at most kKeys + 2 tiles.
+constexpr int kScales = 8;
 
 // A box of tokens of one page: element x, head, token and page.
 __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int head, int token, int page) {
@@ -247,10 +270,30 @@ __device__ __forceinline__ uint4 fetch16(const uint8_t* p, int wide, bool both) 
   return make_uint4(lo.x, lo.y, hi.x, hi.y);
 }
 
+// Element i of a pair of the rows' type.
+template <bool BF>
+__device__ __forceinline__ float half_of(uint32_t w, int i) {
+  const uint16_t r = (uint16_t)(i ? w >> 16 : w);
+  return BF ? __uint_as_float((uint32_t)r << 16) : __half2float(__ushort_as_half(r));
+}
+// Two floats rounded to e4m3, and what they leave (exact: both have the
+// rounding's exponents).
+__device__ __forceinline__ uint32_t e4m3_of(float x, float y) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(y), "f"(x));
+  return r;
+}
+__device__ __forceinline__ void e4m3_away(uint32_t two, float& x, float& y) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
+  x -= __half2float(__ushort_as_half((uint16_t)h));
+  y -= __half2float(__ushort_as_half((uint16_t)(h >> 16)));
+}
+
 template <int DP, int NT, bool BF, bool Q8>
-__global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT, Q8>::kPerSm)
+__global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8>::kThreads, TcShape<DP, NT, BF, Q8>::kPerSm)
     attn_tc(const __grid_constant__ AttnDev p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-  using Shape = TcShape<DP, NT, Q8>;
+  using Shape = TcShape<DP, NT, BF, Q8>;
   constexpr int KS = Shape::kKeys, VS = Shape::kValues;
   constexpr int RS = Shape::kRaw > 0 ? Shape::kRaw : 1;
   constexpr int kFeed = Shape::kFeedWarps;
@@ -259,10 +302,11 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
   unsigned char* smem = tc_smem + ((1024 - (smem_u32(tc_smem) & 1023)) & 1023);
   unsigned char* sq = smem;
   unsigned char* sk = smem + Shape::kQBytes;
-  unsigned char* sv = sk + KS * Shape::kTileBytes;
-  unsigned char* raw = sv + VS * Shape::kTileBytes;
+  unsigned char* sv = sk + KS * Shape::kKeyBytes;
+  unsigned char* raw = sv + VS * Shape::kValueBytes;
   __shared__ uint64_t k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], raw_full[RS], raw_empty[RS], s_full[NT][2], p_full[NT][2], pv_done[NT], q_full;
-  __shared__ uint32_t tmem_base, sexp[RS][kTile];
+  __shared__ uint32_t tmem_base, sexp[RS][kTile];               // values' exponents
+  __shared__ __align__(16) float sscale[Q8 ? kScales : 1][kTile];  // keys' scales
   __shared__ volatile int dead;
   const topkp_tree_attention_args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -280,18 +324,17 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
   const int n = (split == p.splits - 1 ? tiles : min(t_begin + p.per, tiles)) - t_begin;
 
   if (tid == 0) {
-    constexpr int kParts = Q8 ? kFeed - Shape::kLoadWarps : 1;  // warps that fill a stage
     for (int i = 0; i < KS; ++i) {
-      mbar_init(&k_full[i], kParts);
+      mbar_init(&k_full[i], Q8 ? 2 : 1);
       mbar_init(&k_empty[i], 1);
     }
     for (int i = 0; i < VS; ++i) {
-      mbar_init(&v_full[i], kParts);
+      mbar_init(&v_full[i], Q8 ? kFeed - 1 : 1);  // warps that fill a stage
       mbar_init(&v_empty[i], 1);
     }
     for (int i = 0; i < RS; ++i) {
       mbar_init(&raw_full[i], 2);
-      mbar_init(&raw_empty[i], kFeed - Shape::kLoadWarps);
+      mbar_init(&raw_empty[i], kFeed - 1);
     }
     for (int t = 0; t < NT; ++t) {
       for (int i = 0; i < 2; ++i) {
@@ -322,6 +365,7 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
     const int node = r / G;
     const int hq = h * G + (r - node * G);
     const bool in = r < rows;
+    float q_scale = 1.0f;
     {
       // the row of Q into its place
       const uint16_t* qr = reinterpret_cast<const uint16_t*>(a.q) + b * a.q_batch_stride +
@@ -329,7 +373,68 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
       auto piece = [&](int c) {
         return in && c * 8 < a.D ? *reinterpret_cast<const uint4*>(qr + c * 8) : make_uint4(0, 0, 0, 0);
       };
-      if constexpr (Shape::kQInTmem) {
+      const uint32_t q_tmem = tm + ((uint32_t)((warp & 3) * 32) << 16) + Shape::kQ + tile * Shape::kQColumns;
+      if constexpr (Q8) {
+        // The row times a power of two that brings its largest magnitude to
+        // e4m3's top binade, as kTerms e4m3 that add up to it: 8 significant
+        // bits are two times 4, fp16's 11 three times.  Elements more than
+        // 2^17 below the largest lose what lies 2^19 below it.
+        uint32_t amax = 0;
+        bool finite = true;
+#pragma unroll 2
+        for (int c = 0; c < DP / 8; ++c) {
+          const uint4 v = piece(c);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t m = __float_as_uint(half_of<BF>(w[i >> 1], i & 1)) & 0x7fffffffu;
+            finite = finite && m < 0x7f800000u;
+            amax = max(amax, m);
+          }
+        }
+        const int e = max((int)(amax >> 23) - 127 - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0), -126);
+        const float inv = finite ? __uint_as_float((uint32_t)(127 - e) << 23) : 0.0f;
+        q_scale = finite ? __uint_as_float((uint32_t)(127 + e) << 23) : __uint_as_float(0x7fc00000u);
+#pragma unroll 1
+        for (int c = 0; c < DP / 64; ++c) {
+          uint32_t t[Shape::kTerms][16];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 v = piece(c * 8 + i);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float x[4];
+#pragma unroll
+              for (int u = 0; u < 4; ++u) x[u] = half_of<BF>(w[2 * k + (u >> 1)], u & 1) * inv;
+#pragma unroll
+              for (int term = 0; term < Shape::kTerms; ++term) {
+                const uint32_t lo = e4m3_of(x[0], x[1]), hi = e4m3_of(x[2], x[3]);
+                t[term][2 * i + k] = lo | (hi << 16);
+                e4m3_away(lo, x[0], x[1]);
+                e4m3_away(hi, x[2], x[3]);
+              }
+            }
+          }
+#pragma unroll
+          for (int term = 0; term < Shape::kTerms; ++term) {
+            if constexpr (Shape::kQInTmem) {
+              tc_st16(q_tmem + term * (DP / 4) + c * 16, t[term]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint4*>(sq + (tile * Shape::kTerms + term) * (kTcRows * DP) + swizzled<kTcRows>(tid & 127, c * 4 + i)) =
+                    make_uint4(t[term][4 * i], t[term][4 * i + 1], t[term][4 * i + 2], t[term][4 * i + 3]);
+            }
+          }
+        }
+        if constexpr (Shape::kQInTmem) {
+          tc_wait_st();
+          tc_fence_before();
+        } else {
+          fence_proxy_async_shared();
+        }
+      } else if constexpr (Shape::kQInTmem) {
 #pragma unroll
         for (int c = 0; c < DP / 64; ++c) {
           uint32_t w[32];
@@ -341,7 +446,7 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
             w[4 * i + 2] = v.z;
             w[4 * i + 3] = v.w;
           }
-          tc_st32(tm + ((uint32_t)((warp & 3) * 32) << 16) + Shape::kQ + tile * (DP / 2) + c * 32, w);
+          tc_st32(q_tmem + c * 32, w);
         }
         tc_wait_st();
         tc_fence_before();
@@ -358,7 +463,7 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
     const bool seen = in && node < nodes;
     const uint64_t bits = seen && a.tree ? a.tree[b * a.T + node] : 0;
     const bool idle = row0 + warp * 32 >= rows;  // the whole warp
-    const float sc0 = a.scale * kLog2e;
+    const float sc0 = a.scale * kLog2e * q_scale;
     const float sc = sc0 > 0.0f ? sc0 : 1.0f;  // a scale of zero or less is applied to the products first
     const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t ocol = lanes + Shape::kO + tile * DP;
@@ -379,6 +484,21 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
       tc_ld32(s1, sb + 32);
       tc_wait_ld();
       const int t0 = (t_begin + j) * kTile;
+      if (Q8) {  // the keys' scales, powers of two
+        const float4* f = reinterpret_cast<const float4*>(sscale[j % kScales]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 x = f[i], y = f[8 + i];
+          s0[4 * i] = __float_as_uint(__uint_as_float(s0[4 * i]) * x.x);
+          s0[4 * i + 1] = __float_as_uint(__uint_as_float(s0[4 * i + 1]) * x.y);
+          s0[4 * i + 2] = __float_as_uint(__uint_as_float(s0[4 * i + 2]) * x.z);
+          s0[4 * i + 3] = __float_as_uint(__uint_as_float(s0[4 * i + 3]) * x.w);
+          s1[4 * i] = __float_as_uint(__uint_as_float(s1[4 * i]) * y.x);
+          s1[4 * i + 1] = __float_as_uint(__uint_as_float(s1[4 * i + 1]) * y.y);
+          s1[4 * i + 2] = __float_as_uint(__uint_as_float(s1[4 * i + 2]) * y.z);
+          s1[4 * i + 3] = __float_as_uint(__uint_as_float(s1[4 * i + 3]) * y.w);
+        }
+      }
       if (!(sc0 > 0.0f)) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
@@ -534,7 +654,7 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
       unsigned char* ring = feeder == 0 ? sk : sv;
       uint64_t* full = feeder == 0 ? k_full : v_full;
       uint64_t* empty = feeder == 0 ? k_empty : v_empty;
-      const int S = feeder == 0 ? KS : VS;
+      const int S = feeder == 0 ? KS : VS;  // the stages are of one size here
       const uint16_t* base = reinterpret_cast<const uint16_t*>(ca.data) + h * ca.head_stride;
       const int blk = per_tile ? lane / per_tile : 0, piece = per_tile ? lane - blk * per_tile : 0;
       const bool boxed = lane < per_tile * (DP / 64);
@@ -542,11 +662,11 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
       if (boxed && n > 0) place(min(t_begin * kTile + piece * p.box, len - 1), page, at);
       int st = 0, phase = 1;  // the first round finds every stage empty
       for (int j = 0; j < n; ++j) {
-        unsigned char* dst = ring + st * Shape::kTileBytes;
+        unsigned char* dst = ring + st * Shape::kValueBytes;
         tc_wait(&empty[st], phase, &dead);
         __syncwarp();
         if (p.box && (t_begin + j + 1) * kTile <= len) {
-          if (lane == 0) mbar_arrive_expect_tx(&full[st], Shape::kTileBytes);
+          if (lane == 0) mbar_arrive_expect_tx(&full[st], Shape::kValueBytes);
           __syncwarp();
           if (boxed) {
             tma_box(dst + blk * (kTile * 128) + piece * p.box * 128, map, &full[st], blk * 64, h, at, page);
@@ -572,22 +692,25 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
         }
       }
     } else {
-      // The first warps fill the raw ring, exponents too (a fence of a warp
-      // that widens would wait for such loads), each a run of kRun tiles in
-      // turn; the others widen, keys one tile ahead of values, as the
-      // products go.
-      constexpr int kLoad = Shape::kLoadWarps;
-      constexpr uint32_t kToken = 1u << 16;  // beside a row's two exponents: there is a token
-      if (feeder < kLoad) {
+      // The first warp brings keys, which are operands as they lie, values
+      // into the raw ring, and the scales of both (a fence of a warp that
+      // widens would wait for such loads); the others widen values.
+      constexpr uint32_t kToken = 1u << 16;  // beside a value's exponent: there is a token
+      if (feeder == 0) {
         const uint8_t* ke = a.k.exponents + h * a.k.exp_head_stride;
         const uint8_t* ve = a.v.exponents + h * a.v.exp_head_stride;
-        const int piece = lane & 15;  // boxes: lanes 0-15 keys, 16-31 values
+        // boxes: lanes 0-15 keys (blocks of 128 dims), 16-31 values
+        constexpr int KW = DP < 128 ? DP : 128;  // bytes of a row of a keys' block
+        const bool val = lane >= 16;
+        const int blk = per_tile && !val ? lane / per_tile : 0, piece = per_tile ? (val ? lane - 16 : lane - blk * per_tile) : 0;
+        const bool boxed = val ? piece < per_tile : lane < per_tile * (DP / KW);
+        Ring kr = {0, 1}, rr = {0, 1};
         // All pages of a run are asked for at once, then all its exponents,
         // so that a run waits for each once: this lane's two rows of each
         // tile, and its box (outside the pool past the last token, which
         // reads as zeros).
 #pragma unroll 1
-        for (int j0 = feeder * kRun; j0 < n; j0 += kLoad * kRun) {
+        for (int j0 = 0; j0 < n; j0 += kRun) {
           // The reads are unconditional, at places that exist, and what is not
           // wanted is dropped after: a branch around each would make them wait
           // for one another.
@@ -600,7 +723,7 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
           for (int i = 0; i < kRun; ++i) place(min(t0 + i * kTile + piece * p.box, len - 1), bpage[i], bat[i]);
 #pragma unroll
           for (int i = 0; i < kRun; ++i)
-            if (piece >= per_tile || t0 + i * kTile + piece * p.box >= t_end) bpage[i] = -1;
+            if (!boxed || t0 + i * kTile + piece * p.box >= t_end) bpage[i] = -1;
           uint32_t ek[2 * kRun], ev[2 * kRun];
 #pragma unroll
           for (int i = 0; i < 2 * kRun; ++i) {
@@ -610,49 +733,90 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
             ek[i] = __ldg(ke + q * a.k.exp_page_stride + t * a.k.exp_token_stride);
             ev[i] = __ldg(ve + q * a.v.exp_page_stride + t * a.v.exp_token_stride);
           }
+#pragma unroll 1
+          for (int i = 0; i < kRun && j0 + i < n; ++i) {
+            // the run's registers are indexed by selects, not unrolled code:
+            // the roles of this kernel share the instruction cache
+            uint32_t k2[2] = {0, 0}, v2[2] = {0, 0};
+            int pg = -1, to = 0;
 #pragma unroll
-          for (int i = 0; i < 2 * kRun; ++i) e[i] = e[i] ? kToken | ek[i] | (ev[i] << 8) : 0u;
-#pragma unroll
-          for (int i = 0; i < kRun; ++i) {
-            const int rs = (j0 + i) % RS;
-            const uint32_t phase = ((j0 + i) / RS + 1) & 1;
-            if (j0 + i < n) {
-              tc_wait(&raw_empty[rs], phase, &dead);
-              __syncwarp();
-              // two arrivals: the boxes on their way, and the exponents
-              if (lane == 0) {
-                if (p.box) mbar_arrive_expect_tx(&raw_full[rs], Shape::kRawBytes);
-                else mbar_arrive(&raw_full[rs]);
+            for (int u = 0; u < kRun; ++u)
+              if (u == i) {
+                k2[0] = e[2 * u] ? ek[2 * u] : 127;
+                k2[1] = e[2 * u + 1] ? ek[2 * u + 1] : 127;
+                v2[0] = e[2 * u] ? kToken | ev[2 * u] : 0;
+                v2[1] = e[2 * u + 1] ? kToken | ev[2 * u + 1] : 0;
+                pg = bpage[u];
+                to = bat[u];
               }
+            unsigned char* kd = sk + kr.at * Shape::kKeyBytes;
+            unsigned char* vd = raw + rr.at * Shape::kRawBytes;
+            // each full barrier takes two arrivals: the boxes on their way, and what is stored here
+            tc_wait(&k_empty[kr.at], kr.phase, &dead);
+            __syncwarp();
+            if (p.box) {
+              if (lane == 0) mbar_arrive_expect_tx(&k_full[kr.at], Shape::kKeyBytes);
               __syncwarp();
-              if (piece < per_tile)
-                tma_box(raw + rs * Shape::kRawBytes + (lane >> 4) * (kTile * DP) + piece * p.box * DP, lane < 16 ? &kmap : &vmap,
-                        &raw_full[rs], 0, h, bat[i], bpage[i]);
-              sexp[rs][lane] = e[2 * i];
-              sexp[rs][lane + 32] = e[2 * i + 1];
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&raw_full[rs]);
+              if (boxed && !val) tma_box(kd + blk * (kTile * 128) + piece * p.box * KW, &kmap, &k_full[kr.at], blk * 128, h, to, pg);
+            } else {
+              if (lane == 0) mbar_arrive(&k_full[kr.at]);
+              constexpr int CH = DP / 16;
+              for (int x = lane; x < kTile * CH; x += 32) {
+                const int r = x / CH, c = x - r * CH;
+                int page1 = -1, at1 = 0;
+                if (c * 16 < a.D) find((t_begin + j0 + i) * kTile + r, page1, at1);
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (page1 >= 0)
+                  w = fetch16(reinterpret_cast<const uint8_t*>(a.k.data) + h * a.k.head_stride + (int64_t)page1 * a.k.page_stride +
+                                  (int64_t)at1 * a.k.token_stride + c * 16,
+                              p.wide, c * 16 + 8 < a.D);
+                const uint32_t off = DP == 64 ? (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4)) : swizzled<kTile>(r, c);
+                *reinterpret_cast<uint4*>(kd + off) = w;
+              }
+              fence_proxy_async_shared();
             }
+            float* f = sscale[(j0 + i) % kScales];
+            f[lane] = exponent_scale(k2[0]);
+            f[lane + 32] = exponent_scale(k2[1]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&k_full[kr.at]);
+            tc_wait(&raw_empty[rr.at], rr.phase, &dead);
+            __syncwarp();
+            if (lane == 0) {
+              if (p.box) mbar_arrive_expect_tx(&raw_full[rr.at], Shape::kRawBytes);
+              else mbar_arrive(&raw_full[rr.at]);
+            }
+            __syncwarp();
+            if (boxed && val) tma_box(vd + piece * p.box * DP, &vmap, &raw_full[rr.at], 0, h, to, pg);
+            sexp[rr.at][lane] = v2[0];
+            sexp[rr.at][lane + 32] = v2[1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&raw_full[rr.at]);
+            kr.template step<KS>();
+            rr.template step<RS>();
           }
         }
       } else {
-        const int pt = tid - 32 * (Shape::kSoftWarps + kLoad);
+        const int pt = tid - 32 * (Shape::kSoftWarps + 1);
         constexpr int CH = DP / 16;                  // 16-byte pieces of a cached row
-        constexpr int STEP = 32 * (kFeed - kLoad) / CH;  // rows between a thread's rows
+        constexpr int STEP = 32 * (kFeed - 1) / CH;  // rows between a thread's rows
         const int c = pt % CH, r0 = pt / CH;
         const bool c_in = c * 16 < a.D;
-        // This thread's pieces of one operand of tile j; rows without a token
+        // This thread's pieces of the values of tile j; rows without a token
         // become zeros whatever the box held.  All are read before the first
         // is widened.
         constexpr int NR = (kTile + STEP - 1) / STEP;
-        auto widen = [&](int rs, int j, bool values, unsigned char* dst) {
-          const unsigned char* from = raw + rs * Shape::kRawBytes + (values ? kTile * DP : 0) + c * 16;
+        Ring vr = {0, 1}, rr = {0, 0};  // an empty stage's wait starts passed
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
+          tc_wait(&raw_full[rr.at], rr.phase, &dead);
+          const unsigned char* from = raw + rr.at * Shape::kRawBytes + c * 16;
           uint4 w[NR];
           uint32_t e[NR];
 #pragma unroll
           for (int i = 0; i < NR; ++i) {
             const int r = min(r0 + i * STEP, kTile - 1);
-            e[i] = sexp[rs][r];
+            e[i] = sexp[rr.at][r];
             w[i] = *reinterpret_cast<const uint4*>(from + r * DP);
           }
           if (!p.box) {
@@ -660,12 +824,11 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
             for (int i = 0; i < NR; ++i) {
               uint4 x = make_uint4(0, 0, 0, 0);
               const int r = min(r0 + i * STEP, kTile - 1);
-              if ((sexp[rs][r] & kToken) && c_in) {
-                const topkp_cache& ca = values ? a.v : a.k;
+              if ((sexp[rr.at][r] & kToken) && c_in) {
                 int page, at;
                 find((t_begin + j) * kTile + r, page, at);
-                x = fetch16(reinterpret_cast<const uint8_t*>(ca.data) + h * ca.head_stride + (int64_t)page * ca.page_stride +
-                                (int64_t)at * ca.token_stride + c * 16,
+                x = fetch16(reinterpret_cast<const uint8_t*>(a.v.data) + h * a.v.head_stride + (int64_t)page * a.v.page_stride +
+                                (int64_t)at * a.v.token_stride + c * 16,
                             p.wide, c * 16 + 8 < a.D);
               }
 #pragma unroll
@@ -673,42 +836,27 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
                 if (k == i) w[k] = x;
             }
           }
+          tc_wait(&v_empty[vr.at], vr.phase, &dead);
+          unsigned char* dst = sv + vr.at * Shape::kValueBytes;
+          if (r0 < STEP) {
 #pragma unroll
-          for (int i = 0; i < NR; ++i) {
-            const int r = r0 + i * STEP;
-            if (NR * STEP != kTile && r >= kTile) continue;
-            if (!(e[i] & kToken)) w[i] = make_uint4(0, 0, 0, 0);
-            uint4 lo, hi;
-            widen16<BF>(w[i], (values ? e[i] >> 8 : e[i]) & 0xff, lo, hi);
-            *reinterpret_cast<uint4*>(dst + swizzled<kTile>(r, 2 * c)) = lo;
-            *reinterpret_cast<uint4*>(dst + swizzled<kTile>(r, 2 * c + 1)) = hi;
+            for (int i = 0; i < NR; ++i) {
+              const int r = r0 + i * STEP;
+              if (NR * STEP != kTile && r >= kTile) continue;
+              if (!(e[i] & kToken)) w[i] = make_uint4(0, 0, 0, 0);
+              uint4 lo, hi;
+              widen16<BF>(w[i], e[i] & 0xff, lo, hi);
+              *reinterpret_cast<uint4*>(dst + swizzled<kTile>(r, 2 * c)) = lo;
+              *reinterpret_cast<uint4*>(dst + swizzled<kTile>(r, 2 * c + 1)) = hi;
+            }
           }
-        };
-        Ring kr = {0, 1}, vr = {0, 1}, rr = {0, 0};  // an empty stage's wait starts passed
-        int r_last = 0;
-        for (int j = 0; j <= n && n > 0; ++j) {
-          if (j < n) {
-            tc_wait(&raw_full[rr.at], rr.phase, &dead);
-            tc_wait(&k_empty[kr.at], kr.phase, &dead);
-            if (r0 < STEP) widen(rr.at, j, false, sk + kr.at * Shape::kTileBytes);
-          }
-          if (j > 0) {
-            tc_wait(&v_empty[vr.at], vr.phase, &dead);
-            if (r0 < STEP) widen(r_last, j - 1, true, sv + vr.at * Shape::kTileBytes);
-          }
-          // one fence for both
           fence_proxy_async_shared();
           __syncwarp();
           if (lane == 0) {
-            if (j < n) mbar_arrive(&k_full[kr.at]);
-            if (j > 0) {
-              mbar_arrive(&v_full[vr.at]);
-              mbar_arrive(&raw_empty[r_last]);
-            }
+            mbar_arrive(&v_full[vr.at]);
+            mbar_arrive(&raw_empty[rr.at]);
           }
-          if (j > 0) vr.template step<VS>();
-          kr.template step<KS>();
-          r_last = rr.at;
+          vr.template step<VS>();
           rr.template step<RS>();
         }
       }
@@ -717,23 +865,34 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
     // ---- matrix instructions ----
     constexpr uint32_t kind = BF ? 1u : 0u;
     constexpr uint32_t common = (1u << 4) | (kind << 7) | (kind << 10) | ((uint32_t)(kTcRows / 16) << 24);
-    constexpr uint32_t i_qk = common | ((uint32_t)(kTile / 8) << 17);
+    // e4m3 by e4m3 takes 32 dims a step: both formats are code 0
+    constexpr uint32_t i_qk = (Q8 ? (1u << 4) | ((uint32_t)(kTcRows / 16) << 24) : common) | ((uint32_t)(kTile / 8) << 17);
     constexpr uint32_t i_pv = common | (1u << 16) | ((uint32_t)(DP / 8) << 17);
     const uint32_t q0 = smem_u32(sq), k0 = smem_u32(sk), v0 = smem_u32(sv);
     Ring kr = {0, 0}, vr = {0, 0};
     // S of row tile t against the keys of stage kr, into buffer `buf`
     auto product_s = [&](int t, int buf) {
-      const uint64_t kd = operand(k0 + kr.at * Shape::kTileBytes, 16, 1024);
       const uint32_t d = tm + (t * 2 + buf) * 64;
+      const uint32_t ka = k0 + kr.at * Shape::kKeyBytes;
+      // rows of 128 bytes swizzled over eight, or (64 e4m3) of 64 bytes
+      const uint64_t kd = Q8 && DP == 64 ? (operand(ka, 16, 512) & ~(7ull << 61)) | (4ull << 61) : operand(ka, 16, 1024);
+      constexpr int STEPS = DP / (Q8 ? 32 : 16);
+      // in 16-byte units a step is 2, a block of 128 bytes of the tile's rows kTile * 8
       if constexpr (Shape::kQInTmem) {
-        const uint32_t qa = tm + Shape::kQ + t * (DP / 2);
+        const uint32_t qa = tm + Shape::kQ + t * Shape::kQColumns;
 #pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk) tc_mma_ts(d, qa + kk * 8, kd + (kk / 4) * (kTile * 8) + (kk % 4) * 2, i_qk, kk > 0);
+        for (int term = 0; term < Shape::kTerms; ++term)
+#pragma unroll
+          for (int kk = 0; kk < STEPS; ++kk)
+            tc_mma_ts<Q8>(d, qa + (term * STEPS + kk) * 8, kd + (kk / 4) * (kTile * 8) + (kk % 4) * 2, i_qk, term + kk > 0);
       } else {
-        const uint64_t qd = operand(q0 + t * (kTcRows * DP * 2), 16, 1024);
+        const uint64_t qd = operand(q0 + t * (Shape::kQBytes / NT), 16, 1024);
 #pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk)  // 16-byte units: a step of 16 dims, a block of 64
-          tc_mma_ss(d, qd + (kk / 4) * (kTcRows * 8) + (kk % 4) * 2, kd + (kk / 4) * (kTile * 8) + (kk % 4) * 2, i_qk, kk > 0);
+        for (int term = 0; term < Shape::kTerms; ++term)
+#pragma unroll
+          for (int kk = 0; kk < STEPS; ++kk)
+            tc_mma_ss<Q8>(d, qd + term * (kTcRows * DP / 16) + (kk / 4) * (kTcRows * 8) + (kk % 4) * 2,
+                          kd + (kk / 4) * (kTile * 8) + (kk % 4) * 2, i_qk, term + kk > 0);
       }
       if (t == NT - 1) tc_commit(&k_empty[kr.at]);
       tc_commit(&s_full[t][buf]);
@@ -762,11 +921,11 @@ __global__ void __launch_bounds__(TcShape<DP, NT, Q8>::kThreads, TcShape<DP, NT,
         tc_wait(&p_full[t][buf], (j >> 1) & 1, &dead);
         if (t == 0) tc_wait(&v_full[vr.at], vr.phase, &dead);
         tc_fence_after();
-        const uint64_t vd = operand(v0 + vr.at * Shape::kTileBytes, kTile * 128, 1024);
+        const uint64_t vd = operand(v0 + vr.at * Shape::kValueBytes, kTile * 128, 1024);
         const uint32_t pa = tm + (t * 2 + buf) * 64;
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)
-          tc_mma_ts(tm + Shape::kO + t * DP, pa + kk * 8, vd + kk * 128, i_pv, j > 0 || kk > 0);
+          tc_mma_ts<false>(tm + Shape::kO + t * DP, pa + kk * 8, vd + kk * 128, i_pv, j > 0 || kk > 0);
         if (t == NT - 1) tc_commit(&v_empty[vr.at]);
         tc_commit(&pv_done[t]);
       }

@@ -49,6 +49,28 @@ __device__ __forceinline__ float exp2_approx(float t) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
   return e;
 }
+// Two fp32 in 64 bits, one instruction for both.
+__device__ __forceinline__ uint64_t two_f32(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void of_two(uint64_t v, uint32_t& lo, uint32_t& hi) { asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t mul_two(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_two(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_two(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 // The next three are called by a whole warp and executed by one thread of it
@@ -485,18 +507,14 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8>::kThreads, TcShape<DP,
       tc_wait_ld();
       const int t0 = (t_begin + j) * kTile;
       if (Q8) {  // the keys' scales, powers of two
-        const float4* f = reinterpret_cast<const float4*>(sscale[j % kScales]);
+        const ulonglong2* f = reinterpret_cast<const ulonglong2*>(sscale[j % kScales]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float4 x = f[i], y = f[8 + i];
-          s0[4 * i] = __float_as_uint(__uint_as_float(s0[4 * i]) * x.x);
-          s0[4 * i + 1] = __float_as_uint(__uint_as_float(s0[4 * i + 1]) * x.y);
-          s0[4 * i + 2] = __float_as_uint(__uint_as_float(s0[4 * i + 2]) * x.z);
-          s0[4 * i + 3] = __float_as_uint(__uint_as_float(s0[4 * i + 3]) * x.w);
-          s1[4 * i] = __float_as_uint(__uint_as_float(s1[4 * i]) * y.x);
-          s1[4 * i + 1] = __float_as_uint(__uint_as_float(s1[4 * i + 1]) * y.y);
-          s1[4 * i + 2] = __float_as_uint(__uint_as_float(s1[4 * i + 2]) * y.z);
-          s1[4 * i + 3] = __float_as_uint(__uint_as_float(s1[4 * i + 3]) * y.w);
+          const ulonglong2 x = f[i], y = f[8 + i];
+          of_two(mul_two(two_f32(s0[4 * i], s0[4 * i + 1]), x.x), s0[4 * i], s0[4 * i + 1]);
+          of_two(mul_two(two_f32(s0[4 * i + 2], s0[4 * i + 3]), x.y), s0[4 * i + 2], s0[4 * i + 3]);
+          of_two(mul_two(two_f32(s1[4 * i], s1[4 * i + 1]), y.x), s1[4 * i], s1[4 * i + 1]);
+          of_two(mul_two(two_f32(s1[4 * i + 2], s1[4 * i + 3]), y.y), s1[4 * i + 2], s1[4 * i + 3]);
         }
       }
       if (!(sc0 > 0.0f)) {
@@ -520,9 +538,10 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8>::kThreads, TcShape<DP,
           s1[i] = v1 & (1u << i) ? s1[i] : 0xff800000u;
         }
       }
-      float mx = -INFINITY;
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // four chains
 #pragma unroll
-      for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fmaxf(__uint_as_float(s0[i]), __uint_as_float(s1[i])));
+      for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], fmaxf(__uint_as_float(s0[i]), __uint_as_float(s1[i])));
+      const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
       const float top = mx == -INFINITY ? -INFINITY : mx * sc;
       if (j == 0) {
         m = top;
@@ -549,20 +568,26 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8>::kThreads, TcShape<DP,
         }
       }
       const float base = m == -INFINITY ? 0.0f : m;
-      float sum0 = 0.0f, sum1 = 0.0f;
+      const uint64_t sc2 = two_f32(__float_as_uint(sc), __float_as_uint(sc)), base2 = two_f32(__float_as_uint(-base), __float_as_uint(-base));
+      uint64_t sum0 = 0ull, sum1 = 0ull;
       uint32_t pk[32];
 #pragma unroll
       for (int i = 0; i < 32; i += 2) {
-        const float x0 = exp2_approx(fmaf(__uint_as_float(s0[i]), sc, -base));
-        const float x1 = exp2_approx(fmaf(__uint_as_float(s0[i + 1]), sc, -base));
-        const float y0 = exp2_approx(fmaf(__uint_as_float(s1[i]), sc, -base));
-        const float y1 = exp2_approx(fmaf(__uint_as_float(s1[i + 1]), sc, -base));
-        sum0 += x0 + y0;
-        sum1 += x1 + y1;
-        pk[i / 2] = pack2<BF>(x0, x1);
-        pk[16 + i / 2] = pack2<BF>(y0, y1);
+        uint32_t x0, x1, y0, y1;
+        of_two(fma_two(two_f32(s0[i], s0[i + 1]), sc2, base2), x0, x1);
+        of_two(fma_two(two_f32(s1[i], s1[i + 1]), sc2, base2), y0, y1);
+        const float p0 = exp2_approx(__uint_as_float(x0)), p1 = exp2_approx(__uint_as_float(x1));
+        const float r0 = exp2_approx(__uint_as_float(y0)), r1 = exp2_approx(__uint_as_float(y1));
+        sum0 = add_two(sum0, two_f32(__float_as_uint(p0), __float_as_uint(p1)));
+        sum1 = add_two(sum1, two_f32(__float_as_uint(r0), __float_as_uint(r1)));
+        pk[i / 2] = pack2<BF>(p0, p1);
+        pk[16 + i / 2] = pack2<BF>(r0, r1);
       }
-      l += sum0 + sum1;
+      {
+        uint32_t x0, x1;
+        of_two(add_two(sum0, sum1), x0, x1);
+        l += __uint_as_float(x0) + __uint_as_float(x1);
+      }
       tc_st32(sb, pk);
       tc_wait_st();
       tc_fence_before();

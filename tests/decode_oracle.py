@@ -44,7 +44,8 @@ def quantise(x):
 
 def attention(q, k, v, ctx, n, sees, scale):
     """One request.  q [T, Hq, D], k, v [len, Hkv, D] float64 (tokens 0 .. ctx + n), sees [T, n] bool.
-    Returns out, lse, weight sums of |v| and a bound of the products' magnitude."""
+    Returns out, lse, weight sums of |v|, a bound of the products' magnitude, and how far a product may be off where
+    Q is a sum of e4m3 terms: each element by half of e4m3's smallest step, 2^-10, with the row's largest at 224 or more."""
     T, Hq, D = q.shape
     L, Hkv = k.shape[0], k.shape[1]
     G = Hq // Hkv
@@ -52,6 +53,7 @@ def attention(q, k, v, ctx, n, sees, scale):
     lse = torch.full((T, Hq), -math.inf, dtype=torch.float64)
     absv = torch.zeros(T, Hq, D, dtype=torch.float64)
     big = torch.zeros(T, Hq, dtype=torch.float64)
+    off = torch.zeros(T, Hq, dtype=torch.float64)
     for i in range(T):
         vis = torch.zeros(L, dtype=torch.bool)
         if i < n:
@@ -69,15 +71,16 @@ def attention(q, k, v, ctx, n, sees, scale):
             absv[i, h] = p @ vv.abs() / t
             lse[i, h] = m + torch.log(t)
             big[i, h] = (kk.abs() @ q[i, h].abs()).max() * scale
-    return out, lse, absv, big
+            off[i, h] = kk.abs().sum(1).max() * q[i, h].abs().max() * scale * 2.0 ** -17
+    return out, lse, absv, big, off
 
 
-def attention_bounds(dtype, out, lse, absv, big, L, D, vmax):
+def attention_bounds(dtype, out, lse, absv, big, L, D, vmax, off=0):
     """How far a result may be: the output's own rounding, the probabilities'
     (relative to the type, with fp16's absolute 2^-25 below its normal
     range), the products' fp32 sums, and the exponentials' and sums' fp32."""
     u, e32 = HALF[dtype], 2.0 ** -24
-    ds = (D + 8) * e32 * big                      # a product of D terms in fp32, scaled
+    ds = (D + 8) * e32 * big + off                # a product of D terms in fp32, scaled
     rel = 2 * ds + (L + 64) * e32 + 2.0 ** -21
     tol = u * out.abs() + absv * (u * (1 + u) + rel[..., None]) + 1e-30
     if dtype == torch.float16:

@@ -328,7 +328,7 @@ def make_tree(B, T, seed, empty=False):
 
 
 def attend(tk, dtype, cache, T, Hq, Hkv, D, P, contexts, tree=None, nodes=None, seed=0, capacity=None, scale=None,
-           max_context=None, gap=False, extra=2, stream=None, vfill=math.nan):
+           max_context=None, gap=False, extra=2, vfill=math.nan, spread=0.0, kv=(1.0, 1.5), qsize=1.2):
     """Builds a cache that holds NaN wherever no live token is, runs the call, checks every element."""
     g = torch.Generator().manual_seed(seed)
     B = len(contexts)
@@ -349,7 +349,8 @@ def attend(tk, dtype, cache, T, Hq, Hkv, D, P, contexts, tree=None, nodes=None, 
         t = torch.arange(ln)
         page, at = (table[b].long()[t // P], t % P) if paged else (torch.full((ln,), b), t)
         for i in (0, 1):
-            x = torch.randn(ln, Hkv, D, generator=g) * (1.0 if i == 0 else 1.5)
+            x = torch.randn(ln, Hkv, D, generator=g) * kv[i]
+            x = x * torch.exp(spread * torch.randn(ln, Hkv, 1, generator=g))
             if quant:
                 q, e = R.quantise(x)
                 full[i][page, at] = q.float()
@@ -357,7 +358,8 @@ def attend(tk, dtype, cache, T, Hq, Hkv, D, P, contexts, tree=None, nodes=None, 
             else:
                 full[i][page, at] = x
     store = [x.to(kind) for x in full]
-    q = (torch.randn(B, T, Hq, D, generator=g) * 1.2).to(T_[dtype])
+    q = torch.randn(B, T, Hq, D, generator=g) * qsize
+    q = (q * torch.exp(2 * spread * torch.randn(B, T, Hq, D, generator=g))).to(T_[dtype])
     bits, words = (None, None) if tree is None else tree
     scale = D ** -0.5 if scale is None else scale
     dev = [x.cuda() for x in store]
@@ -385,9 +387,9 @@ def attend(tk, dtype, cache, T, Hq, Hkv, D, P, contexts, tree=None, nodes=None, 
         if quant:
             k, v = (torch.ldexp(x, e[page, at][..., None] - 127) for x, e in zip((k, v), exps))
         sees = (torch.tril(torch.ones(T, T, dtype=torch.bool)) if bits is None else bits[b])[:, :n]
-        o, l, absv, big = R.attention(q[b].double(), k, v, ctx, n, sees, scale)
+        o, l, absv, big, off = R.attention(q[b].double(), k, v, ctx, n, sees, scale)
         vmax = float(v.abs().max()) if v.numel() else 0.0
-        tol, ltol = R.attention_bounds(T_[dtype], o, l, absv, big, lens[b], D, vmax)
+        tol, ltol = R.attention_bounds(T_[dtype], o, l, absv, big, lens[b], D, vmax, off if quant else 0)
         bad = ~((out[b] - o).abs() <= tol)
         assert not bad.any(), (b, contexts[b], bad.nonzero()[0].tolist(), float((out[b] - o).abs().max()))
         assert torch.equal(torch.isinf(lse[b]), torch.isinf(l)), (b, contexts[b])
@@ -411,6 +413,42 @@ def test_attention_long_and_split(tk, cache, T, G, D, P):
     attend(tk, "bf16", cache, T, G, 1, D, P, [5000, 2999, 1, 0], tree=make_tree(4, T, 3), seed=7)
     attend(tk, "bf16", cache, T, G, 1, D, P, [9001], seed=8)
     attend(tk, "bf16", cache, T, G, 1, D, P, [700, 2100], seed=9, max_context=64)   # the bound is wrong: results are not
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T,G,D", [(1, 4, 128), (20, 4, 64), (64, 4, 128), (8, 2, 256)])
+def test_attention_quantised_sizes(tk, dtype, T, G, D):
+    """Rows of very different scales, and all-large or all-small keys, values and queries."""
+    attend(tk, dtype, "e4m3", T, G, 1, D, 16, [300, 70], spread=1.0, seed=1)
+    attend(tk, dtype, "e4m3", T, G, 1, D, 16, [300, 70], kv=(30.0, 800.0), qsize=0.02, seed=2)
+    attend(tk, dtype, "e4m3", T, G, 1, D, 16, [300, 70], kv=(2e-3, 0.01), qsize=200.0, seed=3)
+    if dtype == "bf16":   # scales beyond 2^7, and far below fp16's range
+        attend(tk, dtype, "e4m3", T, G, 1, D, 16, [300, 70], kv=(1e6, 1e7), qsize=1e-6, seed=4)
+        attend(tk, dtype, "e4m3", T, G, 1, D, 16, [300, 70], kv=(1e-9, 1e-12), qsize=1e8, seed=5)
+
+
+def test_attention_nan_goes_where_it_is_seen(tk):
+    """A value or key that is NaN spoils the rows that see it (e4m3's NaN code too)."""
+    g = torch.Generator().manual_seed(1)
+    for cache in ("bf16", "e4m3"):
+        B, T, Hq, D = 2, 3, 4, 128
+        k, v = (torch.randn(B, 40, 1, D, generator=g) for _ in (0, 1))
+        k[0, 5, 0, 7] = math.nan
+        v[1, 6, 0, 9] = math.nan
+        q = torch.randn(B, T, Hq, D, generator=g).to(torch.bfloat16).cuda()
+        ctx = torch.tensor([30, 30], dtype=torch.int32).cuda()
+        kw = {}
+        if cache == "e4m3":
+            kc, vc = (torch.zeros(B, 40, 1, D, dtype=torch.uint8, device="cuda").view(R.E4M3) for _ in (0, 1))
+            ke, ve = (torch.zeros(B, 40, 1, dtype=torch.uint8, device="cuda") for _ in (0, 1))
+            tk.cache_write(k.reshape(-1, 1, D).to(torch.bfloat16).cuda(), v.reshape(-1, 1, D).to(torch.bfloat16).cuda(),
+                           torch.arange(B * 40, device="cuda"), kc, vc, k_exp=ke, v_exp=ve)
+            kw = dict(k_exp=ke, v_exp=ve)
+        else:
+            kc, vc = k.to(torch.bfloat16).cuda(), v.to(torch.bfloat16).cuda()
+        out = tk.tree_attention(q, kc, vc, ctx, **kw).cpu()
+        assert torch.isnan(out[0]).all()
+        assert torch.isnan(out[1, :, :, 9]).all() and torch.isfinite(out[1, :, :, :9]).all() and torch.isfinite(out[1, :, :, 10:]).all()
 
 
 @pytest.mark.parametrize("T", [4, 33])

@@ -214,7 +214,7 @@ AttnPlan plan_attention(const topkp_tree_attention_args& a, int num_sms) {
   // to), four tiles for a CTA's start and end, and writing and reading the
   // partial outputs.
   const int64_t nt = row_tiles(a);
-  const double slots = (a.D > 128 || nt == 2 || a.k.dtype == TOPKP_E4M3 ? 1.0 : 2.0) * num_sms;
+  const double slots = (nt == 2 || a.D > (a.k.dtype == TOPKP_E4M3 ? 64 : 128) ? 1.0 : 2.0) * num_sms;
   const double base = (double)(a.B * a.Hkv * ((rows + nt * kTcRows - 1) / (nt * kTcRows)));
   // a tile takes a CTA about 0.9 us (1.3 with two of them on an SM); a part
   // of every row costs 8 bytes an element at the copy's rate

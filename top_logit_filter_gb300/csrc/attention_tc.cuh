@@ -162,9 +162,11 @@ template <int DP, int NT, bool BF, bool Q8>
 struct TcShape {
   static constexpr int kSoftWarps = 4 * NT;
   // 16 bits: one warp for keys, one for values; e4m3: one loads, the others widen
-  static constexpr int kFeedWarps = !Q8 ? 2 : NT == 1 ? 9 : 7;
+  static constexpr int kFeedWarps = !Q8 ? 2 : NT == 2 ? 7 : DP >= 128 ? 9 : 3;
   static constexpr int kThreads = 32 * (kSoftWarps + kFeedWarps + 1);
-  static constexpr int kPerSm = !Q8 && NT == 1 && DP <= 128 ? 2 : 1;
+  // two CTAs leave room for two warps that widen, enough for 64 dims only
+  // (128 rows of 128 dims over e4m3: 258 us with two CTAs, 228 with one)
+  static constexpr int kPerSm = NT == 1 && DP <= (Q8 ? 64 : 128) ? 2 : 1;
   // e4m3 keys are operands as they lie: Q is then a sum of terms in e4m3
   static constexpr int kTerms = !Q8 ? 1 : BF ? 2 : 3;
   static constexpr int kKeyBytes = kTile * DP * (Q8 ? 1 : 2), kValueBytes = kTile * DP * 2, kRawBytes = kTile * DP;
@@ -828,46 +830,48 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8>::kThreads, TcShape<DP,
         const int c = pt % CH, r0 = pt / CH;
         const bool c_in = c * 16 < a.D;
         // This thread's pieces of the values of tile j; rows without a token
-        // become zeros whatever the box held.  All are read before the first
-        // is widened.
+        // become zeros whatever the box held.  Two or
+        // three are read before the first is widened.
         constexpr int NR = (kTile + STEP - 1) / STEP;
+        constexpr int NB = NR % 3 == 0 ? 3 : NR % 2 == 0 ? 2 : 1;  // at a time
         Ring vr = {0, 1}, rr = {0, 0};  // an empty stage's wait starts passed
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
           tc_wait(&raw_full[rr.at], rr.phase, &dead);
-          const unsigned char* from = raw + rr.at * Shape::kRawBytes + c * 16;
-          uint4 w[NR];
-          uint32_t e[NR];
-#pragma unroll
-          for (int i = 0; i < NR; ++i) {
-            const int r = min(r0 + i * STEP, kTile - 1);
-            e[i] = sexp[rr.at][r];
-            w[i] = *reinterpret_cast<const uint4*>(from + r * DP);
-          }
-          if (!p.box) {
-#pragma unroll 1
-            for (int i = 0; i < NR; ++i) {
-              uint4 x = make_uint4(0, 0, 0, 0);
-              const int r = min(r0 + i * STEP, kTile - 1);
-              if ((sexp[rr.at][r] & kToken) && c_in) {
-                int page, at;
-                find((t_begin + j) * kTile + r, page, at);
-                x = fetch16(reinterpret_cast<const uint8_t*>(a.v.data) + h * a.v.head_stride + (int64_t)page * a.v.page_stride +
-                                (int64_t)at * a.v.token_stride + c * 16,
-                            p.wide, c * 16 + 8 < a.D);
-              }
-#pragma unroll
-              for (int k = 0; k < NR; ++k)
-                if (k == i) w[k] = x;
-            }
-          }
           tc_wait(&v_empty[vr.at], vr.phase, &dead);
+          const unsigned char* from = raw + rr.at * Shape::kRawBytes + c * 16;
           unsigned char* dst = sv + vr.at * Shape::kValueBytes;
-          if (r0 < STEP) {
+#pragma unroll 1
+          for (int i0 = 0; i0 < NR; i0 += NB) {
+            uint4 w[NB];
+            uint32_t e[NB];
 #pragma unroll
-            for (int i = 0; i < NR; ++i) {
-              const int r = r0 + i * STEP;
-              if (NR * STEP != kTile && r >= kTile) continue;
+            for (int i = 0; i < NB; ++i) {
+              const int r = min(r0 + (i0 + i) * STEP, kTile - 1);
+              e[i] = sexp[rr.at][r];
+              w[i] = *reinterpret_cast<const uint4*>(from + r * DP);
+            }
+            if (!p.box) {
+#pragma unroll 1
+              for (int i = 0; i < NB; ++i) {
+                uint4 x = make_uint4(0, 0, 0, 0);
+                const int r = min(r0 + (i0 + i) * STEP, kTile - 1);
+                if ((sexp[rr.at][r] & kToken) && c_in) {
+                  int page, at;
+                  find((t_begin + j) * kTile + r, page, at);
+                  x = fetch16(reinterpret_cast<const uint8_t*>(a.v.data) + h * a.v.head_stride + (int64_t)page * a.v.page_stride +
+                                  (int64_t)at * a.v.token_stride + c * 16,
+                              p.wide, c * 16 + 8 < a.D);
+                }
+#pragma unroll
+                for (int k = 0; k < NB; ++k)
+                  if (k == i) w[k] = x;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+              const int r = r0 + (i0 + i) * STEP;
+              if (r0 >= STEP || (NR * STEP != kTile && r >= kTile)) continue;
               if (!(e[i] & kToken)) w[i] = make_uint4(0, 0, 0, 0);
               uint4 lo, hi;
               widen16<BF>(w[i], e[i] & 0xff, lo, hi);

@@ -32,6 +32,23 @@ def test_exports_match_the_header(lib):
         assert hasattr(lib, name), name
 
 
+def test_header_is_c(tmp_path):
+    """include/topkp_decode.h compiles as C99, and its structures are those of the binding."""
+    import shutil
+    import subprocess
+    from top_logit_filter_gb300 import _lib
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    src = tmp_path / "sizes.c"
+    src.write_text('#include <stdio.h>\n#include "topkp_decode.h"\nint main(void) { printf("%zu %zu %zu", sizeof(topkp_state), '
+                   'sizeof(topkp_cache), sizeof(topkp_tree_attention_args)); return 0; }\n')
+    exe = str(tmp_path / "sizes")
+    subprocess.run([cc, "-std=c99", "-Wall", "-Werror", "-I", os.path.join(ROOT, "include"), str(src), "-o", exe], check=True)
+    got = [int(x) for x in subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split()]
+    assert got == [ctypes.sizeof(t) for t in (_lib.State, _lib.Cache, _lib.TreeAttentionArgs)]
+
+
 def test_beam_select_refusals(lib):
     def call(x=FAKE, B=2, K=3, V=8, ld=8, dt=BF16, sc=FAKE + MB, fin=None, pad=0, n=4, o=(2, 3, 4), ws=5, wn=1 << 16):
         outs = [None if i is None else FAKE + i * MB for i in o]

@@ -97,17 +97,17 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.topkp_beam_select.argtypes = [vp, i64, i64, i64, i64, c_int, vp, vp, ctypes.c_int32, ctypes.c_int32, vp, vp, vp,
                                       vp, ctypes.c_size_t, vp]
     lib.topkp_beam_select.restype = c_int
-    lib.topkp_beam_reorder.argtypes = [ctypes.POINTER(State), i64, i64, i64, vp, vp, vp]
+    lib.topkp_beam_reorder.argtypes = [vp, i64, i64, i64, vp, vp, vp]
     lib.topkp_beam_reorder.restype = c_int
-    lib.topkp_cache_write.argtypes = [vp, vp, i64, i64, i64, i64, i64, i64, i64, c_int, vp, ctypes.POINTER(Cache),
-                                      ctypes.POINTER(Cache), i64, i64, vp]
+    lib.topkp_cache_write.argtypes = [vp, vp, i64, i64, i64, i64, i64, i64, i64, c_int, vp, vp,
+                                      vp, i64, i64, vp]
     lib.topkp_cache_write.restype = c_int
-    lib.topkp_cache_read.argtypes = [vp, i64, i64, i64, ctypes.POINTER(Cache), ctypes.POINTER(Cache), i64, i64, c_int,
+    lib.topkp_cache_read.argtypes = [vp, i64, i64, i64, vp, vp, i64, i64, c_int,
                                      vp, vp, vp]
     lib.topkp_cache_read.restype = c_int
-    lib.topkp_tree_attention_workspace_size.argtypes = [ctypes.POINTER(TreeAttentionArgs)]
+    lib.topkp_tree_attention_workspace_size.argtypes = [vp]
     lib.topkp_tree_attention_workspace_size.restype = ctypes.c_size_t
-    lib.topkp_tree_attention.argtypes = [ctypes.POINTER(TreeAttentionArgs), vp]
+    lib.topkp_tree_attention.argtypes = [vp, vp]
     lib.topkp_tree_attention.restype = c_int
     lib.topkp_last_error_string.argtypes = []
     lib.topkp_last_error_string.restype = ctypes.c_char_p

@@ -16,19 +16,29 @@ head).  Every call runs forward only: none records a gradient.
 """
 from __future__ import annotations
 
-import ctypes
+import struct
 
 from . import TopKPError, _lib
 
 torch = None    # imported by the first call, as the package itself does
 _CODES = {}     # torch dtype -> topkp_dtype
+_E4M3 = None    # torch.float8_e4m3fn
+
+# The C structures, packed straight from Python values: a ctypes.Structure
+# takes several times as long to fill, which is most of a small call's time.
+_CACHE = struct.Struct("=QQi4x6q")
+_STATE = struct.Struct("=QQ7q")
+_ATTENTION = struct.Struct("=QQQ" + 2 * "QQi4x6q" + "QQQQQQ16qif")
+assert _CACHE.size == _lib.ctypes.sizeof(_lib.Cache) and _STATE.size == _lib.ctypes.sizeof(_lib.State)
+assert _ATTENTION.size == _lib.ctypes.sizeof(_lib.TreeAttentionArgs)
 
 
 def _ready():
     """The loaded library; imports torch once."""
-    global torch
+    global torch, _E4M3
     if torch is None:
         import torch as module
+        _E4M3 = module.float8_e4m3fn
         _CODES.update({module.float32: _lib.TOPKP_F32, module.float16: _lib.TOPKP_F16, module.bfloat16: _lib.TOPKP_BF16})
         torch = module
     return _lib._lib or _lib.load()
@@ -43,7 +53,7 @@ def _dtype_code(t) -> int:
 
 def _ptr(t):
     # a present but empty tensor may have no address: any one will do, since empty problems return before it is used
-    return None if t is None else t.data_ptr() or (16 if t.numel() == 0 else None)
+    return 0 if t is None else t.data_ptr() or (16 if t.numel() == 0 else 0)
 
 
 def _cuda(t, name, dim=None, dtype=None, device=None):
@@ -188,37 +198,48 @@ def beam_reorder(states, parent, lengths=None, time_dim: int = 1, out=None):
         if lengths.shape != (B, K):
             raise ValueError("lengths must be shaped like parent")
         lengths = lengths.contiguous()
-    table = (_lib.State * max(len(src), 1))()
+    rows, table = B * K, []
     for i, (s, d) in enumerate(zip(src, dst)):
+        shape = s.shape
         for t in (s,) if d is s else (s, d):
             if not isinstance(t, torch.Tensor) or t.device != dev:
                 raise ValueError(f"states[{i}] must be a CUDA tensor on {dev}")
-            if t.dim() < 1 or t.shape[0] != B * K or t.shape != s.shape or t.dtype != s.dtype:
+            if len(shape) < 1 or shape[0] != rows or t.shape != shape or t.dtype != s.dtype:
                 raise ValueError(f"states[{i}] must have {B} x {K} rows, and its output its shape and dtype")
-        row, blk, blocks, entries, size = _layout(s, time_dim if s.dim() > 1 else 1, "a state")
-        drow, dblk = (row, blk) if d is s else _layout(d, time_dim if d.dim() > 1 else 1, "an output")[:2]
-        table[i] = _lib.State(_ptr(s), _ptr(d), row, drow, blk, dblk, blocks, entries, size)
-    _launch(dev, lib.topkp_beam_reorder, table, len(src), B, K, _ptr(parent), _ptr(lengths))
+        if len(shape) == 4 and time_dim == 1 and s.is_contiguous() and s.numel():
+            # [rows, time, heads, dim], the usual cache
+            size = shape[2] * shape[3] * s.element_size()
+            row = blk = shape[1] * size
+            blocks, entries = 1, shape[1]
+        else:
+            row, blk, blocks, entries, size = _layout(s, time_dim if len(shape) > 1 else 1, "a state")
+        drow, dblk = (row, blk) if d is s or d.stride() == s.stride() else _layout(d, time_dim if len(shape) > 1 else 1, "an output")[:2]
+        table.append(_STATE.pack(_ptr(s), _ptr(d), row, drow, blk, dblk, blocks, entries, size))
+    _launch(dev, lib.topkp_beam_reorder, b"".join(table), len(src), B, K, _ptr(parent), _ptr(lengths))
     return dst[0] if single else dst
 
 
 def _cache(t, exp, name, device, row_dtype):
-    _cuda(t, name, 4, None, device)
-    quant = t.dtype == torch.float8_e4m3fn
-    if not quant and t.dtype != row_dtype:
-        raise TypeError(f"{name} must be {row_dtype} or torch.float8_e4m3fn, not {t.dtype}")
-    if t.shape[3] > 1 and t.stride(3) != 1:
+    """The fields of a topkp_cache."""
+    if not isinstance(t, torch.Tensor) or t.device != device or not t.is_cuda or t.dim() != 4:
+        raise ValueError(f"{name} must be a 4-D CUDA tensor on {device}")
+    dtype, shape = t.dtype, t.shape
+    p0, p1, p2, p3 = t.stride()
+    if p3 != 1 and shape[3] > 1:
         raise ValueError(f"{name}: a head's elements must be contiguous")
-    if quant != (exp is not None):
+    if dtype != _E4M3:
+        if dtype != row_dtype:
+            raise TypeError(f"{name} must be {row_dtype} or torch.float8_e4m3fn, not {dtype}")
+        if exp is not None:
+            raise ValueError(f"{name}: exponents go with torch.float8_e4m3fn, and only with it")
+        return _ptr(t), 0, _CODES[dtype], p0, p1, p2, 0, 0, 0
+    if exp is None:
         raise ValueError(f"{name}: exponents go with torch.float8_e4m3fn, and only with it")
-    p0, p1, p2, _ = t.stride()
-    if not quant:
-        return _lib.Cache(_ptr(t), None, _dtype_code(t), p0, p1, p2, 0, 0, 0)
     if not isinstance(exp, torch.Tensor) or exp.dtype != torch.uint8 or exp.device != device:
         raise ValueError(f"{name}'s exponents must be a uint8 tensor on {device}")
-    if exp.shape != t.shape[:3]:
-        raise ValueError(f"{name}'s exponents must be {tuple(t.shape[:3])}, not {tuple(exp.shape)}")
-    return _lib.Cache(_ptr(t), _ptr(exp), _lib.TOPKP_E4M3, p0, p1, p2, *exp.stride())
+    if exp.shape != shape[:3]:
+        raise ValueError(f"{name}'s exponents must be {tuple(shape[:3])}, not {tuple(exp.shape)}")
+    return _ptr(t), _ptr(exp), _lib.TOPKP_E4M3, p0, p1, p2, *exp.stride()
 
 
 def _pair(k_cache, v_cache):
@@ -260,8 +281,8 @@ def cache_write(k, v, slots, k_cache, v_cache, k_exp=None, v_exp=None):
         raise ValueError(f"rows are {H} x {D} and the cache's {tuple(k_cache.shape[2:])}")
     last = rows[-1]
     _launch(dev, lib.topkp_cache_write, _ptr(rows[0]), _ptr(last) if v is not None else None, N, H, D,
-            *rows[0].stride()[:2], *last.stride()[:2], dt, _ptr(slots), ctypes.byref(kc),
-            ctypes.byref(vc) if vc is not None else None, *k_cache.shape[:2])
+            *rows[0].stride()[:2], *last.stride()[:2], dt, _ptr(slots), _CACHE.pack(*kc),
+            None if vc is None else _CACHE.pack(*vc), *k_cache.shape[:2])
 
 
 def cache_read(slots, k_cache, v_cache, k_exp=None, v_exp=None, dtype=None):
@@ -284,8 +305,8 @@ def cache_read(slots, k_cache, v_cache, k_exp=None, v_exp=None, dtype=None):
     N, (H, D) = slots.shape[0], k_cache.shape[2:]
     k = torch.empty((N, H, D), dtype=dtype, device=dev)
     v = torch.empty((N, H, D), dtype=dtype, device=dev) if vc is not None else None
-    _launch(dev, lib.topkp_cache_read, _ptr(slots), N, H, D, ctypes.byref(kc),
-            ctypes.byref(vc) if vc is not None else None, *k_cache.shape[:2], _dtype_code(k), _ptr(k), _ptr(v))
+    _launch(dev, lib.topkp_cache_read, _ptr(slots), N, H, D, _CACHE.pack(*kc),
+            None if vc is None else _CACHE.pack(*vc), *k_cache.shape[:2], _dtype_code(k), _ptr(k), _ptr(v))
     return k, v
 
 
@@ -334,23 +355,21 @@ def tree_attention(q, k_cache, v_cache, context, pages=None, tree=None, nodes=No
         tree = tree.contiguous()
     if out is None:
         out = torch.empty((B, T, Hq, D), dtype=q.dtype, device=dev)
-    if out.shape != q.shape or out.dtype != q.dtype or out.device != dev or (D > 1 and out.stride(3) != 1):
+    elif out.shape != q.shape or out.dtype != q.dtype or out.device != dev or (D > 1 and out.stride(3) != 1):
         raise ValueError("out must match q in shape, dtype and device, with its last dimension contiguous")
     lse = torch.empty((B, T, Hq), dtype=torch.float32, device=dev) if want_lse else None
     max_pages = 1 if pages is None else pages.shape[1]
-    qs, os = q.stride(), out.stride()
-    a = _lib.TreeAttentionArgs(
-        q=_ptr(q), out=_ptr(out), lse=_ptr(lse), k=kc, v=vc, table=_ptr(pages),
-        context=_ptr(context), nodes=_ptr(nodes), tree=_ptr(tree), B=B, T=T, Hq=Hq, Hkv=Hkv, D=D,
-        pages=pool, page_size=page_size, max_pages=max_pages,
-        ld_table=0 if pages is None else pages.stride(0) if B > 1 else max_pages,
-        max_context=max_pages * page_size if max_context is None else int(max_context),
-        q_batch_stride=qs[0], q_token_stride=qs[1], q_head_stride=qs[2],
-        out_batch_stride=os[0], out_token_stride=os[1], out_head_stride=os[2],
-        dtype=_dtype_code(q), scale=float(D) ** -0.5 if scale is None else float(scale))
-    need = int(lib.topkp_tree_attention_workspace_size(ctypes.byref(a)))
+    q0, q1, q2, _ = q.stride()
+    o0, o1, o2, _ = out.stride()
+    shape = (B, T, Hq, Hkv, D, pool, page_size, max_pages,
+             0 if pages is None else pages.stride(0) if B > 1 else max_pages,
+             max_pages * page_size if max_context is None else int(max_context), q0, q1, q2, o0, o1, o2, _CODES[q.dtype],
+             float(D) ** -0.5 if scale is None else float(scale))
+    front = (_ptr(q), _ptr(out), _ptr(lse), *kc, *vc, _ptr(pages), _ptr(context), _ptr(nodes), _ptr(tree))
+    args = _ATTENTION.pack(*front, 0, 0, *shape)
+    need = lib.topkp_tree_attention_workspace_size(args)
     if need:
         workspace = _workspace(workspace, need, dev)
-        a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel()
-    _launch(dev, lib.topkp_tree_attention, ctypes.byref(a))
+        args = _ATTENTION.pack(*front, _ptr(workspace), workspace.numel(), *shape)
+    _launch(dev, lib.topkp_tree_attention, args)
     return (out, lse) if want_lse else out

@@ -9,6 +9,11 @@
 // one rounding, and reading back has none: 4 significant bits always fit the
 // row's type.  A scale that is not a power of two would use up to one more
 // binade of e4m3's sixteen, and add a rounding on either side.
+//
+// Measured, heads of 8 x 128, bf16 and e4m3: 65501 tokens written in 102 us
+// (4.0 TB/s; bound by instructions, 172 a thread for eight elements: maxima
+// over the row, scaling, conversion, addresses), 32749 read in 37 (5.5 TB/s),
+// 64 written in 2.2 (a launch).
 #include "common.cuh"
 #include "decode.h"
 

@@ -190,14 +190,16 @@ topkp_status topkp_cache_read(const int64_t* slots, int64_t N, int64_t H, int64_
  *   workspace   device, at least topkp_tree_attention_workspace_size()
  *               bytes, 256-byte aligned.
  * D is a multiple of 8, at most TOPKP_MAX_HEAD_DIM; pointers and strides of
- * q, out and the caches are multiples of 16 bytes (8 for an e4m3 cache).
+ * q, out and the caches are multiples of 16 bytes (8 for an e4m3 cache);
+ * exponents are strided by less than 2^32.
  * Products and sums are fp32; probabilities are rounded to dtype before the
  * product with the values.  Over an e4m3 cache q is taken as a sum of e4m3
  * terms (an element is off by at most about 2^-18 of the largest of its row),
- * and with fp16 rows a cached value beyond fp16's range is an infinity.  One
- * launch, or two where the tokens are split.  A value that is not finite spoils the rows of
- * its request that do not see it too, if it is that of a drafted node;
- * tokens past the last node are never used.
+ * and with fp16 rows a cached value beyond fp16's range is an infinity.  A
+ * value that is not finite spoils the rows of its request that do not see it
+ * too, if it is that of a drafted node, and an infinite one may leave NaN;
+ * tokens past the last node are never used.  One launch, or two where the
+ * tokens are split.
  */
 typedef struct {
   const void* q;

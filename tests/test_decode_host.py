@@ -178,6 +178,26 @@ def test_tree_attention_refusals(lib):
     assert call(B=1, max_context=60000, max_pages=4096, ld_table=4096, pages=8192, workspace=None) == INVALID
 
 
+def test_tree_attention_refuses_wide_exponent_strides(lib):
+    from top_logit_filter_gb300 import _lib
+
+    def call(eps=64, ets=4, pages=8, page_size=16):
+        k, v = _cache(eps=eps, ets=ets), _cache(data=FAKE + 48 * MB, exp=FAKE + 64 * MB)
+        a = _lib.TreeAttentionArgs(q=FAKE, out=FAKE + MB, k=k, v=v, table=FAKE + 2 * MB, context=FAKE + 3 * MB, workspace=None,
+                                   workspace_bytes=0, B=2, T=0, Hq=8, Hkv=4, D=64, pages=pages, page_size=page_size, max_pages=4,
+                                   ld_table=4, max_context=64, q_batch_stride=2048, q_token_stride=512, q_head_stride=64,
+                                   out_batch_stride=2048, out_token_stride=512, out_head_stride=64, dtype=BF16, scale=0.125)
+        assert lib.topkp_tree_attention(ctypes.byref(a), None) == 0     # nothing to do
+        a.T = 4
+        st = lib.topkp_tree_attention(ctypes.byref(a), None)
+        return st, lib.topkp_last_error_string().decode()
+    for kw in (dict(eps=1 << 32), dict(ets=1 << 32)):
+        st, why = call(**kw)
+        assert st == INVALID and "32 bits" in why, (kw, why)
+    st, why = call(eps=1 << 32, pages=1)                                # a stride that nothing is multiplied with
+    assert "32 bits" not in why
+
+
 def test_no_device_fails_loudly(lib):
     if torch.cuda.is_available():
         pytest.skip("a GPU is present")

@@ -416,6 +416,17 @@ def test_attention_long_and_split(tk, cache, T, G, D, P):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T,G,D,P", [(31, 1, 128, 16), (8, 4, 128, 64), (32, 1, 64, 8), (16, 2, 256, 32), (11, 3, 96, 16),
+                                     (33, 1, 128, 64), (1, 32, 72, 0), (1, 1, 256, 24), (4, 8, 128, 5)])
+def test_attention_few_rows_quantised(tk, dtype, T, G, D, P):
+    """Around 32 rows, where four warps begin to share a row's tokens: tiles' quarters that see nothing, one part and many."""
+    contexts = [0, 1, 7, 15, 16, 17, 31, 48, 49, 63, 64, 65, 200]
+    attend(tk, dtype, "e4m3", T, 2 * G, 2, D, P, contexts, seed=T + G)
+    attend(tk, dtype, "e4m3", T, G, 1, D, P, [0, 3, 50, 64, 130], tree=make_tree(5, T, T), nodes=[T, 0, 1, T, T], seed=T)
+    attend(tk, dtype, "e4m3", T, G, 1, D, P, [3000, 17], spread=1.0, seed=5)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("T,G,D", [(1, 4, 128), (20, 4, 64), (64, 4, 128), (8, 2, 256)])
 def test_attention_quantised_sizes(tk, dtype, T, G, D):
     """Rows of very different scales, and all-large or all-small keys, values and queries."""

@@ -164,11 +164,11 @@ bool make_map(CUtensorMap* map, const topkp_cache& c, const topkp_tree_attention
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DP, int NT, bool BF, bool Q8>
+template <int DP, int NT, bool BF, bool Q8, int SH = 1>
 cudaError_t launch_tc(AttnDev p, cudaStream_t s) {
-  using Shape = TcShape<DP, NT, BF, Q8>;
+  using Shape = TcShape<DP, NT, BF, Q8, SH>;
   const topkp_tree_attention_args& a = p.a;
-  cudaError_t e = cudaFuncSetAttribute(attn_tc<DP, NT, BF, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kSmem);
+  cudaError_t e = cudaFuncSetAttribute(attn_tc<DP, NT, BF, Q8, SH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kSmem);
   if (e != cudaSuccess) return e;
   // tokens of a box: they lie in one page, and eight rows make a swizzle's group
   CUtensorMap km = {}, vm = {};
@@ -182,15 +182,25 @@ cudaError_t launch_tc(AttnDev p, cudaStream_t s) {
     p.box = 0;
   const int64_t rows = a.T * (a.Hq / a.Hkv);
   const dim3 grid((unsigned)((rows + NT * kTcRows - 1) / (NT * kTcRows)), (unsigned)p.splits, (unsigned)(a.B * a.Hkv));
-  attn_tc<DP, NT, BF, Q8><<<grid, Shape::kThreads, Shape::kSmem, s>>>(p, km, vm);
+  attn_tc<DP, NT, BF, Q8, SH><<<grid, Shape::kThreads, Shape::kSmem, s>>>(p, km, vm);
   return cudaGetLastError();
 }
 
 // Tiles of 128 rows of a CTA (256 dims leave tensor memory for one).
 int row_tiles(const topkp_tree_attention_args& a) { return a.T * (a.Hq / a.Hkv) > kTcRows && a.D <= 128 ? 2 : 1; }
 
+// Whether four warps share each row's tokens: up to 32 rows over e4m3, at 65 to
+// 128 dims.  64 single tokens to 8000, in us with and without: 303 / 350 (fp16
+// 340 / 365); it gives nothing at 64 dims (217 / 218) or 256 (313 / 311).
+bool few_rows(const topkp_tree_attention_args& a) {
+  return a.k.dtype == TOPKP_E4M3 && a.D > 64 && a.D <= 128 && a.T * (a.Hq / a.Hkv) <= 32;
+}
+
 template <bool BF, bool Q8>
 cudaError_t launch_dim(const AttnDev& p, cudaStream_t s) {
+  if constexpr (Q8) {
+    if (few_rows(p.a)) return launch_tc<128, 1, BF, true, 4>(p, s);
+  }
   const bool two = row_tiles(p.a) == 2;
   if (p.a.D <= 64) return two ? launch_tc<64, 2, BF, Q8>(p, s) : launch_tc<64, 1, BF, Q8>(p, s);
   if (p.a.D <= 128) return two ? launch_tc<128, 2, BF, Q8>(p, s) : launch_tc<128, 1, BF, Q8>(p, s);
@@ -218,7 +228,8 @@ AttnPlan plan_attention(const topkp_tree_attention_args& a, int num_sms) {
   // to), four tiles for a CTA's start and end, and writing and reading the
   // partial outputs.
   const int64_t nt = row_tiles(a);
-  const double slots = (nt == 2 || a.D > (a.k.dtype == TOPKP_E4M3 ? 64 : 128) ? 1.0 : 2.0) * num_sms;
+  const bool pair = few_rows(a) && a.dtype == TOPKP_BF16;
+  const double slots = (nt == 2 || a.D > (a.k.dtype == TOPKP_E4M3 && !pair ? 64 : 128) ? 1.0 : 2.0) * num_sms;
   const double base = (double)(a.B * a.Hkv * ((rows + nt * kTcRows - 1) / (nt * kTcRows)));
   // a tile takes a CTA about 0.9 us (1.3 with two of them on an SM); a part
   // of every row costs 8 bytes an element at the copy's rate

@@ -163,15 +163,25 @@ __device__ __forceinline__ uint32_t swizzled(int r, int c) {
 
 __device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull; }
 
-template <int DP, int NT, bool BF, bool Q8>
+// Among the softmax warps of one row tile.
+__device__ __forceinline__ void softmax_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// SH warps share a row's tokens.  With up to 32 rows over e4m3 the four softmax
+// warps hold a copy of the rows each and take a quarter of every tile's tokens
+// (for O's product the others' are zeros); their O, maxima and sums are joined
+// at the end.
+template <int DP, int NT, bool BF, bool Q8, int SH>
 struct TcShape {
   static constexpr int kSoftWarps = 4 * NT;
   // 16 bits: one warp for keys, one for values; e4m3: one loads, the others widen
-  static constexpr int kFeedWarps = !Q8 ? 2 : NT == 2 ? 7 : DP >= 128 ? 9 : 3;
+  // then bf16's 128 dims leave room for two CTAs an SM (64
+  // single tokens of 64 query and 8 cache heads to 8000: 303 us, with one 318)
+  static constexpr bool kPair = SH == 4 && BF;
+  static constexpr int kFeedWarps = !Q8 ? 2 : NT == 2 ? 7 : kPair ? 5 : DP >= 128 ? 9 : 3;
   static constexpr int kThreads = 32 * (kSoftWarps + kFeedWarps + 1);
-  // two CTAs leave room for two warps that widen, enough for 64 dims only
+  // with a warp to a row two CTAs leave room for two warps that widen, enough for 64 dims only
   // (128 rows of 128 dims over e4m3: 258 us with two CTAs, 228 with one)
-  static constexpr int kPerSm = NT == 1 && DP <= (Q8 ? 64 : 128) ? 2 : 1;
+  static constexpr int kPerSm = NT == 1 && DP <= (Q8 && !kPair ? 64 : 128) ? 2 : 1;
   // e4m3 keys are operands as they lie: Q is then a sum of terms in e4m3
   static constexpr int kTerms = !Q8 ? 1 : BF ? 2 : 3;
   static constexpr int kKeyBytes = kTile * DP * (Q8 ? 1 : 2), kValueBytes = kTile * DP * 2, kRawBytes = kTile * DP;
@@ -184,9 +194,9 @@ struct TcShape {
   static constexpr int kQBytes = kQInTmem ? 0 : NT * kTcRows * DP * (Q8 ? kTerms : 2);
   // stages of keys, of values, and of raw e4m3 values.  Keys free theirs as
   // soon as their product is done, well before the softmax
-  static constexpr int kKeys = Q8 ? (DP <= 128 ? 4 : 2) : DP == 64 || (DP == 128 && NT == 2) ? 4 : DP == 256 ? 3 : 2;
-  static constexpr int kValues = !Q8 ? kKeys : DP == 256 ? (BF ? 3 : 1) : DP == 128 && NT == 2 ? 2 : 3;
-  static constexpr int kRaw = !Q8 ? 0 : DP == 256 ? 2 : 4;
+  static constexpr int kKeys = Q8 ? (kPair ? 3 : DP <= 128 ? 4 : 2) : DP == 64 || (DP == 128 && NT == 2) ? 4 : DP == 256 ? 3 : 2;
+  static constexpr int kValues = !Q8 ? kKeys : kPair ? 2 : DP == 256 ? (BF ? 3 : 1) : DP == 128 && NT == 2 ? 2 : 3;
+  static constexpr int kRaw = !Q8 ? 0 : DP == 256 || kPair ? 2 : 4;
   static constexpr uint32_t kQ = NT * 128;  // after two S of 64 columns a row tile
   static constexpr uint32_t kO = kQ + (kQInTmem ? NT * kQColumns : 0);
   static constexpr int kColumns = kO + NT * DP <= 256 ? 256 : 512;
@@ -319,10 +329,12 @@ __device__ __forceinline__ void e4m3_away(uint32_t two, float& x, float& y) {
   y -= __half2float(__ushort_as_half((uint16_t)(h >> 16)));
 }
 
-template <int DP, int NT, bool BF, bool Q8>
-__global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8>::kThreads, TcShape<DP, NT, BF, Q8>::kPerSm)
+template <int DP, int NT, bool BF, bool Q8, int SH>
+__global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH>::kThreads, TcShape<DP, NT, BF, Q8, SH>::kPerSm)
     attn_tc(const __grid_constant__ AttnDev p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-  using Shape = TcShape<DP, NT, BF, Q8>;
+  using Shape = TcShape<DP, NT, BF, Q8, SH>;
+  static_assert(SH == 1 || (SH == 4 && NT == 1 && DP == 128 && Q8), "a row's tokens go to one warp or to four");
+  constexpr int H = 32 / SH;  // half of a thread's columns of S
   constexpr int KS = Shape::kKeys, VS = Shape::kValues;
   constexpr int RS = Shape::kRaw > 0 ? Shape::kRaw : 1;
   constexpr int kFeed = Shape::kFeedWarps;
@@ -390,7 +402,7 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8>::kThreads, TcShape<DP,
   if (warp < Shape::kSoftWarps) {
     // ---- softmax: thread = row ----
     const int tile = NT == 1 ? 0 : warp >> 2;
-    const int r = row0 + tid;
+    const int r = SH == 1 ? row0 + tid : lane;
     const int node = r / G;
     const int hq = h * G + (r - node * G);
     const bool in = r < rows;
@@ -406,8 +418,8 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8>::kThreads, TcShape<DP,
       if constexpr (Q8) {
         // The row times a power of two that brings its largest magnitude to
         // e4m3's top binade, as kTerms e4m3 that add up to it: 8 significant
-        // bits are two times 4, fp16's 11 three times.  Elements more than
-        // 2^17 below the largest lose what lies 2^19 below it.
+        // bits are two times 4, fp16's 11 three times.  What e4m3's smallest
+        // step of 2^-9 cuts off lies 2^18 below the largest.
         uint32_t amax = 0;
         bool finite = true;
 #pragma unroll 2
@@ -491,7 +503,8 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8>::kThreads, TcShape<DP,
     // if they saw the context; what they get is not written
     const bool seen = in && node < nodes;
     const uint64_t bits = seen && a.tree ? a.tree[b * a.T + node] : 0;
-    const bool idle = row0 + warp * 32 >= rows;  // the whole warp
+    const bool idle = SH == 1 && row0 + warp * 32 >= rows;  // the whole warp
+    const int c0 = SH == 1 ? 0 : warp * 2 * H;                 // the thread's first column of S
     const float sc0 = a.scale * kLog2e * q_scale;
     const float sc = sc0 > 0.0f ? sc0 : 1.0f;  // a scale of zero or less is applied to the products first
     const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
@@ -508,16 +521,27 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8>::kThreads, TcShape<DP,
       }
       __syncwarp();
       tc_fence_after();
-      uint32_t s0[32], s1[32];
-      tc_ld32(s0, sb);
-      tc_ld32(s1, sb + 32);
-      tc_wait_ld();
+      uint32_t s0[H], s1[H];
+      if constexpr (SH == 1) {
+        tc_ld32(s0, sb);
+        tc_ld32(s1, sb + 32);
+        tc_wait_ld();
+      } else {
+        uint32_t both[16];
+        tc_ld16(both, sb + c0);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+          s0[i] = both[i];
+          s1[i] = both[H + i];
+        }
+      }
       const int t0 = (t_begin + j) * kTile;
       if (Q8) {  // the keys' scales, powers of two
-        const ulonglong2* f = reinterpret_cast<const ulonglong2*>(sscale[j % kScales]);
+        const ulonglong2* f = reinterpret_cast<const ulonglong2*>(sscale[j % kScales] + c0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const ulonglong2 x = f[i], y = f[8 + i];
+        for (int i = 0; i < H / 4; ++i) {
+          const ulonglong2 x = f[i], y = f[H / 4 + i];
           of_two(mul_two(two_f32(s0[4 * i], s0[4 * i + 1]), x.x), s0[4 * i], s0[4 * i + 1]);
           of_two(mul_two(two_f32(s0[4 * i + 2], s0[4 * i + 3]), x.y), s0[4 * i + 2], s0[4 * i + 3]);
           of_two(mul_two(two_f32(s1[4 * i], s1[4 * i + 1]), y.x), s1[4 * i], s1[4 * i + 1]);
@@ -526,7 +550,7 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8>::kThreads, TcShape<DP,
       }
       if (!(sc0 > 0.0f)) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < H; ++i) {
           s0[i] = __float_as_uint(__uint_as_float(s0[i]) * sc0);
           s1[i] = __float_as_uint(__uint_as_float(s1[i]) * sc0);
         }
@@ -537,17 +561,17 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8>::kThreads, TcShape<DP,
         uint64_t vis;
         if (a.tree) vis = d >= 64 ? 0 : d >= 0 ? bits >> d : (bits << -d) | low_bits(-d);
         else vis = low_bits(node + 1 - d);
-        vis &= low_bits(len - t0);
-        const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> 32);
+        vis = (vis & low_bits(len - t0)) >> c0;
+        const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> H);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < H; ++i) {
           s0[i] = v0 & (1u << i) ? s0[i] : 0xff800000u;
           s1[i] = v1 & (1u << i) ? s1[i] : 0xff800000u;
         }
       }
       float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // four chains
 #pragma unroll
-      for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], fmaxf(__uint_as_float(s0[i]), __uint_as_float(s1[i])));
+      for (int i = 0; i < H; ++i) m4[i & 3] = fmaxf(m4[i & 3], fmaxf(__uint_as_float(s0[i]), __uint_as_float(s1[i])));
       const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
       const float top = mx == -INFINITY ? -INFINITY : mx * sc;
       if (j == 0) {
@@ -577,9 +601,9 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8>::kThreads, TcShape<DP,
       const float base = m == -INFINITY ? 0.0f : m;
       const uint64_t sc2 = two_f32(__float_as_uint(sc), __float_as_uint(sc)), base2 = two_f32(__float_as_uint(-base), __float_as_uint(-base));
       uint64_t sum0 = 0ull, sum1 = 0ull;
-      uint32_t pk[32];
+      uint32_t pk[H];
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) {
+      for (int i = 0; i < H; i += 2) {
         uint32_t x0, x1, y0, y1;
         of_two(fma_two(two_f32(s0[i], s0[i + 1]), sc2, base2), x0, x1);
         of_two(fma_two(two_f32(s1[i], s1[i + 1]), sc2, base2), y0, y1);
@@ -588,14 +612,21 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8>::kThreads, TcShape<DP,
         sum0 = add_two(sum0, two_f32(__float_as_uint(p0), __float_as_uint(p1)));
         sum1 = add_two(sum1, two_f32(__float_as_uint(r0), __float_as_uint(r1)));
         pk[i / 2] = pack2<BF>(p0, p1);
-        pk[16 + i / 2] = pack2<BF>(r0, r1);
+        pk[H / 2 + i / 2] = pack2<BF>(r0, r1);
       }
       {
         uint32_t x0, x1;
         of_two(add_two(sum0, sum1), x0, x1);
         l += __uint_as_float(x0) + __uint_as_float(x1);
       }
-      tc_st32(sb, pk);
+      if constexpr (SH == 1) {
+        tc_st32(sb, pk);
+      } else {  // zeros for the tokens of the other warps
+        uint32_t row[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) row[i] = i / H == warp ? pk[i % H] : 0u;
+        tc_st32(sb, row);
+      }
       tc_wait_st();
       tc_fence_before();
       // a parity tells one phase from the next only: product n - 2 is seen done
@@ -610,12 +641,87 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8>::kThreads, TcShape<DP,
     }
     const int64_t all_rows = a.B * a.T * a.Hq;
     const int64_t row = (b * a.T + node) * a.Hq + hq;
+    float part = 1.0f;  // this warp's weight in the row
+    if constexpr (SH > 1) {
+      // the warps' maxima and sums, then O in blocks of 64 dims, by way of the
+      // rings, which are done with: every tile has been through its products
+      float* sums = reinterpret_cast<float*>(sk);
+      sums[warp * 32 + lane] = m;
+      sums[(SH + warp) * 32 + lane] = l;
+      softmax_barrier();
+      float all_m = -INFINITY, all_l = 0.0f;
+#pragma unroll
+      for (int w = 0; w < SH; ++w) all_m = fmaxf(all_m, sums[w * 32 + lane]);
+      const float ref = all_m == -INFINITY ? 0.0f : all_m;
+#pragma unroll
+      for (int w = 0; w < SH; ++w) all_l += sums[(SH + w) * 32 + lane] * exp2f(sums[w * 32 + lane] - ref);
+      part = exp2f(m - ref);
+      m = all_m;
+      l = all_l;
+    }
     if (!seen) l = 0.0f;
     const float inv = l > 0.0f ? 1.0f / l : l;
     const float lse = l > 0.0f ? (m + log2f(l)) * kLn2 : l == 0.0f ? -INFINITY : l;
     const bool write = in && !dead;
+    if constexpr (SH > 1) {
+      constexpr int kLine = 68;  // floats from row to row, 16 bytes off a multiple of the banks
+      static_assert(KS * Shape::kKeyBytes + VS * Shape::kValueBytes >= SH * 32 * kLine * 4, "the rings hold a block of O");
+      float* ring = reinterpret_cast<float*>(sk);
 #pragma unroll 1
-    for (int c = 0; c < DP; c += 32) {
+      for (int c = 0; c < DP; c += 64) {
+        softmax_barrier();  // what the last block, or the sums, left has been read
+#pragma unroll
+        for (int k = 0; k < 64; k += 32) {
+          uint32_t o[32];
+          if (n > 0) {
+            tc_ld32(o, ocol + c + k);
+            tc_wait_ld();
+          }
+          float4* to = reinterpret_cast<float4*>(ring + (warp * 32 + lane) * kLine + k);
+          const float f = part * inv;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            to[i] = n > 0 && l != 0.0f ? make_float4(__uint_as_float(o[4 * i]) * f, __uint_as_float(o[4 * i + 1]) * f,
+                                                     __uint_as_float(o[4 * i + 2]) * f, __uint_as_float(o[4 * i + 3]) * f)
+                                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+        softmax_barrier();
+        const int d = c + c0;  // 16 dims of the row
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+          for (int w = 0; w < SH; ++w) {
+            const float4 u = *reinterpret_cast<const float4*>(ring + (w * 32 + lane) * kLine + c0 + 4 * i);
+            t = make_float4(t.x + u.x, t.y + u.y, t.z + u.z, t.w + u.w);
+          }
+          x[4 * i] = t.x;
+          x[4 * i + 1] = t.y;
+          x[4 * i + 2] = t.z;
+          x[4 * i + 3] = t.w;
+        }
+        if (write) {
+          if (p.splits > 1) {
+            float4* po = reinterpret_cast<float4*>(p.part_o + ((int64_t)split * all_rows + row) * a.D + d);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (d + i * 4 < a.D) po[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+          } else {
+            uint4* po = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + b * a.out_batch_stride +
+                                                 node * a.out_token_stride + hq * a.out_head_stride + d);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (d + i * 8 < a.D)
+                po[i] = make_uint4(pack2<BF>(x[8 * i], x[8 * i + 1]), pack2<BF>(x[8 * i + 2], x[8 * i + 3]),
+                                   pack2<BF>(x[8 * i + 4], x[8 * i + 5]), pack2<BF>(x[8 * i + 6], x[8 * i + 7]));
+          }
+        }
+        __syncwarp();
+      }
+    }
+#pragma unroll 1
+    for (int c = 0; SH == 1 && c < DP; c += 32) {
       uint32_t o[32];
       if (n > 0) {
         tc_ld32(o, ocol + c);
@@ -645,7 +751,7 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8>::kThreads, TcShape<DP,
       }
       __syncwarp();
     }
-    if (write) {
+    if (write && (SH == 1 || warp == 0)) {
       if (p.splits > 1) p.part_l[(int64_t)split * all_rows + row] = lse;
       else if (a.lse) a.lse[row] = lse;
     }
@@ -759,11 +865,11 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8>::kThreads, TcShape<DP,
           uint32_t ek[2 * kRun], ev[2 * kRun];
 #pragma unroll
           for (int i = 0; i < 2 * kRun; ++i) {
-            const bool in = page[i] >= 0 && page[i] < a.pages && t0 + i * 32 + lane < t_end;
-            const int64_t q = in ? page[i] : 0, t = in ? at[i] : 0;
+            const bool in = (uint32_t)page[i] < (uint32_t)a.pages && t0 + i * 32 + lane < t_end;
+            const uint32_t q = in ? page[i] : 0, t = in ? at[i] : 0;  // strides have 32 bits
             e[i] = in ? kToken : 0;
-            ek[i] = __ldg(ke + q * a.k.exp_page_stride + t * a.k.exp_token_stride);
-            ev[i] = __ldg(ve + q * a.v.exp_page_stride + t * a.v.exp_token_stride);
+            ek[i] = __ldg(ke + (uint64_t)q * (uint32_t)a.k.exp_page_stride + (uint64_t)t * (uint32_t)a.k.exp_token_stride);
+            ev[i] = __ldg(ve + (uint64_t)q * (uint32_t)a.v.exp_page_stride + (uint64_t)t * (uint32_t)a.v.exp_token_stride);
           }
 #pragma unroll 1
           for (int i = 0; i < kRun && j0 + i < n; ++i) {

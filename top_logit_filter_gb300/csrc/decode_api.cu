@@ -403,6 +403,9 @@ topkp_status topkp_tree_attention(const topkp_tree_attention_args* args, void* s
   if (!st) st = check_cache(fn, "v", &a.v, a.Hkv, a.D, a.pages, a.page_size, a.dtype);
   if (st) return st;
   if (a.k.dtype != a.v.dtype) return fail(TOPKP_ERR_PARAM_INVALID, "%s: the caches have two dtypes", fn);
+  for (const topkp_cache* c : {&a.k, &a.v})
+    if (c->exponents && ((a.pages > 1 && c->exp_page_stride > UINT32_MAX) || (a.page_size > 1 && c->exp_token_stride > UINT32_MAX)))
+      return fail(TOPKP_ERR_PARAM_INVALID, "%s: a stride of exponents has more than 32 bits", fn);
   if (!cache_by_8(a.k) || !cache_by_8(a.v))
     return fail(TOPKP_ERR_PARAM_INVALID, "%s: a cache's pointer or strides are not multiples of 8 elements", fn);
   for (const int64_t s : {a.q_batch_stride, a.q_token_stride, a.q_head_stride, a.out_batch_stride, a.out_token_stride, a.out_head_stride})

@@ -84,6 +84,19 @@ def _vec(t, n, dtype, name, device):
     return t.contiguous()
 
 
+def _workspace(workspace, need, device):
+    """The caller's workspace if it has ``need`` bytes in one piece (an
+    expanded or strided tensor counts more elements than it has memory for),
+    or a new one for None."""
+    torch = _torch()
+    if workspace is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    if (not torch.is_tensor(workspace) or workspace.dtype != torch.uint8 or workspace.device != device
+            or workspace.numel() < need or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on {device}")
+    return workspace
+
+
 def apply(logits, p=None, k=None, out=None):
     """aclnnApplyTopKTopP: filter a [B, V] CUDA tensor of logits.
 
@@ -248,10 +261,7 @@ def sample_v2(logits, k=None, p=None, min_p=None, q=None, eps: float = 1e-10, ks
         if q.stride(1) != 1:
             q = q.contiguous()
     need = int(lib.topkp_sample_v2_workspace_size(B, V, dt))
-    if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    if workspace.dtype != torch.uint8 or workspace.device != dev or workspace.numel() < need:
-        raise ValueError(f"workspace must be a uint8 tensor of at least {need} bytes on {dev}")
+    workspace = _workspace(workspace, need, dev)
     token = select = idx = sm = None
     if need_sample_result:
         idx = torch.empty((B, V), dtype=torch.int32, device=dev)
@@ -283,10 +293,7 @@ def sort(logits, workspace=None):
     B, V = logits.shape
     dev = logits.device
     need = int(lib.topkp_sort_workspace_size(B, V, dt))
-    if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    if workspace.dtype != torch.uint8 or workspace.device != dev or workspace.numel() < need:
-        raise ValueError(f"workspace must be a uint8 tensor of at least {need} bytes on {dev}")
+    workspace = _workspace(workspace, need, dev)
     sv = torch.empty((B, V), dtype=logits.dtype, device=dev)
     si = torch.empty((B, V), dtype=torch.int32, device=dev)
     with torch.cuda.device(dev):

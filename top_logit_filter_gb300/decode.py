@@ -18,7 +18,7 @@ from __future__ import annotations
 
 import struct
 
-from . import TopKPError, _lib
+from . import TopKPError, _lib, _workspace
 
 torch = None    # imported by the first call, as the package itself does
 _CODES = {}     # torch dtype -> topkp_dtype
@@ -86,14 +86,6 @@ def _launch(device, call, *args):
             status = call(*args, torch._C._cuda_getCurrentRawStream(index))
     if status != _lib.TOPKP_SUCCESS:
         raise TopKPError(status, _lib.last_error())
-
-
-def _workspace(workspace, need, device):
-    if workspace is None:
-        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
-    if workspace.dtype != torch.uint8 or workspace.device != device or workspace.numel() < need:
-        raise ValueError(f"workspace must be a uint8 tensor of at least {need} bytes on {device}")
-    return workspace
 
 
 def beam_select(logits, scores, n: int, finished=None, pad_token: int = 0, workspace=None):

@@ -180,8 +180,8 @@ topkp_status topkp_cache_read(const int64_t* slots, int64_t N, int64_t H, int64_
  *               zeros.  NULL: page b is request b's whole cache (page_size
  *               its capacity, pages == B, max_pages == 1).
  *   context     device, [B] int32; read as if clamped to [0, capacity],
- *               capacity = max_pages * page_size.  Nodes beyond the capacity
- *               are seen by none.
+ *               capacity = max_pages * page_size, at most 2^31 - 1024.
+ *               Nodes beyond the capacity are seen by none.
  *   nodes       device, [B] int32 (1 .. T), or NULL (T for all).
  *   tree        device, [B, T] uint64, T <= TOPKP_MAX_TREE, or NULL.
  *   scale       of the products.

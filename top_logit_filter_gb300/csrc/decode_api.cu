@@ -48,6 +48,10 @@ topkp_status launched(const char* fn, cudaError_t e, int launches) {
 // workspace's size does not depend on it.
 constexpr int kPlanSms = 152;
 
+// The attention's places of tokens are 32 bits, and its loads look ahead by up
+// to a run of tiles: the largest capacity, so that none of them wraps.
+constexpr int64_t kMostTokens = INT_MAX - 1023;
+
 }  // namespace
 
 extern "C" {
@@ -392,7 +396,7 @@ topkp_status topkp_tree_attention(const topkp_tree_attention_args* args, void* s
     return fail(TOPKP_ERR_PARAM_INVALID, "%s: a tree of %lld nodes (up to %d)", fn, (long long)a.T, TOPKP_MAX_TREE);
   if (a.B == 0 || a.T == 0) return TOPKP_SUCCESS;
   if (a.pages < 1 || a.page_size < 1 || a.max_pages < 1 || a.pages > INT_MAX || a.page_size > INT_MAX ||
-      a.max_pages > INT_MAX / a.page_size || (a.table && a.ld_table < a.max_pages) ||
+      a.max_pages > kMostTokens / a.page_size || (a.table && a.ld_table < a.max_pages) ||
       (!a.table && (a.max_pages != 1 || a.pages != a.B)))
     return fail(TOPKP_ERR_PARAM_INVALID, "%s: pages=%lld page_size=%lld max_pages=%lld ld_table=%lld", fn, (long long)a.pages,
                 (long long)a.page_size, (long long)a.max_pages, (long long)a.ld_table);

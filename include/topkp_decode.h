@@ -193,7 +193,8 @@ topkp_status topkp_cache_read(const int64_t* slots, int64_t N, int64_t H, int64_
  * q, out and the caches are multiples of 16 bytes (8 for an e4m3 cache);
  * exponents are strided by less than 2^32.
  * Products and sums are fp32; probabilities are rounded to dtype before the
- * product with the values.  Over an e4m3 cache q is taken as a sum of e4m3
+ * product with the values (fp16's weights below 2^-32 of the row's largest
+ * become zero there, those below 2^-21 lose bits).  Over an e4m3 cache q is taken as a sum of e4m3
  * terms (an element is off by at most about 2^-18 of the largest of its row),
  * and with fp16 rows a cached value beyond fp16's range is an infinity.  A
  * value that is not finite spoils the rows of its request that do not see it

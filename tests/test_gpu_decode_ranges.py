@@ -1,0 +1,94 @@
+"""The attention and the cache beyond the usual: far tails of fp16
+probabilities, chains of more than 64 nodes, and the kernels that only many
+tokens reach."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+import decode_oracle as R  # noqa: E402
+from test_gpu_decode import T_, attend, awkward, tk  # noqa: E402,F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ attention
+@pytest.mark.parametrize("cache", ["f16", "e4m3"])
+@pytest.mark.parametrize("T,D", [(1, 128), (16, 128), (40, 64), (80, 128), (3, 256)])
+def test_attention_fp16_far_tail(tk, cache, T, D):
+    """A few tokens at 1 and 2^18 of them 18 below, which together weigh a thousandth: all in one part of the work."""
+    L, G, u = 1 << 18, 2, 2.0 ** -11
+    kind = R.E4M3 if cache == "e4m3" else torch.float16
+    k = torch.zeros(1, L + T, 1, D)
+    v = torch.full((1, L + T, 1, D), 8.0)
+    k[..., 0] = -18.0
+    peaks = [0, 16, 32, 48]     # one for each quarter of the first tile
+    k[:, peaks, :, 0] = 0.0
+    v[:, peaks] = 1.0
+    q = torch.zeros(1, T, G, D, dtype=torch.float16)
+    q[..., 0] = 1.0
+    kw = {}
+    if cache == "e4m3":
+        one = torch.full((1, L + T, 1), 127, dtype=torch.uint8).cuda()
+        kw = dict(k_exp=one, v_exp=one.clone())
+    out, lse = tk.tree_attention(q.cuda(), k.to(kind).cuda(), v.to(kind).cuda(), torch.tensor([L], dtype=torch.int32).cuda(),
+                                 scale=1.0, max_context=1, want_lse=True, **kw)
+    tk.device_status()
+    for i in range(T):
+        tail = (L - 4 + i + 1) * math.exp(-18.0)
+        want = (4 + 8 * tail) / (4 + tail)
+        # the sums of 64 tokens at a time and of all tiles; each tail probability is off by half of fp16's smallest
+        # step, 2^-25, at 2^7 times its size or less often
+        e = (L / 64 + 64) * 2.0 ** -24 + 2.0 ** -21
+        tol = want * (u + e + L / 16 * 2.0 ** -24) + 8 * (L + T) * 2.0 ** -32
+        assert (out[0, i].double().cpu() - want).abs().max() <= tol, (i, float(out[0, i, 0, 0]), want)
+        assert (lse[0, i].double().cpu() - math.log(4 + tail)).abs().max() <= e
+
+
+@pytest.mark.parametrize("dtype,cache", [("bf16", "own"), ("f16", "own"), ("bf16", "e4m3"), ("f16", "e4m3")])
+@pytest.mark.parametrize("T,Hq,Hkv,D,P", [(65, 4, 2, 64, 16), (129, 3, 1, 128, 0), (500, 2, 1, 128, 48), (300, 1, 1, 256, 64)])
+def test_attention_long_chains(tk, dtype, cache, T, Hq, Hkv, D, P):
+    """Chains of more than 64 nodes, whole and ragged, over no context and some."""
+    attend(tk, dtype, cache, T, Hq, Hkv, D, P, [0, 1, 70], seed=T)
+    attend(tk, dtype, cache, T, Hq, Hkv, D, P, [0, 40, 333], nodes=[T, T // 2, 64], seed=T + 1)
+
+
+# ---------------------------------------------------------------------- cache
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("N,H,D,P", [(5003, 8, 128, 48), (20011, 3, 80, 64), (40013, 1, 128, 16)])
+def test_cache_of_many_tokens(tk, dtype, N, H, D, P):
+    """As many rows as make a thread take four tokens."""
+    g = torch.Generator().manual_seed(N)
+    pages = -(-N // P) + 3
+    slots = torch.randperm(pages * P, generator=g)[:N]
+    slots[::31] = -1
+    slots[5::97] = pages * P + 4
+    keep = (slots >= 0) & (slots < pages * P)
+    k, v = awkward(N, H, D, dtype, N), awkward(N, H, D, dtype, N + 1)
+    ints = torch.int32 if dtype == "f32" else torch.int16
+    kc, vc = (torch.zeros(pages, P, H, D, dtype=T_[dtype], device="cuda") for _ in (0, 1))
+    tk.cache_write(k.cuda(), v.cuda(), slots.cuda(), kc, vc)
+    for x, c, r in zip((k, v), (kc, vc), tk.cache_read(slots.cuda(), kc, vc)):
+        want = torch.zeros(pages * P, H, D, dtype=T_[dtype])
+        want[slots[keep]] = x[keep]
+        assert torch.equal(c.cpu().view(-1, H, D).view(ints), want.view(ints))
+        back = x.clone()
+        back[~keep] = 0
+        assert torch.equal(r.cpu().view(ints), back.view(ints))
+    kc, vc = (torch.zeros(pages, P, H, D, dtype=torch.uint8, device="cuda").view(R.E4M3) for _ in (0, 1))
+    ke, ve = (torch.full((pages, P, H), 9, dtype=torch.uint8, device="cuda") for _ in (0, 1))
+    tk.cache_write(k.cuda(), v.cuda(), slots.cuda(), kc, vc, k_exp=ke, v_exp=ve)
+    read = {o: tk.cache_read(slots.cuda(), kc, vc, k_exp=ke, v_exp=ve, dtype=T_[o]) for o in ("f32", "f16", "bf16")}
+    for i, (x, c, e) in enumerate(((k, kc, ke), (v, vc, ve))):
+        q, byte = R.quantise(x)
+        want, wexp = torch.zeros(pages * P, H, D, dtype=torch.float64), torch.full((pages * P, H), 9)
+        want[slots[keep]], wexp[slots[keep]] = q[keep], byte[keep].long()
+        assert torch.equal(e.cpu().view(-1, H).long(), wexp)
+        got = c.cpu().view(torch.uint8).view(R.E4M3).float().double().view(-1, H, D)
+        assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(got.nan_to_num(nan=0), want.nan_to_num(nan=0))
+        value = torch.ldexp(q, byte[..., None] - 127)
+        value[~keep] = 0
+        for o, pair in read.items():
+            w, r = value.float().to(T_[o]), pair[i].cpu()
+            assert torch.equal(torch.isnan(r), torch.isnan(w))
+            assert torch.equal(r.masked_fill(torch.isnan(r), 0), w.masked_fill(torch.isnan(w), 0)), o

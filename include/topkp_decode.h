@@ -58,12 +58,14 @@ extern "C" {
  *              device, [B, n] float, int32 (beam of the request), int32.
  *   workspace  device, at least topkp_beam_select_workspace_size(...) bytes,
  *              256-byte aligned; contents on entry do not matter.
- * Candidates are compared in 64-bit fixed point of 2^-40.  The normaliser of
- * a row is summed from fp32 exponentials: its error is below 1e-6, so two
- * candidates of different beams that lie nearer than that may change places;
- * those of one beam never do.  A finite logit beyond +-60000 counts as
- * +-60000 (a mask may have left the lowest value of its type).  NaN and +inf
- * logits give unspecified output.  Two launches.
+ * Scores and logits may be any finite numbers (a dead beam's -1e9, a mask of
+ * the type's lowest value).  Candidates are compared in 64-bit floating point,
+ * those of one beam by their logits.  The normaliser of a row is summed from
+ * fp32 exponentials: its error is below 1e-6, so two candidates of different
+ * beams that lie nearer than that, or than a step of 64 bits, may change
+ * places; those of one beam never do.  A candidate below fp32's range comes
+ * out with score -inf.  NaN and +inf among logits or scores give unspecified
+ * output.  Two launches.
  */
 size_t topkp_beam_select_workspace_size(int64_t B, int64_t K, int64_t V, topkp_dtype dtype, int32_t n);
 topkp_status topkp_beam_select(const void* logits, int64_t B, int64_t K, int64_t V, int64_t ld_logits,

@@ -79,7 +79,11 @@ topkp_status topkp_beam_select(const void* logits, int64_t B, int64_t K, int64_t
  * has one block of `time` entries; [rows, heads, time, dim] has `heads`
  * blocks.  Entries of a block are contiguous; strides are in bytes.
  * dst == src with equal strides reorders in place; otherwise dst must not
- * overlap any src of the call.
+ * overlap any src of the call.  States may lie between each other's rows and
+ * blocks (views of one tensor): no byte may be written that another state
+ * reads or writes.  That is decided exactly for equal strides; states of two
+ * block strides may not interleave within a row, nor states of two row
+ * strides at all.
  */
 typedef struct {
   const void* src;

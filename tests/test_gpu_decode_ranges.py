@@ -7,7 +7,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 import decode_oracle as R  # noqa: E402
-from test_gpu_decode import T_, attend, awkward, tk  # noqa: E402,F401
+from test_gpu_decode import T_, attend, awkward, ref_reorder, tk  # noqa: E402,F401
 
 pytestmark = pytest.mark.gpu
 
@@ -92,3 +92,30 @@ def test_cache_of_many_tokens(tk, dtype, N, H, D, P):
             w, r = value.float().to(T_[o]), pair[i].cpu()
             assert torch.equal(torch.isnan(r), torch.isnan(w))
             assert torch.equal(r.masked_fill(torch.isnan(r), 0), w.masked_fill(torch.isnan(w), 0)), o
+
+
+# ----------------------------------------------------------------- reordering
+@pytest.mark.parametrize("dtype,dim", [(torch.bfloat16, 8), (torch.float32, 3), (torch.uint8, 5)])
+def test_reorder_interleaved_views(tk, dtype, dim):
+    """Keys and values of every layer in one tensor, rows outermost: all of them states of one call."""
+    g = torch.Generator().manual_seed(dim)
+    B, K = 3, 4
+    c = torch.randint(0, 100, (B * K, 20, 2, 9, 2, dim), generator=g).to(dtype)
+    parent = torch.randint(0, K, (B, K), generator=g, dtype=torch.int32)
+    lengths = torch.randint(0, 12, (B, K), generator=g, dtype=torch.int32)
+    for ln in (None, lengths):
+        want = torch.stack([torch.stack([ref_reorder(c[:, i, j], c[:, i, j], parent, ln, 1) for j in (0, 1)], 1) for i in range(20)], 1)
+        dev = c.cuda()
+        tk.beam_reorder([dev[:, i, j] for i in range(20) for j in (0, 1)], parent.cuda(), lengths=None if ln is None else ln.cuda())
+        assert torch.equal(dev.cpu(), want)
+    # heads before time, and from one half into the other
+    h = torch.randint(0, 100, (B * K, 3, 2, 9, dim), generator=g).to(dtype)
+    want = torch.stack([ref_reorder(h[:, :, j], h[:, :, j], parent, None, 2) for j in (0, 1)], 2)
+    dev = h.cuda()
+    tk.beam_reorder([dev[:, :, j] for j in (0, 1)], parent.cuda(), time_dim=2)
+    assert torch.equal(dev.cpu(), want)
+    dev = c.cuda()
+    tk.beam_reorder(dev[:, :, 0], parent.cuda(), out=dev[:, :, 1], time_dim=2)
+    want = c.clone()
+    want[:, :, 1] = ref_reorder(c[:, :, 0], c[:, :, 1], parent, None, 2)
+    assert torch.equal(dev.cpu(), want)

@@ -1,9 +1,11 @@
 // C ABI of the decoding calls (topkp_decode.h): argument checks (host only,
 // no device sync) and launches, in the order of api.cu: null pointers, then
 // dtypes, then shapes.
+#include <algorithm>
 #include <climits>
 #include <cstdarg>
 #include <cstdio>
+#include <cstdlib>
 
 #include "decode.h"
 #include "internal.h"
@@ -42,6 +44,77 @@ topkp_status launched(const char* fn, cudaError_t e, int launches) {
   }
   report_launches(launches);
   return TOPKP_SUCCESS;
+}
+
+// One side of a state of the reordering: rows of blocks of bytes.
+struct Region {
+  uintptr_t at;
+  int64_t row, block;    // strides
+  int64_t blocks, len;   // of a row; bytes of a block
+  int64_t extent;        // bytes from a row's first to its last
+  int64_t state;
+  bool written;
+  uintptr_t end(int64_t rows) const { return at + (uintptr_t)((rows - 1) * row + extent); }
+  uintptr_t residue() const { return at % (uintptr_t)row; }
+};
+int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b < 0); }
+// Whether two regions of `rows` rows share a byte.  Exact where their strides
+// are equal; with two block strides a row counts as one block from its first
+// byte to its last, and with two row strides the whole regions do.
+bool share(const Region& a, const Region& b, int64_t rows) {
+  if (a.at >= b.end(rows) || b.at >= a.end(rows)) return false;
+  if (rows > 1 && a.row != b.row) return true;
+  const bool whole = (a.blocks > 1 || b.blocks > 1) && !(a.blocks > 1 && b.blocks > 1 && a.block == b.block);
+  const int64_t na = whole ? 1 : a.blocks, nb = whole ? 1 : b.blocks, la = whole ? a.extent : a.len, lb = whole ? b.extent : b.len;
+  // block p of row i and block q of row j share one iff -lb < d - (i - j) row - (p - q) block < la
+  const int64_t d = (int64_t)(b.at - a.at), m0 = floor_div(d, a.row);
+  for (int64_t m = std::max(m0 - 1, 1 - rows); m <= std::min(m0 + 2, rows - 1); ++m) {
+    const int64_t e = d - m * a.row;
+    if (na == 1 && nb == 1) {
+      if (-lb < e && e < la) return true;
+      continue;
+    }
+    const int64_t low = std::max(floor_div(e - la, a.block) + 1, 1 - nb), high = std::min(floor_div(e + lb - 1, a.block), na - 1);
+    if (low <= high) return true;
+  }
+  return false;
+}
+// Two regions that share a byte, one of them written; false if there are none.
+// Regions are sorted by address and, where a cluster of them lies interleaved
+// (views of one tensor), by their place within a row.
+bool clash(Region* r, int64_t n, int64_t rows, const Region** one, const Region** other) {
+  std::sort(r, r + n, [](const Region& a, const Region& b) { return a.at < b.at; });
+  auto bad = [&](const Region& a, const Region& b) {
+    if (!(a.written || b.written) || !share(a, b, rows)) return false;
+    *one = &a;
+    *other = &b;
+    return true;
+  };
+  for (int64_t first = 0, last; first < n; first = last) {
+    uintptr_t end = r[first].end(rows);
+    bool alike = true;
+    for (last = first + 1; last < n && r[last].at < end; ++last) {
+      end = std::max(end, r[last].end(rows));
+      alike = alike && r[last].row == r[first].row;
+    }
+    if (last - first == 1) continue;
+    if (!alike) {
+      for (int64_t i = first; i < last; ++i)
+        for (int64_t j = i + 1; j < last && r[j].at < r[i].end(rows); ++j)
+          if (bad(r[i], r[j])) return true;
+      continue;
+    }
+    std::sort(r + first, r + last, [](const Region& a, const Region& b) { return a.residue() < b.residue(); });
+    const uintptr_t row = (uintptr_t)r[first].row;
+    for (int64_t i = first; i < last; ++i) {
+      const uintptr_t to = r[i].residue() + (uintptr_t)r[i].extent;
+      for (int64_t j = i + 1; j < last && r[j].residue() < to; ++j)
+        if (bad(r[i], r[j])) return true;
+      for (int64_t j = first; to > row && j < i && r[j].residue() < to - row; ++j)  // past the row's end
+        if (bad(r[i], r[j])) return true;
+    }
+  }
+  return false;
 }
 
 // The slices are planned for this many SMs whatever the device, so that the
@@ -157,21 +230,34 @@ topkp_status topkp_beam_reorder(const topkp_state* states, int64_t count, int64_
     if (s.src == s.dst && (s.src_row_stride != s.dst_row_stride || (s.blocks > 1 && s.src_block_stride != s.dst_block_stride)))
       return fail(TOPKP_ERR_PARAM_INVALID, "%s: state %lld is in place with two layouts", fn, (long long)i);
   }
-  for (int64_t i = 0; i < count; ++i) {
+  Region few[64];
+  Region* regions = few;
+  if (count > 32) regions = count <= (int64_t)(SIZE_MAX / 2 / sizeof(Region)) ? (Region*)malloc((size_t)count * 2 * sizeof(Region)) : nullptr;
+  if (!regions) return fail(TOPKP_ERR_PARAM_INVALID, "%s: no memory for %lld states", fn, (long long)count);
+  int64_t n = 0;
+  topkp_status st = TOPKP_SUCCESS;
+  for (int64_t i = 0; i < count && !st; ++i) {
     const topkp_state& s = states[i];
     if (s.blocks == 0 || s.entries == 0 || s.entry_bytes == 0) continue;
     const Range d = span(s, true);
     if (overlap(d, index[0]) || overlap(d, index[1]))
-      return fail(TOPKP_ERR_PARAM_INVALID, "%s: state %lld overlaps parent or lengths", fn, (long long)i);
-    for (int64_t j = 0; j < count; ++j) {
-      const topkp_state& o = states[j];
-      if (o.blocks == 0 || o.entries == 0 || o.entry_bytes == 0) continue;
-      if (!(j == i && s.src == s.dst) && overlap(d, span(o, false)))
-        return fail(TOPKP_ERR_PARAM_INVALID, "%s: state %lld is written over state %lld", fn, (long long)i, (long long)j);
-      if (j > i && overlap(d, span(o, true)))
-        return fail(TOPKP_ERR_PARAM_INVALID, "%s: states %lld and %lld are written to one place", fn, (long long)i, (long long)j);
-    }
+      st = fail(TOPKP_ERR_PARAM_INVALID, "%s: state %lld overlaps parent or lengths", fn, (long long)i);
+    const int64_t len = s.entries * s.entry_bytes;
+    regions[n++] = {(uintptr_t)s.dst, s.dst_row_stride, s.dst_block_stride, s.blocks, len, (s.blocks - 1) * s.dst_block_stride + len, i, true};
+    if (s.src != s.dst)
+      regions[n++] = {(uintptr_t)s.src, s.src_row_stride, s.src_block_stride, s.blocks, len, (s.blocks - 1) * s.src_block_stride + len, i, false};
   }
+  const Region *one, *other;
+  if (!st && clash(regions, n, B * K, &one, &other)) {
+    if (one->written && other->written)
+      st = fail(TOPKP_ERR_PARAM_INVALID, "%s: states %lld and %lld are written to one place", fn, (long long)std::min(one->state, other->state),
+                (long long)std::max(one->state, other->state));
+    else
+      st = fail(TOPKP_ERR_PARAM_INVALID, "%s: state %lld is written over state %lld", fn, (long long)(one->written ? one : other)->state,
+                (long long)(one->written ? other : one)->state);
+  }
+  if (regions != few) free(regions);
+  if (st) return st;
   int dev = 0;
   if (device_sms(&dev) <= 0) return fail(TOPKP_ERR_LAUNCH, "%s: no usable CUDA device", fn);
   int launches = 0;

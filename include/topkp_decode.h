@@ -139,7 +139,9 @@ typedef struct {
  * for a row of zeros); the stored value is x * 2^-e rounded to e4m3 once, to
  * the nearest, ties to even, and the stored exponent e + 127.  Infinities
  * become the largest value, NaN stays NaN.  As the scale is a power of two
- * the only error of the cache is that one rounding.
+ * the only error of the cache is that one rounding.  At the top of a type's
+ * range it goes past it: fp16 magnitudes from 63488 stand for 65536, bf16 and
+ * fp32 ones from 1.9375 * 2^127 for 2^128.
  *
  *   k, v        device, [N, H, D] of dtype (v NULL together with v_cache
  *               NULL: keys alone).
@@ -157,7 +159,7 @@ topkp_status topkp_cache_write(const void* k, const void* v, int64_t N, int64_t 
  * topkp_cache_read -- the reverse: row i of k and v ([N, H, D] of dtype,
  * contiguous) gets the values at slots[i]; a slot outside the cache gives a
  * row of zeros.  A quantised cache is read as its exact values, rounded once
- * to dtype.
+ * to dtype; a value beyond dtype's range is an infinity.
  */
 topkp_status topkp_cache_read(const int64_t* slots, int64_t N, int64_t H, int64_t D, const topkp_cache* k_cache,
                               const topkp_cache* v_cache, int64_t pages, int64_t page_size, topkp_dtype dtype, void* k,
@@ -202,7 +204,8 @@ topkp_status topkp_cache_read(const int64_t* slots, int64_t N, int64_t H, int64_
  * product with the values (fp16's weights below 2^-32 of the row's largest
  * become zero there, those below 2^-21 lose bits).  Over an e4m3 cache q is taken as a sum of e4m3
  * terms (an element is off by at most about 2^-18 of the largest of its row),
- * and with fp16 rows a cached value beyond fp16's range is an infinity.  A
+ * and cached values are rounded to dtype: exact within its range, an infinity
+ * beyond it, and with fp16 rows in steps of 2^-24 below 2^-14.  A
  * value that is not finite spoils the rows of its request that do not see it
  * too, if it is that of a drafted node, and an infinite one may leave NaN;
  * tokens past the last node are never used.  One launch, or two where the

@@ -119,3 +119,22 @@ def test_reorder_interleaved_views(tk, dtype, dim):
     want = c.clone()
     want[:, :, 1] = ref_reorder(c[:, :, 0], c[:, :, 1], parent, None, 2)
     assert torch.equal(dev.cpu(), want)
+
+
+@pytest.mark.parametrize("dtype,last,step,top", [("f16", 63456.0, 63488.0, 65536.0),
+                                                 ("bf16", 1.9296875 * 2.0 ** 127, 1.9375 * 2.0 ** 127, math.inf),
+                                                 ("f32", (1.9375 - 2.0 ** -23) * 2.0 ** 127, 1.9375 * 2.0 ** 127, math.inf)])
+@pytest.mark.parametrize("D,P", [(64, 16), (7, 3)])
+def test_cache_at_the_end_of_a_type(tk, dtype, last, step, top, D, P):
+    """The rounding to e4m3 takes a type's largest magnitudes past its range; below them it does not."""
+    t = T_[dtype]
+    x = torch.ones(4, 1, D, dtype=t)
+    x[0, 0, 1], x[1, 0, 2], x[2, 0, 3], x[3, 0, 0] = last, step, -step, torch.finfo(t).max
+    c = torch.zeros(2, P, 1, D, dtype=torch.uint8, device="cuda").view(R.E4M3)
+    e = torch.zeros(2, P, 1, dtype=torch.uint8, device="cuda")
+    at = torch.arange(4, device="cuda")
+    tk.cache_write(x.cuda(), None, at, c, None, k_exp=e)
+    own, f32 = (tk.cache_read(at, c, None, k_exp=e, dtype=o)[0][:, 0].float().cpu() for o in (t, torch.float32))
+    assert own[0, 1] == f32[0, 1] == (61440.0 if dtype == "f16" else 1.875 * 2.0 ** 127)
+    assert own[1, 2] == math.inf and own[2, 3] == -math.inf and own[3, 0] == math.inf
+    assert f32[1, 2] == top and f32[2, 3] == -top and f32[3, 0] == top

@@ -6,8 +6,10 @@
 // smallest power of two with amax <= 448 * 2^e; 448 = 1.75 * 2^8, so from
 // amax = 1.f * 2^x it is e = x - 8, plus one if 1.f > 1.75: two integer
 // operations on the bits.  Scaling by 2^-e is exact, so the stored value has
-// one rounding, and reading back has none: 4 significant bits always fit the
-// row's type.  A scale that is not a power of two would use up to one more
+// one rounding, and reading back has none within the type's range, where 4
+// significant bits always fit.  That one rounding goes past the range at its
+// very top: fp16 magnitudes from 63488 become 65536, bf16 and fp32 ones from
+// 1.9375 * 2^127 become 2^128, and both read back as infinities.  A scale that is not a power of two would use up to one more
 // binade of e4m3's sixteen, and add a rounding on either side.
 //
 // Measured, heads of 8 x 128, bf16 and e4m3: 65501 tokens written in 102 us

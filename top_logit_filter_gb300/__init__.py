@@ -323,4 +323,5 @@ def last_launch_count() -> int:
     return _lib.load().topkp_last_launch_count()
 
 
-from .decode import beam_reorder, beam_select, cache_read, cache_write, tree_attention  # noqa: E402,F401
+from .decode import (beam_reorder, beam_select, beam_select_workspace_size, cache_read, cache_write,  # noqa: E402,F401
+                     tree_attention, tree_attention_workspace_size)

@@ -302,6 +302,19 @@ def cache_read(slots, k_cache, v_cache, k_exp=None, v_exp=None, dtype=None):
     return k, v
 
 
+def tree_attention_workspace_size(q, k_cache, pages=None, max_context=None) -> int:
+    """Bytes of workspace ``tree_attention`` needs for tensors of these shapes
+    and dtypes (their values are not read)."""
+    lib = _ready()
+    pool, page_size, Hkv, D = k_cache.shape
+    B, T, Hq = q.shape[:3]
+    max_pages = 1 if pages is None else pages.shape[1]
+    cache = (0, 0, _lib.TOPKP_E4M3 if k_cache.dtype == _E4M3 else _CODES[k_cache.dtype], 0, 0, 0, 0, 0, 0)
+    shape = (B, T, Hq, Hkv, D, pool, page_size, max_pages, max_pages,
+             max_pages * page_size if max_context is None else int(max_context), 0, 0, 0, 0, 0, 0, _dtype_code(q), 0.0)
+    return int(lib.topkp_tree_attention_workspace_size(_ATTENTION.pack(0, 0, 0, *cache, *cache, 0, 0, 0, 0, 0, 0, *shape)))
+
+
 def tree_attention(q, k_cache, v_cache, context, pages=None, tree=None, nodes=None, k_exp=None, v_exp=None,
                    scale=None, max_context=None, out=None, want_lse: bool = False, workspace=None):
     """Attention of drafted nodes over a cache and each other (topkp_tree_attention).
@@ -314,8 +327,9 @@ def tree_attention(q, k_cache, v_cache, context, pages=None, tree=None, nodes=No
     None is a chain, and T = 1 ordinary decoding.  nodes: [B] int32, how many
     of the T nodes a request has.  scale: D ** -0.5 when None.  max_context:
     a bound of ``context`` known on the host, which plans the work (the
-    capacity when None).  Returns out ([B, T, Hq, D]), or (out, lse) with
-    lse [B, T, Hq] float32."""
+    capacity when None).  ``workspace``: a uint8 tensor of at least
+    ``tree_attention_workspace_size`` bytes (allocated when None).  Returns
+    out ([B, T, Hq, D]), or (out, lse) with lse [B, T, Hq] float32."""
     lib = _ready()
     _cuda(q, "q", 4)
     if q.dtype not in (torch.float16, torch.bfloat16):

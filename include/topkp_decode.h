@@ -14,8 +14,9 @@
  * The conventions of topkp.h hold: device pointers owned by the caller, no
  * allocation per call, asynchronous launches on the caller's stream, host
  * checks that never synchronise, topkp_last_error_string() for the reason of
- * a refusal, and on any non-zero status nothing was launched.  Every result
- * is deterministic.
+ * a refusal.  On a refusal nothing was launched; after TOPKP_ERR_LAUNCH of a
+ * call of several launches, those before the failed one may have been.  Every
+ * result is deterministic.
  */
 #ifndef TOPKP_DECODE_H
 #define TOPKP_DECODE_H
@@ -104,7 +105,8 @@ typedef struct {
  *            lengths[b][parent[b][j]] entries of each block are live and
  *            move; the rest of the destination row keeps what it held.
  * In place a row that is its own parent costs nothing.  One launch for every
- * 32 states.
+ * 32 states whose places and sizes are multiples of 16 bytes (4 where K is
+ * above 32), of 4, and of neither.
  */
 topkp_status topkp_beam_reorder(const topkp_state* states, int64_t count, int64_t B, int64_t K, const int32_t* parent,
                                 const int32_t* lengths, void* stream);

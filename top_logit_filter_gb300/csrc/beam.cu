@@ -41,8 +41,8 @@
 namespace topkp {
 namespace {
 
-// (64 x 4 x 128256 bf16, 32 x 32 x 151936 fp32: 28.7, 148 us with 256
-// threads, 27.5, 129 with 512, 31.6, 135 with 1024)
+// (one request, 64 x 4 x 128256 bf16, 32 x 32 x 151936 fp32: 10.2, 28.0, 149
+// us with 256 threads, 10.9, 26.6, 124 with 512, 12.6, 30.1, 113 with 1024)
 constexpr int kMergeThreads = 512;
 constexpr int kMW = kMergeThreads / 32;
 constexpr int kPool = 1024;  // units, then elements, of a request that may be chosen
@@ -410,7 +410,7 @@ __device__ __forceinline__ void next_best(F&& each, G&& key_of, unsigned long lo
 }
 
 // One CTA per request, its launch under the scan's end.  Launched alone and
-// from a cold cache 16 us at n = 8, K = 4, 38 at n = 64, K = 32.
+// from a cold cache 17 us at n = 8, K = 4, 30 at n = 64, K = 32.
 template <int DT>
 __global__ void __launch_bounds__(kMergeThreads) beam_merge(const BeamArgs a) {
   using raw = typename DType<DT>::raw;

@@ -155,3 +155,45 @@ def test_beam_many_wide_beams(tk, dtype, K, V, B):
     scores[0, 1] = -1e9
     check(tk, rows(B * K, V, dtype, V), scores, 64, fin, pad=V - 1)
     check(tk, rows(B * K, V, dtype, V + 1), scores, K)
+
+
+@pytest.mark.parametrize("dtype,K,V,n", [("f32", 32, 151936, 64), ("bf16", 16, 152064, 128), ("f16", 64, 32000, 100)])
+def test_beam_few_live_among_many(tk, dtype, K, V, n):
+    """One or two live beams hold all the best: the groups of units bound them badly, and thousands of units pass."""
+    x = rows(K, V, dtype, n)
+    for dead in (-INF, -1e9, -3e38, -40.0):
+        s = torch.full((1, K), dead)
+        s[0, K // 2] = -1.0
+        check(tk, x, s, n)
+        s[0, K - 1] = -1.5
+        fin = torch.zeros(1, K, dtype=torch.uint8)
+        fin[0, ::5] = 1
+        check(tk, x, s, n, fin, pad=3)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_beam_thousands_of_equal_units(tk, dtype):
+    """More equal maxima than are listed at once, equal to the last bit or nearly so, over beams of equal and other scores."""
+    K, V = 12, 151936
+    s = torch.tensor([[0.0, -1.0, 0.0, -1e9, 0.0, -0.5, -INF, 0.0, -2.0, 0.0, 0.0, 0.0]])
+    z = torch.zeros(K, V, dtype=T_[dtype])
+    check(tk, z, s, 128)
+    z[:, ::2] = -0.0
+    z[7, 77777] = -1.0
+    check(tk, z, s, 70, torch.tensor([[0, 0, 1, 0, 0, 0, 0, 1, 0, 0, 0, 1]], dtype=torch.uint8), pad=9)
+    few = rows(K, V, dtype, 5).clamp(-2, 2).round()     # the largest value in every unit
+    check(tk, few, s, 128)
+    near = torch.full((K, V), 2.0).view(torch.int32) + torch.randint(0, 3, (K, V), generator=torch.Generator().manual_seed(1), dtype=torch.int32)
+    check(tk, near.view(torch.float32).to(T_[dtype]), s, 64)
+
+
+def test_beam_signed_zeros(tk):
+    """Nothing but zeros of either sign, where bounds and sums are exactly zero too."""
+    g = torch.Generator().manual_seed(2)
+    for K, V, n in ((32, 1, 32), (32, 2, 50), (5, 1, 9), (3, 700, 20)):
+        sign = torch.where(torch.rand(K, V, generator=g) < 0.5, 0.0, -0.0)
+        fin = (torch.rand(1, K, generator=g) < 0.3).to(torch.uint8)
+        for zero in (0.0, -0.0):
+            check(tk, sign, torch.full((1, K), zero), n)
+            check(tk, sign, torch.full((1, K), zero), n, fin)
+            check(tk, torch.full((K, V), -0.0, dtype=torch.bfloat16), torch.full((1, K), zero), n, fin)

@@ -514,10 +514,12 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const BeamArgs a) {
   auto fill_keys = [&](int m) {
     for (int i = tid; i < m; i += kMergeThreads) pool.key[i] = key_of(pool.place[i]);
   };
-  // Bounds in fp32, each with twice what four of its roundings can amount to:
-  // a candidate is at least at_least(k, x), and one of t or more has a logit
-  // of at least low_of(k, t).
-  auto slack = [&](int k, float x) { return 4.8e-7f * (fabsf(score32[k]) + fabsf(base32[k]) + fabsf(less32[k]) + fabsf(x)); };
+  // Bounds in fp32, each with twice what four of its roundings can amount to
+  // (and never 0, which as a key lies above -0): a candidate is at least
+  // at_least(k, x), and one of t or more has a logit of at least low_of(k, t).
+  auto slack = [&](int k, float x) {
+    return 1e-30f + 4.8e-7f * (fabsf(score32[k]) + fabsf(base32[k]) + fabsf(less32[k]) + fabsf(x));
+  };
   auto at_least = [&](int k, float x) {
     return state[k] == 2 ? score32[k] : score32[k] + ((x - base32[k]) - less32[k]) - slack(k, x);
   };

@@ -30,7 +30,7 @@
 // DRAM), both kernels 124; 64 x 4 x 128256 bf16, n = 8, scan 17 us (3.8 TB/s:
 // issue, and the latency of CTAs that live for a few loads), both 26.5, the
 // merge being a chain of dependent steps on one CTA a request; one request of
-// 4 x 32000 10.9, two such chains.  Logits beyond +-60000 throughout: 135 and
+// 4 x 32000 11.0, two such chains.  Logits beyond +-60000 throughout: 135 and
 // 28; 31 of 32 beams marked with -1e9 (nth_unit() is called for): 258.
 #include <float.h>
 #include <limits.h>
@@ -42,7 +42,7 @@ namespace topkp {
 namespace {
 
 // (one request, 64 x 4 x 128256 bf16, 32 x 32 x 151936 fp32: 10.2, 28.0, 149
-// us with 256 threads, 10.9, 26.6, 124 with 512, 12.6, 30.1, 113 with 1024)
+// us with 256 threads, 11.0, 26.5, 124 with 512, 12.6, 30.1, 113 with 1024)
 constexpr int kMergeThreads = 512;
 constexpr int kMW = kMergeThreads / 32;
 constexpr int kPool = 1024;  // units, then elements, of a request that may be chosen

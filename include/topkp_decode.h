@@ -11,6 +11,17 @@
  *   topkp_tree_attention  attention of one token, a drafted chain or a
  *                         drafted tree of each request over its cache
  *
+ * and when several continuations share a prompt, or drafted tokens are tried:
+ *
+ *   topkp_shared_attention  the same where requests share a prefix, whose keys
+ *                         and values are read once for all of them
+ *   topkp_draft_verify    which drafted tokens the target's probabilities
+ *                         accept, and the token to go on with
+ *   topkp_cache_compact   the accepted tokens of a tree move up behind the
+ *                         context
+ *   topkp_cache_fork      block tables and pages follow the requests that go
+ *                         on: forked, freed and grown
+ *
  * The conventions of topkp.h hold: device pointers owned by the caller, no
  * allocation per call, asynchronous launches on the caller's stream, host
  * checks that never synchronise, topkp_last_error_string() for the reason of
@@ -34,6 +45,8 @@ extern "C" {
  * is given by masks (a chain may be longer). */
 #define TOPKP_MAX_HEAD_DIM 256
 #define TOPKP_MAX_TREE 64
+/* Largest number of rows of a block table that topkp_cache_fork takes or makes. */
+#define TOPKP_MAX_ROWS 8192
 
 /*
  * topkp_beam_select -- one step of beam search.  For request b, beam k and
@@ -236,6 +249,181 @@ typedef struct {
  * max_pages) and the dtypes of args only. */
 size_t topkp_tree_attention_workspace_size(const topkp_tree_attention_args* args);
 topkp_status topkp_tree_attention(const topkp_tree_attention_args* args, void* stream);
+
+/*
+ * topkp_shared_attention -- topkp_tree_attention of requests that share a
+ * prefix.  The B requests are `groups` runs of B / groups consecutive ones;
+ * tokens [0, shared[g]) are the same for all requests of group g (the same
+ * pages, or equal contents), and are read once for all of them, through the
+ * block table of the group's first request.  The result is that of
+ * topkp_tree_attention but for the order of the sums.
+ *
+ *   args        as for topkp_tree_attention; table is not NULL.
+ *   shared      device, [groups] int32.  What is read once is the largest
+ *               multiple of 64 tokens within shared[g] and within the context
+ *               of every request of the group that has a node; a value of
+ *               zero or less, or one that is too small, costs speed only.
+ *   groups      at least 1, divides B.
+ *   max_shared  an upper bound of shared[g] that plans how the work is split
+ *               (results hold for any value).
+ * args->workspace has topkp_shared_attention_workspace_size() bytes.  Three
+ * launches.
+ */
+size_t topkp_shared_attention_workspace_size(const topkp_tree_attention_args* args, int64_t groups, int64_t max_shared);
+topkp_status topkp_shared_attention(const topkp_tree_attention_args* args, const int32_t* shared, int64_t groups,
+                                    int64_t max_shared, void* stream);
+
+/*
+ * topkp_draft_verify -- speculative decoding's choice.  Request b has T
+ * drafted nodes, node 0 the last accepted token (its own token is not looked
+ * at).  With p the softmax of the target's logits after node n, the children
+ * of n are tried in increasing order, and the walk goes on at the first that
+ * is accepted; where none is, one token is drawn, and the walk ends.
+ *   draft given: the children's tokens are independent draws from q, the
+ *     softmax of the draft's logits after n.  Child c with token x is accepted
+ *     iff uniform[c] * q(x) < p(x); after a child that is not, p becomes
+ *     max(p - q, 0) over its sum.
+ *   draft NULL: the children are certain (q is 1 at the child's token): x is
+ *     accepted iff uniform[c] < p(x), and otherwise taken out of p, whose rest
+ *     is divided by its sum.
+ *   The token drawn is the largest p(v) / (race[v] + eps), the lowest v of
+ *     equal ones; with race i.i.d. from Exp(1) it is a draw from p.  Where
+ *     nothing is left of p (which roundings alone can bring about) it is drawn
+ *     from p as it was at first.
+ *   uniform and race both NULL (greedy): a child is accepted iff its token is
+ *     the lowest index of the largest logit after n, and that is the token
+ *     drawn.  draft must be NULL.
+ * With uniform numbers of [0, 1) the emitted tokens are distributed as the
+ * target's own.  A token outside [0, V) is never accepted and changes nothing.
+ *
+ *   target     device, [B, T, V] of dtype, strides in elements (node_stride
+ *              >= V), V contiguous; -inf is a token that the filter removed.
+ *              Only the rows of the accepted path are read.
+ *   draft      device, the same, or NULL; rows of accepted nodes that have
+ *              children are read.
+ *   tokens     device, [B, T] int32.
+ *   parent     device, [B, T] int32: node i (i > 0) is a child of
+ *              parent[b][i] < i, other nodes are nobody's; NULL: a chain.
+ *   nodes      device, [B] int32 (clamped to [0, T]), or NULL (T for all).
+ *   uniform    device, [B, T] float (that of node 0 is not used).
+ *   race       device, [B, V] float, row stride ld_race; expected >= 0.
+ *   eps        added to every race, >= 0.
+ *   T          1 .. TOPKP_MAX_TREE.  V at most TOPKP_MAX_V.
+ *   count      device, [B] int32: nodes of the accepted path, node 0 included;
+ *              0 for a request without nodes.
+ *   path       device, [B, T] int32: the nodes of that path, then -1.
+ *   token      device, [B] int32: the token drawn; -1 for a request without
+ *              nodes, and where a row has no logit above -inf.
+ *   logprob    device, [B, T] float, or NULL: log p (of the node's whole row)
+ *              of the path's second token and on, and behind them of the token
+ *              drawn; 0 elsewhere.
+ * Sums of exponentials are fp32 within a warp and 64-bit beyond; a decision
+ * may differ from exact arithmetic where its two sides lie within about 1e-6
+ * (relative to p) of one another.  NaN and +inf give an unspecified result.
+ * One launch.
+ */
+typedef struct {
+  const void* target;
+  const void* draft;
+  const int32_t* tokens;
+  const int32_t* parent;
+  const int32_t* nodes;
+  const float* uniform;
+  const float* race;
+  int32_t* count;
+  int32_t* path;
+  int32_t* token;
+  float* logprob;
+  int64_t B, T, V;
+  int64_t target_batch_stride, target_node_stride, draft_batch_stride, draft_node_stride, ld_race;
+  topkp_dtype dtype;
+  float eps;
+} topkp_draft_verify_args;
+topkp_status topkp_draft_verify(const topkp_draft_verify_args* args, void* stream);
+
+/*
+ * One tensor of pages for topkp_cache_fork and topkp_cache_compact: page p
+ * has `blocks` blocks of page_size entries of entry_bytes bytes, one after
+ * another; strides in bytes.  A cache [pages, page_size, heads, dim] has one
+ * block; [pages, heads, page_size, dim] has `heads`.  Keys, values and
+ * exponents of every layer are states of one call.  States may lie between
+ * each other's pages (views of one tensor) but share no byte, as in
+ * topkp_beam_reorder.
+ */
+typedef struct {
+  void* data;
+  int64_t page_stride, block_stride;
+  int64_t blocks, entry_bytes;
+} topkp_pages;
+
+/*
+ * topkp_cache_fork -- new row n of the block table goes on from old row
+ * source[n], whose first lengths[source[n]] tokens are live.
+ *   - Whole pages are shared with the old row.  A partly filled last page
+ *     stays with the first new row that continues it, if nobody else holds
+ *     it; every other row gets a free page and a copy of the live tokens.
+ *   - The row then grows by free pages to hold `grow` tokens more, but to no
+ *     more than max_pages pages.  Its other entries become -1.
+ *   - What the old rows held and no new row does is given up.  refs counts
+ *     the holders of a page; one without any is free.  Holders outside the
+ *     table (another table, a prefix kept for later) count like rows.
+ *   - Free pages are given out in increasing order: row after row, a row's
+ *     copy before its growth.
+ * So one call forks, reorders, frees (a row that no source names), starts
+ * (a source outside [0, R) is an empty row) and grows requests.  Where fewer
+ * pages are free than wanted nothing happens: missing[0] is how many lack,
+ * the new table is all -1, refs_out equals refs, no page is written.
+ *
+ *   states     host array of `count` descriptors, read during the call.
+ *   table      device, [R, max_pages] int32, row stride ld_table; an entry
+ *              outside [0, pages) holds nothing and goes on as -1.
+ *   lengths    device, [R] int32, clamped to [0, max_pages * page_size].
+ *   source     device, [N] int32.
+ *   grow       device, [N] int32, or NULL: grow_all for every row.
+ *   refs       device, [pages] int32, at least 1 for every entry of the table.
+ *   table_out  device, [N, max_pages] int32, row stride ld_out; not table.
+ *   refs_out   device, [pages] int32; refs itself, or apart from it.
+ *   missing    device, [1] int32.
+ *   workspace  device, at least topkp_cache_fork_workspace_size() bytes,
+ *              256-byte aligned.
+ * R and N are at most TOPKP_MAX_ROWS, R or N times max_pages at most 2^30;
+ * N == 0 frees every row.  One launch, and one for every 128 states.
+ */
+typedef struct {
+  const topkp_pages* states;
+  const int32_t* table;
+  const int32_t* lengths;
+  const int32_t* source;
+  const int32_t* grow;
+  const int32_t* refs;
+  int32_t* table_out;
+  int32_t* refs_out;
+  int32_t* missing;
+  void* workspace;
+  size_t workspace_bytes;
+  int64_t count, R, N, max_pages, ld_table, ld_out, pages, page_size, grow_all;
+} topkp_cache_fork_args;
+size_t topkp_cache_fork_workspace_size(int64_t N, int64_t pages);
+topkp_status topkp_cache_fork(const topkp_cache_fork_args* args, void* stream);
+
+/*
+ * topkp_cache_compact -- of request b's tokens from start[b] on, those at
+ * start[b] + keep[b][j] move to start[b] + j, j < kept[b] (topkp_draft_verify's
+ * path and count, after which the request's length is start[b] + kept[b]).
+ * All are read as they were before the call.  An entry with keep[b][j] <= j,
+ * or of which either place lies outside the request's pages, is left alone.
+ *
+ *   states     host array of `count` descriptors, read during the call.
+ *   table      device, [B, max_pages] int32, row stride ld_table, or NULL:
+ *              page b is request b's whole cache (pages == B, max_pages 1).
+ *              No two requests hold a page that either moves tokens in.
+ *   start, kept  device, [B] int32.
+ *   keep       device, [B, W] contiguous int32, W at most TOPKP_MAX_TREE.
+ * One launch for every 128 states.
+ */
+topkp_status topkp_cache_compact(const topkp_pages* states, int64_t count, int64_t B, int64_t W, const int32_t* table,
+                                 int64_t ld_table, int64_t max_pages, int64_t pages, int64_t page_size,
+                                 const int32_t* start, const int32_t* keep, const int32_t* kept, void* stream);
 
 #ifdef __cplusplus
 }

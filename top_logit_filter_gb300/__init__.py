@@ -17,6 +17,10 @@ and, for decoding with beams or drafted tokens (``decode``):
     cache_write(k, v, slots, k_cache, v_cache)
     k, v = cache_read(slots, k_cache, v_cache)
     out = tree_attention(q, k_cache, v_cache, context, pages=None, tree=None)
+    out = shared_attention(q, k_cache, v_cache, context, pages, shared, tree=None)
+    count, path, token = draft_verify(target, tokens, uniform=None, race=None, draft=None)
+    states = cache_compact(states, start, keep, kept, pages=None)
+    pages, refs, missing = cache_fork(states, pages, lengths, source, refs, grow=0)
 
 Semantics: section 2 of the web page "CANN ops-nn 算子实战：
 ApplyTopKTopPWithSorted 的 top-k/top-p 采样过滤原理与 aclnn 调用指南" --
@@ -323,5 +327,6 @@ def last_launch_count() -> int:
     return _lib.load().topkp_last_launch_count()
 
 
-from .decode import (beam_reorder, beam_select, beam_select_workspace_size, cache_read, cache_write,  # noqa: E402,F401
-                     tree_attention, tree_attention_workspace_size)
+from .decode import (beam_reorder, beam_select, beam_select_workspace_size, cache_compact, cache_fork,  # noqa: E402,F401
+                     cache_fork_workspace_size, cache_read, cache_write, draft_verify, shared_attention,
+                     shared_attention_workspace_size, tree_attention, tree_attention_workspace_size)

@@ -28,12 +28,15 @@ EXPORTS = ("topkp_apply", "topkp_apply_sample", "topkp_apply_sorted", "topkp_sam
 
 # every entry point declared in include/topkp_decode.h
 DECODE_EXPORTS = ("topkp_beam_select", "topkp_beam_select_workspace_size", "topkp_beam_reorder", "topkp_cache_write",
-                  "topkp_cache_read", "topkp_tree_attention", "topkp_tree_attention_workspace_size")
+                  "topkp_cache_read", "topkp_tree_attention", "topkp_tree_attention_workspace_size", "topkp_shared_attention",
+                  "topkp_shared_attention_workspace_size", "topkp_draft_verify", "topkp_cache_compact", "topkp_cache_fork",
+                  "topkp_cache_fork_workspace_size")
 TOPKP_E4M3 = 3
 TOPKP_MAX_BEAMS = 64
 TOPKP_MAX_CANDIDATES = 128
 TOPKP_MAX_HEAD_DIM = 256
 TOPKP_MAX_TREE = 64
+TOPKP_MAX_ROWS = 8192
 
 
 class State(ctypes.Structure):
@@ -58,6 +61,26 @@ class TreeAttentionArgs(ctypes.Structure):
                                       "max_context", "q_batch_stride", "q_token_stride", "q_head_stride",
                                       "out_batch_stride", "out_token_stride", "out_head_stride")] + [
         ("dtype", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class DraftVerifyArgs(ctypes.Structure):
+    """topkp_draft_verify_args"""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("target", "draft", "tokens", "parent", "nodes", "uniform", "race", "count",
+                                               "path", "token", "logprob")] + [
+        (n, ctypes.c_int64) for n in ("B", "T", "V", "target_batch_stride", "target_node_stride", "draft_batch_stride",
+                                      "draft_node_stride", "ld_race")] + [("dtype", ctypes.c_int), ("eps", ctypes.c_float)]
+
+
+class Pages(ctypes.Structure):
+    """topkp_pages"""
+    _fields_ = [("data", ctypes.c_void_p)] + [(n, ctypes.c_int64) for n in ("page_stride", "block_stride", "blocks", "entry_bytes")]
+
+
+class CacheForkArgs(ctypes.Structure):
+    """topkp_cache_fork_args"""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("states", "table", "lengths", "source", "grow", "refs", "table_out", "refs_out",
+                                               "missing", "workspace")] + [("workspace_bytes", ctypes.c_size_t)] + [
+        (n, ctypes.c_int64) for n in ("count", "R", "N", "max_pages", "ld_table", "ld_out", "pages", "page_size", "grow_all")]
 
 
 _lib = None
@@ -109,6 +132,18 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.topkp_tree_attention_workspace_size.restype = ctypes.c_size_t
     lib.topkp_tree_attention.argtypes = [vp, vp]
     lib.topkp_tree_attention.restype = c_int
+    lib.topkp_shared_attention_workspace_size.argtypes = [vp, i64, i64]
+    lib.topkp_shared_attention_workspace_size.restype = ctypes.c_size_t
+    lib.topkp_shared_attention.argtypes = [vp, vp, i64, i64, vp]
+    lib.topkp_shared_attention.restype = c_int
+    lib.topkp_draft_verify.argtypes = [vp, vp]
+    lib.topkp_draft_verify.restype = c_int
+    lib.topkp_cache_compact.argtypes = [vp, i64, i64, i64, vp, i64, i64, i64, i64, vp, vp, vp, vp]
+    lib.topkp_cache_compact.restype = c_int
+    lib.topkp_cache_fork_workspace_size.argtypes = [i64, i64]
+    lib.topkp_cache_fork_workspace_size.restype = ctypes.c_size_t
+    lib.topkp_cache_fork.argtypes = [vp, vp]
+    lib.topkp_cache_fork.restype = c_int
     lib.topkp_last_error_string.argtypes = []
     lib.topkp_last_error_string.restype = ctypes.c_char_p
     lib.topkp_device_status.argtypes = [vp]

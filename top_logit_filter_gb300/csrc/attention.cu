@@ -9,8 +9,15 @@
 // cache's bytes bound the work (64 single tokens, 32 query and 8 cache heads
 // of 128, contexts to 8192: 251 us, 6.4 TB/s; 2 x 131000 tokens: 153 us, 5.3,
 // in one round of CTAs), with more the products and exponentials.
+//
+// topkp_shared_attention: what requests share is one launch in which a group
+// is a request with the nodes of all its requests, so its keys and values are
+// read once a group; each request's own tokens are another, beside it; the
+// join takes the parts of both.
 #include <cuda.h>
 #include <math.h>
+
+#include <algorithm>
 
 #include "common.cuh"
 #include "decode.h"
@@ -32,6 +39,15 @@ struct AttnDev {
   int page_shift;
   int wide;           // an e4m3 row may be read 16 bytes at a time
   int box;            // tokens of a TMA box, 0: plain copies
+  int parts;          // whether outputs are partial ones (to be joined)
+  // Requests that share a prefix.  stage 1: the shared tokens; a request of
+  // `a` is then a group, its nodes those of all its requests in turn.  Stage
+  // 2: each request's own tokens.  0: all tokens of each request.
+  int stage;
+  int size;                // requests of a group
+  int inner;               // stage 1: nodes of a request
+  int64_t q_member;        // stage 1: from request to request in q
+  const int32_t* shared;   // [groups]
 };
 
 // Tokens of request b that its nodes may see: the context, and the end of
@@ -47,6 +63,20 @@ __device__ __forceinline__ void request_span(const topkp_tree_attention_args& a,
 }
 
 constexpr int kTile = 64;  // tokens
+
+// Tokens that group g's requests read together: whole tiles within what they
+// share and within the context of each that has a node.  By a whole warp.
+__device__ __forceinline__ int shared_span(const AttnDev& p, int64_t g) {
+  const topkp_tree_attention_args& a = p.a;
+  int most = p.shared[g];
+  for (int i = threadIdx.x & 31; i < p.size; i += 32) {
+    const int64_t r = g * p.size + i;
+    if (!a.nodes || a.nodes[r] > 0) most = min(most, a.context[r]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) most = min(most, __shfl_xor_sync(0xffffffffu, most, o));
+  return (int)min((long long)max(most, 0), (long long)(a.max_pages * a.page_size)) / kTile * kTile;
+}
 
 template <bool BF>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -182,8 +212,22 @@ cudaError_t launch_tc(AttnDev p, cudaStream_t s) {
     p.box = 0;
   const int64_t rows = a.T * (a.Hq / a.Hkv);
   const dim3 grid((unsigned)((rows + NT * kTcRows - 1) / (NT * kTcRows)), (unsigned)p.splits, (unsigned)(a.B * a.Hkv));
-  attn_tc<DP, NT, BF, Q8, SH><<<grid, Shape::kThreads, Shape::kSmem, s>>>(p, km, vm);
-  return cudaGetLastError();
+  if (p.stage != 2) {
+    attn_tc<DP, NT, BF, Q8, SH><<<grid, Shape::kThreads, Shape::kSmem, s>>>(p, km, vm);
+    return cudaGetLastError();
+  }
+  // the requests' own tokens run beside the shared ones
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(Shape::kThreads);
+  cfg.dynamicSmemBytes = Shape::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_tc<DP, NT, BF, Q8, SH>, p, km, vm);
 }
 
 // Tiles of 128 rows of a CTA (256 dims leave tensor memory for one).
@@ -216,32 +260,63 @@ cudaError_t attention_take_device_error(unsigned int* out) {
   return e;
 }
 
+namespace {
+
+// What a tile of a CTA's costs and how many CTAs the device holds.
+struct Cost {
+  double base;   // CTAs of one part
+  double slots;  // resident ones
+  double tile;   // us a tile
+  int64_t tiles;
+};
+Cost cost_of(const topkp_tree_attention_args& a, int64_t tokens, int num_sms) {
+  const int64_t nt = row_tiles(a), rows = a.T * (a.Hq / a.Hkv);
+  const bool pair = few_rows(a) && a.dtype == TOPKP_BF16;
+  Cost c;
+  c.slots = (nt == 2 || a.D > (a.k.dtype == TOPKP_E4M3 && !pair ? 64 : 128) ? 1.0 : 2.0) * num_sms;
+  c.base = (double)(a.B * a.Hkv * ((rows + nt * kTcRows - 1) / (nt * kTcRows)));
+  // a tile takes a CTA about 0.9 us (1.3 with two of them on an SM)
+  c.tile = c.slots > num_sms ? 1.3 : 0.9;
+  c.tiles = (tokens + kTile - 1) / kTile;
+  return c;
+}
+int64_t bounded_context(const topkp_tree_attention_args& a) {
+  const int64_t cap = a.max_pages * a.page_size;
+  return a.max_context < cap ? (a.max_context > 0 ? a.max_context : 0) : cap;
+}
+// The shared tokens' launch: a group's requests are one, its nodes theirs.
+topkp_tree_attention_args as_groups(const topkp_tree_attention_args& a, int64_t groups) {
+  topkp_tree_attention_args g = a;
+  const int64_t size = a.B / groups;
+  g.B = groups;
+  g.T = a.T * size;
+  g.q_batch_stride *= size;
+  g.ld_table *= size;
+  g.tree = nullptr;
+  g.lse = nullptr;
+  return g;
+}
+
+}  // namespace
+
 AttnPlan plan_attention(const topkp_tree_attention_args& a, int num_sms) {
   AttnPlan p;
-  const int64_t rows = a.T * (a.Hq / a.Hkv);
-  const int64_t cap = a.max_pages * a.page_size;
-  const int64_t len = (a.max_context < cap ? (a.max_context > 0 ? a.max_context : 0) : cap) + a.T;
-  const int64_t tiles = (len + kTile - 1) / kTile;
+  const Cost c = cost_of(a, bounded_context(a) + a.T, num_sms);
   // Parts of equal size, whatever a request's length, so that the CTAs of
   // ragged requests even out.  In units of a tile's time: the rounds of CTAs
   // (between whole ones, as for equal requests, and what ragged ones average
   // to), four tiles for a CTA's start and end, and writing and reading the
   // partial outputs.
-  const int64_t nt = row_tiles(a);
-  const bool pair = few_rows(a) && a.dtype == TOPKP_BF16;
-  const double slots = (nt == 2 || a.D > (a.k.dtype == TOPKP_E4M3 && !pair ? 64 : 128) ? 1.0 : 2.0) * num_sms;
-  const double base = (double)(a.B * a.Hkv * ((rows + nt * kTcRows - 1) / (nt * kTcRows)));
-  // a tile takes a CTA about 0.9 us (1.3 with two of them on an SM); a part
-  // of every row costs 8 bytes an element at the copy's rate
-  const double join = (double)(a.B * a.T * a.Hq * a.D) * 8.0 / 6.8e6 / (slots > num_sms ? 1.3 : 0.9);
+  // A part of every row costs 8 bytes an element at the copy's rate.
+  const double join = (double)(a.B * a.T * a.Hq * a.D) * 8.0 / 6.8e6 / c.tile;
   double best = -1.0;
   p.splits = 1;
-  p.per = (int)tiles;
-  for (int64_t n = 1; n <= kMaxParts && n <= tiles; ++n) {
-    const int64_t per = (tiles + n - 1) / n;
-    if ((tiles + per - 1) / per != n) continue;
+  p.per = (int)c.tiles;
+  for (int64_t n = 1; n <= kMaxParts && n <= c.tiles; ++n) {
+    const int64_t per = (c.tiles + n - 1) / n;
+    if ((c.tiles + per - 1) / per != n) continue;
     const double part = (double)per + 4.0;
-    const double rounds = base * n / slots;
+    const double rounds = c.base * n / c.slots;
     double cost = rounds <= 1.0 ? part : 0.5 * (ceil(rounds) + rounds + 0.5) * part;
     if (n > 1) cost += 3.0 + join * n;
     if (best < 0 || cost < best) {
@@ -250,20 +325,59 @@ AttnPlan plan_attention(const topkp_tree_attention_args& a, int num_sms) {
       p.per = (int)per;
     }
   }
+  p.us = best * c.tile;
   p.part_bytes = p.splits > 1 ? (size_t)p.splits * (size_t)(a.B * a.T * a.Hq) * (a.D + 1) * sizeof(float) : 0;
   return p;
 }
 
-cudaError_t launch_attention(const topkp_tree_attention_args& a, const AttnPlan& plan, int* launches, cudaStream_t s) {
-  AttnDev p;
+// Parts of the shared tokens and of the requests' own, which run side by
+// side: both kernels' CTAs fill the device together.
+SharedPlan plan_shared(const topkp_tree_attention_args& a, int64_t groups, int64_t max_shared, int num_sms) {
+  SharedPlan s;
+  const AttnPlan alone = plan_attention(a, num_sms);
+  s.groups = 0;  // every request by itself
+  s.own = alone;
+  s.part_bytes = alone.part_bytes;
+  const int64_t context = bounded_context(a), front = std::min(max_shared, context) / kTile * kTile;
+  if (groups >= a.B || front <= 0) return s;
+  const Cost x = cost_of(as_groups(a, groups), front, num_sms), y = cost_of(a, context - front + a.T + kTile - 1, num_sms);
+  const double join = (double)(a.B * a.T * a.Hq * a.D) * 8.0 / 6.8e6;
+  static const int counts[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32, 40, 48, 64, 80, 96};
+  double best = -1.0;
+  for (const int i : counts) {
+    const int64_t px = (x.tiles + i - 1) / i, nx = (x.tiles + px - 1) / px;
+    if (i > x.tiles) break;
+    for (const int j : counts) {
+      const int64_t py = (y.tiles + j - 1) / j, ny = (y.tiles + py - 1) / py;
+      if (j > y.tiles || nx + ny > kMaxParts) break;
+      const double tx = ((double)px + 4.0) * x.tile, ty = ((double)py + 4.0) * y.tile;
+      const double fx = x.base * nx / x.slots, fy = y.base * ny / y.slots, fill = fx + fy;
+      double us = std::max(tx, ty);
+      if (fill > 1.0) us = std::max(us, 0.5 * (ceil(fill) + fill + 0.5) * (fx * tx + fy * ty) / fill);
+      us += 4.0 + join * (nx + ny);
+      if (best < 0 || us < best) {
+        best = us;
+        s.front.splits = (int)nx;
+        s.front.per = (int)px;
+        s.own.splits = (int)ny;
+        s.own.per = (int)py;
+      }
+    }
+  }
+  if (alone.us <= best) {  // little is shared: not worth another launch
+    s.own = alone;
+    return s;
+  }
+  s.groups = groups;
+  s.part_bytes = (size_t)(s.front.splits + s.own.splits) * (size_t)(a.B * a.T * a.Hq) * (a.D + 1) * sizeof(float);
+  return s;
+}
+
+namespace {
+
+AttnDev device_args(const topkp_tree_attention_args& a) {
+  AttnDev p = {};
   p.a = a;
-  p.splits = plan.splits;
-  p.per = plan.per;
-  const size_t all = (size_t)(a.B * a.T * a.Hq);
-  p.part_o = reinterpret_cast<float*>(a.workspace);
-  p.part_l = p.part_o + (plan.splits > 1 ? (size_t)plan.splits * all * a.D : 0);
-  p.page_mul = 0;
-  p.page_shift = 0;
   if (a.page_size > 1) {  // t / page_size = (t * mul) >> (32 + shift), exact below 2^31
     int l = 1;
     while ((1LL << l) < a.page_size) ++l;
@@ -274,14 +388,23 @@ cudaError_t launch_attention(const topkp_tree_attention_args& a, const AttnPlan&
     return ((uintptr_t)c.data | (uintptr_t)c.page_stride | (uintptr_t)c.token_stride | (uintptr_t)c.head_stride) % 16 == 0;
   };
   p.wide = a.D % 16 == 0 && by16(a.k) && by16(a.v);
-  const bool bf = a.dtype == TOPKP_BF16, q8 = a.k.dtype == TOPKP_E4M3;
-  cudaError_t e = bf ? (q8 ? launch_dim<true, true>(p, s) : launch_dim<true, false>(p, s))
-                     : (q8 ? launch_dim<false, true>(p, s) : launch_dim<false, false>(p, s));
-  *launches = 1;
-  if (e != cudaSuccess || plan.splits <= 1) return e;
-  // the join's launch overlaps the parts; it waits for them itself
+  return p;
+}
+// Room for the partial outputs of all parts: their rows, then their log-sums.
+void give_parts(AttnDev& p, int parts) {
+  const size_t all = (size_t)(p.a.B * p.a.T * p.a.Hq);
+  p.part_o = reinterpret_cast<float*>(p.a.workspace);
+  p.part_l = p.part_o + (parts > 1 ? (size_t)parts * all * p.a.D : 0);
+}
+cudaError_t launch_parts(const AttnDev& p, cudaStream_t s) {
+  const bool bf = p.a.dtype == TOPKP_BF16, q8 = p.a.k.dtype == TOPKP_E4M3;
+  return bf ? (q8 ? launch_dim<true, true>(p, s) : launch_dim<true, false>(p, s))
+            : (q8 ? launch_dim<false, true>(p, s) : launch_dim<false, false>(p, s));
+}
+// The join's launch overlaps the parts; it waits for them itself.
+cudaError_t launch_join(const AttnDev& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((all + 3) / 4));
+  cfg.gridDim = dim3((unsigned)((p.a.B * p.a.T * p.a.Hq + 3) / 4));
   cfg.blockDim = dim3(128);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -289,8 +412,53 @@ cudaError_t launch_attention(const topkp_tree_attention_args& a, const AttnPlan&
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  return p.a.dtype == TOPKP_BF16 ? cudaLaunchKernelEx(&cfg, attn_join<true>, p) : cudaLaunchKernelEx(&cfg, attn_join<false>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_attention(const topkp_tree_attention_args& a, const AttnPlan& plan, int* launches, cudaStream_t s) {
+  AttnDev p = device_args(a);
+  p.splits = plan.splits;
+  p.per = plan.per;
+  p.parts = plan.splits > 1;
+  give_parts(p, plan.splits);
+  const cudaError_t e = launch_parts(p, s);
+  *launches = 1;
+  if (e != cudaSuccess || plan.splits <= 1) return e;
   *launches = 2;
-  return bf ? cudaLaunchKernelEx(&cfg, attn_join<true>, p) : cudaLaunchKernelEx(&cfg, attn_join<false>, p);
+  return launch_join(p, s);
+}
+
+cudaError_t launch_shared(const topkp_tree_attention_args& a, const int32_t* shared, const SharedPlan& plan, int* launches, cudaStream_t s) {
+  if (!plan.groups) return launch_attention(a, plan.own, launches, s);
+  const int parts = plan.front.splits + plan.own.splits;
+  const size_t all = (size_t)(a.B * a.T * a.Hq);
+  AttnDev own = device_args(a);
+  give_parts(own, parts);
+  own.parts = 1;
+  own.size = (int)(a.B / plan.groups);
+  own.shared = shared;
+  AttnDev front = own;
+  front.a = as_groups(a, plan.groups);
+  front.stage = 1;
+  front.inner = (int)a.T;
+  front.q_member = a.q_batch_stride;
+  front.splits = plan.front.splits;
+  front.per = plan.front.per;
+  *launches = 0;
+  cudaError_t e = launch_parts(front, s);
+  if (e != cudaSuccess) return e;
+  AttnDev join = own;
+  join.splits = parts;
+  own.stage = 2;
+  own.splits = plan.own.splits;
+  own.per = plan.own.per;
+  own.part_o += (size_t)front.splits * all * a.D;
+  own.part_l += (size_t)front.splits * all;
+  e = launch_parts(own, s);
+  *launches = 3;
+  return e != cudaSuccess ? e : launch_join(join, s);
 }
 
 }  // namespace topkp

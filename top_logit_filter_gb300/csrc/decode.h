@@ -77,14 +77,97 @@ struct CacheRowsArgs {
 cudaError_t launch_cache_write(topkp_dtype dt, const CacheRowsArgs& a, cudaStream_t s);
 cudaError_t launch_cache_read(topkp_dtype dt, const CacheRowsArgs& a, cudaStream_t s);
 
+// ----------------------------------------------------------------- verify
+constexpr int kVerifyThreads = 512;
+enum { kVerifyRatio, kVerifyCertain, kVerifyGreedy };
+
+struct VerifyArgs {
+  const void* target;
+  const void* draft;      // or nullptr
+  int64_t t_batch, t_node, d_batch, d_node;
+  const int32_t* tokens;  // [B, T]
+  const int32_t* parent;  // [B, T], or nullptr (a chain)
+  const int32_t* nodes;   // or nullptr
+  const float* uniform;   // [B, T], or nullptr together with race (greedy)
+  const float* race;
+  int64_t ld_race;
+  float eps;
+  int64_t B;
+  int32_t T, V;
+  int32_t cs;     // CTAs of a request
+  int32_t whole;  // rows and variates may be read 16 bytes at a time
+  int32_t* count;
+  int32_t* path;
+  int32_t* token;
+  float* logprob;  // or nullptr
+};
+int verify_cluster(int64_t B, int64_t V, int esize, int num_sms);
+cudaError_t launch_verify(topkp_dtype dt, const VerifyArgs& a, cudaStream_t s);
+
+// ------------------------------------------------------------------ pages
+constexpr int kPageStates = 128;  // per launch (the descriptors travel as kernel parameters)
+constexpr int kForkThreads = 1024, kForkCtas = 8;
+
+struct ForkArgs {
+  const int32_t* table;
+  const int32_t* lengths;
+  const int32_t* source;
+  const int32_t* grow;  // or nullptr: grow_all
+  const int32_t* refs;
+  int32_t* table_out;
+  int32_t* refs_out;
+  int32_t* missing;
+  // workspace
+  int32_t* hold;   // [pages] references that do not come from the old rows, or are carried over
+  int32_t* claim;  // [pages] the first new row whose partial last page it is
+  int32_t* fresh;  // [pages] free pages in the order they are given out
+  int4* copies;    // [N] source page, its copy, tokens (0: none)
+  int64_t ld, ld_out;
+  int64_t pages;
+  int32_t R, N, M, page_size, grow_all;
+};
+struct PageState {
+  char* data;
+  int64_t page_stride, block_stride, blocks, entry_bytes;
+  int32_t unit;  // bytes moved by a thread: 16, 4 or 1
+};
+struct CopyArgs {
+  PageState st[kPageStates];
+  const int4* copies;
+  int32_t count, N, page_size;
+  int32_t chunks;  // set by the launcher
+};
+struct CompactArgs {
+  PageState st[kPageStates];
+  const int32_t* table;  // or nullptr
+  const int32_t* start;
+  const int32_t* keep;
+  const int32_t* kept;
+  int64_t ld, pages;
+  int32_t B, W, M, page_size, count;
+  int32_t chunks;  // set by the launcher
+};
+size_t fork_workspace(int64_t N, int64_t pages);
+cudaError_t launch_fork(const ForkArgs& a, cudaStream_t s);
+cudaError_t launch_page_copy(const CopyArgs& a, cudaStream_t s);
+cudaError_t launch_compact(const CompactArgs& a, cudaStream_t s);
+
 // -------------------------------------------------------------- attention
 struct AttnPlan {
   int splits;         // parts of a request's tokens
   int per;            // tiles of 64 tokens of a part
   size_t part_bytes;  // workspace: partial outputs and their (lse) rows
+  double us;          // estimated
 };
 AttnPlan plan_attention(const topkp_tree_attention_args& a, int num_sms);
 // part_o: [splits][B * T * Hq][D] float, part_l: [splits][B * T * Hq] float
 cudaError_t launch_attention(const topkp_tree_attention_args& a, const AttnPlan& p, int* launches, cudaStream_t s);
+struct SharedPlan {
+  int64_t groups;       // 0: every request by itself
+  AttnPlan front, own;  // splits and tiles of the shared tokens, and of each request's own
+  size_t part_bytes;
+};
+SharedPlan plan_shared(const topkp_tree_attention_args& a, int64_t groups, int64_t max_shared, int num_sms);
+cudaError_t launch_shared(const topkp_tree_attention_args& a, const int32_t* shared, const SharedPlan& p, int* launches, cudaStream_t s);
 
 }  // namespace topkp

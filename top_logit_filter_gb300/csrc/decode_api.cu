@@ -353,6 +353,76 @@ topkp_status cache_shapes(const char* fn, int64_t N, int64_t H, int64_t D, int64
 
 }  // namespace
 
+namespace {
+
+// What both attention calls check of their arguments but for the workspace.
+topkp_status check_attention(const char* fn, const topkp_tree_attention_args& a) {
+  if (a.dtype != TOPKP_F16 && a.dtype != TOPKP_BF16)
+    return fail(TOPKP_ERR_PARAM_INVALID, "%s: dtype %d (fp16 or bf16 is wanted)", fn, (int)a.dtype);
+  if (a.B < 0 || a.T < 0 || a.Hkv < 1 || a.Hq < 1 || a.Hq % a.Hkv)
+    return fail(TOPKP_ERR_PARAM_INVALID, "%s: B=%lld T=%lld Hq=%lld Hkv=%lld (Hq a multiple of Hkv)", fn, (long long)a.B,
+                (long long)a.T, (long long)a.Hq, (long long)a.Hkv);
+  if (a.D < 8 || a.D > TOPKP_MAX_HEAD_DIM || a.D % 8)
+    return fail(TOPKP_ERR_PARAM_INVALID, "%s: head dimension %lld (a multiple of 8 up to %d)", fn, (long long)a.D, TOPKP_MAX_HEAD_DIM);
+  if (a.tree && a.T > TOPKP_MAX_TREE)
+    return fail(TOPKP_ERR_PARAM_INVALID, "%s: a tree of %lld nodes (up to %d)", fn, (long long)a.T, TOPKP_MAX_TREE);
+  if (a.B == 0 || a.T == 0) return TOPKP_SUCCESS;
+  if (a.pages < 1 || a.page_size < 1 || a.max_pages < 1 || a.pages > INT_MAX || a.page_size > INT_MAX ||
+      a.max_pages > kMostTokens / a.page_size || (a.table && a.ld_table < a.max_pages) ||
+      (!a.table && (a.max_pages != 1 || a.pages != a.B)))
+    return fail(TOPKP_ERR_PARAM_INVALID, "%s: pages=%lld page_size=%lld max_pages=%lld ld_table=%lld", fn, (long long)a.pages,
+                (long long)a.page_size, (long long)a.max_pages, (long long)a.ld_table);
+  if (!a.q || !a.out || !a.context) return fail(TOPKP_ERR_PARAM_NULLPTR, "%s: q, out or context is NULL", fn);
+  if (a.B * a.Hkv > 65535 || a.T * (a.Hq / a.Hkv) > 65535LL * 16 || a.Hq > INT_MAX || a.T > INT_MAX)
+    return fail(TOPKP_ERR_PARAM_INVALID, "%s: B * Hkv above 65535, or too many rows", fn);
+  topkp_status st = check_cache(fn, "k", &a.k, a.Hkv, a.D, a.pages, a.page_size, a.dtype);
+  if (!st) st = check_cache(fn, "v", &a.v, a.Hkv, a.D, a.pages, a.page_size, a.dtype);
+  if (st) return st;
+  if (a.k.dtype != a.v.dtype) return fail(TOPKP_ERR_PARAM_INVALID, "%s: the caches have two dtypes", fn);
+  for (const topkp_cache* c : {&a.k, &a.v})
+    if (c->exponents && ((a.pages > 1 && c->exp_page_stride > UINT32_MAX) || (a.page_size > 1 && c->exp_token_stride > UINT32_MAX)))
+      return fail(TOPKP_ERR_PARAM_INVALID, "%s: a stride of exponents has more than 32 bits", fn);
+  if (!cache_by_8(a.k) || !cache_by_8(a.v))
+    return fail(TOPKP_ERR_PARAM_INVALID, "%s: a cache's pointer or strides are not multiples of 8 elements", fn);
+  for (const int64_t s : {a.q_batch_stride, a.q_token_stride, a.q_head_stride, a.out_batch_stride, a.out_token_stride, a.out_head_stride})
+    if (s < 0 || s % 8) return fail(TOPKP_ERR_PARAM_INVALID, "%s: a stride of q or out is not a multiple of 8", fn);
+  if ((uintptr_t)a.q % 16 || (uintptr_t)a.out % 16 || (uintptr_t)a.lse % 4 || (uintptr_t)a.table % 4 ||
+      (uintptr_t)a.context % 4 || (uintptr_t)a.nodes % 4 || (uintptr_t)a.tree % 8)
+    return fail(TOPKP_ERR_PARAM_INVALID, "%s: a pointer is not aligned (q and out to 16 bytes, others to their element)", fn);
+  if ((a.B > 1 && a.out_batch_stride < a.D) || (a.T > 1 && a.out_token_stride < a.D) || (a.Hq > 1 && a.out_head_stride < a.D))
+    return fail(TOPKP_ERR_PARAM_INVALID, "%s: a stride of out is below D", fn);
+  return TOPKP_SUCCESS;
+}
+// The workspace's size, and that no output lies over another or an input.
+topkp_status check_places(const char* fn, const topkp_tree_attention_args& a, size_t need, const Range& shared) {
+  if (need && (!a.workspace || (uintptr_t)a.workspace % 256 || a.workspace_bytes < need))
+    return fail(TOPKP_ERR_PARAM_INVALID, "%s: the workspace needs %zu bytes, 256-byte aligned", fn, need);
+  const Range ins[10] = {
+      {a.q, (size_t)((a.B - 1) * a.q_batch_stride + (a.T - 1) * a.q_token_stride + (a.Hq - 1) * a.q_head_stride + a.D) * 2},
+      cache_span(a.k, a.Hkv, a.D, a.pages, a.page_size),
+      cache_span(a.v, a.Hkv, a.D, a.pages, a.page_size),
+      exp_span(a.k, a.Hkv, a.pages, a.page_size),
+      exp_span(a.v, a.Hkv, a.pages, a.page_size),
+      {a.context, (size_t)a.B * 4},
+      {a.table, (size_t)((a.B - 1) * a.ld_table + a.max_pages) * 4},
+      {a.tree, (size_t)(a.B * a.T) * 8},
+      {a.nodes, (size_t)a.B * 4},
+      shared};
+  const Range outs[3] = {
+      {a.out, (size_t)((a.B - 1) * a.out_batch_stride + (a.T - 1) * a.out_token_stride + (a.Hq - 1) * a.out_head_stride + a.D) * 2},
+      {a.lse, (size_t)(a.B * a.T * a.Hq) * 4},
+      {a.workspace, need}};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 10; ++j)
+      if (overlap(outs[i], ins[j])) return fail(TOPKP_ERR_PARAM_INVALID, "%s: an output or the workspace overlaps an input", fn);
+    for (int j = i + 1; j < 3; ++j)
+      if (overlap(outs[i], outs[j])) return fail(TOPKP_ERR_PARAM_INVALID, "%s: two outputs (or the workspace) overlap", fn);
+  }
+  return TOPKP_SUCCESS;
+}
+
+}  // namespace
+
 extern "C" {
 
 topkp_status topkp_cache_write(const void* k, const void* v, int64_t N, int64_t H, int64_t D, int64_t k_token_stride,
@@ -471,68 +541,302 @@ topkp_status topkp_tree_attention(const topkp_tree_attention_args* args, void* s
   report_launches(0);
   if (!args) return fail(TOPKP_ERR_PARAM_NULLPTR, "%s: args is NULL", fn);
   const topkp_tree_attention_args& a = *args;
-  if (a.dtype != TOPKP_F16 && a.dtype != TOPKP_BF16)
-    return fail(TOPKP_ERR_PARAM_INVALID, "%s: dtype %d (fp16 or bf16 is wanted)", fn, (int)a.dtype);
-  if (a.B < 0 || a.T < 0 || a.Hkv < 1 || a.Hq < 1 || a.Hq % a.Hkv)
-    return fail(TOPKP_ERR_PARAM_INVALID, "%s: B=%lld T=%lld Hq=%lld Hkv=%lld (Hq a multiple of Hkv)", fn, (long long)a.B,
-                (long long)a.T, (long long)a.Hq, (long long)a.Hkv);
-  if (a.D < 8 || a.D > TOPKP_MAX_HEAD_DIM || a.D % 8)
-    return fail(TOPKP_ERR_PARAM_INVALID, "%s: head dimension %lld (a multiple of 8 up to %d)", fn, (long long)a.D, TOPKP_MAX_HEAD_DIM);
-  if (a.tree && a.T > TOPKP_MAX_TREE)
-    return fail(TOPKP_ERR_PARAM_INVALID, "%s: a tree of %lld nodes (up to %d)", fn, (long long)a.T, TOPKP_MAX_TREE);
-  if (a.B == 0 || a.T == 0) return TOPKP_SUCCESS;
-  if (a.pages < 1 || a.page_size < 1 || a.max_pages < 1 || a.pages > INT_MAX || a.page_size > INT_MAX ||
-      a.max_pages > kMostTokens / a.page_size || (a.table && a.ld_table < a.max_pages) ||
-      (!a.table && (a.max_pages != 1 || a.pages != a.B)))
-    return fail(TOPKP_ERR_PARAM_INVALID, "%s: pages=%lld page_size=%lld max_pages=%lld ld_table=%lld", fn, (long long)a.pages,
-                (long long)a.page_size, (long long)a.max_pages, (long long)a.ld_table);
-  if (!a.q || !a.out || !a.context) return fail(TOPKP_ERR_PARAM_NULLPTR, "%s: q, out or context is NULL", fn);
-  if (a.B * a.Hkv > 65535 || a.T * (a.Hq / a.Hkv) > 65535LL * 16 || a.Hq > INT_MAX || a.T > INT_MAX)
-    return fail(TOPKP_ERR_PARAM_INVALID, "%s: B * Hkv above 65535, or too many rows", fn);
-  topkp_status st = check_cache(fn, "k", &a.k, a.Hkv, a.D, a.pages, a.page_size, a.dtype);
-  if (!st) st = check_cache(fn, "v", &a.v, a.Hkv, a.D, a.pages, a.page_size, a.dtype);
-  if (st) return st;
-  if (a.k.dtype != a.v.dtype) return fail(TOPKP_ERR_PARAM_INVALID, "%s: the caches have two dtypes", fn);
-  for (const topkp_cache* c : {&a.k, &a.v})
-    if (c->exponents && ((a.pages > 1 && c->exp_page_stride > UINT32_MAX) || (a.page_size > 1 && c->exp_token_stride > UINT32_MAX)))
-      return fail(TOPKP_ERR_PARAM_INVALID, "%s: a stride of exponents has more than 32 bits", fn);
-  if (!cache_by_8(a.k) || !cache_by_8(a.v))
-    return fail(TOPKP_ERR_PARAM_INVALID, "%s: a cache's pointer or strides are not multiples of 8 elements", fn);
-  for (const int64_t s : {a.q_batch_stride, a.q_token_stride, a.q_head_stride, a.out_batch_stride, a.out_token_stride, a.out_head_stride})
-    if (s < 0 || s % 8) return fail(TOPKP_ERR_PARAM_INVALID, "%s: a stride of q or out is not a multiple of 8", fn);
-  if ((uintptr_t)a.q % 16 || (uintptr_t)a.out % 16 || (uintptr_t)a.lse % 4 || (uintptr_t)a.table % 4 ||
-      (uintptr_t)a.context % 4 || (uintptr_t)a.nodes % 4 || (uintptr_t)a.tree % 8)
-    return fail(TOPKP_ERR_PARAM_INVALID, "%s: a pointer is not aligned (q and out to 16 bytes, others to their element)", fn);
-  if ((a.B > 1 && a.out_batch_stride < a.D) || (a.T > 1 && a.out_token_stride < a.D) || (a.Hq > 1 && a.out_head_stride < a.D))
-    return fail(TOPKP_ERR_PARAM_INVALID, "%s: a stride of out is below D", fn);
+  topkp_status st = check_attention(fn, a);
+  if (st || a.B == 0 || a.T == 0) return st;
   const AttnPlan p = plan_attention(a, kPlanSms);
-  if (p.part_bytes && (!a.workspace || (uintptr_t)a.workspace % 256 || a.workspace_bytes < p.part_bytes))
-    return fail(TOPKP_ERR_PARAM_INVALID, "%s: the workspace needs %zu bytes, 256-byte aligned", fn, p.part_bytes);
-  const Range ins[9] = {
-      {a.q, (size_t)((a.B - 1) * a.q_batch_stride + (a.T - 1) * a.q_token_stride + (a.Hq - 1) * a.q_head_stride + a.D) * 2},
-      cache_span(a.k, a.Hkv, a.D, a.pages, a.page_size),
-      cache_span(a.v, a.Hkv, a.D, a.pages, a.page_size),
-      exp_span(a.k, a.Hkv, a.pages, a.page_size),
-      exp_span(a.v, a.Hkv, a.pages, a.page_size),
-      {a.context, (size_t)a.B * 4},
-      {a.table, (size_t)((a.B - 1) * a.ld_table + a.max_pages) * 4},
-      {a.tree, (size_t)(a.B * a.T) * 8},
-      {a.nodes, (size_t)a.B * 4}};
-  const Range outs[3] = {
-      {a.out, (size_t)((a.B - 1) * a.out_batch_stride + (a.T - 1) * a.out_token_stride + (a.Hq - 1) * a.out_head_stride + a.D) * 2},
-      {a.lse, (size_t)(a.B * a.T * a.Hq) * 4},
-      {a.workspace, p.part_bytes}};
-  for (int i = 0; i < 3; ++i) {
-    for (int j = 0; j < 9; ++j)
-      if (overlap(outs[i], ins[j])) return fail(TOPKP_ERR_PARAM_INVALID, "%s: an output or the workspace overlaps an input", fn);
-    for (int j = i + 1; j < 3; ++j)
-      if (overlap(outs[i], outs[j])) return fail(TOPKP_ERR_PARAM_INVALID, "%s: two outputs (or the workspace) overlap", fn);
-  }
+  st = check_places(fn, a, p.part_bytes, {nullptr, 0});
+  if (st) return st;
   int dev = 0;
   if (device_sms(&dev) <= 0) return fail(TOPKP_ERR_LAUNCH, "%s: no usable CUDA device", fn);
   int launches = 0;
   const cudaError_t e = launch_attention(a, p, &launches, (cudaStream_t)stream);
   return launched(fn, e, launches);
+}
+
+size_t topkp_shared_attention_workspace_size(const topkp_tree_attention_args* args, int64_t groups, int64_t max_shared) {
+  if (!args || args->B <= 0 || args->T <= 0 || args->Hkv <= 0 || args->Hq < args->Hkv || args->D <= 0 ||
+      args->max_pages <= 0 || args->page_size <= 0 || groups < 1 || args->B % groups)
+    return 0;
+  return plan_shared(*args, groups, max_shared, kPlanSms).part_bytes;
+}
+
+topkp_status topkp_shared_attention(const topkp_tree_attention_args* args, const int32_t* shared, int64_t groups,
+                                    int64_t max_shared, void* stream) {
+  const char* fn = "topkp_shared_attention";
+  report_launches(0);
+  if (!args) return fail(TOPKP_ERR_PARAM_NULLPTR, "%s: args is NULL", fn);
+  const topkp_tree_attention_args& a = *args;
+  topkp_status st = check_attention(fn, a);
+  if (st) return st;
+  if (groups < 1 || a.B % groups)
+    return fail(TOPKP_ERR_PARAM_INVALID, "%s: %lld groups of %lld requests", fn, (long long)groups, (long long)a.B);
+  if (a.B == 0 || a.T == 0) return TOPKP_SUCCESS;
+  if (!a.table || !shared) return fail(TOPKP_ERR_PARAM_NULLPTR, "%s: table or shared is NULL", fn);
+  if ((uintptr_t)shared % 4) return fail(TOPKP_ERR_PARAM_INVALID, "%s: a pointer is not aligned to its element size", fn);
+  // a group's rows are counted in 32 bits, its row tiles in a grid's first dimension
+  if (a.B / groups * a.T > INT_MAX / a.Hq)
+    return fail(TOPKP_ERR_PARAM_INVALID, "%s: too many rows in a group", fn);
+  const SharedPlan p = plan_shared(a, groups, max_shared, kPlanSms);
+  st = check_places(fn, a, p.part_bytes, {shared, (size_t)groups * 4});
+  if (st) return st;
+  int dev = 0;
+  if (device_sms(&dev) <= 0) return fail(TOPKP_ERR_LAUNCH, "%s: no usable CUDA device", fn);
+  int launches = 0;
+  const cudaError_t e = launch_shared(a, shared, p, &launches, (cudaStream_t)stream);
+  return launched(fn, e, launches);
+}
+
+}  // extern "C"
+
+namespace {
+
+// The states of a page call: sizes, strides, and that none shares a byte with
+// another or with one of the call's other arguments.
+topkp_status check_states(const char* fn, const topkp_pages* states, int64_t count, int64_t pages, int64_t page_size,
+                          const Range* others, int n_others) {
+  Region few[64];
+  Region* regions = few;
+  if (count > 64) regions = count <= (int64_t)(SIZE_MAX / 2 / sizeof(Region)) ? (Region*)malloc((size_t)count * sizeof(Region)) : nullptr;
+  if (!regions) return fail(TOPKP_ERR_PARAM_INVALID, "%s: no memory for %lld states", fn, (long long)count);
+  int64_t n = 0;
+  topkp_status st = TOPKP_SUCCESS;
+  for (int64_t i = 0; i < count && !st; ++i) {
+    const topkp_pages& s = states[i];
+    if (s.blocks < 0 || s.entry_bytes < 0 || s.page_stride < 0 || s.block_stride < 0) {
+      st = fail(TOPKP_ERR_PARAM_INVALID, "%s: state %lld has a negative size or stride", fn, (long long)i);
+    } else if (s.blocks && s.entry_bytes) {
+      if (!s.data) {
+        st = fail(TOPKP_ERR_PARAM_NULLPTR, "%s: state %lld has a NULL pointer", fn, (long long)i);
+        break;
+      }
+      if (s.entry_bytes > (INT64_MAX >> 32) || s.blocks > (INT64_MAX >> 40) || (s.blocks > 1 && s.block_stride < page_size * s.entry_bytes)) {
+        st = fail(TOPKP_ERR_PARAM_INVALID, "%s: state %lld has entries too large, or blocks that overlap", fn, (long long)i);
+        break;
+      }
+      const int64_t len = page_size * s.entry_bytes, extent = (s.blocks - 1) * s.block_stride + len;
+      if (pages > 1 && s.page_stride < extent) {
+        st = fail(TOPKP_ERR_PARAM_INVALID, "%s: state %lld has pages that overlap", fn, (long long)i);
+        break;
+      }
+      regions[n++] = {(uintptr_t)s.data, s.page_stride > extent ? s.page_stride : extent, s.block_stride, s.blocks, len, extent, i, true};
+      const Range whole = {s.data, (size_t)((pages - 1) * s.page_stride + extent)};
+      for (int k = 0; k < n_others && !st; ++k)
+        if (overlap(whole, others[k])) st = fail(TOPKP_ERR_PARAM_INVALID, "%s: state %lld overlaps another argument", fn, (long long)i);
+    }
+  }
+  const Region *one, *other;
+  if (!st && clash(regions, n, pages, &one, &other))
+    st = fail(TOPKP_ERR_PARAM_INVALID, "%s: states %lld and %lld share a byte", fn, (long long)std::min(one->state, other->state),
+              (long long)std::max(one->state, other->state));
+  if (regions != few) free(regions);
+  return st;
+}
+PageState page_state(const topkp_pages& s) {
+  PageState p = {(char*)s.data, s.page_stride, s.block_stride, s.blocks, s.entry_bytes, 1};
+  uint64_t all = (uint64_t)(uintptr_t)s.data | (uint64_t)s.page_stride | (uint64_t)s.entry_bytes;
+  if (s.blocks > 1) all |= (uint64_t)s.block_stride;
+  p.unit = all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : 1;
+  return p;
+}
+size_t table_span(int64_t rows, int64_t ld, int64_t columns) { return rows > 0 ? (size_t)((rows - 1) * ld + columns) * 4 : 0; }
+
+}  // namespace
+
+extern "C" {
+
+size_t topkp_cache_fork_workspace_size(int64_t N, int64_t pages) {
+  if (N < 0 || N > TOPKP_MAX_ROWS || pages < 1 || pages > INT_MAX) return 0;
+  return fork_workspace(N, pages);
+}
+
+topkp_status topkp_cache_fork(const topkp_cache_fork_args* args, void* stream) {
+  const char* fn = "topkp_cache_fork";
+  report_launches(0);
+  if (!args) return fail(TOPKP_ERR_PARAM_NULLPTR, "%s: args is NULL", fn);
+  const topkp_cache_fork_args& a = *args;
+  if (a.count < 0 || a.R < 0 || a.N < 0 || a.R > TOPKP_MAX_ROWS || a.N > TOPKP_MAX_ROWS)
+    return fail(TOPKP_ERR_PARAM_INVALID, "%s: count=%lld R=%lld N=%lld (rows up to %d)", fn, (long long)a.count, (long long)a.R,
+                (long long)a.N, TOPKP_MAX_ROWS);
+  if (a.pages < 1 || a.pages > INT_MAX || a.page_size < 1 || a.page_size > INT_MAX || a.max_pages < 1 ||
+      a.max_pages > (1 << 30) || a.max_pages * std::max(a.R, a.N) > (1 << 30) || a.max_pages > INT_MAX / a.page_size ||
+      a.ld_table < a.max_pages || a.ld_out < a.max_pages)
+    return fail(TOPKP_ERR_PARAM_INVALID, "%s: pages=%lld page_size=%lld max_pages=%lld ld_table=%lld ld_out=%lld", fn, (long long)a.pages,
+                (long long)a.page_size, (long long)a.max_pages, (long long)a.ld_table, (long long)a.ld_out);
+  if (a.grow_all < 0 || a.grow_all > INT_MAX) return fail(TOPKP_ERR_PARAM_INVALID, "%s: grow_all=%lld", fn, (long long)a.grow_all);
+  if ((a.count && !a.states) || (a.R && (!a.table || !a.lengths)) || (a.N && (!a.source || !a.table_out)) || !a.refs || !a.refs_out || !a.missing)
+    return fail(TOPKP_ERR_PARAM_NULLPTR, "%s: states, table, lengths, source, refs or an output is NULL", fn);
+  for (const void* p : {(const void*)a.table, (const void*)a.lengths, (const void*)a.source, (const void*)a.grow, (const void*)a.refs,
+                        (const void*)a.table_out, (const void*)a.refs_out, (const void*)a.missing})
+    if ((uintptr_t)p % 4) return fail(TOPKP_ERR_PARAM_INVALID, "%s: a pointer is not aligned to its element size", fn);
+  const size_t need = fork_workspace(a.N, a.pages);
+  if (!a.workspace || (uintptr_t)a.workspace % 256 || a.workspace_bytes < need)
+    return fail(TOPKP_ERR_PARAM_INVALID, "%s: the workspace needs %zu bytes, 256-byte aligned", fn, need);
+  const size_t pool = (size_t)a.pages * 4;
+  const Range all[9] = {{a.table, table_span(a.R, a.ld_table, a.max_pages)}, {a.lengths, (size_t)a.R * 4}, {a.source, (size_t)a.N * 4},
+                        {a.grow, (size_t)a.N * 4}, {a.refs, pool}, {a.table_out, table_span(a.N, a.ld_out, a.max_pages)},
+                        {a.refs_out, pool}, {a.missing, 4}, {a.workspace, need}};
+  for (int i = 5; i < 9; ++i)
+    for (int j = 0; j < i; ++j)
+      if (!(i == 6 && j == 4 && a.refs == a.refs_out) && overlap(all[i], all[j]))
+        return fail(TOPKP_ERR_PARAM_INVALID, "%s: an output or the workspace overlaps an input or another output", fn);
+  const topkp_status st = check_states(fn, a.states, a.count, a.pages, a.page_size, all, 9);
+  if (st) return st;
+  int dev = 0;
+  if (device_sms(&dev) <= 0) return fail(TOPKP_ERR_LAUNCH, "%s: no usable CUDA device", fn);
+  ForkArgs f = {};
+  f.table = a.table;
+  f.lengths = a.lengths;
+  f.source = a.source;
+  f.grow = a.grow;
+  f.refs = a.refs;
+  f.table_out = a.table_out;
+  f.refs_out = a.refs_out;
+  f.missing = a.missing;
+  const size_t each = (pool + 255) / 256 * 256;
+  f.hold = (int32_t*)a.workspace;
+  f.claim = (int32_t*)((char*)a.workspace + each);
+  f.fresh = (int32_t*)((char*)a.workspace + 2 * each);
+  f.copies = (int4*)((char*)a.workspace + 3 * each);
+  f.ld = a.ld_table;
+  f.ld_out = a.ld_out;
+  f.pages = a.pages;
+  f.R = (int32_t)a.R;
+  f.N = (int32_t)a.N;
+  f.M = (int32_t)a.max_pages;
+  f.page_size = (int32_t)a.page_size;
+  f.grow_all = (int32_t)a.grow_all;
+  cudaError_t e = launch_fork(f, (cudaStream_t)stream);
+  if (e != cudaSuccess || a.N == 0) return launched(fn, e, 1);
+  int launches = 1;
+  CopyArgs c;
+  c.copies = f.copies;
+  c.N = f.N;
+  c.page_size = f.page_size;
+  c.count = 0;
+  for (int64_t i = 0; i <= a.count; ++i) {
+    if (i < a.count && a.states[i].blocks && a.states[i].entry_bytes) c.st[c.count++] = page_state(a.states[i]);
+    if (c.count == kPageStates || (i == a.count && c.count)) {
+      e = launch_page_copy(c, (cudaStream_t)stream);
+      if (e != cudaSuccess) return launched(fn, e, 0);
+      ++launches;
+      c.count = 0;
+    }
+  }
+  return launched(fn, cudaSuccess, launches);
+}
+
+topkp_status topkp_cache_compact(const topkp_pages* states, int64_t count, int64_t B, int64_t W, const int32_t* table,
+                                 int64_t ld_table, int64_t max_pages, int64_t pages, int64_t page_size,
+                                 const int32_t* start, const int32_t* keep, const int32_t* kept, void* stream) {
+  const char* fn = "topkp_cache_compact";
+  report_launches(0);
+  if (count < 0 || B < 0 || B > 65535 || W < 0 || W > TOPKP_MAX_TREE)
+    return fail(TOPKP_ERR_PARAM_INVALID, "%s: count=%lld B=%lld (up to 65535) W=%lld (up to %d)", fn, (long long)count, (long long)B,
+                (long long)W, TOPKP_MAX_TREE);
+  if (count == 0 || B == 0 || W == 0) return TOPKP_SUCCESS;
+  if (pages < 1 || pages > INT_MAX || page_size < 1 || page_size > INT_MAX || max_pages < 1 || max_pages > INT_MAX ||
+      (table && ld_table < max_pages) || (!table && (max_pages != 1 || pages != B)))
+    return fail(TOPKP_ERR_PARAM_INVALID, "%s: pages=%lld page_size=%lld max_pages=%lld ld_table=%lld", fn, (long long)pages,
+                (long long)page_size, (long long)max_pages, (long long)ld_table);
+  if (!states || !start || !keep || !kept) return fail(TOPKP_ERR_PARAM_NULLPTR, "%s: states, start, keep or kept is NULL", fn);
+  for (const void* p : {(const void*)table, (const void*)start, (const void*)keep, (const void*)kept})
+    if ((uintptr_t)p % 4) return fail(TOPKP_ERR_PARAM_INVALID, "%s: a pointer is not aligned to its element size", fn);
+  const Range index[4] = {{table, table ? table_span(B, ld_table, max_pages) : 0}, {start, (size_t)B * 4}, {keep, (size_t)(B * W) * 4}, {kept, (size_t)B * 4}};
+  const topkp_status st = check_states(fn, states, count, pages, page_size, index, 4);
+  if (st) return st;
+  int dev = 0;
+  if (device_sms(&dev) <= 0) return fail(TOPKP_ERR_LAUNCH, "%s: no usable CUDA device", fn);
+  CompactArgs c;
+  c.table = table;
+  c.start = start;
+  c.keep = keep;
+  c.kept = kept;
+  c.ld = ld_table;
+  c.pages = pages;
+  c.B = (int32_t)B;
+  c.W = (int32_t)W;
+  c.M = (int32_t)max_pages;
+  c.page_size = (int32_t)page_size;
+  c.count = 0;
+  int launches = 0;
+  for (int64_t i = 0; i <= count; ++i) {
+    if (i < count && states[i].blocks && states[i].entry_bytes) c.st[c.count++] = page_state(states[i]);
+    if (c.count == kPageStates || (i == count && c.count)) {
+      const cudaError_t e = launch_compact(c, (cudaStream_t)stream);
+      if (e != cudaSuccess) return launched(fn, e, 0);
+      ++launches;
+      c.count = 0;
+    }
+  }
+  return launched(fn, cudaSuccess, launches);
+}
+
+topkp_status topkp_draft_verify(const topkp_draft_verify_args* args, void* stream) {
+  const char* fn = "topkp_draft_verify";
+  report_launches(0);
+  if (!args) return fail(TOPKP_ERR_PARAM_NULLPTR, "%s: args is NULL", fn);
+  const topkp_draft_verify_args& a = *args;
+  if (!row_type(a.dtype)) return fail(TOPKP_ERR_PARAM_INVALID, "%s: unknown dtype %d", fn, (int)a.dtype);
+  if (a.B < 0 || a.B > INT_MAX / 16 || a.V < 1 || a.V > TOPKP_MAX_V)
+    return fail(TOPKP_ERR_PARAM_INVALID, "%s: B=%lld V=%lld (V is 1 to %lld)", fn, (long long)a.B, (long long)a.V, (long long)TOPKP_MAX_V);
+  if (a.T < 1 || a.T > TOPKP_MAX_TREE) return fail(TOPKP_ERR_PARAM_INVALID, "%s: %lld nodes (1 to %d)", fn, (long long)a.T, TOPKP_MAX_TREE);
+  if (!a.uniform != !a.race || (!a.race && a.draft))
+    return fail(TOPKP_ERR_PARAM_INVALID, "%s: uniform and race go together, and draft goes with them", fn);
+  if (!(a.eps >= 0.0f)) return fail(TOPKP_ERR_PARAM_INVALID, "%s: eps is negative or NaN", fn);
+  if (a.B == 0) return TOPKP_SUCCESS;
+  if (!a.target || !a.tokens || !a.count || !a.path || !a.token)
+    return fail(TOPKP_ERR_PARAM_NULLPTR, "%s: target, tokens or an output is NULL", fn);
+  if (a.target_batch_stride < 0 || (a.T > 1 && a.target_node_stride < a.V) ||
+      (a.draft && (a.draft_batch_stride < 0 || (a.T > 1 && a.draft_node_stride < a.V))) || (a.race && a.B > 1 && a.ld_race < a.V))
+    return fail(TOPKP_ERR_PARAM_INVALID, "%s: a row stride below V=%lld, or a negative one", fn, (long long)a.V);
+  const int es = esize(a.dtype);
+  if ((uintptr_t)a.target % es || (uintptr_t)a.draft % es)
+    return fail(TOPKP_ERR_PARAM_INVALID, "%s: a pointer is not aligned to its element size", fn);
+  for (const void* p : {(const void*)a.tokens, (const void*)a.parent, (const void*)a.nodes, (const void*)a.uniform, (const void*)a.race,
+                        (const void*)a.count, (const void*)a.path, (const void*)a.token, (const void*)a.logprob})
+    if ((uintptr_t)p % 4) return fail(TOPKP_ERR_PARAM_INVALID, "%s: a pointer is not aligned to its element size", fn);
+  const size_t nodes = (size_t)(a.B * a.T) * 4, rows = (size_t)a.B * 4;
+  const Range ins[7] = {{a.target, (size_t)((a.B - 1) * a.target_batch_stride + (a.T - 1) * a.target_node_stride + a.V) * es},
+                        {a.draft, (size_t)((a.B - 1) * a.draft_batch_stride + (a.T - 1) * a.draft_node_stride + a.V) * es},
+                        {a.tokens, nodes}, {a.parent, nodes}, {a.nodes, rows}, {a.uniform, nodes},
+                        {a.race, (size_t)((a.B - 1) * a.ld_race + a.V) * 4}};
+  const Range outs[4] = {{a.count, rows}, {a.path, nodes}, {a.token, rows}, {a.logprob, nodes}};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 7; ++j)
+      if (overlap(outs[i], ins[j])) return fail(TOPKP_ERR_PARAM_INVALID, "%s: an output overlaps an input", fn);
+    for (int j = i + 1; j < 4; ++j)
+      if (overlap(outs[i], outs[j])) return fail(TOPKP_ERR_PARAM_INVALID, "%s: two outputs overlap", fn);
+  }
+  int dev = 0;
+  if (device_sms(&dev) <= 0) return fail(TOPKP_ERR_LAUNCH, "%s: no usable CUDA device", fn);
+  VerifyArgs v = {};
+  v.target = a.target;
+  v.draft = a.draft;
+  v.t_batch = a.target_batch_stride;
+  v.t_node = a.target_node_stride;
+  v.d_batch = a.draft_batch_stride;
+  v.d_node = a.draft_node_stride;
+  v.tokens = a.tokens;
+  v.parent = a.parent;
+  v.nodes = a.nodes;
+  v.uniform = a.uniform;
+  v.race = a.race;
+  v.ld_race = a.ld_race;
+  v.eps = a.eps;
+  v.B = a.B;
+  v.T = (int32_t)a.T;
+  v.V = (int32_t)a.V;
+  v.cs = verify_cluster(a.B, a.V, es, kPlanSms);
+  // every row that is read begins on 16 bytes and ends on whole ones
+  uint64_t all = (uint64_t)(uintptr_t)a.target | (uint64_t)(uintptr_t)a.draft | (uint64_t)(uintptr_t)a.race | (uint64_t)a.V * es;
+  if (a.B > 1) all |= (uint64_t)a.target_batch_stride * es | (uint64_t)a.ld_race * 4 | (a.draft ? (uint64_t)a.draft_batch_stride * es : 0);
+  if (a.T > 1) all |= (uint64_t)a.target_node_stride * es | (a.draft ? (uint64_t)a.draft_node_stride * es : 0);
+  v.whole = all % 16 == 0;
+  v.count = a.count;
+  v.path = a.path;
+  v.token = a.token;
+  v.logprob = a.logprob;
+  return launched(fn, launch_verify(a.dtype, v, (cudaStream_t)stream), 1);
 }
 
 }  // extern "C"

@@ -9,6 +9,13 @@ manner: CUDA tensors in, the calling thread's current stream, no CPU path.
     k, v = cache_read(slots, k_cache, v_cache, k_exp=None, v_exp=None, dtype=None)
     out = tree_attention(q, k_cache, v_cache, context, pages=None, tree=None, ...)
 
+and, for several continuations of one prompt and for drafted tokens:
+
+    out = shared_attention(q, k_cache, v_cache, context, pages, shared, tree=None, ...)
+    count, path, token = draft_verify(target, tokens, uniform=None, race=None, draft=None, parent=None, ...)
+    states = cache_compact(states, start, keep, kept, pages=None)
+    pages, refs, missing = cache_fork(states, pages, lengths, source, refs, grow=0)
+
 A cache is [pages, page_size, heads, dim] with a block table, or
 [requests, capacity, heads, dim] without one; its elements are of the rows'
 type, or ``torch.float8_e4m3fn`` with a uint8 exponent for each (page, token,
@@ -29,8 +36,13 @@ _E4M3 = None    # torch.float8_e4m3fn
 _CACHE = struct.Struct("=QQi4x6q")
 _STATE = struct.Struct("=QQ7q")
 _ATTENTION = struct.Struct("=QQQ" + 2 * "QQi4x6q" + "QQQQQQ16qif")
+_VERIFY = struct.Struct("=11Q8qif")
+_PAGES = struct.Struct("=Q4q")
+_FORK = struct.Struct("=11Q9q")
 assert _CACHE.size == _lib.ctypes.sizeof(_lib.Cache) and _STATE.size == _lib.ctypes.sizeof(_lib.State)
 assert _ATTENTION.size == _lib.ctypes.sizeof(_lib.TreeAttentionArgs)
+assert _VERIFY.size == _lib.ctypes.sizeof(_lib.DraftVerifyArgs)
+assert _PAGES.size == _lib.ctypes.sizeof(_lib.Pages) and _FORK.size == _lib.ctypes.sizeof(_lib.CacheForkArgs)
 
 
 def _ready():
@@ -302,17 +314,30 @@ def cache_read(slots, k_cache, v_cache, k_exp=None, v_exp=None, dtype=None):
     return k, v
 
 
-def tree_attention_workspace_size(q, k_cache, pages=None, max_context=None) -> int:
-    """Bytes of workspace ``tree_attention`` needs for tensors of these shapes
-    and dtypes (their values are not read)."""
-    lib = _ready()
+def _attention_shape(q, k_cache, pages, max_context):
+    """An argument block that holds shapes and dtypes only."""
     pool, page_size, Hkv, D = k_cache.shape
     B, T, Hq = q.shape[:3]
     max_pages = 1 if pages is None else pages.shape[1]
     cache = (0, 0, _lib.TOPKP_E4M3 if k_cache.dtype == _E4M3 else _CODES[k_cache.dtype], 0, 0, 0, 0, 0, 0)
     shape = (B, T, Hq, Hkv, D, pool, page_size, max_pages, max_pages,
              max_pages * page_size if max_context is None else int(max_context), 0, 0, 0, 0, 0, 0, _dtype_code(q), 0.0)
-    return int(lib.topkp_tree_attention_workspace_size(_ATTENTION.pack(0, 0, 0, *cache, *cache, 0, 0, 0, 0, 0, 0, *shape)))
+    return _ATTENTION.pack(0, 0, 0, *cache, *cache, 0, 0, 0, 0, 0, 0, *shape)
+
+
+def tree_attention_workspace_size(q, k_cache, pages=None, max_context=None) -> int:
+    """Bytes of workspace ``tree_attention`` needs for tensors of these shapes
+    and dtypes (their values are not read)."""
+    lib = _ready()
+    return int(lib.topkp_tree_attention_workspace_size(_attention_shape(q, k_cache, pages, max_context)))
+
+
+def shared_attention_workspace_size(q, k_cache, pages, groups: int, max_context=None, max_shared=None) -> int:
+    """Bytes of workspace ``shared_attention`` needs for tensors of these
+    shapes and dtypes (their values are not read) and that many groups."""
+    lib = _ready()
+    most = pages.shape[1] * k_cache.shape[1] if max_shared is None else int(max_shared)
+    return int(lib.topkp_shared_attention_workspace_size(_attention_shape(q, k_cache, pages, max_context), int(groups), most))
 
 
 def tree_attention(q, k_cache, v_cache, context, pages=None, tree=None, nodes=None, k_exp=None, v_exp=None,
@@ -331,6 +356,39 @@ def tree_attention(q, k_cache, v_cache, context, pages=None, tree=None, nodes=No
     ``tree_attention_workspace_size`` bytes (allocated when None).  Returns
     out ([B, T, Hq, D]), or (out, lse) with lse [B, T, Hq] float32."""
     lib = _ready()
+    return _attention(q, k_cache, v_cache, context, pages, tree, nodes, k_exp, v_exp, scale, max_context, out, want_lse, workspace,
+                      lib.topkp_tree_attention_workspace_size, lib.topkp_tree_attention, ())
+
+
+def shared_attention(q, k_cache, v_cache, context, pages, shared, tree=None, nodes=None, k_exp=None, v_exp=None, scale=None,
+                     max_context=None, max_shared=None, out=None, want_lse: bool = False, workspace=None):
+    """``tree_attention`` of requests that share a prefix, whose keys and
+    values are read once for all of them (topkp_shared_attention).
+
+    shared: [groups] int32; the B requests are that many runs of as many
+    consecutive ones, and the first shared[g] tokens of group g's requests are
+    the same: the same pages (as ``cache_fork`` leaves them) or equal ones.
+    max_shared: a bound of ``shared`` known on the host, which plans the work
+    (the capacity when None).  ``workspace``: a uint8 tensor of at least
+    ``shared_attention_workspace_size`` bytes (allocated when None).
+    Everything else as for ``tree_attention``; the result differs from its by
+    the order of the sums only."""
+    lib = _ready()
+    _cuda(q, "q", 4)
+    _cuda(shared, "shared", 1, torch.int32, q.device)
+    _cuda(pages, "pages", 2, torch.int32, q.device)
+    shared = shared.contiguous()
+    groups = shared.shape[0]
+    if groups < 1 or q.shape[0] % groups:
+        raise ValueError(f"{q.shape[0]} requests do not make {groups} groups")
+    most = pages.shape[1] * k_cache.shape[1] if max_shared is None else int(max_shared)
+    return _attention(q, k_cache, v_cache, context, pages, tree, nodes, k_exp, v_exp, scale, max_context, out, want_lse, workspace,
+                      lambda args: lib.topkp_shared_attention_workspace_size(args, groups, most), lib.topkp_shared_attention,
+                      (_ptr(shared), groups, most))
+
+
+def _attention(q, k_cache, v_cache, context, pages, tree, nodes, k_exp, v_exp, scale, max_context, out, want_lse, workspace, size,
+               call, more):
     _cuda(q, "q", 4)
     if q.dtype not in (torch.float16, torch.bfloat16):
         raise TypeError(f"q must be float16 or bfloat16, not {q.dtype}")
@@ -373,9 +431,194 @@ def tree_attention(q, k_cache, v_cache, context, pages=None, tree=None, nodes=No
              float(D) ** -0.5 if scale is None else float(scale))
     front = (_ptr(q), _ptr(out), _ptr(lse), *kc, *vc, _ptr(pages), _ptr(context), _ptr(nodes), _ptr(tree))
     args = _ATTENTION.pack(*front, 0, 0, *shape)
-    need = lib.topkp_tree_attention_workspace_size(args)
+    need = size(args)
     if need:
         workspace = _workspace(workspace, need, dev)
         args = _ATTENTION.pack(*front, _ptr(workspace), workspace.numel(), *shape)
-    _launch(dev, lib.topkp_tree_attention, args)
+    _launch(dev, call, args, *more)
     return (out, lse) if want_lse else out
+
+
+def draft_verify(target, tokens, uniform=None, race=None, draft=None, parent=None, nodes=None, eps: float = 1e-10,
+                 want_logprob: bool = False):
+    """Which drafted tokens the target accepts, and the token to go on with (topkp_draft_verify).
+
+    target: [B, T, V] CUDA tensor (float32, float16 or bfloat16), the
+    target's logits after each node, filtered or not; tokens: [B, T] int32,
+    the nodes' tokens (node 0 is the last accepted one); parent: [B, T]
+    int32, each node's parent, an earlier node, or None for a chain; draft:
+    like target, the logits that the children of a node were drawn from, or
+    None where they were not drawn (the best ones, say).  uniform: [B, T]
+    float32 of [0, 1), and race: [B, V] float32 of Exp(1), the random numbers
+    of acceptance and of the draw; both None is greedy decoding.  nodes: [B]
+    int32, how many of the T nodes a request has.
+
+    Returns count [B] int32 (nodes of the accepted path, node 0 included),
+    path [B, T] int32 (those nodes, then -1) and token [B] int32, and with
+    ``want_logprob`` logprob [B, T] float32: log-probabilities of the
+    path's tokens behind node 0's, then of the drawn one."""
+    lib = _ready()
+    _cuda(target, "target", 3)
+    dt, dev = _dtype_code(target), target.device
+    B, T, V = target.shape
+    if V > 1 and target.stride(2) != 1:
+        target = target.contiguous()
+    ds = (0, 0)
+    if draft is not None:
+        _cuda(draft, "draft", 3, target.dtype, dev)
+        if draft.shape != target.shape:
+            raise ValueError(f"draft is {tuple(draft.shape)} and target {tuple(target.shape)}")
+        if V > 1 and draft.stride(2) != 1:
+            draft = draft.contiguous()
+        ds = draft.stride()
+    if (uniform is None) != (race is None):
+        raise ValueError("uniform and race go together")
+    if uniform is None and draft is not None:
+        raise ValueError("draft goes with uniform and race")
+    many = [tokens, parent, uniform]
+    for i, (name, dtype) in enumerate((("tokens", torch.int32), ("parent", torch.int32), ("uniform", torch.float32))):
+        t = many[i]
+        if t is None and i:
+            continue
+        _cuda(t, name, 2, dtype, dev)
+        if t.shape != (B, T):
+            raise ValueError(f"{name} must be {(B, T)}, not {tuple(t.shape)}")
+        many[i] = t.contiguous()
+    if race is not None:
+        _cuda(race, "race", 2, torch.float32, dev)
+        if race.shape != (B, V):
+            raise ValueError(f"race must be {(B, V)}, not {tuple(race.shape)}")
+        if V > 1 and race.stride(1) != 1 or B > 1 and race.stride(0) < V:
+            race = race.contiguous()
+    nodes = _vec(nodes, B, torch.int32, "nodes", dev)
+    out = torch.empty((B, T + 2), dtype=torch.int32, device=dev) if B == 1 else None
+    if out is not None:  # one allocation for a single request, whose call is all latency
+        count, token, path = out[0, :1], out[0, 1:2], out[:, 2:]
+    else:
+        count, token = torch.empty((2, B), dtype=torch.int32, device=dev)
+        path = torch.empty((B, T), dtype=torch.int32, device=dev)
+    logprob = torch.empty((B, T), dtype=torch.float32, device=dev) if want_logprob else None
+    ts = target.stride()
+    args = _VERIFY.pack(_ptr(target), _ptr(draft), *map(_ptr, (many[0], many[1], nodes, many[2], race, count, path, token, logprob)),
+                        B, T, V, ts[0], ts[1] if T > 1 else V, ds[0], ds[1] if T > 1 else V,
+                        V if race is None or B <= 1 else race.stride(0), dt, float(eps))
+    _launch(dev, lib.topkp_draft_verify, args)
+    return (count, path, token, logprob) if want_logprob else (count, path, token)
+
+
+def _page_states(states, time_dim, dev, pages=None, page_size=None):
+    """(tensors, packed descriptors, pages, page size) of a sequence of tensors of pages."""
+    many = [states] if torch.is_tensor(states) else list(states)
+    packed = []
+    for i, t in enumerate(many):
+        if not isinstance(t, torch.Tensor) or t.device != dev:
+            raise ValueError(f"states[{i}] must be a CUDA tensor on {dev}")
+        if t.dim() < 2 or not 1 <= time_dim < t.dim():
+            raise ValueError(f"states[{i}] must be [pages, page_size, ...] with its tokens along dimension {time_dim}")
+        shape = t.shape
+        if pages is None:
+            pages, page_size = shape[0], shape[time_dim]
+        if shape[0] != pages or shape[time_dim] != page_size:
+            raise ValueError(f"states[{i}] has {shape[0]} pages of {shape[time_dim]} tokens, others {pages} of {page_size}")
+        row, blk, blocks, _, size = _layout(t, time_dim, "a state")
+        packed.append(_PAGES.pack(_ptr(t), row, blk, blocks, size))
+    return many, b"".join(packed), pages, page_size
+
+
+def cache_fork(states, pages, lengths, source, refs, grow=0, time_dim: int = 1, out=None, refs_out=None, workspace=None):
+    """Block tables and pages follow the requests that go on (topkp_cache_fork).
+
+    states: one tensor or a sequence of them, each [pages, page_size, ...] and
+    dense within a page, of any dtype (keys, values and exponents of every
+    layer); pages: [R, max_pages] int32, the block table; lengths: [R] int32,
+    live tokens of its rows; source: [N] int32, the row that each new row goes
+    on from (-1: an empty one); refs: [pool] int32, holders of each page; grow:
+    tokens that every new row shall have room for besides, or [N] int32.
+
+    Whole pages are shared, a partly filled last one is copied for all but one
+    of its rows, what nobody goes on with is freed, and new pages are the free
+    ones of the lowest numbers.  Returns (pages [N, max_pages], refs, missing
+    [1] int32): with too few free pages nothing happens but that ``missing``
+    says how many lack and the new table is all -1.  The new row n holds
+    ``lengths[source[n]]`` tokens.  ``out``: where the new table goes;
+    ``refs_out``: where the new counts go (``refs`` itself to update it)."""
+    lib = _ready()
+    _cuda(pages, "pages", 2, torch.int32)
+    dev = pages.device
+    R, M = pages.shape
+    if M > 1 and pages.stride(1) != 1 or R > 1 and pages.stride(0) < M:
+        pages = pages.contiguous()
+    lengths = _vec(lengths, R, torch.int32, "lengths", dev)
+    _cuda(source, "source", 1, torch.int32, dev)
+    N = source.shape[0]
+    source = source.contiguous()
+    _cuda(refs, "refs", 1, torch.int32, dev)
+    pool = refs.shape[0]
+    if refs_out is not None:
+        _cuda(refs_out, "refs_out", 1, torch.int32, dev)
+        if refs_out.shape != refs.shape or not refs_out.is_contiguous():
+            raise ValueError("refs_out must be contiguous and shaped like refs")
+    refs = refs.contiguous()
+    if refs_out is None:
+        refs_out = torch.empty_like(refs)
+    many, packed, pool_, page_size = _page_states(states, time_dim, dev)
+    if not many:
+        raise ValueError("no states: the page size is theirs")
+    if pool_ != pool:
+        raise ValueError(f"refs counts {pool} pages and the states have {pool_}")
+    grow_all = 0
+    if isinstance(grow, torch.Tensor):
+        grow = _vec(grow, N, torch.int32, "grow", dev)
+    else:
+        grow, grow_all = None, int(grow)
+    if out is None:
+        out = torch.empty((N, M), dtype=torch.int32, device=dev)
+    elif out.shape != (N, M) or out.dtype != torch.int32 or out.device != dev or (M > 1 and out.stride(1) != 1) or (N > 1 and out.stride(0) < M):
+        raise ValueError(f"out must be a {(N, M)} int32 tensor on {dev} with contiguous rows")
+    missing = torch.empty((1,), dtype=torch.int32, device=dev)
+    workspace = _workspace(workspace, int(lib.topkp_cache_fork_workspace_size(N, pool)), dev)
+    args = _FORK.pack(_lib.ctypes.cast(_lib.ctypes.c_char_p(packed), _lib.ctypes.c_void_p).value or 0, _ptr(pages), _ptr(lengths),
+                      _ptr(source), _ptr(grow), _ptr(refs), _ptr(out), _ptr(refs_out), _ptr(missing), _ptr(workspace),
+                      workspace.numel(), len(many), R, N, M, pages.stride(0) if R > 1 else M, out.stride(0) if N > 1 else M, pool,
+                      page_size, grow_all)
+    _launch(dev, lib.topkp_cache_fork, args)
+    return out, refs_out, missing
+
+
+def cache_fork_workspace_size(N: int, pool: int) -> int:
+    """Bytes of workspace ``cache_fork`` needs for N new rows and a pool of that many pages."""
+    return int(_ready().topkp_cache_fork_workspace_size(N, pool))
+
+
+def cache_compact(states, start, keep, kept, pages=None, time_dim: int = 1):
+    """The kept tokens of each request move up, in place (topkp_cache_compact).
+
+    states: one tensor or a sequence of them, each [pages, page_size, ...] and
+    dense within a page, with ``pages`` [B, max_pages] int32 (the block
+    table), or [B, capacity, ...] without; start: [B] int32; keep: [B, W]
+    int32, W <= 64; kept: [B] int32.  The token at start[b] + keep[b, j] moves
+    to start[b] + j, j < kept[b], where keep[b, j] > j: after ``draft_verify``
+    start is the context, keep the path and kept its count.  Returns states."""
+    lib = _ready()
+    _cuda(keep, "keep", 2, torch.int32)
+    dev = keep.device
+    B, W = keep.shape
+    keep = keep.contiguous()
+    start, kept = _vec(start, B, torch.int32, "start", dev), _vec(kept, B, torch.int32, "kept", dev)
+    many, packed, pool, page_size = _page_states(states, time_dim, dev)
+    if not many:
+        return states
+    M, ld = 1, 1
+    if pages is not None:
+        _cuda(pages, "pages", 2, torch.int32, dev)
+        if pages.shape[0] != B:
+            raise ValueError(f"pages has {pages.shape[0]} rows and keep {B}")
+        M = pages.shape[1]
+        if M > 1 and pages.stride(1) != 1 or B > 1 and pages.stride(0) < M:
+            pages = pages.contiguous()
+        ld = pages.stride(0) if B > 1 else M
+    elif pool != B:
+        raise ValueError(f"without a block table a state holds one entry a request ({B}), not {pool}")
+    _launch(dev, lib.topkp_cache_compact, packed, len(many), B, W, _ptr(pages), ld, M, pool, page_size, _ptr(start), _ptr(keep),
+            _ptr(kept))
+    return states

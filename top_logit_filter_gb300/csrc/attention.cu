@@ -14,90 +14,15 @@
 // is a request with the nodes of all its requests, so its keys and values are
 // read once a group; each request's own tokens are another, beside it; the
 // join takes the parts of both.
-#include <cuda.h>
-#include <math.h>
-
 #include <algorithm>
 
-#include "common.cuh"
-#include "decode.h"
-#include "internal.h"
+#include "attention_launch.cuh"
 
 namespace topkp {
-namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
+cudaError_t launch_grouped(const AttnDev& p, cudaStream_t s);            // attention_shared.cu
+cudaError_t grouped_take_device_error(unsigned int* out);
 
-struct AttnDev {
-  topkp_tree_attention_args a;
-  int splits;
-  int per;        // tiles of a part; the last part takes what is left
-  float* part_o;  // [splits][B * T * Hq][D]
-  float* part_l;  // [splits][B * T * Hq]
-  uint32_t page_mul;  // reciprocal of page_size below 2^31, 0: divide
-  int page_shift;
-  int wide;           // an e4m3 row may be read 16 bytes at a time
-  int box;            // tokens of a TMA box, 0: plain copies
-  int parts;          // whether outputs are partial ones (to be joined)
-  // Requests that share a prefix.  stage 1: the shared tokens; a request of
-  // `a` is then a group, its nodes those of all its requests in turn.  Stage
-  // 2: each request's own tokens.  0: all tokens of each request.
-  int stage;
-  int size;                // requests of a group
-  int inner;               // stage 1: nodes of a request
-  int64_t q_member;        // stage 1: from request to request in q
-  const int32_t* shared;   // [groups]
-};
-
-// Tokens of request b that its nodes may see: the context, and the end of
-// the drafted nodes.
-__device__ __forceinline__ void request_span(const topkp_tree_attention_args& a, int64_t b, int* ctx, int* len,
-                                             int* nodes) {
-  const long long cap = a.max_pages * a.page_size;
-  const long long c = min((long long)max(a.context[b], 0), cap);
-  const int n = a.nodes ? min(max(a.nodes[b], 0), (int)a.T) : (int)a.T;
-  *ctx = (int)c;
-  *len = (int)min(c + n, cap);
-  *nodes = n;
-}
-
-constexpr int kTile = 64;  // tokens
-
-// Tokens that group g's requests read together: whole tiles within what they
-// share and within the context of each that has a node.  By a whole warp.
-__device__ __forceinline__ int shared_span(const AttnDev& p, int64_t g) {
-  const topkp_tree_attention_args& a = p.a;
-  int most = p.shared[g];
-  for (int i = threadIdx.x & 31; i < p.size; i += 32) {
-    const int64_t r = g * p.size + i;
-    if (!a.nodes || a.nodes[r] > 0) most = min(most, a.context[r]);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) most = min(most, __shfl_xor_sync(0xffffffffu, most, o));
-  return (int)min((long long)max(most, 0), (long long)(a.max_pages * a.page_size)) / kTile * kTile;
-}
-
-template <bool BF>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t r;
-  if (BF) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float exponent_scale(uint32_t e) { return __uint_as_float(e ? e << 23 : 0x400000u); }
-
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool in) {
-  const int n = in ? 16 : 0;
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-
-}  // namespace
-}  // namespace topkp
-
-#include "attention_tc.cuh"
-
-namespace topkp {
 namespace {
 
 // Joins the parts of a row: weights exp(lse_i - lse).  One warp per row; a
@@ -158,105 +83,15 @@ __global__ void __launch_bounds__(128) attn_join(const __grid_constant__ AttnDev
   if (lane == 0 && a.lse) a.lse[row] = total > 0.0f ? m + log2f(total) * kLn2 : total == 0.0f ? -INFINITY : total;
 }
 
-// The driver's encoder of tensor maps, looked up once (null where it is missing).
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiled encoder() {
-  static const EncodeTiled fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-        r != cudaDriverEntryPointSuccess) {
-      cudaGetLastError();
-      f = nullptr;
-    }
-    return reinterpret_cast<EncodeTiled>(f);
-  }();
-  return fn;
-}
-// A cache as (element, head, token, page); false where TMA cannot take it.
-bool make_map(CUtensorMap* map, const topkp_cache& c, const topkp_tree_attention_args& a, int box, int width,
-              CUtensorMapSwizzle swizzle) {
-  const bool q8 = c.dtype == TOPKP_E4M3;
-  const uint64_t es = q8 ? 1 : 2;
-  // a dimension of one entry may have any stride: give it one that is valid
-  auto stride = [&](int64_t s, int64_t count) { return count > 1 ? (uint64_t)s * es : ((uint64_t)a.D * es + 15) / 16 * 16; };
-  const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.Hkv, (cuuint64_t)a.page_size, (cuuint64_t)a.pages};
-  const cuuint64_t strides[3] = {stride(c.head_stride, a.Hkv), stride(c.token_stride, a.page_size), stride(c.page_stride, a.pages)};
-  for (const cuuint64_t s : strides)
-    if (s % 16 || s >= (1ull << 40)) return false;
-  if ((uintptr_t)c.data % 16) return false;
-  const cuuint32_t boxes[4] = {(cuuint32_t)width, 1, (cuuint32_t)box, 1}, steps[4] = {1, 1, 1, 1};
-  const EncodeTiled encode = encoder();
-  return encode && encode(map, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, c.data, dims, strides,
-                          boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-template <int DP, int NT, bool BF, bool Q8, int SH = 1>
-cudaError_t launch_tc(AttnDev p, cudaStream_t s) {
-  using Shape = TcShape<DP, NT, BF, Q8, SH>;
-  const topkp_tree_attention_args& a = p.a;
-  cudaError_t e = cudaFuncSetAttribute(attn_tc<DP, NT, BF, Q8, SH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kSmem);
-  if (e != cudaSuccess) return e;
-  // tokens of a box: they lie in one page, and eight rows make a swizzle's group
-  CUtensorMap km = {}, vm = {};
-  p.box = kTile;
-  if (a.table)
-    while (p.box > 4 && a.page_size % p.box) p.box /= 2;
-  // operands are swizzled (rows of 128 bytes, or of 64 e4m3); raw values are not
-  constexpr auto by128 = CU_TENSOR_MAP_SWIZZLE_128B, by64 = CU_TENSOR_MAP_SWIZZLE_64B, plain = CU_TENSOR_MAP_SWIZZLE_NONE;
-  if (p.box < 8 || !make_map(&km, a.k, a, p.box, !Q8 ? 64 : DP < 128 ? DP : 128, Q8 && DP == 64 ? by64 : by128) ||
-      !make_map(&vm, a.v, a, p.box, Q8 ? DP : 64, Q8 ? plain : by128))
-    p.box = 0;
-  const int64_t rows = a.T * (a.Hq / a.Hkv);
-  const dim3 grid((unsigned)((rows + NT * kTcRows - 1) / (NT * kTcRows)), (unsigned)p.splits, (unsigned)(a.B * a.Hkv));
-  if (p.stage != 2) {
-    attn_tc<DP, NT, BF, Q8, SH><<<grid, Shape::kThreads, Shape::kSmem, s>>>(p, km, vm);
-    return cudaGetLastError();
-  }
-  // the requests' own tokens run beside the shared ones
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(Shape::kThreads);
-  cfg.dynamicSmemBytes = Shape::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_tc<DP, NT, BF, Q8, SH>, p, km, vm);
-}
-
-// Tiles of 128 rows of a CTA (256 dims leave tensor memory for one).
-int row_tiles(const topkp_tree_attention_args& a) { return a.T * (a.Hq / a.Hkv) > kTcRows && a.D <= 128 ? 2 : 1; }
-
-// Whether four warps share each row's tokens: up to 32 rows over e4m3, at 65 to
-// 128 dims.  64 single tokens to 8000, in us with and without: 303 / 350 (fp16
-// 340 / 365); it gives nothing at 64 dims (217 / 218) or 256 (313 / 311).
-bool few_rows(const topkp_tree_attention_args& a) {
-  return a.k.dtype == TOPKP_E4M3 && a.D > 64 && a.D <= 128 && a.T * (a.Hq / a.Hkv) <= 32;
-}
-
-template <bool BF, bool Q8>
-cudaError_t launch_dim(const AttnDev& p, cudaStream_t s) {
-  if constexpr (Q8) {
-    if (few_rows(p.a)) return launch_tc<128, 1, BF, true, 4>(p, s);
-  }
-  const bool two = row_tiles(p.a) == 2;
-  if (p.a.D <= 64) return two ? launch_tc<64, 2, BF, Q8>(p, s) : launch_tc<64, 1, BF, Q8>(p, s);
-  if (p.a.D <= 128) return two ? launch_tc<128, 2, BF, Q8>(p, s) : launch_tc<128, 1, BF, Q8>(p, s);
-  return launch_tc<256, 1, BF, Q8>(p, s);
-}
-
 }  // namespace
 
 cudaError_t attention_take_device_error(unsigned int* out) {
   const unsigned int zero = 0;
+  unsigned int grouped = 0;
   cudaError_t e = cudaMemcpyFromSymbol(out, g_attention_error, sizeof(*out));
   if (e == cudaSuccess && *out) e = cudaMemcpyToSymbol(g_attention_error, &zero, sizeof(zero));
+  if (e == cudaSuccess) e = grouped_take_device_error(&grouped);
+  *out |= grouped;
   return e;
 }
 
@@ -396,11 +231,6 @@ void give_parts(AttnDev& p, int parts) {
   p.part_o = reinterpret_cast<float*>(p.a.workspace);
   p.part_l = p.part_o + (parts > 1 ? (size_t)parts * all * p.a.D : 0);
 }
-cudaError_t launch_parts(const AttnDev& p, cudaStream_t s) {
-  const bool bf = p.a.dtype == TOPKP_BF16, q8 = p.a.k.dtype == TOPKP_E4M3;
-  return bf ? (q8 ? launch_dim<true, true>(p, s) : launch_dim<true, false>(p, s))
-            : (q8 ? launch_dim<false, true>(p, s) : launch_dim<false, false>(p, s));
-}
 // The join's launch overlaps the parts; it waits for them itself.
 cudaError_t launch_join(const AttnDev& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
@@ -421,9 +251,8 @@ cudaError_t launch_attention(const topkp_tree_attention_args& a, const AttnPlan&
   AttnDev p = device_args(a);
   p.splits = plan.splits;
   p.per = plan.per;
-  p.parts = plan.splits > 1;
   give_parts(p, plan.splits);
-  const cudaError_t e = launch_parts(p, s);
+  const cudaError_t e = launch_parts<false>(p, s);
   *launches = 1;
   if (e != cudaSuccess || plan.splits <= 1) return e;
   *launches = 2;
@@ -436,7 +265,6 @@ cudaError_t launch_shared(const topkp_tree_attention_args& a, const int32_t* sha
   const size_t all = (size_t)(a.B * a.T * a.Hq);
   AttnDev own = device_args(a);
   give_parts(own, parts);
-  own.parts = 1;
   own.size = (int)(a.B / plan.groups);
   own.shared = shared;
   AttnDev front = own;
@@ -447,7 +275,7 @@ cudaError_t launch_shared(const topkp_tree_attention_args& a, const int32_t* sha
   front.splits = plan.front.splits;
   front.per = plan.front.per;
   *launches = 0;
-  cudaError_t e = launch_parts(front, s);
+  cudaError_t e = launch_grouped(front, s);
   if (e != cudaSuccess) return e;
   AttnDev join = own;
   join.splits = parts;
@@ -456,7 +284,7 @@ cudaError_t launch_shared(const topkp_tree_attention_args& a, const int32_t* sha
   own.per = plan.own.per;
   own.part_o += (size_t)front.splits * all * a.D;
   own.part_l += (size_t)front.splits * all;
-  e = launch_parts(own, s);
+  e = launch_grouped(own, s);
   *launches = 3;
   return e != cudaSuccess ? e : launch_join(join, s);
 }

@@ -343,7 +343,7 @@ __device__ __forceinline__ void e4m3_away(uint32_t two, float& x, float& y) {
   y -= __half2float(__ushort_as_half((uint16_t)(h >> 16)));
 }
 
-template <int DP, int NT, bool BF, bool Q8, int SH>
+template <bool GROUPED, int DP, int NT, bool BF, bool Q8, int SH>
 __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH>::kThreads, TcShape<DP, NT, BF, Q8, SH>::kPerSm)
     attn_tc(const __grid_constant__ AttnDev p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using Shape = TcShape<DP, NT, BF, Q8, SH>;
@@ -373,12 +373,13 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH>::kThreads, TcShape
   const int row0 = blockIdx.x * (NT * kTcRows);
   const int split = blockIdx.y;
   int ctx, len, nodes, tile0 = 0;
-  if (p.stage == 1) {
+  const bool front = GROUPED && p.stage == 1;
+  if (front) {
     ctx = len = shared_span(p, b);
     nodes = 0;  // asked for row by row
   } else {
     request_span(a, b, &ctx, &len, &nodes);
-    if (p.stage == 2) tile0 = shared_span(p, b / p.size) / kTile;
+    if (GROUPED) tile0 = shared_span(p, b / p.size) / kTile;
   }
   const int tiles = (len + kTile - 1) / kTile;
   const int t_begin = min(tile0 + split * p.per, tiles);
@@ -427,12 +428,12 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH>::kThreads, TcShape
     const int hq = h * G + (r - node * G);
     const bool in = r < rows;
     // the node's request within its group, and its place there
-    const int member = p.stage == 1 ? node / p.inner : 0, place_in = node - member * (p.stage == 1 ? p.inner : 0);
+    const int member = front ? node / p.inner : 0, place_in = front ? node - member * p.inner : node;
     float q_scale = 1.0f;
     {
       // the row of Q into its place
       const uint16_t* qr = reinterpret_cast<const uint16_t*>(a.q) + b * a.q_batch_stride +
-                           (in ? member * p.q_member + place_in * a.q_token_stride + hq * a.q_head_stride : 0);
+                           (in ? (front ? member * p.q_member : 0) + place_in * a.q_token_stride + hq * a.q_head_stride : 0);
       auto piece = [&](int c) {
         return in && c * 8 < a.D ? *reinterpret_cast<const uint4*>(qr + c * 8) : make_uint4(0, 0, 0, 0);
       };
@@ -523,7 +524,7 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH>::kThreads, TcShape
     }
     // rows past the last (their Q is zero) and of missing nodes go along as
     // if they saw the context; what they get is not written
-    if (p.stage == 1 && in) nodes = a.nodes ? a.nodes[b * p.size + member] : p.inner;
+    if (front && in) nodes = a.nodes ? a.nodes[b * p.size + member] : p.inner;
     const bool seen = in && place_in < nodes;
     const uint64_t bits = seen && a.tree ? a.tree[b * a.T + node] : 0;
     const bool idle = SH == 1 && row0 + warp * 32 >= rows;  // the whole warp
@@ -726,7 +727,7 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH>::kThreads, TcShape
           x[4 * i + 3] = t.w;
         }
         if (write) {
-          if (p.parts) {
+          if (GROUPED || p.splits > 1) {
             float4* po = reinterpret_cast<float4*>(p.part_o + ((int64_t)split * all_rows + row) * a.D + d);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -754,7 +755,7 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH>::kThreads, TcShape
 #pragma unroll
       for (int i = 0; i < 32; ++i) o[i] = n > 0 && l != 0.0f ? __float_as_uint(__uint_as_float(o[i]) * inv) : 0u;
       if (write) {
-        if (p.parts) {
+        if (GROUPED || p.splits > 1) {
           uint4* po = reinterpret_cast<uint4*>(p.part_o + ((int64_t)split * all_rows + row) * a.D + c);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -776,7 +777,7 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH>::kThreads, TcShape
       __syncwarp();
     }
     if (write && (SH == 1 || warp == 0)) {
-      if (p.parts) p.part_l[(int64_t)split * all_rows + row] = lse;
+      if (GROUPED || p.splits > 1) p.part_l[(int64_t)split * all_rows + row] = lse;
       else if (a.lse) a.lse[row] = lse;
     }
     tc_fence_before();
@@ -1098,7 +1099,7 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH>::kThreads, TcShape
     tc_fence_before();
   }
   // a join that waits for this launch waits for the one before it, too
-  if (p.stage == 2) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (GROUPED && p.stage == 2) asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncwarp();
   __syncthreads();
   if (dead) {  // products and copies may still be in flight: time for them to end

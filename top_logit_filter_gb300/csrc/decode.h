@@ -95,13 +95,14 @@ struct VerifyArgs {
   int64_t B;
   int32_t T, V;
   int32_t cs;     // CTAs of a request
+  int32_t ahead;  // nodes of a step
   int32_t whole;  // rows and variates may be read 16 bytes at a time
   int32_t* count;
   int32_t* path;
   int32_t* token;
   float* logprob;  // or nullptr
 };
-int verify_cluster(int64_t B, int64_t V, int esize, int num_sms);
+void verify_plan(int64_t B, int64_t V, int esize, bool draft, int num_sms, int* cs, int* ahead);
 cudaError_t launch_verify(topkp_dtype dt, const VerifyArgs& a, cudaStream_t s);
 
 // ------------------------------------------------------------------ pages

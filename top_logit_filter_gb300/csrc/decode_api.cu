@@ -826,7 +826,7 @@ topkp_status topkp_draft_verify(const topkp_draft_verify_args* args, void* strea
   v.B = a.B;
   v.T = (int32_t)a.T;
   v.V = (int32_t)a.V;
-  v.cs = verify_cluster(a.B, a.V, es, kPlanSms);
+  verify_plan(a.B, a.V, es, a.draft != nullptr, kPlanSms, &v.cs, &v.ahead);
   // every row that is read begins on 16 bytes and ends on whole ones
   uint64_t all = (uint64_t)(uintptr_t)a.target | (uint64_t)(uintptr_t)a.draft | (uint64_t)(uintptr_t)a.race | (uint64_t)a.V * es;
   if (a.B > 1) all |= (uint64_t)a.target_batch_stride * es | (uint64_t)a.ld_race * 4 | (a.draft ? (uint64_t)a.draft_batch_stride * es : 0);

@@ -15,9 +15,14 @@
 // through distributed shared memory, so that a pass ends in one barrier and
 // every CTA takes the same decision by itself.
 //
-// Sums are fp32 in a thread (at most a few tens of terms of a batch, then a
-// few tens of batches), 64 bits from the warps' sums on.
+// A step may read the rows of several nodes, each the first child of the one
+// before, while few requests leave the device idle: a chain whose tokens are
+// accepted is then decided in one step.
+//
+// Sums are fp32 in a thread (a batch's few tens of terms, then a few tens of
+// batches) and a warp, fixed point beyond.
 #include <limits.h>
+#include <type_traits>
 
 #include "common.cuh"
 #include "decode.h"
@@ -26,6 +31,7 @@ namespace topkp {
 namespace {
 
 constexpr int kVW = kVerifyThreads / 32;
+constexpr float kLog2e = 1.4426950408889634f;   // (off by 2^-26 of itself: a sum whose terms lie e^-20 below the largest by 3e-7)
 constexpr float kLog2eHi = 1.44268798828125f;  // log2 e to 16 bits
 constexpr float kLog2eLo = 7.0526077e-06f;     // the rest
 
@@ -75,29 +81,23 @@ struct Sum {
   float m, s;
 };
 
-// Vectors of 16 bytes; the first and last of a row may stick out of it.
+// A row as vectors of 16 bytes: `head` elements before the first of them, and
+// what is left behind the last.
 template <int DT>
 struct Row {
   using raw = typename DType<DT>::raw;
   static constexpr int VEC = 16 / (int)sizeof(raw);
   const raw* x;
-  int V, off, vectors;  // elements that the first vector begins before the row
-  __device__ __forceinline__ Row(const raw* p, int n)
-      : x(p), V(n), off((int)(((uintptr_t)p & 15) / sizeof(raw))), vectors((int)(((long long)off + n + VEC - 1) / VEC)) {}
-  __device__ __forceinline__ uint4 load(int v) const {
-    const int e = v * VEC - off;
-    if (e >= 0 && e <= V - VEC) return __ldg(reinterpret_cast<const uint4*>(x + e));
-    return edge(e);
+  int V, head, vectors;
+  __device__ __forceinline__ Row(const raw* p, int n) : x(p), V(n) {
+    head = min((int)((16 - ((uintptr_t)p & 15)) % 16 / sizeof(raw)), n);
+    vectors = (n - head) / VEC;
   }
-  __device__ __noinline__ uint4 edge(int e) const {
-    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const uint32_t r = e + j >= 0 && e + j < V ? (uint32_t)x[e + j] : (uint32_t)DType<DT>::kNegInf;
-      if (sizeof(raw) == 4) w[j % 4] = r;
-      else w[(j >> 1) % 4] |= r << (16 * (j & 1));
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+  __device__ __forceinline__ const uint4* at(int v) const { return reinterpret_cast<const uint4*>(x + head) + v; }
+  // element k of those that lie in no vector, up to 2 VEC - 2 of them: its place, or -1
+  __device__ __forceinline__ int loose(int k) const {
+    const int i = k < head ? k : k + vectors * VEC;
+    return i < V ? i : -1;
   }
 };
 template <int DT>
@@ -123,26 +123,41 @@ __device__ __forceinline__ void pair_of(const uint4& q, int j, float& a, float& 
   }
 }
 
+// The largest element of U vectors; 16-bit types two at a time.
+template <int DT, int U>
+__device__ __forceinline__ float largest(const uint4 (&q)[U]) {
+  if constexpr (DT == TOPKP_F32) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(q[u].x), __uint_as_float(q[u].y)), fmaxf(__uint_as_float(q[u].z), __uint_as_float(q[u].w))));
+    return m;
+  } else {
+    using pair = typename std::conditional<DT == TOPKP_F16, __half2, __nv_bfloat162>::type;
+    auto as = [](const uint32_t& w) { return *reinterpret_cast<const pair*>(&w); };
+    pair m = __hmax2(__hmax2(as(q[0].x), as(q[0].y)), __hmax2(as(q[0].z), as(q[0].w)));
+#pragma unroll
+    for (int u = 1; u < U; ++u) m = __hmax2(m, __hmax2(__hmax2(as(q[u].x), as(q[u].y)), __hmax2(as(q[u].z), as(q[u].w))));
+    if constexpr (DT == TOPKP_F16) {
+      const float2 f = __half22float2(m);
+      return fmaxf(f.x, f.y);
+    } else {
+      const float2 f = __bfloat1622float2(m);
+      return fmaxf(f.x, f.y);
+    }
+  }
+}
 // U vectors into a thread's share.
 template <int DT, int U>
 __device__ __forceinline__ void absorb(const uint4 (&q)[U], Sum& s) {
   constexpr int PAIRS = Row<DT>::VEC / 2;
-  float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-#pragma unroll
-    for (int j = 0; j < PAIRS; ++j) {
-      float a, b;
-      pair_of<DT>(q[u], j, a, b);
-      top[j & 1] = fmaxf(top[j & 1], fmaxf(a, b));
-    }
-  const float mx = fmaxf(top[0], top[1]);
+  const float mx = largest<DT, U>(q);
   if (mx > s.m) {
     s.s *= s.m == -INFINITY ? 0.0f : exp_fast(s.m - mx);
     s.m = mx;
   }
   if (s.m == -INFINITY) return;
-  const uint64_t less = two(-s.m, -s.m), hi = two(kLog2eHi, kLog2eHi), lo = two(kLog2eLo, kLog2eLo);
+  const uint64_t less = two(-s.m, -s.m), scale = two(kLog2e, kLog2e);
   uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
   for (int u = 0; u < U; ++u)
@@ -150,8 +165,7 @@ __device__ __forceinline__ void absorb(const uint4 (&q)[U], Sum& s) {
     for (int j = 0; j < PAIRS; ++j) {
       float a, b;
       pair_of<DT>(q[u], j, a, b);
-      const uint64_t t = add_two(two(a, b), less);
-      apart(fma_two(t, hi, mul_two(t, lo)), a, b);
+      apart(mul_two(add_two(two(a, b), less), scale), a, b);
       sum[j & 1] = add_two(sum[j & 1], two(ex2(a), ex2(b)));
     }
   float a, b;
@@ -159,17 +173,27 @@ __device__ __forceinline__ void absorb(const uint4 (&q)[U], Sum& s) {
   s.s += a + b;
 }
 
-// What a warp hands to every CTA of its cluster, and what a step leaves there.
+__device__ __forceinline__ void prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+constexpr int kAhead = 4;  // nodes of a step, at most
+enum { kGo, kPass, kDraw };
+
+// What the warps of a cluster hand to each other, and what a step leaves.
 struct Shared {
-  float4 part[2][16 * kVW];
+  float4 part[2][kAhead][16 * kVW];
   int32_t parent[TOPKP_MAX_TREE], tokens[TOPKP_MAX_TREE], path[TOPKP_MAX_TREE], tried[TOPKP_MAX_TREE];
-  float uniform[TOPKP_MAX_TREE], logprob[TOPKP_MAX_TREE];
-  float xt[TOPKP_MAX_TREE], xd[TOPKP_MAX_TREE];  // the children's logits
-  double px[TOPKP_MAX_TREE], qx[TOPKP_MAX_TREE];
-  float mt, md, factor;
-  double st, sd, weight, less;
-  unsigned long long bloom, best;
-  int chosen, next, tries, again;
+  float uniform[TOPKP_MAX_TREE];
+  float xt[TOPKP_MAX_TREE], xd[TOPKP_MAX_TREE];    // the children's logits
+  float gap[TOPKP_MAX_TREE], sum[TOPKP_MAX_TREE];  // of the emitted tokens: logit less the row's largest, the row's sum
+  // the node that the walk has come to
+  float mt, md, st, sd;     // the rows' largest logits and sums of exponentials
+  float weight, factor;     // W and a of the comment above, times st and st / sd
+  unsigned long long open;  // children to be tried
+  unsigned long long best;
+  uint32_t bound;  // a candidate's key of the draw
+  int state, node, depth, tries, top, token;
+  int n;                    // nodes of the request
+  const void *target, *draft;  // its rows
 };
 
 struct Team {
@@ -183,11 +207,11 @@ __device__ __forceinline__ void team_sync(const Team& t) {
   if (t.cs > 1) cluster_sync_all();
   else __syncthreads();
 }
-// This warp's part to all CTAs (lane 0's value).
-__device__ __forceinline__ void hand_out(const Team& t, Shared& sh, const float4& v) {
+// This warp's part to all CTAs, a lane a CTA.
+__device__ __forceinline__ void hand_out(const Team& t, Shared& sh, int set, int place, const float4& v) {
   const int lane = threadIdx.x & 31;
   if (lane < t.cs) {
-    float4* to = &sh.part[t.at][t.rank * kVW + (threadIdx.x >> 5)];
+    float4* to = &sh.part[t.at][set][place];
     if (t.cs == 1) {
       *to = v;
     } else {
@@ -196,17 +220,7 @@ __device__ __forceinline__ void hand_out(const Team& t, Shared& sh, const float4
     }
   }
 }
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
 __device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-__device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
@@ -219,69 +233,398 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
   }
   return v;
 }
-// Maximum and sum over the warps' parts, by one warp.
-__device__ __forceinline__ void join_sums(const Team& t, const Shared& sh, bool second, float& m, double& s) {
-  const int lane = threadIdx.x & 31, n = t.cs * kVW;
-  m = -INFINITY;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, second ? sh.part[t.at][i].z : sh.part[t.at][i].x);
-  m = warp_max(m);
-  s = 0.0;
-  for (int i = lane; i < n; i += 32) {
-    const float4 v = sh.part[t.at][i];
-    const float pm = second ? v.z : v.x, ps = second ? v.w : v.y;
-    if (pm > -INFINITY) s += (double)(ps * exp_one(pm, m));
+// Maxima and sums of both rows over the warps' n parts, by one warp: a lane's
+// up to eight parts side by side, since one after another their latency was
+// most of a step's time.
+template <bool DRAFT>
+__device__ __forceinline__ void join_sums(const float4* part, int n, float& mt, float& st, float& md, float& sd) {
+  constexpr int E = 16 * kVW / 32;
+  const int lane = threadIdx.x & 31;
+  float4 v[E];
+#pragma unroll
+  for (int k = 0; k < E; ++k) v[k] = lane + 32 * k < n ? part[lane + 32 * k] : make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
+  mt = v[0].x;
+  md = v[0].z;
+#pragma unroll
+  for (int k = 1; k < E; ++k) {
+    mt = fmaxf(mt, v[k].x);
+    md = fmaxf(md, v[k].z);
   }
-  s = warp_sum(s);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+    if (DRAFT) md = fmaxf(md, __shfl_xor_sync(0xffffffffu, md, o));
+  }
+  const float rt = mt == -INFINITY ? 0.0f : mt, rd = md == -INFINITY ? 0.0f : md;
+  st = sd = 0.0f;
+#pragma unroll
+  for (int k = 0; k < E; ++k) {
+    if (k > 0 && 32 * k >= n) break;
+    st = fmaf(v[k].y, exp_fast(v[k].x - rt), st);
+    if (DRAFT) sd = fmaf(v[k].w, exp_fast(v[k].z - rd), sd);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    st += __shfl_xor_sync(0xffffffffu, st, o);
+    if (DRAFT) sd += __shfl_xor_sync(0xffffffffu, sd, o);
+  }
 }
+// A warp's shares as one.
 __device__ __forceinline__ Sum warp_join(const Sum& s) {
   Sum r;
-  r.m = warp_max(s.m);
+  r.m = s.m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) r.m = fmaxf(r.m, __shfl_xor_sync(0xffffffffu, r.m, o));
   r.s = warp_sum(s.m == -INFINITY ? 0.0f : s.s * exp_fast(s.m - r.m));
   return r;
+}
+
+// Largest element and sum of this CTA's part of a row, by `threads` threads,
+// of which this is `who`; a warp's joined.  Rows are given to warps rather
+// than both to each: two rows' loads in flight did not fit the registers
+// (53 against 45 thousand cycles a step of 128 x 152064 fp32).  With GREEDY
+// `first` is the place of the largest.
+template <int DT, bool GREEDY>
+__device__ __forceinline__ Sum scan(const typename DType<DT>::raw* x, int V, int rank, int cs, int threads, int who, uint32_t& first) {
+  constexpr int VEC = Row<DT>::VEC;
+  Sum s = {-INFINITY, 0.0f}, loose = {-INFINITY, 0.0f};
+  uint32_t at_loose = 0;
+  first = 0xffffffffu;
+  const Row<DT> r(x, V);
+  const int per = (r.vectors + cs - 1) / cs, begin = min(per * rank, r.vectors), n = min(per, r.vectors - begin);
+  if (rank == 0 && who < 2 * VEC - 2) {  // what lies in no vector
+    const int i = r.loose(who);
+    if (i >= 0) {
+      // (greedy: apart, since it may lie behind the vectors, and of equal elements the first counts)
+      Sum& one = GREEDY ? loose : s;
+      one.m = DType<DT>::to_float(x[i]);
+      one.s = one.m > -INFINITY ? 1.0f : 0.0f;
+      at_loose = (uint32_t)i;
+    }
+  }
+  const uint4* p = r.at(begin) + who;
+  const int place = (begin + who) * VEC + r.head;
+  // U vectors, all read before the first is used; `all`: none is beyond the end
+  auto take = [&](auto count, auto all, int at) {
+    constexpr int U = decltype(count)::value;
+    constexpr bool ALL = decltype(all)::value;
+    uint4 q[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) q[u] = ALL || at + u * threads + who < n ? __ldg(p + at + u * threads) : nothing<DT>();
+    const float before = s.m;
+    absorb<DT, U>(q, s);
+    if (GREEDY && s.m > before) {  // its first place
+#pragma unroll
+      for (int u = U - 1; u >= 0; --u)
+#pragma unroll
+        for (int j = VEC / 2 - 1; j >= 0; --j) {
+          float a, b;
+          pair_of<DT>(q[u], j, a, b);
+          const uint32_t e = (uint32_t)(place + (at + u * threads) * VEC + 2 * j);
+          if (b == s.m) first = e + 1;
+          if (a == s.m) first = e;
+        }
+    }
+  };
+  using One = std::integral_constant<int, 1>;
+  using Eight = std::integral_constant<int, 8>;
+  int at = 0;
+  for (; at + 8 * threads <= n; at += 8 * threads) take(Eight(), std::true_type(), at);
+  if (n - at > threads) {
+    take(Eight(), std::false_type(), at);
+  } else if (n > at) {
+    take(One(), std::false_type(), at);
+  }
+  if (GREEDY && loose.m > -INFINITY) {
+    if (loose.m > s.m) {
+      s.s = s.m == -INFINITY ? 0.0f : s.s * exp_fast(s.m - loose.m);
+      s.m = loose.m;
+      first = at_loose;
+    } else if (loose.m == s.m) {
+      first = min(first, at_loose);
+    }
+    s.s += exp_fast(loose.m - s.m);
+  }
+  const Sum w = warp_join(s);
+  if (GREEDY) first = __reduce_min_sync(0xffffffffu, s.m == w.m ? first : 0xffffffffu);
+  return w;
 }
 
 // A candidate of the draw: the larger key, the lower index.
 __device__ __forceinline__ unsigned long long candidate(float key, int i) {
   return (unsigned long long)__float_as_uint(key) << 32 | (uint32_t)~i;
 }
+// The children of a node, by a whole warp.
+__device__ __forceinline__ unsigned long long children(const Shared& sh, int node, int n) {
+  const int lane = threadIdx.x & 31;
+  const bool lo = lane > node && lane < n && sh.parent[lane] == node;
+  const bool hi = lane + 32 > node && lane + 32 < n && sh.parent[lane + 32] == node;
+  return __ballot_sync(0xffffffffu, lo) | (unsigned long long)__ballot_sync(0xffffffffu, hi) << 32;
+}
 
-// A CTA's elements of a node's rows, once more: f(i, target's logit, draft's,
-// the race's variate) for each, -inf and 0 for what is not read.
-template <int DT, bool DRAFT, bool RACE, typename F>
-__device__ __forceinline__ void each_element(const VerifyArgs& a, const Team& team, const typename DType<DT>::raw* t,
-                                             const typename DType<DT>::raw* d, bool draft, const float* race, F f) {
-  constexpr int VEC = Row<DT>::VEC, U = 2;
+// This CTA's elements of a row.
+template <int DT>
+__device__ __forceinline__ void part_of(const VerifyArgs& a, const Team& team, int& first, int& last) {
+  constexpr int VEC = Row<DT>::VEC;
   const int per = ((a.V + a.cs - 1) / a.cs + VEC - 1) / VEC * VEC;
-  const int first = min(per * (int)team.rank, a.V), last = min(first + per, a.V);
-  if (a.whole) {  // all rows 16 bytes at a time
+  first = min(per * (int)team.rank, a.V);
+  last = min(first + per, a.V);
+}
+
+// A thread's sum of max(exp(x - mt) - factor exp(y - md), 0).
+template <int DT>
+__device__ __forceinline__ float weigh(const VerifyArgs& a, const Team& team, const typename DType<DT>::raw* t,
+                                       const typename DType<DT>::raw* d, float mt, float md, float factor) {
+  constexpr int VEC = Row<DT>::VEC, U = 4;
+  int first, last;
+  part_of<DT>(a, team, first, last);
+  float sum = 0.0f;
+  if (mt == -INFINITY) return 0.0f;
+  const bool drafted = md > -INFINITY;
+  const uint64_t hi = two(kLog2eHi, kLog2eHi), lo = two(kLog2eLo, kLog2eLo);
+  const uint64_t lt = two(-mt, -mt), ld = drafted ? two(-md, -md) : 0ull;
+  auto exps = [&](float& x, float& y, uint64_t less) {
+    const uint64_t v = add_two(two(x, y), less);
+    apart(fma_two(v, hi, mul_two(v, lo)), x, y);
+    x = ex2(x);
+    y = ex2(y);
+  };
+  auto add = [&](float x, float y, float c, float g) {
+    exps(x, y, lt);
+    exps(c, g, ld);
+    sum += fmaxf(fmaf(-factor, c, x), 0.0f) + fmaxf(fmaf(-factor, g, y), 0.0f);
+  };
+  if (a.whole) {
     for (int i0 = first + (int)threadIdx.x * VEC; i0 < last; i0 += U * kVerifyThreads * VEC) {
       uint4 qt[U], qd[U];
-      float4 e[U][VEC / 4];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int i = i0 + u * kVerifyThreads * VEC;
-        const bool in = i < last;
-        qt[u] = in ? __ldg(reinterpret_cast<const uint4*>(t + i)) : nothing<DT>();
-        qd[u] = DRAFT && draft && in ? __ldg(reinterpret_cast<const uint4*>(d + i)) : nothing<DT>();
-#pragma unroll
-        for (int k = 0; k < VEC / 4; ++k)
-          e[u][k] = RACE && in ? __ldg(reinterpret_cast<const float4*>(race + i) + k) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        qt[u] = i < last ? __ldg(reinterpret_cast<const uint4*>(t + i)) : nothing<DT>();
+        qd[u] = i < last ? __ldg(reinterpret_cast<const uint4*>(d + i)) : nothing<DT>();
       }
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int j = 0; j < VEC / 2; ++j) {
-          const int i = i0 + u * kVerifyThreads * VEC + 2 * j;
-          float x, y, c = -INFINITY, g = -INFINITY;
+          float x, y, c, g;
           pair_of<DT>(qt[u], j, x, y);
-          if (DRAFT) pair_of<DT>(qd[u], j, c, g);
-          f(i, x, c, j & 1 ? e[u][j / 2].z : e[u][j / 2].x);
-          f(i + 1, y, g, j & 1 ? e[u][j / 2].w : e[u][j / 2].y);
+          pair_of<DT>(qd[u], j, c, g);
+          add(x, y, c, g);
         }
     }
   } else {
-    for (int i = first + (int)threadIdx.x; i < last; i += kVerifyThreads)
-      f(i, DType<DT>::to_float(t[i]), DRAFT && draft ? DType<DT>::to_float(d[i]) : -INFINITY, RACE ? race[i] : 0.0f);
+    for (int i = first + (int)threadIdx.x; i < last; i += 2 * kVerifyThreads) {
+      const bool two_of = i + kVerifyThreads < last;
+      add(DType<DT>::to_float(t[i]), two_of ? DType<DT>::to_float(t[i + kVerifyThreads]) : -INFINITY, DType<DT>::to_float(d[i]),
+          two_of ? DType<DT>::to_float(d[i + kVerifyThreads]) : -INFINITY);
+    }
+  }
+  return sum;
+}
+
+// The best candidate of this warp's elements: the largest
+// (exp(x - mt) - factor exp(y - md)) / (variate + eps), of equal ones the
+// first.  No element can be better than exp(x - mt) / (variate + eps), which
+// a few instructions tell to 2^-14; what that leaves in the race, few
+// elements of a row, is worked out with care, a lane's best first, so that
+// the bound rises fast.  (With care for every element: 33 thousand cycles a
+// CTA for 4 x 128256 bf16 over 64 requests, and the draft's row read again.)
+template <int DT, int MODE>
+__device__ __forceinline__ unsigned long long draw(const VerifyArgs& a, const Team& team, Shared& sh, const typename DType<DT>::raw* t,
+                                                   const typename DType<DT>::raw* d, const float* race, float factor, int tries) {
+  constexpr int VEC = Row<DT>::VEC, K = 16, U = K / VEC;
+  const float mt = sh.mt, md = sh.md, eps = a.eps;
+  int first, last;
+  part_of<DT>(a, team, first, last);
+  unsigned long long best = 0ull;
+  if (mt == -INFINITY) return 0ull;
+  for (int base = first; base < last; base += K * kVerifyThreads) {
+    // element k of this thread; about what it is in the race
+    auto place = [&](int k) {
+      return base + (a.whole ? ((k / VEC) * kVerifyThreads + (int)threadIdx.x) * VEC + k % VEC : k * kVerifyThreads + (int)threadIdx.x);
+    };
+    float r[K];
+    auto rough = [&](int k, float x, float y, float v, float w) {
+      const uint64_t e = mul_two(add_two(two(x, y), two(-mt, -mt)), two(1.4426950408889634f, 1.4426950408889634f));
+      float p, q, g, h;
+      apart(e, p, q);
+      apart(add_two(two(v, w), two(eps, eps)), g, h);
+      asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(g));
+      asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(h));
+      r[k] = ex2(p) * g;
+      r[k + 1] = ex2(q) * h;
+    };
+    if (a.whole) {
+      uint4 q[U];
+      float4 v[U][VEC / 4];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = place(u * VEC);
+        q[u] = i < last ? __ldg(reinterpret_cast<const uint4*>(t + i)) : nothing<DT>();
+#pragma unroll
+        for (int k = 0; k < VEC / 4; ++k) v[u][k] = i < last ? __ldg(reinterpret_cast<const float4*>(race + i) + k) : make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j) {
+          float x, y;
+          pair_of<DT>(q[u], j, x, y);
+          rough(u * VEC + 2 * j, x, y, j & 1 ? v[u][j / 2].z : v[u][j / 2].x, j & 1 ? v[u][j / 2].w : v[u][j / 2].y);
+        }
+    } else {
+#pragma unroll
+      for (int k = 0; k < K; k += 2) {
+        const int i = place(k), j = place(k + 1);
+        rough(k, i < last ? DType<DT>::to_float(t[i]) : -INFINITY, j < last ? DType<DT>::to_float(t[j]) : -INFINITY,
+              i < last ? race[i] : 1.0f, j < last ? race[j] : 1.0f);
+      }
+    }
+    for (;;) {
+      float top = r[0];
+#pragma unroll
+      for (int k = 1; k < K; ++k) top = fmaxf(top, r[k]);
+      const uint32_t bound = *(volatile uint32_t*)&sh.bound;
+      const bool go = top > 0.0f && top * 1.00006103515625f >= __uint_as_float(bound);
+      if (!__any_sync(0xffffffffu, go)) break;
+      if (go) {
+        int at = 0;
+        bool found = false;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          const bool me = !found && r[k] == top;
+          if (me) {
+            at = k;
+            r[k] = 0.0f;
+          }
+          found = found || me;
+        }
+        const int i = place(at);
+        float e = exp_one(DType<DT>::to_float(t[i]), mt);
+        if (MODE == kVerifyRatio && factor > 0.0f) {
+          const float y = DType<DT>::to_float(d[i]);
+          if (y > -INFINITY) e = fmaxf(fmaf(-factor, exp_one(y, md), e), 0.0f);
+        }
+        if (MODE == kVerifyCertain)
+          for (int k = 0; k < tries; ++k)
+            if (sh.tried[k] == i) e = 0.0f;
+        if (e > 0.0f) {
+          const float key = __fdiv_rn(e, race[i] + eps);
+          const unsigned long long c = candidate(key, i);
+          best = c > best ? c : best;
+          if (__float_as_uint(key) > bound) atomicMax(&sh.bound, __float_as_uint(key));
+        }
+      }
+      __syncwarp();
+    }
+  }
+  return warp_max(best);
+}
+
+// The walk as far as the rows that were read go, by one warp: children in
+// turn, on to the next node of the step where its token is accepted.  `set`
+// is the node's among the step's, of `parts` parts each; resumed: after a pass for the weight of
+// what is left at sh.node.
+template <int DT, int MODE>
+__device__ __forceinline__ void decide(const VerifyArgs& a, const Team& team, Shared& sh, int n, int sets, int parts, bool resumed) {
+  constexpr bool DRAFT = MODE == kVerifyRatio, GREEDY = MODE == kVerifyGreedy;
+  const int lane = threadIdx.x & 31;
+  int node = sh.node, depth = sh.depth, state = kDraw, tries = 0, top = -1;
+  float mt = sh.mt, md = sh.md, st = sh.st, sd = sh.sd, weight = sh.weight, factor = sh.factor;
+  unsigned long long open = sh.open, bloom = 0ull;
+  if (resumed) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 16 * kVW / 32; ++k)
+      if (lane + 32 * k < parts) sum += sh.part[team.at][0][lane + 32 * k].x;
+    weight = warp_sum(sum);
+  }
+  float inverse = 1.0f / sd;
+  for (int set = 0;;) {
+    if (!resumed) {
+      join_sums<DRAFT>(sh.part[team.at][set], parts, mt, st, md, sd);
+      if (GREEDY) {
+        uint32_t f = 0xffffffffu;
+        for (int i = lane; i < parts; i += 32) {
+          const float4 v = sh.part[team.at][set][i];
+          if (v.x == mt) f = min(f, __float_as_uint(v.z));
+        }
+        top = (int)__reduce_min_sync(0xffffffffu, f);
+        if (mt == -INFINITY || top < 0 || top >= a.V) top = -1;
+      }
+      inverse = 1.0f / sd;
+      open = children(sh, node, n);
+      weight = st;
+      factor = 0.0f;
+      tries = 0;
+      bloom = 0ull;
+    }
+    const int next = open ? __ffsll((long long)open) - 1 : -1;  // the step's next node, where this is not resumed
+    int chosen = -1;
+    state = kDraw;
+    while (open) {
+      const int c = __ffsll((long long)open) - 1;
+      open &= open - 1;
+      const int x = sh.tokens[c];
+      if (x < 0 || x >= a.V) continue;
+      if (GREEDY) {
+        if (x == top) chosen = c;
+      } else {
+        float left = exp_one(sh.xt[c], mt), q = 1.0f;
+        if (sh.xt[c] == -INFINITY) left = 0.0f;
+        if (DRAFT) {
+          q = sd > 0.0f && sh.xd[c] > -INFINITY ? exp_one(sh.xd[c], md) : 0.0f;
+          if (sh.uniform[c] * (q * inverse) * weight < fmaf(-factor, q, left) || (q == 0.0f && left > 0.0f)) {
+            chosen = c;
+          } else {
+            if (sd > 0.0f) factor += weight * inverse;
+            if (open) {
+              state = kPass;
+              break;
+            }
+          }
+        } else {
+          if (bloom >> ((x >> 3) & 63) & 1)
+            for (int i = 0; i < tries; ++i)
+              if (sh.tried[i] == x) left = 0.0f;
+          if (sh.uniform[c] * weight < left) {
+            chosen = c;
+          } else if (left > 0.0f) {
+            weight = fmaxf(weight - left, 0.0f);
+            if (lane == 0) sh.tried[tries] = x;
+            __syncwarp();
+            ++tries;
+            bloom |= 1ull << ((x >> 3) & 63);
+          }
+        }
+      }
+      if (chosen >= 0) break;
+    }
+    if (chosen < 0) break;
+    if (lane == 0) {
+      sh.gap[depth] = GREEDY ? 0.0f : sh.xt[chosen] - mt;
+      sh.sum[depth] = st;
+      sh.path[depth + 1] = chosen;
+    }
+    ++depth;
+    node = chosen;
+    state = kGo;
+    if (resumed || chosen != next || ++set >= sets) break;
+  }
+  if (lane == 0) {
+    sh.state = state;
+    sh.node = node;
+    sh.depth = depth;
+    sh.mt = mt;
+    sh.md = md;
+    sh.st = st;
+    sh.sd = sd;
+    sh.weight = weight;
+    sh.factor = factor;
+    sh.open = open;
+    sh.tries = tries;
+    sh.top = top;
   }
 }
 
@@ -289,254 +632,141 @@ template <int DT, int MODE>
 __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const __grid_constant__ VerifyArgs a) {
   using raw = typename DType<DT>::raw;
   constexpr bool DRAFT = MODE == kVerifyRatio, GREEDY = MODE == kVerifyGreedy;
-  constexpr int VEC = Row<DT>::VEC;
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Team team = {a.cs, a.cs > 1 ? cluster_ctarank() : 0u, 0};
-  const int64_t b = blockIdx.x / a.cs;
-  const int n = a.nodes ? min(max(a.nodes[b], 0), a.T) : a.T;
-  if (tid < a.T) {
-    const int64_t i = b * a.T + tid;
-    sh.parent[tid] = a.parent ? a.parent[i] : tid - 1;
-    sh.tokens[tid] = a.tokens[i];
-    sh.uniform[tid] = a.uniform ? a.uniform[i] : 0.0f;
-    sh.path[tid] = -1;
-    sh.logprob[tid] = 0.0f;
+  if (a.cs > 1) cluster_arrive();
+  {
+    const int64_t b = blockIdx.x / a.cs;
+    const int n = a.nodes ? min(max(a.nodes[b], 0), a.T) : a.T;
+    if (tid < a.T) {
+      const int64_t i = b * a.T + tid;
+      sh.parent[tid] = a.parent ? a.parent[i] : tid - 1;
+      sh.tokens[tid] = a.tokens[i];
+      sh.uniform[tid] = a.uniform ? a.uniform[i] : 0.0f;
+      sh.path[tid] = tid == 0 && n > 0 ? 0 : -1;
+    }
+    if (tid == 0) {
+      sh.node = sh.depth = sh.bound = 0;
+      sh.token = -1;
+      sh.n = n;
+      sh.target = reinterpret_cast<const raw*>(a.target) + b * a.t_batch;
+      sh.draft = reinterpret_cast<const raw*>(a.draft) + (DRAFT ? b * a.d_batch : 0);
+    }
   }
+  __syncthreads();
   // every CTA of the cluster has started before one writes into another's memory
-  team_sync(team);
-  int node = 0, depth = 0, token = -1;
-  const raw* target = reinterpret_cast<const raw*>(a.target) + b * a.t_batch;
-  const raw* draft = reinterpret_cast<const raw*>(a.draft) + (DRAFT ? b * a.d_batch : 0);
-  if (n > 0) {
-    if (tid == 0) sh.path[0] = 0;
-    for (;;) {
-      // the children, and their logits
-      unsigned long long kids = 0;
-      {
-        const bool lo = lane > node && lane < n && sh.parent[lane] == node;
-        const bool hi = lane + 32 > node && lane + 32 < n && sh.parent[lane + 32] == node;
-        kids = __ballot_sync(0xffffffffu, lo) | (unsigned long long)__ballot_sync(0xffffffffu, hi) << 32;
-      }
-      const raw* t = target + node * a.t_node;
-      const raw* d = draft + (DRAFT ? node * a.d_node : 0);
-      const bool drafted = DRAFT && kids != 0;
-      if (!GREEDY && warp < 2) {
-        const int c = warp * 32 + lane;
-        if (kids >> c & 1) {
-          const int x = sh.tokens[c];
-          const bool in = x >= 0 && x < a.V;
-          sh.xt[c] = in ? DType<DT>::to_float(t[x]) : -INFINITY;
-          sh.xd[c] = DRAFT && in ? DType<DT>::to_float(d[x]) : -INFINITY;
-        }
-      }
-      // largest elements and sums of both rows
-      Sum st = {-INFINITY, 0.0f}, sd = {-INFINITY, 0.0f};
-      uint32_t first = 0xffffffffu;  // of the largest element
-      const Row<DT> rt(t, a.V), rd(DRAFT ? d : t, a.V);
-      {
-        constexpr int U = 4;
-        const int per = (max(rt.vectors, rd.vectors) + a.cs - 1) / a.cs;
-        const int begin = per * (int)team.rank, te = min(begin + per, rt.vectors), de = min(begin + per, rd.vectors);
-        for (int v = begin + tid; v < begin + per; v += U * kVerifyThreads) {
-          uint4 q[U], r[U];
+  if (a.cs > 1) cluster_wait();
+  // (what a pass does not need waits in shared memory: its loads take half the registers)
+  auto target = [&](int node) { return reinterpret_cast<const raw*>(sh.target) + node * a.t_node; };
+  auto draft = [&](int node) { return reinterpret_cast<const raw*>(sh.draft) + (DRAFT ? node * a.d_node : 0); };
+  while (sh.n > 0) {
+    // Largest elements and sums of the node's rows, and of its first child's
+    // and so on: all warps a node, or half or a quarter of them.
+    int sets = 0;
+    {
+      int list[kAhead], next = sh.node, node = -1;
 #pragma unroll
-          for (int u = 0; u < U; ++u) q[u] = v + u * kVerifyThreads < te ? rt.load(v + u * kVerifyThreads) : nothing<DT>();
-          if (DRAFT && drafted) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) r[u] = v + u * kVerifyThreads < de ? rd.load(v + u * kVerifyThreads) : nothing<DT>();
-          }
-          const float before = st.m;
-          absorb<DT, U>(q, st);
-          if (GREEDY && st.m > before) {  // its first place
-#pragma unroll
-            for (int u = U - 1; u >= 0; --u)
-#pragma unroll
-              for (int j = VEC / 2 - 1; j >= 0; --j) {
-                float x, y;
-                pair_of<DT>(q[u], j, x, y);
-                const uint32_t e = (uint32_t)((v + u * kVerifyThreads) * VEC - rt.off + 2 * j);
-                if (y == st.m) first = e + 1;
-                if (x == st.m) first = e;
-              }
-          }
-          if (DRAFT && drafted) absorb<DT, U>(r, sd);
+      for (int g = 0; g < kAhead; ++g) {
+        list[g] = next;
+        if (next >= 0 && g < a.ahead) {
+          ++sets;
+          const unsigned long long kids = children(sh, next, sh.n);
+          next = kids ? __ffsll((long long)kids) - 1 : -1;
         }
       }
-      {
-        const Sum w = warp_join(st);
-        float4 part = make_float4(w.m, w.s, -INFINITY, 0.0f);
-        if (DRAFT) {
-          const Sum x = warp_join(sd);
-          part.z = x.m;
-          part.w = x.s;
+      const int parts = kVW / (sets > 2 ? 4 : sets), which = warp / parts, threads = 32 * parts, who = tid & (threads - 1);
+#pragma unroll
+      for (int g = 0; g < kAhead; ++g)
+        if (g == which && g < sets) node = list[g];
+      if (node >= 0) {
+        auto token_of = [&]() {  // a child's token; none of the vocabulary for other threads
+          return !GREEDY && who < TOPKP_MAX_TREE && (children(sh, node, sh.n) >> (who & 63) & 1) ? sh.tokens[who] : -1;
+        };
+        const bool drafted = DRAFT && children(sh, node, sh.n) != 0;
+        int x = token_of();
+        if (x >= 0 && x < a.V) {  // the children's logits: asked for early, read once the row is through
+          prefetch(target(node) + x);
+          if (DRAFT) prefetch(draft(node) + x);
         }
-        if (GREEDY) part.z = __uint_as_float(__reduce_min_sync(0xffffffffu, st.m == w.m ? first : 0xffffffffu));
-        hand_out(team, sh, part);
+        // the second half of the warps takes the draft's row, where there are children
+        const int half = threads / 2;
+        const bool second = drafted && who >= half;
+        uint32_t first;
+        const Sum got = scan<DT, GREEDY>(second ? draft(node) : target(node), a.V, (int)team.rank, a.cs, drafted ? half : threads,
+                                         drafted ? who & (half - 1) : who, first);
+        float4 mine = make_float4(got.m, got.s, -INFINITY, 0.0f);
+        if (DRAFT && second) mine = make_float4(-INFINITY, 0.0f, got.m, got.s);
+        if (GREEDY) mine.z = __uint_as_float(first);
+        x = token_of();
+        if (x >= 0 && x < a.V) {
+          sh.xt[who] = DType<DT>::to_float(target(node)[x]);
+          if (DRAFT) sh.xd[who] = DType<DT>::to_float(draft(node)[x]);
+        }
+        hand_out(team, sh, which, (int)team.rank * parts + warp % parts, mine);
       }
-      team_sync(team);
-      if (warp == 0) {
-        float mt, md = -INFINITY;
-        double zt, zd = 0.0;
-        join_sums(team, sh, false, mt, zt);
-        if (DRAFT) join_sums(team, sh, true, md, zd);
-        int top = 0;
-        if (GREEDY) {
-          uint32_t f = 0xffffffffu;
-          for (int i = lane; i < a.cs * kVW; i += 32) {
-            const float4 v = sh.part[team.at][i];
-            if (v.x == mt) f = min(f, __float_as_uint(v.z));
-          }
-          top = (int)__reduce_min_sync(0xffffffffu, f);
-          if (mt == -INFINITY || top < 0 || top >= a.V) top = -1;
-        } else {
-          for (int c = lane; c < TOPKP_MAX_TREE; c += 32)
-            if (kids >> c & 1) {
-              sh.px[c] = sh.xt[c] > -INFINITY ? exp((double)sh.xt[c] - mt) / zt : 0.0;
-              if (DRAFT) sh.qx[c] = sh.xd[c] > -INFINITY ? exp((double)sh.xd[c] - md) / zd : 0.0;
-            }
-        }
-        if (lane == 0) {
-          sh.mt = mt;
-          sh.md = md;
-          sh.st = zt;
-          sh.sd = zd;
-          sh.less = 0.0;
-          sh.weight = 1.0;
-          sh.tries = 0;
-          sh.bloom = 0ull;
-          sh.best = (unsigned long long)(long long)top;
-        }
-      }
+    }
+    team_sync(team);
+    for (bool resumed = false;; resumed = true) {
+      if (warp == 0) decide<DT, MODE>(a, team, sh, sh.n, sets, (resumed ? kVW : kVW / (sets > 2 ? 4 : sets)) * a.cs, resumed);
       team.at ^= 1;
-      // the children in turn, by one thread; a pass of all where the weight of what is left is wanted
-      unsigned long long open = kids;
-      int chosen = -1;
-      for (;;) {
-        if (tid == 0) {
-          chosen = -1;
-          bool pass = false;
-          while (open && chosen < 0 && !pass) {
-            const int c = __ffsll((long long)open) - 1;
-            open &= open - 1;
-            const int x = sh.tokens[c];
-            if (x < 0 || x >= a.V) continue;
-            if (GREEDY) {
-              if (x == (int)(long long)sh.best) chosen = c;
-              continue;
-            }
-            double left = sh.px[c], q = 1.0;
-            if (DRAFT) {
-              q = sh.qx[c];
-              left -= sh.less * q;
-            } else if (sh.bloom >> ((x >> 3) & 63) & 1) {
-              for (int i = 0; i < sh.tries; ++i)
-                if (sh.tried[i] == x) left = 0.0;
-            }
-            if ((double)sh.uniform[c] * q * sh.weight < left) {
-              chosen = c;
-            } else if (DRAFT) {
-              sh.less += sh.weight;
-              pass = open != 0;
-            } else if (left > 0.0) {
-              sh.weight = fmax(sh.weight - left, 0.0);
-              sh.tried[sh.tries++] = x;
-              sh.bloom |= 1ull << ((x >> 3) & 63);
-            }
-          }
-          if (chosen >= 0 && a.logprob) sh.logprob[depth] = (float)((double)(GREEDY ? sh.mt : sh.xt[chosen]) - sh.mt - log(sh.st));
-          sh.chosen = chosen;
-          sh.again = pass;
-          if (DRAFT) sh.factor = sh.sd > 0.0 ? (float)(sh.less * sh.st / sh.sd) : 0.0f;
-        }
-        __syncthreads();
-        chosen = sh.chosen;
-        if (!DRAFT || !sh.again) break;
-        // the weight of max(p - less q, 0)
-        float sum = 0.0f;
-        const float mt = sh.mt, md = sh.md, factor = sh.factor;
-        each_element<DT, DRAFT, false>(a, team, t, d, true, nullptr, [&](int, float x, float y, float) {
-          const float e = x > -INFINITY ? exp_fast(x - mt) : 0.0f, g = y > -INFINITY ? exp_fast(y - md) : 0.0f;
-          sum += fmaxf(fmaf(-factor, g, e), 0.0f);
-        });
-        sum = warp_sum(sum);
-        hand_out(team, sh, make_float4(sum, 0.0f, 0.0f, 0.0f));
+      __syncthreads();
+      if (!DRAFT || sh.state != kPass) break;
+      // the weight of what is left: the sum of max(p - a q, 0)
+      const float sum = warp_sum(weigh<DT>(a, team, target(sh.node), draft(sh.node), sh.mt, sh.md, sh.factor));
+      hand_out(team, sh, 0, (int)team.rank * kVW + warp, make_float4(sum, 0.0f, 0.0f, 0.0f));
+      team_sync(team);
+    }
+    if (sh.state == kGo) continue;
+    // the draw, from what is left; from the whole where nothing is
+    if (GREEDY) {
+      if (tid == 0) sh.token = sh.top;
+    } else {
+      float factor = DRAFT ? sh.factor : 0.0f;
+      int tries = sh.tries;
+      for (int round = 0;; ++round) {
+        unsigned long long best =
+            draw<DT, MODE>(a, team, sh, target(sh.node), draft(sh.node), a.race + (blockIdx.x / a.cs) * a.ld_race, factor, tries);
+        hand_out(team, sh, 0, (int)team.rank * kVW + warp, make_float4(__uint_as_float((uint32_t)best), __uint_as_float((uint32_t)(best >> 32)), 0.0f, 0.0f));
         team_sync(team);
         if (warp == 0) {
-          double w = 0.0;
-          for (int i = lane; i < a.cs * kVW; i += 32) w += (double)sh.part[team.at][i].x;
-          w = warp_sum(w);
-          if (lane == 0) sh.weight = w / sh.st;
+          best = 0ull;
+          for (int i = lane; i < a.cs * kVW; i += 32) {
+            const float4 v = sh.part[team.at][0][i];
+            const unsigned long long c = (unsigned long long)__float_as_uint(v.y) << 32 | __float_as_uint(v.x);
+            best = c > best ? c : best;
+          }
+          best = warp_max(best);
+          if (lane == 0) {
+            sh.best = best;
+            sh.token = best ? (int)~(uint32_t)best : -1;
+          }
         }
         team.at ^= 1;
         __syncthreads();
-      }
-      if (chosen >= 0) {
-        node = chosen;
-        ++depth;
-        if (tid == 0) sh.path[depth] = node;
+        if (sh.best || round || (factor == 0.0f && tries == 0)) break;
+        factor = 0.0f;
+        tries = 0;
         __syncthreads();
-        continue;
       }
-      // the draw, from what is left; from the whole where nothing is
-      if (GREEDY) {
-        token = (int)(long long)sh.best;
-      } else {
-        const float* race = a.race + b * a.ld_race;
-        const float mt = sh.mt, md = sh.md, eps = a.eps;
-        float factor = DRAFT ? sh.factor : 0.0f;
-        unsigned long long bloom = sh.bloom;
-        const int tries = sh.tries;
-        for (int round = 0;; ++round) {
-          unsigned long long best = 0ull;
-          const bool less = DRAFT && factor > 0.0f;
-          each_element<DT, DRAFT, true>(a, team, t, d, less, race, [&](int i, float x, float y, float variate) {
-            float e = x > -INFINITY ? exp_one(x, mt) : 0.0f;
-            if (less && y > -INFINITY) e = fmaxf(fmaf(-factor, exp_one(y, md), e), 0.0f);
-            if (!DRAFT && (bloom >> ((i >> 3) & 63) & 1))
-              for (int k = 0; k < tries; ++k)
-                if (sh.tried[k] == i) e = 0.0f;
-            if (e > 0.0f) {
-              const unsigned long long c = candidate(__fdiv_rn(e, variate + eps), i);
-              best = c > best ? c : best;
-            }
-          });
-          best = warp_max(best);
-          hand_out(team, sh, make_float4(__uint_as_float((uint32_t)best), __uint_as_float((uint32_t)(best >> 32)), 0.0f, 0.0f));
-          team_sync(team);
-          if (warp == 0) {
-            best = 0ull;
-            for (int i = lane; i < a.cs * kVW; i += 32) {
-              const float4 v = sh.part[team.at][i];
-              const unsigned long long c = (unsigned long long)__float_as_uint(v.y) << 32 | __float_as_uint(v.x);
-              best = c > best ? c : best;
-            }
-            best = warp_max(best);
-            if (lane == 0) sh.best = best;
-          }
-          team.at ^= 1;
-          __syncthreads();
-          if (sh.best || round || (factor == 0.0f && bloom == 0ull)) break;
-          factor = 0.0f;
-          bloom = 0ull;
-          __syncthreads();
-        }
-        token = sh.best ? (int)~(uint32_t)sh.best : -1;
-      }
-      if (tid == 0 && a.logprob && token >= 0)
-        sh.logprob[depth] = (float)((double)DType<DT>::to_float(t[token]) - sh.mt - log(sh.st));
-      break;
-    }
-    __syncthreads();
-  }
-  if (team.rank == 0) {
-    if (tid < a.T) {
-      a.path[b * a.T + tid] = sh.path[tid];
-      if (a.logprob) a.logprob[b * a.T + tid] = sh.logprob[tid];
     }
     if (tid == 0) {
-      a.count[b] = n > 0 ? depth + 1 : 0;
-      a.token[b] = token;
+      const int token = sh.token;
+      sh.gap[sh.depth] = token >= 0 ? DType<DT>::to_float(target(sh.node)[token]) - sh.mt : 0.0f;
+      sh.sum[sh.depth] = token >= 0 ? sh.st : 1.0f;
+    }
+    __syncthreads();
+    break;
+  }
+  if (team.rank == 0) {
+    const int64_t b = blockIdx.x / a.cs;
+    if (tid < a.T) {
+      a.path[b * a.T + tid] = sh.path[tid];
+      if (a.logprob) a.logprob[b * a.T + tid] = sh.n > 0 && tid <= sh.depth ? sh.gap[tid] - logf(sh.sum[tid]) : 0.0f;
+    }
+    if (tid == 0) {
+      a.count[b] = sh.n > 0 ? sh.depth + 1 : 0;
+      a.token[b] = sh.token;
     }
   }
   // none leaves while another may still write into its memory
@@ -570,13 +800,23 @@ cudaError_t launch_dt(const VerifyArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// CTAs of a request: as many as two an SM allow, but none with fewer than
-// 256 vectors of a row.
-int verify_cluster(int64_t B, int64_t V, int esize, int num_sms) {
+// CTAs of a request: as many as two an SM allow, but none with fewer than 256
+// vectors of a row, and 16 (whose barriers take longer) only while they leave
+// half the SMs alone: 4 requests of 128256 bf16 17.5 us with 16 and 19.6 with
+// 8, 16 requests 31.3 and 25.7; 64 requests 48 with 4, 60 with 8, 55 with 2.
+//
+// Nodes of a step, ahead of what is known to be accepted: with the draft's
+// probabilities most children are, so four, unless a node's rows alone keep
+// DRAM busy (128 x 152064 fp32: one 158 us, four 168; 64 chains over 128256
+// bf16: one 57.5, four 48; one request of 32000 fp16 19.8 and 13.4); two where
+// children are certain or greedy, which fewer are (64 x 128256 bf16, greedy:
+// one 19.6, two 17.5, four 20.0).
+void verify_plan(int64_t B, int64_t V, int esize, bool draft, int num_sms, int* cs, int* ahead) {
   const int64_t vectors = (V * esize + 15) / 16;
-  int cs = 1;
-  while (cs < 16 && B * cs * 2 <= 2LL * num_sms && vectors >= 256LL * cs * 2) cs *= 2;
-  return cs;
+  *cs = 1;
+  while (*cs < 16 && B * *cs * 2 <= (*cs == 8 ? num_sms / 2 : 2LL * num_sms) && vectors >= 256LL * *cs * 2) *cs *= 2;
+  const int64_t bytes = B * V * esize * (draft ? 2 : 1);
+  *ahead = bytes > 64 << 20 ? 1 : draft ? kAhead : 2;
 }
 
 cudaError_t launch_verify(topkp_dtype dt, const VerifyArgs& a, cudaStream_t s) {

@@ -109,6 +109,10 @@ cudaError_t launch_verify(topkp_dtype dt, const VerifyArgs& a, cudaStream_t s);
 constexpr int kPageStates = 128;  // per launch (the descriptors travel as kernel parameters)
 constexpr int kForkThreads = 1024, kForkCtas = 8;
 
+struct Reciprocal {
+  uint32_t mul;  // 0: divide by 1
+  int32_t shift;
+};
 struct ForkArgs {
   const int32_t* table;
   const int32_t* lengths;
@@ -126,6 +130,7 @@ struct ForkArgs {
   int64_t ld, ld_out;
   int64_t pages;
   int32_t R, N, M, page_size, grow_all;
+  Reciprocal by_page, by_columns;  // set by the launcher
 };
 struct PageState {
   char* data;

@@ -54,98 +54,151 @@ __device__ __forceinline__ void all_sync() {
   cluster_sync_all();
 }
 
+__device__ __forceinline__ int divided(uint32_t x, const Reciprocal& r) { return r.mul ? (int)(__umulhi(x, r.mul) >> r.shift) : (int)x; }
+
 // What a new row takes over and asks for.
 struct Taken {
-  int source;  // old row, or -1
-  int full;    // whole pages
-  int part;    // tokens of the last page, where it is partly filled
-  int last;    // that page, or -1
-  int need;    // pages the row will have
+  int source;     // old row
+  int full;       // whole pages
+  int last;       // the partly filled page behind them; -1: none, -2: an entry that holds nothing
+  int need;       // pages the row will have
 };
 __device__ __forceinline__ int clamped_length(const ForkArgs& a, int row) {
   const long long cap = (long long)a.M * a.page_size;
   return (int)min((long long)max(a.lengths[row], 0), cap);
 }
-__device__ __forceinline__ Taken take(const ForkArgs& a, int n) {
+__device__ __forceinline__ Taken take(const ForkArgs& a, int n, int* part) {
   Taken t;
   const int s = a.source[n];
-  t.source = s >= 0 && s < a.R ? s : -1;
-  const int len = t.source < 0 ? 0 : clamped_length(a, s);
-  t.full = len / a.page_size;
-  t.part = len - t.full * a.page_size;
+  const int grow = max(a.grow ? a.grow[n] : a.grow_all, 0);
+  const bool in = s >= 0 && s < a.R;
+  t.source = in ? s : -1;
+  const int len = in ? clamped_length(a, s) : 0;
+  t.full = divided(len, a.by_page);
+  *part = len - t.full * a.page_size;
   t.last = -1;
-  if (t.part) {
+  if (*part) {
     const int g = a.table[(int64_t)s * a.ld + t.full];
-    if (g >= 0 && g < a.pages) t.last = g;
+    t.last = g >= 0 && g < a.pages ? g : -2;
   }
-  const long long want = (long long)len + max(a.grow ? a.grow[n] : a.grow_all, 0);
-  t.need = (int)min((long long)a.M, (want + a.page_size - 1) / a.page_size);
+  const int tokens = len + min(grow, a.M * a.page_size - len);
+  t.need = tokens ? divided(tokens - 1, a.by_page) + 1 : 0;
   return t;
 }
-// Whether row n goes on with its partly filled page: the first to claim it,
-// and nobody else holds it.
-__device__ __forceinline__ bool keeps(const ForkArgs& a, const Taken& t, int n) {
-  return t.last >= 0 && __ldcg(&a.claim[t.last]) == n && __ldcg(&a.hold[t.last]) == 0;
-}
 
-__global__ void __launch_bounds__(kForkThreads) fork_kernel(const __grid_constant__ ForkArgs a) {
-  extern __shared__ int fork_smem[];
-  int* children = fork_smem;       // [R] new rows of an old one
-  int* base = fork_smem + a.R;     // [N] the first of a row's fresh pages
+__global__ void __launch_bounds__(kForkThreads, 1) fork_kernel(const __grid_constant__ ForkArgs a) {
+  extern __shared__ int4 fork_smem[];
+  Taken* taken = reinterpret_cast<Taken*>(fork_smem);          // [N]
+  int* base = reinterpret_cast<int*>(fork_smem + a.N);         // [N] the first of a row's fresh pages; complemented if it is a copy
+  int* children = base + a.N;                                  // [R] new rows of an old one
+  int* whole = children + a.R;                                 // [R] whole pages of an old row
   __shared__ int ws[32], free_pages[kForkCtas];
   const int tid = threadIdx.x;
   const uint32_t rank = cluster_ctarank();
-  const int all = kForkThreads * kForkCtas, me = (int)rank * kForkThreads + tid;
+  constexpr int all = kForkThreads * kForkCtas;
+  const int me = (int)rank * kForkThreads + tid;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int64_t p = me; p < a.pages; p += all) {
     __stcg(&a.hold[p], a.refs[p]);
     __stcg(&a.claim[p], INT_MAX);
   }
-  for (int r = tid; r < a.R; r += kForkThreads) children[r] = 0;
+  for (int r = tid; r < a.R; r += kForkThreads) {
+    children[r] = 0;
+    whole[r] = divided(clamped_length(a, r), a.by_page);
+  }
   __syncthreads();
+  // every CTA looks at every new row: rather than wait for another's answer
   for (int n = tid; n < a.N; n += kForkThreads) {
-    const int s = a.source[n];
-    if (s >= 0 && s < a.R) atomicAdd(&children[s], 1);
+    int part;
+    const Taken t = take(a, n, &part);
+    taken[n] = t;
+    base[n] = part;
+    if (t.source >= 0) atomicAdd(&children[t.source], 1);
   }
   all_sync();
-  // what the old rows held goes, what the new ones share comes
+  // what the old rows held goes, what the new ones share comes; several
+  // entries a thread at once
   const int entries = a.R * a.M;
-  for (int x = me; x < entries; x += all) {
-    const int r = x / a.M, i = x - r * a.M;
-    const int p = a.table[(int64_t)r * a.ld + i];
-    if (p < 0 || p >= a.pages) continue;
-    const int change = (i < clamped_length(a, r) / a.page_size ? children[r] : 0) - 1;
-    if (change) atomicAdd(&a.hold[p], change);
+  for (int x0 = me; x0 < entries; x0 += 4 * all) {
+    int p[4], change[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int x = x0 + k * all;
+      p[k] = -1;
+      change[k] = 0;
+      if (x < entries) {
+        const int r = divided(x, a.by_columns), i = x - r * a.M;
+        p[k] = a.table[(int64_t)r * a.ld + i];
+        change[k] = (i < whole[r] ? children[r] : 0) - 1;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (change[k] && p[k] >= 0 && p[k] < a.pages) atomicAdd(&a.hold[p[k]], change[k]);
   }
-  for (int n = me; n < a.N; n += all) {
-    const Taken t = take(a, n);
-    if (t.last >= 0) atomicMin(&a.claim[t.last], n);
-  }
+  for (int n = me; n < a.N; n += all)
+    if (taken[n].last >= 0) atomicMin(&a.claim[taken[n].last], n);
   all_sync();
-  // every row's demand, and the free pages of this CTA's part of the pool
+  // the free pages of this CTA's part of the pool, ranked: a thread four pages
+  const int64_t per = ((a.pages + kForkCtas - 1) / kForkCtas + 3) / 4 * 4;
+  const int64_t first = min(per * (int64_t)rank, a.pages), last = min(first + per, a.pages);
+  int h[4];
+  uint32_t free4 = 0, kept4 = 0;  // bit k: of page k
+  auto look = [&](int64_t p) {
+    // (both arrays go on to a multiple of 256 bytes)
+    const int4 x = p < last ? __ldcg(reinterpret_cast<const int4*>(a.hold + p)) : make_int4(1, 1, 1, 1);
+    const int4 y = p < last ? __ldcg(reinterpret_cast<const int4*>(a.claim + p)) : make_int4(0, 0, 0, 0);
+    const int c[4] = {y.x, y.y, y.z, y.w};
+    h[0] = x.x, h[1] = x.y, h[2] = x.z, h[3] = x.w;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (p + k >= last) h[k] = 1;
+    free4 = kept4 = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      free4 |= (uint32_t)(h[k] == 0 && c[k] == INT_MAX) << k;
+      kept4 |= (uint32_t)(h[k] == 0 && c[k] != INT_MAX) << k;
+    }
+  };
+  look(first + 4 * tid);
+  // Every row's demand.  A row goes on with its partly filled page if it is
+  // the first to claim it, and nobody else holds it.
   int total = 0;
   for (int n0 = 0; n0 < a.N; n0 += kForkThreads) {
     const int n = n0 + tid;
     int want = 0;
+    bool copy = false;
     if (n < a.N) {
-      const Taken t = take(a, n);
-      want = max(t.need - t.full - (t.part > 0), 0) + (t.last >= 0 && !keeps(a, t, n));
+      const Taken t = taken[n];
+      if (t.last >= 0) {
+        const int claim = __ldcg(&a.claim[t.last]), hold = __ldcg(&a.hold[t.last]);
+        copy = claim != n || hold != 0;
+      }
+      want = max(t.need - t.full - (t.last != -1), 0) + copy;
     }
     int sum;
-    const int before = scan(want, &sum, ws);
-    if (n < a.N) base[n] = total + before;
+    const int before = total + scan(want, &sum, ws);
     total += sum;
+    if (n < a.N) {
+      if (n % kForkCtas == (int)rank) a.copies[n] = make_int4(taken[n].last, before, copy ? base[n] : 0, 0);
+      base[n] = copy ? ~before : before;
+    }
   }
-  const int64_t per = ((a.pages + kForkCtas - 1) / kForkCtas + 3) / 4 * 4;
-  const int64_t first = min(per * (int64_t)rank, a.pages), last = min(first + per, a.pages);
-  int many = 0;
-  for (int64_t p = first + tid; p < last; p += kForkThreads) many += __ldcg(&a.hold[p]) == 0 && __ldcg(&a.claim[p]) == INT_MAX;
-  int here;
-  scan(many, &here, ws);
-  if (tid < kForkCtas) {
-    const uint32_t to = dsmem_addr(&free_pages[rank], (uint32_t)tid);
-    dsmem_st_u32(to, (uint32_t)here);
+  int here, sum, sum0;
+  int k0 = scan(__popc(free4), &sum0, ws);  // of the first chunk; further ones are only counted now
+  here = sum0;
+  for (int64_t p0 = first + 4 * kForkThreads; p0 < last; p0 += 4 * kForkThreads) {
+    const int h0 = h[0], h1 = h[1], h2 = h[2], h3 = h[3];
+    const uint32_t f = free4, g = kept4;
+    look(p0 + 4 * tid);
+    const int mine = __popc(free4);
+    scan(mine, &sum, ws);
+    here += sum;
+    h[0] = h0, h[1] = h1, h[2] = h2, h[3] = h3;
+    free4 = f;
+    kept4 = g;
   }
+  if (tid < kForkCtas) dsmem_st_u32(dsmem_addr(&free_pages[rank], (uint32_t)tid), (uint32_t)here);
   all_sync();
   int before = 0, most = 0;
   for (int c = 0; c < kForkCtas; ++c) {
@@ -154,66 +207,65 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const __grid_constan
   }
   const int lacking = max(total - most, 0);
   if (me == 0) a.missing[0] = lacking;
-  // ranks of the free pages, and the references as they will be
+  // the first `total` free pages are given out; the references as they will be
   for (int64_t p0 = first; p0 < last; p0 += 4 * kForkThreads) {
     const int64_t p = p0 + 4 * tid;
-    int h[4], mine = 0;
-    bool is_free[4], kept[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const bool in = p + k < last;
-      h[k] = in ? __ldcg(&a.hold[p + k]) : 1;
-      const bool claimed = in && __ldcg(&a.claim[p + k]) != INT_MAX;
-      is_free[k] = h[k] == 0 && !claimed;
-      kept[k] = h[k] == 0 && claimed;
-      mine += is_free[k];
+    if (p0 > first) {
+      look(p);
+      k0 = scan(__popc(free4), &sum0, ws);
     }
-    int sum;
-    int k0 = before + scan(mine, &sum, ws);
+    int rank_of = before + k0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if (p + k >= last) continue;
-      const bool given = is_free[k] && k0 < total;
-      if (given) __stcg(&a.fresh[k0], (int)(p + k));
-      k0 += is_free[k];
-      a.refs_out[p + k] = lacking ? a.refs[p + k] : h[k] + kept[k] + given;
+      const bool is_free = free4 >> k & 1, given = is_free && rank_of < total;
+      if (given) __stcg(&a.fresh[rank_of], (int)(p + k));
+      rank_of += is_free;
+      a.refs_out[p + k] = lacking ? a.refs[p + k] : h[k] + (int)(kept4 >> k & 1) + given;
     }
-    before += sum;
+    before += sum0;
   }
   all_sync();
-  // the new table, and the pages to copy
+  // the new table, and where copies go
   for (int n = me; n < a.N; n += all) {
-    const Taken t = take(a, n);
-    const bool copy = !lacking && t.last >= 0 && !keeps(a, t, n);
-    a.copies[n] = make_int4(t.last, copy ? __ldcg(&a.fresh[base[n]]) : -1, copy ? t.part : 0, 0);
+    // (written above by this cluster's CTA n mod 8: a release and acquire ago)
+    int4 c = __ldcg(&a.copies[n]);
+    if (lacking) c.z = 0;
+    if (c.z) c.y = __ldcg(&a.fresh[c.y]);
+    a.copies[n] = c;
   }
   const int slots = a.N * a.M;
-  for (int x = me; x < slots; x += all) {
-    const int n = x / a.M, i = x - n * a.M;
-    int p = -1;
-    if (!lacking) {
-      const Taken t = take(a, n);
-      if (i < t.full) {
-        p = a.table[(int64_t)t.source * a.ld + i];
-        if (p < 0 || p >= a.pages) p = -1;
-      } else {
-        const bool copy = t.last >= 0 && !keeps(a, t, n);
-        const int k = i - t.full - (t.part > 0);  // among the grown ones
-        if (k < 0) p = copy ? __ldcg(&a.fresh[base[n]]) : t.last;
-        else if (i < t.need) p = __ldcg(&a.fresh[base[n] + copy + k]);
+  for (int x0 = me; x0 < slots; x0 += 4 * all) {
+    int p[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int x = x0 + k * all;
+      p[k] = -1;
+      if (x < slots && !lacking) {
+        const int n = divided(x, a.by_columns), i = x - n * a.M;
+        const Taken t = taken[n];
+        const int b = base[n], g = i - t.full - (t.last != -1);  // g: among the grown pages
+        if (i < t.full) p[k] = a.table[(int64_t)t.source * a.ld + i];
+        else if (g < 0) p[k] = b < 0 ? __ldcg(&a.fresh[~b]) : t.last;
+        else if (i < t.need) p[k] = __ldcg(&a.fresh[b < 0 ? ~b + 1 + g : b + g]);
       }
     }
-    a.table_out[(int64_t)n * a.ld_out + i] = p;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int x = x0 + k * all;
+      if (x < slots) {
+        const int n = divided(x, a.by_columns), i = x - n * a.M;
+        a.table_out[(int64_t)n * a.ld_out + i] = p[k] >= 0 && p[k] < a.pages ? p[k] : -1;
+      }
+    }
   }
-  // no CTA leaves while another may still write its count here
-  all_sync();
 }
 
 // --------------------------------------------------------------------- copies
 constexpr int kCopyThreads = 256, kCopyDepth = 8;
 
 template <typename U>
-__device__ __forceinline__ void copy_units(const PageState& st, const int4& c, int chunks) {
+__device__ __noinline__ void copy_blocks(const PageState& st, const int4& c, int chunks) {
   const int64_t live = (int64_t)c.z * st.entry_bytes / (int64_t)sizeof(U);  // of a block
   const int64_t total = live * st.blocks;
   const char* src = st.data + c.x * st.page_stride;
@@ -233,7 +285,26 @@ __device__ __forceinline__ void copy_units(const PageState& st, const int4& c, i
       if (i0 + k * kCopyThreads < total) *reinterpret_cast<U*>(dst + at[k]) = r[k];
   }
 }
-__global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const __grid_constant__ CopyArgs a) {
+template <typename U>
+__device__ __forceinline__ void copy_units(const PageState& st, const int4& c, int chunks) {
+  if (st.blocks == 1 && (int64_t)c.z * st.entry_bytes <= INT_MAX / 2) {  // the usual page: bytes one after another
+    const U* from = reinterpret_cast<const U*>(st.data + c.x * st.page_stride);
+    U* to = reinterpret_cast<U*>(st.data + c.y * st.page_stride);
+    const int n = (int)(c.z * st.entry_bytes / (int64_t)sizeof(U));
+    for (int i = blockIdx.x * (kCopyThreads * kCopyDepth) + threadIdx.x; i < n; i += chunks * (kCopyThreads * kCopyDepth)) {
+      U r[kCopyDepth];
+#pragma unroll
+      for (int k = 0; k < kCopyDepth; ++k)
+        if (i + k * kCopyThreads < n) r[k] = from[i + k * kCopyThreads];
+#pragma unroll
+      for (int k = 0; k < kCopyDepth; ++k)
+        if (i + k * kCopyThreads < n) to[i + k * kCopyThreads] = r[k];
+    }
+    return;
+  }
+  copy_blocks<U>(st, c, chunks);
+}
+__global__ void __launch_bounds__(kCopyThreads, 4) page_copy_kernel(const __grid_constant__ CopyArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 c = a.copies[blockIdx.y];
   if (c.z <= 0) return;
@@ -323,15 +394,29 @@ int64_t widest(const PageState* st, int count, int64_t entries) {
 
 }  // namespace
 
+static_assert(7 * TOPKP_MAX_ROWS * sizeof(int) <= 226 * 1024, "the rows do not fit shared memory");
+// x / d = (x * mul) >> (32 + shift), exact for x below 2^31
+Reciprocal reciprocal(int64_t d) {
+  if (d <= 1) return {0u, 0};
+  int l = 1;
+  while ((1LL << l) < d) ++l;
+  return {(uint32_t)(((1ull << (31 + l)) + d - 1) / d), l - 1};
+}
+
 size_t fork_workspace(int64_t N, int64_t pages) {
   const size_t p = ((size_t)pages * sizeof(int32_t) + 255) / 256 * 256;
   return 3 * p + ((size_t)N * sizeof(int4) + 255) / 256 * 256;
 }
 
 cudaError_t launch_fork(const ForkArgs& a, cudaStream_t s) {
-  const size_t smem = ((size_t)a.R + a.N) * sizeof(int);
-  const cudaError_t e = cudaFuncSetAttribute(fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * TOPKP_MAX_ROWS * (int)sizeof(int));
-  if (e != cudaSuccess) return e;
+  ForkArgs b = a;
+  b.by_page = reciprocal(a.page_size);
+  b.by_columns = reciprocal(a.M);
+  const size_t smem = (size_t)a.R * 2 * sizeof(int) + (size_t)a.N * 5 * sizeof(int);
+  if (smem > 40 << 10) {  // beyond what a kernel has unasked
+    const cudaError_t e = cudaFuncSetAttribute(fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 7 * TOPKP_MAX_ROWS * (int)sizeof(int));
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kForkCtas);
   cfg.blockDim = dim3(kForkThreads);
@@ -343,7 +428,7 @@ cudaError_t launch_fork(const ForkArgs& a, cudaStream_t s) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fork_kernel, a);
+  return cudaLaunchKernelEx(&cfg, fork_kernel, b);
 }
 
 // The copies' launch overlaps the bookkeeping (or the states before); they

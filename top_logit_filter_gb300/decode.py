@@ -37,12 +37,11 @@ _CACHE = struct.Struct("=QQi4x6q")
 _STATE = struct.Struct("=QQ7q")
 _ATTENTION = struct.Struct("=QQQ" + 2 * "QQi4x6q" + "QQQQQQ16qif")
 _VERIFY = struct.Struct("=11Q8qif")
-_PAGES = struct.Struct("=Q4q")
 _FORK = struct.Struct("=11Q9q")
 assert _CACHE.size == _lib.ctypes.sizeof(_lib.Cache) and _STATE.size == _lib.ctypes.sizeof(_lib.State)
 assert _ATTENTION.size == _lib.ctypes.sizeof(_lib.TreeAttentionArgs)
 assert _VERIFY.size == _lib.ctypes.sizeof(_lib.DraftVerifyArgs)
-assert _PAGES.size == _lib.ctypes.sizeof(_lib.Pages) and _FORK.size == _lib.ctypes.sizeof(_lib.CacheForkArgs)
+assert struct.calcsize("=Q4q") == _lib.ctypes.sizeof(_lib.Pages) and _FORK.size == _lib.ctypes.sizeof(_lib.CacheForkArgs)
 
 
 def _ready():
@@ -458,71 +457,90 @@ def draft_verify(target, tokens, uniform=None, race=None, draft=None, parent=Non
     ``want_logprob`` logprob [B, T] float32: log-probabilities of the
     path's tokens behind node 0's, then of the drawn one."""
     lib = _ready()
-    _cuda(target, "target", 3)
-    dt, dev = _dtype_code(target), target.device
+    if not isinstance(target, torch.Tensor) or not target.is_cuda or target.dim() != 3:
+        raise ValueError("target must be a 3-D CUDA tensor")
+    dt, dev = _CODES.get(target.dtype), target.device
+    if dt is None:
+        raise TypeError(f"unsupported dtype {target.dtype} (float32, float16 or bfloat16)")
     B, T, V = target.shape
-    if V > 1 and target.stride(2) != 1:
+    ts = target.stride()
+    if ts[2] != 1 and V > 1:
         target = target.contiguous()
+        ts = target.stride()
     ds = (0, 0)
     if draft is not None:
         _cuda(draft, "draft", 3, target.dtype, dev)
         if draft.shape != target.shape:
             raise ValueError(f"draft is {tuple(draft.shape)} and target {tuple(target.shape)}")
-        if V > 1 and draft.stride(2) != 1:
-            draft = draft.contiguous()
         ds = draft.stride()
+        if ds[2] != 1 and V > 1:
+            draft = draft.contiguous()
+            ds = draft.stride()
     if (uniform is None) != (race is None):
         raise ValueError("uniform and race go together")
     if uniform is None and draft is not None:
         raise ValueError("draft goes with uniform and race")
-    many = [tokens, parent, uniform]
-    for i, (name, dtype) in enumerate((("tokens", torch.int32), ("parent", torch.int32), ("uniform", torch.float32))):
-        t = many[i]
-        if t is None and i:
-            continue
-        _cuda(t, name, 2, dtype, dev)
-        if t.shape != (B, T):
-            raise ValueError(f"{name} must be {(B, T)}, not {tuple(t.shape)}")
-        many[i] = t.contiguous()
+    tokens = _of_nodes(tokens, torch.int32, "tokens", B, T, dev)
+    if parent is not None:
+        parent = _of_nodes(parent, torch.int32, "parent", B, T, dev)
+    ld = V
     if race is not None:
+        uniform = _of_nodes(uniform, torch.float32, "uniform", B, T, dev)
         _cuda(race, "race", 2, torch.float32, dev)
         if race.shape != (B, V):
             raise ValueError(f"race must be {(B, V)}, not {tuple(race.shape)}")
-        if V > 1 and race.stride(1) != 1 or B > 1 and race.stride(0) < V:
+        ld, one = race.stride()
+        if V > 1 and one != 1 or B > 1 and ld < V:
             race = race.contiguous()
-    nodes = _vec(nodes, B, torch.int32, "nodes", dev)
-    out = torch.empty((B, T + 2), dtype=torch.int32, device=dev) if B == 1 else None
-    if out is not None:  # one allocation for a single request, whose call is all latency
-        count, token, path = out[0, :1], out[0, 1:2], out[:, 2:]
-    else:
-        count, token = torch.empty((2, B), dtype=torch.int32, device=dev)
-        path = torch.empty((B, T), dtype=torch.int32, device=dev)
+            ld = V
+        if B <= 1:
+            ld = V
+    if nodes is not None:
+        nodes = _vec(nodes, B, torch.int32, "nodes", dev)
+    count, token = torch.empty(B, dtype=torch.int32, device=dev), torch.empty(B, dtype=torch.int32, device=dev)
+    path = torch.empty((B, T), dtype=torch.int32, device=dev)
     logprob = torch.empty((B, T), dtype=torch.float32, device=dev) if want_logprob else None
-    ts = target.stride()
-    args = _VERIFY.pack(_ptr(target), _ptr(draft), *map(_ptr, (many[0], many[1], nodes, many[2], race, count, path, token, logprob)),
-                        B, T, V, ts[0], ts[1] if T > 1 else V, ds[0], ds[1] if T > 1 else V,
-                        V if race is None or B <= 1 else race.stride(0), dt, float(eps))
+    args = _VERIFY.pack(_ptr(target), _ptr(draft), _ptr(tokens), _ptr(parent), _ptr(nodes), _ptr(uniform), _ptr(race), _ptr(count),
+                        _ptr(path), _ptr(token), _ptr(logprob), B, T, V, ts[0], ts[1] if T > 1 else V, ds[0], ds[1] if T > 1 else V,
+                        ld, dt, eps)
     _launch(dev, lib.topkp_draft_verify, args)
     return (count, path, token, logprob) if want_logprob else (count, path, token)
 
 
-def _page_states(states, time_dim, dev, pages=None, page_size=None):
+def _of_nodes(t, dtype, name, B, T, device):
+    """A tensor with an entry for each node of each request."""
+    if not isinstance(t, torch.Tensor) or t.device != device or t.shape != (B, T):
+        raise ValueError(f"{name} must be a {(B, T)} tensor on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    return t.contiguous()
+
+
+_PACKERS = {}   # by the number of states: their descriptors in one piece
+
+
+def _page_states(states, time_dim, dev):
     """(tensors, packed descriptors, pages, page size) of a sequence of tensors of pages."""
-    many = [states] if torch.is_tensor(states) else list(states)
-    packed = []
+    many = [states] if isinstance(states, torch.Tensor) else list(states)
+    values, like, pages, page_size = [], None, None, None
     for i, t in enumerate(many):
         if not isinstance(t, torch.Tensor) or t.device != dev:
             raise ValueError(f"states[{i}] must be a CUDA tensor on {dev}")
-        if t.dim() < 2 or not 1 <= time_dim < t.dim():
-            raise ValueError(f"states[{i}] must be [pages, page_size, ...] with its tokens along dimension {time_dim}")
         shape = t.shape
-        if pages is None:
-            pages, page_size = shape[0], shape[time_dim]
-        if shape[0] != pages or shape[time_dim] != page_size:
-            raise ValueError(f"states[{i}] has {shape[0]} pages of {shape[time_dim]} tokens, others {pages} of {page_size}")
-        row, blk, blocks, _, size = _layout(t, time_dim, "a state")
-        packed.append(_PAGES.pack(_ptr(t), row, blk, blocks, size))
-    return many, b"".join(packed), pages, page_size
+        # layers of one shape lie alike
+        if shape != like or t.dtype is not kind or not t.is_contiguous():
+            if len(shape) < 2 or not 1 <= time_dim < len(shape):
+                raise ValueError(f"states[{i}] must be [pages, page_size, ...] with its tokens along dimension {time_dim}")
+            if pages is None:
+                pages, page_size = shape[0], shape[time_dim]
+            if shape[0] != pages or shape[time_dim] != page_size:
+                raise ValueError(f"states[{i}] has {shape[0]} pages of {shape[time_dim]} tokens, others {pages} of {page_size}")
+            row, blk, blocks, _, size = _layout(t, time_dim, "a state")
+            like, kind = (shape, t.dtype) if t.is_contiguous() else (None, None)
+        values += (t.data_ptr() or 16, row, blk, blocks, size)
+    n = len(many)
+    pack = _PACKERS.get(n) or _PACKERS.setdefault(n, struct.Struct("=" + "Q4q" * n).pack)
+    return many, pack(*values), pages, page_size
 
 
 def cache_fork(states, pages, lengths, source, refs, grow=0, time_dim: int = 1, out=None, refs_out=None, workspace=None):
@@ -577,7 +595,8 @@ def cache_fork(states, pages, lengths, source, refs, grow=0, time_dim: int = 1, 
         raise ValueError(f"out must be a {(N, M)} int32 tensor on {dev} with contiguous rows")
     missing = torch.empty((1,), dtype=torch.int32, device=dev)
     workspace = _workspace(workspace, int(lib.topkp_cache_fork_workspace_size(N, pool)), dev)
-    args = _FORK.pack(_lib.ctypes.cast(_lib.ctypes.c_char_p(packed), _lib.ctypes.c_void_p).value or 0, _ptr(pages), _ptr(lengths),
+    held = _lib.ctypes.c_char_p(packed)  # keeps the descriptors where the call reads them
+    args = _FORK.pack(_lib.ctypes.cast(held, _lib.ctypes.c_void_p).value, _ptr(pages), _ptr(lengths),
                       _ptr(source), _ptr(grow), _ptr(refs), _ptr(out), _ptr(refs_out), _ptr(missing), _ptr(workspace),
                       workspace.numel(), len(many), R, N, M, pages.stride(0) if R > 1 else M, out.stride(0) if N > 1 else M, pool,
                       page_size, grow_all)

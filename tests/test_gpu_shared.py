@@ -56,8 +56,11 @@ def build_case(dtype, cache, shared, size, own, T, Hkv, D, P, seed, nodes=None, 
 
 
 def attend(tk, dtype, cache, shared, size, own, T, Hq, Hkv, D, P, tree=None, nodes=None, seed=0, say=None, scale=None, launches=None,
-           max_context=None, max_shared=None, qview=False, spread=0.0):
+           max_context=None, max_shared=None, qview=False, spread=0.0, capacity=0):
+    """capacity: of the table, beyond the live tokens; with it bounds may be given that make the call plan for much longer ones."""
     g, B, contexts, table, store, exps = build_case(dtype, cache, shared, size, own, T, Hkv, D, P, seed, nodes, spread)
+    if capacity > table.shape[1] * P:
+        table = torch.cat([table, torch.full((B, -(-capacity // P) - table.shape[1]), -1, dtype=torch.int32)], 1)
     quant = cache == "e4m3"
     q = (1.2 * torch.randn(B, T, Hq, D, generator=g)).to(T_[dtype])
     bits, words = (None, None) if tree is None else tree
@@ -102,11 +105,13 @@ def attend(tk, dtype, cache, shared, size, own, T, Hq, Hkv, D, P, tree=None, nod
 def test_one_prefix(tk, dtype, cache, size, T, Hq, Hkv, D, P):
     g = torch.Generator().manual_seed(size)
     own = torch.randint(0, 90, (size,), generator=g).tolist()
-    attend(tk, dtype, cache, [1500], size, own, T, Hq, Hkv, D, P, seed=1, max_context=1600, max_shared=1500,
-           launches=3 if size >= 30 else None)
+    attend(tk, dtype, cache, [1500], size, own, T, Hq, Hkv, D, P, seed=1, max_context=1600, max_shared=1500)
+    # planned as if they were far longer: the grouped kernels, in several parts each
+    for bound in (40000, 120000):
+        attend(tk, dtype, cache, [1500], size, own, T, Hq, Hkv, D, P, seed=1, max_context=bound, max_shared=bound - 500, capacity=bound, launches=3)
     if T > 1:
-        attend(tk, dtype, cache, [1111], size, own, T, Hq, Hkv, D, P, tree=make_tree(size, T, 2), seed=2, max_context=1250, max_shared=1111,
-               qview=True)
+        attend(tk, dtype, cache, [1111], size, own, T, Hq, Hkv, D, P, tree=make_tree(size, T, 2), seed=2, max_context=60000, max_shared=59000,
+               qview=True, capacity=60000, launches=3)
 
 
 @pytest.mark.parametrize("cache", ["own", "e4m3"])
@@ -116,18 +121,23 @@ def test_ragged_groups_and_requests(tk, cache):
     nodes = [3, 0, 1, 2, 3, 3] * 5
     for D in (64, 128):
         # shared lengths around a tile's, and none; requests without nodes
-        attend(tk, "bf16", cache, [0, 63, 64, 65, 1000, 129], size, own * 6, 3, 4, 2, D, 16, nodes=nodes * 6, seed=3, max_shared=1000)
+        attend(tk, "bf16", cache, [0, 63, 64, 65, 1000, 129], size, own * 6, 3, 4, 2, D, 16, nodes=nodes * 6, seed=3, max_shared=39000,
+               capacity=40000, launches=3)
     # a request that has no node and a short context of its own does not shorten the prefix of the others, nor read past it
-    attend(tk, "bf16", cache, [900], size, own, 3, 4, 2, 128, 16, nodes=nodes, seed=4, launches=3, max_context=1100, max_shared=900)
+    attend(tk, "bf16", cache, [900], size, own, 3, 4, 2, 128, 16, nodes=nodes, seed=4, launches=3, max_context=40000, max_shared=39000,
+           capacity=40000)
 
 
 def test_any_bound_of_what_is_shared(tk):
     own = [5 * i % 97 for i in range(48)]
     for say in ([700], [640], [639], [1], [0], [-5], [704 - 1]):
-        attend(tk, "bf16", "own", [700], 48, own, 1, 4, 1, 128, 16, say=say, seed=5, max_context=800, max_shared=700)
+        attend(tk, "bf16", "own", [700], 48, own, 1, 4, 1, 128, 16, say=say, seed=5, max_context=60000, max_shared=59000,
+               capacity=60000, launches=3)
     # too much is cut to the shortest context (equal contents up to there)
-    attend(tk, "bf16", "own", [704], 48, [0] + own[1:], 1, 4, 1, 128, 64, say=[704], seed=6, max_context=900, max_shared=704)
-    attend(tk, "bf16", "own", [704], 48, [0] * 48, 1, 4, 1, 128, 64, say=[10 ** 9], seed=6, max_context=900, max_shared=704)
+    attend(tk, "bf16", "own", [704], 48, [0] + own[1:], 1, 4, 1, 128, 64, say=[704], seed=6, max_context=60000, max_shared=59000,
+           capacity=60000, launches=3)
+    attend(tk, "bf16", "own", [704], 48, [0] * 48, 1, 4, 1, 128, 64, say=[10 ** 9], seed=6, max_context=60000, max_shared=59000,
+           capacity=60000, launches=3)
     # wrong bounds plan badly and change nothing
     attend(tk, "bf16", "own", [2000], 48, own, 1, 4, 1, 128, 16, seed=7, max_context=128, max_shared=128)
     attend(tk, "bf16", "own", [300], 48, own, 1, 4, 1, 128, 16, seed=8)
@@ -135,7 +145,7 @@ def test_any_bound_of_what_is_shared(tk):
 
 def test_extremes(tk):
     own = [7 * i % 50 for i in range(40)]
-    kw = dict(seed=9, max_context=1100, max_shared=1000)
+    kw = dict(seed=9, max_context=60000, max_shared=59000, capacity=60000, launches=3)
     attend(tk, "bf16", "own", [1000], 40, own, 1, 8, 2, 128, 16, scale=8.0, **kw)
     attend(tk, "f16", "e4m3", [1000], 40, own, 2, 8, 2, 128, 16, spread=1.0, **kw)
     attend(tk, "bf16", "own", [1000], 40, own, 1, 8, 2, 128, 16, scale=0.0, **kw)
@@ -153,8 +163,9 @@ def test_workspace_streams_and_graph(tk):
     k, v = (x.cuda() for x in store)
     ctx, table = torch.tensor(contexts, dtype=torch.int32).cuda(), table.cuda()
     shared = torch.tensor([800, 1000], dtype=torch.int32).cuda()
-    kw = dict(max_context=1120, max_shared=1000, want_lse=True)
-    need = tk.shared_attention_workspace_size(q, k, table, 2, max_context=1120, max_shared=1000)
+    table = torch.cat([table, torch.full((B, 3000), -1, dtype=torch.int32, device="cuda")], 1)    # (room that nobody uses yet)
+    kw = dict(max_context=40000, max_shared=39000, want_lse=True)
+    need = tk.shared_attention_workspace_size(q, k, table, 2, max_context=40000, max_shared=39000)
     want = tk.shared_attention(q, k, v, ctx, table, shared, **kw)
     assert tk.last_launch_count() == 3 and need > 0
     got = tk.shared_attention(q, k, v, ctx, table, shared, workspace=torch.empty(need, dtype=torch.uint8, device="cuda"), **kw)

@@ -1098,8 +1098,11 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH>::kThreads, TcShape
     }
     tc_fence_before();
   }
-  // a join that waits for this launch waits for the one before it, too
-  if (GROUPED && p.stage == 2) asm volatile("griddepcontrol.wait;" ::: "memory");
+  // A join that waits for this launch waits for the one before it, too: its
+  // last CTA does not end before that has.  (All of them waiting would hold
+  // the SMs that the rest of this launch is to run on.)
+  if (GROUPED && p.stage == 2 && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncwarp();
   __syncthreads();
   if (dead) {  // products and copies may still be in flight: time for them to end

@@ -127,7 +127,7 @@ bool make_map(CUtensorMap* map, const topkp_cache& c, const topkp_tree_attention
 
 template <bool GROUPED, int DP, int NT, bool BF, bool Q8, int SH = 1>
 cudaError_t launch_tc(AttnDev p, cudaStream_t s) {
-  using Shape = TcShape<DP, NT, BF, Q8, SH>;
+  using Shape = TcShape<GROUPED, DP, NT, BF, Q8, SH>;
   const topkp_tree_attention_args& a = p.a;
   cudaError_t e = cudaFuncSetAttribute(attn_tc<GROUPED, DP, NT, BF, Q8, SH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kSmem);
   if (e != cudaSuccess) return e;
@@ -171,10 +171,19 @@ bool few_rows(const topkp_tree_attention_args& a) {
   return a.k.dtype == TOPKP_E4M3 && a.D > 64 && a.D <= 128 && a.T * (a.Hq / a.Hkv) <= 32;
 }
 
+// Two warps to a row for 33 to 64 of them, where requests share a prefix.
+bool some_rows(const topkp_tree_attention_args& a) {
+  const int64_t rows = a.T * (a.Hq / a.Hkv);
+  return a.k.dtype == TOPKP_E4M3 && a.D > 64 && a.D <= 128 && rows > 32 && rows <= 64;
+}
+
 template <bool GROUPED, bool BF, bool Q8>
 cudaError_t launch_dim(const AttnDev& p, cudaStream_t s) {
   if constexpr (Q8) {
     if (few_rows(p.a)) return launch_tc<GROUPED, 128, 1, BF, true, 4>(p, s);
+    if constexpr (GROUPED) {
+      if (some_rows(p.a)) return launch_tc<GROUPED, 128, 1, BF, true, 2>(p, s);
+    }
   }
   const bool two = row_tiles(p.a) == 2;
   if (p.a.D <= 64) return two ? launch_tc<GROUPED, 64, 2, BF, Q8>(p, s) : launch_tc<GROUPED, 64, 1, BF, Q8>(p, s);

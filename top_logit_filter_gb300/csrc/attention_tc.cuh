@@ -183,15 +183,21 @@ __device__ __forceinline__ void softmax_barrier() { asm volatile("bar.sync 1, 12
 // SH warps share a row's tokens.  With up to 32 rows over e4m3 the four softmax
 // warps hold a copy of the rows each and take a quarter of every tile's tokens
 // (for O's product the others' are zeros); their O, maxima and sums are joined
-// at the end.
-template <int DP, int NT, bool BF, bool Q8, int SH>
+// at the end.  With up to 64 rows two pairs of warps take a half.
+template <bool GROUPED, int DP, int NT, bool BF, bool Q8, int SH>
 struct TcShape {
   static constexpr int kSoftWarps = 4 * NT;
   // 16 bits: one warp for keys, one for values; e4m3: one loads, the others widen
   // then bf16's 128 dims leave room for two CTAs an SM (64
   // single tokens of 64 query and 8 cache heads to 8000: 303 us, with one 318)
-  static constexpr bool kPair = SH == 4 && BF;
-  static constexpr int kFeedWarps = !Q8 ? 2 : NT == 2 ? 7 : kPair ? 5 : DP >= 128 ? 9 : 3;
+  static constexpr bool kPair = SH == 4 && BF && !GROUPED;
+  // Where there are registers for it, keys, values and their scales are brought
+  // by a warp each, and two groups of warps widen values in turn: a single
+  // loading warp, with the latency of its own instructions and loads, was what
+  // a tile waited for (1845 of 2107 cycles), then the widening (1300 of 1620).
+  static constexpr bool kSplit = Q8 && NT == 1 && DP >= 128 && !kPair;
+  static constexpr int kFeedWarps = !Q8 ? 2 : NT == 2 ? 7 : kPair ? 5 : DP >= 128 ? 11 : 3;
+  static constexpr int kWiden = kFeedWarps - (kSplit ? 3 : 1);  // warps that widen e4m3 values
   static constexpr int kThreads = 32 * (kSoftWarps + kFeedWarps + 1);
   // with a warp to a row two CTAs leave room for two warps that widen, enough for 64 dims only
   // (128 rows of 128 dims over e4m3: 258 us with two CTAs, 228 with one)
@@ -211,6 +217,10 @@ struct TcShape {
   static constexpr int kKeys = Q8 ? (kPair ? 3 : DP <= 128 ? 4 : 2) : DP == 64 || (DP == 128 && NT == 2) ? 4 : DP == 256 ? 3 : 2;
   static constexpr int kValues = !Q8 ? kKeys : kPair ? 2 : DP == 256 ? (BF ? 3 : 1) : DP == 128 && NT == 2 ? 2 : 3;
   static constexpr int kRaw = !Q8 ? 0 : DP == 256 || kPair ? 2 : 4;
+  // A group of warps widens every kGroups-th tile.  A wait on a stage's
+  // barrier must not pass by the phase before the one that it is for: the
+  // tiles between two uses of a stage see to that, so two groups need two stages.
+  static constexpr int kGroups = kSplit && kValues >= 2 ? 2 : 1;
   static constexpr uint32_t kQ = NT * 128;  // after two S of 64 columns a row tile
   static constexpr uint32_t kO = kQ + (kQInTmem ? NT * kQColumns : 0);
   static constexpr int kColumns = kO + NT * DP <= 256 ? 256 : 512;
@@ -344,11 +354,12 @@ __device__ __forceinline__ void e4m3_away(uint32_t two, float& x, float& y) {
 }
 
 template <bool GROUPED, int DP, int NT, bool BF, bool Q8, int SH>
-__global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH>::kThreads, TcShape<DP, NT, BF, Q8, SH>::kPerSm)
+__global__ void __launch_bounds__(TcShape<GROUPED, DP, NT, BF, Q8, SH>::kThreads, TcShape<GROUPED, DP, NT, BF, Q8, SH>::kPerSm)
     attn_tc(const __grid_constant__ AttnDev p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-  using Shape = TcShape<DP, NT, BF, Q8, SH>;
-  static_assert(SH == 1 || (SH == 4 && NT == 1 && DP == 128 && Q8), "a row's tokens go to one warp or to four");
-  constexpr int H = 32 / SH;  // half of a thread's columns of S
+  using Shape = TcShape<GROUPED, DP, NT, BF, Q8, SH>;
+  static_assert(SH == 1 || ((SH == 4 || SH == 2) && NT == 1 && DP == 128 && Q8), "a row's tokens go to one warp, two or four");
+  constexpr int H = 32 / SH;     // half of a thread's columns of S
+  constexpr int kOwn = 128 / SH;  // rows, each held by SH warps
   constexpr int KS = Shape::kKeys, VS = Shape::kValues;
   constexpr int RS = Shape::kRaw > 0 ? Shape::kRaw : 1;
   constexpr int kFeed = Shape::kFeedWarps;
@@ -391,12 +402,12 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH>::kThreads, TcShape
       mbar_init(&k_empty[i], 1);
     }
     for (int i = 0; i < VS; ++i) {
-      mbar_init(&v_full[i], Q8 ? kFeed - 1 : 1);  // warps that fill a stage
+      mbar_init(&v_full[i], Q8 ? Shape::kWiden / Shape::kGroups : 1);  // warps that fill a stage
       mbar_init(&v_empty[i], 1);
     }
     for (int i = 0; i < RS; ++i) {
       mbar_init(&raw_full[i], 2);
-      mbar_init(&raw_empty[i], kFeed - 1);
+      mbar_init(&raw_empty[i], Shape::kWiden / Shape::kGroups);
     }
     for (int t = 0; t < NT; ++t) {
       for (int i = 0; i < 2; ++i) {
@@ -423,7 +434,8 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH>::kThreads, TcShape
   if (warp < Shape::kSoftWarps) {
     // ---- softmax: thread = row ----
     const int tile = NT == 1 ? 0 : warp >> 2;
-    const int r = SH == 1 ? row0 + tid : lane;
+    const int r = SH == 1 ? row0 + tid : tid & (kOwn - 1);
+    const int quarter = SH == 1 ? 0 : tid / kOwn;  // which of the warps that hold the row
     const int node = r / G;
     const int hq = h * G + (r - node * G);
     const bool in = r < rows;
@@ -528,7 +540,7 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH>::kThreads, TcShape
     const bool seen = in && place_in < nodes;
     const uint64_t bits = seen && a.tree ? a.tree[b * a.T + node] : 0;
     const bool idle = SH == 1 && row0 + warp * 32 >= rows;  // the whole warp
-    const int c0 = SH == 1 ? 0 : warp * 2 * H;                 // the thread's first column of S
+    const int c0 = quarter * 2 * H;                 // the thread's first column of S
     const float sc0 = a.scale * kLog2e * q_scale;
     const float sc = sc0 > 0.0f ? sc0 : 1.0f;  // a scale of zero or less is applied to the products first
     const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
@@ -551,8 +563,9 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH>::kThreads, TcShape
         tc_ld32(s1, sb + 32);
         tc_wait_ld();
       } else {
-        uint32_t both[16];
-        tc_ld16(both, sb + c0);
+        uint32_t both[2 * H];
+        if constexpr (SH == 4) tc_ld16(both, sb + c0);
+        else tc_ld32(both, sb + c0);
         tc_wait_ld();
 #pragma unroll
         for (int i = 0; i < H; ++i) {
@@ -649,7 +662,7 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH>::kThreads, TcShape
       } else {  // zeros for the tokens of the other warps
         uint32_t row[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) row[i] = i / H == warp ? pk[i % H] : 0u;
+        for (int i = 0; i < 32; ++i) row[i] = i / H == quarter ? pk[i % H] : 0u;
         tc_st32(sb, row);
       }
       tc_wait_st();
@@ -671,15 +684,15 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH>::kThreads, TcShape
       // the warps' maxima and sums, then O in blocks of 64 dims, by way of the
       // rings, which are done with: every tile has been through its products
       float* sums = reinterpret_cast<float*>(sk);
-      sums[warp * 32 + lane] = m;
-      sums[(SH + warp) * 32 + lane] = l;
+      sums[tid] = m;
+      sums[128 + tid] = l;
       softmax_barrier();
       float all_m = -INFINITY, all_l = 0.0f;
 #pragma unroll
-      for (int w = 0; w < SH; ++w) all_m = fmaxf(all_m, sums[w * 32 + lane]);
+      for (int w = 0; w < SH; ++w) all_m = fmaxf(all_m, sums[w * kOwn + r]);
       const float ref = all_m == -INFINITY ? 0.0f : all_m;
 #pragma unroll
-      for (int w = 0; w < SH; ++w) all_l += sums[(SH + w) * 32 + lane] * exp2f(sums[w * 32 + lane] - ref);
+      for (int w = 0; w < SH; ++w) all_l += sums[128 + w * kOwn + r] * exp2f(sums[w * kOwn + r] - ref);
       part = exp2f(m - ref);
       m = all_m;
       l = all_l;
@@ -690,7 +703,8 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH>::kThreads, TcShape
     const bool write = in && !dead;
     if constexpr (SH > 1) {
       constexpr int kLine = 68;  // floats from row to row, 16 bytes off a multiple of the banks
-      static_assert(KS * Shape::kKeyBytes + VS * Shape::kValueBytes >= SH * 32 * kLine * 4, "the rings hold a block of O");
+      static_assert(KS * Shape::kKeyBytes + VS * Shape::kValueBytes >= 128 * kLine * 4, "the rings hold a block of O");
+      constexpr int DW = 2 * H;  // dims of a block of 64 that a thread writes
       float* ring = reinterpret_cast<float*>(sk);
 #pragma unroll 1
       for (int c = 0; c < DP; c += 64) {
@@ -702,7 +716,7 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH>::kThreads, TcShape
             tc_ld32(o, ocol + c + k);
             tc_wait_ld();
           }
-          float4* to = reinterpret_cast<float4*>(ring + (warp * 32 + lane) * kLine + k);
+          float4* to = reinterpret_cast<float4*>(ring + tid * kLine + k);
           const float f = part * inv;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -711,14 +725,14 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH>::kThreads, TcShape
                                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
         softmax_barrier();
-        const int d = c + c0;  // 16 dims of the row
-        float x[16];
+        const int d = c + c0;
+        float x[DW];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < DW / 4; ++i) {
           float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
           for (int w = 0; w < SH; ++w) {
-            const float4 u = *reinterpret_cast<const float4*>(ring + (w * 32 + lane) * kLine + c0 + 4 * i);
+            const float4 u = *reinterpret_cast<const float4*>(ring + (w * kOwn + r) * kLine + c0 + 4 * i);
             t = make_float4(t.x + u.x, t.y + u.y, t.z + u.z, t.w + u.w);
           }
           x[4 * i] = t.x;
@@ -730,13 +744,13 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH>::kThreads, TcShape
           if (GROUPED || p.splits > 1) {
             float4* po = reinterpret_cast<float4*>(p.part_o + ((int64_t)split * all_rows + row) * a.D + d);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < DW / 4; ++i)
               if (d + i * 4 < a.D) po[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
           } else {
             uint4* po = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + b * a.out_batch_stride +
                                                  node * a.out_token_stride + hq * a.out_head_stride + d);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < DW / 8; ++i)
               if (d + i * 8 < a.D)
                 po[i] = make_uint4(pack2<BF>(x[8 * i], x[8 * i + 1]), pack2<BF>(x[8 * i + 2], x[8 * i + 3]),
                                    pack2<BF>(x[8 * i + 4], x[8 * i + 5]), pack2<BF>(x[8 * i + 6], x[8 * i + 7]));
@@ -776,7 +790,7 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH>::kThreads, TcShape
       }
       __syncwarp();
     }
-    if (write && (SH == 1 || warp == 0)) {
+    if (write && quarter == 0) {
       if (GROUPED || p.splits > 1) p.part_l[(int64_t)split * all_rows + row] = lse;
       else if (a.lse) a.lse[row] = lse;
     }
@@ -855,11 +869,115 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH>::kThreads, TcShape
         }
       }
     } else {
-      // The first warp brings keys, which are operands as they lie, values
-      // into the raw ring, and the scales of both (a fence of a warp that
-      // widens would wait for such loads); the others widen values.
+      // The first warp (or the first two) brings keys, which are operands as
+      // they lie, values into the raw ring, and the scales of both (a fence of
+      // a warp that widens would wait for such loads); the others widen values.
       constexpr uint32_t kToken = 1u << 16;  // beside a value's exponent: there is a token
-      if (feeder == 0) {
+      if (Shape::kSplit && feeder < 2) {
+        // Keys (blocks of 128 dims), or values; a lane a box, its page
+        // (outside the pool past the last token, which reads as zeros) looked
+        // up a tile ahead.
+        constexpr int KW = DP < 128 ? DP : 128;  // bytes of a row of a keys' block
+        const bool val = feeder == 1;
+        const int blk = per_tile && !val ? lane / per_tile : 0, piece = per_tile ? lane - blk * per_tile : 0;
+        const bool boxed = lane < per_tile * (val ? 1 : DP / KW);
+        const int t_end = min(len, (t_begin + n) * kTile);
+        int pg = -1, to = 0;
+        auto look = [&](int j) {
+          const int t = (t_begin + j) * kTile + piece * p.box;
+          place(min(t, len - 1), pg, to);
+          if (!boxed || t >= t_end) pg = -1;
+        };
+        if (n > 0) look(0);
+        Ring ring = {0, 1};
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
+          uint64_t* full = val ? &raw_full[ring.at] : &k_full[ring.at];
+          unsigned char* to_smem = val ? raw + ring.at * Shape::kRawBytes : sk + ring.at * Shape::kKeyBytes;
+          // each full barrier takes two arrivals: this one, and that of the warp with the scales
+          tc_wait(val ? &raw_empty[ring.at] : &k_empty[ring.at], ring.phase, &dead);
+          __syncwarp();
+          if (p.box) {
+            if (lane == 0) mbar_arrive_expect_tx(full, val ? Shape::kRawBytes : Shape::kKeyBytes);
+            __syncwarp();
+            if (boxed) {
+              if (val) tma_box(to_smem + piece * p.box * DP, &vmap, full, 0, h, to, pg);
+              else tma_box(to_smem + blk * (kTile * 128) + piece * p.box * KW, &kmap, full, blk * 128, h, to, pg);
+            }
+          } else {
+            if (!val) {  // (values are read by the warps that widen them)
+              constexpr int CH = DP / 16;
+              for (int x = lane; x < kTile * CH; x += 32) {
+                const int r = x / CH, c = x - r * CH;
+                int page1 = -1, at1 = 0;
+                if (c * 16 < a.D) find((t_begin + j) * kTile + r, page1, at1);
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (page1 >= 0)
+                  w = fetch16(reinterpret_cast<const uint8_t*>(a.k.data) + h * a.k.head_stride + (int64_t)page1 * a.k.page_stride +
+                                  (int64_t)at1 * a.k.token_stride + c * 16,
+                              p.wide, c * 16 + 8 < a.D);
+                *reinterpret_cast<uint4*>(to_smem + swizzled<kTile>(r, c)) = w;
+              }
+              fence_proxy_async_shared();
+              __syncwarp();
+            }
+            if (lane == 0) mbar_arrive(full);
+          }
+          if (j + 1 < n) look(j + 1);
+          if (val) ring.template step<RS>();
+          else ring.template step<KS>();
+        }
+      } else if (Shape::kSplit && feeder == 2) {
+        // This warp brings the scales: all pages of a run are asked for at
+        // once, then all its exponents, this lane's two tokens of each tile.
+        const uint8_t* ke = a.k.exponents + h * a.k.exp_head_stride;
+        const uint8_t* ve = a.v.exponents + h * a.v.exp_head_stride;
+        Ring kr = {0, 1}, rr = {0, 1};
+#pragma unroll 1
+        for (int j0 = 0; j0 < n; j0 += kRun) {
+          // (unconditional reads, at places that exist: a branch around each would make them wait for one another)
+          int page[2 * kRun], at[2 * kRun];
+          uint32_t e[2 * kRun], ek[2 * kRun], ev[2 * kRun];
+          const int t0 = (t_begin + j0) * kTile, t_end = min(len, (t_begin + n) * kTile);
+#pragma unroll
+          for (int i = 0; i < 2 * kRun; ++i) place(min(t0 + i * 32 + lane, len - 1), page[i], at[i]);
+#pragma unroll
+          for (int i = 0; i < 2 * kRun; ++i) {
+            const bool in = (uint32_t)page[i] < (uint32_t)a.pages && t0 + i * 32 + lane < t_end;
+            const uint32_t q = in ? page[i] : 0, t = in ? at[i] : 0;  // strides have 32 bits
+            e[i] = in ? kToken : 0;
+            ek[i] = __ldg(ke + (uint64_t)q * (uint32_t)a.k.exp_page_stride + (uint64_t)t * (uint32_t)a.k.exp_token_stride);
+            ev[i] = __ldg(ve + (uint64_t)q * (uint32_t)a.v.exp_page_stride + (uint64_t)t * (uint32_t)a.v.exp_token_stride);
+          }
+#pragma unroll 1
+          for (int i = 0; i < kRun && j0 + i < n; ++i) {
+            // the run's registers are indexed by selects, not unrolled code
+            uint32_t k2[2] = {0, 0}, v2[2] = {0, 0};
+#pragma unroll
+            for (int u = 0; u < kRun; ++u)
+              if (u == i) {
+                k2[0] = e[2 * u] ? ek[2 * u] : 127;
+                k2[1] = e[2 * u + 1] ? ek[2 * u + 1] : 127;
+                v2[0] = e[2 * u] ? kToken | ev[2 * u] : 0;
+                v2[1] = e[2 * u + 1] ? kToken | ev[2 * u + 1] : 0;
+              }
+            // an arrival of a later round must not be taken for the other warp's of this one
+            tc_wait(&k_empty[kr.at], kr.phase, &dead);
+            float* f = sscale[(j0 + i) % kScales];
+            f[lane] = exponent_scale(k2[0]);
+            f[lane + 32] = exponent_scale(k2[1]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&k_full[kr.at]);
+            tc_wait(&raw_empty[rr.at], rr.phase, &dead);
+            sexp[rr.at][lane] = v2[0];
+            sexp[rr.at][lane + 32] = v2[1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&raw_full[rr.at]);
+            kr.template step<KS>();
+            rr.template step<RS>();
+          }
+        }
+      } else if (!Shape::kSplit && feeder == 0) {
         const uint8_t* ke = a.k.exponents + h * a.k.exp_head_stride;
         const uint8_t* ve = a.v.exponents + h * a.v.exp_head_stride;
         // boxes: lanes 0-15 keys (blocks of 128 dims), 16-31 values
@@ -960,9 +1078,11 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH>::kThreads, TcShape
           }
         }
       } else {
-        const int pt = tid - 32 * (Shape::kSoftWarps + 1);
+        constexpr int GROUPS = Shape::kGroups, kTeam = Shape::kWiden / GROUPS;  // warps that share a tile
+        const int pw = warp - (Shape::kSoftWarps + kFeed - Shape::kWiden), group = pw / kTeam;
+        const int pt = (pw - group * kTeam) * 32 + lane;
         constexpr int CH = DP / 16;                  // 16-byte pieces of a cached row
-        constexpr int STEP = 32 * (kFeed - 1) / CH;  // rows between a thread's rows
+        constexpr int STEP = 32 * kTeam / CH;  // rows between a thread's rows
         const int c = pt % CH, r0 = pt / CH;
         const bool c_in = c * 16 < a.D;
         // This thread's pieces of the values of tile j; rows without a token
@@ -971,8 +1091,12 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH>::kThreads, TcShape
         constexpr int NR = (kTile + STEP - 1) / STEP;
         constexpr int NB = NR % 3 == 0 ? 3 : NR % 2 == 0 ? 2 : 1;  // at a time
         Ring vr = {0, 1}, rr = {0, 0};  // an empty stage's wait starts passed
+        if (group) {
+          vr.template step<VS>();
+          rr.template step<RS>();
+        }
 #pragma unroll 1
-        for (int j = 0; j < n; ++j) {
+        for (int j = group; j < n; j += GROUPS) {
           tc_wait(&raw_full[rr.at], rr.phase, &dead);
           tc_wait(&v_empty[vr.at], vr.phase, &dead);
           const unsigned char* from = raw + rr.at * Shape::kRawBytes + c * 16;
@@ -1021,8 +1145,11 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH>::kThreads, TcShape
             mbar_arrive(&v_full[vr.at]);
             mbar_arrive(&raw_empty[rr.at]);
           }
-          vr.template step<VS>();
-          rr.template step<RS>();
+#pragma unroll
+          for (int i = 0; i < GROUPS; ++i) {
+            vr.template step<VS>();
+            rr.template step<RS>();
+          }
         }
       }
     }

@@ -104,9 +104,9 @@ struct Cost {
   double tile;   // us a tile
   int64_t tiles;
 };
-Cost cost_of(const topkp_tree_attention_args& a, int64_t tokens, bool grouped, int num_sms) {
+Cost cost_of(const topkp_tree_attention_args& a, int64_t tokens, bool lone, int num_sms) {
   const int64_t nt = row_tiles(a), rows = a.T * (a.Hq / a.Hkv);
-  const bool pair = !grouped && few_rows(a) && a.dtype == TOPKP_BF16;
+  const bool pair = !lone && few_rows(a) && a.dtype == TOPKP_BF16;
   Cost c;
   c.slots = (nt == 2 || a.D > (a.k.dtype == TOPKP_E4M3 && !pair ? 64 : 128) ? 1.0 : 2.0) * num_sms;
   c.base = (double)(a.B * a.Hkv * ((rows + nt * kTcRows - 1) / (nt * kTcRows)));
@@ -175,7 +175,7 @@ SharedPlan plan_shared(const topkp_tree_attention_args& a, int64_t groups, int64
   s.part_bytes = alone.part_bytes;
   const int64_t context = bounded_context(a), front = std::min(max_shared, context) / kTile * kTile;
   if (groups >= a.B || front <= 0) return s;
-  const Cost x = cost_of(as_groups(a, groups), front, true, num_sms), y = cost_of(a, context - front + a.T + kTile - 1, true, num_sms);
+  const Cost x = cost_of(as_groups(a, groups), front, true, num_sms), y = cost_of(a, context - front + a.T + kTile - 1, false, num_sms);
   // As fitted to 15 x 4 choices of parts of seven cases (8 to 512 rows a
   // group's head, 4000 to 65500 shared tokens, both kinds of cache; the choice
   // made is at worst 10% slower than the best, in six cases at most 6%): a

@@ -125,11 +125,11 @@ bool make_map(CUtensorMap* map, const topkp_cache& c, const topkp_tree_attention
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool GROUPED, int DP, int NT, bool BF, bool Q8, int SH = 1>
+template <bool GROUPED, int DP, int NT, bool BF, bool Q8, int SH = 1, bool LONE = false>
 cudaError_t launch_tc(AttnDev p, cudaStream_t s) {
-  using Shape = TcShape<GROUPED, DP, NT, BF, Q8, SH>;
+  using Shape = TcShape<DP, NT, BF, Q8, SH, LONE>;
   const topkp_tree_attention_args& a = p.a;
-  cudaError_t e = cudaFuncSetAttribute(attn_tc<GROUPED, DP, NT, BF, Q8, SH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kSmem);
+  cudaError_t e = cudaFuncSetAttribute(attn_tc<GROUPED, DP, NT, BF, Q8, SH, LONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kSmem);
   if (e != cudaSuccess) return e;
   // tokens of a box: they lie in one page, and eight rows make a swizzle's group
   CUtensorMap km = {}, vm = {};
@@ -144,7 +144,7 @@ cudaError_t launch_tc(AttnDev p, cudaStream_t s) {
   const int64_t rows = a.T * (a.Hq / a.Hkv);
   const dim3 grid((unsigned)((rows + NT * kTcRows - 1) / (NT * kTcRows)), (unsigned)p.splits, (unsigned)(a.B * a.Hkv));
   if (!GROUPED || p.stage != 2) {
-    attn_tc<GROUPED, DP, NT, BF, Q8, SH><<<grid, Shape::kThreads, Shape::kSmem, s>>>(p, km, vm);
+    attn_tc<GROUPED, DP, NT, BF, Q8, SH, LONE><<<grid, Shape::kThreads, Shape::kSmem, s>>>(p, km, vm);
     return cudaGetLastError();
   }
   // the requests' own tokens run beside the shared ones
@@ -158,7 +158,7 @@ cudaError_t launch_tc(AttnDev p, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_tc<GROUPED, DP, NT, BF, Q8, SH>, p, km, vm);
+  return cudaLaunchKernelEx(&cfg, attn_tc<GROUPED, DP, NT, BF, Q8, SH, LONE>, p, km, vm);
 }
 
 // Tiles of 128 rows of a CTA (256 dims leave tensor memory for one).
@@ -180,6 +180,9 @@ bool some_rows(const topkp_tree_attention_args& a) {
 template <bool GROUPED, bool BF, bool Q8>
 cudaError_t launch_dim(const AttnDev& p, cudaStream_t s) {
   if constexpr (Q8) {
+    if constexpr (GROUPED && BF) {
+      if (few_rows(p.a) && p.stage == 1) return launch_tc<GROUPED, 128, 1, BF, true, 4, true>(p, s);
+    }
     if (few_rows(p.a)) return launch_tc<GROUPED, 128, 1, BF, true, 4>(p, s);
     if constexpr (GROUPED) {
       if (some_rows(p.a)) return launch_tc<GROUPED, 128, 1, BF, true, 2>(p, s);

@@ -184,13 +184,14 @@ __device__ __forceinline__ void softmax_barrier() { asm volatile("bar.sync 1, 12
 // warps hold a copy of the rows each and take a quarter of every tile's tokens
 // (for O's product the others' are zeros); their O, maxima and sums are joined
 // at the end.  With up to 64 rows two pairs of warps take a half.
-template <bool GROUPED, int DP, int NT, bool BF, bool Q8, int SH>
+template <int DP, int NT, bool BF, bool Q8, int SH, bool LONE>
 struct TcShape {
   static constexpr int kSoftWarps = 4 * NT;
   // 16 bits: one warp for keys, one for values; e4m3: one loads, the others widen
-  // then bf16's 128 dims leave room for two CTAs an SM (64
-  // single tokens of 64 query and 8 cache heads to 8000: 303 us, with one 318)
-  static constexpr bool kPair = SH == 4 && BF && !GROUPED;
+  // then bf16's 128 dims leave room for two CTAs an SM, which short requests
+  // are better for (128 single tokens of 64 query and 8 cache heads to 500:
+  // 64 us, fp16 with one CTA 87), LONE: one all the same, for a long prefix
+  static constexpr bool kPair = SH == 4 && BF && !LONE;
   // Where there are registers for it, keys, values and their scales are brought
   // by a warp each, and two groups of warps widen values in turn: a single
   // loading warp, with the latency of its own instructions and loads, was what
@@ -353,10 +354,10 @@ __device__ __forceinline__ void e4m3_away(uint32_t two, float& x, float& y) {
   y -= __half2float(__ushort_as_half((uint16_t)(h >> 16)));
 }
 
-template <bool GROUPED, int DP, int NT, bool BF, bool Q8, int SH>
-__global__ void __launch_bounds__(TcShape<GROUPED, DP, NT, BF, Q8, SH>::kThreads, TcShape<GROUPED, DP, NT, BF, Q8, SH>::kPerSm)
+template <bool GROUPED, int DP, int NT, bool BF, bool Q8, int SH, bool LONE>
+__global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH, LONE>::kThreads, TcShape<DP, NT, BF, Q8, SH, LONE>::kPerSm)
     attn_tc(const __grid_constant__ AttnDev p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-  using Shape = TcShape<GROUPED, DP, NT, BF, Q8, SH>;
+  using Shape = TcShape<DP, NT, BF, Q8, SH, LONE>;
   static_assert(SH == 1 || ((SH == 4 || SH == 2) && NT == 1 && DP == 128 && Q8), "a row's tokens go to one warp, two or four");
   constexpr int H = 32 / SH;     // half of a thread's columns of S
   constexpr int kOwn = 128 / SH;  // rows, each held by SH warps

@@ -11,6 +11,12 @@ lets the caches follow the selected beams in place.
 ``verify_tree``: a tree of drafted tokens goes through the model in one pass
 over the same kind of cache; the filter and the sample pick a token after
 every node, and the longest drafted path that agrees with them is accepted.
+
+``sample_drafted``: one prompt goes on as several samples over a paged cache.
+Its pages are shared, attention reads the prompt once for all samples, and each
+round a drafted tree of every sample is verified against the target's
+probabilities, its accepted tokens move up behind the context, and pages grow
+or return to the pool, all without a word from the host.
 """
 from __future__ import annotations
 
@@ -127,6 +133,88 @@ def verify_tree(model, caches, lengths, tokens, tree, above, k=50):
         path.append(child[0])
 
 
+class PagedCaches:
+    """Pages of keys and values a layer, a block table and the pages' holders."""
+
+    def __init__(self, model, pool, page_size, max_pages, device="cuda"):
+        shape = (pool, page_size, model.Hkv, model.D)
+        self.kv = [[torch.zeros(shape, dtype=torch.bfloat16, device=device) for _ in (0, 1)] for _ in range(model.layers)]
+        self.states = [t for pair in self.kv for t in pair]
+        self.page_size = page_size
+        self.pages = torch.full((0, max_pages), -1, dtype=torch.int32, device=device)
+        self.lengths = torch.zeros(0, dtype=torch.int32, device=device)
+        self.refs = torch.zeros(pool, dtype=torch.int32, device=device)
+
+    def fork(self, source, grow):
+        """Row n goes on from row source[n] (-1: it begins), with room for ``grow`` more tokens."""
+        self.pages, _, self.missing = tk.cache_fork(self.states, self.pages, self.lengths, source, self.refs, grow=grow, refs_out=self.refs)
+        old = torch.cat([self.lengths, torch.zeros(1, dtype=torch.int32, device=source.device)])
+        self.lengths = old[source.long()]  # (-1 is the last, a zero)
+
+    def attend(self, tree=None, shared=None, longest=None):
+        """For ToyModel.forward: new tokens stand at lengths[r] and on."""
+        def run(layer, q, k, v):
+            R, T = q.shape[:2]
+            at = self.lengths[:, None].long() + torch.arange(T, device=q.device)
+            page = self.pages.long().gather(1, at // self.page_size)
+            slots = torch.where(page >= 0, page * self.page_size + at % self.page_size, -1).view(-1)
+            kc, vc = self.kv[layer]
+            tk.cache_write(k.reshape(R * T, *k.shape[2:]), v.reshape(R * T, *v.shape[2:]), slots, kc, vc)
+            if shared is None:
+                return tk.tree_attention(q, kc, vc, self.lengths, pages=self.pages, tree=tree)
+            return tk.shared_attention(q, kc, vc, self.lengths, self.pages, shared, tree=tree, max_context=longest)
+        return run
+
+
+def sample_drafted(model, prompt, samples=8, rounds=6, page_size=16, above=(0, 0, 0, 1, 1, 2, 3), seed=0):
+    """prompt [P], P > 1.  Draws ``samples`` continuations of it; ``above`` is each drafted node's parent.
+    Returns each sample's tokens, and the log-probability the target gave them when they were accepted or drawn."""
+    dev = prompt.device
+    g = torch.Generator(device=dev).manual_seed(seed)
+    T, P, N = len(above), prompt.numel(), samples
+    parent = torch.tensor(above, dtype=torch.int32, device=dev).expand(N, T).contiguous()
+    masks = [1]
+    for i in range(1, T):
+        masks.append(masks[above[i]] | 1 << i)
+    tree = torch.tensor(masks, device=dev).expand(N, T).contiguous()
+    longest = P + rounds * T
+    caches = PagedCaches(model, pool=(N + 1) * (-(-longest // page_size) + 1), page_size=page_size, max_pages=-(-longest // page_size) + 1)
+    # the prompt but its last token, once; then a row for each sample
+    caches.fork(torch.full((1,), -1, dtype=torch.int32, device=dev), P - 1)
+    model.forward(prompt[None, :-1], caches.attend())
+    caches.lengths += P - 1
+    shared = caches.lengths.clone()
+    caches.fork(torch.zeros(N, dtype=torch.int32, device=dev), T)
+    stay = torch.arange(N, dtype=torch.int32, device=dev)
+    last = prompt[-1].expand(N).clone()
+    out, logps = [[] for _ in range(N)], [[] for _ in range(N)]
+
+    def race(*shape):
+        return torch.empty(shape, device=dev).exponential_(generator=g)
+
+    for _ in range(rounds):
+        # a cheap draft: what the embedding alone says comes next, a token of each node's parent's distribution
+        tokens = last[:, None].expand(N, T).clone()
+        draft = torch.empty((N, T, model.vocab), device=dev, dtype=torch.bfloat16)
+        for i in range(T):
+            if i:
+                tokens[:, i] = (draft[:, above[i]].float() - torch.log(race(N, model.vocab))).argmax(1)
+            draft[:, i] = model.norm(model.embed[tokens[:, i]]) @ model.head
+        target = model.forward(tokens, caches.attend(tree, shared, longest))
+        count, path, token, logp = tk.draft_verify(target, tokens.int(), torch.rand((N, T), generator=g, device=dev), race(N, model.vocab),
+                                                   draft=draft, parent=parent, want_logprob=True)
+        tk.cache_compact(caches.states, caches.lengths, path, count, pages=caches.pages)
+        caches.lengths = caches.lengths + count
+        caches.fork(stay, T)     # pages past the accepted tokens return, new ones come
+        last = token.long()
+        # (the host only looks on)
+        for n, (c, p, t, l) in enumerate(zip(count.tolist(), path.tolist(), token.tolist(), logp.tolist())):
+            out[n] += [int(tokens[n, i]) for i in p[1:c]] + [t]
+            logps[n] += l[:c]
+    assert int(caches.missing) == 0
+    return out, logps
+
+
 def main():
     model = ToyModel()
     prompts = torch.randint(0, model.vocab, (2, 12), device="cuda")
@@ -144,6 +232,8 @@ def main():
     nodes = torch.cat([prompts[:1, -1:], torch.randint(0, model.vocab, (1, 6), device="cuda")], 1)
     path, token = verify_tree(model, caches, start + prompts.shape[1] - 1, nodes, torch.tensor([masks], device="cuda"), above)
     print("accepted nodes", path, "next token", token)
+    out, _ = sample_drafted(model, prompts[0])
+    print("samples of one prompt:", [len(t) for t in out], "tokens, the first", out[0])
     tk.device_status()
 
 

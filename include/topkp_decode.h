@@ -255,8 +255,8 @@ topkp_status topkp_tree_attention(const topkp_tree_attention_args* args, void* s
  * prefix.  The B requests are `groups` runs of B / groups consecutive ones;
  * tokens [0, shared[g]) are the same for all requests of group g (the same
  * pages, or equal contents), and are read once for all of them, through the
- * block table of the group's first request.  The result is that of
- * topkp_tree_attention but for the order of the sums.
+ * block table of the group's first request that has a node.  The result is
+ * that of topkp_tree_attention but for the order of the sums.
  *
  *   args        as for topkp_tree_attention; table is not NULL.
  *   shared      device, [groups] int32.  What is read once is the largest
@@ -298,9 +298,10 @@ topkp_status topkp_shared_attention(const topkp_tree_attention_args* args, const
  *
  *   target     device, [B, T, V] of dtype, strides in elements (node_stride
  *              >= V), V contiguous; -inf is a token that the filter removed.
- *              Only the rows of the accepted path are read.
- *   draft      device, the same, or NULL; rows of accepted nodes that have
- *              children are read.
+ *              Rows of nodes that are not accepted do not matter (those of
+ *              first children may be read).
+ *   draft      device, the same, or NULL; rows of nodes without children are
+ *              not read.
  *   tokens     device, [B, T] int32.
  *   parent     device, [B, T] int32: node i (i > 0) is a child of
  *              parent[b][i] < i, other nodes are nobody's; NULL: a chain.

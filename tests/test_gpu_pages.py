@@ -63,7 +63,6 @@ def check_fork(tk, g, table, lengths, source, refs, grow, P, tensors, in_place=F
         new, counts, missing, copies = R.fork(table, lengths, source, refs, growths, P)
     else:
         new, counts, missing, copies = R.fork([[-1] * M], [0], [-1 for _ in source], refs, growths, P)
-    before = [t.clone() for t, _ in tensors]
     want = [t.clone() for t, _ in tensors]
     for t, (_, dim) in zip(want, tensors):
         v = t.movedim(dim, 1)
@@ -80,10 +79,11 @@ def check_fork(tk, g, table, lengths, source, refs, grow, P, tensors, in_place=F
         got_table, got_refs, got_missing = tk.cache_fork(some, *args, **kw)
         assert got_table.tolist() == new
         assert got_refs.tolist() == counts and int(got_missing) == missing
-    for t, w, b in zip(dev, want, before):
+    for t, w in zip(dev, want):
         t = t.cpu()
-        for p in range(pool):
-            assert torch.equal(t[p], w[p]), (p, [c for c in copies if p in c[:2]])
+        if not torch.equal(t, w):
+            p = next(p for p in range(pool) if not torch.equal(t[p], w[p]))
+            raise AssertionError((p, [c for c in copies if p in c[:2]]))
     return new, counts, missing
 
 
@@ -116,6 +116,36 @@ def test_fork_identity_everything_and_nothing(tk):
     check_fork(tk, g, table, lengths, [4] * 40, refs, 9, 8, tensors)
     # no old row at all: requests begin
     check_fork(tk, g, [], [], [-1, 0, 5], [0] * 20 + [1] * 180, [0, 17, 40], 8, tensors, M=6)
+
+
+@pytest.mark.parametrize("pool,holes", [(70001, 0.5), (40003, 0.999), (32768, 0.0), (8191, 1.0)])
+def test_fork_large_pools(tk, pool, holes):
+    """Free pages ranked over several rounds of the pool, few of them and many."""
+    g = torch.Generator().manual_seed(pool)
+    refs = (torch.rand(pool, generator=g) < holes).int()
+    refs[torch.randint(0, pool, (600,), generator=g)] = 0        # some are free in any case
+    where = torch.nonzero(refs == 0)[:, 0]
+    where = where[torch.randperm(where.numel(), generator=g)][:90].tolist()
+    table = [where[i * 6:i * 6 + 6] + [-1] * 3 for i in range(15)]
+    for p in where:
+        refs[p] += 1
+    lengths = torch.randint(0, 13, (15,), generator=g).tolist()
+    source = torch.randint(-1, 15, (40,), generator=g).tolist()
+    check_fork(tk, g, table, lengths, source, refs.tolist(), torch.randint(0, 12, (40,), generator=g).tolist(), 2,
+               [(bytes_of(g, pool, 2, 4), 1)])
+
+
+def test_fork_the_most_rows(tk):
+    """8192 rows on either side: shared memory at its largest."""
+    g = torch.Generator().manual_seed(6)
+    R, pool = 8192, 60000
+    order = torch.randperm(pool, generator=g)
+    table = torch.stack([order[:R], order[R:2 * R], torch.full((R,), -1)], 1)
+    lengths = torch.randint(0, 9, (R,), generator=g)
+    refs = torch.zeros(pool, dtype=torch.int64)
+    refs[order[:2 * R]] = 1
+    source = torch.randint(0, R, (R,), generator=g)
+    check_fork(tk, g, table.tolist(), lengths.tolist(), source.tolist(), refs.tolist(), 3, 4, [(bytes_of(g, pool, 4, 3), 1)])
 
 
 def test_fork_short_of_pages(tk):

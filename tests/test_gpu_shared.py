@@ -128,6 +128,34 @@ def test_ragged_groups_and_requests(tk, cache):
            capacity=40000)
 
 
+@pytest.mark.parametrize("cache", ["own", "e4m3"])
+def test_a_group_whose_first_requests_are_padding(tk, cache):
+    """Requests without nodes hold no pages and no context: the prefix is read through the first that has any."""
+    size, T, P = 20, 2, 16
+    own = [9 * i % 70 for i in range(2 * size)]
+    nodes = ([0, 0, 1] + [2] * (size - 3)) + [0] * size      # and a group of nothing but padding
+    g, B, contexts, table, store, exps = build_case("bf16", cache, [640, 500], size, own, T, 1, 128, P, 3, nodes)
+    table = torch.cat([table, torch.full((B, 4000), -1, dtype=torch.int32)], 1)
+    for b in range(B):
+        if nodes[b] == 0:
+            table[b] = -1 if b % 2 else 2 ** 31 - 1
+            contexts[b] = 0 if b % 2 else 10 ** 9
+    q = torch.randn(B, T, 8, 128, generator=g).to(torch.bfloat16)
+    kw = {} if cache == "own" else dict(k_exp=exps[0].to(torch.uint8).cuda(), v_exp=exps[1].to(torch.uint8).cuda())
+    args = [q.cuda(), *(x.cuda() for x in store), torch.tensor(contexts, dtype=torch.int32).cuda(), table.cuda()]
+    shared = torch.tensor([640, 500], dtype=torch.int32).cuda()
+    kw.update(nodes=torch.tensor(nodes, dtype=torch.int32).cuda(), want_lse=True)
+    out, lse = tk.shared_attention(*args, shared, **kw)
+    assert tk.last_launch_count() == 3
+    want, wlse = tk.tree_attention(*args[:4], pages=args[4], max_context=800, **kw)
+    tk.device_status()
+    on = torch.tensor([i < nodes[b] for b in range(B) for i in range(T)]).view(B, T)
+    assert (out[~on] == 0).all() and (lse[~on] == -math.inf).all()
+    # both are within the same bounds of 64 bits (tested above and beside tree_attention): values of about 1 over 600 tokens
+    assert ((out.float() - want.float()).abs()[on] <= 2 * 2.0 ** -8 * (want.float().abs()[on] + 1.5)).all()
+    assert ((lse - wlse).abs()[on] <= 1e-3).all()
+
+
 def test_any_bound_of_what_is_shared(tk):
     own = [5 * i % 97 for i in range(48)]
     for say in ([700], [640], [639], [1], [0], [-5], [704 - 1]):

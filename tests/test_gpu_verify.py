@@ -192,6 +192,22 @@ def test_layouts(tk):
     check(tk, e)
 
 
+def test_far_rows_and_a_long_vocabulary(tk):
+    """Rows whose element offsets pass 2^32, and the largest vocabulary."""
+    d = make(3, 3, 5000, "bf16", "ratio", False, seed=21)
+    far = torch.empty(2 ** 32 + 60000, dtype=torch.bfloat16, device="cuda")
+    dev = {}
+    for i, k in enumerate(("target", "draft")):
+        x = far.as_strided((3, 3, 5000), (2 ** 31 + 8 * i, 5000, 1), 17000 * i)     # (the second lies in the gaps of the first)
+        x.copy_(d[k].cuda())
+        dev[k] = x
+    check(tk, d, device=dev)
+    del far, dev
+    V = 1 << 23
+    for dtype, mode in (("f32", "ratio"), ("bf16", "certain")):
+        check(tk, make(1, 2, V, dtype, mode, False, seed=22), most_near=0)
+
+
 def test_other_stream_graph_and_two_at_once(tk):
     d = {k: None if v is None else v.cuda() for k, v in make(10, 8, 20000, "bf16", "ratio", True, seed=11).items()}
     f = {k: None if v is None else v.cuda() for k, v in make(10, 8, 20000, "bf16", "ratio", True, seed=12).items()}

@@ -20,7 +20,8 @@
 
 namespace topkp {
 
-cudaError_t launch_grouped(const AttnDev& p, cudaStream_t s);            // attention_shared.cu
+// attention_shared.cu
+cudaError_t launch_grouped(const AttnDev& front, const AttnDev& own, cudaStream_t s);
 cudaError_t grouped_take_device_error(unsigned int* out);
 
 namespace {
@@ -263,7 +264,8 @@ cudaError_t launch_attention(const topkp_tree_attention_args& a, const AttnPlan&
   p.splits = plan.splits;
   p.per = plan.per;
   give_parts(p, plan.splits);
-  const cudaError_t e = launch_parts<false>(p, s);
+  Maps maps;
+  const cudaError_t e = launch_parts<false>(p, maps, s);
   *launches = 1;
   if (e != cudaSuccess || plan.splits <= 1) return e;
   *launches = 2;
@@ -283,11 +285,9 @@ cudaError_t launch_shared(const topkp_tree_attention_args& a, const int32_t* sha
   front.stage = 1;
   front.inner = (int)a.T;
   front.q_member = a.q_batch_stride;
+  front.ld_member = a.ld_table;
   front.splits = plan.front.splits;
   front.per = plan.front.per;
-  *launches = 0;
-  cudaError_t e = launch_grouped(front, s);
-  if (e != cudaSuccess) return e;
   AttnDev join = own;
   join.splits = parts;
   own.stage = 2;
@@ -295,7 +295,7 @@ cudaError_t launch_shared(const topkp_tree_attention_args& a, const int32_t* sha
   own.per = plan.own.per;
   own.part_o += (size_t)front.splits * all * a.D;
   own.part_l += (size_t)front.splits * all;
-  e = launch_grouped(own, s);
+  const cudaError_t e = launch_grouped(front, own, s);
   *launches = 3;
   return e != cudaSuccess ? e : launch_join(join, s);
 }

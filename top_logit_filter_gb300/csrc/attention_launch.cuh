@@ -31,6 +31,7 @@ struct AttnDev {
   int size;                // requests of a group
   int inner;               // stage 1: nodes of a request
   int64_t q_member;        // stage 1: from request to request in q
+  int64_t ld_member;       // and in the block table
   const int32_t* shared;   // [groups]
 };
 
@@ -54,16 +55,25 @@ __device__ __forceinline__ void request_span(const topkp_tree_attention_args& a,
 constexpr int kTile = 64;  // tokens
 
 // Tokens that group g's requests read together: whole tiles within what they
-// share and within the context of each that has a node.  By a whole warp.
-__device__ __forceinline__ int shared_span(const AttnDev& p, int64_t g) {
+// share and within the context of each that has a node; and the first of
+// those, whose block table they are read through.  By a whole warp.
+__device__ __forceinline__ int shared_span(const AttnDev& p, int64_t g, int* first) {
   const topkp_tree_attention_args& a = p.a;
-  int most = p.shared[g];
+  int most = p.shared[g], who = p.size;
   for (int i = threadIdx.x & 31; i < p.size; i += 32) {
     const int64_t r = g * p.size + i;
-    if (!a.nodes || a.nodes[r] > 0) most = min(most, a.context[r]);
+    if (!a.nodes || a.nodes[r] > 0) {
+      most = min(most, a.context[r]);
+      who = min(who, i);
+    }
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) most = min(most, __shfl_xor_sync(0xffffffffu, most, o));
+  for (int o = 16; o > 0; o >>= 1) {
+    most = min(most, __shfl_xor_sync(0xffffffffu, most, o));
+    who = min(who, __shfl_xor_sync(0xffffffffu, who, o));
+  }
+  *first = who;
+  if (who == p.size) return 0;
   return (int)min((long long)max(most, 0), (long long)(a.max_pages * a.page_size)) / kTile * kTile;
 }
 
@@ -125,26 +135,42 @@ bool make_map(CUtensorMap* map, const topkp_cache& c, const topkp_tree_attention
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// What a launch leaves for the next one of the same call: the maps of the
+// same caches (a box's shape depends on the kernel's head dimension only).
+struct Maps {
+  CUtensorMap k, v;
+  int box = -1;  // tokens of a box, 0: TMA cannot take the caches, -1: not made
+};
+
 template <bool GROUPED, int DP, int NT, bool BF, bool Q8, int SH = 1, bool LONE = false>
-cudaError_t launch_tc(AttnDev p, cudaStream_t s) {
+cudaError_t launch_tc(AttnDev p, Maps& maps, cudaStream_t s) {
   using Shape = TcShape<DP, NT, BF, Q8, SH, LONE>;
   const topkp_tree_attention_args& a = p.a;
-  cudaError_t e = cudaFuncSetAttribute(attn_tc<GROUPED, DP, NT, BF, Q8, SH, LONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kSmem);
-  if (e != cudaSuccess) return e;
-  // tokens of a box: they lie in one page, and eight rows make a swizzle's group
-  CUtensorMap km = {}, vm = {};
-  p.box = kTile;
-  if (a.table)
-    while (p.box > 4 && a.page_size % p.box) p.box /= 2;
-  // operands are swizzled (rows of 128 bytes, or of 64 e4m3); raw values are not
-  constexpr auto by128 = CU_TENSOR_MAP_SWIZZLE_128B, by64 = CU_TENSOR_MAP_SWIZZLE_64B, plain = CU_TENSOR_MAP_SWIZZLE_NONE;
-  if (p.box < 8 || !make_map(&km, a.k, a, p.box, !Q8 ? 64 : DP < 128 ? DP : 128, Q8 && DP == 64 ? by64 : by128) ||
-      !make_map(&vm, a.v, a, p.box, Q8 ? DP : 64, Q8 ? plain : by128))
-    p.box = 0;
+  // (asked for once a device and thread)
+  static thread_local int configured = -1;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (configured != dev) {
+    const cudaError_t e = cudaFuncSetAttribute(attn_tc<GROUPED, DP, NT, BF, Q8, SH, LONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kSmem);
+    if (e != cudaSuccess) return e;
+    configured = dev;
+  }
+  if (maps.box < 0) {
+    // tokens of a box: they lie in one page, and eight rows make a swizzle's group
+    maps.box = kTile;
+    if (a.table)
+      while (maps.box > 4 && a.page_size % maps.box) maps.box /= 2;
+    // operands are swizzled (rows of 128 bytes, or of 64 e4m3); raw values are not
+    constexpr auto by128 = CU_TENSOR_MAP_SWIZZLE_128B, by64 = CU_TENSOR_MAP_SWIZZLE_64B, plain = CU_TENSOR_MAP_SWIZZLE_NONE;
+    if (maps.box < 8 || !make_map(&maps.k, a.k, a, maps.box, !Q8 ? 64 : DP < 128 ? DP : 128, Q8 && DP == 64 ? by64 : by128) ||
+        !make_map(&maps.v, a.v, a, maps.box, Q8 ? DP : 64, Q8 ? plain : by128))
+      maps.box = 0;
+  }
+  p.box = maps.box;
   const int64_t rows = a.T * (a.Hq / a.Hkv);
   const dim3 grid((unsigned)((rows + NT * kTcRows - 1) / (NT * kTcRows)), (unsigned)p.splits, (unsigned)(a.B * a.Hkv));
   if (!GROUPED || p.stage != 2) {
-    attn_tc<GROUPED, DP, NT, BF, Q8, SH, LONE><<<grid, Shape::kThreads, Shape::kSmem, s>>>(p, km, vm);
+    attn_tc<GROUPED, DP, NT, BF, Q8, SH, LONE><<<grid, Shape::kThreads, Shape::kSmem, s>>>(p, maps.k, maps.v);
     return cudaGetLastError();
   }
   // the requests' own tokens run beside the shared ones
@@ -158,7 +184,7 @@ cudaError_t launch_tc(AttnDev p, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_tc<GROUPED, DP, NT, BF, Q8, SH, LONE>, p, km, vm);
+  return cudaLaunchKernelEx(&cfg, attn_tc<GROUPED, DP, NT, BF, Q8, SH, LONE>, p, maps.k, maps.v);
 }
 
 // Tiles of 128 rows of a CTA (256 dims leave tensor memory for one).
@@ -178,27 +204,27 @@ bool some_rows(const topkp_tree_attention_args& a) {
 }
 
 template <bool GROUPED, bool BF, bool Q8>
-cudaError_t launch_dim(const AttnDev& p, cudaStream_t s) {
+cudaError_t launch_dim(const AttnDev& p, Maps& maps, cudaStream_t s) {
   if constexpr (Q8) {
     if constexpr (GROUPED && BF) {
-      if (few_rows(p.a) && p.stage == 1) return launch_tc<GROUPED, 128, 1, BF, true, 4, true>(p, s);
+      if (few_rows(p.a) && p.stage == 1) return launch_tc<GROUPED, 128, 1, BF, true, 4, true>(p, maps, s);
     }
-    if (few_rows(p.a)) return launch_tc<GROUPED, 128, 1, BF, true, 4>(p, s);
+    if (few_rows(p.a)) return launch_tc<GROUPED, 128, 1, BF, true, 4>(p, maps, s);
     if constexpr (GROUPED) {
-      if (some_rows(p.a)) return launch_tc<GROUPED, 128, 1, BF, true, 2>(p, s);
+      if (some_rows(p.a)) return launch_tc<GROUPED, 128, 1, BF, true, 2>(p, maps, s);
     }
   }
   const bool two = row_tiles(p.a) == 2;
-  if (p.a.D <= 64) return two ? launch_tc<GROUPED, 64, 2, BF, Q8>(p, s) : launch_tc<GROUPED, 64, 1, BF, Q8>(p, s);
-  if (p.a.D <= 128) return two ? launch_tc<GROUPED, 128, 2, BF, Q8>(p, s) : launch_tc<GROUPED, 128, 1, BF, Q8>(p, s);
-  return launch_tc<GROUPED, 256, 1, BF, Q8>(p, s);
+  if (p.a.D <= 64) return two ? launch_tc<GROUPED, 64, 2, BF, Q8>(p, maps, s) : launch_tc<GROUPED, 64, 1, BF, Q8>(p, maps, s);
+  if (p.a.D <= 128) return two ? launch_tc<GROUPED, 128, 2, BF, Q8>(p, maps, s) : launch_tc<GROUPED, 128, 1, BF, Q8>(p, maps, s);
+  return launch_tc<GROUPED, 256, 1, BF, Q8>(p, maps, s);
 }
 
 template <bool GROUPED>
-cudaError_t launch_parts(const AttnDev& p, cudaStream_t s) {
+cudaError_t launch_parts(const AttnDev& p, Maps& maps, cudaStream_t s) {
   const bool bf = p.a.dtype == TOPKP_BF16, q8 = p.a.k.dtype == TOPKP_E4M3;
-  return bf ? (q8 ? launch_dim<GROUPED, true, true>(p, s) : launch_dim<GROUPED, true, false>(p, s))
-            : (q8 ? launch_dim<GROUPED, false, true>(p, s) : launch_dim<GROUPED, false, false>(p, s));
+  return bf ? (q8 ? launch_dim<GROUPED, true, true>(p, maps, s) : launch_dim<GROUPED, true, false>(p, maps, s))
+            : (q8 ? launch_dim<GROUPED, false, true>(p, maps, s) : launch_dim<GROUPED, false, false>(p, maps, s));
 }
 
 }  // namespace

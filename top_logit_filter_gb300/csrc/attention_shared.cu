@@ -4,7 +4,11 @@
 
 namespace topkp {
 
-cudaError_t launch_grouped(const AttnDev& p, cudaStream_t s) { return launch_parts<true>(p, s); }
+cudaError_t launch_grouped(const AttnDev& front, const AttnDev& own, cudaStream_t s) {
+  Maps maps;
+  const cudaError_t e = launch_parts<true>(front, maps, s);
+  return e != cudaSuccess ? e : launch_parts<true>(own, maps, s);
+}
 
 cudaError_t grouped_take_device_error(unsigned int* out) {
   const unsigned int zero = 0;

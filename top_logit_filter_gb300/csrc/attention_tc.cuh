@@ -384,14 +384,14 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH, LONE>::kThreads, T
   const int h = (int)(bh - b * a.Hkv);
   const int row0 = blockIdx.x * (NT * kTcRows);
   const int split = blockIdx.y;
-  int ctx, len, nodes, tile0 = 0;
+  int ctx, len, nodes, tile0 = 0, first = 0;
   const bool front = GROUPED && p.stage == 1;
   if (front) {
-    ctx = len = shared_span(p, b);
+    ctx = len = shared_span(p, b, &first);
     nodes = 0;  // asked for row by row
   } else {
     request_span(a, b, &ctx, &len, &nodes);
-    if (GROUPED) tile0 = shared_span(p, b / p.size) / kTile;
+    if (GROUPED) tile0 = shared_span(p, b / p.size, &first) / kTile;
   }
   const int tiles = (len + kTile - 1) / kTile;
   const int t_begin = min(tile0 + split * p.per, tiles);
@@ -799,7 +799,7 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH, LONE>::kThreads, T
   } else if (warp < Shape::kSoftWarps + kFeed) {
     // ---- keys and values ----
     const int feeder = warp - Shape::kSoftWarps;
-    const int32_t* table = a.table ? a.table + b * a.ld_table : nullptr;
+    const int32_t* table = a.table ? a.table + b * a.ld_table + (front ? first * p.ld_member : 0) : nullptr;
     // the page and place of token t; the page may lie outside the pool
     auto place = [&](int t, int& page, int& at) {
       page = (int)b;

@@ -564,21 +564,24 @@ def cache_fork(states, pages, lengths, source, refs, grow=0, time_dim: int = 1, 
     _cuda(pages, "pages", 2, torch.int32)
     dev = pages.device
     R, M = pages.shape
-    if M > 1 and pages.stride(1) != 1 or R > 1 and pages.stride(0) < M:
+    ld, one = pages.stride()
+    if M > 1 and one != 1 or R > 1 and ld < M:
         pages = pages.contiguous()
+        ld = M
     lengths = _vec(lengths, R, torch.int32, "lengths", dev)
     _cuda(source, "source", 1, torch.int32, dev)
     N = source.shape[0]
     source = source.contiguous()
     _cuda(refs, "refs", 1, torch.int32, dev)
     pool = refs.shape[0]
-    if refs_out is not None:
+    if refs_out is None:
+        refs = refs.contiguous()
+        refs_out = torch.empty(pool, dtype=torch.int32, device=dev)
+    else:
         _cuda(refs_out, "refs_out", 1, torch.int32, dev)
         if refs_out.shape != refs.shape or not refs_out.is_contiguous():
             raise ValueError("refs_out must be contiguous and shaped like refs")
-    refs = refs.contiguous()
-    if refs_out is None:
-        refs_out = torch.empty_like(refs)
+        refs = refs.contiguous()
     many, packed, pool_, page_size = _page_states(states, time_dim, dev)
     if not many:
         raise ValueError("no states: the page size is theirs")
@@ -590,16 +593,17 @@ def cache_fork(states, pages, lengths, source, refs, grow=0, time_dim: int = 1, 
     else:
         grow, grow_all = None, int(grow)
     if out is None:
-        out = torch.empty((N, M), dtype=torch.int32, device=dev)
+        out, ld_out = torch.empty((N, M), dtype=torch.int32, device=dev), M
     elif out.shape != (N, M) or out.dtype != torch.int32 or out.device != dev or (M > 1 and out.stride(1) != 1) or (N > 1 and out.stride(0) < M):
         raise ValueError(f"out must be a {(N, M)} int32 tensor on {dev} with contiguous rows")
-    missing = torch.empty((1,), dtype=torch.int32, device=dev)
-    workspace = _workspace(workspace, int(lib.topkp_cache_fork_workspace_size(N, pool)), dev)
+    else:
+        ld_out = out.stride(0) if N > 1 else M
+    missing = torch.empty(1, dtype=torch.int32, device=dev)
+    workspace = _workspace(workspace, lib.topkp_cache_fork_workspace_size(N, pool), dev)
     held = _lib.ctypes.c_char_p(packed)  # keeps the descriptors where the call reads them
-    args = _FORK.pack(_lib.ctypes.cast(held, _lib.ctypes.c_void_p).value, _ptr(pages), _ptr(lengths),
-                      _ptr(source), _ptr(grow), _ptr(refs), _ptr(out), _ptr(refs_out), _ptr(missing), _ptr(workspace),
-                      workspace.numel(), len(many), R, N, M, pages.stride(0) if R > 1 else M, out.stride(0) if N > 1 else M, pool,
-                      page_size, grow_all)
+    args = _FORK.pack(_lib.ctypes.cast(held, _lib.ctypes.c_void_p).value, _ptr(pages), _ptr(lengths), _ptr(source), _ptr(grow),
+                      _ptr(refs), _ptr(out), _ptr(refs_out), _ptr(missing), _ptr(workspace), workspace.numel(), len(many), R, N, M,
+                      ld if R > 1 else M, ld_out, pool, page_size, grow_all)
     _launch(dev, lib.topkp_cache_fork, args)
     return out, refs_out, missing
 

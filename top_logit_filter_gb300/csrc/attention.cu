@@ -14,6 +14,8 @@
 // is a request with the nodes of all its requests, so its keys and values are
 // read once a group; each request's own tokens are another, beside it; the
 // join takes the parts of both.
+#include <string.h>
+
 #include <algorithm>
 
 #include "attention_launch.cuh"
@@ -168,7 +170,8 @@ AttnPlan plan_attention(const topkp_tree_attention_args& a, int num_sms) {
 
 // Parts of the shared tokens and of the requests' own, which run side by
 // side: both kernels' CTAs fill the device together.
-SharedPlan plan_shared(const topkp_tree_attention_args& a, int64_t groups, int64_t max_shared, int num_sms) {
+namespace {
+SharedPlan choose_shared(const topkp_tree_attention_args& a, int64_t groups, int64_t max_shared, int num_sms) {
   SharedPlan s;
   const AttnPlan alone = plan_attention(a, num_sms);
   s.groups = 0;  // every request by itself
@@ -218,6 +221,23 @@ SharedPlan plan_shared(const topkp_tree_attention_args& a, int64_t groups, int64
   s.groups = groups;
   s.part_bytes = (size_t)(s.front.splits + s.own.splits) * (size_t)(a.B * a.T * a.Hq) * (a.D + 1) * sizeof(float);
   return s;
+}
+}  // namespace
+
+// (The choice takes longer than a launch, and a program asks for it twice a
+// call and for the same shapes call after call: the last one is kept.)
+SharedPlan plan_shared(const topkp_tree_attention_args& a, int64_t groups, int64_t max_shared, int num_sms) {
+  struct Shapes {
+    int64_t v[14];
+  };
+  const Shapes shapes = {{a.B, a.T, a.Hq, a.Hkv, a.D, a.page_size, a.max_pages, a.max_context, a.dtype, a.k.dtype, groups, max_shared, num_sms, 1}};
+  static thread_local Shapes last = {};
+  static thread_local SharedPlan plan;
+  if (memcmp(&last, &shapes, sizeof(shapes))) {
+    plan = choose_shared(a, groups, max_shared, num_sms);
+    last = shapes;
+  }
+  return plan;
 }
 
 namespace {

@@ -375,7 +375,8 @@ def shared_attention(q, k_cache, v_cache, context, pages, shared, tree=None, nod
     lib = _ready()
     _cuda(q, "q", 4)
     _cuda(shared, "shared", 1, torch.int32, q.device)
-    _cuda(pages, "pages", 2, torch.int32, q.device)
+    if not isinstance(pages, torch.Tensor) or pages.dim() != 2:
+        raise ValueError("pages must be a 2-D CUDA tensor")
     shared = shared.contiguous()
     groups = shared.shape[0]
     if groups < 1 or q.shape[0] % groups:

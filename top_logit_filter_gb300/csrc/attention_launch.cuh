@@ -192,12 +192,16 @@ int row_tiles(const topkp_tree_attention_args& a) { return a.T * (a.Hq / a.Hkv) 
 
 // Whether four warps share each row's tokens: up to 32 rows over e4m3, at 65 to
 // 128 dims.  64 single tokens to 8000, in us with and without: 303 / 350 (fp16
-// 340 / 365); it gives nothing at 64 dims (217 / 218) or 256 (313 / 311).
+// 340 / 365 with one loading warp; 276 with a warp each for keys, values and
+// scales); it gives nothing at 64 dims (217 / 218) or 256 (313 / 311).
 bool few_rows(const topkp_tree_attention_args& a) {
   return a.k.dtype == TOPKP_E4M3 && a.D > 64 && a.D <= 128 && a.T * (a.Hq / a.Hkv) <= 32;
 }
 
-// Two warps to a row for 33 to 64 of them, where requests share a prefix.
+// Two warps to a row for 33 to 64 of them, where requests share a prefix (16
+// groups of 8 single tokens of 64 query and 8 cache heads, prefixes to 32000:
+// 399 us, the own tokens' kernel alike; with one warp a row the softmax takes
+// 1520 of a tile's 1650 cycles, with two 1030).
 bool some_rows(const topkp_tree_attention_args& a) {
   const int64_t rows = a.T * (a.Hq / a.Hkv);
   return a.k.dtype == TOPKP_E4M3 && a.D > 64 && a.D <= 128 && rows > 32 && rows <= 64;

@@ -267,7 +267,8 @@ topkp_status topkp_tree_attention(const topkp_tree_attention_args* args, void* s
  *   max_shared  an upper bound of shared[g] that plans how the work is split
  *               (results hold for any value).
  * args->workspace has topkp_shared_attention_workspace_size() bytes.  Three
- * launches.
+ * launches, or those of topkp_tree_attention where the plan finds too little
+ * shared to be worth them.
  */
 size_t topkp_shared_attention_workspace_size(const topkp_tree_attention_args* args, int64_t groups, int64_t max_shared);
 topkp_status topkp_shared_attention(const topkp_tree_attention_args* args, const int32_t* shared, int64_t groups,
@@ -319,8 +320,8 @@ topkp_status topkp_shared_attention(const topkp_tree_attention_args* args, const
  *              of the path's second token and on, and behind them of the token
  *              drawn; 0 elsewhere.
  * Probabilities and sums are fp32; a decision may differ from exact arithmetic
- * where its two sides lie within about 1e-6 (relative to p) of one another.  NaN and +inf give an unspecified result.
- * One launch.
+ * where its two sides lie within about 1e-6 (relative to p) of one another.
+ * NaN and +inf give an unspecified result.  One launch.
  */
 typedef struct {
   const void* target;

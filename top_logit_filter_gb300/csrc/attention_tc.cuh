@@ -1226,11 +1226,6 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH, LONE>::kThreads, T
     }
     tc_fence_before();
   }
-  // A join that waits for this launch waits for the one before it, too: its
-  // last CTA does not end before that has.  (All of them waiting would hold
-  // the SMs that the rest of this launch is to run on.)
-  if (GROUPED && p.stage == 2 && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1)
-    asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncwarp();
   __syncthreads();
   if (dead) {  // products and copies may still be in flight: time for them to end
@@ -1240,6 +1235,13 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH, LONE>::kThreads, T
   if (warp == Shape::kSoftWarps + kFeed) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(Shape::kColumns) : "memory");
+    // A join that waits for this launch waits for the one before it, too: its
+    // last CTA does not end before that has.  (All of them waiting would hold
+    // the SMs that the rest of this launch is to run on.)  Its tensor memory
+    // is free by then: a CTA of the launch before may be on this SM and still
+    // be asking for it, and neither would ever go on.
+    if (GROUPED && p.stage == 2 && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1)
+      asm volatile("griddepcontrol.wait;" ::: "memory");
   }
 }
 

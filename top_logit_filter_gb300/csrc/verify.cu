@@ -7,7 +7,12 @@
 //   a_{k+1} = a_k + W_k,   W_k = sum max(p - a_k q, 0),   a_0 = 0, W_0 = 1,
 // so a child costs two probabilities, and a further child one pass over the
 // node's two rows.  The token drawn when no child is accepted is the largest
-// of max(p - a q, 0) / (race + eps): no normaliser, no prefix sums.
+// of max(p - a q, 0) / (race + eps): no normaliser, no prefix sums.  Where
+// children are certain what is left is the row less the tokens tried: W loses
+// p(x), and is summed afresh, by a pass over the row without them, when less
+// than half of the last sum is left and another child asks for it.  (Carried
+// on as a difference W keeps the sum's error: off by 12% of itself after a
+// token of 1 - 3e-7.)
 //
 // Only rows down the accepted path are needed (about four of a tree of 64
 // nodes).  Rows are cut over the cluster's CTAs; a row's second reading comes
@@ -196,6 +201,7 @@ struct Shared {
   float mt, md, st, sd;     // the rows' largest logits and sums of exponentials
   float weight, factor;     // W and a of the comment above, times st and st / sd
   unsigned long long open;  // children to be tried
+  unsigned long long bloom;  // of the tokens tried, eight neighbours to a bit
   unsigned long long best;
   uint32_t bound;  // a candidate's key of the draw
   int state, node, depth, tries, top, token;
@@ -430,6 +436,36 @@ __device__ __forceinline__ float weigh(const VerifyArgs& a, const Team& team, co
   return sum;
 }
 
+// Eight neighbouring tokens to a bit.
+__device__ __forceinline__ unsigned long long bloom_bit(int x) { return 1ull << ((x >> 3) & 63); }
+
+// A thread's sum of exp(x - mt) over the tokens that have not been tried.  It
+// is asked for where the tried ones held most of the row, and few elements may
+// be all that counts: each is worked out with care, and what a sum's rounding
+// drops is kept (tens to hundreds of terms a thread, one after another).
+template <int DT>
+__device__ __forceinline__ float weigh_rest(const VerifyArgs& a, const Team& team, const Shared& sh, const typename DType<DT>::raw* t) {
+  int first, last;
+  part_of<DT>(a, team, first, last);
+  const float mt = sh.mt;
+  const unsigned long long bloom = sh.bloom;
+  const int tries = sh.tries;
+  float sum = 0.0f, low = 0.0f;
+  if (mt == -INFINITY) return 0.0f;
+#pragma unroll 4
+  for (int i = first + (int)threadIdx.x; i < last; i += kVerifyThreads) {
+    float e = exp_one(DType<DT>::to_float(t[i]), mt);
+    if (bloom & bloom_bit(i))
+      for (int k = 0; k < tries; ++k)
+        if (sh.tried[k] == i) e = 0.0f;
+    e -= low;
+    const float next = sum + e;
+    low = (next - sum) - e;
+    sum = next;
+  }
+  return sum;
+}
+
 // The best candidate of this warp's elements: the largest
 // (exp(x - mt) - factor exp(y - md)) / (variate + eps), of equal ones the
 // first.  No element can be better than exp(x - mt) / (variate + eps), which
@@ -537,15 +573,16 @@ template <int DT, int MODE>
 __device__ __forceinline__ void decide(const VerifyArgs& a, const Team& team, Shared& sh, int n, int sets, int parts, bool resumed) {
   constexpr bool DRAFT = MODE == kVerifyRatio, GREEDY = MODE == kVerifyGreedy;
   const int lane = threadIdx.x & 31;
-  int node = sh.node, depth = sh.depth, state = kDraw, tries = 0, top = -1;
+  int node = sh.node, depth = sh.depth, state = kDraw, tries = resumed ? sh.tries : 0, top = -1;
   float mt = sh.mt, md = sh.md, st = sh.st, sd = sh.sd, weight = sh.weight, factor = sh.factor;
-  unsigned long long open = sh.open, bloom = 0ull;
+  unsigned long long open = sh.open, bloom = resumed ? sh.bloom : 0ull;
+  float whole = 0.0f;
   if (resumed) {
     float sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < 16 * kVW / 32; ++k)
       if (lane + 32 * k < parts) sum += sh.part[team.at][0][lane + 32 * k].x;
-    weight = warp_sum(sum);
+    weight = whole = warp_sum(sum);
   }
   float inverse = 1.0f / sd;
   for (int set = 0;;) {
@@ -562,7 +599,7 @@ __device__ __forceinline__ void decide(const VerifyArgs& a, const Team& team, Sh
       }
       inverse = 1.0f / sd;
       open = children(sh, node, n);
-      weight = st;
+      weight = whole = st;
       factor = 0.0f;
       tries = 0;
       bloom = 0ull;
@@ -592,7 +629,7 @@ __device__ __forceinline__ void decide(const VerifyArgs& a, const Team& team, Sh
             }
           }
         } else {
-          if (bloom >> ((x >> 3) & 63) & 1)
+          if (bloom & bloom_bit(x))
             for (int i = 0; i < tries; ++i)
               if (sh.tried[i] == x) left = 0.0f;
           if (sh.uniform[c] * weight < left) {
@@ -602,7 +639,11 @@ __device__ __forceinline__ void decide(const VerifyArgs& a, const Team& team, Sh
             if (lane == 0) sh.tried[tries] = x;
             __syncwarp();
             ++tries;
-            bloom |= 1ull << ((x >> 3) & 63);
+            bloom |= bloom_bit(x);
+            if (open && weight < 0.5f * whole) {
+              state = kPass;
+              break;
+            }
           }
         }
       }
@@ -630,6 +671,7 @@ __device__ __forceinline__ void decide(const VerifyArgs& a, const Team& team, Sh
     sh.weight = weight;
     sh.factor = factor;
     sh.open = open;
+    sh.bloom = bloom;
     sh.tries = tries;
     sh.top = top;
   }
@@ -718,9 +760,12 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const __grid_
       if (warp == 0) decide<DT, MODE>(a, team, sh, sh.n, sets, (resumed ? kVW : kVW / (sets > 2 ? 4 : sets)) * a.cs, resumed);
       team.at ^= 1;
       __syncthreads();
-      if (!DRAFT || sh.state != kPass) break;
-      // the weight of what is left: the sum of max(p - a q, 0)
-      const float sum = warp_sum(weigh<DT>(a, team, target(sh.node), draft(sh.node), sh.mt, sh.md, sh.factor));
+      if (GREEDY || sh.state != kPass) break;
+      // the weight of what is left: the sum of max(p - a q, 0), or of p but for the tokens tried
+      float sum;
+      if constexpr (DRAFT) sum = weigh<DT>(a, team, target(sh.node), draft(sh.node), sh.mt, sh.md, sh.factor);
+      else sum = weigh_rest<DT>(a, team, sh, target(sh.node));
+      sum = warp_sum(sum);
       hand_out(team, sh, 0, (int)team.rank * kVW + warp, make_float4(sum, 0.0f, 0.0f, 0.0f));
       team_sync(team);
     }

@@ -196,8 +196,10 @@ struct TcShape {
   // by a warp each, and two groups of warps widen values in turn: a single
   // loading warp, with the latency of its own instructions and loads, was what
   // a tile waited for (1845 of 2107 cycles), then the widening (1300 of 1620).
-  static constexpr bool kSplit = Q8 && NT == 1 && DP >= 128 && !kPair;
-  static constexpr int kFeedWarps = !Q8 ? 2 : NT == 2 ? 7 : kPair ? 5 : DP >= 128 ? 11 : 3;
+  // Heads of 256 gain nothing (8 / 2 heads over bf16, with and without: 64 single
+  // tokens to 8000 173 / 170 us, 4 x 64 nodes to 16000 61.5 / 60.0).
+  static constexpr bool kSplit = Q8 && NT == 1 && DP == 128 && !kPair;
+  static constexpr int kFeedWarps = !Q8 ? 2 : NT == 2 ? 7 : kPair ? 5 : kSplit ? 11 : DP >= 128 ? 9 : 3;
   static constexpr int kWiden = kFeedWarps - (kSplit ? 3 : 1);  // warps that widen e4m3 values
   static constexpr int kThreads = 32 * (kSoftWarps + kFeedWarps + 1);
   // with a warp to a row two CTAs leave room for two warps that widen, enough for 64 dims only
@@ -221,7 +223,8 @@ struct TcShape {
   // A group of warps widens every kGroups-th tile.  A wait on a stage's
   // barrier must not pass by the phase before the one that it is for: the
   // tiles between two uses of a stage see to that, so two groups need two stages.
-  static constexpr int kGroups = kSplit && kValues >= 2 ? 2 : 1;
+  static constexpr int kGroups = kSplit ? 2 : 1;
+  static_assert(kGroups == 1 || kValues >= 2, "a stage of values for each group");
   static constexpr uint32_t kQ = NT * 128;  // after two S of 64 columns a row tile
   static constexpr uint32_t kO = kQ + (kQInTmem ? NT * kQColumns : 0);
   static constexpr int kColumns = kO + NT * DP <= 256 ? 256 : 512;
@@ -875,13 +878,10 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH, LONE>::kThreads, T
       // a warp that widens would wait for such loads); the others widen values.
       constexpr uint32_t kToken = 1u << 16;  // beside a value's exponent: there is a token
       if (Shape::kSplit && feeder < 2) {
-        // Keys (blocks of 128 dims), or values; a lane a box, its page
-        // (outside the pool past the last token, which reads as zeros) looked
-        // up a tile ahead.
-        constexpr int KW = DP < 128 ? DP : 128;  // bytes of a row of a keys' block
-        const bool val = feeder == 1;
-        const int blk = per_tile && !val ? lane / per_tile : 0, piece = per_tile ? lane - blk * per_tile : 0;
-        const bool boxed = lane < per_tile * (val ? 1 : DP / KW);
+        // Keys, or values; a lane a box, its page (outside the pool past the
+        // last token, which reads as zeros) looked up a tile ahead.
+        const bool val = feeder == 1, boxed = lane < per_tile;
+        const int piece = boxed ? lane : 0;
         const int t_end = min(len, (t_begin + n) * kTile);
         int pg = -1, to = 0;
         auto look = [&](int j) {
@@ -902,8 +902,7 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH, LONE>::kThreads, T
             if (lane == 0) mbar_arrive_expect_tx(full, val ? Shape::kRawBytes : Shape::kKeyBytes);
             __syncwarp();
             if (boxed) {
-              if (val) tma_box(to_smem + piece * p.box * DP, &vmap, full, 0, h, to, pg);
-              else tma_box(to_smem + blk * (kTile * 128) + piece * p.box * KW, &kmap, full, blk * 128, h, to, pg);
+              tma_box(to_smem + piece * p.box * DP, val ? &vmap : &kmap, full, 0, h, to, pg);
             }
           } else {
             if (!val) {  // (values are read by the warps that widen them)

@@ -151,7 +151,7 @@ class PagedCaches:
         old = torch.cat([self.lengths, torch.zeros(1, dtype=torch.int32, device=source.device)])
         self.lengths = old[source.long()]  # (-1 is the last, a zero)
 
-    def attend(self, tree=None, shared=None, longest=None):
+    def attend(self, tree=None, shared=None, longest=None, prefix=None):
         """For ToyModel.forward: new tokens stand at lengths[r] and on."""
         def run(layer, q, k, v):
             R, T = q.shape[:2]
@@ -162,7 +162,7 @@ class PagedCaches:
             tk.cache_write(k.reshape(R * T, *k.shape[2:]), v.reshape(R * T, *v.shape[2:]), slots, kc, vc)
             if shared is None:
                 return tk.tree_attention(q, kc, vc, self.lengths, pages=self.pages, tree=tree)
-            return tk.shared_attention(q, kc, vc, self.lengths, self.pages, shared, tree=tree, max_context=longest)
+            return tk.shared_attention(q, kc, vc, self.lengths, self.pages, shared, tree=tree, max_context=longest, max_shared=prefix)
         return run
 
 
@@ -200,7 +200,7 @@ def sample_drafted(model, prompt, samples=8, rounds=6, page_size=16, above=(0, 0
             if i:
                 tokens[:, i] = (draft[:, above[i]].float() - torch.log(race(N, model.vocab))).argmax(1)
             draft[:, i] = model.norm(model.embed[tokens[:, i]]) @ model.head
-        target = model.forward(tokens, caches.attend(tree, shared, longest))
+        target = model.forward(tokens, caches.attend(tree, shared, longest, P - 1))
         count, path, token, logp = tk.draft_verify(target, tokens.int(), torch.rand((N, T), generator=g, device=dev), race(N, model.vocab),
                                                    draft=draft, parent=parent, want_logprob=True)
         tk.cache_compact(caches.states, caches.lengths, path, count, pages=caches.pages)

@@ -265,7 +265,9 @@ topkp_status topkp_tree_attention(const topkp_tree_attention_args* args, void* s
  *               zero or less, or one that is too small, costs speed only.
  *   groups      at least 1, divides B.
  *   max_shared  an upper bound of shared[g] that plans how the work is split
- *               (results hold for any value).
+ *               (results hold for any value).  The nearer the better: what
+ *               it leaves of max_context is planned as the requests' own, so
+ *               with a bound far above the truth few CTAs take those.
  * args->workspace has topkp_shared_attention_workspace_size() bytes.  Three
  * launches, or those of topkp_tree_attention where the plan finds too little
  * shared to be worth them.

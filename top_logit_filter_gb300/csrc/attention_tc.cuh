@@ -397,8 +397,14 @@ __global__ void __launch_bounds__(TcShape<DP, NT, BF, Q8, SH, LONE>::kThreads, T
     if (GROUPED) tile0 = shared_span(p, b / p.size, &first) / kTile;
   }
   const int tiles = (len + kTile - 1) / kTile;
-  const int t_begin = min(tile0 + split * p.per, tiles);
-  const int n = (split == p.splits - 1 ? tiles : min(t_begin + p.per, tiles)) - t_begin;
+  // Tiles of a part, as planned; more where what is shared, or what is a
+  // request's own, is longer than the bounds that it was planned by (groups
+  // with prefixes of different lengths), so that the last part is not left
+  // with all the rest (4 groups of 8 requests of 32000 tokens, planned for
+  // 28000 shared, of which one group shares 8000: 262 us, 358 without).
+  const int per = GROUPED ? max(p.per, (tiles - tile0 + p.splits - 1) / p.splits) : p.per;
+  const int t_begin = min(tile0 + split * per, tiles);
+  const int n = (split == p.splits - 1 ? tiles : min(t_begin + per, tiles)) - t_begin;
 
   if (tid == 0) {
     for (int i = 0; i < KS; ++i) {

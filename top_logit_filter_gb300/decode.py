@@ -368,7 +368,8 @@ def shared_attention(q, k_cache, v_cache, context, pages, shared, tree=None, nod
     consecutive ones, and the first shared[g] tokens of group g's requests are
     the same: the same pages (as ``cache_fork`` leaves them) or equal ones.
     max_shared: a bound of ``shared`` known on the host, which plans the work
-    (the capacity when None).  ``workspace``: a uint8 tensor of at least
+    (the capacity when None: give it where far less is shared, since what it
+    leaves of max_context is planned as the requests' own).  ``workspace``: a uint8 tensor of at least
     ``shared_attention_workspace_size`` bytes (allocated when None).
     Everything else as for ``tree_attention``; the result differs from its by
     the order of the sums only."""

@@ -466,7 +466,7 @@ def draft_verify(target, tokens, uniform=None, race=None, draft=None, parent=Non
         raise TypeError(f"unsupported dtype {target.dtype} (float32, float16 or bfloat16)")
     B, T, V = target.shape
     ts = target.stride()
-    if ts[2] != 1 and V > 1:
+    if ts[2] != 1 and V > 1 or ts[1] < V and T > 1:
         target = target.contiguous()
         ts = target.stride()
     ds = (0, 0)
@@ -475,7 +475,7 @@ def draft_verify(target, tokens, uniform=None, race=None, draft=None, parent=Non
         if draft.shape != target.shape:
             raise ValueError(f"draft is {tuple(draft.shape)} and target {tuple(target.shape)}")
         ds = draft.stride()
-        if ds[2] != 1 and V > 1:
+        if ds[2] != 1 and V > 1 or ds[1] < V and T > 1:
             draft = draft.contiguous()
             ds = draft.stride()
     if (uniform is None) != (race is None):

@@ -409,7 +409,7 @@ def _attention(q, k_cache, v_cache, context, pages, tree, nodes, k_exp, v_exp, s
         _cuda(pages, "pages", 2, torch.int32, dev)
         if pages.shape[0] != B:
             raise ValueError(f"pages has {pages.shape[0]} rows and q {B} requests")
-        if pages.shape[1] > 1 and pages.stride(1) != 1:
+        if pages.shape[1] > 1 and pages.stride(1) != 1 or B > 1 and pages.stride(0) < pages.shape[1]:
             pages = pages.contiguous()
     elif pool != B:
         raise ValueError(f"without a block table the cache holds one entry a request ({B}), not {pool}")

@@ -441,10 +441,12 @@ __device__ __forceinline__ unsigned long long bloom_bit(int x) { return 1ull << 
 
 // A thread's sum of exp(x - mt) over the tokens that have not been tried.  It
 // is asked for where the tried ones held most of the row, and few elements may
-// be all that counts: each is worked out with care, and what a sum's rounding
-// drops is kept (tens to hundreds of terms a thread, one after another).
+// be all that counts: each is worked out with care, and what the rounding of a
+// sum of vectors drops is kept.  One request of 128256 bf16 that needs it
+// takes 6 us more, 64 of them 12.5 (22.5 an element at a time).
 template <int DT>
 __device__ __forceinline__ float weigh_rest(const VerifyArgs& a, const Team& team, const Shared& sh, const typename DType<DT>::raw* t) {
+  constexpr int VEC = Row<DT>::VEC, U = 4;
   int first, last;
   part_of<DT>(a, team, first, last);
   const float mt = sh.mt;
@@ -452,16 +454,57 @@ __device__ __forceinline__ float weigh_rest(const VerifyArgs& a, const Team& tea
   const int tries = sh.tries;
   float sum = 0.0f, low = 0.0f;
   if (mt == -INFINITY) return 0.0f;
-#pragma unroll 4
-  for (int i = first + (int)threadIdx.x; i < last; i += kVerifyThreads) {
-    float e = exp_one(DType<DT>::to_float(t[i]), mt);
-    if (bloom & bloom_bit(i))
-      for (int k = 0; k < tries; ++k)
-        if (sh.tried[k] == i) e = 0.0f;
+  auto add = [&](float e) {
     e -= low;
     const float next = sum + e;
     low = (next - sum) - e;
     sum = next;
+  };
+  if (a.whole) {
+    for (int i0 = first + (int)threadIdx.x * VEC; i0 < last; i0 += U * kVerifyThreads * VEC) {
+      uint4 q[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * kVerifyThreads * VEC;
+        q[u] = i < last ? __ldg(reinterpret_cast<const uint4*>(t + i)) : nothing<DT>();
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * kVerifyThreads * VEC;  // a multiple of VEC, as V is: a vector's elements share a bit
+        const bool some = (bloom & bloom_bit(i)) != 0;
+        float part = 0.0f;
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j) {
+          float x, y;
+          pair_of<DT>(q[u], j, x, y);
+          if (some)
+            for (int k = 0; k < tries; ++k) {
+              x = sh.tried[k] == i + 2 * j ? -INFINITY : x;
+              y = sh.tried[k] == i + 2 * j + 1 ? -INFINITY : y;
+            }
+          part += exp_one(x, mt) + exp_one(y, mt);
+        }
+        add(part);
+      }
+    }
+  } else {
+    for (int i0 = first + (int)threadIdx.x; i0 < last; i0 += 2 * U * kVerifyThreads) {
+      float x[2 * U];
+#pragma unroll
+      for (int u = 0; u < 2 * U; ++u) {
+        const int i = i0 + u * kVerifyThreads;
+        x[u] = i < last ? DType<DT>::to_float(t[i]) : -INFINITY;
+      }
+      float part = 0.0f;
+#pragma unroll
+      for (int u = 0; u < 2 * U; ++u) {
+        const int i = i0 + u * kVerifyThreads;
+        if (bloom & bloom_bit(i))
+          for (int k = 0; k < tries; ++k) x[u] = sh.tried[k] == i ? -INFINITY : x[u];
+        part += exp_one(x[u], mt);
+      }
+      add(part);
+    }
   }
   return sum;
 }

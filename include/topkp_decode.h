@@ -414,7 +414,8 @@ topkp_status topkp_cache_fork(const topkp_cache_fork_args* args, void* stream);
  * start[b] + keep[b][j] move to start[b] + j, j < kept[b] (topkp_draft_verify's
  * path and count, after which the request's length is start[b] + kept[b]).
  * All are read as they were before the call.  An entry with keep[b][j] <= j,
- * or of which either place lies outside the request's pages, is left alone.
+ * or of which either place lies outside the request's pages, is left alone,
+ * and so is a request with start[b] < 0.
  *
  *   states     host array of `count` descriptors, read during the call.
  *   table      device, [B, max_pages] int32, row stride ld_table, or NULL:

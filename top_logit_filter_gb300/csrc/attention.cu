@@ -7,7 +7,7 @@
 // sum of the softmax; a request's tokens are split over CTAs when there are
 // few rows, and the parts joined by their log-sums.  With up to 128 rows the
 // cache's bytes bound the work (64 single tokens, 32 query and 8 cache heads
-// of 128, contexts to 8192: 251 us, 6.4 TB/s; 2 x 131000 tokens: 153 us, 5.3,
+// of 128, contexts to 8192: 251 to 263 us, 6.1 to 6.4 TB/s; 2 x 131000 tokens: 153 us, 5.3,
 // in one round of CTAs), with more the products and exponentials.
 //
 // topkp_shared_attention: what requests share is one launch in which a group

@@ -44,7 +44,7 @@
 // small ones matters together), so they are widened.
 //
 // 512 rows a head (64 nodes, 64 query and 8 cache heads of 128), 16 requests
-// to 16000 tokens: 404 us over bf16 (1.0 PFLOP/s), 487 over e4m3 (0.83).  The
+// to 16000 tokens: 404 us over bf16 (1.0 PFLOP/s), 505 over e4m3 (0.80).  The
 // softmax warps bound both: an exponential for every 256 multiply-adds, and
 // the waits of the two products and the softmax of a tile on one another.
 #pragma once

@@ -13,8 +13,8 @@
 // Measured: one row of 253 pages to eight, 12.4 us, about 8.5 of them the
 // bookkeeping's four phases (a barrier about 1 us, a phase one to two reads
 // that depend on one another); 32 x 8 beams of 74 pages, 8 states, 21.5; 64
-// rows to 1024, 503 MB of copies, 108: 5.4 TB/s of writes, where filling
-// memory alone reaches 4.0 and a copy 6.8 of both.
+// rows to 1024, 503 MB of copies, 108: 4.7 TB/s of writes over the whole
+// call, where filling memory alone reaches 4.0 (part of these stay in L2).
 //
 // Compacting: a thread owns one column (16 bytes, or fewer where alignment
 // wants it) of an entry and takes a request's kept tokens in order, eight

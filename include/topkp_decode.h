@@ -321,8 +321,9 @@ topkp_status topkp_shared_attention(const topkp_tree_attention_args* args, const
  *   logprob    device, [B, T] float, or NULL: log p (of the node's whole row)
  *              of the path's second token and on, and behind them of the token
  *              drawn; 0 elsewhere.
- * Probabilities and sums are fp32; a decision may differ from exact arithmetic
- * where its two sides lie within about 1e-6 (relative to p) of one another.
+ * Probabilities and sums are fp32, and one below 2^-126 of its row's largest
+ * counts as zero; otherwise a decision may differ from exact arithmetic where
+ * its two sides lie within about 1e-6 (relative to p) of one another.
  * NaN and +inf give an unspecified result.  One launch.
  */
 typedef struct {

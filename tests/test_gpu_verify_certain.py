@@ -90,3 +90,18 @@ def test_one_request_and_many(tk):  # noqa: F811
         cases = [sharp("bf16", 32000, [0.998, 0.9], 0.5, side, 5) for side in (-1, 1)]
         d = batch("bf16", 32000, (cases * copies)[:copies])
         assert check(tk, d, most_near=0).tolist() == [2 if i % 2 == 0 else 1 for i in range(copies)]
+
+
+@pytest.mark.parametrize("drafted", [False, True])
+def test_what_fp32_does_not_hold_counts_as_zero(tk, drafted):  # noqa: F811
+    """A token 2^-127 times as probable as the largest: neither accepted nor drawn, where 2^-125 is."""
+    for power, kept in ((-125, True), (-127, False)):
+        x = torch.full((1, 2, 300), -math.inf)
+        x[:, :, 7], x[:, :, 9] = 0.0, power * math.log(2.0)
+        kw = dict(draft=x.cuda()) if drafted else {}
+        race = torch.ones(1, 300)
+        race[0, 7] = 2.0 ** 64                     # (and 9 has a race so short that it would win by a factor of two)
+        race[0, 9] = 2.0 ** (64 + power - 1)
+        tokens = torch.tensor([[0, 9]], dtype=torch.int32)
+        count, path, token = tk.draft_verify(x.cuda(), tokens.cuda(), uniform=torch.zeros(1, 2).cuda(), race=race.cuda(), eps=0.0, **kw)
+        assert int(count) == (2 if kept else 1) and int(token) == (9 if kept else 7), (power, int(count), int(token))

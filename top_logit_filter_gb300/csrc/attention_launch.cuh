@@ -16,7 +16,7 @@ namespace topkp {
 struct AttnDev {
   topkp_tree_attention_args a;
   int splits;
-  int per;        // tiles of a part; the last part takes what is left
+  int per;        // tiles of a part (in the grouped kernel at least); the last part takes what is left
   float* part_o;  // [splits][B * T * Hq][D]
   float* part_l;  // [splits][B * T * Hq]
   uint32_t page_mul;  // reciprocal of page_size below 2^31, 0: divide
